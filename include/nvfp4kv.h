@@ -79,6 +79,13 @@ typedef enum nvfp4kv_status {
 #define NVFP4KV_FLAG_PACE_TIMEOUT 0x10u /* a pacing wait between the units of
                                            a decode CTA ran out; pacing
                                            carries no data, results stand  */
+#define NVFP4KV_FLAG_BAD_SCALE 0x20u    /* an E4M3 cache's scale was outside
+                                           [2^-64, 2^64] (the nearer end is
+                                           used, 2^-64 for a NaN)          */
+#define NVFP4KV_FLAG_BAD_LENGTH 0x40u   /* page table: a request's lengths or
+                                           page count cannot be            */
+#define NVFP4KV_FLAG_TABLE_FULL 0x80u   /* page table: the step's rows, pages
+                                           or new pages do not fit         */
 
 const char* nvfp4kv_status_string(int status);
 const char* nvfp4kv_last_error_detail(void);
@@ -165,7 +172,9 @@ typedef struct nvfp4kv_plan_options {
                                  SM120 NVFP4 qk_correction layout, row-sum
                                  reduction, and lse", description).  At most
                                  8 query rows per kv head; mma.sync with the
-                                 FP4 operands expanded exactly to f16      */
+                                 FP4 operands expanded exactly to f16,
+                                 5 attention over an E4M3 cache: the plan is
+                                 run with nvfp4kv_e4m3_decode_run          */
   int32_t num_sms;            /* >0: override the device's SM count          */
   int32_t ctas_per_sm;        /* >0: override the occupancy query            */
   int32_t out_dtype;          /* output element: 0 bf16 (default), 1 f16      */
@@ -183,7 +192,8 @@ typedef struct nvfp4kv_plan_info {
   int32_t batch, num_qo_heads, num_kv_heads, head_dim_qk, head_dim_vo;
   int32_t page_size, causal;
   int32_t kernel;          /* 1 tensor-core, 2 CUDA-core, 3 tcgen05, 4 FP4
-                              query and probabilities (two launches)       */
+                              query and probabilities (two launches), 5 E4M3
+                              cache                                        */
   int32_t num_units;       /* attention work units (grid x)                  */
   int32_t row_blocks;      /* query-row blocks per unit (grid y)             */
   int32_t rows_per_block;  /* query rows (G x qo positions) per CTA          */
@@ -389,6 +399,156 @@ int nvfp4kv_static_workspace_flags(const nvfp4kv_plan_info* info, uint32_t* flag
 int nvfp4kv_workspace_flags(const nvfp4kv_plan_info* info,
                             const void* workspace, uint32_t* flags,
                             int32_t clear, cudaStream_t stream);
+
+/* ---- the step's page table ------------------------------------------------- */
+/* Device lists of one serving step, the arguments of the entry points above
+ * and below, written by nvfp4kv_build_page_table. */
+typedef struct nvfp4kv_step_table {
+  int32_t* qo_indptr;      /* [dev, batch + 1] first row of each request      */
+  int32_t* kv_indptr;      /* [dev, batch + 1] first page of each request     */
+  int32_t* last_page_len;  /* [dev, batch] tokens of the last page, 0 without */
+  int32_t* kv_indices;     /* [dev, max_pages] page ids                       */
+  int32_t* batch_idx;      /* [dev, max_tokens] request of each row           */
+  int32_t* positions;      /* [dev, max_tokens] position of each row          */
+  int64_t* slot_map;       /* [dev, max_tokens, may be NULL] page * page_size
+                              + slot of each row                              */
+  int32_t* free_head;      /* [dev, 1] the free list's head after the step    */
+  int32_t max_pages, max_tokens;  /* capacities of the lists                  */
+} nvfp4kv_step_table;
+
+/* Build a step's page table and slot maps on the device, from lengths that
+ * only the device may know.  Request b holds kv_len[b] tokens after the step,
+ * qo_len[b] of them new (its rows of this step, the last positions).  Its
+ * first ceil((kv_len - qo_len) / page_size) pages stand in its row of the
+ * block table; the pages it still lacks are taken from the free list in
+ * request order and entered into its row.
+ *   kv_len, qo_len [dev, batch];
+ *   block_table [dev]  entry (b, c) at block_table[b * block_table_stride + c],
+ *                 c < max_pages_per_request; rows must not overlap;
+ *   free_pages [dev, num_free], free_head [dev, may be NULL = 0]  pages
+ *                 free_pages[*free_head ..) are free.  The new head goes to
+ *                 out->free_head, which must be another word (every CTA reads
+ *                 the old one): copy it back, or swap the two, for the next
+ *                 step;
+ *   batch at most 8192; page_size 1 to 65536 (the caches here have 16 or 1);
+ *   a request has at most 2^30 tokens.
+ * Entries of the lists past the step's rows and pages, and table entries past
+ * a request's pages, are left as they were.  A batch that cannot be (a length
+ * below 0 or above 2^30, qo_len > kv_len, more pages than a table row) sets
+ * NVFP4KV_FLAG_BAD_LENGTH, one that does not fit the lists or the free list
+ * sets NVFP4KV_FLAG_TABLE_FULL in device_flags [dev, may be NULL]; then
+ * nothing else is written.  One launch; can be captured in a CUDA graph. */
+int nvfp4kv_build_page_table(const int32_t* kv_len, const int32_t* qo_len, int32_t batch,
+                             int32_t page_size, int32_t* block_table,
+                             int64_t block_table_stride, int32_t max_pages_per_request,
+                             const int32_t* free_pages, int32_t num_free,
+                             const int32_t* free_head, const nvfp4kv_step_table* out,
+                             uint32_t* device_flags, cudaStream_t stream);
+
+/* ---- rotary positions ------------------------------------------------------- */
+/* Frequencies: pair i of rotary_dim / 2 turns by f_i = base^(-2 i / rotary_dim)
+ * radians a position.  factor stretches positions for long contexts: all
+ * frequencies are divided by it where original_max_position is 0; otherwise by
+ * parts: with r_i = original_max_position * f_i / 2 pi rotations over the
+ * original length, g = clamp((r_i - low) / (high - low), 0, 1) of the
+ * frequency is kept, f_i * ((1 - g) / factor + g). */
+typedef struct nvfp4kv_rope_options {
+  double base;                    /* > 1, for example 10000                  */
+  double factor;                  /* > 0; 1: no scaling                      */
+  int64_t original_max_position;  /* 0: all frequencies alike                */
+  double low_rotations, high_rotations;  /* 0 <= low < high (by parts only)  */
+} nvfp4kv_rope_options;
+
+/* Fill freq_host [host, rotary_dim / 2]: turns a position in units of 2^-64
+ * (modulo one turn), the table of nvfp4kv_rope once it is on the device.
+ * rotary_dim is even, 2 to 512. */
+int nvfp4kv_rope_frequencies(int32_t rotary_dim, const nvfp4kv_rope_options* options,
+                             uint64_t* freq_host);
+
+/* Rotate the first rotary_dim dims of every query and key head by its row's
+ * position and copy the others: with angle = position * f_i and the pair
+ * (x1, x2) = dims (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when interleaved,
+ *   y1 = attention_factor * (x1 cos - x2 sin),
+ *   y2 = attention_factor * (x2 cos + x1 sin),
+ * in float32 from angles exact to 2^-26 turns at any position, rounded once.
+ *   q [dev]  element (row, head, d) at q[row*q_stride_tok + head*q_stride_head
+ *            + d], q_out the same with its strides, k and k_out likewise;
+ *            strides in elements, multiples of 8; 16-byte aligned.  q_out may
+ *            be q (and k_out k) with the same strides; otherwise an output
+ *            must not overlap an input.  num_qo_heads or num_kv_heads may be
+ *            0 (its pointers are not read).
+ *   positions [dev, num_tokens]  any int32; rows past num_tokens stay.
+ *   head_dim  a multiple of 8, at most 512; rotary_dim even, at most head_dim.
+ *   dtype     0 bf16, 1 f16 (inputs and outputs).
+ *   freq [dev, rotary_dim / 2]  the table of nvfp4kv_rope_frequencies.
+ * One launch; can be captured in a CUDA graph. */
+int nvfp4kv_rope(const void* q, int64_t q_stride_tok, int64_t q_stride_head, void* q_out,
+                 int64_t q_out_stride_tok, int64_t q_out_stride_head, int32_t num_qo_heads,
+                 const void* k, int64_t k_stride_tok, int64_t k_stride_head, void* k_out,
+                 int64_t k_out_stride_tok, int64_t k_out_stride_head, int32_t num_kv_heads,
+                 int32_t num_tokens, const int32_t* positions, int32_t head_dim,
+                 int32_t rotary_dim, int32_t interleaved, int32_t dtype, const uint64_t* freq,
+                 float attention_factor, cudaStream_t stream);
+
+/* ---- the E4M3 cache ------------------------------------------------------------ */
+/* A paged cache of 8-bit E4M3 codes with one float32 scale per page and kv
+ * head, for layers whose keys or values 4 bits hurt: K = code * k_scale[page,
+ * head], V likewise.  Byte strides, each buffer its own, as in
+ * nvfp4kv_paged_cache; the row of one (page, slot, head) is contiguous. */
+typedef struct nvfp4kv_e4m3_cache {
+  uint8_t* k_data;  /* [dev] E4M3, Dk bytes per (page, slot, head)            */
+  uint8_t* v_data;  /* [dev] E4M3, Dv bytes per (page, slot, head)            */
+  float* k_scale;   /* [dev] one per (page, head), in [2^-64, 2^64] where the */
+  float* v_scale;   /* [dev]   page holds tokens                              */
+  int64_t k_stride_page, k_stride_slot, k_stride_head;    /* bytes, x 16      */
+  int64_t v_stride_page, v_stride_slot, v_stride_head;    /* bytes, x 16      */
+  int64_t k_scale_stride_page, k_scale_stride_head;       /* bytes, x 4       */
+  int64_t v_scale_stride_page, v_scale_stride_head;       /* bytes, x 4       */
+  int32_t num_pages;
+  int32_t page_size;    /* tokens per page: 16 or 1                           */
+  int32_t num_kv_heads;
+  int32_t head_dim_qk;  /* multiples of 32, at most 512; attention: the pairs */
+  int32_t head_dim_vo;  /*   of nvfp4kv_paged_cache                           */
+} nvfp4kv_e4m3_cache;
+
+/* Quantise a step's new tokens and store them into their pages.  Request b's
+ * rows qo_indptr[b] .. qo_indptr[b + 1) of k and v are its last tokens,
+ * positions L_b - n_b .. L_b - 1 (the page table AFTER the step), as in
+ * nvfp4kv_decode_append_run.  A page of one kv head, of K or of V, whose slots
+ * [a, z) the step writes gets, with m the largest finite |x| it writes,
+ *   w = 2^e, the smallest e in [-64, 64] with 448 * 2^e >= m;
+ *   scale s = w when a = 0 (the page is new), else max(old scale, w);
+ *   codes E4M3_RNE_satfinite(x / s); where s > old scale, the a older tokens'
+ *   codes become E4M3_RNE(code * (old / s)).
+ * Slots from z on are left as they were.  Infinities saturate; a NaN is stored
+ * as a NaN code and makes the outputs that read it NaN.
+ *   k [dev]  element (row, h, d) at k[row*k_stride_tok + h*k_stride_head + d];
+ *            strides in elements, multiples of 8; 16-byte aligned; v likewise.
+ *   dtype    0 bf16, 1 f16.
+ *   num_rows rows that k and v hold; those past qo_indptr[batch] are not read.
+ *   device_flags [dev, may be NULL]  a request whose rows, lengths or page
+ *            count cannot be is skipped, and so is a page id out of the pool:
+ *            NVFP4KV_FLAG_BAD_APPEND_TARGET; an old scale outside the range:
+ *            NVFP4KV_FLAG_BAD_SCALE.
+ * Two requests must not write the same page in one call (its scale and codes
+ * would be of either).  One launch; can be captured in a CUDA graph. */
+int nvfp4kv_e4m3_append(const nvfp4kv_e4m3_cache* cache, const void* k, int64_t k_stride_tok,
+                        int64_t k_stride_head, const void* v, int64_t v_stride_tok,
+                        int64_t v_stride_head, int32_t dtype, int32_t num_rows,
+                        const int32_t* qo_indptr, const int32_t* kv_indptr,
+                        const int32_t* kv_indices, const int32_t* last_page_len, int32_t batch,
+                        uint32_t* device_flags, cudaStream_t stream);
+
+/* nvfp4kv_decode_run over an E4M3 cache: the same plan (made with kernel = 5),
+ * split, merge, live lengths, outputs and flags.
+ *   q [dev]  as in nvfp4kv_decode_run; q_dtype 0 bf16, 1 f16.
+ * A scale outside [2^-64, 2^64] sets NVFP4KV_FLAG_BAD_SCALE.  Slots past a
+ * request's length may hold anything. */
+int nvfp4kv_e4m3_decode_run(const nvfp4kv_plan_info* info, const void* q, int64_t q_stride_tok,
+                            int64_t q_stride_head, int32_t q_dtype,
+                            const nvfp4kv_e4m3_cache* cache, const int32_t* kv_indices,
+                            float sm_scale, void* workspace, uint64_t workspace_bytes, void* out,
+                            float* lse, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -27,6 +27,9 @@ FLAG_BAD_APPEND_TARGET = 0x2
 FLAG_COPY_TIMEOUT = 0x4
 FLAG_BAD_LIVE_LENGTH = 0x8
 FLAG_PACE_TIMEOUT = 0x10
+FLAG_BAD_SCALE = 0x20
+FLAG_BAD_LENGTH = 0x40
+FLAG_TABLE_FULL = 0x80
 
 
 class PagedCacheStruct(C.Structure):
@@ -62,6 +65,29 @@ class PlanInfo(C.Structure):
         ("device_last_page_len", C.c_void_p), ("off_row_max", C.c_uint64)]
 
 
+class StepTableStruct(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in (
+        "qo_indptr", "kv_indptr", "last_page_len", "kv_indices", "batch_idx", "positions",
+        "slot_map", "free_head")] + [("max_pages", C.c_int32), ("max_tokens", C.c_int32)]
+
+
+class RopeOptions(C.Structure):
+    _fields_ = [("base", C.c_double), ("factor", C.c_double),
+                ("original_max_position", C.c_int64), ("low_rotations", C.c_double),
+                ("high_rotations", C.c_double)]
+
+
+class E4m3CacheStruct(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("k_data", "v_data", "k_scale", "v_scale")] + [
+        (n, C.c_int64) for n in (
+            "k_stride_page", "k_stride_slot", "k_stride_head",
+            "v_stride_page", "v_stride_slot", "v_stride_head",
+            "k_scale_stride_page", "k_scale_stride_head",
+            "v_scale_stride_page", "v_scale_stride_head")] + [
+        (n, C.c_int32) for n in ("num_pages", "page_size", "num_kv_heads",
+                                 "head_dim_qk", "head_dim_vo")]
+
+
 _vp, _i32, _i64, _u64, _f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_uint64, C.c_float
 SIGNATURES = {
     "nvfp4kv_status_string": (C.c_char_p, [C.c_int]),
@@ -92,6 +118,19 @@ SIGNATURES = {
     "nvfp4kv_decode_run_static": (C.c_int, [
         C.POINTER(PlanInfo), _vp, _vp, _i64, _i64, C.POINTER(PagedCacheStruct), _vp, _f32,
         _vp, _vp, _vp]),
+    "nvfp4kv_build_page_table": (C.c_int, [
+        _vp, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _i32, _vp, C.POINTER(StepTableStruct), _vp,
+        _vp]),
+    "nvfp4kv_rope_frequencies": (C.c_int, [_i32, C.POINTER(RopeOptions), _vp]),
+    "nvfp4kv_rope": (C.c_int, [
+        _vp, _i64, _i64, _vp, _i64, _i64, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32,
+        _vp, _i32, _i32, _i32, _i32, _vp, _f32, _vp]),
+    "nvfp4kv_e4m3_append": (C.c_int, [
+        C.POINTER(E4m3CacheStruct), _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32, _vp, _vp, _vp,
+        _vp, _i32, _vp, _vp]),
+    "nvfp4kv_e4m3_decode_run": (C.c_int, [
+        C.POINTER(PlanInfo), _vp, _i64, _i64, _i32, C.POINTER(E4m3CacheStruct), _vp, _f32, _vp,
+        _u64, _vp, _vp, _vp]),
 }
 
 

@@ -33,7 +33,6 @@ int fail(int status, const char* fmt, ...);
 }
 
 namespace nvfp4kv {
-// Record a message for nvfp4kv_last_error_detail() and return `status`.
 int set_error_detail(int status, const char* message) { return fail(status, "%s", message); }
 }  // namespace nvfp4kv
 
@@ -138,11 +137,12 @@ CacheView view_of(const nvfp4kv_paged_cache* c) {
   return v;
 }
 
-bool lookup_kernel(int kind, int dk, int dv, int rows, AttendConfig* cfg) {
+bool lookup_kernel(int kind, int dk, int dv, int page_size, int rows, AttendConfig* cfg) {
   if (kind == kKernelTensorCore) return attend_config_tc(dk, dv, rows, cfg);
   if (kind == kKernelCudaCore) return attend_config_simt(dk, dv, rows, cfg);
   if (kind == kKernelTcgen05) return attend_config_tcgen05(dk, dv, rows, cfg);
   if (kind == kKernelFp4QP) return attend_config_tc_fp4qp(dk, dv, rows, 2, cfg);
+  if (kind == kKernelE4m3) return attend_config_e4m3(dk, dv, page_size, rows, cfg);
   return false;
 }
 
@@ -301,7 +301,7 @@ int nvfp4kv_decode_plan(const int32_t* qo_indptr_h, const int32_t* kv_indptr_h,
                 "force_chunk_tokens %d must be a non-negative multiple of 16",
                 opts.force_chunk_tokens);
   if (opts.max_splits < 0 || opts.num_sms < 0 || opts.ctas_per_sm < 0 || opts.kernel < 0 ||
-      opts.kernel > 4)
+      opts.kernel > kKernelE4m3)
     return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "bad plan option");
   const int G = num_qo_heads / num_kv_heads;
 
@@ -353,12 +353,14 @@ int nvfp4kv_decode_plan(const int32_t* qo_indptr_h, const int32_t* kv_indptr_h,
   if (kind == 0)
     kind = (head_dim_qk == 128 && head_dim_vo == 128 && max_rows > 16) ? kKernelTcgen05
                                                                        : kKernelTensorCore;
-  const int want_rows = kind == kKernelTcgen05 ? std::max(max_rows, 1) : (max_rows <= 8 ? 8 : 16);
-  if (!lookup_kernel(kind, head_dim_qk, head_dim_vo, want_rows, &cfg))
+  const int want_rows = kind == kKernelTcgen05 || kind == kKernelE4m3 ? std::max(max_rows, 1)
+                                                                      : (max_rows <= 8 ? 8 : 16);
+  if (!lookup_kernel(kind, head_dim_qk, head_dim_vo, page_size, want_rows, &cfg))
     return fail(NVFP4KV_ERR_UNSUPPORTED, "no %s kernel for head dims (%d, %d)%s",
                 kind == kKernelTensorCore ? "tensor-core"
                 : kind == kKernelTcgen05  ? "tcgen05"
                 : kind == kKernelFp4QP    ? "FP4 query/probability"
+                : kind == kKernelE4m3     ? "E4M3-cache"
                                           : "CUDA-core",
                 head_dim_qk, head_dim_vo,
                 kind == kKernelFp4QP && want_rows > 8 ? " and more than 8 query rows per kv head"
@@ -604,15 +606,10 @@ int nvfp4kv_decode_plan(const int32_t* qo_indptr_h, const int32_t* kv_indptr_h,
 
 namespace {
 
-int check_run(const nvfp4kv_plan_info* info, const void* q, int64_t qst, int64_t qsh,
-              const nvfp4kv_paged_cache* cache, const int32_t* kv_indices,
-              const void* workspace, uint64_t workspace_bytes, const void* out) {
-  if (!info || info->magic != kPlanMagic)
-    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "info is not a plan");
-  if (int st = check_cache(cache, true)) return st;
-  if (cache->num_kv_heads != info->num_kv_heads || cache->head_dim_qk != info->head_dim_qk ||
-      cache->head_dim_vo != info->head_dim_vo || cache->page_size != info->page_size)
-    return fail(NVFP4KV_ERR_PLAN_MISMATCH, "cache dims differ from the plan");
+// The checks of a run apart from its cache: plan, workspace, device, query.
+int check_plan_run(const nvfp4kv_plan_info* info, const void* q, int64_t qst, int64_t qsh,
+                   const int32_t* kv_indices, const void* workspace, uint64_t workspace_bytes,
+                   const void* out) {
   if (!workspace || workspace_bytes < info->workspace_bytes || !aligned(workspace, 256))
     return fail(NVFP4KV_ERR_WORKSPACE_TOO_SMALL, "workspace needs %llu bytes, 256-aligned",
                 (unsigned long long)info->workspace_bytes);
@@ -631,6 +628,49 @@ int check_run(const nvfp4kv_plan_info* info, const void* q, int64_t qst, int64_t
     return fail(NVFP4KV_ERR_INVALID_ARGUMENT,
                 "q must be 16-byte aligned with strides multiple of 8 elements");
   return NVFP4KV_OK;
+}
+
+int check_run(const nvfp4kv_plan_info* info, const void* q, int64_t qst, int64_t qsh,
+              const nvfp4kv_paged_cache* cache, const int32_t* kv_indices,
+              const void* workspace, uint64_t workspace_bytes, const void* out) {
+  if (!info || info->magic != kPlanMagic)
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "info is not a plan");
+  if (int st = check_cache(cache, true)) return st;
+  if (cache->num_kv_heads != info->num_kv_heads || cache->head_dim_qk != info->head_dim_qk ||
+      cache->head_dim_vo != info->head_dim_vo || cache->page_size != info->page_size)
+    return fail(NVFP4KV_ERR_PLAN_MISMATCH, "cache dims differ from the plan");
+  if (info->kernel == kKernelE4m3)
+    return fail(NVFP4KV_ERR_PLAN_MISMATCH, "plan made for the E4M3 cache (kernel 5)");
+  return check_plan_run(info, q, qst, qsh, kv_indices, workspace, workspace_bytes, out);
+}
+
+// The launch parameters that every attention kernel shares.
+AttendParams run_params(const nvfp4kv_plan_info* info, const void* q, int64_t qst, int64_t qsh,
+                        const CacheView& view, const int32_t* kv_indices, void* workspace,
+                        void* out, float* lse) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  AttendParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_stride_tok = qst;
+  p.q_stride_head = qsh;
+  p.cache = view;
+  p.kv_indices = kv_indices;
+  p.units = reinterpret_cast<const WorkUnit*>(ws + info->off_units);
+  p.num_units = info->num_units;
+  p.num_qo_heads = info->num_qo_heads;
+  p.group = info->num_qo_heads / info->num_kv_heads;
+  p.causal = info->causal;
+  p.split = info->split;
+  p.page_size = info->page_size;
+  p.out_f16 = info->out_dtype == 1;
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.partial_o = reinterpret_cast<float*>(ws + info->off_partial_o);
+  p.partial_lse = reinterpret_cast<float*>(ws + info->off_partial_lse);
+  p.counters = reinterpret_cast<int*>(ws + info->off_counters);
+  p.flags = reinterpret_cast<uint32_t*>(ws + info->off_flags);
+  p.live_last_page_len = info->device_last_page_len;
+  return p;
 }
 
 }  // namespace
@@ -682,36 +722,17 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
                    attend_config_dec(info->head_dim_qk, info->head_dim_vo, 8,
                                      info->num_units <= info->num_sms ? 1 : 4, &cfg);
   if (!dec && !lookup_kernel(info->kernel, info->head_dim_qk, info->head_dim_vo,
-                             info->rows_per_block, &cfg))
+                             info->page_size, info->rows_per_block, &cfg))
     return fail(NVFP4KV_ERR_UNSUPPORTED, "planned kernel not available");
   cudaError_t e = prepare_kernel(cfg);
   if (e != cudaSuccess) return cuda_fail(e, "kernel attributes");
   if (!(sm_scale > 0.f)) sm_scale = 1.0f / std::sqrt(static_cast<float>(info->head_dim_qk));
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  AttendParams p{};
-  p.q = static_cast<const uint16_t*>(q_bf16);
-  p.q_stride_tok = q_stride_tok;
-  p.q_stride_head = q_stride_head;
-  p.cache = view_of(cache);
-  p.kv_indices = kv_indices;
-  p.units = reinterpret_cast<const WorkUnit*>(ws + info->off_units);
-  p.num_units = info->num_units;
-  p.num_qo_heads = info->num_qo_heads;
-  p.group = info->num_qo_heads / info->num_kv_heads;
-  p.causal = info->causal;
-  p.split = info->split;
-  p.page_size = info->page_size;
-  p.out_f16 = info->out_dtype == 1;
+  AttendParams p = run_params(info, q_bf16, q_stride_tok, q_stride_head, view_of(cache),
+                              kv_indices, workspace, out_bf16, lse);
   p.qk_scale_log2 = static_cast<float>(static_cast<double>(sm_scale) *
                                        cache->k_global_scale * 1.4426950408889634);
   p.v_scale = cache->v_global_scale;
-  p.out = static_cast<uint16_t*>(out_bf16);
-  p.lse = lse;
-  p.partial_o = reinterpret_cast<float*>(ws + info->off_partial_o);
-  p.partial_lse = reinterpret_cast<float*>(ws + info->off_partial_lse);
-  p.counters = reinterpret_cast<int*>(ws + info->off_counters);
-  p.flags = reinterpret_cast<uint32_t*>(ws + info->off_flags);
-  p.live_last_page_len = info->device_last_page_len;
   if (nt) {
     p.new_k = static_cast<const uint16_t*>(nt->k);
     p.new_v = static_cast<const uint16_t*>(nt->v);
@@ -744,6 +765,43 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
 }
 
 }  // namespace
+
+namespace nvfp4kv {
+
+int attend_e4m3(const nvfp4kv_plan_info* info, const void* q, int64_t q_stride_tok,
+                int64_t q_stride_head, int32_t q_dtype, const CacheView& view, int num_kv_heads,
+                int page_size, int head_dim_qk, int head_dim_vo, const int32_t* kv_indices,
+                float sm_scale, void* workspace, uint64_t workspace_bytes, void* out, float* lse,
+                cudaStream_t stream) {
+  if (!info || info->magic != kPlanMagic)
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "info is not a plan");
+  if (info->kernel != kKernelE4m3)
+    return fail(NVFP4KV_ERR_PLAN_MISMATCH, "the E4M3 cache needs a plan with kernel = 5");
+  if (num_kv_heads != info->num_kv_heads || head_dim_qk != info->head_dim_qk ||
+      head_dim_vo != info->head_dim_vo || page_size != info->page_size)
+    return fail(NVFP4KV_ERR_PLAN_MISMATCH, "cache dims differ from the plan");
+  if (int st = check_plan_run(info, q, q_stride_tok, q_stride_head, kv_indices, workspace,
+                              workspace_bytes, out))
+    return st;
+  if (info->num_units == 0) return ok();
+  AttendConfig cfg{};
+  if (!lookup_kernel(kKernelE4m3, info->head_dim_qk, info->head_dim_vo, info->page_size,
+                     info->rows_per_block, &cfg))
+    return fail(NVFP4KV_ERR_UNSUPPORTED, "planned kernel not available");
+  cudaError_t e = prepare_kernel(cfg);
+  if (e != cudaSuccess) return cuda_fail(e, "kernel attributes");
+  if (!(sm_scale > 0.f)) sm_scale = 1.0f / std::sqrt(static_cast<float>(info->head_dim_qk));
+  AttendParams p = run_params(info, q, q_stride_tok, q_stride_head, view, kv_indices, workspace,
+                              out, lse);
+  p.qk_scale_log2 = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
+  p.v_scale = 1.f;
+  p.q_f16 = q_dtype;
+  e = launch_attend(cfg, p, info->num_units, info->row_blocks, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  return ok();
+}
+
+}  // namespace nvfp4kv
 
 extern "C" {
 

@@ -1,0 +1,500 @@
+// attend_e4m3.cu -- attention over a paged cache of E4M3 codes with one scale
+// per page and kv head, blocks of at most 8 query rows, sm_103a.
+//
+// With a_j, b_j the K and V scale of token j's page and c_j, d_j its codes:
+//   s_j = sm_scale * a_j * (q . c_j),  o = sum_j p_j b_j d_j / sum_j p_j,
+//   p_j = exp(s_j), over the keys that the row sees; lse = ln sum_j p_j.
+//  * Codes are exact in f16 (cvt.rn.f16x2.e4m3x2), so both products run on
+//    mma.sync m16n8k16 with f16 operands and f32 accumulators, and no element
+//    is multiplied by a scale: a_j joins the row's factor of the score, and
+//    b_j joins the exponent.  With x_j the score in log2 units the value
+//    weight is p'_j = 2^(x_j + log2 b_j - m), and the row sum takes
+//    p'_j * 2^(-log2 b_j), so m may follow x + log2 b: p' <= 2^8 then fits
+//    f16 for any scales, and the partial states are ordinary ones.
+//  * A warp owns every WARPS-th tile of 16 tokens (one page, or sixteen
+//    1-token pages) and streams its K rows, V rows and scales through a ring
+//    of STAGES stages with cp.async, rows and pages at any byte strides.
+//  * S^T = C Q^T (M = 16 tokens, N = 8 query rows): a lane's 16 contiguous
+//    bytes of a K row are the A operand of four k-steps under a permutation
+//    of the dims that Q's fragments share.  O^T += D^T P'^T with P' kept in
+//    registers (movmatrix); the A operand interleaves two V rows bytewise.
+//  * K chunks are stored xor 4 on odd rows and V chunks xor the row's bits
+//    1-2, and a tile's tokens are taken in the order m -> m ^ ((m >> 1) & 1),
+//    so the lanes' 16-byte reads hit distinct banks.
+//  * The maximum is raised only when a value exceeds it by more than 2^8.
+// HBM bounds it: Dk + Dv bytes a token and kv head.
+#include <cstdint>
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "device_common.cuh"
+#include "epilogue.cuh"
+#include "internal.h"
+
+namespace nvfp4kv {
+namespace {
+
+using namespace dev;
+
+constexpr float kRaiseLog2 = 8.f;
+constexpr float kMinScale = 0x1p-64f, kMaxScale = 0x1p64f;
+
+template <int DK, int DV, int WARPS, int STAGES>
+struct E4Traits {
+  static constexpr int RB = 8;
+  static constexpr int K_BYTES = 16 * DK, V_BYTES = 16 * DV;
+  static constexpr int OFF_V = K_BYTES, OFF_SC = OFF_V + V_BYTES;  // 16 K scales, 16 V scales
+  static constexpr int STAGE_BYTES = OFF_SC + 128;
+  static constexpr int KCH = DK / 64;                 // 16-byte chunks of a K row per lane
+  static constexpr int KSTEPS = DK / 16;
+  static constexpr int VCB = DV >= 128 ? 16 : DV / 8;  // V bytes per lane per chunk
+  static constexpr int VCH = DV / 8 / VCB;            // V chunks per lane
+  static constexpr int MT = DV / 16;                  // PV m-tiles
+  static constexpr int PIPE_BYTES = WARPS * STAGES * STAGE_BYTES;
+  static constexpr int COMB_BYTES = WARPS * RB * (DV + 2) * 4;
+  static constexpr int MAIN_BYTES = PIPE_BYTES > COMB_BYTES ? PIPE_BYTES : COMB_BYTES;
+  static constexpr int QROW = DK + 8;                 // f16 elements, padded
+  static constexpr int OFF_Q = MAIN_BYTES;
+  static constexpr int OFF_ROW = OFF_Q + RB * QROW * 2;
+  static constexpr int SMEM = OFF_ROW + 2 * RB * 4 + 16;
+  static_assert(DK % 64 == 0 && DV % 64 == 0, "head dims");
+};
+
+__device__ __forceinline__ int tok_of(int m) { return m ^ ((m >> 1) & 1); }
+
+// physical 16-byte chunk of logical chunk ch of row r
+template <int DK>
+__device__ __forceinline__ int k_pos(int r, int ch) {
+  return DK >= 128 ? ch ^ ((r & 1) << 2) : ch;
+}
+template <int DV>
+__device__ __forceinline__ int v_pos(int r, int ch) {
+  return DV >= 128 ? ch ^ (r & 6) : ch ^ ((r >> 1) & 2);
+}
+
+__device__ __forceinline__ void cp_async_4(uint32_t s, const void* g) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(s), "l"(g));
+}
+__device__ __forceinline__ void cp_async_16a(uint32_t s, const void* g) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(g));
+}
+__device__ __forceinline__ float lds_f32(uint32_t a) { return __uint_as_float(lds_u32<0>(a)); }
+
+// 2^lo <= s <= 2^hi, or the nearer end with the flag set
+__device__ __forceinline__ float checked_scale(float s, uint32_t* flags) {
+  const float c = fminf(fmaxf(s, kMinScale), kMaxScale);
+  if (c != s) atomicOr(flags, 0x20u);
+  return c;
+}
+// log2 of a positive normal float, exact for a power of two
+__device__ __forceinline__ float log2_scale(float s) {
+  const uint32_t u = __float_as_uint(s);
+  float r;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(__uint_as_float((u & 0x7FFFFFu) | 0x3F800000u)));
+  return static_cast<float>(static_cast<int>(u >> 23) - 127) + r;
+}
+
+// P1: 1-token pages
+template <int DK, int DV, int WARPS, int STAGES, int MINB, bool P1>
+__global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const AttendParams p) {
+  using T = E4Traits<DK, DV, WARPS, STAGES>;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint16_t* sQ = reinterpret_cast<uint16_t*>(smem + T::OFF_Q);
+  float* sRowF = reinterpret_cast<float*>(smem + T::OFF_ROW);
+  int* sRowLim = reinterpret_cast<int*>(sRowF + T::RB);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const WorkUnit u = load_unit(p);
+  const int G = p.group, R = G * u.qo_len;
+  const int row0 = blockIdx.y * T::RB;
+  if (row0 >= R) return;
+  const int ntiles = P1 ? (u.num_pages + 15) / 16 : u.num_pages;
+  const int npw = ntiles > warp ? (ntiles - warp + WARPS - 1) / WARPS : 0;
+  const int32_t* pidx = p.kv_indices + u.page_begin;
+  const CacheView& c = p.cache;
+
+  // Page ids: 16-token pages, lane k holds the page of this warp's tile
+  // 32 blk + k; 1-token pages, lane r (and r + 16) the page of row r of the
+  // tile to be copied next.  An id out of the pool reads page 0, flagged.
+  auto checked = [&](int32_t id) -> int32_t {
+    if (id < 0 || id >= c.num_pages) {
+      atomicOr(p.flags, 0x1u);
+      return 0;
+    }
+    return id;
+  };
+  auto load_ids = [&](int blk) -> int32_t {
+    int32_t id = 0;
+    if constexpr (P1) {
+      const int j = (warp + blk * WARPS) * 16 + (lane & 15);
+      if (blk < npw) id = checked(__ldg(pidx + min(j, u.num_pages - 1)));
+    } else {
+      const int j = 32 * blk + lane;
+      if (j < npw) id = checked(__ldg(pidx + warp + j * WARPS));
+    }
+    return id;
+  };
+  int32_t ids_cur = load_ids(0);
+  int32_t ids_nxt = (P1 || npw > 32) ? load_ids(1) : 0;
+
+  // ---- Q rows -------------------------------------------------------------
+  constexpr int QCH = T::RB * DK / 8;
+  constexpr int QPT = (QCH + WARPS * 32 - 1) / (WARPS * 32);
+  uint4 qv[QPT];
+#pragma unroll
+  for (int k = 0; k < QPT; ++k) {
+    const int ci = tid + k * WARPS * 32;
+    const int r = row0 + ci / (DK / 8);
+    qv[k] = make_uint4(0u, 0u, 0u, 0u);
+    if (ci < QCH && r < R)
+      qv[k] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(u.qo_begin + r / G) * p.q_stride_tok +
+                                              (int64_t)(u.h_kv * G + r % G) * p.q_stride_head +
+                                              (ci % (DK / 8)) * 8);
+  }
+  if (tid < T::RB) reinterpret_cast<int*>(sRowF)[tid] = 0;  // per-row amax bits
+  __syncthreads();
+
+  // ---- the tile pipeline ---------------------------------------------------
+  const uint32_t ring = smem_addr(smem) + warp * STAGES * T::STAGE_BYTES;
+  const uint8_t* kb = c.k_data + (int64_t)u.h_kv * c.k_sh;
+  const uint8_t* vb = c.v_data + (int64_t)u.h_kv * c.v_sh;
+  // scales: lanes 0-15 K, 16-31 V, of the page that holds row lane & 15
+  const uint8_t* scb = lane < 16 ? c.k_sf + (int64_t)u.h_kv * c.ksf_sh
+                                 : c.v_sf + (int64_t)u.h_kv * c.vsf_sh;
+  const int64_t scp = lane < 16 ? c.ksf_sp : c.vsf_sp;
+  constexpr int KR = DK / 16, VR = DV / 16;          // 16-byte chunks of a row
+  constexpr int KN = KR / 2, VN = VR / 2;            // copies per lane
+  constexpr int KRI = 32 / KR > 0 ? 32 / KR : 1;     // rows a copy of the warp covers
+  constexpr int VRI = 32 / VR > 0 ? 32 / VR : 1;
+  static_assert(KR <= 32 && VR <= 32, "row chunks");
+  const int kr = lane / KR, kc = lane % KR, vr = lane / VR, vc = lane % VR;
+  // the pages of the tile in a lane's page register
+  auto issue = [&](int32_t ids, int jl, int js) {
+    const uint32_t st = ring + js * T::STAGE_BYTES;
+    const int32_t pg = P1 ? 0 : __shfl_sync(0xffffffffu, ids, jl & 31);
+    const uint8_t* kpage = kb + (int64_t)pg * c.k_sp + 16 * kc;
+    const uint8_t* vpage = vb + (int64_t)pg * c.v_sp + 16 * vc;
+#pragma unroll
+    for (int i = 0; i < KN; ++i) {
+      const int r = kr + i * KRI;
+      const uint8_t* src = P1 ? kpage + (int64_t)__shfl_sync(0xffffffffu, ids, r) * c.k_sp
+                              : kpage + r * c.k_ss;
+      cp_async_16a(st + r * DK + 16 * k_pos<DK>(r, kc), src);
+    }
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+      const int r = vr + i * VRI;
+      const uint8_t* src = P1 ? vpage + (int64_t)__shfl_sync(0xffffffffu, ids, r) * c.v_sp
+                              : vpage + r * c.v_ss;
+      cp_async_16a(st + T::OFF_V + r * DV + 16 * v_pos<DV>(r, vc), src);
+    }
+    cp_async_4(st + T::OFF_SC + 4 * lane, scb + (int64_t)(P1 ? ids : pg) * scp);
+    cp_async_commit();
+  };
+  // tile j of this warp into stage js; ids for it are in ids_cur
+  auto advance = [&](int j, int js) {
+    if (j < npw) {
+      issue(ids_cur, j, js);
+      if (P1 || (j & 31) == 31) {
+        ids_cur = ids_nxt;
+        ids_nxt = load_ids(P1 ? j + 2 : j / 32 + 2);
+      }
+    } else {
+      cp_async_commit();  // one group per tile for the wait count
+    }
+  };
+#pragma unroll
+  for (int j = 0; j < STAGES - 1; ++j) advance(j, j);
+
+  // ---- Q: per-row power-of-two prescale into f16, row limits ---------------
+  auto q2 = [&](uint32_t w) -> float2 {
+    if (p.q_f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return make_float2(bf16_bits_to_f32(w & 0xFFFFu), bf16_bits_to_f32(w >> 16));
+  };
+#pragma unroll
+  for (int k = 0; k < QPT; ++k) {
+    const int ci = tid + k * WARPS * 32;
+    if (ci >= QCH) continue;
+    const uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
+    float am = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = q2(w[j]);
+      am = fmaxf(am, fmaxf(fabsf(x.x), fabsf(x.y)));
+    }
+    atomicMax(reinterpret_cast<int*>(sRowF) + ci / (DK / 8), __float_as_int(am));
+  }
+  __syncthreads();
+  float rowf[QPT];
+#pragma unroll
+  for (int k = 0; k < QPT; ++k) {
+    const int ci = tid + k * WARPS * 32;
+    if (ci >= QCH) continue;
+    const int rr = ci / (DK / 8), r = row0 + rr;
+    const float amax = __int_as_float(reinterpret_cast<const int*>(sRowF)[rr]);
+    int e = 0;  // amax * 2^e in [2^14, 2^15)
+    if (amax > 0.f) e = 14 - (int)((__float_as_uint(amax) >> 23) & 0xFF) + 127;
+    e = max(-120, min(120, e));
+    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+    const uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = q2(w[j]);
+      h[j] = f32x2_to_f16x2(x.x * up, x.y * up);
+    }
+    *reinterpret_cast<uint4*>(sQ + rr * T::QROW + (ci % (DK / 8)) * 8) =
+        make_uint4(h[0], h[1], h[2], h[3]);
+    if (ci % (DK / 8) == 0)
+      sRowLim[rr] = r >= R ? -1 : (p.causal ? (u.kv_len - u.qo_len + r / G) : (u.kv_len - 1));
+    rowf[k] = r >= R ? 0.f : p.qk_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < QPT; ++k) {
+    const int ci = tid + k * WARPS * 32;
+    if (ci < QCH && ci % (DK / 8) == 0) sRowF[ci / (DK / 8)] = rowf[k];
+  }
+  __syncthreads();
+
+  // this lane's query rows 2t and 2t + 1: score factor, -m (m the running
+  // maximum of x + log2 b, once the row has one: bit k of has_max) and sum
+  float f2[2], nm2[2], lrow[2];
+  uint32_t has_max = 0;
+  int min_lim = u.kv_len - 1;
+  for (int rr = 0; rr < T::RB; ++rr)
+    if (sRowLim[rr] >= 0) min_lim = min(min_lim, sRowLim[rr]);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    f2[k] = sRowF[2 * t + k];
+    nm2[k] = 0.f;
+    lrow[k] = 0.f;
+  }
+  const int lim0 = sRowLim[2 * t], lim1 = sRowLim[2 * t + 1];
+  auto lane_threshold = [&]() {
+    float th = INFINITY;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      th = fminf(th, (has_max >> k) & 1u ? kRaiseLog2
+                                         : ((k ? lim1 : lim0) >= 0 ? -INFINITY : INFINITY));
+    return th;
+  };
+  float thr_lane = lane_threshold();
+  // Q fragments: k-step 4 cc + m covers the 4 dims 16 (4 cc + t) + 4 m ..
+  uint32_t qreg[T::KSTEPS][2];
+#pragma unroll
+  for (int kk = 0; kk < T::KSTEPS; ++kk) {
+    const uint2 lo = *reinterpret_cast<const uint2*>(sQ + g * T::QROW + 16 * (4 * (kk / 4) + t) +
+                                                     4 * (kk % 4));
+    qreg[kk][0] = lo.x;
+    qreg[kk][1] = lo.y;
+  }
+  float oacc[T::MT][4];
+#pragma unroll
+  for (int mt = 0; mt < T::MT; ++mt)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) oacc[mt][k] = 0.f;
+
+  // rows this lane reads: tokens of mma rows g, g + 8 (K) and of P columns
+  // 2t, 2t + 1, 2t + 8, 2t + 9 (V)
+  const int kr0 = tok_of(g), vt0 = tok_of(2 * t), vt1 = vt0 ^ 1;
+
+#pragma unroll 1
+  for (int i = 0; i < npw; ++i) {
+    const int is = i % STAGES;
+    cp_async_wait<STAGES - 2>();
+    __syncwarp();  // the stage has landed; the one before it has been read
+    advance(i + STAGES - 1, (i + STAGES - 1) % STAGES);
+    const uint32_t st = ring + is * T::STAGE_BYTES;
+    const int tok0 = u.tok_begin + (warp + i * WARPS) * 16;
+
+    // ---- S^T = C Q^T ------------------------------------------------------
+    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int cc = 0; cc < T::KCH; ++cc) {
+      const uint32_t ka = st + kr0 * DK + 16 * k_pos<DK>(kr0, 4 * cc + t);
+      const uint4 a4 = lds_v4<0>(ka), b4 = lds_v4<8 * DK>(ka);
+      const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const uint32_t f[4] = {e4m3x2_to_f16x2(a[m] & 0xFFFFu), e4m3x2_to_f16x2(b[m] & 0xFFFFu),
+                               e4m3x2_to_f16x2(a[m] >> 16), e4m3x2_to_f16x2(b[m] >> 16)};
+        if (m & 1)
+          mma_16816(sb, f, qreg[4 * cc + m][0], qreg[4 * cc + m][1]);
+        else
+          mma_16816(sa, f, qreg[4 * cc + m][0], qreg[4 * cc + m][1]);
+      }
+    }
+    // ---- the tile's scales: tokens kr0 (A) and kr0 + 8 (B) -----------------
+    const uint32_t sc = st + T::OFF_SC + 4 * kr0;
+    const float ksA = checked_scale(lds_f32(sc), p.flags);
+    const float lvA = log2_scale(checked_scale(lds_f32(sc + 64), p.flags));
+    const float ksB = P1 ? checked_scale(lds_f32(sc + 32), p.flags) : ksA;
+    const float lvB = P1 ? log2_scale(checked_scale(lds_f32(sc + 96), p.flags)) : lvA;
+    // x[0..3] = tokens kr0, kr0, kr0 + 8, kr0 + 8 x rows 2t, 2t + 1, 2t, 2t + 1
+    float x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      x[k] = fmaf(sa[k] + sb[k], f2[k & 1] * (k < 2 ? ksA : ksB),
+                  nm2[k & 1] + (k < 2 ? lvA : lvB));
+    if (tok0 + 15 > min_lim) {
+      const int ta = tok0 + kr0, tb = ta + 8;
+      if (ta > lim0) x[0] = -INFINITY;
+      if (ta > lim1) x[1] = -INFINITY;
+      if (tb > lim0) x[2] = -INFINITY;
+      if (tb > lim1) x[3] = -INFINITY;
+    }
+    const bool trig = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) > thr_lane;
+    if (__builtin_expect(__any_sync(0xffffffffu, trig), 0)) {
+      // raise each row's maximum to this tile's (a row's values sit in the 8
+      // lanes of the same t)
+      float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) {
+        mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+        mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
+      }
+      float corr[2] = {1.f, 1.f};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const bool has = (has_max >> k) & 1u;
+        if (mx[k] != -INFINITY && (!has || mx[k] > 0.f)) {
+          if (has) corr[k] = ex2(-mx[k]);
+          nm2[k] -= mx[k];
+          has_max |= 1u << k;
+          x[k] -= mx[k];
+          x[k + 2] -= mx[k];
+        }
+        lrow[k] *= corr[k];
+      }
+      thr_lane = lane_threshold();
+      if (corr[0] != 1.f || corr[1] != 1.f) {
+#pragma unroll
+        for (int mt = 0; mt < T::MT; ++mt) {
+          oacc[mt][0] *= corr[0];
+          oacc[mt][1] *= corr[1];
+          oacc[mt][2] *= corr[0];
+          oacc[mt][3] *= corr[1];
+        }
+      }
+    }
+    const float p0 = ex2(x[0]), p1 = ex2(x[1]), p2 = ex2(x[2]), p3 = ex2(x[3]);
+    const float ivA = ex2(-lvA), ivB = P1 ? ex2(-lvB) : ivA;
+    lrow[0] += p0 * ivA + p2 * ivB;
+    lrow[1] += p1 * ivA + p3 * ivB;
+    const uint32_t pf0 = movmatrix_trans(f32x2_to_f16x2(p0, p1));
+    const uint32_t pf1 = movmatrix_trans(f32x2_to_f16x2(p2, p3));
+
+    // ---- O^T += D^T P'^T ----------------------------------------------------
+    const int valid = u.kv_len - tok0;  // slots past it may hold a NaN code
+#pragma unroll
+    for (int cc = 0; cc < T::VCH; ++cc) {
+      constexpr int VW = T::VCB / 4;
+      uint32_t w[4][VW];  // tokens vt0, vt1, vt0 + 8, vt1 + 8
+      if constexpr (T::VCB == 16) {
+        const uint32_t a0 = st + T::OFF_V + vt0 * DV + 16 * v_pos<DV>(vt0, 8 * cc + g);
+        const uint32_t a1 = st + T::OFF_V + vt1 * DV + 16 * v_pos<DV>(vt1, 8 * cc + g);
+        const uint4 q0 = lds_v4<0>(a0), q1 = lds_v4<0>(a1);
+        const uint4 q2v = lds_v4<8 * DV>(a0), q3 = lds_v4<8 * DV>(a1);
+        w[0][0] = q0.x; w[0][1] = q0.y; w[0][2] = q0.z; w[0][3] = q0.w;
+        w[1][0] = q1.x; w[1][1] = q1.y; w[1][2] = q1.z; w[1][3] = q1.w;
+        w[2][0] = q2v.x; w[2][1] = q2v.y; w[2][2] = q2v.z; w[2][3] = q2v.w;
+        w[3][0] = q3.x; w[3][1] = q3.y; w[3][2] = q3.z; w[3][3] = q3.w;
+      } else {
+        const uint32_t a0 = st + T::OFF_V + vt0 * DV + 16 * v_pos<DV>(vt0, g / 2) + 8 * (g & 1);
+        const uint32_t a1 = st + T::OFF_V + vt1 * DV + 16 * v_pos<DV>(vt1, g / 2) + 8 * (g & 1);
+        const uint2 q0 = lds_v2<0>(a0), q1 = lds_v2<0>(a1);
+        const uint2 q2v = lds_v2<8 * DV>(a0), q3 = lds_v2<8 * DV>(a1);
+        w[0][0] = q0.x; w[0][1] = q0.y;
+        w[1][0] = q1.x; w[1][1] = q1.y;
+        w[2][0] = q2v.x; w[2][1] = q2v.y;
+        w[3][0] = q3.x; w[3][1] = q3.y;
+      }
+      if (valid < 16) {
+#pragma unroll
+        for (int k = 0; k < VW; ++k) {
+          if (vt0 >= valid) w[0][k] = 0;
+          if (vt1 >= valid) w[1][k] = 0;
+          if (vt0 + 8 >= valid) w[2][k] = 0;
+          if (vt1 + 8 >= valid) w[3][k] = 0;
+        }
+      }
+      // m-tile of byte pair m: rows g and g + 8 are the dims of bytes 2m, 2m+1
+#pragma unroll
+      for (int k = 0; k < VW; ++k) {
+        const uint32_t l0 = __byte_perm(w[0][k], w[1][k], 0x5140);
+        const uint32_t h0 = __byte_perm(w[0][k], w[1][k], 0x7362);
+        const uint32_t l1 = __byte_perm(w[2][k], w[3][k], 0x5140);
+        const uint32_t h1 = __byte_perm(w[2][k], w[3][k], 0x7362);
+        const int mt = cc * (T::VCB / 2) + 2 * k;
+        const uint32_t fa[4] = {e4m3x2_to_f16x2(l0 & 0xFFFFu), e4m3x2_to_f16x2(l0 >> 16),
+                                e4m3x2_to_f16x2(l1 & 0xFFFFu), e4m3x2_to_f16x2(l1 >> 16)};
+        const uint32_t fb[4] = {e4m3x2_to_f16x2(h0 & 0xFFFFu), e4m3x2_to_f16x2(h0 >> 16),
+                                e4m3x2_to_f16x2(h1 & 0xFFFFu), e4m3x2_to_f16x2(h1 >> 16)};
+        mma_16816(oacc[mt], fa, pf0, pf1);
+        mma_16816(oacc[mt + 1], fb, pf0, pf1);
+      }
+    }
+  }
+  cp_async_wait<0>();
+
+  // ---- combine the warps ---------------------------------------------------
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) lrow[k] += __shfl_xor_sync(0xffffffffu, lrow[k], o);
+  __syncthreads();  // every warp is done with its ring
+  float* sO = reinterpret_cast<float*>(smem);   // [WARPS][RB][DV]
+  float* sM = sO + WARPS * T::RB * DV;          // [WARPS][RB]
+  float* sL = sM + WARPS * T::RB;               // [WARPS][RB]
+  if (g == 0) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      sM[warp * T::RB + 2 * t + k] = (has_max >> k) & 1u ? -nm2[k] : -INFINITY;
+      sL[warp * T::RB + 2 * t + k] = lrow[k];
+    }
+  }
+#pragma unroll
+  for (int mt = 0; mt < T::MT; ++mt) {
+    constexpr int PC = T::VCB / 2;  // m-tiles of a chunk
+    const int d = (mt / PC) * 128 + g * T::VCB + 2 * (mt % PC);
+    float* o0 = sO + (warp * T::RB + 2 * t) * DV + d;
+    *reinterpret_cast<float2*>(o0) = make_float2(oacc[mt][0], oacc[mt][2]);
+    *reinterpret_cast<float2*>(o0 + DV) = make_float2(oacc[mt][1], oacc[mt][3]);
+  }
+  __syncthreads();
+  finish_unit<T::RB, DV, WARPS>(p, u, row0, R, sM, sL, sO, sRowF);
+}
+
+template <int DK, int DV, int WARPS, int STAGES, int MINB>
+bool make_e4m3(bool page1, AttendConfig* cfg) {
+  using T = E4Traits<DK, DV, WARPS, STAGES>;
+  cfg->kind = kKernelE4m3;
+  cfg->dk = DK;
+  cfg->dv = DV;
+  cfg->rows = T::RB;
+  cfg->warps = WARPS;
+  cfg->smem_bytes = T::SMEM;
+  cfg->units_per_cta = 1;
+  cfg->func = page1
+                  ? reinterpret_cast<const void*>(attend_e4m3_kernel<DK, DV, WARPS, STAGES, MINB, true>)
+                  : reinterpret_cast<const void*>(attend_e4m3_kernel<DK, DV, WARPS, STAGES, MINB, false>);
+  return true;
+}
+
+}  // namespace
+
+bool attend_config_e4m3(int dk, int dv, int page_size, int rows, AttendConfig* cfg) {
+  (void)rows;  // more rows: more row blocks
+  const bool p1 = page_size == 1;
+  if (dk == 64 && dv == 64) return make_e4m3<64, 64, 4, 6, 3>(p1, cfg);
+  if (dk == 128 && dv == 128) return make_e4m3<128, 128, 4, 4, 3>(p1, cfg);
+  if (dk == 256 && dv == 128) return make_e4m3<256, 128, 4, 4, 2>(p1, cfg);
+  if (dk == 256 && dv == 256) return make_e4m3<256, 256, 4, 3, 2>(p1, cfg);
+  if (dk == 512 && dv == 256) return make_e4m3<512, 256, 4, 4, 1>(p1, cfg);
+  return false;
+}
+
+}  // namespace nvfp4kv

@@ -1,0 +1,206 @@
+// e4m3_append.cu -- new tokens into a paged cache of E4M3 codes with one
+// float32 scale per page and kv head, sm_103a.
+//
+// A block is one page of one kv head of K or V.  A step that writes its slots
+// [a, z) computes, with m the largest finite |x| of the new elements,
+//   w = 2^e, the smallest e in [-64, 64] with 448 * 2^e >= m (e = -64 for m = 0),
+//   s = w for a = 0, else max(s_old, w);
+//   new codes  E4M3_RNE_satfinite(x / s);
+//   where s > s_old and a > 0, slots [0, a) are coded anew: E4M3_RNE(code * (s_old / s)).
+// Powers of two lose nothing against m / 448 (codes have their own exponent;
+// the block's largest code lies in (224, 448]), make x / s and the re-coding
+// of normal codes exact, and leave every rounding one decision of the
+// hardware's conversion from float32: x / s is exact but for results below
+// 2^-126, far under the smallest code's half step.  A scale that something
+// else has put in the cache need not be a power of two: x / s is then one
+// correctly rounded division before the conversion.
+//
+// Bound by HBM (2 B in, 1 B out an element) for prompts, by latency for a
+// decode step.  A warp owns a block: its new elements stay in registers
+// between the maximum (one integer redux over the bits of |x|) and the
+// conversion, so each is read once, and no other warp touches the block.
+#include <cstdint>
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "device_common.cuh"
+#include "internal.h"
+
+namespace nvfp4kv {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr float kMinScale = 0x1p-64f, kMaxScale = 0x1p64f;
+
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (F16) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  } else {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+}
+
+// two E4M3 codes, a in the low byte
+__device__ __forceinline__ uint32_t code2(float a, float b) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// the bits of |x| where it is finite, else 0
+__device__ __forceinline__ uint32_t finite_size(float x) {
+  const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
+  return u < 0x7F800000u ? u : 0u;
+}
+
+// 2^e: the smallest power of two with 448 * 2^e >= m, e in [-64, 64].
+// 448 = 1.75 * 2^8, so for m = f * 2^k (1 <= f < 2) e is k - 8, or k - 7 where
+// f > 1.75.
+__device__ __forceinline__ float scale_for(uint32_t m_bits) {
+  int e = static_cast<int>(m_bits >> 23) - 127 - 8 + ((m_bits & 0x7FFFFFu) > 0x600000u);
+  e = max(-64, min(64, e));
+  return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// NCH: 16-byte chunks of new elements a lane holds (16 rows of 16 * NCH dims)
+template <bool F16, int NCH>
+__device__ __forceinline__ void append_block(const E4m3AppendParams& p, int kv, int h, int page,
+                                             int a, int z, int64_t row0, int lane) {
+  const int D = p.dim[kv], per_row = D / 8, n = (z - a) * per_row;
+  const uint16_t* src = p.src[kv] + row0 * p.src_tok[kv] + h * p.src_head[kv];
+  uint8_t* dst = p.data[kv] + page * p.sp[kv] + h * p.sh[kv];
+  float* sc = reinterpret_cast<float*>(p.scale[kv] + page * p.scp[kv] + h * p.sch[kv]);
+  float s_old = a > 0 ? *sc : 0.f;
+  uint4 v[NCH];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = lane + 32 * i;
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (c < n)
+      v[i] = *reinterpret_cast<const uint4*>(src + (c / per_row) * p.src_tok[kv] +
+                                             8 * (c % per_row));
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = unpack2<F16>(w[j]);
+      m = max(m, max(finite_size(x.x), finite_size(x.y)));
+    }
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  float s = scale_for(m);
+  if (a > 0) {
+    if (!(s_old >= kMinScale && s_old <= kMaxScale)) {  // no scale of this format
+      if (lane == 0 && p.flags) atomicOr(p.flags, 0x20u);
+      s_old = kMinScale;
+    }
+    s = fmaxf(s, s_old);
+    if (s > s_old) {
+      const float f = __fdiv_rn(s_old, s);
+      for (int c = lane; c < a * per_row; c += 32) {
+        uint2* at = reinterpret_cast<uint2*>(dst + (c / per_row) * p.ss[kv] + 8 * (c % per_row));
+        const uint2 old = *at;
+        const uint32_t w[2] = {old.x, old.y};
+        uint32_t o[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 lo = unpack2<true>(dev::e4m3x2_to_f16x2(w[j] & 0xFFFFu));
+          const float2 hi = unpack2<true>(dev::e4m3x2_to_f16x2(w[j] >> 16));
+          o[j] = code2(lo.x * f, lo.y * f) | (code2(hi.x * f, hi.y * f) << 16);
+        }
+        *at = make_uint2(o[0], o[1]);
+      }
+    }
+  }
+  const bool exact = (__float_as_uint(s) & 0x7FFFFFu) == 0;  // a power of two
+  const float inv = __uint_as_float((254u << 23) - (__float_as_uint(s) & 0x7F800000u));
+  auto scaled = [&](float x) { return exact ? x * inv : __fdiv_rn(x, s); };
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = lane + 32 * i;
+    if (c >= n) break;
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = unpack2<F16>(w[j]);
+      o[j] = code2(scaled(x.x), scaled(x.y));
+    }
+    *reinterpret_cast<uint2*>(dst + (a + c / per_row) * p.ss[kv] + 8 * (c % per_row)) =
+        make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+  }
+  if (lane == 0) *sc = s;
+}
+
+// CTA (x, y) takes request y; its warps walk the request's (page, head, K or
+// V) blocks.
+template <bool F16, int NCH>
+__global__ void __launch_bounds__(kWarps * 32) e4m3_append_kernel(const E4m3AppendParams p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
+    const int r0 = p.qo_indptr[b], r1 = p.qo_indptr[b + 1];
+    const int k0 = p.kv_indptr[b], k1 = p.kv_indptr[b + 1], last = p.last_page_len[b];
+    const int n = r1 - r0;
+    if (n == 0) continue;
+    const int64_t len = (int64_t)(k1 - k0 - 1) * p.page_size + last;
+    if (r0 < 0 || n < 0 || r1 > p.num_rows || k0 < 0 || k1 <= k0 || last < 1 ||
+        last > p.page_size || len < n) {
+      if (blockIdx.x == 0 && threadIdx.x == 0 && p.flags) atomicOr(p.flags, 0x2u);
+      continue;
+    }
+    const int64_t begin = len - n;
+    const int first = static_cast<int>(begin / p.page_size);
+    const int blocks = 2 * p.num_kv_heads;
+    const int64_t items = (int64_t)(k1 - k0 - first) * blocks;
+    for (int64_t it = (int64_t)blockIdx.x * kWarps + warp; it < items;
+         it += (int64_t)gridDim.x * kWarps) {
+      const int c = first + static_cast<int>(it / blocks), r = static_cast<int>(it % blocks);
+      const int page = p.kv_indices[k0 + c];
+      if (page < 0 || page >= p.num_pages) {
+        if (lane == 0 && p.flags) atomicOr(p.flags, 0x2u);
+        continue;
+      }
+      const int64_t pos = (int64_t)c * p.page_size;
+      const int a = static_cast<int>(max(begin - pos, (int64_t)0));
+      const int z = static_cast<int>(min(len - pos, (int64_t)p.page_size));
+      append_block<F16, NCH>(p, r & 1, r >> 1, page, a, z, r0 + pos + a - begin, lane);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_e4m3_append(const E4m3AppendParams& p, cudaStream_t stream) {
+  if (p.num_rows == 0 || p.batch == 0) return cudaSuccess;
+  // a request's pages are at most its rows, or rows / page_size + 2 of them
+  int64_t pages = p.num_rows / p.page_size + 2;
+  if (pages > p.num_rows) pages = p.num_rows;
+  int64_t gx = (pages * 2 * p.num_kv_heads + kWarps - 1) / kWarps;
+  const int64_t gy = p.batch < 65535 ? p.batch : 65535;
+  // the longest request alone may hold all rows, so every request gets as
+  // many CTAs as that needs, up to a few waves in all
+  const int64_t cap = (152 * 64 + gy - 1) / gy;
+  if (gx > cap) gx = cap;
+  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  const int dmax = p.dim[0] > p.dim[1] ? p.dim[0] : p.dim[1];
+#define NVFP4KV_E4M3_APPEND(NCH_)                                                  \
+  (p.f16 ? e4m3_append_kernel<true, NCH_> : e4m3_append_kernel<false, NCH_>)<<<    \
+      grid, kWarps * 32, 0, stream>>>(p)
+  if (p.page_size == 1 || dmax <= 64)
+    NVFP4KV_E4M3_APPEND(4);
+  else if (dmax <= 128)
+    NVFP4KV_E4M3_APPEND(8);
+  else if (dmax <= 256)
+    NVFP4KV_E4M3_APPEND(16);
+  else
+    NVFP4KV_E4M3_APPEND(32);
+#undef NVFP4KV_E4M3_APPEND
+  return cudaGetLastError();
+}
+
+}  // namespace nvfp4kv

@@ -81,6 +81,7 @@ struct AttendParams {
   //   row_max[((qo_begin + i) * Hq + h) * row_max_splits + s]
   float* row_max;
   int32_t row_max_splits;
+  int32_t q_f16;  // kernel 5: the query's element, 0 bf16, 1 f16
 };
 
 struct AppendParams {
@@ -120,9 +121,57 @@ struct DequantParams {
   uint32_t* flags;
 };
 
+struct PageTableParams {
+  const int32_t* kv_len;
+  const int32_t* qo_len;
+  int32_t* block_table;
+  int64_t table_stride;  // elements between the rows of two requests
+  const int32_t* free_pages;
+  const int32_t* free_head;  // null: 0
+  int32_t batch, page_size, table_width, num_free, max_tokens, max_pages;
+  int32_t* qo_indptr;
+  int32_t* kv_indptr;
+  int32_t* last_page_len;
+  int32_t* kv_indices;
+  int32_t* batch_idx;
+  int32_t* positions;
+  int64_t* slot_map;
+  int32_t* free_head_out;
+  uint32_t* flags;
+};
+
+struct RopeParams {
+  const uint16_t* q;
+  const uint16_t* k;
+  uint16_t* q_out;
+  uint16_t* k_out;
+  int64_t q_st, q_sh, k_st, k_sh;          // strides in elements (token, head)
+  int64_t qo_st, qo_sh, ko_st, ko_sh;
+  const int32_t* positions;
+  const uint64_t* freq;  // [rotary_dim / 2] turns per position, in 2^-64
+  int32_t num_tokens, num_qo_heads, num_kv_heads, head_dim, rotary_dim, interleaved, f16;
+  float attention_factor;
+};
+
+struct E4m3AppendParams {
+  uint8_t* data[2];   // K, V codes
+  uint8_t* scale[2];  // f32 scales, addressed in bytes
+  int64_t sp[2], ss[2], sh[2];  // code strides (page, slot, head), bytes
+  int64_t scp[2], sch[2];       // scale strides (page, head), bytes
+  int32_t dim[2];
+  const uint16_t* src[2];
+  int64_t src_tok[2], src_head[2];  // elements
+  int32_t num_pages, page_size, num_kv_heads, num_rows, batch, f16;
+  const int32_t* qo_indptr;
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices;
+  const int32_t* last_page_len;
+  uint32_t* flags;
+};
+
 // Kernel families and their launch descriptions (defined in the .cu files).
 enum KernelKind { kKernelTensorCore = 1, kKernelCudaCore = 2, kKernelTcgen05 = 3,
-                  kKernelFp4QP = 4 };
+                  kKernelFp4QP = 4, kKernelE4m3 = 5 };
 
 struct AttendConfig {
   int kind;       // KernelKind
@@ -140,6 +189,14 @@ cudaError_t launch_attend(const AttendConfig& cfg, const AttendParams& p,
                           int grid_x, int grid_y, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_dequantize(const DequantParams& p, cudaStream_t stream);
+cudaError_t launch_page_table(const PageTableParams& p, cudaStream_t stream);
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
+cudaError_t launch_e4m3_append(const E4m3AppendParams& p, cudaStream_t stream);
+// The E4M3-cache attention kernel for (dk, dv), a page size of 16 or 1 and
+// blocks of `rows` query rows; false when not built.
+bool attend_config_e4m3(int dk, int dv, int page_size, int rows, AttendConfig* cfg);
+// Record a message for nvfp4kv_last_error_detail() and return `status`.
+int set_error_detail(int status, const char* message);
 cudaError_t launch_merge(const float* o_partial, const float* lse_partial,
                          const int32_t* merge_indptr, int32_t num_entries,
                          int32_t head_dim_vo, uint16_t* out, float* lse, bool out_f16,

@@ -22,7 +22,6 @@
 #include "nvfp4kv.h"
 
 namespace nvfp4kv {
-int set_error_detail(int status, const char* message);
 int validate_run(const nvfp4kv_plan_info* info, const void* q, int64_t qst, int64_t qsh,
                  const nvfp4kv_paged_cache* cache, const int32_t* kv_indices,
                  const void* workspace, uint64_t workspace_bytes, const void* out);
