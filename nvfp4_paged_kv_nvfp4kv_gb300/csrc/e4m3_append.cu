@@ -17,8 +17,9 @@
 //
 // Bound by HBM (2 B in, 1 B out an element) for prompts, by latency for a
 // decode step.  A warp owns a block: its new elements stay in registers
-// between the maximum (one integer redux over the bits of |x|) and the
-// conversion, so each is read once, and no other warp touches the block.
+// between the maximum (on the packed 16-bit patterns) and the conversion, so
+// each is read once, and no other warp touches the block.  The rows' loads do
+// not wait for the page id, which is on its way together with them.
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -49,12 +50,6 @@ __device__ __forceinline__ uint32_t code2(float a, float b) {
   return r;
 }
 
-// the bits of |x| where it is finite, else 0
-__device__ __forceinline__ uint32_t finite_size(float x) {
-  const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
-  return u < 0x7F800000u ? u : 0u;
-}
-
 // 2^e: the smallest power of two with 448 * 2^e >= m, e in [-64, 64].
 // 448 = 1.75 * 2^8, so for m = f * 2^k (1 <= f < 2) e is k - 8, or k - 7 where
 // f > 1.75.
@@ -64,35 +59,48 @@ __device__ __forceinline__ float scale_for(uint32_t m_bits) {
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// NCH: 16-byte chunks of new elements a lane holds (16 rows of 16 * NCH dims)
-template <bool F16, int NCH>
-__device__ __forceinline__ void append_block(const E4m3AppendParams& p, int kv, int h, int page,
-                                             int a, int z, int64_t row0, int lane) {
-  const int D = p.dim[kv], per_row = D / 8, n = (z - a) * per_row;
-  const uint16_t* src = p.src[kv] + row0 * p.src_tok[kv] + h * p.src_head[kv];
-  uint8_t* dst = p.data[kv] + page * p.sp[kv] + h * p.sh[kv];
-  float* sc = reinterpret_cast<float*>(p.scale[kv] + page * p.scp[kv] + h * p.sch[kv]);
-  float s_old = a > 0 ? *sc : 0.f;
+// A lane keeps one 16-byte column of the new rows (two where a row has more
+// than 32, CP) and every rpp-th row: NCH chunks, 16 rows at most.
+template <bool F16, int NCH, int CP>
+__device__ __forceinline__ void append_block(const E4m3AppendParams& p, int kv, int h,
+                                             const int32_t* page_at, int a, int z, int64_t row0,
+                                             int lane) {
+  const int cols = p.dim[kv] / 8, wide = min(32, cols), rpp = 32 / wide;
+  const int col = lane % wide, r0 = lane / wide, rows = r0 < rpp ? z - a : 0;
+  const uint16_t* src = p.src[kv] + (row0 + r0) * p.src_tok[kv] + h * p.src_head[kv] + 8 * col;
   uint4 v[NCH];
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int c = lane + 32 * i;
+    const int r = (i / CP) * rpp, c = (i % CP) * 256;  // row step, column step
     v[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (c < n)
-      v[i] = *reinterpret_cast<const uint4*>(src + (c / per_row) * p.src_tok[kv] +
-                                             8 * (c % per_row));
+    if (r0 + r < rows && 8 * col + c < p.dim[kv])
+      v[i] = *reinterpret_cast<const uint4*>(src + r * p.src_tok[kv] + c);
   }
-  uint32_t m = 0;
+  const int page = *page_at;  // on its way together with the rows
+  if (page < 0 || page >= p.num_pages) {
+    if (lane == 0 && p.flags) atomicOr(p.flags, 0x2u);
+    return;
+  }
+  uint8_t* dst = p.data[kv] + page * p.sp[kv] + h * p.sh[kv] + 8 * col;
+  float* sc = reinterpret_cast<float*>(p.scale[kv] + page * p.scp[kv] + h * p.sch[kv]);
+  float s_old = a > 0 ? *sc : 0.f;
+  // largest |x|, two 16-bit patterns at a time (their order is that of the
+  // sizes); non-finite values are left out only when there are any
+  constexpr uint32_t kInf = F16 ? 0x7C00u : 0x7F80u;
+  auto largest = [&](auto keep) {
+    uint32_t m2 = 0;
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    for (int i = 0; i < NCH; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 x = unpack2<F16>(w[j]);
-      m = max(m, max(finite_size(x.x), finite_size(x.y)));
+      for (int j = 0; j < 4; ++j) m2 = __vmaxu2(m2, keep(w[j] & 0x7FFF7FFFu));
     }
-  }
-  m = __reduce_max_sync(0xffffffffu, m);
+    return __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+  };
+  uint32_t m = largest([](uint32_t w) { return w; });
+  if (m >= kInf)
+    m = largest([](uint32_t w) { return w & __vcmpltu2(w, kInf | (kInf << 16)); });
+  m = __float_as_uint(unpack2<F16>(m).x);
   float s = scale_for(m);
   if (a > 0) {
     if (!(s_old >= kMinScale && s_old <= kMaxScale)) {  // no scale of this format
@@ -100,47 +108,54 @@ __device__ __forceinline__ void append_block(const E4m3AppendParams& p, int kv, 
       s_old = kMinScale;
     }
     s = fmaxf(s, s_old);
-    if (s > s_old) {
+    if (s > s_old && r0 < rpp) {
       const float f = __fdiv_rn(s_old, s);
-      for (int c = lane; c < a * per_row; c += 32) {
-        uint2* at = reinterpret_cast<uint2*>(dst + (c / per_row) * p.ss[kv] + 8 * (c % per_row));
-        const uint2 old = *at;
-        const uint32_t w[2] = {old.x, old.y};
-        uint32_t o[2];
+      for (int r = r0; r < a; r += rpp)
+        for (int c = 0; 8 * col + c < p.dim[kv]; c += 256) {
+          uint2* at = reinterpret_cast<uint2*>(dst + r * p.ss[kv] + c);
+          const uint2 old = *at;
+          const uint32_t w[2] = {old.x, old.y};
+          uint32_t o[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 lo = unpack2<true>(dev::e4m3x2_to_f16x2(w[j] & 0xFFFFu));
-          const float2 hi = unpack2<true>(dev::e4m3x2_to_f16x2(w[j] >> 16));
-          o[j] = code2(lo.x * f, lo.y * f) | (code2(hi.x * f, hi.y * f) << 16);
+          for (int j = 0; j < 2; ++j) {
+            const float2 lo = unpack2<true>(dev::e4m3x2_to_f16x2(w[j] & 0xFFFFu));
+            const float2 hi = unpack2<true>(dev::e4m3x2_to_f16x2(w[j] >> 16));
+            o[j] = code2(lo.x * f, lo.y * f) | (code2(hi.x * f, hi.y * f) << 16);
+          }
+          *at = make_uint2(o[0], o[1]);
         }
-        *at = make_uint2(o[0], o[1]);
-      }
     }
   }
-  const bool exact = (__float_as_uint(s) & 0x7FFFFFu) == 0;  // a power of two
-  const float inv = __uint_as_float((254u << 23) - (__float_as_uint(s) & 0x7F800000u));
-  auto scaled = [&](float x) { return exact ? x * inv : __fdiv_rn(x, s); };
+  dst += (a + r0) * p.ss[kv];
+  auto store = [&](auto scaled) {
 #pragma unroll
-  for (int i = 0; i < NCH; ++i) {
-    const int c = lane + 32 * i;
-    if (c >= n) break;
-    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-    uint32_t o[4];
+    for (int i = 0; i < NCH; ++i) {
+      const int r = (i / CP) * rpp, c = (i % CP) * 256;
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 x = unpack2<F16>(w[j]);
-      o[j] = code2(scaled(x.x), scaled(x.y));
+      for (int j = 0; j < 4; ++j) {
+        const float2 x = unpack2<F16>(w[j]);
+        o[j] = code2(scaled(x.x), scaled(x.y));
+      }
+      if (r0 + r < rows && 8 * col + c < p.dim[kv])
+        *reinterpret_cast<uint2*>(dst + r * p.ss[kv] + c) =
+            make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
     }
-    *reinterpret_cast<uint2*>(dst + (a + c / per_row) * p.ss[kv] + 8 * (c % per_row)) =
-        make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+  };
+  if ((__float_as_uint(s) & 0x7FFFFFu) == 0) {  // a power of two: its reciprocal is exact
+    const float inv = __uint_as_float((254u << 23) - (__float_as_uint(s) & 0x7F800000u));
+    store([inv](float x) { return x * inv; });
+  } else {
+    store([s](float x) { return __fdiv_rn(x, s); });
   }
   if (lane == 0) *sc = s;
 }
 
 // CTA (x, y) takes request y; its warps walk the request's (page, head, K or
 // V) blocks.
-template <bool F16, int NCH>
-__global__ void __launch_bounds__(kWarps * 32) e4m3_append_kernel(const E4m3AppendParams p) {
+template <bool F16, int NCH, int CP>
+__global__ void __launch_bounds__(kWarps * 32, NCH <= 8 ? 6 : NCH <= 16 ? 4 : 2) e4m3_append_kernel(const E4m3AppendParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
     const int r0 = p.qo_indptr[b], r1 = p.qo_indptr[b + 1];
@@ -160,15 +175,11 @@ __global__ void __launch_bounds__(kWarps * 32) e4m3_append_kernel(const E4m3Appe
     for (int64_t it = (int64_t)blockIdx.x * kWarps + warp; it < items;
          it += (int64_t)gridDim.x * kWarps) {
       const int c = first + static_cast<int>(it / blocks), r = static_cast<int>(it % blocks);
-      const int page = p.kv_indices[k0 + c];
-      if (page < 0 || page >= p.num_pages) {
-        if (lane == 0 && p.flags) atomicOr(p.flags, 0x2u);
-        continue;
-      }
       const int64_t pos = (int64_t)c * p.page_size;
       const int a = static_cast<int>(max(begin - pos, (int64_t)0));
       const int z = static_cast<int>(min(len - pos, (int64_t)p.page_size));
-      append_block<F16, NCH>(p, r & 1, r >> 1, page, a, z, r0 + pos + a - begin, lane);
+      append_block<F16, NCH, CP>(p, r & 1, r >> 1, p.kv_indices + k0 + c, a, z,
+                                 r0 + pos + a - begin, lane);
     }
   }
 }
@@ -188,17 +199,19 @@ cudaError_t launch_e4m3_append(const E4m3AppendParams& p, cudaStream_t stream) {
   if (gx > cap) gx = cap;
   const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
   const int dmax = p.dim[0] > p.dim[1] ? p.dim[0] : p.dim[1];
-#define NVFP4KV_E4M3_APPEND(NCH_)                                                  \
-  (p.f16 ? e4m3_append_kernel<true, NCH_> : e4m3_append_kernel<false, NCH_>)<<<    \
-      grid, kWarps * 32, 0, stream>>>(p)
-  if (p.page_size == 1 || dmax <= 64)
-    NVFP4KV_E4M3_APPEND(4);
+#define NVFP4KV_E4M3_APPEND(NCH_, CP_)                                     \
+  (p.f16 ? e4m3_append_kernel<true, NCH_, CP_>                            \
+         : e4m3_append_kernel<false, NCH_, CP_>)<<<grid, kWarps * 32, 0, stream>>>(p)
+  if (p.page_size == 1)
+    NVFP4KV_E4M3_APPEND(2, 2);
+  else if (dmax <= 64)
+    NVFP4KV_E4M3_APPEND(4, 1);
   else if (dmax <= 128)
-    NVFP4KV_E4M3_APPEND(8);
+    NVFP4KV_E4M3_APPEND(8, 1);
   else if (dmax <= 256)
-    NVFP4KV_E4M3_APPEND(16);
+    NVFP4KV_E4M3_APPEND(16, 1);
   else
-    NVFP4KV_E4M3_APPEND(32);
+    NVFP4KV_E4M3_APPEND(32, 2);
 #undef NVFP4KV_E4M3_APPEND
   return cudaGetLastError();
 }

@@ -30,6 +30,7 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kChunk = 8;
 constexpr int64_t kMaxLen = (int64_t)1 << 30;  // tokens of a request, as in the planner
 
 struct Sums {
@@ -44,9 +45,8 @@ __device__ __forceinline__ Sums shfl_up(const Sums& a, int o) {
           __shfl_up_sync(0xffffffffu, a.taken, o)};
 }
 
-// the last entry of first[0 .. n) that is <= x (first[0] = 0 <= x)
-__device__ __forceinline__ int owner(const int32_t* first, int n, int x) {
-  int lo = 0, hi = n;  // first[lo] <= x < first[hi]
+// the last entry of first[lo .. hi) that is <= x, where first[lo] <= x < first[hi]
+__device__ __forceinline__ int owner(const int32_t* first, int lo, int hi, int x) {
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (first[mid] <= x) lo = mid; else hi = mid;
@@ -138,36 +138,39 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageTablePar
   if (me == 0) *p.free_head_out = head + (int)total.taken;
 
   const int pages = (int)total.pages, tokens = (int)total.tokens;
-  // four neighbouring pages a thread
-  for (int64_t k0 = 4 * (int64_t)me; k0 < pages; k0 += 4 * (int64_t)nt) {
-    int b = owner(s_kv, B, (int)k0);
-    const int m = min(4, pages - (int)k0);
-    int32_t id[4];
+  // A warp takes kChunk * 32 neighbouring pages at a time: two searches give
+  // the requests they span (one, for long requests nearly always), a lane's
+  // own searches stay between those, and its loads, independent of one
+  // another, are on their way together.
+  const int nw = gridDim.x * kWarps;
+  for (int64_t k0 = (int64_t)(blockIdx.x * kWarps + warp) * (32 * kChunk); k0 < pages;
+       k0 += (int64_t)nw * (32 * kChunk)) {
+    const int first = (int)k0, stop = (int)min(k0 + 32 * kChunk, (int64_t)pages);
+    const int lo = owner(s_kv, 0, B, first);
+    const int hi = stop <= s_kv[lo + 1] ? lo + 1 : owner(s_kv, lo, B, stop - 1) + 1;
+    int32_t id[kChunk];
+    int32_t* enter[kChunk];  // where a taken page goes in the table
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (j >= m) break;
-      const int k = (int)k0 + j;
-      while (k >= s_kv[b + 1]) ++b;  // requests without a page are passed over
-      const int c = k - s_kv[b];
-      const int taken = s_free[b + 1] - s_free[b], held = s_kv[b + 1] - s_kv[b] - taken;
-      int32_t* row = p.block_table + b * p.table_stride;
-      if (c < held) {
-        id[j] = row[c];
-      } else {
-        id[j] = p.free_pages[head + s_free[b] + c - held];
-        row[c] = id[j];
+    for (int j = 0; j < kChunk; ++j) {
+      const int k = first + 32 * j + lane;
+      enter[j] = nullptr;
+      if (k < stop) {
+        const int b = owner(s_kv, lo, hi, k), c = k - s_kv[b];
+        const int taken = s_free[b + 1] - s_free[b], held = s_kv[b + 1] - s_kv[b] - taken;
+        int32_t* at = p.block_table + b * p.table_stride + c;
+        if (c >= held) enter[j] = at;
+        id[j] = c < held ? *at : p.free_pages[head + s_free[b] + c - held];
       }
     }
-    if (m == 4 && (reinterpret_cast<uintptr_t>(p.kv_indices) & 15) == 0) {
-      *reinterpret_cast<int4*>(p.kv_indices + k0) = make_int4(id[0], id[1], id[2], id[3]);
-    } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j < m) p.kv_indices[k0 + j] = id[j];
+    for (int j = 0; j < kChunk; ++j) {
+      const int k = first + 32 * j + lane;
+      if (k < stop) p.kv_indices[k] = id[j];
+      if (enter[j]) *enter[j] = id[j];
     }
   }
   for (int64_t t = me; t < tokens; t += nt) {
-    const int b = owner(s_qo, B, (int)t);
+    const int b = owner(s_qo, 0, B, (int)t);
     const int n = s_qo[b + 1] - s_qo[b];
     const int pos = s_len[b] - n + ((int)t - s_qo[b]);
     p.batch_idx[t] = b;
@@ -193,9 +196,9 @@ cudaError_t launch_page_table(const PageTableParams& p, cudaStream_t stream) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  // one CTA per kThreads groups of four pages or kThreads rows, at most two
-  // an SM: more would only repeat the sums
-  const int64_t work = (int64_t)p.max_pages / 4 + p.max_tokens + 1;
+  // one CTA per kWarps chunks of pages or kThreads rows, at most two an SM:
+  // more would only repeat the sums
+  const int64_t work = (int64_t)p.max_pages / kChunk + p.max_tokens + 1;
   int64_t blocks = (work + kThreads - 1) / kThreads;
   if (blocks > 152 * 2) blocks = 152 * 2;
   page_table_kernel<<<static_cast<int>(blocks), kThreads, smem, stream>>>(p);

@@ -13,9 +13,9 @@
 // Bound by HBM for prompts (each element is read and written once) and by
 // latency for a decode step.  A warp takes one token: its lanes compute the
 // R/2 sines and cosines once (into shared memory), and every lane then keeps
-// the eight (half layout) or four (interleaved) pairs of its 16-byte column in
-// registers and walks the heads, so the angles cost a few percent of a
-// 40-head token.  With few tokens the heads are spread over several warps.
+// the eight pairs of its column in registers and walks the heads, so the
+// angles cost a few percent of a 40-head token.  With few tokens the heads are
+// spread over several warps.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -29,6 +29,13 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMaxPairs = 256;  // rotary_dim / 2
+constexpr int kBatch = 4;       // heads whose loads a lane has in flight
+
+// columns of two 16-byte chunks that make up a head (rope_kernel)
+__host__ __device__ __forceinline__ int rope_columns(const RopeParams& p) {
+  return p.interleaved ? (p.head_dim + 15) / 16
+                       : p.rotary_dim / 16 + (p.head_dim - p.rotary_dim + 15) / 16;
+}
 
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
@@ -77,9 +84,13 @@ __device__ __forceinline__ void angles(const RopeParams& p, int64_t t, float2* s
   __syncwarp();
 }
 
-// 16-byte columns.  Half layout: R % 16 == 0, a column holds pairs 8c .. 8c+7
-// (the elements at 8c and R/2 + 8c).  Interleaved: a column holds pairs
-// 4c .. 4c+3.  Columns past the rotary dims are copied.
+// A lane's item is two 16-byte chunks of a head: in the half layout (R % 16 ==
+// 0) the elements 8c .. 8c+7 and R/2 + 8c .., eight pairs, or two neighbouring
+// chunks of the passing dims; interleaved, the elements 16c .. 16c+15, whose
+// pairs past the rotary dims keep their bits.  A lane keeps its column and
+// walks the heads in batches of kBatch: the loads of a batch are issued before
+// its stores (which might alias them for all the compiler knows), and those of
+// the first batch before the angles.
 template <bool F16, bool INTER>
 __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeParams p, int splits) {
   __shared__ __align__(16) float2 s_sc[kWarps][kMaxPairs];
@@ -89,68 +100,78 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeParams p, i
   const int part = static_cast<int>(unit % splits);
   if (t >= p.num_tokens) return;
   float2* sc = s_sc[warp];
-  angles(p, t, sc, lane);
   const int heads = p.num_qo_heads + p.num_kv_heads;
   const int half = p.rotary_dim / 2;
-  const int rcols = INTER ? (half + 3) / 4 : half / 8;  // columns with pairs
-  const int c0 = INTER ? rcols : half / 4;              // first passing 16-byte column
-  const int cols = rcols + p.head_dim / 8 - c0;         // work columns of a head
-  // lanes: column x head; a column keeps its pairs over the heads it walks
-  const int wide = min(32, cols);
-  const int hl = 32 / wide;                             // heads side by side
-  const int my_h = lane / wide;
-  if (my_h >= hl) return;
+  const int rcols = INTER ? 0 : half / 8;  // half layout: columns of pairs, then passing ones
+  const int cols = rope_columns(p);
+  const int wide = min(32, cols), side = 32 / wide;  // heads side by side
+  const int step = splits * side, h0 = part * side + lane / wide;
+  const bool idle = lane / wide >= side;
+  uint4 va[kBatch], vb[kBatch];
+  // the column's two chunks: elements d0 .., d1 .. (d1 may lie past the head)
+  auto chunk0 = [&](int c) { return INTER ? 16 * c : c < rcols ? 8 * c : 2 * half + 16 * (c - rcols); };
+  auto chunk1 = [&](int c) { return !INTER && c < rcols ? half + 8 * c : chunk0(c) + 8; };
+  auto load = [&](int c, int h1) {
+    const int d0 = chunk0(c), d1 = chunk1(c);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int h = h1 + k * step;
+      if (h < heads) {
+        const uint16_t* in = row_of(p, t, h).in;
+        va[k] = *reinterpret_cast<const uint4*>(in + d0);
+        vb[k] = d1 < p.head_dim ? *reinterpret_cast<const uint4*>(in + d1)
+                                : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  };
+  if (!idle && lane % wide < cols) load(lane % wide, h0);
+  angles(p, t, sc, lane);
+  if (idle) return;
   for (int c = lane % wide; c < cols; c += wide) {
-    if (c >= rcols) {  // passing dims
-      const int d = 8 * (c - rcols + c0);
-      for (int h = part * hl + my_h; h < heads; h += splits * hl) {
-        const Row r = row_of(p, t, h);
-        if (r.in != r.out)
-          *reinterpret_cast<uint4*>(r.out + d) = *reinterpret_cast<const uint4*>(r.in + d);
-      }
-      continue;
+    const int d0 = chunk0(c), d1 = chunk1(c);
+    // pairs of this column that turn (8 unless the rotary dims end in it)
+    const int live = INTER ? min(8, max(0, half - 8 * c)) : c < rcols ? 8 : 0;
+    float cs[8], sn[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float2 x = j < live ? sc[8 * c + j] : make_float2(1.f, 0.f);
+      cs[j] = x.x;
+      sn[j] = x.y;
     }
-    constexpr int NP = INTER ? 4 : 8;
-    float cs[NP], sn[NP];
+    if (c >= wide) load(c, h0);
+    for (int h1 = h0; h1 < heads; h1 += kBatch * step) {
+      if (h1 > h0) load(c, h1);
 #pragma unroll
-    for (int j = 0; j < NP; ++j) {
-      const bool in = !INTER || NP * c + j < half;
-      cs[j] = in ? sc[NP * c + j].x : 1.f;
-      sn[j] = in ? sc[NP * c + j].y : 0.f;
-    }
-    if constexpr (INTER) {
-      const int live = min(NP, half - NP * c);  // below 4 where the rotary dims end
-#pragma unroll 4
-      for (int h = part * hl + my_h; h < heads; h += splits * hl) {
-        const Row r = row_of(p, t, h);
-        const uint4 v = *reinterpret_cast<const uint4*>(r.in + 8 * c);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t o[4];
+      for (int k = 0; k < kBatch; ++k) {
+        const int h = h1 + k * step;
+        if (h >= heads) break;
+        uint32_t a[4] = {va[k].x, va[k].y, va[k].z, va[k].w};
+        uint32_t b[4] = {vb[k].x, vb[k].y, vb[k].z, vb[k].w};
+        if constexpr (INTER) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 x = unpack2<F16>(w[j]);
-          const uint32_t y = pack2<F16>(x.x * cs[j] - x.y * sn[j], x.y * cs[j] + x.x * sn[j]);
-          o[j] = j < live ? y : w[j];
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = unpack2<F16>(a[j]), y = unpack2<F16>(b[j]);
+            const uint32_t oa = pack2<F16>(x.x * cs[j] - x.y * sn[j], x.y * cs[j] + x.x * sn[j]);
+            const uint32_t ob = pack2<F16>(y.x * cs[j + 4] - y.y * sn[j + 4],
+                                           y.y * cs[j + 4] + y.x * sn[j + 4]);
+            a[j] = j < live ? oa : a[j];
+            b[j] = j + 4 < live ? ob : b[j];
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = unpack2<F16>(a[j]), y = unpack2<F16>(b[j]);
+            const float c0 = cs[2 * j], c1 = cs[2 * j + 1], s0 = sn[2 * j], s1 = sn[2 * j + 1];
+            const uint32_t oa = pack2<F16>(x.x * c0 - y.x * s0, x.y * c1 - y.y * s1);
+            const uint32_t ob = pack2<F16>(y.x * c0 + x.x * s0, y.y * c1 + x.y * s1);
+            a[j] = live ? oa : a[j];
+            b[j] = live ? ob : b[j];
+          }
         }
-        *reinterpret_cast<uint4*>(r.out + 8 * c) = make_uint4(o[0], o[1], o[2], o[3]);
-      }
-    } else {
-#pragma unroll 4
-      for (int h = part * hl + my_h; h < heads; h += splits * hl) {
-        const Row r = row_of(p, t, h);
-        const uint4 va = *reinterpret_cast<const uint4*>(r.in + 8 * c);
-        const uint4 vb = *reinterpret_cast<const uint4*>(r.in + half + 8 * c);
-        const uint32_t a[4] = {va.x, va.y, va.z, va.w}, b[4] = {vb.x, vb.y, vb.z, vb.w};
-        uint32_t oa[4], ob[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 x = unpack2<F16>(a[j]), y = unpack2<F16>(b[j]);
-          const float c0f = cs[2 * j], c1f = cs[2 * j + 1], s0f = sn[2 * j], s1f = sn[2 * j + 1];
-          oa[j] = pack2<F16>(x.x * c0f - y.x * s0f, x.y * c1f - y.y * s1f);
-          ob[j] = pack2<F16>(y.x * c0f + x.x * s0f, y.y * c1f + x.y * s1f);
-        }
-        *reinterpret_cast<uint4*>(r.out + 8 * c) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
-        *reinterpret_cast<uint4*>(r.out + half + 8 * c) = make_uint4(ob[0], ob[1], ob[2], ob[3]);
+        uint16_t* out = row_of(p, t, h).out;
+        *reinterpret_cast<uint4*>(out + d0) = make_uint4(a[0], a[1], a[2], a[3]);
+        if (d1 < p.head_dim)
+          *reinterpret_cast<uint4*>(out + d1) = make_uint4(b[0], b[1], b[2], b[3]);
       }
     }
   }
@@ -191,8 +212,7 @@ cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
   const bool odd = !p.interleaved && p.rotary_dim % 16 != 0;
   // Heads over several warps while the tokens alone leave SMs without one; a
   // warp has `side` heads side by side (the columns of rope_kernel).
-  const int half = p.rotary_dim / 2;
-  const int cols = p.interleaved ? p.head_dim / 8 : half / 8 + (p.head_dim - p.rotary_dim) / 8;
+  const int cols = rope_columns(p);
   const int side = odd || cols >= 32 ? 1 : 32 / cols;
   const int most = (heads + side - 1) / side;
   int splits = (152 * kWarps * 2 + p.num_tokens - 1) / p.num_tokens;

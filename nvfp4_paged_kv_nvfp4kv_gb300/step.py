@@ -4,11 +4,12 @@ the E4M3 cache with its attention.
 
 Argument marshalling only, as in ``api``.  Tensors are checked for device,
 type and shape here, because a pointer carries none of them; what the library
-can check it checks itself (``NvFp4KvError``).
+can check it checks itself (``NvFp4KvError``).  A decode step waits for these
+calls, so they take what they need of a tensor once and keep what belongs to a
+plan or a cache.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 from typing import Optional
 
@@ -16,7 +17,7 @@ import torch
 
 from . import _lib
 from ._lib import E4m3CacheStruct, RopeOptions, StepTableStruct, check
-from .api import Plan, _outputs
+from .api import Plan
 
 __all__ = ["StepTable", "nvfp4kv_build_page_table", "RopePlan", "nvfp4kv_rope_plan",
            "nvfp4kv_rope", "E4m3Cache", "nvfp4kv_e4m3_append", "nvfp4kv_e4m3_decode_run"]
@@ -24,13 +25,21 @@ __all__ = ["StepTable", "nvfp4kv_build_page_table", "RopePlan", "nvfp4kv_rope_pl
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1}
 
 
-def _device(*tensors) -> int:
-    """The one CUDA device of the tensors, which has to be the current one."""
-    dev = torch.cuda.current_device()
+_fn = {}
+
+
+def _entry(name):
+    """The library's function, looked up once."""
+    fn = _fn.get(name)
+    if fn is None:
+        fn = _fn[name] = getattr(_lib.load(), name)
+    return fn
+
+
+def _wrong_device(dev, *tensors):
     for t in tensors:
         if t.get_device() != dev:
             raise ValueError("tensor on %s, the current device is cuda:%d" % (t.device, dev))
-    return dev
 
 
 def _ints(dtype, **tensors):
@@ -39,29 +48,30 @@ def _ints(dtype, **tensors):
             raise ValueError("%s must be contiguous %s" % (name, dtype))
 
 
-def _flag_ptr(flags):
+def _flag_ptr(flags, dev):
     if flags is None:
         return None
     if flags.dtype not in (torch.int32, torch.uint32) or flags.numel() < 1:
         raise ValueError("device_flags must be a 32-bit integer tensor")
-    _device(flags)
+    _wrong_device(dev, flags)
     return flags.data_ptr()
 
 
-def _stream_of(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+def _stream_of(stream, dev):
+    if stream is None:  # (torch.cuda.current_stream() builds an object on every call)
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _on(stream):
-    """Where the outputs of a call on `stream` are allocated: the caching
-    allocator then keeps their memory in that stream's order."""
+def _empty(shape, dtype, device, stream):
+    """An output of a call on `stream`, allocated in that stream's order (the
+    caching allocator may hand its memory on as soon as it is freed)."""
     if stream is None:
-        return contextlib.nullcontext()
+        return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
-    return torch.cuda.stream(stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 # ---- the step's page table ------------------------------------------------------
@@ -88,8 +98,10 @@ class StepTable:
             raise ValueError("batch_idx, positions and slot_map must have one length")
         if free_head.numel() < 1:
             raise ValueError("free_head is empty")
-        self._tensors = [t for t in (qo_indptr, kv_indptr, last_page_len, kv_indices, batch_idx,
-                                     positions, slot_map, free_head) if t is not None]
+        tensors = [t for t in (qo_indptr, kv_indptr, last_page_len, kv_indices, batch_idx,
+                               positions, slot_map, free_head) if t is not None]
+        if len({t.device for t in tensors}) != 1:
+            raise ValueError("the table's tensors are on different devices")
         s = StepTableStruct()
         for name in ("qo_indptr", "kv_indptr", "last_page_len", "kv_indices", "batch_idx",
                      "positions", "slot_map", "free_head"):
@@ -120,13 +132,16 @@ def nvfp4kv_build_page_table(kv_len, qo_len, block_table, free_pages, free_head,
     batch = table.batch
     if not (kv_len.numel() == qo_len.numel() == block_table.shape[0] == batch):
         raise ValueError("kv_len, qo_len and block_table must have the table's batch")
-    _device(kv_len, qo_len, block_table, free_pages, table.kv_indptr,
-            *(() if free_head is None else (free_head,)))
-    check(_lib.load().nvfp4kv_build_page_table(
+    dev = torch.cuda.current_device()
+    _wrong_device(dev, kv_len, qo_len, block_table, free_pages, table.kv_indptr,
+                  *(() if free_head is None else (free_head,)))
+    st = _entry("nvfp4kv_build_page_table")(
         kv_len.data_ptr(), qo_len.data_ptr(), batch, page_size, block_table.data_ptr(),
         block_table.stride(0), block_table.shape[1], free_pages.data_ptr(), free_pages.numel(),
         None if free_head is None else free_head.data_ptr(), table._struct,
-        _flag_ptr(device_flags), _stream_of(stream)), "nvfp4kv_build_page_table")
+        _flag_ptr(device_flags, dev), _stream_of(stream, dev))
+    if st:
+        check(st, "nvfp4kv_build_page_table")
     return table
 
 
@@ -161,12 +176,15 @@ def nvfp4kv_rope_plan(head_dim: int, rotary_dim: Optional[int] = None, base: flo
 
 
 def _rows(name, t, head_dim, tokens, dtype):
-    if t.dim() != 3 or t.shape[2] != head_dim or t.stride(2) != 1:
+    """Check [tokens, heads, head_dim]; returns the strides and the heads."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3 or shape[2] != head_dim or strides[2] != 1:
         raise ValueError("%s must be [tokens, heads, %d] with contiguous rows" % (name, head_dim))
     if t.dtype != dtype:
         raise ValueError("%s must be %s" % (name, dtype))
-    if t.shape[0] < tokens:
-        raise ValueError("%s has fewer rows than positions" % name)
+    if shape[0] < tokens:
+        raise ValueError("%s has fewer rows than the call needs" % name)
+    return strides, shape[1]
 
 
 def nvfp4kv_rope(plan: RopePlan, q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions,
@@ -177,35 +195,38 @@ def nvfp4kv_rope(plan: RopePlan, q: Optional[torch.Tensor], k: Optional[torch.Te
     first = q if q is not None else k
     if first is None:
         return None, None
-    if first.dtype not in _DTYPE:
+    dtype = first.dtype
+    code = _DTYPE.get(dtype)
+    if code is None:
         raise ValueError("q and k must be torch.bfloat16 or torch.float16")
     _ints(torch.int32, positions=positions)
-    n, dev = positions.numel(), _device(positions, plan.freq)
-    args = []
-    outs = []
-    for name, x, out in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            args += [None, 0, 0, None, 0, 0, 0]
-            outs.append(None)
-            continue
-        _rows(name, x, plan.head_dim, n, first.dtype)
-        if out is None:
-            with _on(stream):
-                out = torch.empty((n, x.shape[1], plan.head_dim), dtype=x.dtype, device=x.device)
-        else:
-            _rows(name + "_out", out, plan.head_dim, n, first.dtype)
-            if out.shape[1] != x.shape[1]:
-                raise ValueError("%s_out has another number of heads" % name)
-        if x.get_device() != dev or out.get_device() != dev:
-            raise ValueError("%s is not on the current device cuda:%d" % (name, dev))
-        args += [x.data_ptr(), x.stride(0), x.stride(1), out.data_ptr(), out.stride(0),
-                 out.stride(1), x.shape[1]]
-        outs.append(out)
-    check(_lib.load().nvfp4kv_rope(
-        *args, n, positions.data_ptr(), plan.head_dim, plan.rotary_dim, plan.interleaved,
-        _DTYPE[first.dtype], plan.freq.data_ptr(), plan.attention_factor, _stream_of(stream)),
-        "nvfp4kv_rope")
-    return outs[0], outs[1]
+    n, dev = positions.numel(), torch.cuda.current_device()
+    _wrong_device(dev, positions, plan.freq)
+    qa, q_out = _rope_rows(plan, "q", q, q_out, n, dtype, dev, stream)
+    ka, k_out = _rope_rows(plan, "k", k, k_out, n, dtype, dev, stream)
+    st = _entry("nvfp4kv_rope")(
+        *qa, *ka, n, positions.data_ptr(), plan.head_dim, plan.rotary_dim, plan.interleaved,
+        code, plan.freq.data_ptr(), plan.attention_factor, _stream_of(stream, dev))
+    if st:
+        check(st, "nvfp4kv_rope")
+    return q_out, k_out
+
+
+def _rope_rows(plan, name, x, out, n, dtype, dev, stream):
+    """The seven arguments of one of q and k, and its output."""
+    if x is None:
+        return (None, 0, 0, None, 0, 0, 0), None
+    rows, heads = _rows(name, x, plan.head_dim, n, dtype)
+    if out is None:
+        out = _empty((n, heads, plan.head_dim), dtype, x.device, stream)
+        to = (heads * plan.head_dim, plan.head_dim)
+    else:
+        to, out_heads = _rows(name + "_out", out, plan.head_dim, n, dtype)
+        if out_heads != heads:
+            raise ValueError("%s_out has another number of heads" % name)
+    if x.get_device() != dev or out.get_device() != dev:
+        _wrong_device(dev, x, out)
+    return (x.data_ptr(), rows[0], rows[1], out.data_ptr(), to[0], to[1], heads), out
 
 
 # ---- the E4M3 cache ----------------------------------------------------------------
@@ -234,6 +255,7 @@ class E4m3Cache:
         if len({t.device for t in (k_data, v_data, k_scale, v_scale)}) != 1:
             raise ValueError("the cache's tensors are on different devices")
         self.k_data, self.v_data, self.k_scale, self.v_scale = k_data, v_data, k_scale, v_scale
+        self.device = k_data.get_device()
         self.num_pages, self.num_kv_heads, self.page_size = pages, heads, page_size
         self.head_dim_qk, self.head_dim_vo = k_data.shape[3], v_data.shape[3]
         s.num_pages, s.page_size, s.num_kv_heads = pages, page_size, heads
@@ -264,56 +286,78 @@ def nvfp4kv_e4m3_append(cache: E4m3Cache, k: torch.Tensor, v: torch.Tensor, qo_i
     """Quantise the step's new tokens, k [rows, Hkv, Dk] and v [rows, Hkv, Dv]
     (request b's rows qo_indptr[b] .. qo_indptr[b + 1) are its last tokens),
     into their pages; the page table (int32, device) is that after the step."""
-    if k.dtype not in _DTYPE:
+    code = _DTYPE.get(k.dtype)
+    if code is None:
         raise ValueError("k must be torch.bfloat16 or torch.float16")
     rows, batch = k.shape[0], last_page_len.numel()
-    _rows("k", k, cache.head_dim_qk, rows, k.dtype)
-    _rows("v", v, cache.head_dim_vo, rows, k.dtype)
-    if k.shape[1] != cache.num_kv_heads or v.shape[1] != cache.num_kv_heads or \
-            v.shape[0] != rows:
+    ks, k_heads = _rows("k", k, cache.head_dim_qk, rows, k.dtype)
+    vs, v_heads = _rows("v", v, cache.head_dim_vo, rows, k.dtype)
+    if k_heads != cache.num_kv_heads or v_heads != k_heads or v.shape[0] != rows:
         raise ValueError("k and v must have the cache's heads and one number of rows")
     _ints(torch.int32, qo_indptr=qo_indptr, kv_indptr=kv_indptr, kv_indices=kv_indices,
           last_page_len=last_page_len)
     if qo_indptr.numel() != batch + 1 or kv_indptr.numel() != batch + 1:
         raise ValueError("indptrs must have one entry more than last_page_len")
-    _device(cache.k_data, k, v, qo_indptr, kv_indptr, kv_indices, last_page_len)
-    check(_lib.load().nvfp4kv_e4m3_append(
-        cache._struct, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-        v.stride(1), _DTYPE[k.dtype], rows, qo_indptr.data_ptr(), kv_indptr.data_ptr(),
-        kv_indices.data_ptr(), last_page_len.data_ptr(), batch, _flag_ptr(device_flags),
-        _stream_of(stream)), "nvfp4kv_e4m3_append")
+    dev = torch.cuda.current_device()
+    _wrong_device(dev, cache.k_data, k, v, qo_indptr, kv_indptr, kv_indices, last_page_len)
+    st = _entry("nvfp4kv_e4m3_append")(
+        cache._struct, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], code, rows,
+        qo_indptr.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(),
+        last_page_len.data_ptr(), batch, _flag_ptr(device_flags, dev), _stream_of(stream, dev))
+    if st:
+        check(st, "nvfp4kv_e4m3_append")
+
+
+class _Run:
+    """What every run of a plan with kernel 5 needs, taken from it once."""
+
+    def __init__(self, plan: Plan):
+        i = plan.info
+        if plan.workspace is None:
+            raise ValueError("the plan has no workspace (allocate=False)")
+        self.rows, self.heads = i.total_qo_rows, i.num_qo_heads
+        self.dk, self.dv, self.pages = i.head_dim_qk, i.head_dim_vo, i.total_kv_pages
+        self.dtype = torch.float16 if i.out_dtype == 1 else torch.bfloat16
+        self.workspace, self.nbytes = plan.workspace.data_ptr(), plan.workspace.numel()
+        self.device = plan.workspace.get_device()
+        self.out_shape, self.lse_shape = (self.rows, self.heads, self.dv), (self.rows, self.heads)
 
 
 def nvfp4kv_e4m3_decode_run(plan: Plan, q: torch.Tensor, cache: E4m3Cache, kv_indices,
                             sm_scale: float = 0.0, out=None, lse=None, stream=None):
     """Attention over an E4M3 cache with a plan made with ``kernel=5``: returns
     (out [rows, Hq, Dv], lse [rows, Hq])."""
-    info = plan.info
-    rows, hq = info.total_qo_rows, info.num_qo_heads
-    if q.dtype not in _DTYPE:
+    r = plan.__dict__.get("_e4m3_run")
+    if r is None:
+        r = plan._e4m3_run = _Run(plan)
+    code = _DTYPE.get(q.dtype)
+    if code is None:
         raise ValueError("q must be torch.bfloat16 or torch.float16")
-    _rows("q", q, info.head_dim_qk, rows, q.dtype)
-    if q.shape[1] != hq:
+    qs, heads = _rows("q", q, r.dk, r.rows, q.dtype)
+    if heads != r.heads:
         raise ValueError("q must have the plan's heads")
-    _ints(torch.int32, kv_indices=kv_indices)
-    if kv_indices.numel() < info.total_kv_pages:
+    if kv_indices.dtype != torch.int32 or not kv_indices.is_contiguous():
+        raise ValueError("kv_indices must be contiguous torch.int32")
+    if kv_indices.numel() < r.pages:
         raise ValueError("kv_indices has fewer entries than the plan's pages")
-    if plan.workspace is None:
-        raise ValueError("the plan has no workspace (allocate=False)")
-    _device(q, cache.k_data, kv_indices, plan.workspace)
-    if out is None or lse is None:
-        with _on(stream):
-            out, lse = _outputs(plan, out, lse, q.device)
-    want = torch.float16 if info.out_dtype == 1 else torch.bfloat16
-    if tuple(out.shape) != (rows, hq, info.head_dim_vo) or out.dtype != want or \
-            not out.is_contiguous():
-        raise ValueError("out must be contiguous %s [rows, Hq, Dv]" % want)
-    if tuple(lse.shape) != (rows, hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    dev = torch.cuda.current_device()
+    if not (q.get_device() == kv_indices.get_device() == cache.device == r.device == dev):
+        _wrong_device(dev, q, kv_indices, cache.k_data, plan.workspace)
+    if out is None:
+        out = _empty(r.out_shape, r.dtype, q.device, stream)
+    elif tuple(out.shape) != r.out_shape or out.dtype != r.dtype or not out.is_contiguous():
+        raise ValueError("out must be contiguous %s [rows, Hq, Dv]" % r.dtype)
+    if lse is None:
+        lse = _empty(r.lse_shape, torch.float32, q.device, stream)
+    elif tuple(lse.shape) != r.lse_shape or lse.dtype != torch.float32 or \
+            not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [rows, Hq]")
-    _device(out, lse)
-    check(_lib.load().nvfp4kv_e4m3_decode_run(
-        info, q.data_ptr(), q.stride(0), q.stride(1), _DTYPE[q.dtype], cache._struct,
-        kv_indices.data_ptr(), sm_scale or 0.0, plan.workspace.data_ptr(),
-        plan.workspace.numel(), out.data_ptr(), lse.data_ptr(), _stream_of(stream)),
-        "nvfp4kv_e4m3_decode_run")
+    if out.get_device() != dev or lse.get_device() != dev:
+        _wrong_device(dev, out, lse)
+    st = _entry("nvfp4kv_e4m3_decode_run")(
+        plan.info, q.data_ptr(), qs[0], qs[1], code, cache._struct, kv_indices.data_ptr(),
+        sm_scale or 0.0, r.workspace, r.nbytes, out.data_ptr(), lse.data_ptr(),
+        _stream_of(stream, dev))
+    if st:
+        check(st, "nvfp4kv_e4m3_decode_run")
     return out, lse
