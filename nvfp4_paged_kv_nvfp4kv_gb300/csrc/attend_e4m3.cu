@@ -486,8 +486,11 @@ bool make_e4m3(bool page1, AttendConfig* cfg) {
 
 }  // namespace
 
-bool attend_config_e4m3(int dk, int dv, int page_size, int rows, AttendConfig* cfg) {
-  (void)rows;  // more rows: more row blocks
+bool attend_config_e4m3(int dk, int dv, int page_size, int rows, bool out_f16,
+                        AttendConfig* cfg) {
+  // more rows than one block: the tensor-memory kernel where it is built, else
+  // blocks of 8 rows, each reading the keys again
+  if (rows > 8 && attend_config_e4m3_ext(dk, dv, page_size, rows, out_f16, cfg)) return true;
   const bool p1 = page_size == 1;
   if (dk == 64 && dv == 64) return make_e4m3<64, 64, 4, 6, 3>(p1, cfg);
   if (dk == 128 && dv == 128) return make_e4m3<128, 128, 4, 4, 3>(p1, cfg);

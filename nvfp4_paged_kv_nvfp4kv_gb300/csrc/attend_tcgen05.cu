@@ -48,240 +48,24 @@
 #include "device_common.cuh"
 #include "epilogue.cuh"
 #include "internal.h"
+#include "tcgen05.cuh"
 
 namespace nvfp4kv {
 namespace {
 
 using namespace dev;
+using namespace tc5;
 
 constexpr int kTileTok = 128;
 constexpr int kThreads = 416;  // softmax warps 0-7, dequant warps 8-11, issue warp 12
 constexpr int kKB = 3;         // K_hat / V_hat buffers
 constexpr float kRaise = 8.f;  // log2 of the largest p before m is raised
-// Wait bounds (the defaults give up after about a second; a test build
-// shortens them to about a millisecond).
-#ifndef NVFP4KV_TG5_SLEEP_NS
-#define NVFP4KV_TG5_SLEEP_NS 20000
-#endif
-#ifndef NVFP4KV_TG5_POLLS
-#define NVFP4KV_TG5_POLLS 50000
-#endif
-#ifndef NVFP4KV_TG5_IDLE_POLLS
-#define NVFP4KV_TG5_IDLE_POLLS (1u << 21)
-#endif
 // Test build only: the first dequant warp of CTA (0, 0) withholds its arrival
 // for the first tile, so the product issuer's bounded wait runs out and the
 // CTA takes the abort path (flag 0x4, every wait returns, the kernel ends).
 #ifndef NVFP4KV_TG5_TEST_SKIP_ARRIVE
 #define NVFP4KV_TG5_TEST_SKIP_ARRIVE 0
 #endif
-constexpr uint32_t kSleepNs = NVFP4KV_TG5_SLEEP_NS;  // suspend hint of one poll
-constexpr uint32_t kPolls = NVFP4KV_TG5_POLLS;       // polls before a wait gives up
-constexpr uint32_t kIdlePolls = NVFP4KV_TG5_IDLE_POLLS;  // idle rounds of the issuer
-
-// ---- tensor memory, tcgen05 and barrier helpers (inline PTX) -------------
-__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t ncols) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
-                   smem_addr(dst)),
-               "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish() {
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(taddr),
-               "r"(ncols)
-               : "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory");
-}
-__device__ __forceinline__ void fence_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-}
-// 32 lanes x 16 columns: thread i <-> lane (address lane + i)
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15}, [%16];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                 "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
-// NC consecutive columns (a multiple of 8) of this thread's lane
-template <int NC>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t* r) {
-  static_assert(NC % 8 == 0, "columns");
-  if constexpr (NC % 16 == 0) {
-#pragma unroll
-    for (int c = 0; c < NC / 16; ++c) tmem_ld16(taddr + 16 * c, r + 16 * c);
-  } else {
-#pragma unroll
-    for (int c = 0; c < NC / 8; ++c) tmem_ld8(taddr + 8 * c, r + 8 * c);
-  }
-}
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16};\n" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-      : "memory");
-}
-template <int NC>
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t* r) {
-  static_assert(NC % 8 == 0, "columns");
-  if constexpr (NC % 16 == 0) {
-#pragma unroll
-    for (int c = 0; c < NC / 16; ++c) tmem_st16(taddr + 16 * c, r + 16 * c);
-  } else {
-#pragma unroll
-    for (int c = 0; c < NC / 8; ++c) tmem_st8(taddr + 8 * c, r + 8 * c);
-  }
-}
-// Wait for outstanding tcgen05.ld and make their results the registers'
-// current values for the code that follows.
-template <int NR>
-__device__ __forceinline__ void tmem_wait_ld(uint32_t* r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-#pragma unroll
-  for (int k = 0; k < NR; ++k) asm volatile("" : "+r"(r[k]));
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
-}
-
-// Shared-memory matrix descriptor: start address, leading / stride byte
-// offsets (16-byte units), descriptor version 1, swizzle mode.
-constexpr uint32_t kSwz128 = 2, kSwz64 = 4, kSwz32 = 6;
-__device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo,
-                                              uint32_t swz) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)((lbo >> 4) & 0x3FFFu) << 16) |
-         ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | ((uint64_t)swz << 61);
-}
-// Instruction descriptor, kind::f16: f16 A and B, f32 D, operand majors
-// (0 = K-major, 1 = MN-major), N >> 3, M >> 4.
-constexpr uint32_t idesc_f16(int M, int N, int a_mn, int b_mn) {
-  return (1u << 4) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
-         ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-// D[tmem] (+)= A[tmem] . B[smem]
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// D[tmem] (+)= A[smem] . B[smem]
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                        uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
-}
-// one arrival on `bar` once every tcgen05 operation this thread issued is done
-__device__ __forceinline__ void umma_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(
-          smem_addr(bar))
-      : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_addr(bar)) : "memory");
-}
-// non-blocking test of a phase
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ void named_sync(int id, int n) {
-  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(n) : "memory");
-}
-__device__ __forceinline__ bool named_or(int id, int n, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, %3, p;\n"
-      " selp.u32 %0, 1, 0, q;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)v), "r"(id), "r"(n)
-      : "memory");
-  return r != 0;
-}
-// One poll that may suspend the thread until the phase completes (or the
-// hinted time, in ns, elapses): waiting warps sleep instead of spinning and
-// leave the issue slots to the warps that work.
-__device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity), "r"(kSleepNs)
-      : "memory");
-  return ok != 0;
-}
-// Bounded wait (at least kPolls polls, at most kPolls * kSleepNs ns); gives
-// up early once another thread of the CTA gave up.
-__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                         uint32_t* flags) {
-  for (uint32_t it = 0; it < kPolls; ++it) {
-    if (mbar_try_wait_sleep(bar, parity)) return true;
-    if (*abort) return false;
-  }
-  *abort = 1;
-  atomicOr(flags, 0x4u);
-  return false;
-}
-// Bounded wait that ignores the abort flag (the wind-down of copies and
-// products in flight).
-__device__ __forceinline__ void drain_bar(uint64_t* bar, uint32_t parity, uint32_t* flags) {
-  for (uint32_t it = 0; it < kPolls; ++it)
-    if (mbar_try_wait_sleep(bar, parity)) return;
-  atomicOr(flags, 0x4u);
-}
-// max of three floats in one instruction
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-// order-preserving float <-> int keys (for integer max reductions)
-__device__ __forceinline__ int fkey(float f) {
-  const int i = __float_as_int(f);
-  return i >= 0 ? i : i ^ 0x7FFFFFFF;
-}
-__device__ __forceinline__ float funkey(int k) {
-  return __int_as_float(k >= 0 ? k : k ^ 0x7FFFFFFF);
-}
 
 template <int N>
 struct Tg5 {
@@ -316,13 +100,6 @@ struct Tg5 {
   static_assert(ONES + 8 <= TCOLS, "tensor memory");
   static_assert(SMEM <= 232448, "shared memory");
 };
-
-// swizzled byte offset inside a 1024-byte-aligned operand region (the
-// operand layouts' 16-byte-chunk xor with address bits 7..)
-template <int B>
-__device__ __forceinline__ uint32_t swz(uint32_t off) {
-  return off ^ (((off >> 7) & ((1u << B) - 1)) << 4);
-}
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, 1) attend_tcgen05_kernel(const AttendParams p) {

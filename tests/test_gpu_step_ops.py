@@ -386,7 +386,17 @@ def attend_case(kv, new, hq, hkv, dk, dv, causal=False, page=16, layout="HND", d
     by at most Dk 2^-23 * sm_scale sum|q k| (f32 sums of exact f16 products)
     and the exponential by 2^-21 relative, so a weight by that delta; weights
     are rounded to f16 (2^-11 relative, 2^-25 of the row's largest weight times
-    scale at least); normalised sums and a merge of split states in f32: 2^-19."""
+    scale at least); normalised sums and a merge of split states in f32: 2^-19.
+
+    With more than 8 rows a block the tensor-memory kernel runs: it adds E4M3
+    pieces, each the rounded rest (off by at most 2^-4 of it), of the query and
+    of the weights.  Query pieces, with the row's largest |q| in [128, 256), are
+    exact but for elements whose last bit is below the smallest code 2^-9: off
+    by 2^-10, 2^-17 of the largest |q|, so a score by 2^-17 * sm_scale max|q|
+    sum|k| more.  Weights, after f16, are off by (2^-4)^pieces of themselves and
+    by half the last piece's smallest code, 2^-10 / 32^(pieces - 1), where the
+    row's largest is 2^5 or more: 2^-20 of that with two pieces (bf16 outputs),
+    2^-25 (and f16's own floor) with three."""
     c = CacheCase(kv, page, hkv, dk, dv, layout, seed=seed, spread=spread)
     if stale:  # slots past every length hold NaN codes
         for b, n in enumerate(kv):
@@ -418,8 +428,14 @@ def attend_case(kv, new, hq, hkv, dk, dv, causal=False, page=16, layout="HND", d
         rows = slice(int(qo[b]), int(qo[b + 1]))
         ref, rl, mean, reach, floor = R.attention(R.to_np(q[rows]), k, v, vs, scale, causal)
         delta = (dk * 2.0 ** -23 * reach + 2.0 ** -21)
-        tol = (eps * np.abs(ref) + (mean * (2.0 ** -11 + 2.0 ** -19 + 2 * delta[..., None])
-                                    + 2.0 ** -25 * floor) * (1 + eps)
+        weight, least = 2.0 ** -11, 2.0 ** -25
+        if plan.info.rows_per_block > 8:
+            pieces = 3 if out == "f16" else 2
+            delta = delta + 2.0 ** -17 * scale * (np.abs(R.to_np(q[rows])).max(-1)
+                                                  * np.abs(k).sum(-1).max())
+            weight, least = weight + 2.0 ** (-4 * pieces), 2.0 ** (-15 - 5 * (pieces - 1)) * 1.1
+        tol = (eps * np.abs(ref) + (mean * (weight + 2.0 ** -19 + 2 * delta[..., None])
+                                    + least * floor) * (1 + eps)
                + float(torch.finfo(DT[out]).smallest_normal) * eps)
         err = np.abs(got[rows] - ref)
         assert np.isfinite(got[rows]).all()
