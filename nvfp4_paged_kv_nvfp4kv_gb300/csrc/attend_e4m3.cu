@@ -319,8 +319,9 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
       const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
       for (int m = 0; m < 4; ++m) {
-        const uint32_t f[4] = {e4m3x2_to_f16x2(a[m] & 0xFFFFu), e4m3x2_to_f16x2(b[m] & 0xFFFFu),
-                               e4m3x2_to_f16x2(a[m] >> 16), e4m3x2_to_f16x2(b[m] >> 16)};
+        uint32_t f[4];
+        e4m3x4_to_f16(a[m], f[0], f[2]);
+        e4m3x4_to_f16(b[m], f[1], f[3]);
         if (m & 1)
           mma_16816(sb, f, qreg[4 * cc + m][0], qreg[4 * cc + m][1]);
         else
@@ -429,10 +430,11 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
         const uint32_t l1 = __byte_perm(w[2][k], w[3][k], 0x5140);
         const uint32_t h1 = __byte_perm(w[2][k], w[3][k], 0x7362);
         const int mt = cc * (T::VCB / 2) + 2 * k;
-        const uint32_t fa[4] = {e4m3x2_to_f16x2(l0 & 0xFFFFu), e4m3x2_to_f16x2(l0 >> 16),
-                                e4m3x2_to_f16x2(l1 & 0xFFFFu), e4m3x2_to_f16x2(l1 >> 16)};
-        const uint32_t fb[4] = {e4m3x2_to_f16x2(h0 & 0xFFFFu), e4m3x2_to_f16x2(h0 >> 16),
-                                e4m3x2_to_f16x2(h1 & 0xFFFFu), e4m3x2_to_f16x2(h1 >> 16)};
+        uint32_t fa[4], fb[4];
+        e4m3x4_to_f16(l0, fa[0], fa[1]);
+        e4m3x4_to_f16(l1, fa[2], fa[3]);
+        e4m3x4_to_f16(h0, fb[0], fb[1]);
+        e4m3x4_to_f16(h1, fb[2], fb[3]);
         mma_16816(oacc[mt], fa, pf0, pf1);
         mma_16816(oacc[mt + 1], fb, pf0, pf1);
       }

@@ -21,16 +21,16 @@
 // One CTA = one work unit (request, kv head, chunk of pages) x N = 16, 32 or
 // 64 query rows (the G heads of the group times the query positions); tiles of
 // 128 tokens; M = 128 tokens (S^T) or 128 value dims (O^T) fill the product
-// for any N.  11 warps (12 would still leave a thread 168 registers, 13 only
-// 128: the softmax threads then spill):
-//  * loaders (warps 8-9): cp.async of the tile's K and V rows straight into
+// for any N.  19 warps at N = 64:
+//  * loaders (two warps): cp.async of the tile's K and V rows straight into
 //    the 128-byte-swizzled operand layout (K: K-major, V: MN-major, both rows
-//    of 128 bytes), any byte strides and both page sizes; V rows past the
-//    request's end are zeroed (they may hold NaN codes);
-//  * issue (warp 10, one thread): S^T = K Q^T into one of two tiles, O^T +=
-//    V^T P^T, each once its inputs are ready;
-//  * softmax (warps 0-7; thread = token of S^T, half of the query rows): the
+//    of 128 bytes), any byte strides and both page sizes;
+//  * issue (two threads): S^T = K Q^T into the stage's tile of tensor memory,
+//    and O^T += V^T P^T, each once its inputs are ready;
+//  * softmax (four warps for each 16 query rows; thread = token of S^T): the
 //    token's K scale joins the row's factor, log2 of its V scale the exponent.
+//    The work of a tile is short chains, so many warps with few rows each beat
+//    few warps with many (8 warps of 32 rows took twice the time).
 // The running maximum is raised only when a value exceeds 2^8.  Every wait is
 // bounded; one that runs out sets flag 0x4 and the CTA winds down.
 #include <cstdint>
@@ -50,8 +50,8 @@ using namespace dev;
 using namespace tc5;
 
 constexpr int kTileTok = 128;
-constexpr int kThreads = 352;  // softmax warps 0-7, loaders 8-9, issue 10
 constexpr int kLoaders = 2;  // warps, 64 rows of a tile each
+constexpr int kAllSoftmax = 5;  // named barriers 1 .. 4: the column groups
 constexpr float kRaise = 8.f;  // log2 of the largest weight before m is raised
 constexpr float kPeak = 5.f;   // log2 of the weight of a new maximum
 constexpr float kMinScale = 0x1p-64f, kMaxScale = 0x1p64f;
@@ -66,15 +66,22 @@ __device__ __forceinline__ void umma8_ss(uint32_t d, uint64_t a, uint64_t b, uin
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
-// two f32 -> two E4M3 codes (a in the low byte) and back to f16x2
-__device__ __forceinline__ uint32_t e4m3x2_of_f32(float a, float b) {
-  unsigned short r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+// four values (two f16x2) -> four E4M3 codes, the first in the low byte, and
+// back (16-bit halves by register pairs: the conversions address them directly)
+__device__ __forceinline__ uint32_t e4m3x4_of_f16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f16x2 l, %1;\n"
+      " cvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n mov.b32 %0, {l, h};\n}\n"
+      : "=r"(r)
+      : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
-  unsigned short r;
-  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+__device__ __forceinline__ uint32_t e4m3x4_of_f32(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n"
+      " cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}\n"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
 }
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
@@ -84,6 +91,11 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
 }
 __device__ __forceinline__ void cp_async_16a(uint32_t s, const void* g) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(g));
+}
+// one arrival on `bar` once this thread's earlier cp.async copies have landed
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_addr(bar))
+               : "memory");
 }
 __device__ __forceinline__ void cp_async_4(uint32_t s, const void* g) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(s), "l"(g));
@@ -122,7 +134,10 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 
 template <int DK, int DV, int N, int NP>
 struct Ext {
-  static constexpr int NH = N / 2;                 // query rows per softmax thread
+  static constexpr int NH = N >= 32 ? 16 : 8;      // query rows per softmax thread
+  static constexpr int CG = N / NH;                // column groups of four warps
+  static constexpr int SW = 4 * CG;                // softmax warps
+  static constexpr int THREADS = 32 * (SW + kLoaders + 2);
   static constexpr int NQ = 3;                     // query pieces (2 used for bf16)
   static constexpr int KB = kTileTok * DK, VB = kTileTok * DV;
   static constexpr int QB = N * DK;                // one query piece
@@ -134,7 +149,7 @@ struct Ext {
   static constexpr int PB = PATOMS * PSTRIDE;
   static constexpr uint32_t PSWZ = PA == 32 ? kSwz32 : PA == 64 ? kSwz64 : kSwz128;
   static constexpr int PSWB = PA == 32 ? 1 : PA == 64 ? 2 : 3;
-  static constexpr int SCB = kTileTok * 8;         // the tile's scales
+  static constexpr int SCB = kTileTok * 12;        // K scale, log2 and inverse of the V scale
   static constexpr int MISC = 8192;
   static constexpr int FIXED = 2 * PB + NQ * QB + MISC + 1024;
   static constexpr int KS = (232448 - FIXED) / (KB + VB + SCB) >= 4 ? 4 : 3;  // tiles in flight
@@ -145,7 +160,7 @@ struct Ext {
   static constexpr int OFF_SC = OFF_Q + NQ * QB;
   static constexpr int OFF_MISC = OFF_SC + KS * SCB;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;  // + alignment slack
-  static constexpr int SCOL = 0, OCOL = 2 * N;     // S^T x2, O^T blocks of 128 value dims
+  static constexpr int SCOL = 0, OCOL = KS * N;    // S^T, one per stage; O^T blocks of 128 dims
   static constexpr int COLS = OCOL + (DV / 128) * PN;
   static constexpr int TCOLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static constexpr uint32_t IDESC_QK = idesc_f16(128, N, 0, 0);
@@ -153,16 +168,15 @@ struct Ext {
   static_assert(DK % 128 == 0 && DV % 128 == 0, "operand rows of 128 bytes");
   static_assert(OFF_P % 1024 == 0 && OFF_Q % 1024 == 0 && OFF_MISC % 16 == 0, "align");
   static_assert(SMEM <= 232448 && COLS <= 512 && PN % 16 == 0 && PN <= 256, "resources");
-  static_assert(16 * 8 + 16 + (8 * N + 2 * N + 4 + 4 * N) * 4 <= MISC, "misc");
+  static_assert(20 * 8 + 16 + (8 * N + 2 * N + 4 + 4 * N) * 4 <= MISC, "misc");
 };
 
 // P1: 1-token pages
 template <int DK, int DV, int N, int NP, bool P1>
-__global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
+    attend_e4m3_ext_kernel(const AttendParams p) {
   using T = Ext<DK, DV, N, NP>;
-  constexpr int NH = T::NH, KS = T::KS;
-  constexpr int CW = NH < 16 ? NH : 16;  // columns per softmax chunk
-  constexpr int NCH = NH / CW;
+  constexpr int NH = T::NH, KS = T::KS, SW = T::SW, ST = 32 * SW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -170,16 +184,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const Atte
   uint8_t* sV = smem + T::OFF_V;
   uint8_t* sP = smem + T::OFF_P;
   uint8_t* sQ = smem + T::OFF_Q;
-  float* sSc = reinterpret_cast<float*>(smem + T::OFF_SC);  // [KS][K 128 | V 128]
+  float* sSc = reinterpret_cast<float*>(smem + T::OFF_SC);  // [KS][3][128]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::OFF_MISC);
-  uint64_t* kv_full = bars;       // [KS] loaders -> issue
+  uint64_t* landed = bars;        // [KS] copies of a tile -> S^T issue
   uint64_t* kv_empty = bars + 4;  // [KS] PV done -> loaders
-  uint64_t* s_full = bars + 8;    // [2] QK done -> softmax
-  uint64_t* p_full = bars + 10;   // [2] softmax -> issue
-  uint64_t* pv_done = bars + 12;  // [2] PV done -> softmax
-  uint64_t* q_full = bars + 14;   // Q ready -> issue
-  uint64_t* fin = bars + 15;      // wind-down of the products
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 16);
+  uint64_t* s_full = bars + 8;    // [KS] QK done, scales in -> softmax
+  uint64_t* p_full = bars + 12;   // [2] softmax -> issue
+  uint64_t* pv_done = bars + 14;  // [2] PV done -> softmax
+  uint64_t* q_full = bars + 16;   // Q ready -> issue
+  uint64_t* fin = bars + 17;      // [2] wind-down of the two issuers' products
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 20);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_minlim = reinterpret_cast<int*>(s_tmem + 2);
   // per query row: score factor, -m, raise threshold, causal limit
@@ -215,16 +229,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const Atte
 
   if (tid == 0) {
     for (int b = 0; b < KS; ++b) {
-      mbar_init(&kv_full[b], kLoaders);
+      mbar_init(&landed[b], 32 * kLoaders);
       mbar_init(&kv_empty[b], 1);
+      mbar_init(&s_full[b], 2);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], 8);
+      mbar_init(&fin[b], 1);
+      mbar_init(&p_full[b], SW);
       mbar_init(&pv_done[b], 1);
     }
-    mbar_init(q_full, 8);
-    mbar_init(fin, 1);
+    mbar_init(q_full, SW);
     mbar_init_fence();
     *s_abort = 0;
     *s_minlim = INT32_MAX;
@@ -239,10 +253,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const Atte
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  if (warp >= 8 && warp < 8 + kLoaders) {
-    // ================= loaders: warp 8 + w copies rows 64 w .. + 63 ==========
+  if (warp >= SW && warp < SW + kLoaders) {
+    // ================= loaders: warp SW + w copies rows 64 w .. + 63 ==========
     const CacheView& c = p.cache;
-    const int r0 = 64 * (warp - 8);
+    const int r0 = 64 * (warp - SW);
     const uint8_t* kb = c.k_data + (int64_t)u.h_kv * c.k_sh;
     const uint8_t* vb = c.v_data + (int64_t)u.h_kv * c.v_sh;
     const uint8_t* ksb = c.k_sf + (int64_t)u.h_kv * c.ksf_sh;
@@ -261,88 +275,129 @@ __global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const Atte
       }
       return id;
     };
-    // 8 lanes copy 128 bytes of a row, 4 rows an instruction
+    // 8 lanes copy 128 bytes of a row, 4 rows an instruction: 16 rows (a page
+    // at page size 16) from row `first` of the tile; lane0: the lane that holds
+    // the first one's page id
+    const int r4 = lane >> 3, ch = lane & 7;
+    // swizzled 16-byte chunk of this lane's rows 8 i + r4 and 8 i + 4 + r4
+    const uint32_t at0 = r4 * 128 + ((ch ^ r4) << 4), at1 = (r4 + 4) * 128 + ((ch ^ (r4 + 4)) << 4);
     auto copy = [&](uint32_t tile, const uint8_t* base, int64_t sp, int64_t ss, int32_t pid,
-                    int half) {
-      const int r4 = lane >> 3, ch = lane & 7;
+                    int first, int lane0) {
+      const uint32_t dst = tile + first * 128;
+      if constexpr (P1) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + r4, row = r0 + 32 * half + r;
-        const int32_t pg = __shfl_sync(0xffffffffu, pid, r);
-        const uint8_t* src = base + pg * sp + (P1 ? 0 : (row % kPageSize) * ss) + 16 * ch;
-        cp_async_16a(tile + row * 128 + ((ch ^ (row & 7)) << 4), src);
+        for (int k = 0; k < 4; ++k) {
+          const int32_t pg = __shfl_sync(0xffffffffu, pid, lane0 + 4 * k + r4);
+          cp_async_16a(dst + (k >> 1) * 1024 + (k & 1 ? at1 : at0), base + pg * sp + 16 * ch);
+        }
+      } else {
+        const uint8_t* src =
+            base + __shfl_sync(0xffffffffu, pid, lane0) * sp + r4 * ss + 16 * ch;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          cp_async_16a(dst + (k >> 1) * 1024 + (k & 1 ? at1 : at0), src + 4 * k * ss);
       }
     };
     auto issue = [&](int t, int32_t pid0, int32_t pid1) {
       const int st = t % KS;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int32_t pid = half ? pid1 : pid0;
+      for (int g = 0; g < 4; ++g) {
+        const int32_t pid = g < 2 ? pid0 : pid1;
+        const int first = r0 + 16 * g, lane0 = 16 * (g & 1);
 #pragma unroll
         for (int b = 0; b < DK / 128; ++b)
           copy(smem_addr(sK) + st * T::KB + b * (kTileTok * 128), kb + 128 * b, c.k_sp, c.k_ss,
-               pid, half);
+               pid, first, lane0);
 #pragma unroll
         for (int b = 0; b < DV / 128; ++b)
           copy(smem_addr(sV) + st * T::VB + b * (kTileTok * 128), vb + 128 * b, c.v_sp, c.v_ss,
-               pid, half);
-        const uint32_t sc = smem_addr(sSc) + st * T::SCB + 4 * (r0 + 32 * half + lane);
-        cp_async_4(sc, ksb + pid * c.ksf_sp);
-        cp_async_4(sc + 4 * kTileTok, vsb + pid * c.vsf_sp);
+               pid, first, lane0);
       }
+      const uint32_t sc = smem_addr(sSc) + st * T::SCB + 4 * (r0 + lane);
+      cp_async_4(sc, ksb + pid0 * c.ksf_sp);
+      cp_async_4(sc + 128, ksb + pid1 * c.ksf_sp);
+      cp_async_4(sc + 4 * kTileTok, vsb + pid0 * c.vsf_sp);
+      cp_async_4(sc + 4 * kTileTok + 128, vsb + pid1 * c.vsf_sp);
     };
-    constexpr int LAG = KS - 2;  // tiles between a tile's copies and its hand-over
     int32_t next0 = load_pid(0, 0), next1 = load_pid(0, 1);
-    for (int t = 0; t < ntiles + LAG; ++t) {
-      if (t < ntiles) {
-        if (t >= KS) {
-          bool ok = true;
-          if (lane == 0) ok = wait_bar(&kv_empty[t % KS], (t / KS - 1) & 1, s_abort, p.flags);
-          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-          tc_fence_after();
-        }
-        const int32_t pid0 = next0, pid1 = next1;
-        next0 = load_pid(t + 1, 0);
-        next1 = load_pid(t + 1, 1);
-        issue(t, pid0, pid1);
+    for (int t = 0; t < ntiles; ++t) {
+      if (t >= KS) {
+        bool ok = true;
+        if (lane == 0) ok = wait_bar(&kv_empty[t % KS], (t / KS - 1) & 1, s_abort, p.flags);
+        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        tc_fence_after();
       }
-      cp_async_commit();
-      if (t < LAG) continue;
-      cp_async_wait<LAG>();  // this thread's copies of tile i landed
-      const int i = t - LAG;
-      __syncwarp();
+      const int32_t pid0 = next0, pid1 = next1;
+      next0 = load_pid(t + 1, 0);
+      next1 = load_pid(t + 1, 1);
+      issue(t, pid0, pid1);
+      cp_async_arrive(&landed[t % KS]);  // once this thread's copies have landed
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+  } else if (warp == SW + kLoaders) {
+    // ======== S^T issue: once a tile has landed, its scales and the rows past
+    // the end are put in order by the warp and one thread issues the products ==
+    const uint64_t kd0 = smem_desc(smem_addr(sK), 16, 1024, kSwz128);
+    const uint64_t qd0 = smem_desc(smem_addr(sQ), 16, 1024, kSwz128);
+    for (int k = 0; k < ntiles; ++k) {
+      // (a stage is refilled after PV(k - KS): its S^T has been consumed)
+      const int st = k % KS;
+      bool ok = true;
+      if (lane == 0) ok = wait_bar(&landed[st], (k / KS) & 1, s_abort, p.flags);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       // rows past the request's end or the unit's pages: no NaN code times 0
-      const int live = min(u.kv_len - u.tok_begin, unit_tok) - i * kTileTok;
-      for (int row = max(live, r0); row < r0 + 64; ++row)
+      const int live = min(u.kv_len - u.tok_begin, unit_tok) - k * kTileTok;
+      for (int row = max(live, 0); row < kTileTok; ++row)
 #pragma unroll
         for (int b = 0; b < DV / 128; ++b)
-          *reinterpret_cast<uint32_t*>(sV + (i % KS) * T::VB + b * (kTileTok * 128) + row * 128 +
+          *reinterpret_cast<uint32_t*>(sV + st * T::VB + b * (kTileTok * 128) + row * 128 +
                                        4 * lane) = 0u;
+      // the tokens' scales as the softmax threads use them
+      float* sc = sSc + st * (T::SCB / 4) + lane;
+#pragma unroll
+      for (int part = 0; part < 4; ++part, sc += 32) {
+        const float ks = sc[0], vs = sc[kTileTok];
+        const float ksc = fminf(fmaxf(ks, kMinScale), kMaxScale);
+        const float vsc = fminf(fmaxf(vs, kMinScale), kMaxScale);
+        if (ksc != ks || vsc != vs) atomicOr(p.flags, 0x20u);
+        const float lv = log2_scale(vsc);
+        sc[0] = ksc;
+        sc[kTileTok] = lv;
+        sc[2 * kTileTok] = ex2(-lv);
+      }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&kv_full[i % KS]);
+      if (lane == 0) {
+        if (k == 0) ok = wait_bar(q_full, 0, s_abort, p.flags);
+        if (ok) {
+          tc_fence_after();
+          const uint32_t d = tmem + T::SCOL + N * st;
+          const uint64_t kd = kd0 + ((st * T::KB) >> 4);
+          for (int q = 0; q < nq; ++q)
+#pragma unroll
+            for (int kk = 0; kk < DK / 32; ++kk)
+              umma8_ss(d, kd + (((kk >> 2) * (kTileTok * 128) + (kk & 3) * 32) >> 4),
+                       qd0 + ((q * T::QB + (kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4),
+                       T::IDESC_QK, (q > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&s_full[st]);
+          mbar_arrive(&s_full[st]);  // (the softmax threads read the scales)
+        }
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
     }
-    cp_async_wait<0>();
-  } else if (warp == 8 + kLoaders) {
-    // ================= product issue (one thread) ==========================
     if (lane == 0) {
-      const uint64_t kd0 = smem_desc(smem_addr(sK), 16, 1024, kSwz128);
-      const uint64_t qd0 = smem_desc(smem_addr(sQ), 16, 1024, kSwz128);
+      umma_commit(&fin[0]);  // wind-down: every product issued has completed
+      drain_bar(&fin[0], 0, p.flags);
+    }
+    __syncwarp();
+  } else if (warp == SW + kLoaders + 1) {
+    // ======== O^T issue (one thread) ==========================================
+    if (lane == 0) {
       const uint64_t vd0 = smem_desc(smem_addr(sV), kTileTok * 128, 1024, kSwz128);
       const uint64_t pd0 = smem_desc(smem_addr(sP), T::PSTRIDE, 8 * T::PA, T::PSWZ);
-      auto issue_qk = [&](int k) {
-        tc_fence_after();
-        const uint32_t d = tmem + T::SCOL + N * (k & 1);
-        const uint64_t kd = kd0 + (((k % KS) * T::KB) >> 4);
-        for (int q = 0; q < nq; ++q)
-#pragma unroll
-          for (int kk = 0; kk < DK / 32; ++kk)
-            umma8_ss(d, kd + (((kk >> 2) * (kTileTok * 128) + (kk & 3) * 32) >> 4),
-                     qd0 + ((q * T::QB + (kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4),
-                     T::IDESC_QK, (q > 0 || kk > 0) ? 1u : 0u);
-        umma_commit(&s_full[k & 1]);
-      };
-      auto issue_pv = [&](int i) {
+      for (int i = 0; i < ntiles; ++i) {
+        if (!wait_bar(&p_full[i & 1], (i >> 1) & 1, s_abort, p.flags)) break;
         tc_fence_after();
         const uint64_t vd = vd0 + (((i % KS) * T::VB) >> 4);
         const uint64_t pd = pd0 + (((i & 1) * T::PB) >> 4);
@@ -355,43 +410,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const Atte
                      pd + ((k * 32 * T::PA) >> 4), T::IDESC_PV, (i > 0 || k > 0) ? 1u : 0u);
         umma_commit(&pv_done[i & 1]);
         umma_commit(&kv_empty[i % KS]);
-      };
-      // whichever product has its inputs: S(qk) once its tile is in and S
-      // buffer qk & 1 was consumed (PV(qk - 2) issued), O += PV(pv) once P(pv)
-      // is written
-      bool ok = wait_bar(q_full, 0, s_abort, p.flags);
-      int qk = 0, pv = 0;
-      uint32_t idle = 0;
-      while (ok && pv < ntiles) {
-        bool prog = false;
-        if (qk < ntiles && qk < pv + 2 && mbar_test_wait(&kv_full[qk % KS], (qk / KS) & 1)) {
-          issue_qk(qk);
-          ++qk;
-          prog = true;
-        }
-        if (pv < qk && mbar_test_wait(&p_full[pv & 1], (pv >> 1) & 1)) {
-          issue_pv(pv);
-          ++pv;
-          prog = true;
-        }
-        if (prog) {
-          idle = 0;
-          continue;
-        }
-        if (*s_abort) break;
-        if (++idle > kIdlePolls) {
-          *s_abort = 1;
-          atomicOr(p.flags, 0x4u);
-          break;
-        }
-        __nanosleep(32);
       }
-      umma_commit(fin);  // wind-down: every product issued has completed
-      drain_bar(fin, 0, p.flags);
+      umma_commit(&fin[1]);
+      drain_bar(&fin[1], 0, p.flags);
     }
     __syncwarp();
   } else {
-    // ================= softmax + epilogue (warps 0-7) ======================
+    // ================= softmax + epilogue ==================================
     const int c0 = (warp >> 2) * NH;  // this thread's first query row
     auto q2 = [&](uint32_t w) -> float2 {
       if (p.q_f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
@@ -409,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const Atte
       return v;
     };
 #pragma unroll 4
-    for (int ci = tid; ci < QCH; ci += 256) {
+    for (int ci = tid; ci < QCH; ci += ST) {
       const uint4 v = q_load(ci);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       float am = 0.f;
@@ -420,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const Atte
       }
       atomicMax(&s_qamax[ci / (DK / 8)], __float_as_int(am));
     }
-    named_sync(3, 256);
+    named_sync(kAllSoftmax, ST);
     auto exp_of = [&](int r) {  // e with amax * 2^e in [128, 256)
       const float amax = __int_as_float(s_qamax[r]);
       int e = 0;
@@ -428,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const Atte
       return max(-120, min(120, e));
     };
 #pragma unroll 2
-    for (int ci = tid; ci < QCH; ci += 256) {
+    for (int ci = tid; ci < QCH; ci += ST) {
       const uint4 v = q_load(ci);
       const int r = ci / (DK / 8), c8 = ci % (DK / 8);
       const float up = __uint_as_float((uint32_t)(127 + exp_of(r)) << 23);
@@ -443,17 +468,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const Atte
       const uint32_t off = (uint32_t)(c8 >> 4) * (N * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
                            (c8 & 15) * 8;
       for (int q = 0; q < nq; ++q) {
-        uint32_t h[4];
+        uint32_t h[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          h[e] = e4m3x2_of_f32(rest[e].x, rest[e].y);
-          const uint32_t back = e4m3x2_to_f16x2(h[e]);
-          const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&back));
-          rest[e].x -= b.x;
-          rest[e].y -= b.y;
+        for (int e = 0; e < 2; ++e) {
+          h[e] = e4m3x4_of_f32(rest[2 * e].x, rest[2 * e].y, rest[2 * e + 1].x, rest[2 * e + 1].y);
+          uint32_t back[2];
+          e4m3x4_to_f16(h[e], back[0], back[1]);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back[k]));
+            rest[2 * e + k].x -= f.x;
+            rest[2 * e + k].y -= f.y;
+          }
         }
-        *reinterpret_cast<uint2*>(sQ + q * T::QB + swz<3>(off)) =
-            make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+        *reinterpret_cast<uint2*>(sQ + q * T::QB + swz<3>(off)) = make_uint2(h[0], h[1]);
       }
     }
     if (tid < N) {
@@ -474,69 +502,64 @@ __global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const Atte
       s_m[r] = -INFINITY;
     }
     fence_async_smem();
-    named_sync(3, 256);
+    named_sync(kAllSoftmax, ST);
     if (lane == 0) mbar_arrive(q_full);
     const int min_lim = *s_minlim;
     const int nvalid = min(N, R - row0);  // columns that are real query rows
     const bool active = c0 < nvalid;      // warp-uniform
 
     const int gbar = 1 + (warp >> 2), gtid = tid & 127;
-    auto warp_wait = [&](uint64_t* bar, uint32_t parity) {
-      bool ok = true;
-      if (lane == 0) ok = wait_bar(bar, parity, s_abort, p.flags);
-      return __shfl_sync(0xffffffffu, ok, 0);
+    auto warp_wait = [&](uint64_t* bar, uint32_t parity) {  // (every lane: no hand-over)
+      wait_bar(bar, parity, s_abort, p.flags);
+      __syncwarp();
     };
-    // The two column halves (warps 0-3 and 4-7) are independent groups: each
-    // votes and reduces over its own 128 threads (barrier 1 + half).  A wait
+    // The column groups (four warps each, the tile's 128 tokens) are
+    // independent: each votes and reduces over its own 128 threads.  A wait
     // that runs out sets the abort flag; the loop then runs to its end with
     // every later wait returning at once, so no thread leaves a barrier
     // sequence the others still follow.
-    bool unset = active;  // some column of this half has no maximum yet
+    bool unset = active;  // some column of this group has no maximum yet
+    // where this thread's pieces go in a P^T buffer: byte o of its token's row
+    // lies in atom o / PA, 16-byte chunks xor-swizzled
+    uint32_t p_at[NP];
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+      const uint32_t o = q * N + c0;
+      p_at[q] = (o / T::PA) * T::PSTRIDE +
+                swz<T::PSWB>((uint32_t)(j >> 3) * (8 * T::PA) + (j & 7) * T::PA + o % T::PA);
+    }
     uint64_t lsum[NH / 2];  // this token's share of the row sums, two rows each
 #pragma unroll
     for (int e = 0; e < NH / 2; ++e) lsum[e] = 0;
     for (int i = 0; i < ntiles; ++i) {
       const int sb = i & 1;
-      // S(i) done also means PV(i-2) done: P buffer sb is free again
-      warp_wait(&kv_full[i % KS], (i / KS) & 1);  // (passed: the tile's scales are visible)
-      warp_wait(&s_full[sb], (i >> 1) & 1);
+      warp_wait(&s_full[i % KS], (i / KS) & 1);
       tc_fence_after();
       const int tile_tok0 = u.tok_begin + i * kTileTok;
       const int tok = tile_tok0 + j;
-      const bool tok_ok = tok < tok_end;
       const bool mask_rows = tile_tok0 + kTileTok - 1 > min_lim;
       float x[NH];
       uint64_t iv2 = 0;
       bool trig = false;
       if (active) {
-        // this token's scales
-        const float* sc = sSc + (i % KS) * (T::SCB / 4);
-        float ks = tok_ok ? sc[j] : 1.f, vs = tok_ok ? sc[kTileTok + j] : 1.f;
-        const float ksc = fminf(fmaxf(ks, kMinScale), kMaxScale);
-        const float vsc = fminf(fmaxf(vs, kMinScale), kMaxScale);
-        if (ksc != ks || vsc != vs) atomicOr(p.flags, 0x20u);
-        const float lv = log2_scale(vsc);
-        const float iv1 = ex2(-lv);
-        const uint64_t ks2 = pack_f32x2(ksc, ksc), lv2 = pack_f32x2(lv, lv);
-        iv2 = pack_f32x2(iv1, iv1);
+        const float* sc = sSc + (i % KS) * (T::SCB / 4) + j;  // this token's scales
+        const float ks = sc[0], lv = sc[kTileTok], iv = sc[2 * kTileTok];
+        const uint64_t ks2 = pack_f32x2(ks, ks), lv2 = pack_f32x2(lv, lv);
+        iv2 = pack_f32x2(iv, iv);
+        uint32_t sv[NH];
+        tmem_ld<NH>(tmem + lane_base + T::SCOL + N * (i % KS) + c0, sv);
+        tmem_wait_ld<NH>(sv);
 #pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-          uint32_t sv[CW];
-          const int cb = c0 + ch * CW;
-          tmem_ld<CW>(tmem + lane_base + T::SCOL + N * sb + cb, sv);
-          tmem_wait_ld<CW>(sv);
+        for (int e4 = 0; e4 < NH; e4 += 4) {
+          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(s_f + c0 + e4);
+          const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + c0 + e4);
 #pragma unroll
-          for (int e4 = 0; e4 < CW; e4 += 4) {
-            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(s_f + cb + e4);
-            const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + cb + e4);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint64_t s2 = pack_f32x2(__uint_as_float(sv[e4 + 2 * e]),
-                                             __uint_as_float(sv[e4 + 2 * e + 1]));
-              unpack_f32x2(fma_f32x2(s2, mul_f32x2(e ? f.y : f.x, ks2),
-                                     add_f32x2(e ? nm.y : nm.x, lv2)),
-                           x[ch * CW + e4 + 2 * e], x[ch * CW + e4 + 2 * e + 1]);
-            }
+          for (int e = 0; e < 2; ++e) {
+            const uint64_t s2 = pack_f32x2(__uint_as_float(sv[e4 + 2 * e]),
+                                           __uint_as_float(sv[e4 + 2 * e + 1]));
+            unpack_f32x2(fma_f32x2(s2, mul_f32x2(e ? f.y : f.x, ks2),
+                                   add_f32x2(e ? nm.y : nm.x, lv2)),
+                         x[e4 + 2 * e], x[e4 + 2 * e + 1]);
           }
         }
         if (mask_rows) {
@@ -562,17 +585,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const Atte
           for (int e = 2; e < NH; e += 2) mx = fmax3(mx, x[e], x[e + 1]);
           trig = mx > kRaise;
         }
-        trig = trig && tok_ok;
+        if (tile_tok0 + kTileTok > tok_end && tok >= tok_end) {  // past the unit's end
+          trig = false;
+#pragma unroll
+          for (int e = 0; e < NH; ++e) x[e] = -INFINITY;
+        }
       }
       if (named_or(gbar, 128, trig)) {
-        // ---- raise this half's maxima to the tile's row maxima ---------------
+        // ---- raise this group's maxima to the tile's row maxima ---------------
         if (gtid < NH) s_max[c0 + gtid] = INT32_MIN;
         named_sync(gbar, 128);
         if (active) {  // lane e keeps column e's warp maximum: one atomic per lane
           int kk = INT32_MIN;
 #pragma unroll
           for (int e = 0; e < NH; ++e) {
-            const int k = __reduce_max_sync(0xffffffffu, fkey(tok_ok ? x[e] : -INFINITY));
+            const int k = __reduce_max_sync(0xffffffffu, fkey(x[e]));
             kk = lane == e ? k : kk;
           }
           if (lane < NH) atomicMax(&s_max[c0 + lane], kk);
@@ -606,54 +633,51 @@ __global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const Atte
 #pragma unroll
           for (int e = 0; e < NH / 2; ++e)
             lsum[e] = mul_f32x2(lsum[e], *reinterpret_cast<const uint64_t*>(s_corr + c0 + 2 * e));
-          for (int blk = 0; blk < (DV / 128) * NP; ++blk)
+          for (int blk = 0; blk < (DV / 128) * NP; ++blk) {
+            uint32_t ov[NH];
+            const uint32_t oa = tmem + lane_base + T::OCOL + blk * N + c0;
+            tmem_ld<NH>(oa, ov);
+            tmem_wait_ld<NH>(ov);
 #pragma unroll
-            for (int ch = 0; ch < NCH; ++ch) {
-              uint32_t ov[CW];
-              const uint32_t oa = tmem + lane_base + T::OCOL + blk * N + c0 + ch * CW;
-              tmem_ld<CW>(oa, ov);
-              tmem_wait_ld<CW>(ov);
-#pragma unroll
-              for (int e = 0; e < CW; ++e)
-                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * s_corr[c0 + ch * CW + e]);
-              tmem_st<CW>(oa, ov);
-            }
+            for (int e = 0; e < NH; ++e)
+              ov[e] = __float_as_uint(__uint_as_float(ov[e]) * s_corr[c0 + e]);
+            tmem_st<NH>(oa, ov);
+          }
           tmem_wait_st();
         }
       }
       // ---- weights: the P^T row of this token, NP pieces ----------------------
+      if (i >= 2) warp_wait(&pv_done[sb], ((i - 2) >> 1) & 1);  // P buffer sb is free
       if (active) {
-        // Row byte off of this token lies in atom off / PA; 16-byte chunks are
-        // xor-swizzled inside the atom's 1024-byte blocks.
-        uint8_t* pt = sP + sb * T::PB;
-        const uint32_t pj = (uint32_t)(j >> 3) * (8 * T::PA) + (j & 7) * T::PA;
-        auto at = [&](int piece, int e) {
-          const uint32_t o = piece * N + c0 + e;
-          return pt + (o / T::PA) * T::PSTRIDE + swz<T::PSWB>(pj + o % T::PA);
-        };
+        uint32_t h[NP][NH / 4];
 #pragma unroll
-        for (int e8 = 0; e8 < NH; e8 += 8) {
-          uint32_t h[NP][4];
+        for (int e = 0; e < NH / 4; ++e) {
+          uint32_t rest[2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float a = 0.f, b = 0.f;
-            if (tok_ok) {
-              a = ex2(x[e8 + 2 * e]);
-              b = ex2(x[e8 + 2 * e + 1]);
-            }
-            lsum[e8 / 2 + e] = fma_f32x2(pack_f32x2(a, b), iv2, lsum[e8 / 2 + e]);
-            uint32_t rest = f32x2_to_f16x2(a, b);
-#pragma unroll
-            for (int q = 0; q < NP; ++q) {
-              h[q][e] = e4m3x2_of_f16x2(rest);
-              if (q + 1 < NP)  // (rest - piece) * 32: exact in f16
-                rest = hmul2(hsub2(rest, e4m3x2_to_f16x2(h[q][e])), 0x50005000u);
-            }
+          for (int k = 0; k < 2; ++k) {
+            const int col = 4 * e + 2 * k;
+            const float a = ex2(x[col]), b = ex2(x[col + 1]);
+            lsum[col / 2] = fma_f32x2(pack_f32x2(a, b), iv2, lsum[col / 2]);
+            rest[k] = f32x2_to_f16x2(a, b);
           }
 #pragma unroll
-          for (int q = 0; q < NP; ++q)
-            *reinterpret_cast<uint2*>(at(q, e8)) =
-                make_uint2(h[q][0] | (h[q][1] << 16), h[q][2] | (h[q][3] << 16));
+          for (int q = 0; q < NP; ++q) {
+            h[q][e] = e4m3x4_of_f16(rest[0], rest[1]);
+            if (q + 1 < NP) {  // (rest - piece) * 32: exact in f16
+              uint32_t back[2];
+              e4m3x4_to_f16(h[q][e], back[0], back[1]);
+              rest[0] = hmul2(hsub2(rest[0], back[0]), 0x50005000u);
+              rest[1] = hmul2(hsub2(rest[1], back[1]), 0x50005000u);
+            }
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+          uint8_t* at = sP + sb * T::PB + p_at[q];
+          if constexpr (NH == 16)
+            *reinterpret_cast<uint4*>(at) = make_uint4(h[q][0], h[q][1], h[q][2], h[q][3]);
+          else
+            *reinterpret_cast<uint2*>(at) = make_uint2(h[q][0], h[q][1]);
         }
       }
       fence_async_smem();
@@ -686,62 +710,58 @@ __global__ void __launch_bounds__(kThreads, 1) attend_e4m3_ext_kernel(const Atte
       const bool partial = p.split && u.num_splits > 1;
       const int Hq = p.num_qo_heads;
       if (active) {
-        // lane e (mod CW) derives normaliser and output row of column e, once
-        const int e_l = lane & (CW - 1);
+        // lane e (mod NH) derives normaliser and output row of column e, once
+        const int e_l = lane & (NH - 1), col_l = c0 + e_l;
         uint16_t* const out_u = p.out + (int64_t)u.qo_begin * Hq * DV;
         float* const part_u = partial ? p.partial_o + (int64_t)u.partial_base * DV : nullptr;
-#pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-          const int col_l = c0 + ch * CW + e_l;
-          float f_l = 0.f;
-          int64_t off_l = 0;  // output row of the column, from the unit's first row
-          if (col_l < nvalid) {
-            const float L = s_l[col_l] + s_l[N + col_l] + s_l[2 * N + col_l] + s_l[3 * N + col_l];
-            const float m = s_m[col_l];
-            const bool any = L > 0.f && m != -INFINITY;
-            f_l = any ? 1.f / L : 0.f;
-            const float lse_v = any ? (m + log2f(L)) * kLn2 : -INFINITY;
-            const int gr = row0 + col_l, qi = gr / G, head = u.h_kv * G + gr % G;
-            off_l = partial ? ((int64_t)qi * Hq + head) * u.num_splits + u.split
-                            : (int64_t)qi * Hq + head;
-            if (q4 == 0 && lane < CW) {
-              if (!partial) {
-                if (p.lse) p.lse[(int64_t)u.qo_begin * Hq + off_l] = lse_v;
-              } else {
-                p.partial_lse[(int64_t)u.partial_base + off_l] = lse_v;
-              }
+        float f_l = 0.f;
+        int64_t off_l = 0;  // output row of the column, from the unit's first row
+        if (col_l < nvalid) {
+          const float L = s_l[col_l] + s_l[N + col_l] + s_l[2 * N + col_l] + s_l[3 * N + col_l];
+          const float m = s_m[col_l];
+          const bool any = L > 0.f && m != -INFINITY;
+          f_l = any ? 1.f / L : 0.f;
+          const float lse_v = any ? (m + log2f(L)) * kLn2 : -INFINITY;
+          const int gr = row0 + col_l, qi = gr / G, head = u.h_kv * G + gr % G;
+          off_l = partial ? ((int64_t)qi * Hq + head) * u.num_splits + u.split
+                          : (int64_t)qi * Hq + head;
+          if (q4 == 0 && lane < NH) {
+            if (!partial) {
+              if (p.lse) p.lse[(int64_t)u.qo_begin * Hq + off_l] = lse_v;
+            } else {
+              p.partial_lse[(int64_t)u.partial_base + off_l] = lse_v;
             }
           }
+        }
 #pragma unroll
-          for (int b = 0; b < DV / 128; ++b) {
-            float o[CW];
+        for (int b = 0; b < DV / 128; ++b) {
+          float o[NH];
 #pragma unroll
-            for (int q = NP - 1; q >= 0; --q) {  // o = o0 + (o1 + o2 / 32) / 32
-              uint32_t ov[CW];
-              tmem_ld<CW>(tmem + lane_base + T::OCOL + b * T::PN + q * N + c0 + ch * CW, ov);
-              tmem_wait_ld<CW>(ov);
+          for (int q = NP - 1; q >= 0; --q) {  // o = o0 + (o1 + o2 / 32) / 32
+            uint32_t ov[NH];
+            tmem_ld<NH>(tmem + lane_base + T::OCOL + b * T::PN + q * N + c0, ov);
+            tmem_wait_ld<NH>(ov);
 #pragma unroll
-              for (int e = 0; e < CW; ++e)
-                o[e] = q == NP - 1 ? __uint_as_float(ov[e])
-                                   : fmaf(o[e], 0.03125f, __uint_as_float(ov[e]));
-            }
+            for (int e = 0; e < NH; ++e)
+              o[e] = q == NP - 1 ? __uint_as_float(ov[e])
+                                 : fmaf(o[e], 0.03125f, __uint_as_float(ov[e]));
+          }
 #pragma unroll
-            for (int e = 0; e < CW; ++e) {
-              const float f = __shfl_sync(0xffffffffu, f_l, e);
-              const int64_t off = __shfl_sync(0xffffffffu, off_l, e);
-              if (c0 + ch * CW + e < nvalid) {
-                const float v = f != 0.f ? o[e] * f : 0.f;
-                if (!partial)
-                  out_u[off * DV + 128 * b + j] = pack_out1(v, p.out_f16);
-                else
-                  part_u[off * DV + 128 * b + j] = v;
-              }
+          for (int e = 0; e < NH; ++e) {
+            const float f = __shfl_sync(0xffffffffu, f_l, e);
+            const int64_t off = __shfl_sync(0xffffffffu, off_l, e);
+            if (c0 + e < nvalid) {
+              const float v = f != 0.f ? o[e] * f : 0.f;
+              if (!partial)
+                out_u[off * DV + 128 * b + j] = pack_out1(v, p.out_f16);
+              else
+                part_u[off * DV + 128 * b + j] = v;
             }
           }
         }
       }
       if (partial)
-        merge_if_last<N, DV, 256, 4>(p, u, row0, R, s_fin, tid, [] { named_sync(3, 256); });
+        merge_if_last<N, DV, ST, 4>(p, u, row0, R, s_fin, tid, [] { named_sync(kAllSoftmax, ST); });
     }
     tc_fence_before();
   }
@@ -760,7 +780,7 @@ bool make_ext(bool p1, AttendConfig* cfg) {
   cfg->dk = DK;
   cfg->dv = DV;
   cfg->rows = N;
-  cfg->warps = kThreads / 32;
+  cfg->warps = Ext<DK, DV, N, NP>::THREADS / 32;
   cfg->units_per_cta = 1;
   cfg->smem_bytes = Ext<DK, DV, N, NP>::SMEM;
   cfg->func = p1 ? reinterpret_cast<const void*>(attend_e4m3_ext_kernel<DK, DV, N, NP, true>)
