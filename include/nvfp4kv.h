@@ -542,6 +542,7 @@ int nvfp4kv_e4m3_append(const nvfp4kv_e4m3_cache* cache, const void* k, int64_t 
 /* nvfp4kv_decode_run over an E4M3 cache: the same plan (made with kernel = 5),
  * split, merge, live lengths, outputs and flags.
  *   q [dev]  as in nvfp4kv_decode_run; q_dtype 0 bf16, 1 f16.
+ *   out [dev]  8-byte aligned.
  * A scale outside [2^-64, 2^64] sets NVFP4KV_FLAG_BAD_SCALE.  Slots past a
  * request's length may hold anything. */
 int nvfp4kv_e4m3_decode_run(const nvfp4kv_plan_info* info, const void* q, int64_t q_stride_tok,

@@ -786,6 +786,8 @@ int attend_e4m3(const nvfp4kv_plan_info* info, const void* q, int64_t q_stride_t
                               workspace_bytes, out))
     return st;
   if (info->num_units == 0) return ok();
+  if (!aligned(out, 8) || !aligned(lse, 4))
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "out must be 8-byte and lse 4-byte aligned");
   AttendConfig cfg{};
   if (!lookup_kernel(kKernelE4m3, info->head_dim_qk, info->head_dim_vo, info->page_size,
                      info->out_dtype, info->rows_per_block, &cfg))

@@ -52,7 +52,8 @@ struct E4Traits {
   static constexpr int VCH = DV / 8 / VCB;            // V chunks per lane
   static constexpr int MT = DV / 16;                  // PV m-tiles
   static constexpr int PIPE_BYTES = WARPS * STAGES * STAGE_BYTES;
-  static constexpr int COMB_BYTES = WARPS * RB * (DV + 2) * 4;
+  static constexpr int OS = DV + 4;                   // row stride of the warps' results
+  static constexpr int COMB_BYTES = WARPS * RB * (OS + 2) * 4;
   static constexpr int MAIN_BYTES = PIPE_BYTES > COMB_BYTES ? PIPE_BYTES : COMB_BYTES;
   static constexpr int QROW = DK + 8;                 // f16 elements, padded
   static constexpr int OFF_Q = MAIN_BYTES;
@@ -448,8 +449,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) lrow[k] += __shfl_xor_sync(0xffffffffu, lrow[k], o);
   __syncthreads();  // every warp is done with its ring
-  float* sO = reinterpret_cast<float*>(smem);   // [WARPS][RB][DV]
-  float* sM = sO + WARPS * T::RB * DV;          // [WARPS][RB]
+  float* sO = reinterpret_cast<float*>(smem);   // [WARPS][RB][OS]
+  float* sM = sO + WARPS * T::RB * T::OS;       // [WARPS][RB]
   float* sL = sM + WARPS * T::RB;               // [WARPS][RB]
   if (g == 0) {
 #pragma unroll
@@ -462,12 +463,12 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
   for (int mt = 0; mt < T::MT; ++mt) {
     constexpr int PC = T::VCB / 2;  // m-tiles of a chunk
     const int d = (mt / PC) * 128 + g * T::VCB + 2 * (mt % PC);
-    float* o0 = sO + (warp * T::RB + 2 * t) * DV + d;
+    float* o0 = sO + (warp * T::RB + 2 * t) * T::OS + d;
     *reinterpret_cast<float2*>(o0) = make_float2(oacc[mt][0], oacc[mt][2]);
-    *reinterpret_cast<float2*>(o0 + DV) = make_float2(oacc[mt][1], oacc[mt][3]);
+    *reinterpret_cast<float2*>(o0 + T::OS) = make_float2(oacc[mt][1], oacc[mt][3]);
   }
   __syncthreads();
-  finish_unit<T::RB, DV, WARPS>(p, u, row0, R, sM, sL, sO, sRowF);
+  finish_rows<T::RB, DV, WARPS, T::OS>(p, u, row0, R, sM, sL, sO, sRowF);
 }
 
 template <int DK, int DV, int WARPS, int STAGES, int MINB>
@@ -494,11 +495,11 @@ bool attend_config_e4m3(int dk, int dv, int page_size, int rows, bool out_f16,
   // blocks of 8 rows, each reading the keys again
   if (rows > 8 && attend_config_e4m3_ext(dk, dv, page_size, rows, out_f16, cfg)) return true;
   const bool p1 = page_size == 1;
-  if (dk == 64 && dv == 64) return make_e4m3<64, 64, 4, 6, 3>(p1, cfg);
-  if (dk == 128 && dv == 128) return make_e4m3<128, 128, 4, 4, 3>(p1, cfg);
-  if (dk == 256 && dv == 128) return make_e4m3<256, 128, 4, 4, 2>(p1, cfg);
+  if (dk == 64 && dv == 64) return make_e4m3<64, 64, 4, 3, 4>(p1, cfg);
+  if (dk == 128 && dv == 128) return make_e4m3<128, 128, 4, 3, 3>(p1, cfg);
+  if (dk == 256 && dv == 128) return make_e4m3<256, 128, 4, 3, 2>(p1, cfg);
   if (dk == 256 && dv == 256) return make_e4m3<256, 256, 4, 3, 2>(p1, cfg);
-  if (dk == 512 && dv == 256) return make_e4m3<512, 256, 4, 4, 1>(p1, cfg);
+  if (dk == 512 && dv == 256) return make_e4m3<512, 256, 8, 2, 1>(p1, cfg);
   return false;
 }
 
