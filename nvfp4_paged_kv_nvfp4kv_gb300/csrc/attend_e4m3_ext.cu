@@ -168,7 +168,7 @@ struct Ext {
   static_assert(DK % 128 == 0 && DV % 128 == 0, "operand rows of 128 bytes");
   static_assert(OFF_P % 1024 == 0 && OFF_Q % 1024 == 0 && OFF_MISC % 16 == 0, "align");
   static_assert(SMEM <= 232448 && COLS <= 512 && PN % 16 == 0 && PN <= 256, "resources");
-  static_assert(20 * 8 + 16 + (8 * N + 2 * N + 4 + 4 * N) * 4 <= MISC, "misc");
+  static_assert(20 * 8 + 16 + (7 * N + 2 * N + 4 + 4 * N) * 4 <= MISC, "misc");
 };
 
 // P1: 1-token pages
@@ -195,7 +195,6 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
   uint64_t* fin = bars + 17;      // [2] wind-down of the two issuers' products
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 20);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
-  int* s_minlim = reinterpret_cast<int*>(s_tmem + 2);
   // per query row: score factor, -m, raise threshold, causal limit
   float* s_f = reinterpret_cast<float*>(s_tmem + 4);
   float* s_nm = s_f + N;
@@ -204,8 +203,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
   float* s_m = reinterpret_cast<float*>(s_lim + N);  // m (log2), -inf before the first tile
   int* s_max = reinterpret_cast<int*>(s_m + N);      // reduction keys, then shifts
   float* s_corr = reinterpret_cast<float*>(s_max + N);
-  int* s_qamax = reinterpret_cast<int*>(s_corr + N);
-  float* s_fin = reinterpret_cast<float*>(s_qamax + N);  // [2N + 4]
+  float* s_fin = s_corr + N;                         // [2N + 4]
   float* s_l = s_fin + 2 * N + 4;                        // [4][N] row sums of the lane quarters
 
   const WorkUnit u = load_unit(p);
@@ -241,9 +239,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
     mbar_init(q_full, SW);
     mbar_init_fence();
     *s_abort = 0;
-    *s_minlim = INT32_MAX;
   }
-  if (tid < N) s_qamax[tid] = 0;
   if (warp == 0) {
     tmem_alloc(s_tmem, T::TCOLS);
     tmem_relinquish();
@@ -422,46 +418,33 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
       if (p.q_f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
       return make_float2(bf16_bits_to_f32(w & 0xFFFFu), bf16_bits_to_f32(w >> 16));
     };
-    // ---- Q pieces, swizzled: 8 dims (one 16-byte load) at a time ------------
-    constexpr int QCH = N * DK / 8;
-    auto q_load = [&](int ci) {
-      const int gr = row0 + ci / (DK / 8);
+    // ---- Q pieces, swizzled: a thread takes 8 dims (16 bytes) of a row, the
+    // row's neighbouring DK / 8 threads share its largest |q| by shuffles --------
+    constexpr int QW = DK / 8;
+    static_assert(N * QW % 32 == 0 && ST % 32 == 0 && QW <= 32, "whole warps of whole rows");
+    for (int ci = tid; ci < N * QW; ci += ST) {
+      const int r = ci / QW, c8 = ci % QW, gr = row0 + r;
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
       if (gr < R)
         v = *reinterpret_cast<const uint4*>(p.q + (int64_t)(u.qo_begin + gr / G) * p.q_stride_tok +
                                             (int64_t)(u.h_kv * G + gr % G) * p.q_stride_head +
-                                            (ci % (DK / 8)) * 8);
-      return v;
-    };
-#pragma unroll 4
-    for (int ci = tid; ci < QCH; ci += ST) {
-      const uint4 v = q_load(ci);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      float am = 0.f;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 x = q2(w[e]);
-        am = fmaxf(am, fmaxf(fabsf(x.x), fabsf(x.y)));
-      }
-      atomicMax(&s_qamax[ci / (DK / 8)], __float_as_int(am));
-    }
-    named_sync(kAllSoftmax, ST);
-    auto exp_of = [&](int r) {  // e with amax * 2^e in [128, 256)
-      const float amax = __int_as_float(s_qamax[r]);
-      int e = 0;
-      if (amax > 0.f) e = 7 - (int)((__float_as_uint(amax) >> 23) & 0xFF) + 127;
-      return max(-120, min(120, e));
-    };
-#pragma unroll 2
-    for (int ci = tid; ci < QCH; ci += ST) {
-      const uint4 v = q_load(ci);
-      const int r = ci / (DK / 8), c8 = ci % (DK / 8);
-      const float up = __uint_as_float((uint32_t)(127 + exp_of(r)) << 23);
+                                            c8 * 8);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
       float2 rest[4];
+      float amax = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         rest[e] = q2(w[e]);
+        amax = fmaxf(amax, fmaxf(fabsf(rest[e].x), fabsf(rest[e].y)));
+      }
+#pragma unroll
+      for (int o = QW / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      int ex = 0;  // amax * 2^ex in [128, 256)
+      if (amax > 0.f) ex = 7 - (int)((__float_as_uint(amax) >> 23) & 0xFF) + 127;
+      ex = max(-120, min(120, ex));
+      const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
         rest[e].x *= up;
         rest[e].y *= up;
       }
@@ -483,28 +466,19 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
         }
         *reinterpret_cast<uint2*>(sQ + q * T::QB + swz<3>(off)) = make_uint2(h[0], h[1]);
       }
-    }
-    if (tid < N) {
-      const int r = tid, gr = row0 + r;
-      if (gr < R) {
-        const int lim = p.causal ? (u.kv_len - u.qo_len + gr / G) : (u.kv_len - 1);
-        s_f[r] = p.qk_scale_log2 * __uint_as_float((uint32_t)(127 - exp_of(r)) << 23);
-        s_nm[r] = 0.f;
-        s_thr[r] = -INFINITY;  // no maximum yet: any visible score raises
-        s_lim[r] = lim;
-        atomicMin(s_minlim, lim);
-      } else {  // padding row: every weight 0, never raises
-        s_f[r] = 0.f;
-        s_nm[r] = -INFINITY;
-        s_thr[r] = INFINITY;
-        s_lim[r] = -1;
+      if (c8 == 0) {
+        const bool real = gr < R;  // a padding row: every weight 0, never raises
+        s_f[r] = real ? p.qk_scale_log2 * __uint_as_float((uint32_t)(127 - ex) << 23) : 0.f;
+        s_nm[r] = real ? 0.f : -INFINITY;
+        s_thr[r] = real ? -INFINITY : INFINITY;  // no maximum yet: any visible score raises
+        s_lim[r] = !real ? -1 : p.causal ? u.kv_len - u.qo_len + gr / G : u.kv_len - 1;
+        s_m[r] = -INFINITY;
       }
-      s_m[r] = -INFINITY;
     }
     fence_async_smem();
     named_sync(kAllSoftmax, ST);
     if (lane == 0) mbar_arrive(q_full);
-    const int min_lim = *s_minlim;
+    const int min_lim = p.causal ? u.kv_len - u.qo_len + row0 / G : u.kv_len - 1;
     const int nvalid = min(N, R - row0);  // columns that are real query rows
     const bool active = c0 < nvalid;      // warp-uniform
 
