@@ -1,5 +1,5 @@
 // attend_e4m3.cu -- attention over a paged cache of E4M3 codes with one scale
-// per page and kv head, blocks of at most 8 query rows, sm_103a.
+// per page and kv head, blocks of 8 or 16 query rows, sm_103a.
 //
 // With a_j, b_j the K and V scale of token j's page and c_j, d_j its codes:
 //   s_j = sm_scale * a_j * (q . c_j),  o = sum_j p_j b_j d_j / sum_j p_j,
@@ -14,7 +14,7 @@
 //  * A warp owns every WARPS-th tile of 16 tokens (one page, or sixteen
 //    1-token pages) and streams its K rows, V rows and scales through a ring
 //    of STAGES stages with cp.async, rows and pages at any byte strides.
-//  * S^T = C Q^T (M = 16 tokens, N = 8 query rows): a lane's 16 contiguous
+//  * S^T = C Q^T (M = 16 tokens, N = 8 query rows, once or twice): a lane's 16 contiguous
 //    bytes of a K row are the A operand of four k-steps under a permutation
 //    of the dims that Q's fragments share.  O^T += D^T P'^T with P' kept in
 //    registers (movmatrix); the A operand interleaves two V rows bytewise.
@@ -40,9 +40,9 @@ using namespace dev;
 constexpr float kRaiseLog2 = 8.f;
 constexpr float kMinScale = 0x1p-64f, kMaxScale = 0x1p64f;
 
-template <int DK, int DV, int WARPS, int STAGES>
+template <int DK, int DV, int WARPS, int STAGES, int NT>
 struct E4Traits {
-  static constexpr int RB = 8;
+  static constexpr int RB = 8 * NT;                   // query rows: NT product columns of 8
   static constexpr int K_BYTES = 16 * DK, V_BYTES = 16 * DV;
   static constexpr int OFF_V = K_BYTES, OFF_SC = OFF_V + V_BYTES;  // 16 K scales, 16 V scales
   static constexpr int STAGE_BYTES = OFF_SC + 128;
@@ -97,9 +97,9 @@ __device__ __forceinline__ float log2_scale(float s) {
 }
 
 // P1: 1-token pages
-template <int DK, int DV, int WARPS, int STAGES, int MINB, bool P1>
+template <int DK, int DV, int WARPS, int STAGES, int NT, int MINB, bool P1>
 __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const AttendParams p) {
-  using T = E4Traits<DK, DV, WARPS, STAGES>;
+  using T = E4Traits<DK, DV, WARPS, STAGES, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   uint16_t* sQ = reinterpret_cast<uint16_t*>(smem + T::OFF_Q);
   float* sRowF = reinterpret_cast<float*>(smem + T::OFF_ROW);
@@ -260,43 +260,50 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
   }
   __syncthreads();
 
-  // this lane's query rows 2t and 2t + 1: score factor, -m (m the running
-  // maximum of x + log2 b, once the row has one: bit k of has_max) and sum
-  float f2[2], nm2[2], lrow[2];
+  // this lane's query rows 8 n + 2t and 8 n + 2t + 1 (k = 2 n and 2 n + 1):
+  // score factor, -m (m the running maximum of x + log2 b, once the row has
+  // one: bit k of has_max) and sum
+  constexpr int NR = 2 * NT;
+  float f2[NR], nm2[NR], lrow[NR];
+  int lim[NR];
   uint32_t has_max = 0;
   int min_lim = u.kv_len - 1;
   for (int rr = 0; rr < T::RB; ++rr)
     if (sRowLim[rr] >= 0) min_lim = min(min_lim, sRowLim[rr]);
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    f2[k] = sRowF[2 * t + k];
+  for (int k = 0; k < NR; ++k) {
+    const int rr = 8 * (k / 2) + 2 * t + k % 2;
+    f2[k] = sRowF[rr];
+    lim[k] = sRowLim[rr];
     nm2[k] = 0.f;
     lrow[k] = 0.f;
   }
-  const int lim0 = sRowLim[2 * t], lim1 = sRowLim[2 * t + 1];
   auto lane_threshold = [&]() {
     float th = INFINITY;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-      th = fminf(th, (has_max >> k) & 1u ? kRaiseLog2
-                                         : ((k ? lim1 : lim0) >= 0 ? -INFINITY : INFINITY));
+    for (int k = 0; k < NR; ++k)
+      th = fminf(th, (has_max >> k) & 1u ? kRaiseLog2 : (lim[k] >= 0 ? -INFINITY : INFINITY));
     return th;
   };
   float thr_lane = lane_threshold();
   // Q fragments: k-step 4 cc + m covers the 4 dims 16 (4 cc + t) + 4 m ..
-  uint32_t qreg[T::KSTEPS][2];
+  uint32_t qreg[NT][T::KSTEPS][2];
 #pragma unroll
-  for (int kk = 0; kk < T::KSTEPS; ++kk) {
-    const uint2 lo = *reinterpret_cast<const uint2*>(sQ + g * T::QROW + 16 * (4 * (kk / 4) + t) +
-                                                     4 * (kk % 4));
-    qreg[kk][0] = lo.x;
-    qreg[kk][1] = lo.y;
-  }
-  float oacc[T::MT][4];
+  for (int n = 0; n < NT; ++n)
 #pragma unroll
-  for (int mt = 0; mt < T::MT; ++mt)
+    for (int kk = 0; kk < T::KSTEPS; ++kk) {
+      const uint2 lo = *reinterpret_cast<const uint2*>(
+          sQ + (8 * n + g) * T::QROW + 16 * (4 * (kk / 4) + t) + 4 * (kk % 4));
+      qreg[n][kk][0] = lo.x;
+      qreg[n][kk][1] = lo.y;
+    }
+  float oacc[NT][T::MT][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) oacc[mt][k] = 0.f;
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int mt = 0; mt < T::MT; ++mt)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) oacc[n][mt][k] = 0.f;
 
   // rows this lane reads: tokens of mma rows g, g + 8 (K) and of P columns
   // 2t, 2t + 1, 2t + 8, 2t + 9 (V)
@@ -312,7 +319,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
     const int tok0 = u.tok_begin + (warp + i * WARPS) * 16;
 
     // ---- S^T = C Q^T ------------------------------------------------------
-    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+    float sa[NT][4] = {}, sb[NT][4] = {};
 #pragma unroll
     for (int cc = 0; cc < T::KCH; ++cc) {
       const uint32_t ka = st + kr0 * DK + 16 * k_pos<DK>(kr0, 4 * cc + t);
@@ -323,10 +330,9 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
         uint32_t f[4];
         e4m3x4_to_f16(a[m], f[0], f[2]);
         e4m3x4_to_f16(b[m], f[1], f[3]);
-        if (m & 1)
-          mma_16816(sb, f, qreg[4 * cc + m][0], qreg[4 * cc + m][1]);
-        else
-          mma_16816(sa, f, qreg[4 * cc + m][0], qreg[4 * cc + m][1]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          mma_16816(m & 1 ? sb[n] : sa[n], f, qreg[n][4 * cc + m][0], qreg[n][4 * cc + m][1]);
       }
     }
     // ---- the tile's scales: tokens kr0 (A) and kr0 + 8 (B) -----------------
@@ -335,59 +341,68 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
     const float lvA = log2_scale(checked_scale(lds_f32(sc + 64), p.flags));
     const float ksB = P1 ? checked_scale(lds_f32(sc + 32), p.flags) : ksA;
     const float lvB = P1 ? log2_scale(checked_scale(lds_f32(sc + 96), p.flags)) : lvA;
-    // x[0..3] = tokens kr0, kr0, kr0 + 8, kr0 + 8 x rows 2t, 2t + 1, 2t, 2t + 1
-    float x[4];
+    // x[n][0..3] = tokens kr0, kr0, kr0 + 8, kr0 + 8 x rows 2n, 2n+1, 2n, 2n+1
+    float x[NT][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      x[k] = fmaf(sa[k] + sb[k], f2[k & 1] * (k < 2 ? ksA : ksB),
-                  nm2[k & 1] + (k < 2 ? lvA : lvB));
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        x[n][k] = fmaf(sa[n][k] + sb[n][k], f2[2 * n + (k & 1)] * (k < 2 ? ksA : ksB),
+                       nm2[2 * n + (k & 1)] + (k < 2 ? lvA : lvB));
     if (tok0 + 15 > min_lim) {
       const int ta = tok0 + kr0, tb = ta + 8;
-      if (ta > lim0) x[0] = -INFINITY;
-      if (ta > lim1) x[1] = -INFINITY;
-      if (tb > lim0) x[2] = -INFINITY;
-      if (tb > lim1) x[3] = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < NR; ++k) {
+        if (ta > lim[k]) x[k / 2][k % 2] = -INFINITY;
+        if (tb > lim[k]) x[k / 2][2 + k % 2] = -INFINITY;
+      }
     }
-    const bool trig = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) > thr_lane;
-    if (__builtin_expect(__any_sync(0xffffffffu, trig), 0)) {
+    float top = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3]));
+#pragma unroll
+    for (int n = 1; n < NT; ++n)
+      top = fmaxf(top, fmaxf(fmaxf(x[n][0], x[n][1]), fmaxf(x[n][2], x[n][3])));
+    if (__builtin_expect(__any_sync(0xffffffffu, top > thr_lane), 0)) {
       // raise each row's maximum to this tile's (a row's values sit in the 8
       // lanes of the same t)
-      float mx[2] = {fmaxf(x[0], x[2]), fmaxf(x[1], x[3])};
+      float corr[NR];
+      bool moved = false;
 #pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
-        mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], o));
-      }
-      float corr[2] = {1.f, 1.f};
+      for (int k = 0; k < NR; ++k) {
+        float mx = fmaxf(x[k / 2][k % 2], x[k / 2][2 + k % 2]);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+        for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        corr[k] = 1.f;
         const bool has = (has_max >> k) & 1u;
-        if (mx[k] != -INFINITY && (!has || mx[k] > 0.f)) {
-          if (has) corr[k] = ex2(-mx[k]);
-          nm2[k] -= mx[k];
+        if (mx != -INFINITY && (!has || mx > 0.f)) {
+          if (has) corr[k] = ex2(-mx);
+          nm2[k] -= mx;
           has_max |= 1u << k;
-          x[k] -= mx[k];
-          x[k + 2] -= mx[k];
+          x[k / 2][k % 2] -= mx;
+          x[k / 2][2 + k % 2] -= mx;
         }
         lrow[k] *= corr[k];
+        moved |= corr[k] != 1.f;
       }
       thr_lane = lane_threshold();
-      if (corr[0] != 1.f || corr[1] != 1.f) {
+      if (moved) {
 #pragma unroll
-        for (int mt = 0; mt < T::MT; ++mt) {
-          oacc[mt][0] *= corr[0];
-          oacc[mt][1] *= corr[1];
-          oacc[mt][2] *= corr[0];
-          oacc[mt][3] *= corr[1];
-        }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int mt = 0; mt < T::MT; ++mt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) oacc[n][mt][k] *= corr[2 * n + (k & 1)];
       }
     }
-    const float p0 = ex2(x[0]), p1 = ex2(x[1]), p2 = ex2(x[2]), p3 = ex2(x[3]);
     const float ivA = ex2(-lvA), ivB = P1 ? ex2(-lvB) : ivA;
-    lrow[0] += p0 * ivA + p2 * ivB;
-    lrow[1] += p1 * ivA + p3 * ivB;
-    const uint32_t pf0 = movmatrix_trans(f32x2_to_f16x2(p0, p1));
-    const uint32_t pf1 = movmatrix_trans(f32x2_to_f16x2(p2, p3));
+    uint32_t pf[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float p0 = ex2(x[n][0]), p1 = ex2(x[n][1]), p2 = ex2(x[n][2]), p3 = ex2(x[n][3]);
+      lrow[2 * n] += p0 * ivA + p2 * ivB;
+      lrow[2 * n + 1] += p1 * ivA + p3 * ivB;
+      pf[n][0] = movmatrix_trans(f32x2_to_f16x2(p0, p1));
+      pf[n][1] = movmatrix_trans(f32x2_to_f16x2(p2, p3));
+    }
 
     // ---- O^T += D^T P'^T ----------------------------------------------------
     const int valid = u.kv_len - tok0;  // slots past it may hold a NaN code
@@ -436,8 +451,11 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
         e4m3x4_to_f16(l1, fa[2], fa[3]);
         e4m3x4_to_f16(h0, fb[0], fb[1]);
         e4m3x4_to_f16(h1, fb[2], fb[3]);
-        mma_16816(oacc[mt], fa, pf0, pf1);
-        mma_16816(oacc[mt + 1], fb, pf0, pf1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_16816(oacc[n][mt], fa, pf[n][0], pf[n][1]);
+          mma_16816(oacc[n][mt + 1], fb, pf[n][0], pf[n][1]);
+        }
       }
     }
   }
@@ -445,35 +463,39 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
 
   // ---- combine the warps ---------------------------------------------------
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+  for (int k = 0; k < NR; ++k)
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) lrow[k] += __shfl_xor_sync(0xffffffffu, lrow[k], o);
   __syncthreads();  // every warp is done with its ring
   float* sO = reinterpret_cast<float*>(smem);   // [WARPS][RB][OS]
   float* sM = sO + WARPS * T::RB * T::OS;       // [WARPS][RB]
   float* sL = sM + WARPS * T::RB;               // [WARPS][RB]
-  if (g == 0) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      sM[warp * T::RB + 2 * t + k] = (has_max >> k) & 1u ? -nm2[k] : -INFINITY;
-      sL[warp * T::RB + 2 * t + k] = lrow[k];
+  for (int n = 0; n < NT; ++n) {
+    const int r0 = warp * T::RB + 8 * n + 2 * t;
+    if (g == 0) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        sM[r0 + k] = (has_max >> (2 * n + k)) & 1u ? -nm2[2 * n + k] : -INFINITY;
+        sL[r0 + k] = lrow[2 * n + k];
+      }
     }
-  }
 #pragma unroll
-  for (int mt = 0; mt < T::MT; ++mt) {
-    constexpr int PC = T::VCB / 2;  // m-tiles of a chunk
-    const int d = (mt / PC) * 128 + g * T::VCB + 2 * (mt % PC);
-    float* o0 = sO + (warp * T::RB + 2 * t) * T::OS + d;
-    *reinterpret_cast<float2*>(o0) = make_float2(oacc[mt][0], oacc[mt][2]);
-    *reinterpret_cast<float2*>(o0 + T::OS) = make_float2(oacc[mt][1], oacc[mt][3]);
+    for (int mt = 0; mt < T::MT; ++mt) {
+      constexpr int PC = T::VCB / 2;  // m-tiles of a chunk
+      const int d = (mt / PC) * 128 + g * T::VCB + 2 * (mt % PC);
+      float* o0 = sO + r0 * T::OS + d;
+      *reinterpret_cast<float2*>(o0) = make_float2(oacc[n][mt][0], oacc[n][mt][2]);
+      *reinterpret_cast<float2*>(o0 + T::OS) = make_float2(oacc[n][mt][1], oacc[n][mt][3]);
+    }
   }
   __syncthreads();
   finish_rows<T::RB, DV, WARPS, T::OS>(p, u, row0, R, sM, sL, sO, sRowF);
 }
 
-template <int DK, int DV, int WARPS, int STAGES, int MINB>
+template <int DK, int DV, int WARPS, int STAGES, int NT, int MINB>
 bool make_e4m3(bool page1, AttendConfig* cfg) {
-  using T = E4Traits<DK, DV, WARPS, STAGES>;
+  using T = E4Traits<DK, DV, WARPS, STAGES, NT>;
   cfg->kind = kKernelE4m3;
   cfg->dk = DK;
   cfg->dv = DV;
@@ -481,9 +503,9 @@ bool make_e4m3(bool page1, AttendConfig* cfg) {
   cfg->warps = WARPS;
   cfg->smem_bytes = T::SMEM;
   cfg->units_per_cta = 1;
-  cfg->func = page1
-                  ? reinterpret_cast<const void*>(attend_e4m3_kernel<DK, DV, WARPS, STAGES, MINB, true>)
-                  : reinterpret_cast<const void*>(attend_e4m3_kernel<DK, DV, WARPS, STAGES, MINB, false>);
+  cfg->func =
+      page1 ? reinterpret_cast<const void*>(attend_e4m3_kernel<DK, DV, WARPS, STAGES, NT, MINB, true>)
+            : reinterpret_cast<const void*>(attend_e4m3_kernel<DK, DV, WARPS, STAGES, NT, MINB, false>);
   return true;
 }
 
@@ -491,15 +513,17 @@ bool make_e4m3(bool page1, AttendConfig* cfg) {
 
 bool attend_config_e4m3(int dk, int dv, int page_size, int rows, bool out_f16,
                         AttendConfig* cfg) {
-  // more rows than one block: the tensor-memory kernel where it is built, else
-  // blocks of 8 rows, each reading the keys again
-  if (rows > 8 && attend_config_e4m3_ext(dk, dv, page_size, rows, out_f16, cfg)) return true;
-  const bool p1 = page_size == 1;
-  if (dk == 64 && dv == 64) return make_e4m3<64, 64, 4, 3, 4>(p1, cfg);
-  if (dk == 128 && dv == 128) return make_e4m3<128, 128, 4, 3, 3>(p1, cfg);
-  if (dk == 256 && dv == 128) return make_e4m3<256, 128, 4, 3, 2>(p1, cfg);
-  if (dk == 256 && dv == 256) return make_e4m3<256, 256, 4, 3, 2>(p1, cfg);
-  if (dk == 512 && dv == 256) return make_e4m3<512, 256, 8, 2, 1>(p1, cfg);
+  // More than 16 rows: the tensor-memory kernel where it is built, else row
+  // blocks that each read the keys again.
+  if (rows > 16 && attend_config_e4m3_ext(dk, dv, page_size, rows, out_f16, cfg)) return true;
+  const bool p1 = page_size == 1, wide = rows > 8;
+  if (dk == 64 && dv == 64)
+    return wide ? make_e4m3<64, 64, 4, 3, 2, 3>(p1, cfg) : make_e4m3<64, 64, 4, 3, 1, 4>(p1, cfg);
+  if (dk == 128 && dv == 128)
+    return wide ? make_e4m3<128, 128, 4, 4, 2, 2>(p1, cfg) : make_e4m3<128, 128, 4, 3, 1, 3>(p1, cfg);
+  if (dk == 256 && dv == 128) return make_e4m3<256, 128, 4, 3, 1, 2>(p1, cfg);
+  if (dk == 256 && dv == 256) return make_e4m3<256, 256, 4, 3, 1, 2>(p1, cfg);
+  if (dk == 512 && dv == 256) return make_e4m3<512, 256, 8, 2, 1, 1>(p1, cfg);
   return false;
 }
 

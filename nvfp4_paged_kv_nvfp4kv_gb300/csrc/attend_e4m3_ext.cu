@@ -18,8 +18,8 @@
 //  * Row sums come from the unsplit float32 weights, a register per query row
 //    and thread, added up over the threads at the end.
 //
-// One CTA = one work unit (request, kv head, chunk of pages) x N = 16, 32 or
-// 64 query rows (the G heads of the group times the query positions); tiles of
+// One CTA = one work unit (request, kv head, chunk of pages) x N = 32 or 64
+// query rows (the G heads of the group times the query positions); tiles of
 // 128 tokens; M = 128 tokens (S^T) or 128 value dims (O^T) fill the product
 // for any N.  19 warps at N = 64:
 //  * loaders (two warps): cp.async of the tile's K and V rows straight into
@@ -134,7 +134,7 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
 
 template <int DK, int DV, int N, int NP>
 struct Ext {
-  static constexpr int NH = N >= 32 ? 16 : 8;      // query rows per softmax thread
+  static constexpr int NH = 16;                    // query rows per softmax thread
   static constexpr int CG = N / NH;                // column groups of four warps
   static constexpr int SW = 4 * CG;                // softmax warps
   static constexpr int THREADS = 32 * (SW + kLoaders + 2);
@@ -143,12 +143,12 @@ struct Ext {
   static constexpr int QB = N * DK;                // one query piece
   // P^T rows: NP * N weight pieces of a token, in atoms of PA bytes
   static constexpr int PN = NP * N;
-  static constexpr int PA = PN <= 32 ? 32 : PN <= 64 ? 64 : 128;
+  static constexpr int PA = PN <= 64 ? 64 : 128;
   static constexpr int PATOMS = (PN + PA - 1) / PA;
   static constexpr int PSTRIDE = kTileTok * PA;    // bytes of one atom column
   static constexpr int PB = PATOMS * PSTRIDE;
-  static constexpr uint32_t PSWZ = PA == 32 ? kSwz32 : PA == 64 ? kSwz64 : kSwz128;
-  static constexpr int PSWB = PA == 32 ? 1 : PA == 64 ? 2 : 3;
+  static constexpr uint32_t PSWZ = PA == 64 ? kSwz64 : kSwz128;
+  static constexpr int PSWB = PA == 64 ? 2 : 3;
   static constexpr int SCB = kTileTok * 12;        // K scale, log2 and inverse of the V scale
   static constexpr int MISC = 8192;
   static constexpr int FIXED = 2 * PB + NQ * QB + MISC + 1024;
@@ -648,10 +648,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
           uint8_t* at = sP + sb * T::PB + p_at[q];
-          if constexpr (NH == 16)
-            *reinterpret_cast<uint4*>(at) = make_uint4(h[q][0], h[q][1], h[q][2], h[q][3]);
-          else
-            *reinterpret_cast<uint2*>(at) = make_uint2(h[q][0], h[q][1]);
+          *reinterpret_cast<uint4*>(at) = make_uint4(h[q][0], h[q][1], h[q][2], h[q][3]);
         }
       }
       fence_async_smem();
@@ -764,15 +761,14 @@ bool make_ext(bool p1, AttendConfig* cfg) {
 
 }  // namespace
 
-// The kernel for (dk, dv), up to `rows` query rows per CTA; f16 outputs take
-// three weight pieces.
+// The kernel for (dk, dv) and more than 16 query rows per kv head; f16 outputs
+// take three weight pieces.
 bool attend_config_e4m3_ext(int dk, int dv, int page_size, int rows, bool out_f16,
                             AttendConfig* cfg) {
   const bool p1 = page_size == 1;
 #define NVFP4KV_EXT(DK_, DV_, N_) \
   return out_f16 ? make_ext<DK_, DV_, N_, 3>(p1, cfg) : make_ext<DK_, DV_, N_, 2>(p1, cfg)
   if (dk == 128 && dv == 128) {
-    if (rows <= 16) NVFP4KV_EXT(128, 128, 16);
     if (rows <= 32) NVFP4KV_EXT(128, 128, 32);
     NVFP4KV_EXT(128, 128, 64);
   }
