@@ -31,7 +31,7 @@
 namespace nvfp4kv {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr float kMinScale = 0x1p-64f, kMaxScale = 0x1p64f;
 
 template <bool F16>
@@ -152,35 +152,83 @@ __device__ __forceinline__ void append_block(const E4m3AppendParams& p, int kv, 
   if (lane == 0) *sc = s;
 }
 
-// CTA (x, y) takes request y; its warps walk the request's (page, head, K or
-// V) blocks.
+// The (page, head, K or V) blocks of all requests form one list; warp w of the
+// grid takes its entries w, w + W, ... (a CTA grid over requests would leave
+// most CTAs without work when their lengths differ).  The requests pass through
+// shared memory kThreads at a time: first row, tokens before the step and
+// first page of each, and the sum of the pages that those before it write.
 template <bool F16, int NCH, int CP>
-__global__ void __launch_bounds__(kWarps * 32, NCH <= 8 ? 6 : NCH <= 16 ? 4 : 2) e4m3_append_kernel(const E4m3AppendParams p) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int b = blockIdx.y; b < p.batch; b += gridDim.y) {
-    const int r0 = p.qo_indptr[b], r1 = p.qo_indptr[b + 1];
-    const int k0 = p.kv_indptr[b], k1 = p.kv_indptr[b + 1], last = p.last_page_len[b];
-    const int n = r1 - r0;
-    if (n == 0) continue;
-    const int64_t len = (int64_t)(k1 - k0 - 1) * p.page_size + last;
-    if (r0 < 0 || n < 0 || r1 > p.num_rows || k0 < 0 || k1 <= k0 || last < 1 ||
-        last > p.page_size || len < n) {
-      if (blockIdx.x == 0 && threadIdx.x == 0 && p.flags) atomicOr(p.flags, 0x2u);
-      continue;
+__global__ void __launch_bounds__(kThreads, NCH <= 8 ? 6 : NCH <= 16 ? 4 : 2)
+    e4m3_append_kernel(const E4m3AppendParams p) {
+  __shared__ int s_row[kThreads], s_new[kThreads], s_kv[kThreads], s_page[kThreads];
+  __shared__ int64_t s_begin[kThreads], s_first[kThreads + 1], s_sum[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int blocks = 2 * p.num_kv_heads;
+  // this warp's next entry: block r of the list's page c (stepped without a
+  // division)
+  const int wid = blockIdx.x * kWarps + warp, W = gridDim.x * kWarps;
+  const int wc = W / blocks, wr = W % blocks;
+  int64_t c = wid / blocks;
+  int r = wid % blocks;
+  for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+    const int b = b0 + tid;
+    int count = 0;
+    if (b < p.batch) {
+      const int r0 = p.qo_indptr[b], r1 = p.qo_indptr[b + 1];
+      const int k0 = p.kv_indptr[b], k1 = p.kv_indptr[b + 1], last = p.last_page_len[b];
+      const int64_t n = (int64_t)r1 - r0, np = (int64_t)k1 - k0;
+      const int64_t len = (np - 1) * p.page_size + last, begin = len - n;
+      if (n != 0) {
+        if (r0 < 0 || n < 0 || r1 > p.num_rows || k0 < 0 || np < 1 || last < 1 ||
+            last > p.page_size || begin < 0) {
+          if (blockIdx.x == 0 && p.flags) atomicOr(p.flags, 0x2u);
+        } else {
+          const int first = static_cast<int>(begin / p.page_size);
+          count = static_cast<int>(np) - first;
+          s_row[tid] = r0;
+          s_new[tid] = static_cast<int>(n);
+          s_kv[tid] = k0 + first;
+          s_begin[tid] = begin;
+          s_page[tid] = first;
+        }
+      }
     }
-    const int64_t begin = len - n;
-    const int first = static_cast<int>(begin / p.page_size);
-    const int blocks = 2 * p.num_kv_heads;
-    const int64_t items = (int64_t)(k1 - k0 - first) * blocks;
-    for (int64_t it = (int64_t)blockIdx.x * kWarps + warp; it < items;
-         it += (int64_t)gridDim.x * kWarps) {
-      const int c = first + static_cast<int>(it / blocks), r = static_cast<int>(it % blocks);
-      const int64_t pos = (int64_t)c * p.page_size;
+    int64_t sum = count;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    if (lane == 31) s_sum[warp] = sum;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      if (w < warp) sum += s_sum[w];
+    s_first[tid] = sum - count;
+    if (tid == kThreads - 1) s_first[kThreads] = sum;
+    __syncthreads();
+    const int64_t pages = s_first[kThreads];
+    while (c < pages) {
+      int lo = 0, hi = kThreads;  // the request whose pages hold entry c
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_first[mid] <= c) lo = mid; else hi = mid;
+      }
+      const int64_t begin = s_begin[lo], len = begin + s_new[lo];
+      const int64_t pos = (s_page[lo] + c - s_first[lo]) * p.page_size;
       const int a = static_cast<int>(max(begin - pos, (int64_t)0));
       const int z = static_cast<int>(min(len - pos, (int64_t)p.page_size));
-      append_block<F16, NCH, CP>(p, r & 1, r >> 1, p.kv_indices + k0 + c, a, z,
-                                 r0 + pos + a - begin, lane);
+      append_block<F16, NCH, CP>(p, r & 1, r >> 1, p.kv_indices + s_kv[lo] + c - s_first[lo], a,
+                                 z, s_row[lo] + pos + a - begin, lane);
+      c += wc;
+      r += wr;
+      if (r >= blocks) {
+        r -= blocks;
+        ++c;
+      }
     }
+    c -= pages;  // counted from the next requests' first page
+    __syncthreads();
   }
 }
 
@@ -188,20 +236,17 @@ __global__ void __launch_bounds__(kWarps * 32, NCH <= 8 ? 6 : NCH <= 16 ? 4 : 2)
 
 cudaError_t launch_e4m3_append(const E4m3AppendParams& p, cudaStream_t stream) {
   if (p.num_rows == 0 || p.batch == 0) return cudaSuccess;
-  // a request's pages are at most its rows, or rows / page_size + 2 of them
-  int64_t pages = p.num_rows / p.page_size + 2;
+  // every row may open a page of its own, else a request's rows fill theirs but
+  // for two: as many warps as blocks at most, and a wave of CTAs
+  int64_t pages = p.num_rows / p.page_size + 2 * (int64_t)p.batch;
   if (pages > p.num_rows) pages = p.num_rows;
-  int64_t gx = (pages * 2 * p.num_kv_heads + kWarps - 1) / kWarps;
-  const int64_t gy = p.batch < 65535 ? p.batch : 65535;
-  // the longest request alone may hold all rows, so every request gets as
-  // many CTAs as that needs, up to a few waves in all
-  const int64_t cap = (152 * 64 + gy - 1) / gy;
-  if (gx > cap) gx = cap;
-  const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+  int64_t grid = (pages * 2 * p.num_kv_heads + kWarps - 1) / kWarps;
+  if (grid > 152 * 6) grid = 152 * 6;
   const int dmax = p.dim[0] > p.dim[1] ? p.dim[0] : p.dim[1];
-#define NVFP4KV_E4M3_APPEND(NCH_, CP_)                                     \
-  (p.f16 ? e4m3_append_kernel<true, NCH_, CP_>                            \
-         : e4m3_append_kernel<false, NCH_, CP_>)<<<grid, kWarps * 32, 0, stream>>>(p)
+#define NVFP4KV_E4M3_APPEND(NCH_, CP_)                                                        \
+  (p.f16 ? e4m3_append_kernel<true, NCH_, CP_>                                                \
+         : e4m3_append_kernel<false, NCH_, CP_>)<<<static_cast<int>(grid), kThreads, 0,        \
+                                                   stream>>>(p)
   if (p.page_size == 1)
     NVFP4KV_E4M3_APPEND(2, 2);
   else if (dmax <= 64)
