@@ -148,6 +148,28 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageTablePar
     const int first = (int)k0, stop = (int)min(k0 + 32 * kChunk, (int64_t)pages);
     const int lo = owner(s_kv, 0, B, first);
     const int hi = stop <= s_kv[lo + 1] ? lo + 1 : owner(s_kv, lo, B, stop - 1) + 1;
+    if (hi == lo + 1) {
+      const int kv0 = s_kv[lo], taken = s_free[lo + 1] - s_free[lo];
+      const int held = s_kv[lo + 1] - kv0 - taken, end = stop - kv0;
+      int32_t* row = p.block_table + lo * p.table_stride;
+      const int32_t* fresh = p.free_pages + (head + s_free[lo]);  // page `held` on
+      const int c0 = first - kv0 + lane;
+      int32_t id[kChunk];
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) {
+        const int c = c0 + 32 * j;
+        if (c < end) id[j] = c < held ? row[c] : fresh[c - held];
+      }
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) {
+        const int c = c0 + 32 * j;
+        if (c < end) {
+          p.kv_indices[kv0 + c] = id[j];
+          if (c >= held) row[c] = id[j];
+        }
+      }
+      continue;
+    }
     int32_t id[kChunk];
     int32_t* enter[kChunk];  // where a taken page goes in the table
 #pragma unroll
