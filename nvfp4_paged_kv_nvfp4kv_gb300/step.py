@@ -36,7 +36,7 @@ def _entry(name):
     return fn
 
 
-def _wrong_device(dev, *tensors):
+def _check_device(dev, *tensors):
     for t in tensors:
         if t.get_device() != dev:
             raise ValueError("tensor on %s, the current device is cuda:%d" % (t.device, dev))
@@ -53,7 +53,7 @@ def _flag_ptr(flags, dev):
         return None
     if flags.dtype not in (torch.int32, torch.uint32) or flags.numel() < 1:
         raise ValueError("device_flags must be a 32-bit integer tensor")
-    _wrong_device(dev, flags)
+    _check_device(dev, flags)
     return flags.data_ptr()
 
 
@@ -108,7 +108,7 @@ class StepTable:
             t = getattr(self, name)
             setattr(s, name, None if t is None else t.data_ptr())
         s.max_pages, s.max_tokens = kv_indices.numel(), tokens
-        self._struct = s
+        self._struct, self._ref = s, C.byref(s)
 
     @classmethod
     def allocate(cls, batch, max_tokens, max_pages, device="cuda", slot_map=True):
@@ -133,12 +133,12 @@ def nvfp4kv_build_page_table(kv_len, qo_len, block_table, free_pages, free_head,
     if not (kv_len.numel() == qo_len.numel() == block_table.shape[0] == batch):
         raise ValueError("kv_len, qo_len and block_table must have the table's batch")
     dev = torch.cuda.current_device()
-    _wrong_device(dev, kv_len, qo_len, block_table, free_pages, table.kv_indptr,
+    _check_device(dev, kv_len, qo_len, block_table, free_pages, table.kv_indptr,
                   *(() if free_head is None else (free_head,)))
     st = _entry("nvfp4kv_build_page_table")(
         kv_len.data_ptr(), qo_len.data_ptr(), batch, page_size, block_table.data_ptr(),
         block_table.stride(0), block_table.shape[1], free_pages.data_ptr(), free_pages.numel(),
-        None if free_head is None else free_head.data_ptr(), table._struct,
+        None if free_head is None else free_head.data_ptr(), table._ref,
         _flag_ptr(device_flags, dev), _stream_of(stream, dev))
     if st:
         check(st, "nvfp4kv_build_page_table")
@@ -154,6 +154,8 @@ class RopePlan:
         self.interleaved = int(bool(interleaved))
         self.attention_factor = float(attention_factor)
         self.freq = freq  # int64 tensor, the bits of the uint64 table
+        self.device, self.table = freq.get_device(), freq.data_ptr()
+        self.layout = (self.head_dim, self.rotary_dim, self.interleaved)
 
 
 def nvfp4kv_rope_plan(head_dim: int, rotary_dim: Optional[int] = None, base: float = 10000.0,
@@ -199,34 +201,35 @@ def nvfp4kv_rope(plan: RopePlan, q: Optional[torch.Tensor], k: Optional[torch.Te
     code = _DTYPE.get(dtype)
     if code is None:
         raise ValueError("q and k must be torch.bfloat16 or torch.float16")
-    _ints(torch.int32, positions=positions)
+    if positions.dtype != torch.int32 or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous torch.int32")
     n, dev = positions.numel(), torch.cuda.current_device()
-    _wrong_device(dev, positions, plan.freq)
-    qa, q_out = _rope_rows(plan, "q", q, q_out, n, dtype, dev, stream)
-    ka, k_out = _rope_rows(plan, "k", k, k_out, n, dtype, dev, stream)
-    st = _entry("nvfp4kv_rope")(
-        *qa, *ka, n, positions.data_ptr(), plan.head_dim, plan.rotary_dim, plan.interleaved,
-        code, plan.freq.data_ptr(), plan.attention_factor, _stream_of(stream, dev))
+    if not positions.get_device() == plan.device == dev:
+        _check_device(dev, positions, plan.freq)
+    qa, q_out = _rope_rows(plan.head_dim, "q", q, q_out, n, dtype, dev, stream)
+    ka, k_out = _rope_rows(plan.head_dim, "k", k, k_out, n, dtype, dev, stream)
+    st = _entry("nvfp4kv_rope")(*qa, *ka, n, positions.data_ptr(), *plan.layout, code, plan.table,
+                                plan.attention_factor, _stream_of(stream, dev))
     if st:
         check(st, "nvfp4kv_rope")
     return q_out, k_out
 
 
-def _rope_rows(plan, name, x, out, n, dtype, dev, stream):
+def _rope_rows(dim, name, x, out, n, dtype, dev, stream):
     """The seven arguments of one of q and k, and its output."""
     if x is None:
         return (None, 0, 0, None, 0, 0, 0), None
-    rows, heads = _rows(name, x, plan.head_dim, n, dtype)
+    rows, heads = _rows(name, x, dim, n, dtype)
     if out is None:
-        out = _empty((n, heads, plan.head_dim), dtype, x.device, stream)
-        to = (heads * plan.head_dim, plan.head_dim)
+        out = _empty((n, heads, dim), dtype, x.device, stream)
+        to0, to1 = heads * dim, dim
     else:
-        to, out_heads = _rows(name + "_out", out, plan.head_dim, n, dtype)
+        (to0, to1, _), out_heads = _rows(name + "_out", out, dim, n, dtype)
         if out_heads != heads:
             raise ValueError("%s_out has another number of heads" % name)
-    if x.get_device() != dev or out.get_device() != dev:
-        _wrong_device(dev, x, out)
-    return (x.data_ptr(), rows[0], rows[1], out.data_ptr(), to[0], to[1], heads), out
+    if not x.get_device() == out.get_device() == dev:
+        _check_device(dev, x, out)
+    return (x.data_ptr(), rows[0], rows[1], out.data_ptr(), to0, to1, heads), out
 
 
 # ---- the E4M3 cache ----------------------------------------------------------------
@@ -260,7 +263,7 @@ class E4m3Cache:
         self.head_dim_qk, self.head_dim_vo = k_data.shape[3], v_data.shape[3]
         s.num_pages, s.page_size, s.num_kv_heads = pages, page_size, heads
         s.head_dim_qk, s.head_dim_vo = self.head_dim_qk, self.head_dim_vo
-        self._struct = s
+        self._struct, self._ref = s, C.byref(s)
 
     @classmethod
     def allocate(cls, num_pages, num_kv_heads, head_dim_qk, head_dim_vo, page_size=16,
@@ -299,9 +302,9 @@ def nvfp4kv_e4m3_append(cache: E4m3Cache, k: torch.Tensor, v: torch.Tensor, qo_i
     if qo_indptr.numel() != batch + 1 or kv_indptr.numel() != batch + 1:
         raise ValueError("indptrs must have one entry more than last_page_len")
     dev = torch.cuda.current_device()
-    _wrong_device(dev, cache.k_data, k, v, qo_indptr, kv_indptr, kv_indices, last_page_len)
+    _check_device(dev, cache.k_data, k, v, qo_indptr, kv_indptr, kv_indices, last_page_len)
     st = _entry("nvfp4kv_e4m3_append")(
-        cache._struct, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], code, rows,
+        cache._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], code, rows,
         qo_indptr.data_ptr(), kv_indptr.data_ptr(), kv_indices.data_ptr(),
         last_page_len.data_ptr(), batch, _flag_ptr(device_flags, dev), _stream_of(stream, dev))
     if st:
@@ -320,6 +323,7 @@ class _Run:
         self.dtype = torch.float16 if i.out_dtype == 1 else torch.bfloat16
         self.workspace, self.nbytes = plan.workspace.data_ptr(), plan.workspace.numel()
         self.device = plan.workspace.get_device()
+        self.info = C.byref(i)
         self.out_shape, self.lse_shape = (self.rows, self.heads, self.dv), (self.rows, self.heads)
 
 
@@ -342,7 +346,7 @@ def nvfp4kv_e4m3_decode_run(plan: Plan, q: torch.Tensor, cache: E4m3Cache, kv_in
         raise ValueError("kv_indices has fewer entries than the plan's pages")
     dev = torch.cuda.current_device()
     if not (q.get_device() == kv_indices.get_device() == cache.device == r.device == dev):
-        _wrong_device(dev, q, kv_indices, cache.k_data, plan.workspace)
+        _check_device(dev, q, kv_indices, cache.k_data, plan.workspace)
     if out is None:
         out = _empty(r.out_shape, r.dtype, q.device, stream)
     elif tuple(out.shape) != r.out_shape or out.dtype != r.dtype or not out.is_contiguous():
@@ -353,9 +357,9 @@ def nvfp4kv_e4m3_decode_run(plan: Plan, q: torch.Tensor, cache: E4m3Cache, kv_in
             not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [rows, Hq]")
     if out.get_device() != dev or lse.get_device() != dev:
-        _wrong_device(dev, out, lse)
+        _check_device(dev, out, lse)
     st = _entry("nvfp4kv_e4m3_decode_run")(
-        plan.info, q.data_ptr(), qs[0], qs[1], code, cache._struct, kv_indices.data_ptr(),
+        r.info, q.data_ptr(), qs[0], qs[1], code, cache._ref, kv_indices.data_ptr(),
         sm_scale or 0.0, r.workspace, r.nbytes, out.data_ptr(), lse.data_ptr(),
         _stream_of(stream, dev))
     if st:
