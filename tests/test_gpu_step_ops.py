@@ -461,6 +461,24 @@ def test_attention_rows(hq, hkv, new, causal, page):
     attend_case((37, 65, 90), new, hq, hkv, 128, 128, causal=causal, page=page, seed=hq + sum(new))
 
 
+@pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (256, 128), (256, 256), (512, 256)])
+@pytest.mark.parametrize("page,layout,out", [(16, "HND", "bf16"), (16, "NHD", "f16"),
+                                             (1, "HND", "bf16")])
+@pytest.mark.parametrize("new", [(5, 4, 0), (9, 16, 1), (13, 16, 40)])
+def test_attention_dims_many_rows(dk, dv, page, layout, out, new):
+    """Up to 10, 32 and 80 rows per kv head: every kernel of every head dim."""
+    attend_case((37, 300, 40), new, 4, 2, dk, dv, causal=True, page=page, layout=layout, out=out,
+                seed=dk + sum(new))
+
+
+@pytest.mark.parametrize("hq,hkv", [(16, 1), (48, 2), (32, 1)])
+def test_attention_wide_groups_split(hq, hkv):
+    """16, 24 and 32 heads to a kv head, one row each, split requests."""
+    _, plan, _ = attend_case((700, 33, 5), (1, 1, 1), hq, hkv, 128, 128, force_chunk_tokens=128,
+                             seed=hq)
+    assert plan.info.split == 1
+
+
 @pytest.mark.parametrize("chunk", [16, 64, 176])
 @pytest.mark.parametrize("new,causal", [((1, 1, 1, 1), False), ((5, 1, 0, 30), True)])
 def test_attention_split(chunk, new, causal):
