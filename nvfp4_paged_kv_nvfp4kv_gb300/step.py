@@ -25,15 +25,9 @@ __all__ = ["StepTable", "nvfp4kv_build_page_table", "RopePlan", "nvfp4kv_rope_pl
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1}
 
 
-_fn = {}
-
-
 def _entry(name):
-    """The library's function, looked up once."""
-    fn = _fn.get(name)
-    if fn is None:
-        fn = _fn[name] = getattr(_lib.load(), name)
-    return fn
+    """The library's function (an attribute of the loaded library)."""
+    return getattr(_lib._lib or _lib.load(), name)
 
 
 def _check_device(dev, *tensors):
