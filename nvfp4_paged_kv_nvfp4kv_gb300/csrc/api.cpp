@@ -137,13 +137,12 @@ CacheView view_of(const nvfp4kv_paged_cache* c) {
   return v;
 }
 
-bool lookup_kernel(int kind, int dk, int dv, int page_size, int out_dtype, int rows,
-                   AttendConfig* cfg) {
+bool lookup_kernel(int kind, int dk, int dv, int page_size, int rows, AttendConfig* cfg) {
   if (kind == kKernelTensorCore) return attend_config_tc(dk, dv, rows, cfg);
   if (kind == kKernelCudaCore) return attend_config_simt(dk, dv, rows, cfg);
   if (kind == kKernelTcgen05) return attend_config_tcgen05(dk, dv, rows, cfg);
   if (kind == kKernelFp4QP) return attend_config_tc_fp4qp(dk, dv, rows, 2, cfg);
-  if (kind == kKernelE4m3) return attend_config_e4m3(dk, dv, page_size, rows, out_dtype == 1, cfg);
+  if (kind == kKernelE4m3) return attend_config_e4m3(dk, dv, page_size, rows, cfg);
   return false;
 }
 
@@ -356,7 +355,7 @@ int nvfp4kv_decode_plan(const int32_t* qo_indptr_h, const int32_t* kv_indptr_h,
                                                                        : kKernelTensorCore;
   const int want_rows = kind == kKernelTcgen05 || kind == kKernelE4m3 ? std::max(max_rows, 1)
                                                                       : (max_rows <= 8 ? 8 : 16);
-  if (!lookup_kernel(kind, head_dim_qk, head_dim_vo, page_size, opts.out_dtype, want_rows, &cfg))
+  if (!lookup_kernel(kind, head_dim_qk, head_dim_vo, page_size, want_rows, &cfg))
     return fail(NVFP4KV_ERR_UNSUPPORTED, "no %s kernel for head dims (%d, %d)%s",
                 kind == kKernelTensorCore ? "tensor-core"
                 : kind == kKernelTcgen05  ? "tcgen05"
@@ -724,7 +723,7 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
                    attend_config_dec(info->head_dim_qk, info->head_dim_vo, 8,
                                      info->num_units <= info->num_sms ? 1 : 4, &cfg);
   if (!dec && !lookup_kernel(info->kernel, info->head_dim_qk, info->head_dim_vo,
-                             info->page_size, info->out_dtype, info->rows_per_block, &cfg))
+                             info->page_size, info->rows_per_block, &cfg))
     return fail(NVFP4KV_ERR_UNSUPPORTED, "planned kernel not available");
   cudaError_t e = prepare_kernel(cfg);
   if (e != cudaSuccess) return cuda_fail(e, "kernel attributes");
@@ -790,7 +789,7 @@ int attend_e4m3(const nvfp4kv_plan_info* info, const void* q, int64_t q_stride_t
     return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "out must be 8-byte and lse 4-byte aligned");
   AttendConfig cfg{};
   if (!lookup_kernel(kKernelE4m3, info->head_dim_qk, info->head_dim_vo, info->page_size,
-                     info->out_dtype, info->rows_per_block, &cfg))
+                     info->rows_per_block, &cfg))
     return fail(NVFP4KV_ERR_UNSUPPORTED, "planned kernel not available");
   cudaError_t e = prepare_kernel(cfg);
   if (e != cudaSuccess) return cuda_fail(e, "kernel attributes");

@@ -10,11 +10,13 @@
 //    four significant bits, so two give a bf16 value's eight and three an f16
 //    value's eleven, down to 2^-18 of the row's largest |q|.
 //    S^T = K (q0 + q1 + ..)^T accumulates in one tile of tensor memory.
-//  * Weights p' = 2^x (at most 2^8): p' = w0 + w1 / 32 (+ w2 / 1024).  Each
-//    piece has its own columns of O^T = V^T (w0 | w1 | ..)^T, added in the
-//    epilogue: eight bits of a weight with two pieces (bf16 outputs), twelve
-//    with three (f16 outputs).  p' = 2^(x - m) lies at 2^5 where the tile
-//    that set m had its largest, so a weight 2^-19 of that is still kept.
+//  * Weights p' = 2^x (at most 2^8): p' = w0 + w1 / 32 + w2 / 1024.  Each piece
+//    has its own columns of O^T = V^T (w0 | w1 | w2)^T, added in the epilogue:
+//    twelve bits of a weight, and a weight 2^-20 of the largest is still kept.
+//    (Two pieces hold eight bits; to keep weights that small they allow only
+//    three bits between a tile's maximum and the raise, and a raise of some of
+//    the rows in most tiles then costs more than the third piece: 223 us
+//    against XXX on 32 requests of 2000-16000 tokens x 64 rows.)
 //  * Row sums come from the unsplit float32 weights, a register per query row
 //    and thread, added up over the threads at the end.
 //
@@ -52,8 +54,8 @@ using namespace tc5;
 constexpr int kTileTok = 128;
 constexpr int kLoaders = 2;  // warps, 64 rows of a tile each
 constexpr int kAllSoftmax = 5;  // named barriers 1 .. 4: the column groups
+constexpr int kPieces = 3;      // of a weight
 constexpr float kRaise = 8.f;  // log2 of the largest weight before m is raised
-constexpr float kPeak = 5.f;   // log2 of the weight of a new maximum
 constexpr float kMinScale = 0x1p-64f, kMaxScale = 0x1p64f;
 
 // D[tmem] (+)= A[smem] . B[smem], E4M3 operands (the instruction descriptor of
@@ -132,7 +134,7 @@ __device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
   return r;
 }
 
-template <int DK, int DV, int N, int NP>
+template <int DK, int DV, int N>
 struct Ext {
   static constexpr int NH = 16;                    // query rows per softmax thread
   static constexpr int CG = N / NH;                // column groups of four warps
@@ -141,14 +143,12 @@ struct Ext {
   static constexpr int NQ = 3;                     // query pieces (2 used for bf16)
   static constexpr int KB = kTileTok * DK, VB = kTileTok * DV;
   static constexpr int QB = N * DK;                // one query piece
-  // P^T rows: NP * N weight pieces of a token, in atoms of PA bytes
-  static constexpr int PN = NP * N;
-  static constexpr int PA = PN <= 64 ? 64 : 128;
-  static constexpr int PATOMS = (PN + PA - 1) / PA;
-  static constexpr int PSTRIDE = kTileTok * PA;    // bytes of one atom column
-  static constexpr int PB = PATOMS * PSTRIDE;
-  static constexpr uint32_t PSWZ = PA == 64 ? kSwz64 : kSwz128;
-  static constexpr int PSWB = PA == 64 ? 2 : 3;
+  // P^T: a token's row of kPieces * N weight pieces, as rows of 128 bytes (three
+  // pieces of 32 rows; two of 64) and, at N = 64, rows of 64 bytes (the third)
+  static constexpr int PN = kPieces * N, PN0 = PN <= 128 ? PN : 128, PN1 = PN - PN0;
+  static constexpr int P1_OFF = kTileTok * 128;
+  static constexpr int PB = P1_OFF + kTileTok * PN1;
+  static_assert(PN1 == 0 || PN1 == 64, "the second rows");
   static constexpr int SCB = kTileTok * 12;        // K scale, log2 and inverse of the V scale
   static constexpr int MISC = 8192;
   static constexpr int FIXED = 2 * PB + NQ * QB + MISC + 1024;
@@ -165,19 +165,19 @@ struct Ext {
   static constexpr int COLS = OCOL + (DV / 128) * PN;
   static constexpr int TCOLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static constexpr uint32_t IDESC_QK = idesc_f16(128, N, 0, 0);
-  static constexpr uint32_t IDESC_PV = idesc_f16(128, PN, 1, 1);
+  static constexpr uint32_t IDESC_PV = idesc_f16(128, PN0, 1, 1);
   static_assert(KS >= 2, "a tile to work on and one on its way");
   static_assert(DK % 128 == 0 && DV % 128 == 0, "operand rows of 128 bytes");
   static_assert(OFF_P % 1024 == 0 && OFF_Q % 1024 == 0 && OFF_MISC % 16 == 0, "align");
-  static_assert(SMEM <= 232448 && COLS <= 512 && PN % 16 == 0 && PN <= 256, "resources");
+  static_assert(SMEM <= 232448 && COLS <= 512 && PN0 % 16 == 0, "resources");
   static_assert(20 * 8 + 16 + (7 * N + 2 * N + 4 + 4 * N) * 4 <= MISC, "misc");
 };
 
 // P1: 1-token pages
-template <int DK, int DV, int N, int NP, bool P1>
-__global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
+template <int DK, int DV, int N, bool P1>
+__global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     attend_e4m3_ext_kernel(const AttendParams p) {
-  using T = Ext<DK, DV, N, NP>;
+  using T = Ext<DK, DV, N>;
   constexpr int NH = T::NH, KS = T::KS, SW = T::SW, ST = 32 * SW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -393,19 +393,25 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
     // ======== O^T issue (one thread) ==========================================
     if (lane == 0) {
       const uint64_t vd0 = smem_desc(smem_addr(sV), kTileTok * 128, 1024, kSwz128);
-      const uint64_t pd0 = smem_desc(smem_addr(sP), T::PSTRIDE, 8 * T::PA, T::PSWZ);
+      const uint64_t pd0 = smem_desc(smem_addr(sP), T::PB, 1024, kSwz128);
+      const uint64_t pd1 = smem_desc(smem_addr(sP) + T::P1_OFF, T::PB, 512, kSwz64);
       for (int i = 0; i < ntiles; ++i) {
         if (!wait_bar(&p_full[i & 1], (i >> 1) & 1, s_abort, p.flags)) break;
         tc_fence_after();
         const uint64_t vd = vd0 + (((i % KS) * T::VB) >> 4);
-        const uint64_t pd = pd0 + (((i & 1) * T::PB) >> 4);
+        const uint64_t buf = ((i & 1) * T::PB) >> 4;
 #pragma unroll
         for (int b = 0; b < DV / 128; ++b)
 #pragma unroll
-          for (int k = 0; k < kTileTok / 32; ++k)
-            umma8_ss(tmem + T::OCOL + b * T::PN,
-                     vd + ((b * (kTileTok * 128) + k * 32 * 128) >> 4),
-                     pd + ((k * 32 * T::PA) >> 4), T::IDESC_PV, (i > 0 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < kTileTok / 32; ++k) {
+            const uint64_t vk = vd + ((b * (kTileTok * 128) + k * 32 * 128) >> 4);
+            const uint32_t acc = (i > 0 || k > 0) ? 1u : 0u;
+            umma8_ss(tmem + T::OCOL + b * T::PN, vk, pd0 + buf + ((k * 32 * 128) >> 4),
+                     T::IDESC_PV, acc);
+            if constexpr (T::PN1 > 0)
+              umma8_ss(tmem + T::OCOL + b * T::PN + T::PN0, vk, pd1 + buf + ((k * 32 * 64) >> 4),
+                       idesc_f16(128, T::PN1, 1, 1), acc);
+          }
         umma_commit(&pv_done[i & 1]);
         umma_commit(&kv_empty[i % KS]);
       }
@@ -495,59 +501,65 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
     // every later wait returning at once, so no thread leaves a barrier
     // sequence the others still follow.
     bool unset = active;  // some column of this group has no maximum yet
-    // where this thread's pieces go in a P^T buffer: byte o of its token's row
-    // lies in atom o / PA, 16-byte chunks xor-swizzled
-    uint32_t p_at[NP];
+    // where this thread's pieces go in a P^T buffer: its token's row, 16-byte
+    // chunks xor-swizzled
+    uint32_t p_at[kPieces];
 #pragma unroll
-    for (int q = 0; q < NP; ++q) {
-      const uint32_t o = q * N + c0;
-      p_at[q] = (o / T::PA) * T::PSTRIDE +
-                swz<T::PSWB>((uint32_t)(j >> 3) * (8 * T::PA) + (j & 7) * T::PA + o % T::PA);
-    }
+    for (int q = 0; q < kPieces; ++q)
+      p_at[q] = q * N < T::PN0 ? swz<3>((uint32_t)j * 128 + q * N + c0)
+                               : T::P1_OFF + swz<2>((uint32_t)j * 64 + q * N - T::PN0 + c0);
     uint64_t lsum[NH / 2];  // this token's share of the row sums, two rows each
 #pragma unroll
     for (int e = 0; e < NH / 2; ++e) lsum[e] = 0;
+    // x: log2-domain scores of tile i relative to the running maxima, with log2
+    // of the token's V scale, -inf where masked or past the unit's end; iv2: the
+    // inverse of that scale, twice
+    auto scores = [&](int i, float (&x)[NH], uint64_t& iv2) {
+      const int tile_tok0 = u.tok_begin + i * kTileTok, tok = tile_tok0 + j;
+      const float* sc = sSc + (i % KS) * (T::SCB / 4) + j;
+      const float ks = sc[0], lv = sc[kTileTok], iv = sc[2 * kTileTok];
+      const uint64_t ks2 = pack_f32x2(ks, ks), lv2 = pack_f32x2(lv, lv);
+      iv2 = pack_f32x2(iv, iv);
+      uint32_t sv[NH];
+      tmem_ld<NH>(tmem + lane_base + T::SCOL + N * (i % KS) + c0, sv);
+      tmem_wait_ld<NH>(sv);
+#pragma unroll
+      for (int e4 = 0; e4 < NH; e4 += 4) {
+        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(s_f + c0 + e4);
+        const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + c0 + e4);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint64_t s2 = pack_f32x2(__uint_as_float(sv[e4 + 2 * e]),
+                                         __uint_as_float(sv[e4 + 2 * e + 1]));
+          unpack_f32x2(fma_f32x2(s2, mul_f32x2(e ? f.y : f.x, ks2),
+                                 add_f32x2(e ? nm.y : nm.x, lv2)),
+                       x[e4 + 2 * e], x[e4 + 2 * e + 1]);
+        }
+      }
+      if (tile_tok0 + kTileTok - 1 > min_lim) {
+#pragma unroll
+        for (int e4 = 0; e4 < NH; e4 += 4) {
+          const int4 lm = *reinterpret_cast<const int4*>(s_lim + c0 + e4);
+          if (tok > lm.x) x[e4] = -INFINITY;
+          if (tok > lm.y) x[e4 + 1] = -INFINITY;
+          if (tok > lm.z) x[e4 + 2] = -INFINITY;
+          if (tok > lm.w) x[e4 + 3] = -INFINITY;
+        }
+      }
+      if (tile_tok0 + kTileTok > tok_end && tok >= tok_end) {
+#pragma unroll
+        for (int e = 0; e < NH; ++e) x[e] = -INFINITY;
+      }
+    };
     for (int i = 0; i < ntiles; ++i) {
       const int sb = i & 1;
       warp_wait(&s_full[i % KS], (i / KS) & 1);
       tc_fence_after();
-      const int tile_tok0 = u.tok_begin + i * kTileTok;
-      const int tok = tile_tok0 + j;
-      const bool mask_rows = tile_tok0 + kTileTok - 1 > min_lim;
       float x[NH];
       uint64_t iv2 = 0;
       bool trig = false;
       if (active) {
-        const float* sc = sSc + (i % KS) * (T::SCB / 4) + j;  // this token's scales
-        const float ks = sc[0], lv = sc[kTileTok], iv = sc[2 * kTileTok];
-        const uint64_t ks2 = pack_f32x2(ks, ks), lv2 = pack_f32x2(lv, lv);
-        iv2 = pack_f32x2(iv, iv);
-        uint32_t sv[NH];
-        tmem_ld<NH>(tmem + lane_base + T::SCOL + N * (i % KS) + c0, sv);
-        tmem_wait_ld<NH>(sv);
-#pragma unroll
-        for (int e4 = 0; e4 < NH; e4 += 4) {
-          const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(s_f + c0 + e4);
-          const ulonglong2 nm = *reinterpret_cast<const ulonglong2*>(s_nm + c0 + e4);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const uint64_t s2 = pack_f32x2(__uint_as_float(sv[e4 + 2 * e]),
-                                           __uint_as_float(sv[e4 + 2 * e + 1]));
-            unpack_f32x2(fma_f32x2(s2, mul_f32x2(e ? f.y : f.x, ks2),
-                                   add_f32x2(e ? nm.y : nm.x, lv2)),
-                         x[e4 + 2 * e], x[e4 + 2 * e + 1]);
-          }
-        }
-        if (mask_rows) {
-#pragma unroll
-          for (int e4 = 0; e4 < NH; e4 += 4) {
-            const int4 lm = *reinterpret_cast<const int4*>(s_lim + c0 + e4);
-            if (tok > lm.x) x[e4] = -INFINITY;
-            if (tok > lm.y) x[e4 + 1] = -INFINITY;
-            if (tok > lm.z) x[e4 + 2] = -INFINITY;
-            if (tok > lm.w) x[e4 + 3] = -INFINITY;
-          }
-        }
+        scores(i, x, iv2);
         if (unset) {
 #pragma unroll
           for (int e4 = 0; e4 < NH; e4 += 4) {
@@ -560,11 +572,6 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
 #pragma unroll
           for (int e = 2; e < NH; e += 2) mx = fmax3(mx, x[e], x[e + 1]);
           trig = mx > kRaise;
-        }
-        if (tile_tok0 + kTileTok > tok_end && tok >= tok_end) {  // past the unit's end
-          trig = false;
-#pragma unroll
-          for (int e = 0; e < NH; ++e) x[e] = -INFINITY;
         }
       }
       if (named_or(gbar, 128, trig)) {
@@ -586,10 +593,9 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
           const int r = c0 + gtid;
           const float tm = funkey(s_max[r]);  // tile maximum, relative to the old m
           const float m_old = s_m[r];
-          float corr = 1.f, delta = 0.f;
-          if (tm != -INFINITY && (m_old == -INFINITY || tm > kPeak)) {
-            delta = tm - kPeak;
-            const float m_new = (m_old == -INFINITY ? 0.f : m_old) + delta;
+          float corr = 1.f;
+          if (tm != -INFINITY && (m_old == -INFINITY || tm > 0.f)) {
+            const float m_new = (m_old == -INFINITY ? 0.f : m_old) + tm;
             if (m_old != -INFINITY) corr = ex2(m_old - m_new);
             s_m[r] = m_new;
             s_nm[r] = -m_new;
@@ -597,19 +603,16 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
             moved = corr != 1.f;
           }
           s_corr[r] = corr;
-          s_max[r] = __float_as_int(delta);
         }
         const bool rescale = named_or(gbar, 128, moved) && i > 0;
         unset = named_or(gbar, 128, gtid < NH && c0 + gtid < nvalid && s_m[c0 + gtid] == -INFINITY);
-#pragma unroll
-        for (int e = 0; e < NH; ++e) x[e] -= __int_as_float(s_max[c0 + e]);
         if (rescale && active) {  // O^T columns and row sums *= corr, once PV(i-1) is done
           warp_wait(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
           tc_fence_after();
 #pragma unroll
           for (int e = 0; e < NH / 2; ++e)
             lsum[e] = mul_f32x2(lsum[e], *reinterpret_cast<const uint64_t*>(s_corr + c0 + 2 * e));
-          for (int blk = 0; blk < (DV / 128) * NP; ++blk) {
+          for (int blk = 0; blk < (DV / 128) * kPieces; ++blk) {
             uint32_t ov[NH];
             const uint32_t oa = tmem + lane_base + T::OCOL + blk * N + c0;
             tmem_ld<NH>(oa, ov);
@@ -621,11 +624,12 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
           }
           tmem_wait_st();
         }
+        if (active) scores(i, x, iv2);  // (again: nothing of the tile is kept over a raise)
       }
-      // ---- weights: the P^T row of this token, NP pieces ----------------------
+      // ---- weights: the P^T row of this token, in pieces ----------------------
       if (i >= 2) warp_wait(&pv_done[sb], ((i - 2) >> 1) & 1);  // P buffer sb is free
       if (active) {
-        uint32_t h[NP][NH / 4];
+        uint32_t h[kPieces][NH / 4];
 #pragma unroll
         for (int e = 0; e < NH / 4; ++e) {
           uint32_t rest[2];
@@ -637,9 +641,9 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
             rest[k] = f32x2_to_f16x2(a, b);
           }
 #pragma unroll
-          for (int q = 0; q < NP; ++q) {
+          for (int q = 0; q < kPieces; ++q) {
             h[q][e] = e4m3x4_of_f16(rest[0], rest[1]);
-            if (q + 1 < NP) {  // (rest - piece) * 32: exact in f16
+            if (q + 1 < kPieces) {  // (rest - piece) * 32: exact in f16
               uint32_t back[2];
               e4m3x4_to_f16(h[q][e], back[0], back[1]);
               rest[0] = hmul2(hsub2(rest[0], back[0]), 0x50005000u);
@@ -648,7 +652,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
           }
         }
 #pragma unroll
-        for (int q = 0; q < NP; ++q) {
+        for (int q = 0; q < kPieces; ++q) {
           uint8_t* at = sP + sb * T::PB + p_at[q];
           *reinterpret_cast<uint4*>(at) = make_uint4(h[q][0], h[q][1], h[q][2], h[q][3]);
         }
@@ -710,13 +714,13 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
         for (int b = 0; b < DV / 128; ++b) {
           float o[NH];
 #pragma unroll
-          for (int q = NP - 1; q >= 0; --q) {  // o = o0 + (o1 + o2 / 32) / 32
+          for (int q = kPieces - 1; q >= 0; --q) {  // o = o0 + (o1 + o2 / 32) / 32
             uint32_t ov[NH];
             tmem_ld<NH>(tmem + lane_base + T::OCOL + b * T::PN + q * N + c0, ov);
             tmem_wait_ld<NH>(ov);
 #pragma unroll
             for (int e = 0; e < NH; ++e)
-              o[e] = q == NP - 1 ? __uint_as_float(ov[e])
+              o[e] = q == kPieces - 1 ? __uint_as_float(ov[e])
                                  : fmaf(o[e], 0.03125f, __uint_as_float(ov[e]));
           }
 #pragma unroll
@@ -747,39 +751,30 @@ __global__ void __launch_bounds__(Ext<DK, DV, N, NP>::THREADS, 1)
   }
 }
 
-template <int DK, int DV, int N, int NP>
+template <int DK, int DV, int N>
 bool make_ext(bool p1, AttendConfig* cfg) {
   cfg->kind = kKernelE4m3;
   cfg->dk = DK;
   cfg->dv = DV;
   cfg->rows = N;
-  cfg->warps = Ext<DK, DV, N, NP>::THREADS / 32;
+  cfg->warps = Ext<DK, DV, N>::THREADS / 32;
   cfg->units_per_cta = 1;
-  cfg->smem_bytes = Ext<DK, DV, N, NP>::SMEM;
-  cfg->func = p1 ? reinterpret_cast<const void*>(attend_e4m3_ext_kernel<DK, DV, N, NP, true>)
-                 : reinterpret_cast<const void*>(attend_e4m3_ext_kernel<DK, DV, N, NP, false>);
+  cfg->smem_bytes = Ext<DK, DV, N>::SMEM;
+  cfg->func = p1 ? reinterpret_cast<const void*>(attend_e4m3_ext_kernel<DK, DV, N, true>)
+                 : reinterpret_cast<const void*>(attend_e4m3_ext_kernel<DK, DV, N, false>);
   return true;
 }
 
 }  // namespace
 
-// The kernel for (dk, dv) and more than 16 query rows per kv head; f16 outputs
-// take three weight pieces.
-bool attend_config_e4m3_ext(int dk, int dv, int page_size, int rows, bool out_f16,
-                            AttendConfig* cfg) {
+// The kernel for (dk, dv) and more than 16 query rows per kv head.
+bool attend_config_e4m3_ext(int dk, int dv, int page_size, int rows, AttendConfig* cfg) {
   const bool p1 = page_size == 1;
-#define NVFP4KV_EXT(DK_, DV_, N_) \
-  return out_f16 ? make_ext<DK_, DV_, N_, 3>(p1, cfg) : make_ext<DK_, DV_, N_, 2>(p1, cfg)
-  if (dk == 128 && dv == 128) {
-    if (rows <= 32) NVFP4KV_EXT(128, 128, 32);
-    NVFP4KV_EXT(128, 128, 64);
-  }
-  // 256 dims: 64 rows would leave two tiles in flight (and no room for a third
-  // weight piece): 48 against 63 us on 8 requests of 512-4096 tokens x 64 rows,
-  // but 302 against 229 us on 16 of 2000-16000
-  if (dk == 256 && dv == 128) NVFP4KV_EXT(256, 128, 32);
-  if (dk == 256 && dv == 256) NVFP4KV_EXT(256, 256, 32);
-#undef NVFP4KV_EXT
+  if (dk == 128 && dv == 128)
+    return rows <= 32 ? make_ext<128, 128, 32>(p1, cfg) : make_ext<128, 128, 64>(p1, cfg);
+  // 256 dims: 64 rows would leave at most two tiles in flight
+  if (dk == 256 && dv == 128) return make_ext<256, 128, 32>(p1, cfg);
+  if (dk == 256 && dv == 256) return make_ext<256, 256, 32>(p1, cfg);
   return false;
 }
 

@@ -192,12 +192,10 @@ cudaError_t launch_dequantize(const DequantParams& p, cudaStream_t stream);
 cudaError_t launch_page_table(const PageTableParams& p, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_e4m3_append(const E4m3AppendParams& p, cudaStream_t stream);
-// The E4M3-cache attention kernel for (dk, dv), a page size of 16 or 1, up to
-// `rows` query rows per kv head and bf16 or f16 outputs; false when not built.
-bool attend_config_e4m3(int dk, int dv, int page_size, int rows, bool out_f16,
-                        AttendConfig* cfg);
-bool attend_config_e4m3_ext(int dk, int dv, int page_size, int rows, bool out_f16,
-                            AttendConfig* cfg);
+// The E4M3-cache attention kernel for (dk, dv), a page size of 16 or 1 and up to
+// `rows` query rows per kv head; false when not built.
+bool attend_config_e4m3(int dk, int dv, int page_size, int rows, AttendConfig* cfg);
+bool attend_config_e4m3_ext(int dk, int dv, int page_size, int rows, AttendConfig* cfg);
 // Record a message for nvfp4kv_last_error_detail() and return `status`.
 int set_error_detail(int status, const char* message);
 cudaError_t launch_merge(const float* o_partial, const float* lse_partial,

@@ -393,10 +393,9 @@ def attend_case(kv, new, hq, hkv, dk, dv, causal=False, page=16, layout="HND", d
     of the weights.  Query pieces, with the row's largest |q| in [128, 256), are
     exact but for elements whose last bit is below the smallest code 2^-9: off
     by 2^-10, 2^-17 of the largest |q|, so a score by 2^-17 * sm_scale max|q|
-    sum|k| more.  Weights, after f16, are off by (2^-4)^pieces of themselves and
-    by half the last piece's smallest code, 2^-10 / 32^(pieces - 1), where the
-    row's largest is 2^5 or more: 2^-20 of that with two pieces (bf16 outputs),
-    2^-25 (and f16's own floor) with three."""
+    sum|k| more.  The three pieces of a weight, after f16, are off by 2^-12 of it
+    and by half the last piece's smallest code, 2^-10 / 1024, where the row's
+    largest is 1 or more: 2^-20 of that (f16's own floor is below)."""
     c = CacheCase(kv, page, hkv, dk, dv, layout, seed=seed, spread=spread)
     if stale:  # slots past every length hold NaN codes
         for b, n in enumerate(kv):
@@ -430,10 +429,9 @@ def attend_case(kv, new, hq, hkv, dk, dv, causal=False, page=16, layout="HND", d
         delta = (dk * 2.0 ** -23 * reach + 2.0 ** -21)
         weight, least = 2.0 ** -11, 2.0 ** -25
         if plan.info.rows_per_block > 8:
-            pieces = 3 if out == "f16" else 2
             delta = delta + 2.0 ** -17 * scale * (np.abs(R.to_np(q[rows])).max(-1)
                                                   * np.abs(k).sum(-1).max())
-            weight, least = weight + 2.0 ** (-4 * pieces), 2.0 ** (-15 - 5 * (pieces - 1)) * 1.1
+            weight, least = weight + 2.0 ** -12, 2.0 ** -20 + 2.0 ** -25
         tol = (eps * np.abs(ref) + (mean * (weight + 2.0 ** -19 + 2 * delta[..., None])
                                     + least * floor) * (1 + eps)
                + float(torch.finfo(DT[out]).smallest_normal) * eps)
