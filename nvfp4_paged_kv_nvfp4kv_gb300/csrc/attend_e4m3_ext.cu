@@ -24,11 +24,11 @@
 // query rows (the G heads of the group times the query positions); tiles of
 // 128 tokens; M = 128 tokens (S^T) or 128 value dims (O^T) fill the product
 // for any N.  19 warps at N = 64:
-//  * loaders (two warps): cp.async of the tile's K and V rows straight into
+//  * loaders (a warp for K, one for V): cp.async of a tile's rows straight into
 //    the 128-byte-swizzled operand layout (K: K-major, V: MN-major, both rows
 //    of 128 bytes), any byte strides and both page sizes;
-//  * issue (two threads): S^T = K Q^T into the stage's tile of tensor memory,
-//    and O^T += V^T P^T, each once its inputs are ready;
+//  * issue (two warps, one thread each): S^T = K Q^T into a ring of tiles in
+//    tensor memory, and O^T += V^T P^T, each once its inputs are ready;
 //  * softmax (four warps for each 16 query rows; thread = token of S^T): the
 //    token's K scale joins the row's factor, log2 of its V scale the exponent.
 //    The work of a tile is short chains, so many warps with few rows each beat
@@ -51,8 +51,13 @@ namespace {
 using namespace dev;
 using namespace tc5;
 
+// Test build only: the K loader of CTA (0, 0) withholds its arrival for the
+// first tile, so the S^T issuer's wait runs out and the CTA winds down.
+#ifndef NVFP4KV_E4M3_TEST_SKIP_ARRIVE
+#define NVFP4KV_E4M3_TEST_SKIP_ARRIVE 0
+#endif
 constexpr int kTileTok = 128;
-constexpr int kLoaders = 2;  // warps, 64 rows of a tile each
+constexpr int kLoaders = 2;  // warps: K, V
 constexpr int kAllSoftmax = 5;  // named barriers 1 .. 4: the column groups
 constexpr int kPieces = 3;      // of a weight
 constexpr float kRaise = 8.f;  // log2 of the largest weight before m is raised
@@ -150,27 +155,33 @@ struct Ext {
   static constexpr int PB = P1_OFF + kTileTok * PN1;
   static_assert(PN1 == 0 || PN1 == 64, "the second rows");
   static constexpr int SCB = kTileTok * 12;        // K scale, log2 and inverse of the V scale
-  static constexpr int MISC = 8192;
-  static constexpr int FIXED = 2 * PB + NQ * QB + MISC + 1024;
-  static constexpr int FIT = (232448 - FIXED) / (KB + VB + SCB);
-  static constexpr int KS = FIT < 4 ? FIT : 4;     // tiles in flight
+  static constexpr int MISC = 4608;
+  static constexpr int FIXED = 2 * PB + NQ * QB + 8 * SCB + MISC + 1024;
+  // Rings: a K tile is done with after its S^T, a V tile after its P^T V, about
+  // three tiles later, so V gets the more stages; S^T tiles in tensor memory
+  // and, behind both, the tokens' scales (read from a K tile's copy until the
+  // softmax has passed it: KR + SB tiles at most).
+  static constexpr int FIT = (232448 - FIXED) / 16384;  // 16 KB blocks that fit
+  static constexpr int KR = DK == 128 ? 3 : DV == 128 ? 3 : 2;
+  static constexpr int VR = DK == 128 ? 5 : DV == 128 ? 3 : 2;
+  static constexpr int SB = 4, SR = 8;
+  static_assert(KR * (DK / 128) + VR * (DV / 128) <= FIT && KR + SB <= SR, "rings");
   static constexpr int OFF_K = 0;
-  static constexpr int OFF_V = OFF_K + KS * KB;
-  static constexpr int OFF_P = OFF_V + KS * VB;
+  static constexpr int OFF_V = OFF_K + KR * KB;
+  static constexpr int OFF_P = OFF_V + VR * VB;
   static constexpr int OFF_Q = OFF_P + 2 * PB;
   static constexpr int OFF_SC = OFF_Q + NQ * QB;
-  static constexpr int OFF_MISC = OFF_SC + KS * SCB;
+  static constexpr int OFF_MISC = OFF_SC + SR * SCB;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;  // + alignment slack
-  static constexpr int SCOL = 0, OCOL = KS * N;    // S^T, one per stage; O^T blocks of 128 dims
+  static constexpr int SCOL = 0, OCOL = SB * N;    // S^T ring, O^T blocks of 128 value dims
   static constexpr int COLS = OCOL + (DV / 128) * PN;
   static constexpr int TCOLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static constexpr uint32_t IDESC_QK = idesc_f16(128, N, 0, 0);
   static constexpr uint32_t IDESC_PV = idesc_f16(128, PN0, 1, 1);
-  static_assert(KS >= 2, "a tile to work on and one on its way");
   static_assert(DK % 128 == 0 && DV % 128 == 0, "operand rows of 128 bytes");
   static_assert(OFF_P % 1024 == 0 && OFF_Q % 1024 == 0 && OFF_MISC % 16 == 0, "align");
   static_assert(SMEM <= 232448 && COLS <= 512 && PN0 % 16 == 0, "resources");
-  static_assert(20 * 8 + 16 + (7 * N + 2 * N + 4 + 4 * N) * 4 <= MISC, "misc");
+  static_assert(36 * 8 + 16 + (7 * N + 2 * N + 4 + 4 * N) * 4 <= MISC, "misc");
 };
 
 // P1: 1-token pages
@@ -178,7 +189,8 @@ template <int DK, int DV, int N, bool P1>
 __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     attend_e4m3_ext_kernel(const AttendParams p) {
   using T = Ext<DK, DV, N>;
-  constexpr int NH = T::NH, KS = T::KS, SW = T::SW, ST = 32 * SW;
+  constexpr int NH = T::NH, KR = T::KR, VR = T::VR, SB = T::SB, SR = T::SR;
+  constexpr int SW = T::SW, ST = 32 * SW;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -186,16 +198,19 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
   uint8_t* sV = smem + T::OFF_V;
   uint8_t* sP = smem + T::OFF_P;
   uint8_t* sQ = smem + T::OFF_Q;
-  float* sSc = reinterpret_cast<float*>(smem + T::OFF_SC);  // [KS][3][128]
+  float* sSc = reinterpret_cast<float*>(smem + T::OFF_SC);  // [SR][3][128]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::OFF_MISC);
-  uint64_t* landed = bars;        // [KS] copies of a tile -> S^T issue
-  uint64_t* kv_empty = bars + 4;  // [KS] PV done -> loaders
-  uint64_t* s_full = bars + 8;    // [KS] QK done, scales in -> softmax
-  uint64_t* p_full = bars + 12;   // [2] softmax -> issue
-  uint64_t* pv_done = bars + 14;  // [2] PV done -> softmax
-  uint64_t* q_full = bars + 16;   // Q ready -> issue
-  uint64_t* fin = bars + 17;      // [2] wind-down of the two issuers' products
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 20);
+  uint64_t* k_landed = bars;       // [KR] a K tile and its scales are in
+  uint64_t* k_empty = bars + 4;    // [KR] S^T done
+  uint64_t* v_landed = bars + 8;   // [VR] a V tile is in
+  uint64_t* v_empty = bars + 14;   // [VR] P^T V done
+  uint64_t* s_full = bars + 20;    // [SB] S^T done, scales in order -> softmax
+  uint64_t* s_empty = bars + 24;   // [SB] S^T read
+  uint64_t* p_full = bars + 28;    // [2] softmax -> O^T issue
+  uint64_t* pv_done = bars + 30;   // [2] P^T V done -> softmax
+  uint64_t* q_full = bars + 32;    // Q ready -> S^T issue
+  uint64_t* fin = bars + 33;       // [2] wind-down of the two issuers' products
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 36);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   // per query row: score factor, -m, raise threshold, causal limit
   float* s_f = reinterpret_cast<float*>(s_tmem + 4);
@@ -228,10 +243,17 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
   const int nq = p.q_f16 ? 3 : 2;
 
   if (tid == 0) {
-    for (int b = 0; b < KS; ++b) {
-      mbar_init(&landed[b], 32 * kLoaders);
-      mbar_init(&kv_empty[b], 1);
+    for (int b = 0; b < KR; ++b) {
+      mbar_init(&k_landed[b], 32);
+      mbar_init(&k_empty[b], 1);
+    }
+    for (int b = 0; b < VR; ++b) {
+      mbar_init(&v_landed[b], 32);
+      mbar_init(&v_empty[b], 1);
+    }
+    for (int b = 0; b < SB; ++b) {
       mbar_init(&s_full[b], 2);
+      mbar_init(&s_empty[b], SW);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&fin[b], 1);
@@ -252,107 +274,121 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
   const uint32_t tmem = *s_tmem;
 
   if (warp >= SW && warp < SW + kLoaders) {
-    // ================= loaders: warp SW + w copies rows 64 w .. + 63 ==========
+    // ================= loaders: warp SW K tiles and scales, SW + 1 V tiles =====
     const CacheView& c = p.cache;
-    const int r0 = 64 * (warp - SW);
-    const uint8_t* kb = c.k_data + (int64_t)u.h_kv * c.k_sh;
-    const uint8_t* vb = c.v_data + (int64_t)u.h_kv * c.v_sh;
+    const bool isv = warp > SW;
+    const uint8_t* base = isv ? c.v_data + (int64_t)u.h_kv * c.v_sh
+                              : c.k_data + (int64_t)u.h_kv * c.k_sh;
+    const int64_t sp = isv ? c.v_sp : c.k_sp, ss = isv ? c.v_ss : c.k_ss;
     const uint8_t* ksb = c.k_sf + (int64_t)u.h_kv * c.ksf_sh;
     const uint8_t* vsb = c.v_sf + (int64_t)u.h_kv * c.vsf_sh;
-    // pages of this lane's rows r0 + lane and r0 + 32 + lane in tile t; a row
-    // past the unit's pages takes the last one (its K row is masked, its V
-    // row zeroed)
-    auto load_pid = [&](int t, int half) -> int32_t {
-      if (t >= ntiles) return 0;
-      const int rel = t * kTileTok + r0 + 32 * half + lane;
-      const int32_t id =
-          __ldg(p.kv_indices + u.page_begin + min(P1 ? rel : rel / kPageSize, u.num_pages - 1));
-      if (id < 0 || id >= c.num_pages) {
-        atomicOr(p.flags, 0x1u);
-        return 0;
+    // pages of this lane's rows 32 g + lane of tile t; a row past the unit's
+    // pages takes the last one (its K row is masked, its V row zeroed)
+    auto load_pids = [&](int t, int32_t (&pid)[4]) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        pid[g] = 0;
+        if (t >= ntiles) continue;
+        const int rel = t * kTileTok + 32 * g + lane;
+        const int32_t id =
+            __ldg(p.kv_indices + u.page_begin + min(P1 ? rel : rel / kPageSize, u.num_pages - 1));
+        if (id < 0 || id >= c.num_pages)
+          atomicOr(p.flags, 0x1u);
+        else
+          pid[g] = id;
       }
-      return id;
     };
     // 8 lanes copy 128 bytes of a row, 4 rows an instruction: 16 rows (a page
-    // at page size 16) from row `first` of the tile; lane0: the lane that holds
-    // the first one's page id
+    // at page size 16) from row 16 g of the tile
     const int r4 = lane >> 3, ch = lane & 7;
     // swizzled 16-byte chunk of this lane's rows 8 i + r4 and 8 i + 4 + r4
     const uint32_t at0 = r4 * 128 + ((ch ^ r4) << 4), at1 = (r4 + 4) * 128 + ((ch ^ (r4 + 4)) << 4);
-    auto copy = [&](uint32_t tile, const uint8_t* base, int64_t sp, int64_t ss, int32_t pid,
-                    int first, int lane0) {
-      const uint32_t dst = tile + first * 128;
-      if constexpr (P1) {
+    auto copy = [&](uint32_t tile, const uint8_t* from, const int32_t (&pid)[4]) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int32_t pg = __shfl_sync(0xffffffffu, pid, lane0 + 4 * k + r4);
-          cp_async_16a(dst + (k >> 1) * 1024 + (k & 1 ? at1 : at0), base + pg * sp + 16 * ch);
+      for (int g = 0; g < 8; ++g) {
+        const uint32_t dst = tile + g * 2048;
+        if constexpr (P1) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int32_t pg = __shfl_sync(0xffffffffu, pid[g >> 1], 16 * (g & 1) + 4 * k + r4);
+            cp_async_16a(dst + (k >> 1) * 1024 + (k & 1 ? at1 : at0), from + pg * sp + 16 * ch);
+          }
+        } else {
+          const uint8_t* src =
+              from + __shfl_sync(0xffffffffu, pid[g >> 1], 16 * (g & 1)) * sp + r4 * ss + 16 * ch;
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            cp_async_16a(dst + (k >> 1) * 1024 + (k & 1 ? at1 : at0), src + 4 * k * ss);
         }
-      } else {
-        const uint8_t* src =
-            base + __shfl_sync(0xffffffffu, pid, lane0) * sp + r4 * ss + 16 * ch;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          cp_async_16a(dst + (k >> 1) * 1024 + (k & 1 ? at1 : at0), src + 4 * k * ss);
       }
     };
-    auto issue = [&](int t, int32_t pid0, int32_t pid1) {
-      const int st = t % KS;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int32_t pid = g < 2 ? pid0 : pid1;
-        const int first = r0 + 16 * g, lane0 = 16 * (g & 1);
-#pragma unroll
-        for (int b = 0; b < DK / 128; ++b)
-          copy(smem_addr(sK) + st * T::KB + b * (kTileTok * 128), kb + 128 * b, c.k_sp, c.k_ss,
-               pid, first, lane0);
-#pragma unroll
-        for (int b = 0; b < DV / 128; ++b)
-          copy(smem_addr(sV) + st * T::VB + b * (kTileTok * 128), vb + 128 * b, c.v_sp, c.v_ss,
-               pid, first, lane0);
-      }
-      const uint32_t sc = smem_addr(sSc) + st * T::SCB + 4 * (r0 + lane);
-      cp_async_4(sc, ksb + pid0 * c.ksf_sp);
-      cp_async_4(sc + 128, ksb + pid1 * c.ksf_sp);
-      cp_async_4(sc + 4 * kTileTok, vsb + pid0 * c.vsf_sp);
-      cp_async_4(sc + 4 * kTileTok + 128, vsb + pid1 * c.vsf_sp);
-    };
-    int32_t next0 = load_pid(0, 0), next1 = load_pid(0, 1);
-    for (int t = 0; t < ntiles; ++t) {
-      if (t >= KS) {
+    const int ring = isv ? VR : KR, bytes = isv ? T::VB : T::KB;
+    const int blocks = isv ? DV / 128 : DK / 128;
+    const uint32_t s0 = smem_addr(isv ? sV : sK);
+    uint64_t* empty = isv ? v_empty : k_empty;
+    uint64_t* landed = isv ? v_landed : k_landed;
+    int32_t next[4];
+    load_pids(0, next);
+    for (int t = 0, st = 0, round = 0; t < ntiles; ++t) {
+      if (round > 0) {
         bool ok = true;
-        if (lane == 0) ok = wait_bar(&kv_empty[t % KS], (t / KS - 1) & 1, s_abort, p.flags);
+        if (lane == 0) ok = wait_bar(&empty[st], (round - 1) & 1, s_abort, p.flags);
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
         tc_fence_after();
       }
-      const int32_t pid0 = next0, pid1 = next1;
-      next0 = load_pid(t + 1, 0);
-      next1 = load_pid(t + 1, 1);
-      issue(t, pid0, pid1);
-      cp_async_arrive(&landed[t % KS]);  // once this thread's copies have landed
+      int32_t pid[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) pid[g] = next[g];
+      load_pids(t + 1, next);
+#pragma unroll 1
+      for (int b = 0; b < blocks; ++b)
+        copy(s0 + st * bytes + b * (kTileTok * 128), base + 128 * b, pid);
+      if (!isv) {
+        const uint32_t sc = smem_addr(sSc) + (t % SR) * T::SCB + 4 * lane;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          cp_async_4(sc + 128 * g, ksb + pid[g] * c.ksf_sp);
+          cp_async_4(sc + 128 * g + 4 * kTileTok, vsb + pid[g] * c.vsf_sp);
+        }
+      }
+      const bool withhold = NVFP4KV_E4M3_TEST_SKIP_ARRIVE && blockIdx.x == 0 &&
+                            blockIdx.y == 0 && !isv && t == 0;
+      if (!withhold) cp_async_arrive(&landed[st]);  // once this thread's copies have landed
+      if (++st == ring) {
+        st = 0;
+        ++round;
+      }
     }
     cp_async_commit();
     cp_async_wait<0>();
   } else if (warp == SW + kLoaders) {
-    // ======== S^T issue: once a tile has landed, its scales and the rows past
-    // the end are put in order by the warp and one thread issues the products ==
+    // ======== S^T issue: one thread the products, then the warp the scales ====
     const uint64_t kd0 = smem_desc(smem_addr(sK), 16, 1024, kSwz128);
     const uint64_t qd0 = smem_desc(smem_addr(sQ), 16, 1024, kSwz128);
-    for (int k = 0; k < ntiles; ++k) {
-      // (a stage is refilled after PV(k - KS): its S^T has been consumed)
-      const int st = k % KS;
+    for (int k = 0, st = 0, round = 0; k < ntiles; ++k) {
       bool ok = true;
-      if (lane == 0) ok = wait_bar(&landed[st], (k / KS) & 1, s_abort, p.flags);
+      if (lane == 0) {
+        ok = wait_bar(&k_landed[st], round & 1, s_abort, p.flags);
+        if (ok && k == 0) ok = wait_bar(q_full, 0, s_abort, p.flags);
+        if (ok && k >= SB) ok = wait_bar(&s_empty[k % SB], (k / SB - 1) & 1, s_abort, p.flags);
+      }
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      // rows past the request's end or the unit's pages: no NaN code times 0
-      const int live = min(u.kv_len - u.tok_begin, unit_tok) - k * kTileTok;
-      for (int row = max(live, 0); row < kTileTok; ++row)
+      fence_async_smem();
+      if (lane == 0) {
+        tc_fence_after();
+        const uint32_t d = tmem + T::SCOL + N * (k % SB);
+        const uint64_t kd = kd0 + ((st * T::KB) >> 4);
+        for (int q = 0; q < nq; ++q)
 #pragma unroll
-        for (int b = 0; b < DV / 128; ++b)
-          *reinterpret_cast<uint32_t*>(sV + st * T::VB + b * (kTileTok * 128) + row * 128 +
-                                       4 * lane) = 0u;
+          for (int kk = 0; kk < DK / 32; ++kk)
+            umma8_ss(d, kd + (((kk >> 2) * (kTileTok * 128) + (kk & 3) * 32) >> 4),
+                     qd0 + ((q * T::QB + (kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4),
+                     T::IDESC_QK, (q > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&s_full[k % SB]);
+        umma_commit(&k_empty[st]);
+      }
       // the tokens' scales as the softmax threads use them
-      float* sc = sSc + st * (T::SCB / 4) + lane;
+      float* sc = sSc + (k % SR) * (T::SCB / 4) + lane;
 #pragma unroll
       for (int part = 0; part < 4; ++part, sc += 32) {
         const float ks = sc[0], vs = sc[kTileTok];
@@ -364,25 +400,12 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
         sc[kTileTok] = lv;
         sc[2 * kTileTok] = ex2(-lv);
       }
-      fence_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        if (k == 0) ok = wait_bar(q_full, 0, s_abort, p.flags);
-        if (ok) {
-          tc_fence_after();
-          const uint32_t d = tmem + T::SCOL + N * st;
-          const uint64_t kd = kd0 + ((st * T::KB) >> 4);
-          for (int q = 0; q < nq; ++q)
-#pragma unroll
-            for (int kk = 0; kk < DK / 32; ++kk)
-              umma8_ss(d, kd + (((kk >> 2) * (kTileTok * 128) + (kk & 3) * 32) >> 4),
-                       qd0 + ((q * T::QB + (kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4),
-                       T::IDESC_QK, (q > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&s_full[st]);
-          mbar_arrive(&s_full[st]);  // (the softmax threads read the scales)
-        }
+      if (lane == 0) mbar_arrive(&s_full[k % SB]);
+      if (++st == KR) {
+        st = 0;
+        ++round;
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
     }
     if (lane == 0) {
       umma_commit(&fin[0]);  // wind-down: every product issued has completed
@@ -390,31 +413,52 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     }
     __syncwarp();
   } else if (warp == SW + kLoaders + 1) {
-    // ======== O^T issue (one thread) ==========================================
-    if (lane == 0) {
-      const uint64_t vd0 = smem_desc(smem_addr(sV), kTileTok * 128, 1024, kSwz128);
-      const uint64_t pd0 = smem_desc(smem_addr(sP), T::PB, 1024, kSwz128);
-      const uint64_t pd1 = smem_desc(smem_addr(sP) + T::P1_OFF, T::PB, 512, kSwz64);
-      for (int i = 0; i < ntiles; ++i) {
-        if (!wait_bar(&p_full[i & 1], (i >> 1) & 1, s_abort, p.flags)) break;
-        tc_fence_after();
-        const uint64_t vd = vd0 + (((i % KS) * T::VB) >> 4);
-        const uint64_t buf = ((i & 1) * T::PB) >> 4;
+    // ======== O^T issue: one thread the products ==============================
+    const uint64_t vd0 = smem_desc(smem_addr(sV), kTileTok * 128, 1024, kSwz128);
+    const uint64_t pd0 = smem_desc(smem_addr(sP), T::PB, 1024, kSwz128);
+    const uint64_t pd1 = smem_desc(smem_addr(sP) + T::P1_OFF, T::PB, 512, kSwz64);
+    for (int i = 0, st = 0, round = 0; i < ntiles; ++i) {
+      bool ok = true;
+      if (lane == 0) ok = wait_bar(&v_landed[st], round & 1, s_abort, p.flags);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      // rows past the request's end or the unit's pages: no NaN code times 0
+      const int live = min(u.kv_len - u.tok_begin, unit_tok) - i * kTileTok;
+      for (int row = max(live, 0); row < kTileTok; ++row)
 #pragma unroll
         for (int b = 0; b < DV / 128; ++b)
+          *reinterpret_cast<uint32_t*>(sV + st * T::VB + b * (kTileTok * 128) + row * 128 +
+                                       4 * lane) = 0u;
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        ok = wait_bar(&p_full[i & 1], (i >> 1) & 1, s_abort, p.flags);
+        if (ok) {
+          tc_fence_after();
+          const uint64_t vd = vd0 + ((st * T::VB) >> 4);
+          const uint64_t buf = ((i & 1) * T::PB) >> 4;
 #pragma unroll
-          for (int k = 0; k < kTileTok / 32; ++k) {
-            const uint64_t vk = vd + ((b * (kTileTok * 128) + k * 32 * 128) >> 4);
-            const uint32_t acc = (i > 0 || k > 0) ? 1u : 0u;
-            umma8_ss(tmem + T::OCOL + b * T::PN, vk, pd0 + buf + ((k * 32 * 128) >> 4),
-                     T::IDESC_PV, acc);
-            if constexpr (T::PN1 > 0)
-              umma8_ss(tmem + T::OCOL + b * T::PN + T::PN0, vk, pd1 + buf + ((k * 32 * 64) >> 4),
-                       idesc_f16(128, T::PN1, 1, 1), acc);
-          }
-        umma_commit(&pv_done[i & 1]);
-        umma_commit(&kv_empty[i % KS]);
+          for (int b = 0; b < DV / 128; ++b)
+#pragma unroll
+            for (int k = 0; k < kTileTok / 32; ++k) {
+              const uint64_t vk = vd + ((b * (kTileTok * 128) + k * 32 * 128) >> 4);
+              const uint32_t acc = (i > 0 || k > 0) ? 1u : 0u;
+              umma8_ss(tmem + T::OCOL + b * T::PN, vk, pd0 + buf + ((k * 32 * 128) >> 4),
+                       T::IDESC_PV, acc);
+              if constexpr (T::PN1 > 0)
+                umma8_ss(tmem + T::OCOL + b * T::PN + T::PN0, vk,
+                         pd1 + buf + ((k * 32 * 64) >> 4), idesc_f16(128, T::PN1, 1, 1), acc);
+            }
+          umma_commit(&pv_done[i & 1]);
+          umma_commit(&v_empty[st]);
+        }
       }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      if (++st == VR) {
+        st = 0;
+        ++round;
+      }
+    }
+    if (lane == 0) {
       umma_commit(&fin[1]);
       drain_bar(&fin[1], 0, p.flags);
     }
@@ -516,12 +560,12 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     // inverse of that scale, twice
     auto scores = [&](int i, float (&x)[NH], uint64_t& iv2) {
       const int tile_tok0 = u.tok_begin + i * kTileTok, tok = tile_tok0 + j;
-      const float* sc = sSc + (i % KS) * (T::SCB / 4) + j;
+      const float* sc = sSc + (i % SR) * (T::SCB / 4) + j;
       const float ks = sc[0], lv = sc[kTileTok], iv = sc[2 * kTileTok];
       const uint64_t ks2 = pack_f32x2(ks, ks), lv2 = pack_f32x2(lv, lv);
       iv2 = pack_f32x2(iv, iv);
       uint32_t sv[NH];
-      tmem_ld<NH>(tmem + lane_base + T::SCOL + N * (i % KS) + c0, sv);
+      tmem_ld<NH>(tmem + lane_base + T::SCOL + N * (i % SB) + c0, sv);
       tmem_wait_ld<NH>(sv);
 #pragma unroll
       for (int e4 = 0; e4 < NH; e4 += 4) {
@@ -553,7 +597,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     };
     for (int i = 0; i < ntiles; ++i) {
       const int sb = i & 1;
-      warp_wait(&s_full[i % KS], (i / KS) & 1);
+      warp_wait(&s_full[i % SB], (i / SB) & 1);
       tc_fence_after();
       float x[NH];
       uint64_t iv2 = 0;
@@ -626,6 +670,9 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
         }
         if (active) scores(i, x, iv2);  // (again: nothing of the tile is kept over a raise)
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_empty[i % SB]);  // this warp has read S^T and the scales
       // ---- weights: the P^T row of this token, in pieces ----------------------
       if (i >= 2) warp_wait(&pv_done[sb], ((i - 2) >> 1) & 1);  // P buffer sb is free
       if (active) {
