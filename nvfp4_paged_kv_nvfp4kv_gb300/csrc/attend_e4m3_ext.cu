@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
 
     const int gbar = 1 + (warp >> 2), gtid = tid & 127;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {  // (every lane: no hand-over)
-      wait_bar(bar, parity, s_abort, p.flags);
+      if (!mbar_test_wait(bar, parity)) wait_bar(bar, parity, s_abort, p.flags);
       __syncwarp();
     };
     // The column groups (four warps each, the tile's 128 tokens) are
@@ -580,19 +580,16 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
                        x[e4 + 2 * e], x[e4 + 2 * e + 1]);
         }
       }
-      if (tile_tok0 + kTileTok - 1 > min_lim) {
+      if (tile_tok0 + kTileTok > min(min_lim + 1, tok_end)) {  // (a unit's last tiles)
+        const int past = tok >= tok_end ? INT32_MIN : INT32_MAX;
 #pragma unroll
         for (int e4 = 0; e4 < NH; e4 += 4) {
           const int4 lm = *reinterpret_cast<const int4*>(s_lim + c0 + e4);
-          if (tok > lm.x) x[e4] = -INFINITY;
-          if (tok > lm.y) x[e4 + 1] = -INFINITY;
-          if (tok > lm.z) x[e4 + 2] = -INFINITY;
-          if (tok > lm.w) x[e4 + 3] = -INFINITY;
+          if (tok > min(lm.x, past)) x[e4] = -INFINITY;
+          if (tok > min(lm.y, past)) x[e4 + 1] = -INFINITY;
+          if (tok > min(lm.z, past)) x[e4 + 2] = -INFINITY;
+          if (tok > min(lm.w, past)) x[e4 + 3] = -INFINITY;
         }
-      }
-      if (tile_tok0 + kTileTok > tok_end && tok >= tok_end) {
-#pragma unroll
-        for (int e = 0; e < NH; ++e) x[e] = -INFINITY;
       }
     };
     for (int i = 0; i < ntiles; ++i) {
