@@ -8,7 +8,7 @@
 //  * Query rows, times a power of two that puts the row's largest |q| into
 //    [128, 256): q = q0 + q1 (+ q2), each piece the rounded rest.  A piece has
 //    four significant bits, so two give a bf16 value's eight and three an f16
-//    value's eleven, down to 2^-18 of the row's largest |q|.
+//    value's eleven, down to 2^-17 of the row's largest |q|.
 //    S^T = K (q0 + q1 + ..)^T accumulates in one tile of tensor memory.
 //  * Weights p' = 2^x (at most 2^8): p' = w0 + w1 / 32 + w2 / 1024.  Each piece
 //    has its own columns of O^T = V^T (w0 | w1 | w2)^T, added in the epilogue:
@@ -23,7 +23,7 @@
 // One CTA = one work unit (request, kv head, chunk of pages) x N = 32 or 64
 // query rows (the G heads of the group times the query positions); tiles of
 // 128 tokens; M = 128 tokens (S^T) or 128 value dims (O^T) fill the product
-// for any N.  19 warps at N = 64:
+// for any N.  20 warps at N = 64:
 //  * loaders (a warp for K, one for V): cp.async of a tile's rows straight into
 //    the 128-byte-swizzled operand layout (K: K-major, V: MN-major, both rows
 //    of 128 bytes), any byte strides and both page sizes;
