@@ -521,7 +521,7 @@ typedef struct nvfp4kv_e4m3_cache {
  *   codes E4M3_RNE_satfinite(x / s); where s > old scale, the a older tokens'
  *   codes become E4M3_RNE(code * (old / s)).
  * Slots from z on are left as they were.  Infinities saturate; a NaN is stored
- * as a NaN code and makes the outputs that read it NaN.
+ * as a NaN code.
  *   k [dev]  element (row, h, d) at k[row*k_stride_tok + h*k_stride_head + d];
  *            strides in elements, multiples of 8; 16-byte aligned; v likewise.
  *   dtype    0 bf16, 1 f16.
@@ -544,7 +544,9 @@ int nvfp4kv_e4m3_append(const nvfp4kv_e4m3_cache* cache, const void* k, int64_t 
  *   q [dev]  as in nvfp4kv_decode_run; q_dtype 0 bf16, 1 f16.
  *   out [dev]  8-byte aligned.
  * A scale outside [2^-64, 2^64] sets NVFP4KV_FLAG_BAD_SCALE.  Slots past a
- * request's length may hold anything. */
+ * request's length may hold anything.  A row with a NaN or an infinity in its
+ * query, or a NaN in a key that it sees, is NaN and so is its lse; a NaN value
+ * makes its dim NaN in the rows that see its token, and in no others. */
 int nvfp4kv_e4m3_decode_run(const nvfp4kv_plan_info* info, const void* q, int64_t q_stride_tok,
                             int64_t q_stride_head, int32_t q_dtype,
                             const nvfp4kv_e4m3_cache* cache, const int32_t* kv_indices,

@@ -22,7 +22,13 @@
 //    1-2, and a tile's tokens are taken in the order m -> m ^ ((m >> 1) & 1),
 //    so the lanes' 16-byte reads hit distinct banks.
 //  * The maximum is raised only when a value exceeds it by more than 2^8.
+//  * NaN: a NaN score makes its row NaN.  A weight of 0 would carry a NaN value
+//    code into the rows that do not see its token, so in tiles that some row
+//    does not see whole the codes are taken out of the product, and the first
+//    such token of each value dim makes that dim NaN in the rows that see it.
 // HBM bounds it: Dk + Dv bytes a token and kv head.
+#include <climits>
+#include <cmath>
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -58,7 +64,8 @@ struct E4Traits {
   static constexpr int QROW = DK + 8;                 // f16 elements, padded
   static constexpr int OFF_Q = MAIN_BYTES;
   static constexpr int OFF_ROW = OFF_Q + RB * QROW * 2;
-  static constexpr int SMEM = OFF_ROW + 2 * RB * 4 + 16;
+  static constexpr int OFF_NAN = OFF_ROW + 2 * RB * 4 + 16;  // [DV] first NaN token taken out
+  static constexpr int SMEM = OFF_NAN + DV * 4;
   static_assert(DK % 64 == 0 && DV % 64 == 0, "head dims");
 };
 
@@ -104,6 +111,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
   uint16_t* sQ = reinterpret_cast<uint16_t*>(smem + T::OFF_Q);
   float* sRowF = reinterpret_cast<float*>(smem + T::OFF_ROW);
   int* sRowLim = reinterpret_cast<int*>(sRowF + T::RB);
+  int* sNan = reinterpret_cast<int*>(smem + T::OFF_NAN);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -155,6 +163,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
                                               (ci % (DK / 8)) * 8);
   }
   if (tid < T::RB) reinterpret_cast<int*>(sRowF)[tid] = 0;  // per-row amax bits
+  for (int d = tid; d < DV; d += WARPS * 32) sNan[d] = INT_MAX;
   __syncthreads();
 
   // ---- the tile pipeline ---------------------------------------------------
@@ -238,7 +247,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
     int e = 0;  // amax * 2^e in [2^14, 2^15)
     if (amax > 0.f) e = 14 - (int)((__float_as_uint(amax) >> 23) & 0xFF) + 127;
     e = max(-120, min(120, e));
-    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+    // (an infinite element makes its row NaN, as 0 * inf does)
+    const float up = isinf(amax) ? NAN : __uint_as_float((uint32_t)(127 + e) << 23);
     const uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
     uint32_t h[4];
 #pragma unroll
@@ -286,6 +296,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
     return th;
   };
   float thr_lane = lane_threshold();
+  bool saw_nan = false;  // a NaN value code was taken out of this lane's products
   // Q fragments: k-step 4 cc + m covers the 4 dims 16 (4 cc + t) + 4 m ..
   uint32_t qreg[NT][T::KSTEPS][2];
 #pragma unroll
@@ -349,7 +360,8 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
       for (int k = 0; k < 4; ++k)
         x[n][k] = fmaf(sa[n][k] + sb[n][k], f2[2 * n + (k & 1)] * (k < 2 ? ksA : ksB),
                        nm2[2 * n + (k & 1)] + (k < 2 ? lvA : lvB));
-    if (tok0 + 15 > min_lim) {
+    const bool masked = tok0 + 15 > min_lim;  // some row does not see some token
+    if (masked) {
       const int ta = tok0 + kr0, tb = ta + 8;
 #pragma unroll
       for (int k = 0; k < NR; ++k) {
@@ -429,13 +441,28 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
         w[2][0] = q2v.x; w[2][1] = q2v.y;
         w[3][0] = q3.x; w[3][1] = q3.y;
       }
-      if (valid < 16) {
+      if (masked) {
 #pragma unroll
-        for (int k = 0; k < VW; ++k) {
-          if (vt0 >= valid) w[0][k] = 0;
-          if (vt1 >= valid) w[1][k] = 0;
-          if (vt0 + 8 >= valid) w[2][k] = 0;
-          if (vt1 + 8 >= valid) w[3][k] = 0;
+        for (int j = 0; j < 4; ++j) {
+          const int tok = (j & 1 ? vt1 : vt0) + (j & 2) * 4;
+          uint32_t nan = 0;
+#pragma unroll
+          for (int k = 0; k < VW; ++k) {
+            if (tok >= valid) w[j][k] = 0;
+            nan |= ((w[j][k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+          }
+          if (nan) {
+            saw_nan = true;
+            const int d0 = 128 * cc + g * T::VCB;
+            for (int b = 0; b < T::VCB; ++b) {
+#pragma unroll
+              for (int k = 0; k < VW; ++k)  // (registers have no index)
+                if (b / 4 == k && ((w[j][k] >> (8 * (b % 4))) & 0x7Fu) == 0x7Fu) {
+                  w[j][k] &= ~(0xFFu << (8 * (b % 4)));
+                  atomicMin(&sNan[d0 + b], tok0 + tok);
+                }
+            }
+          }
         }
       }
       // m-tile of byte pair m: rows g and g + 8 are the dims of bytes 2m, 2m+1
@@ -466,7 +493,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
   for (int k = 0; k < NR; ++k)
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) lrow[k] += __shfl_xor_sync(0xffffffffu, lrow[k], o);
-  __syncthreads();  // every warp is done with its ring
+  const bool any_nan = __syncthreads_or(saw_nan);  // every warp is done with its ring
   float* sO = reinterpret_cast<float*>(smem);   // [WARPS][RB][OS]
   float* sM = sO + WARPS * T::RB * T::OS;       // [WARPS][RB]
   float* sL = sM + WARPS * T::RB;               // [WARPS][RB]
@@ -476,7 +503,10 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
     if (g == 0) {
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        sM[r0 + k] = (has_max >> (2 * n + k)) & 1u ? -nm2[2 * n + k] : -INFINITY;
+        // (a NaN sum counts whatever the maximum, which no NaN score raises)
+        sM[r0 + k] = isnan(lrow[2 * n + k])               ? 0.f
+                     : (has_max >> (2 * n + k)) & 1u ? -nm2[2 * n + k]
+                                                          : -INFINITY;
         sL[r0 + k] = lrow[2 * n + k];
       }
     }
@@ -490,6 +520,13 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
     }
   }
   __syncthreads();
+  if (any_nan) {
+    for (int i = tid; i < WARPS * T::RB * DV; i += WARPS * 32) {
+      const int rr = i / DV, d = i % DV;
+      if (sRowLim[rr % T::RB] >= sNan[d]) sO[rr * T::OS + d] = NAN;
+    }
+    __syncthreads();
+  }
   finish_rows<T::RB, DV, WARPS, T::OS>(p, u, row0, R, sM, sL, sO, sRowF);
 }
 

@@ -35,6 +35,8 @@
 //    beat few warps with many (8 warps of 32 rows 258, 16 of 16 rows 236 us).
 // The running maximum is raised only when a value exceeds 2^8.  Every wait is
 // bounded; one that runs out sets flag 0x4 and the CTA winds down.
+#include <climits>
+#include <cmath>
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -59,6 +61,7 @@ using namespace tc5;
 constexpr int kTileTok = 128;
 constexpr int kLoaders = 2;  // warps: K, V
 constexpr int kAllSoftmax = 5;  // named barriers 1 .. 4: the column groups
+constexpr int kNanReady = 6;
 constexpr int kPieces = 3;      // of a weight
 constexpr float kRaise = 8.f;  // log2 of the largest weight before m is raised
 constexpr float kMinScale = 0x1p-64f, kMaxScale = 0x1p64f;
@@ -181,8 +184,38 @@ struct Ext {
   static_assert(DK % 128 == 0 && DV % 128 == 0, "operand rows of 128 bytes");
   static_assert(OFF_P % 1024 == 0 && OFF_Q % 1024 == 0 && OFF_MISC % 16 == 0, "align");
   static_assert(SMEM <= 232448 && COLS <= 512 && PN0 % 16 == 0, "resources");
-  static_assert(36 * 8 + 16 + (7 * N + 2 * N + 4 + 4 * N) * 4 <= MISC, "misc");
+  static_assert(36 * 8 + 16 + (7 * N + 2 * N + 4 + 4 * N + DV) * 4 <= MISC, "misc");
 };
+
+// A V tile that some row of the block does not see whole (run by a warp): rows
+// from `live` on are zeroed, NaN codes before them too, and first[d] becomes the
+// first token (the tile begins with `tok0`) that had one in value dim d.
+template <int DV>
+__device__ __forceinline__ void no_nan(uint8_t* tile, int live, int tok0, int* first) {
+  const int lane = threadIdx.x & 31;
+  tile += 4 * lane;  // this lane's column of 4 bytes
+  for (int row = max(live, 0); row < kTileTok; ++row)
+#pragma unroll
+    for (int b = 0; b < DV / 128; ++b)
+      *reinterpret_cast<uint32_t*>(tile + b * (kTileTok * 128) + row * 128) = 0u;
+#pragma unroll 1
+  for (int k0 = 0; k0 < kTileTok * (DV / 128); k0 += 16) {  // rows of 128 dims
+    uint8_t* at = tile + k0 * 128;
+    uint32_t nan = 0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      nan |= (*reinterpret_cast<const uint32_t*>(at + 128 * k) & 0x7F7F7F7Fu) + 0x01010101u;
+    if (!(nan & 0x80808080u)) continue;
+    for (int k = 0; k < 16; ++k)
+      for (int e = 0; e < 4; ++e)
+        if ((at[128 * k + e] & 0x7F) == 0x7F) {
+          const int row = (k0 + k) % kTileTok, blk = (k0 + k) / kTileTok;
+          at[128 * k + e] = 0;
+          atomicMin(&first[128 * blk + 16 * ((lane >> 2) ^ (row & 7)) + 4 * (lane & 3) + e],
+                    tok0 + row);
+        }
+  }
+}
 
 // P1: 1-token pages
 template <int DK, int DV, int N, bool P1>
@@ -211,6 +244,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
   uint64_t* p_full = bars + 28;    // [2] softmax -> O^T issue
   uint64_t* pv_done = bars + 30;   // [2] P^T V done -> softmax
   uint64_t* q_full = bars + 32;    // Q ready -> S^T issue
+  uint64_t* v_clean = bars + 35;   // the V tiles from first_part on hold no NaN code
   uint64_t* fin = bars + 33;       // [2] wind-down of the two issuers' products
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 36);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
@@ -223,7 +257,8 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
   int* s_max = reinterpret_cast<int*>(s_m + N);      // reduction keys, then shifts
   float* s_corr = reinterpret_cast<float*>(s_max + N);
   float* s_fin = s_corr + N;                         // [2N + 4]
-  float* s_l = s_fin + 2 * N + 4;                        // [4][N] row sums of the lane quarters
+  float* s_l = s_fin + 2 * N + 4;                    // [4][N] row sums of the lane quarters
+  int* s_nan = reinterpret_cast<int*>(s_l + 4 * N);  // [DV] first NaN token taken out of V
 
   const WorkUnit u = load_unit(p);
   const int G = p.group;
@@ -243,6 +278,12 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
   }
   const int ntiles = max(0, (tok_end - u.tok_begin + kTileTok - 1) / kTileTok);
   const int nq = p.q_f16 ? 3 : 2;
+  // the last token that every row of the block sees
+  auto all_see = [&] { return p.causal ? u.kv_len - u.qo_len + row0 / G : u.kv_len - 1; };
+  // tokens of the unit in the cache; the first tile not all of whose tokens every
+  // row of the block sees
+  const int unit_end = min(u.kv_len - u.tok_begin, unit_tok);
+  const int first_part = max(min(all_see() + 1 - u.tok_begin, unit_end), 0) / kTileTok;
 
   if (tid == 0) {
     for (int b = 0; b < KR; ++b) {
@@ -263,6 +304,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
       mbar_init(&pv_done[b], 1);
     }
     mbar_init(q_full, SW);
+    mbar_init(v_clean, 1);
     mbar_init_fence();
     *s_abort = 0;
   }
@@ -409,6 +451,26 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
         ++round;
       }
     }
+    // The V tiles that some row does not see whole, the last one or two (the rows'
+    // limits lie less than N <= 64 tokens apart): a weight of 0 must not meet a
+    // NaN code.  Done here, as this warp is up to four tiles ahead: 32 requests of
+    // 2000-16000 tokens x 64 rows take 192 us, 190 without, and 197 with the same
+    // work in the warp that issues O^T.
+    static_assert(N <= 64 && VR >= 2, "both tiles fit the ring while O^T waits for v_clean");
+    for (int d = lane; d < DV; d += 32) s_nan[d] = INT_MAX;
+    __syncwarp();
+    bool ok = true;
+    for (int t = first_part; t < ntiles && ok; ++t) {
+      if (lane == 0) ok = wait_bar(&v_landed[t % VR], (t / VR) & 1, s_abort, p.flags);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (ok)
+        no_nan<DV>(sV + (t % VR) * T::VB, unit_end - t * kTileTok, u.tok_begin + t * kTileTok,
+                   s_nan);
+    }
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0 && ok) mbar_arrive(v_clean);
+    named_sync(kNanReady, ST + 32);  // s_nan is complete
     if (lane == 0) {
       umma_commit(&fin[0]);  // wind-down: every product issued has completed
       drain_bar(&fin[0], 0, p.flags);
@@ -421,15 +483,11 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     const uint64_t pd1 = smem_desc(smem_addr(sP) + T::P1_OFF, T::PB, 512, kSwz64);
     for (int i = 0, st = 0, round = 0; i < ntiles; ++i) {
       bool ok = true;
-      if (lane == 0) ok = wait_bar(&v_landed[st], round & 1, s_abort, p.flags);
+      if (lane == 0) {
+        ok = wait_bar(&v_landed[st], round & 1, s_abort, p.flags);
+        if (ok && i >= first_part) ok = wait_bar(v_clean, 0, s_abort, p.flags);
+      }
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
-      // rows past the request's end or the unit's pages: no NaN code times 0
-      const int live = min(u.kv_len - u.tok_begin, unit_tok) - i * kTileTok;
-      for (int row = max(live, 0); row < kTileTok; ++row)
-#pragma unroll
-        for (int b = 0; b < DV / 128; ++b)
-          *reinterpret_cast<uint32_t*>(sV + st * T::VB + b * (kTileTok * 128) + row * 128 +
-                                       4 * lane) = 0u;
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -496,7 +554,8 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
       int ex = 0;  // amax * 2^ex in [128, 256)
       if (amax > 0.f) ex = 7 - (int)((__float_as_uint(amax) >> 23) & 0xFF) + 127;
       ex = max(-120, min(120, ex));
-      const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+      // (an infinite element has no pieces: its row is NaN, as 0 * inf makes it)
+      const float up = isinf(amax) ? NAN : __uint_as_float((uint32_t)(127 + ex) << 23);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         rest[e].x *= up;
@@ -532,7 +591,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     fence_async_smem();
     named_sync(kAllSoftmax, ST);
     if (lane == 0) mbar_arrive(q_full);
-    const int min_lim = p.causal ? u.kv_len - u.qo_len + row0 / G : u.kv_len - 1;
+    const int min_lim = all_see();
     const int nvalid = min(N, R - row0);  // columns that are real query rows
     const bool active = c0 < nvalid;      // warp-uniform
 
@@ -727,6 +786,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
 
     // ---- epilogue: O^T row of value dim j, this thread's query rows -----------
     if (ntiles > 0) warp_wait(&pv_done[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1);
+    named_sync(kNanReady, ST + 32);
     {
       tc_fence_after();
       constexpr float kLn2 = 0.69314718055994530942f;
@@ -742,7 +802,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
         if (col_l < nvalid) {
           const float L = s_l[col_l] + s_l[N + col_l] + s_l[2 * N + col_l] + s_l[3 * N + col_l];
           const float m = s_m[col_l];
-          const bool any = L > 0.f && m != -INFINITY;
+          const bool any = m != -INFINITY || isnan(L);  // (a NaN score need not raise)
           f_l = any ? 1.f / L : 0.f;
           const float lse_v = any ? (m + log2f(L)) * kLn2 : -INFINITY;
           const int gr = row0 + col_l, qi = gr / G, head = u.h_kv * G + gr % G;
@@ -769,6 +829,11 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
               o[e] = q == kPieces - 1 ? __uint_as_float(ov[e])
                                  : fmaf(o[e], 0.03125f, __uint_as_float(ov[e]));
           }
+          if (const int first = s_nan[128 * b + j]; first != INT_MAX) {
+#pragma unroll
+            for (int e = 0; e < NH; ++e)
+              if (s_lim[c0 + e] >= first) o[e] = NAN;
+          }
 #pragma unroll
           for (int e = 0; e < NH; ++e) {
             const float f = __shfl_sync(0xffffffffu, f_l, e);
@@ -784,7 +849,8 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
         }
       }
       if (partial)
-        merge_if_last<N, DV, ST, 4>(p, u, row0, R, s_fin, tid, [] { named_sync(kAllSoftmax, ST); });
+        fold_if_last<N, DV, ST, 1, 4>(p, u, row0, nvalid, reinterpret_cast<int*>(s_fin + 2 * N),
+                                      tid, [] { named_sync(kAllSoftmax, ST); });
     }
     tc_fence_before();
   }

@@ -155,12 +155,106 @@ __device__ __forceinline__ void finish_unit(const AttendParams& p, const WorkUni
                              [] { __syncthreads(); });
 }
 
+// The split group's arrival and, in its last CTA, the fold of the partial
+// states: NT threads (tid in [0, NT)) that synchronise with `sync`, `last` a
+// word in shared memory.  The arrival is one acquire-release atomic after the
+// barrier, which orders the CTA's partial stores before it and the last CTA's
+// loads after it.  A thread folds IT items (row, four dims) at a time, MB
+// partial states loaded together.  A NaN state (a NaN score in its chunk) makes
+// the row NaN, lse too.
+template <int RB, int DV, int NT, int IT, int MB, class Sync>
+__device__ __forceinline__ void fold_if_last(const AttendParams& p, const WorkUnit& u, int row0,
+                                             int rows, int* last, int tid, Sync sync) {
+  using namespace dev;
+  constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+  constexpr int DQ = DV / 4;
+  const int G = p.group, Hq = p.num_qo_heads;
+  sync();
+  if (tid == 0) {
+    int* ctr = p.counters + (int64_t)u.pair * gridDim.y + blockIdx.y;
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(ctr) : "memory");
+    *last = old == u.num_splits - 1;
+    if (*last) *ctr = 0;  // every other CTA of the group has arrived
+  }
+  sync();
+  if (!*last) return;
+  const int S = u.num_splits;
+  for (int i0 = tid; i0 < rows * DQ; i0 += IT * NT) {
+    float M[IT], L[IT];
+    float4 acc[IT];
+    int64_t base[IT];
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      const int idx = i0 + k * NT < rows * DQ ? i0 + k * NT : i0, r = row0 + idx / DQ;
+      base[k] = (int64_t)u.partial_base +
+                ((int64_t)(r / G) * Hq + u.h_kv * G + r % G) * S;
+      M[k] = -INFINITY;
+      L[k] = 0.f;
+      acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const int d4 = i0 % DQ;  // (NT is a multiple of DQ, or DQ of NT with IT = 1)
+    static_assert(NT % DQ == 0, "a thread keeps its dims");
+    for (int s0 = 0; s0 < S; s0 += MB) {
+      float lw[IT][MB];
+      float4 v[IT][MB];
+#pragma unroll
+      for (int k = 0; k < IT; ++k)
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+          lw[k][j] = -INFINITY;
+          v[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (s0 + j < S) {
+            lw[k][j] = __ldcg(p.partial_lse + base[k] + s0 + j) * kLog2e;
+            v[k][j] = __ldcg(reinterpret_cast<const float4*>(p.partial_o + (base[k] + s0 + j) * DV) +
+                             d4);
+          }
+        }
+#pragma unroll
+      for (int k = 0; k < IT; ++k) {
+        float mn = M[k];
+#pragma unroll
+        for (int j = 0; j < MB; ++j) mn = fmaxf(mn, lw[k][j]);
+        if (mn == -INFINITY) {  // nothing yet, or NaN states alone
+#pragma unroll
+          for (int j = 0; j < MB; ++j)
+            if (isnan(lw[k][j])) mn = 0.f;
+          if (mn == -INFINITY) continue;
+        }
+        const float cf = ex2(M[k] - mn);  // 0 for -inf
+        L[k] *= cf;
+        acc[k].x *= cf; acc[k].y *= cf; acc[k].z *= cf; acc[k].w *= cf;
+#pragma unroll
+        for (int j = 0; j < MB; ++j) {
+          const float w = ex2(lw[k][j] - mn);
+          L[k] += w;
+          acc[k].x = fmaf(w, v[k][j].x, acc[k].x);
+          acc[k].y = fmaf(w, v[k][j].y, acc[k].y);
+          acc[k].z = fmaf(w, v[k][j].z, acc[k].z);
+          acc[k].w = fmaf(w, v[k][j].w, acc[k].w);
+        }
+        M[k] = mn;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < IT; ++k) {
+      if (i0 + k * NT >= rows * DQ) break;
+      const int r = row0 + (i0 + k * NT) / DQ;
+      const int64_t row = (int64_t)(u.qo_begin + r / G) * Hq + u.h_kv * G + r % G;
+      const bool any = M[k] != -INFINITY;
+      const float inv = any ? 1.f / L[k] : 0.f;
+      *reinterpret_cast<uint2*>(p.out + row * DV + 4 * d4) =
+          make_uint2(pack_out2(acc[k].x * inv, acc[k].y * inv, p.out_f16),
+                     pack_out2(acc[k].z * inv, acc[k].w * inv, p.out_f16));
+      if (d4 == 0 && p.lse) p.lse[row] = any ? (M[k] + log2f(L[k])) * kLn2 : -INFINITY;
+    }
+  }
+}
+
 // finish_unit for a CTA that is one unit, four dims a thread and only the rows
-// that exist; a split group's arrival is one acquire-release atomic after the
-// CTA's barrier (which orders the CTA's partial stores before it, and the last
-// CTA's loads after it) in place of fences in every thread, and the fold loads
-// all of a thread's items together.  Measured on decode shapes: combine, store,
-// arrival and fold 3.1 -> 2.4 us (head dims 128), 6.0 -> 4.1 us (512 / 256).
+// that exist, and fold_if_last in place of fences in every thread and an item at
+// a time.  Measured on decode shapes: combine, store, arrival and fold 3.1 ->
+// 2.4 us (head dims 128), 6.0 -> 4.1 us (512 / 256).
 // sO rows lie OS floats apart (more than DV: the warps' stores into them then
 // spread over the banks).
 template <int RB, int DV, int WARPS, int OS>
@@ -168,7 +262,7 @@ __device__ __forceinline__ void finish_rows(const AttendParams& p, const WorkUni
                                             int R, const float* sM, const float* sL,
                                             const float* sO, float* sFin) {
   using namespace dev;
-  constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+  constexpr float kLn2 = 0.69314718055994530942f;
   constexpr int NT = WARPS * 32, DQ = DV / 4;
   const int G = p.group, Hq = p.num_qo_heads, tid = threadIdx.x;
   const int rows = min(RB, R - row0);
@@ -214,84 +308,10 @@ __device__ __forceinline__ void finish_rows(const AttendParams& p, const WorkUni
   }
   if (!partial) return;
 
-  int* s_last = reinterpret_cast<int*>(sFin + 2 * RB);
-  __syncthreads();
-  if (tid == 0) {
-    int* ctr = p.counters + (int64_t)u.pair * gridDim.y + blockIdx.y;
-    int old;
-    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(ctr) : "memory");
-    *s_last = old == u.num_splits - 1;
-    if (*s_last) *ctr = 0;  // every other CTA of the group has arrived
-  }
-  __syncthreads();
-  if (!*s_last) return;
-  const int S = u.num_splits;
-  constexpr int IT = (RB * DQ + NT - 1) / NT < 2 ? 1 : 2;  // items of a thread at a time
-  constexpr int MB = IT == 1 ? 16 : 8;                     // partial states loaded together
-  for (int i0 = tid; i0 < rows * DQ; i0 += IT * NT) {
-    float M[IT], L[IT];
-    float4 acc[IT];
-    int64_t base[IT];
-#pragma unroll
-    for (int k = 0; k < IT; ++k) {
-      const int idx = i0 + k * NT < rows * DQ ? i0 + k * NT : i0, r = row0 + idx / DQ;
-      base[k] = (int64_t)u.partial_base +
-                ((int64_t)(r / G) * Hq + u.h_kv * G + r % G) * S;
-      M[k] = -INFINITY;
-      L[k] = 0.f;
-      acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    const int d4 = i0 % DQ;  // (NT is a multiple of DQ, or DQ of NT with IT = 1)
-    static_assert(NT % DQ == 0, "a thread keeps its dims");
-    for (int s0 = 0; s0 < S; s0 += MB) {
-      float lw[IT][MB];
-      float4 v[IT][MB];
-#pragma unroll
-      for (int k = 0; k < IT; ++k)
-#pragma unroll
-        for (int j = 0; j < MB; ++j) {
-          lw[k][j] = -INFINITY;
-          v[k][j] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (s0 + j < S) {
-            lw[k][j] = __ldcg(p.partial_lse + base[k] + s0 + j) * kLog2e;
-            v[k][j] = __ldcg(reinterpret_cast<const float4*>(p.partial_o + (base[k] + s0 + j) * DV) +
-                             d4);
-          }
-        }
-#pragma unroll
-      for (int k = 0; k < IT; ++k) {
-        float mn = M[k];
-#pragma unroll
-        for (int j = 0; j < MB; ++j) mn = fmaxf(mn, lw[k][j]);
-        if (mn == -INFINITY) continue;
-        const float cf = ex2(M[k] - mn);  // 0 for -inf
-        L[k] *= cf;
-        acc[k].x *= cf; acc[k].y *= cf; acc[k].z *= cf; acc[k].w *= cf;
-#pragma unroll
-        for (int j = 0; j < MB; ++j) {
-          const float w = ex2(lw[k][j] - mn);
-          L[k] += w;
-          acc[k].x = fmaf(w, v[k][j].x, acc[k].x);
-          acc[k].y = fmaf(w, v[k][j].y, acc[k].y);
-          acc[k].z = fmaf(w, v[k][j].z, acc[k].z);
-          acc[k].w = fmaf(w, v[k][j].w, acc[k].w);
-        }
-        M[k] = mn;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < IT; ++k) {
-      if (i0 + k * NT >= rows * DQ) break;
-      const int r = row0 + (i0 + k * NT) / DQ;
-      const int64_t row = (int64_t)(u.qo_begin + r / G) * Hq + u.h_kv * G + r % G;
-      const bool any = M[k] != -INFINITY && L[k] > 0.f;
-      const float inv = any ? 1.f / L[k] : 0.f;
-      *reinterpret_cast<uint2*>(p.out + row * DV + 4 * d4) =
-          make_uint2(pack_out2(acc[k].x * inv, acc[k].y * inv, p.out_f16),
-                     pack_out2(acc[k].z * inv, acc[k].w * inv, p.out_f16));
-      if (d4 == 0 && p.lse) p.lse[row] = any ? (M[k] + log2f(L[k])) * kLn2 : -INFINITY;
-    }
-  }
+  constexpr int IT = (RB * DQ + NT - 1) / NT < 2 ? 1 : 2;
+  fold_if_last<RB, DV, NT, IT, IT == 1 ? 16 : 8>(p, u, row0, rows,
+                                                 reinterpret_cast<int*>(sFin + 2 * RB), tid,
+                                                 [] { __syncthreads(); });
 }
 
 }  // namespace nvfp4kv

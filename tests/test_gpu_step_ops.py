@@ -380,13 +380,15 @@ def test_append_bad_old_scale_is_flagged():
 # ---- attention over the E4M3 cache ----------------------------------------------------
 def attend_case(kv, new, hq, hkv, dk, dv, causal=False, page=16, layout="HND", dtype="bf16",
                 out="bf16", seed=0, spread=3, stale=True, only=None, q_scale=1.0, live=None,
-                **plan_kw):
+                edit=None, **plan_kw):
     """Run the attention on a random cache and compare every row with the
     64-bit reference.  The result is rounded once.  Before that: a score is off
     by at most Dk 2^-23 * sm_scale sum|q k| (f32 sums of exact f16 products)
     and the exponential by 2^-21 relative, so a weight by that delta; weights
     are rounded to f16 (2^-11 relative, 2^-25 of the row's largest weight times
-    scale at least); normalised sums and a merge of split states in f32: 2^-19.
+    scale at least); normalised sums and a merge of split states in f32: 2^-19.  ``edit(c, q)``
+    may change the reference cache and the query first; then NaN has to be where
+    the reference has it.
 
     With more than 8 rows a block the tensor-memory kernel runs: it adds E4M3
     pieces, each the rounded rest (off by at most 2^-4 of it), of the query and
@@ -405,6 +407,9 @@ def attend_case(kv, new, hq, hkv, dk, dv, causal=False, page=16, layout="HND", d
         c.upload()
     g = torch.Generator().manual_seed(seed)
     q = torch.randn((sum(new) + 1, hq + 1, dk), generator=g) * q_scale
+    if edit is not None:
+        edit(c, q[:, 1:])
+        c.upload()
     q = q.to(DT[dtype]).cuda()[:, 1:]
     qo = np.concatenate([[0], np.cumsum(new)])
     plan_last = c.last
@@ -415,7 +420,7 @@ def attend_case(kv, new, hq, hkv, dk, dv, causal=False, page=16, layout="HND", d
     o, lse = N.nvfp4kv_e4m3_decode_run(plan, q, c.cache, c.kv_indices)
     assert N.nvfp4kv_workspace_flags(plan) == 0
     o2, lse2 = N.nvfp4kv_e4m3_decode_run(plan, q, c.cache, c.kv_indices)
-    assert torch.equal(lse, lse2) or plan.info.split
+    assert torch.equal(lse.nan_to_num(), lse2.nan_to_num()) or plan.info.split
     got, gl = R.to_np(o), R.to_np(lse)
     eps = torch.finfo(DT[out]).eps / 2
     scale = float(np.float32(1 / math.sqrt(dk)))
@@ -430,16 +435,20 @@ def attend_case(kv, new, hq, hkv, dk, dv, causal=False, page=16, layout="HND", d
         weight, least = 2.0 ** -11, 2.0 ** -25
         if plan.info.rows_per_block > 8:
             delta = delta + 2.0 ** -17 * scale * (np.abs(R.to_np(q[rows])).max(-1)
-                                                  * np.abs(k).sum(-1).max())
+                                                  * np.nansum(np.abs(k), -1).max())
             weight, least = weight + 2.0 ** -12, 2.0 ** -20 + 2.0 ** -25
         tol = (eps * np.abs(ref) + (mean * (weight + 2.0 ** -19 + 2 * delta[..., None])
                                     + least * floor) * (1 + eps)
                + float(torch.finfo(DT[out]).smallest_normal) * eps)
-        err = np.abs(got[rows] - ref)
-        assert np.isfinite(got[rows]).all()
-        assert (err <= tol).all(), (b, float(err.max()), float((err / tol).max()))
+        none, lnone = np.isnan(ref), np.isnan(rl)
+        assert edit is not None or not (none.any() or lnone.any())
+        assert np.array_equal(np.isnan(got[rows]), none)
+        assert np.array_equal(np.isnan(gl[rows]), lnone)
+        err = np.abs(got[rows] - ref)[~none]
+        assert (err <= tol[~none]).all(), (b, float(err.max()), float((err / tol[~none]).max()))
         lerr = np.abs(gl[rows] - rl)
-        assert (lerr <= delta + 2.0 ** -19 + np.abs(rl) * 2.0 ** -22).all(), (b, lerr.max())
+        lok = lerr <= delta + 2.0 ** -19 + np.abs(rl) * 2.0 ** -22
+        assert lok[~lnone].all(), (b, lerr[~lnone].max())
     return c, plan, o
 
 
@@ -521,6 +530,33 @@ def test_attention_live_lengths():
     attend_case((45, 110, 16), (3, 2, 1), 8, 2, 128, 128, causal=True, live=[16, 1, 9], seed=12)
 
 
+@pytest.mark.filterwarnings("ignore:invalid value")
+@pytest.mark.parametrize("page", [16, 1])
+@pytest.mark.parametrize("chunk", [0, 64])
+@pytest.mark.parametrize("dk,dv,hq,hkv,new", [
+    (128, 128, 4, 2, (1, 1, 1)), (128, 128, 8, 2, (4, 3, 2)), (64, 64, 4, 2, (7, 3, 8)),
+    (128, 128, 8, 2, (20, 9, 5)), (256, 256, 4, 2, (30, 9, 5)), (256, 128, 4, 2, (2, 3, 4)),
+    (512, 256, 4, 2, (7, 3, 2))])
+def test_attention_nan_reaches_the_rows_that_see_it(dk, dv, hq, hkv, new, chunk, page):
+    """NaN codes: in V, at tokens that some rows do not see (one dim of those that
+    do) and at one that all see; in K, at the last token, alone in its page; and
+    queries with a NaN or an infinite element."""
+    kv = (200, 33, 150)
+
+    def edit(c, q):
+        def at(b, t):
+            return c.pages(b)[t // page], t % page
+        for t, d, code in ((199, 5, 0x7F), (200 - (new[0] + 1) // 2, dv - 1, 0xFF), (60, 17, 0x7F)):
+            pg, slot = at(0, t)
+            c.codes[1][pg, 0, slot, d] = code
+        pg, slot = at(1, 32)
+        c.codes[0][pg, 1, slot, 3] = 0x7F
+        last = sum(new) - 1
+        q[last, 0, 7], q[last, 1, 9] = math.nan, math.inf
+    attend_case(kv, new, hq, hkv, dk, dv, causal=True, page=page, force_chunk_tokens=chunk,
+                edit=edit, seed=dk + sum(new))
+
+
 def test_attention_nothing_to_do():
     _, plan, o = attend_case((37, 5, 0), (0, 0, 0), 8, 2, 128, 128)
     assert plan.info.num_units == 0 and o.shape == (0, 8, 128)
@@ -569,6 +605,84 @@ def test_attention_refusals():
         N.nvfp4kv_e4m3_decode_run(plan, q[:1], c.cache, c.kv_indices)
     with pytest.raises(ValueError):
         N.nvfp4kv_e4m3_decode_run(plan, q, c.cache, c.kv_indices[:2])
+
+
+def test_attention_plan_with_the_other_entry_points():
+    """Kernel 5's partial states merged once more by the standalone kernel; the
+    NVFP4 entry points refuse the plan."""
+    for new in ((1, 1), (20, 9)):
+        c, plan, o = attend_case((700, 300), new, 8, 2, 128, 128, causal=True, seed=2,
+                                 force_chunk_tokens=128)
+        assert plan.info.split
+        q = torch.randn((sum(new), 8, 128), device="cuda").to(torch.bfloat16)
+        o, lse = N.nvfp4kv_e4m3_decode_run(plan, q, c.cache, c.kv_indices)
+        m, ml = torch.zeros_like(o), torch.zeros_like(lse)
+        N.nvfp4kv_decode_merge(plan, m, ml)
+        # one rounding apart from the same f32 states: a bf16 step at most
+        assert bool(((m.float() - o.float()).abs() <= 2.0 ** -7 * o.float().abs() + 1e-6).all())
+        assert torch.allclose(ml, lse, atol=2.0 ** -18, rtol=2.0 ** -20)
+        nv = N.PagedCache.allocate(W.CacheLayout("HND", c.cache.num_pages, 16, 2, 128, 128))
+        k = torch.zeros((sum(new), 2, 128), dtype=torch.bfloat16, device="cuda")
+        bare = N.nvfp4kv_decode_plan([0, new[0], sum(new)], c.indptr, c.last, 8, 2, 128, 128,
+                                     causal=True, kernel=5, allocate=False)
+        for run in (lambda: N.nvfp4kv_decode_run_static(bare, q, nv, c.kv_indices),
+                    lambda: N.nvfp4kv_decode_append_run(plan, k, k, q, nv, c.kv_indices)):
+            with pytest.raises(N.NvFp4KvError) as e:
+                run()
+            assert e.value.status == _lib.ERR_PLAN_MISMATCH
+
+
+def test_offsets_past_32_bits():
+    """A cache whose pages, rows whose tokens and a table whose requests lie far
+    apart: the first and last bytes of a buffer of 7 GB."""
+    buf = torch.zeros(7 << 30, dtype=torch.uint8, device="cuda")
+    for page in (16, 1):
+        far = (7 << 30) // 40 // 1024 * 1024
+        for new in ((1, 2), (9, 20)):
+            c = CacheCase((250, 300) if page == 16 else (15, 20), page, 2, 128, 128, seed=page)
+            total, block = c.cache.num_pages, page * 128
+            assert total <= 40
+
+            def view(first):
+                return buf[first:].as_strided((total, 2, page, 128), (far, block, 128, 1))
+            c.cache = N.E4m3Cache(view(0), view(4 * block), c.cache.k_scale, c.cache.v_scale)
+            c.upload()
+            k, v = new_rows(sum(new), 2, 128, 128, "bf16", seed=3)
+            c.append(new, k, v)
+            c.run_append(new, k, v)
+            c.check()
+            q = torch.randn((sum(new), 8, 128), generator=torch.Generator().manual_seed(1))
+            q = q.to(torch.bfloat16).cuda()
+            qo = [0, new[0], sum(new)]
+            plan = N.nvfp4kv_decode_plan(qo, c.indptr, c.last, 8, 2, 128, 128, page_size=page,
+                                         causal=True, kernel=5)
+            o, lse = N.nvfp4kv_e4m3_decode_run(plan, q, c.cache, c.kv_indices)
+            near = N.E4m3Cache(c.cache.k_data.contiguous(), c.cache.v_data.contiguous(),
+                               c.cache.k_scale, c.cache.v_scale)
+            o2, lse2 = N.nvfp4kv_e4m3_decode_run(plan, q, near, c.kv_indices)
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
+            assert N.nvfp4kv_workspace_flags(plan) == 0
+    words = buf.view(torch.bfloat16)
+    x = words.as_strided((7, 3, 64), ((7 << 29) // 7, 64, 1))
+    x.copy_(torch.randn((7, 3, 64), device="cuda"))
+    plan = N.nvfp4kv_rope_plan(64)
+    pos = i32([0, 5, 2, 9, 1000, 7, 3])
+    want, _ = N.nvfp4kv_rope(plan, x.contiguous(), None, pos)
+    N.nvfp4kv_rope(plan, x, None, pos, q_out=x)
+    assert torch.equal(x, want)
+    table = buf.view(torch.int32).as_strided((7, 4), ((7 << 28) // 7, 1))
+    table.fill_(-1)
+    out = N.StepTable.allocate(7, 16, 32)
+    kv, qo = [20, 40, 3, 64, 1, 16, 17], [1, 2, 3, 1, 1, 1, 1]
+    N.nvfp4kv_build_page_table(i32(kv), i32(kv), table, i32(range(90, 120)), None, out)
+    near = torch.full((7, 4), -1, dtype=torch.int32, device="cuda")
+    # (all tokens new: 161 rows do not fit 16)
+    assert out.kv_indices.tolist() == [0] * 32
+    out = N.StepTable.allocate(7, 200, 32)
+    for t in (table, near):
+        N.nvfp4kv_build_page_table(i32(kv), i32(kv), t, i32(range(90, 120)), None, out)
+        N.nvfp4kv_build_page_table(i32(kv), i32(qo), t, i32([]), None, out)
+    assert torch.equal(table, near) and int((near >= 90).sum()) == 14
 
 
 def test_two_streams_with_their_own_workspaces():
