@@ -3,9 +3,11 @@
 // rotary positions and the E4M3 cache (argument validation and dispatch).
 #include "nvfp4kv.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <initializer_list>
 
 #include <cuda_runtime_api.h>
 
@@ -43,6 +45,25 @@ bool bad_row_strides(const void* p, int64_t st, int64_t sh) {
   return !aligned(p, 16) || st % 8 || sh % 8 || st < 0 || sh < 0;
 }
 
+// Whether runs of `run` units at all multiples 0 .. count - 1 of the strides lie
+// apart: in order of their strides, each step passes all that lies below it.
+struct Span {
+  int64_t count, stride;
+};
+bool lie_apart(int64_t run, std::initializer_list<Span> spans) {
+  Span by[3];
+  int n = 0;
+  for (const Span& s : spans)
+    if (s.count > 1) by[n++] = s;
+  std::sort(by, by + n, [](const Span& a, const Span& b) { return a.stride < b.stride; });
+  __int128 extent = run;
+  for (int i = 0; i < n; ++i) {
+    if (by[i].stride < extent) return false;
+    extent += static_cast<__int128>(by[i].count - 1) * by[i].stride;
+  }
+  return true;
+}
+
 int check_e4m3_cache(const nvfp4kv_e4m3_cache* c) {
   if (!c) return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "cache is null");
   if (!c->k_data || !c->v_data || !c->k_scale || !c->v_scale)
@@ -66,16 +87,15 @@ int check_e4m3_cache(const nvfp4kv_e4m3_cache* c) {
       if (data[kv][i] < 0 || data[kv][i] % 16)
         return fail(NVFP4KV_ERR_INVALID_ARGUMENT,
                     "data strides must be non-negative multiples of 16 bytes");
-    // a row must not reach into the next slot or head
-    if ((c->page_size > 1 && data[kv][1] < dims[kv]) ||
-        (c->num_kv_heads > 1 && data[kv][2] < dims[kv]) ||
-        (c->num_pages > 1 && data[kv][0] < dims[kv]))
-      return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "cache strides overlap a row");
+    if (!lie_apart(dims[kv], {{c->num_pages, data[kv][0]},
+                              {c->page_size, data[kv][1]},
+                              {c->num_kv_heads, data[kv][2]}}))
+      return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "cache strides make rows overlap");
     for (int i = 0; i < 2; ++i)
       if (scale[kv][i] < 0 || scale[kv][i] % 4)
         return fail(NVFP4KV_ERR_INVALID_ARGUMENT,
                     "scale strides must be non-negative multiples of 4 bytes");
-    if ((c->num_pages > 1 && scale[kv][0] == 0) || (c->num_kv_heads > 1 && scale[kv][1] == 0))
+    if (!lie_apart(4, {{c->num_pages, scale[kv][0]}, {c->num_kv_heads, scale[kv][1]}}))
       return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "scale strides overlap");
   }
   if (!aligned(c->k_data, 16) || !aligned(c->v_data, 16) || !aligned(c->k_scale, 4) ||
@@ -204,12 +224,11 @@ int nvfp4kv_rope(const void* q, int64_t q_stride_tok, int64_t q_stride_head, voi
     return fail(NVFP4KV_ERR_INVALID_ARGUMENT,
                 "rows must be 16-byte aligned with strides multiple of 8 elements");
   // outputs hold every row apart; in place means the same rows
-  auto overlap = [&](int64_t st, int64_t sh, int heads) {
-    return (heads > 1 && sh < head_dim) || (num_tokens > 1 && st < head_dim);
-  };
-  if ((num_qo_heads > 0 && overlap(q_out_stride_tok, q_out_stride_head, num_qo_heads)) ||
-      (num_kv_heads > 0 && overlap(k_out_stride_tok, k_out_stride_head, num_kv_heads)))
-    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "output strides overlap a row");
+  if ((num_qo_heads > 0 && !lie_apart(head_dim, {{num_tokens, q_out_stride_tok},
+                                                 {num_qo_heads, q_out_stride_head}})) ||
+      (num_kv_heads > 0 && !lie_apart(head_dim, {{num_tokens, k_out_stride_tok},
+                                                 {num_kv_heads, k_out_stride_head}})))
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "output strides make rows overlap");
   if ((num_qo_heads > 0 && q == q_out &&
        (q_stride_tok != q_out_stride_tok || q_stride_head != q_out_stride_head)) ||
       (num_kv_heads > 0 && k == k_out &&

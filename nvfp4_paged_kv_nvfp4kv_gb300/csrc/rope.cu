@@ -215,8 +215,8 @@ cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
   const int cols = rope_columns(p);
   const int side = odd || cols >= 32 ? 1 : 32 / cols;
   const int most = (heads + side - 1) / side;
-  int splits = (152 * kWarps * 2 + p.num_tokens - 1) / p.num_tokens;
-  if (splits > most) splits = most;
+  const int64_t want = ((int64_t)152 * kWarps * 2 + p.num_tokens - 1) / p.num_tokens;
+  const int splits = want < most ? static_cast<int>(want) : most;
   const int64_t units = static_cast<int64_t>(p.num_tokens) * splits;
   const unsigned blocks = static_cast<unsigned>((units + kWarps - 1) / kWarps);
   if (odd)

@@ -231,7 +231,8 @@ class E4m3Cache:
     """A paged cache of E4M3 codes: ``k_data`` [pages, Hkv, page_size, Dk] and
     ``v_data`` [pages, Hkv, page_size, Dv] (uint8 or float8_e4m3fn, any strides
     with contiguous rows, so a transposed view gives the [page, slot, head]
-    layout) and float32 scales ``k_scale``, ``v_scale`` [pages, Hkv]."""
+    layout) and float32 scales ``k_scale``, ``v_scale`` [pages, Hkv].  The
+    tensors are those of its making: for others make another cache."""
 
     def __init__(self, k_data, v_data, k_scale, v_scale):
         pages, heads, page_size = k_data.shape[:3]
@@ -315,6 +316,7 @@ class _Run:
         self.rows, self.heads = i.total_qo_rows, i.num_qo_heads
         self.dk, self.dv, self.pages = i.head_dim_qk, i.head_dim_vo, i.total_kv_pages
         self.dtype = torch.float16 if i.out_dtype == 1 else torch.bfloat16
+        self.of = plan.workspace
         self.workspace, self.nbytes = plan.workspace.data_ptr(), plan.workspace.numel()
         self.device = plan.workspace.get_device()
         self.info = C.byref(i)
@@ -326,7 +328,7 @@ def nvfp4kv_e4m3_decode_run(plan: Plan, q: torch.Tensor, cache: E4m3Cache, kv_in
     """Attention over an E4M3 cache with a plan made with ``kernel=5``: returns
     (out [rows, Hq, Dv], lse [rows, Hq])."""
     r = plan.__dict__.get("_e4m3_run")
-    if r is None:
+    if r is None or r.of is not plan.workspace:
         r = plan._e4m3_run = _Run(plan)
     code = _DTYPE.get(q.dtype)
     if code is None:

@@ -132,7 +132,8 @@ def rope_status(**over):
     (dict(qo=None), INVALID), (dict(k=None), INVALID), (dict(ko=None), INVALID),
     (dict(pos=None), INVALID), (dict(freq=None), INVALID), (dict(freq=BUF + 4), INVALID),
     (dict(q=BUF + 8), INVALID), (dict(qst=260), INVALID), (dict(kosh=-128), INVALID),
-    (dict(qosh=64), INVALID), (dict(n=2, kost=64), INVALID),
+    (dict(qosh=64), INVALID), (dict(n=2, kost=64), INVALID), (dict(n=2, qost=128), INVALID),
+    (dict(n=3, kost=128, kosh=256), INVALID),
     (dict(qo=BUF, qost=512), INVALID)])
 def test_rope_refuses(over, status):
     assert rope_status(**over) == status
@@ -178,6 +179,8 @@ BAD_CACHES = [
     (dict(k_stride_slot=136), INVALID), (dict(v_stride_head=-16), INVALID),
     (dict(k_stride_slot=64), INVALID), (dict(v_stride_page=0), INVALID),
     (dict(k_scale_stride_page=6), INVALID), (dict(v_scale_stride_head=0), INVALID),
+    (dict(k_stride_page=256), INVALID), (dict(v_stride_head=128), INVALID),
+    (dict(k_scale_stride_page=4), INVALID),
     (dict(k_scale_stride_page=0), INVALID), (dict(k_data=BUF + 8), INVALID),
     (dict(v_scale=BUF + 2), INVALID)]
 
