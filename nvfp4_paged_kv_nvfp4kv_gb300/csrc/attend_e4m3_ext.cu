@@ -35,6 +35,12 @@
 //    beat few warps with many (8 warps of 32 rows 258, 16 of 16 rows 236 us).
 // The running maximum is raised only when a value exceeds 2^8.  Every wait is
 // bounded; one that runs out sets flag 0x4 and the CTA winds down.
+//
+// Measured: 32 requests of 2000-16000 tokens, 16 new rows of 32 heads each (64
+// rows to a kv head), 192 us, 3.2 TB/s, 0.48 of a plain copy.  The softmax warps'
+// instructions bound it (16 warps x about 390 a tile of 128 tokens, three quarters
+// of the issue slots), then the units' fixed 8 us and their sizes (139 tiles on
+// the busiest SM, 119 on the mean one).
 #include <climits>
 #include <cmath>
 #include <cstdint>

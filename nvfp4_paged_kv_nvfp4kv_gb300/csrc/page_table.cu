@@ -19,6 +19,10 @@
 // request of four neighbouring entries by one binary search.
 // Whether the batch fits is known to every CTA after the sums, so a batch that
 // does not fit writes nothing but the flag.
+// Measured: 64 requests, one token each, 8.2 us replayed (lengths, sums, searches,
+// ids and their stores one after another, 6 us of it the launch itself); 1000
+// requests with 4.1 million pages 18.5 us, 2.0 TB/s: the same chain, then 13
+// thousand page ids a CTA in three or four rounds of loads.
 #include <cstdint>
 
 #include <cuda_runtime.h>

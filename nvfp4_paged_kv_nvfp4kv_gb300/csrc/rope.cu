@@ -15,7 +15,10 @@
 // R/2 sines and cosines once (into shared memory), and every lane then keeps
 // the eight pairs of its column in registers and walks the heads, so the
 // angles cost a few percent of a 40-head token.  With few tokens the heads are
-// spread over several warps.
+// spread over several warps.  Measured (replayed, three sets of tensors in turn):
+// 16384 tokens x 40 heads of 128, bf16, 64 us, 5.25 TB/s (0.79 of a plain copy);
+// 8191 x 18 heads of 256, a quarter rotating, f16, 34.6 us, 4.36 TB/s; 16 tokens
+// 6.2 us, a launch and its dependent loads.
 #include <cstdint>
 
 #include <cuda_bf16.h>
