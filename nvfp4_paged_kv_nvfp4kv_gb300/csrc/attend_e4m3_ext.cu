@@ -157,28 +157,35 @@ struct Ext {
   static constexpr int NQ = 3;                     // query pieces (2 used for bf16)
   static constexpr int KB = kTileTok * DK, VB = kTileTok * DV;
   static constexpr int QB = N * DK;                // one query piece
-  // P^T: a token's row of kPieces * N weight pieces, as rows of 128 bytes (three
-  // pieces of 32 rows; two of 64) and, at N = 64, rows of 64 bytes (the third)
-  static constexpr int PN = kPieces * N, PN0 = PN <= 128 ? PN : 128, PN1 = PN - PN0;
-  static constexpr int P1_OFF = kTileTok * 128;
-  static constexpr int PB = P1_OFF + kTileTok * PN1;
-  static_assert(PN1 == 0 || PN1 == 64, "the second rows");
+  // P^T: a token's kPieces * N weight pieces, one product's N: at N = 32 a row of
+  // 128 bytes a token, at N = 64 a block of 64-byte rows for each piece
+  static constexpr int PN = kPieces * N;
+  static constexpr int PROW = PN <= 128 ? 128 : 64;
+  static constexpr int PBLK = kTileTok * PROW;
+  static constexpr int PB = PROW == 128 ? PBLK : kPieces * PBLK;
+  static_assert(PROW == 128 || N == 64, "a piece fills a 64-byte row");
   static constexpr int SCB = kTileTok * 12;        // K scale, log2 and inverse of the V scale
   static constexpr int MISC = 4608;
-  static constexpr int FIXED = 2 * PB + NQ * QB + 8 * SCB + MISC + 1024;
+  static constexpr int NPB = 2;                    // P^T buffers
+  // Tests of a barrier before a loader or issuer suspends: with 8 softmax warps
+  // there is room for more (1: 96, 16: 89 us, 4 requests of 32771 tokens x 32
+  // rows), with 16 the tests take their issue slots (1: 184, 16: 189 us, 32 of
+  // 2000-16000 x 64).
+  static constexpr int SPINS = SW > 8 ? 1 : 16;
   // Rings: a K tile is done with after its S^T, a V tile after its P^T V, about
   // three tiles later, so V gets the more stages; S^T tiles in tensor memory
   // and, behind both, the tokens' scales (read from a K tile's copy until the
   // softmax has passed it: KR + SB tiles at most).
-  static constexpr int FIT = (232448 - FIXED) / 16384;  // 16 KB blocks that fit
-  static constexpr int KR = DK == 128 ? 3 : DV == 128 ? 3 : 2;
-  static constexpr int VR = DK == 128 ? 5 : DV == 128 ? 3 : 2;
   static constexpr int SB = 4, SR = 8;
+  static constexpr int FIXED = NPB * PB + NQ * QB + SR * SCB + MISC + 1024;
+  static constexpr int FIT = (232448 - FIXED) / 16384;  // 16 KB blocks that fit
+  static constexpr int KR = DK == 128 ? 4 : DV == 128 ? 3 : 2;
+  static constexpr int VR = DK == 128 ? 4 : DV == 128 ? 3 : 2;
   static_assert(KR * (DK / 128) + VR * (DV / 128) <= FIT && KR + SB <= SR, "rings");
   static constexpr int OFF_K = 0;
   static constexpr int OFF_V = OFF_K + KR * KB;
   static constexpr int OFF_P = OFF_V + VR * VB;
-  static constexpr int OFF_Q = OFF_P + 2 * PB;
+  static constexpr int OFF_Q = OFF_P + NPB * PB;
   static constexpr int OFF_SC = OFF_Q + NQ * QB;
   static constexpr int OFF_MISC = OFF_SC + SR * SCB;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;  // + alignment slack
@@ -186,11 +193,11 @@ struct Ext {
   static constexpr int COLS = OCOL + (DV / 128) * PN;
   static constexpr int TCOLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static constexpr uint32_t IDESC_QK = idesc_f16(128, N, 0, 0);
-  static constexpr uint32_t IDESC_PV = idesc_f16(128, PN0, 1, 1);
+  static constexpr uint32_t IDESC_PV = idesc_f16(128, PN, 1, 1);
   static_assert(DK % 128 == 0 && DV % 128 == 0, "operand rows of 128 bytes");
   static_assert(OFF_P % 1024 == 0 && OFF_Q % 1024 == 0 && OFF_MISC % 16 == 0, "align");
-  static_assert(SMEM <= 232448 && COLS <= 512 && PN0 % 16 == 0, "resources");
-  static_assert(36 * 8 + 16 + (7 * N + 2 * N + 4 + 4 * N + DV) * 4 <= MISC, "misc");
+  static_assert(SMEM <= 232448 && COLS <= 512 && PN % 16 == 0 && PN <= 256, "resources");
+  static_assert(60 * 8 + 16 + (7 * N + 2 * N + 4 + 4 * N + DV + 4) * 4 <= MISC, "misc");
 };
 
 // A V tile that some row of the block does not see whole (run by a warp): rows
@@ -223,12 +230,23 @@ __device__ __forceinline__ void no_nan(uint8_t* tile, int live, int tok0, int* f
   }
 }
 
+// wait_bar for a barrier that mostly is ready, or soon will be: tested SPINS times
+// first, as the suspending wait takes about 300 cycles even when it is
+template <int SPINS>
+__device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          uint32_t* flags) {
+#pragma unroll 1
+  for (int k = 0; k < SPINS; ++k)
+    if (mbar_test_wait(bar, parity)) return true;
+  return wait_bar(bar, parity, abort, flags);
+}
+
 // P1: 1-token pages
 template <int DK, int DV, int N, bool P1>
 __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     attend_e4m3_ext_kernel(const AttendParams p) {
   using T = Ext<DK, DV, N>;
-  constexpr int NH = T::NH, KR = T::KR, VR = T::VR, SB = T::SB, SR = T::SR;
+  constexpr int NH = T::NH, KR = T::KR, VR = T::VR, SB = T::SB, SR = T::SR, NPB = T::NPB;
   constexpr int SW = T::SW, ST = 32 * SW;
   extern __shared__ uint8_t smem_raw[];
   // aligned by an offset, not through an integer: the compiler then still knows
@@ -242,17 +260,17 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
   float* sSc = reinterpret_cast<float*>(smem + T::OFF_SC);  // [SR][3][128]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::OFF_MISC);
   uint64_t* k_landed = bars;       // [KR] a K tile and its scales are in
-  uint64_t* k_empty = bars + 4;    // [KR] S^T done
-  uint64_t* v_landed = bars + 8;   // [VR] a V tile is in
-  uint64_t* v_empty = bars + 14;   // [VR] P^T V done
-  uint64_t* s_full = bars + 20;    // [SB] S^T done, scales in order -> softmax
-  uint64_t* s_empty = bars + 24;   // [SB] S^T read
-  uint64_t* p_full = bars + 28;    // [2] softmax -> O^T issue
-  uint64_t* pv_done = bars + 30;   // [2] P^T V done -> softmax
-  uint64_t* q_full = bars + 32;    // Q ready -> S^T issue
-  uint64_t* v_clean = bars + 35;   // the V tiles from first_part on hold no NaN code
-  uint64_t* fin = bars + 33;       // [2] wind-down of the two issuers' products
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 36);
+  uint64_t* k_empty = bars + 8;    // [KR] S^T done, scales read
+  uint64_t* v_landed = bars + 16;  // [VR] a V tile is in
+  uint64_t* v_empty = bars + 24;   // [VR] P^T V done
+  uint64_t* s_full = bars + 32;    // [SB] S^T done, scales in order -> softmax
+  uint64_t* s_empty = bars + 40;   // [SB] S^T read
+  uint64_t* p_full = bars + 48;    // [NPB] softmax -> O^T issue
+  uint64_t* pv_done = bars + 52;   // [NPB] P^T V done -> softmax
+  uint64_t* q_full = bars + 56;    // Q ready -> S^T issue
+  uint64_t* v_clean = bars + 57;   // the V tiles from first_part on hold no NaN code
+  uint64_t* fin = bars + 58;       // [2] wind-down of the two issuers' products
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 60);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   // per query row: score factor, -m, raise threshold, causal limit
   float* s_f = reinterpret_cast<float*>(s_tmem + 4);
@@ -265,31 +283,28 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
   float* s_fin = s_corr + N;                         // [2N + 4]
   float* s_l = s_fin + 2 * N + 4;                    // [4][N] row sums of the lane quarters
   int* s_nan = reinterpret_cast<int*>(s_l + 4 * N);  // [DV] first NaN token taken out of V
+  int* s_tok = s_nan + DV;                           // tok_begin, tok_end of the unit
 
-  const WorkUnit u = load_unit(p);
   const int G = p.group;
-  const int R = G * u.qo_len;
   const int row0 = blockIdx.y * N;
-  if (row0 >= R) return;  // uniform: before any barrier or tensor memory use
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int q4 = warp & 3;       // tensor-memory lane quarter
   const int j = 32 * q4 + lane;  // token of the tile / value dim
   const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
-  const int unit_tok = (P1 ? 1 : kPageSize) * u.num_pages;
-  // tokens of the unit that some row of the block sees
-  int tok_end = min(u.kv_len, u.tok_begin + unit_tok);
+  const int nq = p.q_f16 ? 3 : 2;
+  const WorkUnit u = load_unit(p);
+  const int R = G * u.qo_len;
+  if (row0 >= R) return;  // uniform: before any barrier or tensor memory use
+  // the unit's tokens in the cache, those that some row of the block sees, their
+  // tiles; the last token that every row sees, the first tile that holds a later one
+  const int unit_end = min(u.kv_len - u.tok_begin, (P1 ? 1 : kPageSize) * u.num_pages);
+  int tok_end = u.tok_begin + unit_end, all_see = u.kv_len - 1;
   if (p.causal) {
-    const int last = min(R, row0 + N) - 1;
-    tok_end = min(tok_end, u.kv_len - u.qo_len + last / G + 1);
+    tok_end = min(tok_end, u.kv_len - u.qo_len + (min(R, row0 + N) - 1) / G + 1);
+    all_see = u.kv_len - u.qo_len + row0 / G;
   }
   const int ntiles = max(0, (tok_end - u.tok_begin + kTileTok - 1) / kTileTok);
-  const int nq = p.q_f16 ? 3 : 2;
-  // the last token that every row of the block sees
-  auto all_see = [&] { return p.causal ? u.kv_len - u.qo_len + row0 / G : u.kv_len - 1; };
-  // tokens of the unit in the cache; the first tile not all of whose tokens every
-  // row of the block sees
-  const int unit_end = min(u.kv_len - u.tok_begin, unit_tok);
-  const int first_part = max(min(all_see() + 1 - u.tok_begin, unit_end), 0) / kTileTok;
+  const int first_part = max(min(all_see + 1 - u.tok_begin, unit_end), 0) / kTileTok;
 
   if (tid == 0) {
     for (int b = 0; b < KR; ++b) {
@@ -306,6 +321,8 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&fin[b], 1);
+    }
+    for (int b = 0; b < T::NPB; ++b) {
       mbar_init(&p_full[b], SW);
       mbar_init(&pv_done[b], 1);
     }
@@ -327,25 +344,18 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     // ================= loaders: warp SW K tiles and scales, SW + 1 V tiles =====
     const CacheView& c = p.cache;
     const bool isv = warp > SW;
-    const uint8_t* base = isv ? c.v_data + (int64_t)u.h_kv * c.v_sh
-                              : c.k_data + (int64_t)u.h_kv * c.k_sh;
     const int64_t sp = isv ? c.v_sp : c.k_sp, ss = isv ? c.v_ss : c.k_ss;
-    const uint8_t* ksb = c.k_sf + (int64_t)u.h_kv * c.ksf_sh;
-    const uint8_t* vsb = c.v_sf + (int64_t)u.h_kv * c.vsf_sh;
-    // pages of this lane's rows 32 g + lane of tile t; a row past the unit's
-    // pages takes the last one (its K row is masked, its V row zeroed)
+    // page ids of this lane's rows 32 g + lane of tile t, a tile ahead of their
+    // use (where they are checked: a check here would wait for them); a row past
+    // the unit's pages takes the last one (its K row is masked, its V row zeroed)
     auto load_pids = [&](int t, int32_t (&pid)[4]) {
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         pid[g] = 0;
         if (t >= ntiles) continue;
         const int rel = t * kTileTok + 32 * g + lane;
-        const int32_t id =
-            __ldg(p.kv_indices + u.page_begin + min(P1 ? rel : rel / kPageSize, u.num_pages - 1));
-        if (id < 0 || id >= c.num_pages)
-          atomicOr(p.flags, 0x1u);
-        else
-          pid[g] = id;
+        pid[g] = __ldg(p.kv_indices + u.page_begin +
+                       min(P1 ? rel : rel / kPageSize, u.num_pages - 1));
       }
     };
     // 8 lanes copy 128 bytes of a row, 4 rows an instruction: 16 rows (a page
@@ -377,18 +387,30 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     const uint32_t s0 = smem_addr(isv ? sV : sK);
     uint64_t* empty = isv ? v_empty : k_empty;
     uint64_t* landed = isv ? v_landed : k_landed;
+    bool alive = true;
+    const int h = u.h_kv;
+    const uint8_t* base = isv ? c.v_data + (int64_t)h * c.v_sh : c.k_data + (int64_t)h * c.k_sh;
+    const uint8_t* ksb = c.k_sf + (int64_t)h * c.ksf_sh;
+    const uint8_t* vsb = c.v_sf + (int64_t)h * c.vsf_sh;
     int32_t next[4];
     load_pids(0, next);
+    // tile t goes to stage st for the round-th time
     for (int t = 0, st = 0, round = 0; t < ntiles; ++t) {
       if (round > 0) {
-        bool ok = true;
-        if (lane == 0) ok = wait_bar(&empty[st], (round - 1) & 1, s_abort, p.flags);
-        if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+        if (lane == 0) alive = wait_soon<T::SPINS>(&empty[st], (round - 1) & 1, s_abort, p.flags);
+        alive = __shfl_sync(0xffffffffu, alive, 0);
+        if (!alive) break;
         tc_fence_after();
       }
       int32_t pid[4];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) pid[g] = next[g];
+      for (int g = 0; g < 4; ++g) {
+        pid[g] = next[g];
+        if (pid[g] < 0 || pid[g] >= c.num_pages) {
+          atomicOr(p.flags, 0x1u);
+          pid[g] = 0;
+        }
+      }
       load_pids(t + 1, next);
 #pragma unroll 1
       for (int b = 0; b < blocks; ++b)
@@ -412,17 +434,20 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     cp_async_commit();
     cp_async_wait<0>();
   } else if (warp == SW + kLoaders) {
-    // ======== S^T issue: one thread the products, then the warp the scales ====
+    // ======== S^T issue: one thread the products ==============================
     const uint64_t kd0 = smem_desc(smem_addr(sK), 16, 1024, kSwz128);
     const uint64_t qd0 = smem_desc(smem_addr(sQ), 16, 1024, kSwz128);
-    for (int k = 0, st = 0, round = 0; k < ntiles; ++k) {
-      bool ok = true;
+    bool ok = true;
+    if (lane == 0) ok = wait_soon<T::SPINS>(q_full, 0, s_abort, p.flags);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    for (int k = 0, st = 0, round = 0; k < ntiles && ok; ++k) {
       if (lane == 0) {
-        ok = wait_bar(&k_landed[st], round & 1, s_abort, p.flags);
-        if (ok && k == 0) ok = wait_bar(q_full, 0, s_abort, p.flags);
-        if (ok && k >= SB) ok = wait_bar(&s_empty[k % SB], (k / SB - 1) & 1, s_abort, p.flags);
+        ok = wait_soon<T::SPINS>(&k_landed[st], round & 1, s_abort, p.flags);
+        if (ok && k >= SB)
+          ok = wait_soon<T::SPINS>(&s_empty[k % SB], (k / SB - 1) & 1, s_abort, p.flags);
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
       fence_async_smem();
       if (lane == 0) {
         tc_fence_after();
@@ -434,24 +459,10 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
             umma8_ss(d, kd + (((kk >> 2) * (kTileTok * 128) + (kk & 3) * 32) >> 4),
                      qd0 + ((q * T::QB + (kk >> 2) * (N * 128) + (kk & 3) * 32) >> 4),
                      T::IDESC_QK, (q > 0 || kk > 0) ? 1u : 0u);
+        mbar_arrive(&s_full[k % SB]);  // (the scales landed with K)
         umma_commit(&s_full[k % SB]);
         umma_commit(&k_empty[st]);
       }
-      // the tokens' scales as the softmax threads use them
-      float* sc = sSc + (k % SR) * (T::SCB / 4) + lane;
-#pragma unroll
-      for (int part = 0; part < 4; ++part, sc += 32) {
-        const float ks = sc[0], vs = sc[kTileTok];
-        const float ksc = fminf(fmaxf(ks, kMinScale), kMaxScale);
-        const float vsc = fminf(fmaxf(vs, kMinScale), kMaxScale);
-        if (ksc != ks || vsc != vs) atomicOr(p.flags, 0x20u);
-        const float lv = log2_scale(vsc);
-        sc[0] = ksc;
-        sc[kTileTok] = lv;
-        sc[2 * kTileTok] = ex2(-lv);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_full[k % SB]);
       if (++st == KR) {
         st = 0;
         ++round;
@@ -465,13 +476,12 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     static_assert(N <= 64 && VR >= 2, "both tiles fit the ring while O^T waits for v_clean");
     for (int d = lane; d < DV; d += 32) s_nan[d] = INT_MAX;
     __syncwarp();
-    bool ok = true;
     for (int t = first_part; t < ntiles && ok; ++t) {
-      if (lane == 0) ok = wait_bar(&v_landed[t % VR], (t / VR) & 1, s_abort, p.flags);
+      if (lane == 0) ok = wait_soon<T::SPINS>(&v_landed[t % VR], (t / VR) & 1, s_abort, p.flags);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (ok)
-        no_nan<DV>(sV + (t % VR) * T::VB, unit_end - t * kTileTok, u.tok_begin + t * kTileTok,
-                   s_nan);
+        no_nan<DV>(sV + (t % VR) * T::VB, unit_end - t * kTileTok,
+                   u.tok_begin + t * kTileTok, s_nan);
     }
     fence_async_smem();
     __syncwarp();
@@ -485,40 +495,39 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
   } else if (warp == SW + kLoaders + 1) {
     // ======== O^T issue: one thread the products ==============================
     const uint64_t vd0 = smem_desc(smem_addr(sV), kTileTok * 128, 1024, kSwz128);
-    const uint64_t pd0 = smem_desc(smem_addr(sP), T::PB, 1024, kSwz128);
-    const uint64_t pd1 = smem_desc(smem_addr(sP) + T::P1_OFF, T::PB, 512, kSwz64);
+    const uint64_t pd0 = smem_desc(smem_addr(sP), T::PBLK, 8 * T::PROW,
+                                   T::PROW == 128 ? kSwz128 : kSwz64);
+    bool ok = true;
     for (int i = 0, st = 0, round = 0; i < ntiles; ++i) {
-      bool ok = true;
       if (lane == 0) {
-        ok = wait_bar(&v_landed[st], round & 1, s_abort, p.flags);
-        if (ok && i >= first_part) ok = wait_bar(v_clean, 0, s_abort, p.flags);
+        ok = wait_soon<T::SPINS>(&v_landed[st], round & 1, s_abort, p.flags);
+        if (ok && i >= first_part) ok = wait_soon<T::SPINS>(v_clean, 0, s_abort, p.flags);
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
       fence_async_smem();
       __syncwarp();
       if (lane == 0) {
-        ok = wait_bar(&p_full[i & 1], (i >> 1) & 1, s_abort, p.flags);
+        ok = wait_soon<T::SPINS>(&p_full[i % NPB], (i / NPB) & 1, s_abort, p.flags);
         if (ok) {
           tc_fence_after();
           const uint64_t vd = vd0 + ((st * T::VB) >> 4);
-          const uint64_t buf = ((i & 1) * T::PB) >> 4;
+          const uint64_t buf = ((i % NPB) * T::PB) >> 4;
 #pragma unroll
           for (int b = 0; b < DV / 128; ++b)
 #pragma unroll
             for (int k = 0; k < kTileTok / 32; ++k) {
               const uint64_t vk = vd + ((b * (kTileTok * 128) + k * 32 * 128) >> 4);
               const uint32_t acc = (i > 0 || k > 0) ? 1u : 0u;
-              umma8_ss(tmem + T::OCOL + b * T::PN, vk, pd0 + buf + ((k * 32 * 128) >> 4),
+              umma8_ss(tmem + T::OCOL + b * T::PN, vk, pd0 + buf + ((k * 32 * T::PROW) >> 4),
                        T::IDESC_PV, acc);
-              if constexpr (T::PN1 > 0)
-                umma8_ss(tmem + T::OCOL + b * T::PN + T::PN0, vk,
-                         pd1 + buf + ((k * 32 * 64) >> 4), idesc_f16(128, T::PN1, 1, 1), acc);
             }
-          umma_commit(&pv_done[i & 1]);
+          umma_commit(&pv_done[i % NPB]);
           umma_commit(&v_empty[st]);
         }
       }
-      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) break;
       if (++st == VR) {
         st = 0;
         ++round;
@@ -594,16 +603,22 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
         s_m[r] = -INFINITY;
       }
     }
+    if (tid == 0) {
+      s_tok[0] = u.tok_begin;
+      s_tok[1] = tok_end;
+    }
     fence_async_smem();
     named_sync(kAllSoftmax, ST);
     if (lane == 0) mbar_arrive(q_full);
-    const int min_lim = all_see();
+    // the first tile with a token that some row does not see
+    const int part = (min(all_see + 1, tok_end) - u.tok_begin) >> 7;
+    static_assert(kTileTok == 128, "the shift");
     const int nvalid = min(N, R - row0);  // columns that are real query rows
     const bool active = c0 < nvalid;      // warp-uniform
 
     const int gbar = 1 + (warp >> 2), gtid = tid & 127;
     auto warp_wait = [&](uint64_t* bar, uint32_t parity) {  // (every lane: no hand-over)
-      if (!mbar_test_wait(bar, parity)) wait_bar(bar, parity, s_abort, p.flags);
+      wait_soon<1>(bar, parity, s_abort, p.flags);
       __syncwarp();
     };
     // The column groups (four warps each, the tile's 128 tokens) are
@@ -617,8 +632,8 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     uint32_t p_at[kPieces];
 #pragma unroll
     for (int q = 0; q < kPieces; ++q)
-      p_at[q] = q * N < T::PN0 ? swz<3>((uint32_t)j * 128 + q * N + c0)
-                               : T::P1_OFF + swz<2>((uint32_t)j * 64 + q * N - T::PN0 + c0);
+      p_at[q] = T::PROW == 128 ? swz<3>((uint32_t)j * 128 + q * N + c0)
+                               : q * T::PBLK + swz<2>((uint32_t)j * 64 + c0);
     uint64_t lsum[NH / 2];  // this token's share of the row sums, two rows each
 #pragma unroll
     for (int e = 0; e < NH / 2; ++e) lsum[e] = 0;
@@ -626,9 +641,12 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     // of the token's V scale, -inf where masked or past the unit's end; iv2: the
     // inverse of that scale, twice
     auto scores = [&](int i, float (&x)[NH], uint64_t& iv2) {
-      const int tile_tok0 = u.tok_begin + i * kTileTok, tok = tile_tok0 + j;
       const float* sc = sSc + (i % SR) * (T::SCB / 4) + j;
-      const float ks = sc[0], lv = sc[kTileTok], iv = sc[2 * kTileTok];
+      const float ks0 = sc[0], vs0 = sc[kTileTok];
+      const float ks = fminf(fmaxf(ks0, kMinScale), kMaxScale);
+      const float vs = fminf(fmaxf(vs0, kMinScale), kMaxScale);
+      if (ks != ks0 || vs != vs0) atomicOr(p.flags, 0x20u);
+      const float lv = log2_scale(vs), iv = ex2(-lv);
       const uint64_t ks2 = pack_f32x2(ks, ks), lv2 = pack_f32x2(lv, lv);
       iv2 = pack_f32x2(iv, iv);
       uint32_t sv[NH];
@@ -647,8 +665,9 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
                        x[e4 + 2 * e], x[e4 + 2 * e + 1]);
         }
       }
-      if (tile_tok0 + kTileTok > min(min_lim + 1, tok_end)) {  // (a unit's last tiles)
-        const int past = tok >= tok_end ? INT32_MIN : INT32_MAX;
+      if (i >= part) {  // (a unit's last tiles)
+        const int tok = s_tok[0] + i * kTileTok + j;
+        const int past = tok >= s_tok[1] ? INT32_MIN : INT32_MAX;
 #pragma unroll
         for (int e4 = 0; e4 < NH; e4 += 4) {
           const int4 lm = *reinterpret_cast<const int4*>(s_lim + c0 + e4);
@@ -660,7 +679,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
       }
     };
     for (int i = 0; i < ntiles; ++i) {
-      const int sb = i & 1;
+      const int sb = i % NPB;
       warp_wait(&s_full[i % SB], (i / SB) & 1);
       tc_fence_after();
       float x[NH];
@@ -715,7 +734,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
         const bool rescale = named_or(gbar, 128, moved) && i > 0;
         unset = named_or(gbar, 128, gtid < NH && c0 + gtid < nvalid && s_m[c0 + gtid] == -INFINITY);
         if (rescale && active) {  // O^T columns and row sums *= corr, once PV(i-1) is done
-          warp_wait(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
+          warp_wait(&pv_done[(i - 1) % NPB], ((i - 1) / NPB) & 1);
           tc_fence_after();
 #pragma unroll
           for (int e = 0; e < NH / 2; ++e)
@@ -738,7 +757,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&s_empty[i % SB]);  // this warp has read S^T and the scales
       // ---- weights: the P^T row of this token, in pieces ----------------------
-      if (i >= 2) warp_wait(&pv_done[sb], ((i - 2) >> 1) & 1);  // P buffer sb is free
+      if (i >= NPB) warp_wait(&pv_done[sb], (i / NPB - 1) & 1);  // P buffer sb is free
       if (active) {
         uint32_t h[kPieces][NH / 4];
 #pragma unroll
@@ -791,18 +810,20 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     named_sync(gbar, 128);
 
     // ---- epilogue: O^T row of value dim j, this thread's query rows -----------
-    if (ntiles > 0) warp_wait(&pv_done[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1);
+    // (the unit is read again: kept over the tiles, it would cost them registers)
+    const WorkUnit end = load_unit(p);
+    if (ntiles > 0) warp_wait(&pv_done[(ntiles - 1) % NPB], ((ntiles - 1) / NPB) & 1);
     named_sync(kNanReady, ST + 32);
     {
       tc_fence_after();
       constexpr float kLn2 = 0.69314718055994530942f;
-      const bool partial = p.split && u.num_splits > 1;
+      const bool partial = p.split && end.num_splits > 1;
       const int Hq = p.num_qo_heads;
       if (active) {
         // lane e (mod NH) derives normaliser and output row of column e, once
         const int e_l = lane & (NH - 1), col_l = c0 + e_l;
-        uint16_t* const out_u = p.out + (int64_t)u.qo_begin * Hq * DV;
-        float* const part_u = partial ? p.partial_o + (int64_t)u.partial_base * DV : nullptr;
+        uint16_t* const out_u = p.out + (int64_t)end.qo_begin * Hq * DV;
+        float* const part_u = partial ? p.partial_o + (int64_t)end.partial_base * DV : nullptr;
         float f_l = 0.f;
         int64_t off_l = 0;  // output row of the column, from the unit's first row
         if (col_l < nvalid) {
@@ -811,14 +832,14 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
           const bool any = m != -INFINITY || isnan(L);  // (a NaN score need not raise)
           f_l = any ? 1.f / L : 0.f;
           const float lse_v = any ? (m + log2f(L)) * kLn2 : -INFINITY;
-          const int gr = row0 + col_l, qi = gr / G, head = u.h_kv * G + gr % G;
-          off_l = partial ? ((int64_t)qi * Hq + head) * u.num_splits + u.split
+          const int gr = row0 + col_l, qi = gr / G, head = end.h_kv * G + gr % G;
+          off_l = partial ? ((int64_t)qi * Hq + head) * end.num_splits + end.split
                           : (int64_t)qi * Hq + head;
           if (q4 == 0 && lane < NH) {
             if (!partial) {
-              if (p.lse) p.lse[(int64_t)u.qo_begin * Hq + off_l] = lse_v;
+              if (p.lse) p.lse[(int64_t)end.qo_begin * Hq + off_l] = lse_v;
             } else {
-              p.partial_lse[(int64_t)u.partial_base + off_l] = lse_v;
+              p.partial_lse[(int64_t)end.partial_base + off_l] = lse_v;
             }
           }
         }
@@ -855,7 +876,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
         }
       }
       if (partial)
-        fold_if_last<N, DV, ST, 1, 4>(p, u, row0, nvalid, reinterpret_cast<int*>(s_fin + 2 * N),
+        fold_if_last<N, DV, ST, 1, 4>(p, end, row0, nvalid, reinterpret_cast<int*>(s_fin + 2 * N),
                                       tid, [] { named_sync(kAllSoftmax, ST); });
     }
     tc_fence_before();
