@@ -556,8 +556,8 @@ bool make_e4m3(bool page1, AttendConfig* cfg) {
 bool attend_config_e4m3(int dk, int dv, int page_size, int rows, AttendConfig* cfg) {
   // More than 16 rows: the tensor-memory kernel where it is built, else row
   // blocks that each read the keys again.  Both sides at head dims 128: 16 rows
-  // 28.6 here, 44 us there (16 requests of 512-4096 tokens), 56 and 88 us (4 of
-  // 32771); 32 rows 51.6 and 50.6 us, 105 and 96 us; 64 rows 92 and 64 us.  At
+  // 28.6 here, 39 us there (16 requests of 512-4096 tokens), 56 and 71 us (4 of
+  // 32771); 32 rows 51.6 and 39 us, 105 and 71 us; 64 rows 92 and 51 us.  At
   // 256 / 256: 16 rows 32 and 43 us, 32 rows 66 and 48 us (8 requests).
   if (rows > 16 && attend_config_e4m3_ext(dk, dv, page_size, rows, cfg)) return true;
   const bool p1 = page_size == 1, wide = rows > 8;

@@ -24,9 +24,9 @@
 // query rows (the G heads of the group times the query positions); tiles of
 // 128 tokens; M = 128 tokens (S^T) or 128 value dims (O^T) fill the product
 // for any N.  20 warps at N = 64:
-//  * loaders (a warp for K, one for V): cp.async of a tile's rows straight into
-//    the 128-byte-swizzled operand layout (K: K-major, V: MN-major, both rows
-//    of 128 bytes), any byte strides and both page sizes;
+//  * loaders (a warp for K and the scales, one for V): cp.async of a tile's rows
+//    straight into the 128-byte-swizzled operand layout (K: K-major, V: MN-major,
+//    both rows of 128 bytes), any byte strides and both page sizes;
 //  * issue (two warps, one thread each): S^T = K Q^T into a ring of tiles in
 //    tensor memory, and O^T += V^T P^T, each once its inputs are ready;
 //  * softmax (four warps for each 16 query rows; thread = token of S^T): the
@@ -37,10 +37,12 @@
 // bounded; one that runs out sets flag 0x4 and the CTA winds down.
 //
 // Measured: 32 requests of 2000-16000 tokens, 16 new rows of 32 heads each (64
-// rows to a kv head), 192 us, 3.2 TB/s, 0.48 of a plain copy.  The softmax warps'
-// instructions bound it (16 warps x about 390 a tile of 128 tokens, three quarters
-// of the issue slots), then the units' fixed 8 us and their sizes (139 tiles on
-// the busiest SM, 119 on the mean one).
+// rows to a kv head), 170 us, 3.6 TB/s, 0.54 of a plain copy; 4 requests of 32771
+// tokens x 32 rows 71 us; prompts of 512 rows 82 us.  No unit is full (issue slots
+// 60 %, shared memory 45 %, products a third): a tile's way through the warps
+// bounds it, 1.1 us at either N, and a unit's 12 tiles' worth of start and end.
+// Timed with parts left out: half the query pieces, half of O^T's products, no
+// conversions of weights or no votes change nothing; no loads take 10 % off.
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -172,10 +174,10 @@ struct Ext {
   // rows), with 16 the tests take their issue slots (1: 184, 16: 189 us, 32 of
   // 2000-16000 x 64).
   static constexpr int SPINS = SW > 8 ? 1 : 16;
-  // Rings: a K tile is done with after its S^T, a V tile after its P^T V, about
-  // three tiles later, so V gets the more stages; S^T tiles in tensor memory
-  // and, behind both, the tokens' scales (read from a K tile's copy until the
-  // softmax has passed it: KR + SB tiles at most).
+  // Rings: K tiles until their S^T is done, V tiles until their P^T V is (at 128
+  // dims (3, 5) 181, (4, 4) 176, (5, 3) 184 us, a fifth S^T tile no gain), S^T
+  // tiles in tensor memory and, behind both, the tokens' scales (read from a K
+  // tile's copy until the softmax has passed it: KR + SB tiles at most).
   static constexpr int SB = 4, SR = 8;
   static constexpr int FIXED = NPB * PB + NQ * QB + SR * SCB + MISC + 1024;
   static constexpr int FIT = (232448 - FIXED) / 16384;  // 16 KB blocks that fit
@@ -470,9 +472,8 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     }
     // The V tiles that some row does not see whole, the last one or two (the rows'
     // limits lie less than N <= 64 tokens apart): a weight of 0 must not meet a
-    // NaN code.  Done here, as this warp is up to four tiles ahead: 32 requests of
-    // 2000-16000 tokens x 64 rows take 192 us, 190 without, and 197 with the same
-    // work in the warp that issues O^T.
+    // NaN code.  Done here, as this warp is up to four tiles ahead (1 % of the
+    // launch; in the warp that issues O^T 4 %).
     static_assert(N <= 64 && VR >= 2, "both tiles fit the ring while O^T waits for v_clean");
     for (int d = lane; d < DV; d += 32) s_nan[d] = INT_MAX;
     __syncwarp();
@@ -549,14 +550,21 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     // row's neighbouring DK / 8 threads share its largest |q| by shuffles --------
     constexpr int QW = DK / 8;
     static_assert(N * QW % 32 == 0 && ST % 32 == 0 && QW <= 32, "whole warps of whole rows");
-    for (int ci = tid; ci < N * QW; ci += ST) {
-      const int r = ci / QW, c8 = ci % QW, gr = row0 + r;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    constexpr int QIT = N * QW / ST;
+    uint4 qv[QIT];
+#pragma unroll
+    for (int k = 0; k < QIT; ++k) {
+      const int ci = tid + k * ST, gr = row0 + ci / QW;
+      qv[k] = make_uint4(0u, 0u, 0u, 0u);
       if (gr < R)
-        v = *reinterpret_cast<const uint4*>(p.q + (int64_t)(u.qo_begin + gr / G) * p.q_stride_tok +
-                                            (int64_t)(u.h_kv * G + gr % G) * p.q_stride_head +
-                                            c8 * 8);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        qv[k] = *reinterpret_cast<const uint4*>(
+            p.q + (int64_t)(u.qo_begin + gr / G) * p.q_stride_tok +
+            (int64_t)(u.h_kv * G + gr % G) * p.q_stride_head + ci % QW * 8);
+    }
+#pragma unroll
+    for (int k = 0; k < QIT; ++k) {
+      const int ci = tid + k * ST, r = ci / QW, c8 = ci % QW, gr = row0 + r;
+      const uint32_t w[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
       float2 rest[4];
       float amax = 0.f;
 #pragma unroll
@@ -825,7 +833,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
         uint16_t* const out_u = p.out + (int64_t)end.qo_begin * Hq * DV;
         float* const part_u = partial ? p.partial_o + (int64_t)end.partial_base * DV : nullptr;
         float f_l = 0.f;
-        int64_t off_l = 0;  // output row of the column, from the unit's first row
+        int off_l = 0;  // output row of the column, from the unit's first row
         if (col_l < nvalid) {
           const float L = s_l[col_l] + s_l[N + col_l] + s_l[2 * N + col_l] + s_l[3 * N + col_l];
           const float m = s_m[col_l];
@@ -833,8 +841,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
           f_l = any ? 1.f / L : 0.f;
           const float lse_v = any ? (m + log2f(L)) * kLn2 : -INFINITY;
           const int gr = row0 + col_l, qi = gr / G, head = end.h_kv * G + gr % G;
-          off_l = partial ? ((int64_t)qi * Hq + head) * end.num_splits + end.split
-                          : (int64_t)qi * Hq + head;
+          off_l = partial ? (qi * Hq + head) * end.num_splits + end.split : qi * Hq + head;
           if (q4 == 0 && lane < NH) {
             if (!partial) {
               if (p.lse) p.lse[(int64_t)end.qo_begin * Hq + off_l] = lse_v;
