@@ -556,9 +556,10 @@ bool make_e4m3(bool page1, AttendConfig* cfg) {
 bool attend_config_e4m3(int dk, int dv, int page_size, int rows, AttendConfig* cfg) {
   // More than 16 rows: the tensor-memory kernel where it is built, else row
   // blocks that each read the keys again.  Both sides at head dims 128: 16 rows
-  // 28.6 here, 39 us there (16 requests of 512-4096 tokens), 56 and 71 us (4 of
-  // 32771); 32 rows 51.6 and 39 us, 105 and 71 us; 64 rows 92 and 51 us.  At
-  // 256 / 256: 16 rows 32 and 43 us, 32 rows 66 and 48 us (8 requests).
+  // 27 here, 35 us there (16 requests of 512-4096 tokens), 56 and 66 us (4 of
+  // 32771); 32 rows 51 and 39 us, 104 and 71 us; 64 rows 74 and 51 us.  At
+  // 256 / 256: 16 rows 84 and 78 us, 32 rows 217 and 84 us (8 requests of
+  // 2048-16384 tokens, 8 kv heads), with 2 kv heads 23 and 27, 31 and 35 us.
   if (rows > 16 && attend_config_e4m3_ext(dk, dv, page_size, rows, cfg)) return true;
   const bool p1 = page_size == 1, wide = rows > 8;
   if (dk == 64 && dv == 64)

@@ -16,9 +16,12 @@
 // the eight pairs of its column in registers and walks the heads, so the
 // angles cost a few percent of a 40-head token.  With few tokens the heads are
 // spread over several warps.  Measured (replayed, three sets of tensors in turn):
-// 16384 tokens x 40 heads of 128, bf16, 64 us, 5.25 TB/s (0.79 of a plain copy);
-// 8191 x 18 heads of 256, a quarter rotating, f16, 34.6 us, 4.36 TB/s; 16 tokens
-// 6.2 us, a launch and its dependent loads.
+// 16384 tokens x 40 heads of 128, bf16, 56 us, 6.0 TB/s (0.90 of a plain copy);
+// 8191 x 18 heads of 256, a quarter rotating, f16, 30 us, 5.1 TB/s; 16 tokens
+// 5.5 us, a launch and its dependent loads.  CTAs of one warp (65 and 32 us with
+// two, 72 and 41 with eight: the warps that an SM runs then follow the token
+// order, and the rows they stream stay neighbours), two heads in flight (four: 64
+// and 34), four waves of CTAs at least (one: 58.5 and 31.5, sixteen: 61 and 45).
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -30,9 +33,9 @@
 namespace nvfp4kv {
 namespace {
 
-constexpr int kWarps = 4;
 constexpr int kMaxPairs = 256;  // rotary_dim / 2
-constexpr int kBatch = 4;       // heads whose loads a lane has in flight
+constexpr int kBatch = 2;       // heads whose loads a lane has in flight
+constexpr int kFewest = 152 * 128;  // warps a launch should have: four waves of CTAs
 
 // columns of two 16-byte chunks that make up a head (rope_kernel)
 __host__ __device__ __forceinline__ int rope_columns(const RopeParams& p) {
@@ -95,14 +98,11 @@ __device__ __forceinline__ void angles(const RopeParams& p, int64_t t, float2* s
 // its stores (which might alias them for all the compiler knows), and those of
 // the first batch before the angles.
 template <bool F16, bool INTER>
-__global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeParams p, int splits) {
-  __shared__ __align__(16) float2 s_sc[kWarps][kMaxPairs];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
-  const int64_t t = unit / splits;
-  const int part = static_cast<int>(unit % splits);
-  if (t >= p.num_tokens) return;
-  float2* sc = s_sc[warp];
+__global__ void __launch_bounds__(32) rope_kernel(const RopeParams p, int splits) {
+  __shared__ __align__(16) float2 sc[kMaxPairs];
+  const int lane = threadIdx.x;
+  const int64_t t = blockIdx.x / splits;
+  const int part = static_cast<int>(blockIdx.x % splits);
   const int heads = p.num_qo_heads + p.num_kv_heads;
   const int half = p.rotary_dim / 2;
   const int rcols = INTER ? 0 : half / 8;  // half layout: columns of pairs, then passing ones
@@ -183,14 +183,11 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeParams p, i
 // The half layout where R/2 is not a multiple of 8: its pairs do not lie in
 // 16-byte columns, so single elements are loaded.
 template <bool F16>
-__global__ void __launch_bounds__(kWarps * 32) rope_odd_kernel(const RopeParams p, int splits) {
-  __shared__ __align__(16) float2 s_sc[kWarps][kMaxPairs];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
-  const int64_t t = unit / splits;
-  const int part = static_cast<int>(unit % splits);
-  if (t >= p.num_tokens) return;
-  float2* sc = s_sc[warp];
+__global__ void __launch_bounds__(32) rope_odd_kernel(const RopeParams p, int splits) {
+  __shared__ __align__(16) float2 sc[kMaxPairs];
+  const int lane = threadIdx.x;
+  const int64_t t = blockIdx.x / splits;
+  const int part = static_cast<int>(blockIdx.x % splits);
   angles(p, t, sc, lane);
   const int heads = p.num_qo_heads + p.num_kv_heads, half = p.rotary_dim / 2;
   for (int h = part; h < heads; h += splits) {
@@ -213,23 +210,22 @@ cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
   const int heads = p.num_qo_heads + p.num_kv_heads;
   if (p.num_tokens == 0 || heads == 0) return cudaSuccess;
   const bool odd = !p.interleaved && p.rotary_dim % 16 != 0;
-  // Heads over several warps while the tokens alone leave SMs without one; a
-  // warp has `side` heads side by side (the columns of rope_kernel).
+  // Heads over several warps while the tokens alone are few; a warp has `side`
+  // heads side by side (the columns of rope_kernel).
   const int cols = rope_columns(p);
   const int side = odd || cols >= 32 ? 1 : 32 / cols;
   const int most = (heads + side - 1) / side;
-  const int64_t want = ((int64_t)152 * kWarps * 2 + p.num_tokens - 1) / p.num_tokens;
+  const int64_t want = ((int64_t)kFewest + p.num_tokens - 1) / p.num_tokens;
   const int splits = want < most ? static_cast<int>(want) : most;
-  const int64_t units = static_cast<int64_t>(p.num_tokens) * splits;
-  const unsigned blocks = static_cast<unsigned>((units + kWarps - 1) / kWarps);
+  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(p.num_tokens) * splits);
   if (odd)
-    (p.f16 ? rope_odd_kernel<true> : rope_odd_kernel<false>)<<<blocks, kWarps * 32, 0, stream>>>(
+    (p.f16 ? rope_odd_kernel<true> : rope_odd_kernel<false>)<<<blocks, 32, 0, stream>>>(
         p, splits);
   else if (p.interleaved)
-    (p.f16 ? rope_kernel<true, true> : rope_kernel<false, true>)<<<blocks, kWarps * 32, 0,
+    (p.f16 ? rope_kernel<true, true> : rope_kernel<false, true>)<<<blocks, 32, 0,
                                                                   stream>>>(p, splits);
   else
-    (p.f16 ? rope_kernel<true, false> : rope_kernel<false, false>)<<<blocks, kWarps * 32, 0,
+    (p.f16 ? rope_kernel<true, false> : rope_kernel<false, false>)<<<blocks, 32, 0,
                                                                     stream>>>(p, splits);
   return cudaGetLastError();
 }
