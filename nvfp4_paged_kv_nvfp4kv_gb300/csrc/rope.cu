@@ -180,27 +180,75 @@ __global__ void __launch_bounds__(32) rope_kernel(const RopeParams p, int splits
   }
 }
 
-// The half layout where R/2 is not a multiple of 8: its pairs do not lie in
-// 16-byte columns, so single elements are loaded.
-template <bool F16>
+// The half layout where R/2 is not a multiple of 8: the pairs of a 16-byte column
+// do not lie in another one.  A lane still loads, turns and stores whole columns
+// (CP of them), and takes the other halves of its pairs from shared memory, where
+// the warp lays the heads of a step.  8192 tokens x 48 heads of 128, 66 dims
+// turning: 45 us, 4.5 TB/s (element by element 115 us).
+template <bool F16, int CP>
 __global__ void __launch_bounds__(32) rope_odd_kernel(const RopeParams p, int splits) {
   __shared__ __align__(16) float2 sc[kMaxPairs];
+  __shared__ __align__(16) uint16_t rows[kBatch][256 * CP];
   const int lane = threadIdx.x;
   const int64_t t = blockIdx.x / splits;
   const int part = static_cast<int>(blockIdx.x % splits);
   angles(p, t, sc, lane);
   const int heads = p.num_qo_heads + p.num_kv_heads, half = p.rotary_dim / 2;
-  for (int h = part; h < heads; h += splits) {
-    const Row r = row_of(p, t, h);
-    for (int i = lane; i < half; i += 32) {
-      const float x = one<F16>(r.in[i]), y = one<F16>(r.in[half + i]);
-      const float2 a = sc[i];
-      const uint32_t o = pack2<F16>(x * a.x - y * a.y, y * a.x + x * a.y);
-      r.out[i] = static_cast<uint16_t>(o);
-      r.out[half + i] = static_cast<uint16_t>(o >> 16);
+  const int cols = p.head_dim / 8, wide = min(32, cols), side = 32 / wide, step = splits * side;
+  const int hs = lane / wide, col = lane % wide;  // this lane's head of a step, its column
+  float cs[CP][8], sn[CP][8];  // y = x cs + (the other of the pair) sn
+#pragma unroll
+  for (int c = 0; c < CP; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int d = 8 * (col + 32 * c) + j;
+      const float2 a = d < 2 * half ? sc[d < half ? d : d - half] : make_float2(1.f, 0.f);
+      cs[c][j] = a.x;
+      sn[c][j] = d < half ? -a.y : a.y;
     }
-    if (r.in != r.out)
-      for (int d = p.rotary_dim + lane; d < p.head_dim; d += 32) r.out[d] = r.in[d];
+  for (int b = part * side; b < heads; b += kBatch * step) {  // (the whole warp together)
+    uint4 v[kBatch][CP];
+    auto mine = [&](int k, int c) {
+      return hs < side && b + hs + k * step < heads && col + 32 * c < cols;
+    };
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int c = 0; c < CP; ++c)
+        if (mine(k, c))
+          v[k][c] = reinterpret_cast<const uint4*>(row_of(p, t, b + hs + k * step).in)[col + 32 * c];
+    __syncwarp();  // the last step's rows have been read
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int c = 0; c < CP; ++c)
+        if (mine(k, c))
+          *reinterpret_cast<uint4*>(rows[k] + hs * p.head_dim + 8 * (col + 32 * c)) = v[k][c];
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+      for (int c = 0; c < CP; ++c) {
+        if (!mine(k, c)) continue;
+        const uint16_t* row = rows[k] + hs * p.head_dim;
+        uint32_t w[4] = {v[k][c].x, v[k][c].y, v[k][c].z, v[k][c].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int d = 8 * (col + 32 * c) + 2 * j;
+          const float2 x = unpack2<F16>(w[j]);
+          float y[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int o = d + e < half ? d + e + half : d + e - half;  // the other of the pair
+            const float z = d + e < 2 * half ? one<F16>(row[o]) : 0.f;
+            y[e] = (e ? x.y : x.x) * cs[c][2 * j + e] + z * sn[c][2 * j + e];
+          }
+          // (dims that pass keep their bits; rotary_dim is even)
+          if (d < 2 * half) w[j] = pack2<F16>(y[0], y[1]);
+        }
+        reinterpret_cast<uint4*>(row_of(p, t, b + hs + k * step).out)[col + 32 * c] =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
   }
 }
 
@@ -212,14 +260,17 @@ cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream) {
   const bool odd = !p.interleaved && p.rotary_dim % 16 != 0;
   // Heads over several warps while the tokens alone are few; a warp has `side`
   // heads side by side (the columns of rope_kernel).
-  const int cols = rope_columns(p);
-  const int side = odd || cols >= 32 ? 1 : 32 / cols;
+  const int cols = odd ? p.head_dim / 8 : rope_columns(p);
+  const int side = cols >= 32 ? 1 : 32 / cols;
   const int most = (heads + side - 1) / side;
   const int64_t want = ((int64_t)kFewest + p.num_tokens - 1) / p.num_tokens;
   const int splits = want < most ? static_cast<int>(want) : most;
   const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(p.num_tokens) * splits);
-  if (odd)
-    (p.f16 ? rope_odd_kernel<true> : rope_odd_kernel<false>)<<<blocks, 32, 0, stream>>>(
+  if (odd && cols > 32)
+    (p.f16 ? rope_odd_kernel<true, 2> : rope_odd_kernel<false, 2>)<<<blocks, 32, 0, stream>>>(
+        p, splits);
+  else if (odd)
+    (p.f16 ? rope_odd_kernel<true, 1> : rope_odd_kernel<false, 1>)<<<blocks, 32, 0, stream>>>(
         p, splits);
   else if (p.interleaved)
     (p.f16 ? rope_kernel<true, true> : rope_kernel<false, true>)<<<blocks, 32, 0,
