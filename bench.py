@@ -46,7 +46,7 @@ TRAFFIC = {
                             ("attend_dec.cu", "device_common.cuh", "epilogue.cuh", "internal.h",
                              "quantize.cuh")),
     "prefix_cache_extend": ("attend_tcgen05_prefix_cache_extend.json",
-                            ("attend_tcgen05.cu",) + _COMMON),
+                            ("attend_tcgen05.cu", "tcgen05.cuh") + _COMMON),
 }
 
 
