@@ -21,7 +21,7 @@
 // each is read once, and no other warp touches the block.  The rows' loads do
 // not wait for the page id, which is on its way together with them.  Measured
 // (replayed): 7 prompt chunks, 10.5 thousand tokens of 8 heads x (128 + 128),
-// 17.3 us, 3.6 TB/s: the request list's loads and sums come first (4 us), then
+// 16.6 us, 3.7 TB/s: the request list's loads and sums come first (4 us), then
 // each warp's blocks in turn, a load's latency each; 16 requests of one token
 // 6.2 us, a launch and four dependent loads.
 #include <cstdint>

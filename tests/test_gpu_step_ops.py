@@ -703,6 +703,47 @@ def test_two_streams_with_their_own_workspaces():
                                                                     atol=2.0 ** -7, rtol=2.0 ** -7)
 
 
+@pytest.mark.parametrize("page,new", [(16, (20, 9)), (1, (20, 9)), (16, (300, 1)), (1, (1, 2))])
+def test_append_rope_and_extend_in_a_graph(page, new):
+    """Every form of the kernels that a step of prompts takes, captured once and
+    replayed with other inputs: the same bits as the calls one by one."""
+    c = CacheCase((700, 333), page, 2, 128, 128, seed=page + new[0])
+    plan = N.nvfp4kv_decode_plan([0, new[0], sum(new)], c.indptr, c.last, 8, 2, 128, 128,
+                                 page_size=page, causal=True, kernel=5, force_chunk_tokens=256)
+    assert plan.info.split
+    rope = N.nvfp4kv_rope_plan(128, 66)          # whole columns with halves inside them
+    pos = i32(range(sum(new)))
+    q = torch.zeros((sum(new), 8, 128), dtype=torch.bfloat16, device="cuda")
+    k, v = (torch.zeros((sum(new), 2, 128), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    o = torch.zeros((sum(new), 8, 128), dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((sum(new), 8), device="cuda")
+    flags, qo = new_flags(), i32([0, new[0], sum(new)])
+
+    def step(o, lse):
+        q2, k2 = N.nvfp4kv_rope(rope, q, k, pos)
+        N.nvfp4kv_e4m3_append(c.cache, k2, v, qo, c.kv_indptr, c.kv_indices, c.last_page_len, flags)
+        N.nvfp4kv_e4m3_decode_run(plan, q2, c.cache, c.kv_indices, out=o, lse=lse)
+    step(o, lse)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        step(o, lse)
+    g = torch.Generator().manual_seed(3)
+    for _ in range(3):
+        for t in (q, k, v):
+            t.copy_(torch.randn(t.shape, generator=g).to(torch.bfloat16))
+        c.upload()
+        graph.replay()
+        torch.cuda.synchronize()
+        codes, scales = c.cache.k_data.clone(), c.cache.v_scale.clone()
+        o2, lse2 = torch.zeros_like(o), torch.zeros_like(lse)
+        c.upload()
+        step(o2, lse2)
+        assert torch.equal(codes, c.cache.k_data) and torch.equal(scales, c.cache.v_scale)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert int(flags) == 0 and N.nvfp4kv_workspace_flags(plan) == 0
+
+
 # ---- together ---------------------------------------------------------------------------
 def test_decode_steps_together_in_a_graph():
     """A decode loop: the table from device lengths, rotary positions, the

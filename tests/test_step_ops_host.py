@@ -278,3 +278,48 @@ def test_runs_refuse_plans_of_the_other_cache():
     s.k_global_scale = s.v_global_scale = 1.0
     for fn in (L.nvfp4kv_decode_run, L.nvfp4kv_decode_attend):
         assert fn(C.byref(p5.info), BUF, 256, 128, C.byref(s), *tail) == _lib.ERR_PLAN_MISMATCH
+
+
+@pytest.mark.parametrize("kv,new,split", [
+    ([8000] * 32, [16] * 32, False),                       # even: whole requests
+    ([1000 + 1526 * i for i in range(20)], [16] * 20, True),   # a long tail on 152 SMs
+    ([100, 60000] + [4000] * 11, [16] * 13, True),
+    ([300] * 400, [16] * 400, False),
+    ([30000] + [200] * 60, [0] + [20] * 60, None)])
+def test_extend_plan_evens_out_the_sms(kv, new, split):
+    """Plans of many rows a kv head may take several waves; every page of every
+    request with rows is in one unit of each kv head, and the busiest SM's work
+    (tiles and 12 a unit, longest first) is not above that of whole requests."""
+    qo = np.concatenate([[0], np.cumsum(new)])
+    np_ = [-(-n // 16) for n in kv]
+    kvp = np.concatenate([[0], np.cumsum(np_)])
+    last = [n - 16 * (p - 1) for n, p in zip(kv, np_)]
+    plan = N.nvfp4kv_decode_plan(qo, kvp, last, 32, 8, 128, 128, causal=True, kernel=5,
+                                 num_sms=152, ctas_per_sm=1, allocate=False)
+    i = plan.info
+    if split is not None:
+        assert bool(i.split) == split
+    units = plan.host[:48 * i.num_units].numpy().view(np.int32).reshape(i.num_units, -1)
+    assert units.shape[1] == 12
+    field = {n: units[:, k] for k, n in enumerate(
+        ["b", "h", "page_begin", "pages", "tok_begin", "kv_len", "qo_begin", "qo_len", "split",
+         "splits", "base", "pair"])}
+    for b, n in enumerate(new):
+        for h in range(8):
+            at = (field["b"] == b) & (field["h"] == h)
+            assert bool(at.any()) == (n > 0)
+            spans = sorted(zip(field["page_begin"][at], field["pages"][at]))
+            end = kvp[b]
+            for begin, pages in spans:
+                assert begin == end and (field["tok_begin"][at] % 128 == 0).all()
+                end += pages
+            assert end == (kvp[b + 1] if n else kvp[b])
+
+    def busiest(tiles):
+        sms = [0] * 152
+        for t in sorted(tiles, reverse=True):
+            k = sms.index(min(sms))
+            sms[k] += t + 12
+        return max(sms)
+    whole = [-(-p // 8) for p, n in zip(np_, new) if n for _ in range(8)]
+    assert busiest([-(-p // 8) for p in field["pages"]]) <= busiest(whole)
