@@ -464,34 +464,52 @@ int nvfp4kv_decode_plan(const int32_t* qo_indptr_h, const int32_t* kv_indptr_h,
     }
     // The extend kernel over an E4M3 cache (one CTA an SM, long units): the grid
     // may be several waves, so the chunk is the one whose units, longest first,
-    // keep the busiest SM shortest: that of one wave or the longest request in 1
-    // to 8 pieces.  20 requests of 1000-30000 tokens 293 -> 186 us, 13 of
-    // 100-60000 332 -> 262 us; even batches keep their whole requests.
+    // keep the busiest SM shortest: that of one wave or the longest request in up
+    // to 8 pieces.  20 requests of 1000-30000 tokens 290 -> 183 us, 13 of
+    // 100-60000 332 -> 246 us; even batches keep their whole requests.
     if (kind == kKernelE4m3 && rows_per_block > 16 && opts.force_chunk_tokens == 0 &&
         opts.max_splits == 0 && max_np > kMinChunkPages) {
-      std::vector<int64_t> cost, sms(num_sms);
-      int64_t least = INT64_MAX, best = chunk;
-      for (int j = 0; j <= 8; ++j) {
+      std::vector<int64_t> sms(num_sms);  // a heap, the least loaded SM first
+      std::vector<std::pair<int64_t, int64_t>> rest;  // units that are not whole chunks
+      int64_t least = INT64_MAX, best = chunk, mean = 0;
+      for (int j : {1, 2, 3, 4, 5, 6, 8, 0}) {  // pieces; 0: one wave's chunk
         int64_t c = j == 0 ? chunk : (max_np + j - 1) / j;
         c = std::min<int64_t>(std::max<int64_t>((c + 7) / 8 * 8, kMinChunkPages), max_np);
-        if (ctas_for(c) > 8192) continue;  // (so many even out by themselves)
-        cost.clear();
-        for (int b = 0; b < batch; ++b)
-          for (int64_t at = 0; nq[b] > 0 && at < nt[b]; at += c)
-            cost.insert(cost.end(), (size_t)num_kv_heads * row_blocks_of(b),
-                        (std::min(c, nt[b] - at) + 7) / 8 + kUnitTiles);
-        std::sort(cost.begin(), cost.end(), std::greater<int64_t>());
-        sms.assign(num_sms, 0);  // a heap, the least loaded first
-        int64_t most = 0;
-        for (int64_t x : cost) {
-          std::pop_heap(sms.begin(), sms.end(), std::greater<int64_t>());
-          most = std::max(most, sms.back() += x);
-          std::push_heap(sms.begin(), sms.end(), std::greater<int64_t>());
+        if (ctas_for(c) > 4096) continue;  // (so many even out by themselves)
+        auto cost = [](int64_t pages) { return (pages + 7) / 8 + kUnitTiles; };
+        int64_t full = 0, work = 0, most = 0;
+        rest.clear();
+        for (int b = 0; b < batch; ++b) {
+          if (nq[b] == 0) continue;
+          const int64_t alike = (int64_t)num_kv_heads * row_blocks_of(b);
+          full += alike * (nt[b] / c);
+          if (nt[b] % c) rest.push_back({cost(nt[b] % c), alike});
         }
+        std::sort(rest.begin(), rest.end(), std::greater<>());
+        sms.assign(num_sms, 0);
+        auto add = [&](int64_t x, int64_t times) {
+          work += x * times;
+          for (; times > 0; --times) {
+            const int64_t v = sms[0] + x;
+            int at = 0;
+            for (int k; (k = 2 * at + 1) < num_sms; at = k) {
+              if (k + 1 < num_sms && sms[k + 1] < sms[k]) ++k;
+              if (sms[k] >= v) break;
+              sms[at] = sms[k];
+            }
+            sms[at] = v;
+            most = std::max(most, v);
+          }
+        };
+        add(cost(c), full);
+        for (const auto& [x, times] : rest) add(x, times);
         if (most < least) {
           least = most;
           best = c;
         }
+        // whole requests have the least work: within 3 % of its mean is enough
+        if (j == 1) mean = work / num_sms;
+        if (least * 32 <= mean * 33) break;
       }
       chunk = best;
     }
