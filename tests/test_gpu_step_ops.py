@@ -337,6 +337,27 @@ def test_append_values_at_the_edges():
     assert int(f) == 0
 
 
+@pytest.mark.parametrize("dk,dv,heads", [(32, 96, 5), (128, 64, 8), (512, 256, 3), (256, 256, 1)])
+def test_append_one_token_pages_at_the_edges(dk, dv, heads):
+    """The same values where a warp takes all heads of a token; a page id out of
+    the pool leaves its token's page as it was."""
+    c = CacheCase((40, 9), 1, heads, dk, dv, seed=dk)
+    k, v = new_rows(49, heads, dk, dv, "bf16", seed=2)
+    k[0], k[1], v[1], k[2], v[2] = 0.0, 448.0, 450.0, math.inf, -math.inf
+    k[3, :, 4], v[4, heads - 1, dv - 1], v[7, 0] = math.nan, -math.inf, math.nan
+    k[5], v[6] = 1e-30, 1e38
+    page = int(c.ids[11])
+    old = [x[page].copy() for x in (*c.codes, *c.scale)]
+    c.append((40, 9), k, v)
+    for x, y in zip((*c.codes, *c.scale), old):
+        x[page] = y
+    c.kv_indices[11] = 10 ** 6
+    f = new_flags()
+    c.run_append((40, 9), k, v, f)
+    c.check()
+    assert int(f) == _lib.FLAG_BAD_APPEND_TARGET
+
+
 def test_append_skips_and_flags():
     kv, new = (20, 20, 20, 20), (2, 2, 2, 2)
     base = CacheCase(kv, 16, 2, 64, 64, seed=3)
