@@ -357,13 +357,15 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
     const float lvA = log2_scale(checked_scale(lds_f32(sc + 64), p.flags));
     const float ksB = P1 ? checked_scale(lds_f32(sc + 32), p.flags) : ksA;
     const float lvB = P1 ? log2_scale(checked_scale(lds_f32(sc + 96), p.flags)) : lvA;
+    // (the scale times the sum: times the factor it could pass float32's range
+    // where the score does not)
     // x[n][0..3] = tokens kr0, kr0, kr0 + 8, kr0 + 8 x rows 2n, 2n+1, 2n, 2n+1
     float x[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        x[n][k] = fmaf(sa[n][k] + sb[n][k], f2[2 * n + (k & 1)] * (k < 2 ? ksA : ksB),
+        x[n][k] = fmaf((sa[n][k] + sb[n][k]) * (k < 2 ? ksA : ksB), f2[2 * n + (k & 1)],
                        nm2[2 * n + (k & 1)] + (k < 2 ? lvA : lvB));
     const bool masked = tok0 + 15 > min_lim;  // some row does not see some token
     if (masked) {

@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
         for (int e = 0; e < 2; ++e) {
           const uint64_t s2 = pack_f32x2(__uint_as_float(sv[e4 + 2 * e]),
                                          __uint_as_float(sv[e4 + 2 * e + 1]));
-          unpack_f32x2(fma_f32x2(s2, mul_f32x2(e ? f.y : f.x, ks2),
+          unpack_f32x2(fma_f32x2(mul_f32x2(s2, ks2), e ? f.y : f.x,
                                  add_f32x2(e ? nm.y : nm.x, lv2)),
                        x[e4 + 2 * e], x[e4 + 2 * e + 1]);
         }

@@ -578,6 +578,17 @@ def test_attention_nan_reaches_the_rows_that_see_it(dk, dv, hq, hkv, new, chunk,
                 edit=edit, seed=dk + sum(new))
 
 
+@pytest.mark.parametrize("rows", [1, 12, 40])
+def test_attention_zero_scores_at_the_ends_of_the_range(rows):
+    """Keys of nothing but zero codes under the largest scale, and queries as
+    large as their type allows: scores of 0, so the mean of the values."""
+    def edit(c, q):
+        c.codes[0][:] = 0
+        c.scale[0][:] = 2.0 ** 64
+        q *= 2.0 ** 120
+    attend_case((1, 40), (1, rows), 2, 1, 128, 128, edit=edit, seed=rows)
+
+
 def test_attention_nothing_to_do():
     _, plan, o = attend_case((37, 5, 0), (0, 0, 0), 8, 2, 128, 128)
     assert plan.info.num_units == 0 and o.shape == (0, 8, 128)
