@@ -269,6 +269,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
   uint64_t* s_empty = bars + 40;   // [SB] S^T read
   uint64_t* p_full = bars + 48;    // [NPB] softmax -> O^T issue
   uint64_t* pv_done = bars + 52;   // [NPB] P^T V done -> softmax
+  uint64_t* v_seen = bars + 54;    // O^T issue has seen V tile first_part + 1 - VR land
   uint64_t* q_full = bars + 56;    // Q ready -> S^T issue
   uint64_t* v_clean = bars + 57;   // the V tiles from first_part on hold no NaN code
   uint64_t* fin = bars + 58;       // [2] wind-down of the two issuers' products
@@ -330,6 +331,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     }
     mbar_init(q_full, SW);
     mbar_init(v_clean, 1);
+    mbar_init(v_seen, 1);
     mbar_init_fence();
     *s_abort = 0;
   }
@@ -473,13 +475,19 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     // The V tiles that some row does not see whole, the last one or two (the rows'
     // limits lie less than N <= 64 tokens apart): a weight of 0 must not meet a
     // NaN code.  Done here, as this warp is up to four tiles ahead (1 % of the
-    // launch; in the warp that issues O^T 4 %).
+    // launch; in the warp that issues O^T 4 %).  A wait by parity tells a phase
+    // from the one before it only, and this warp has not followed the V ring: the
+    // O^T issuer, which has, says when the stages' earlier tiles have landed
+    // (v_seen; tile first_part + 1 - VR is the later of the two, and neither it nor
+    // a tile before it waits for v_clean).
     static_assert(N <= 64 && VR >= 2, "both tiles fit the ring while O^T waits for v_clean");
     for (int d = lane; d < DV; d += 32) s_nan[d] = INT_MAX;
-    __syncwarp();
+    if (lane == 0 && ok && first_part < ntiles) ok = wait_soon<T::SPINS>(v_seen, 0, s_abort, p.flags);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
     for (int t = first_part; t < ntiles && ok; ++t) {
       if (lane == 0) ok = wait_soon<T::SPINS>(&v_landed[t % VR], (t / VR) & 1, s_abort, p.flags);
       ok = __shfl_sync(0xffffffffu, ok, 0);
+      __syncwarp();  // (a shuffle orders no memory: the tile is lane 0's to see until here)
       if (ok)
         no_nan<DV>(sV + (t % VR) * T::VB, unit_end - t * kTileTok,
                    u.tok_begin + t * kTileTok, s_nan);
@@ -499,9 +507,11 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     const uint64_t pd0 = smem_desc(smem_addr(sP), T::PBLK, 8 * T::PROW,
                                    T::PROW == 128 ? kSwz128 : kSwz64);
     bool ok = true;
+    if (lane == 0 && first_part + 1 < VR) mbar_arrive(v_seen);  // (their stages' first tiles)
     for (int i = 0, st = 0, round = 0; i < ntiles; ++i) {
       if (lane == 0) {
         ok = wait_soon<T::SPINS>(&v_landed[st], round & 1, s_abort, p.flags);
+        if (ok && i == first_part + 1 - VR) mbar_arrive(v_seen);
         if (ok && i >= first_part) ok = wait_soon<T::SPINS>(v_clean, 0, s_abort, p.flags);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
