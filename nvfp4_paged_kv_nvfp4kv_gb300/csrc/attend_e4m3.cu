@@ -6,11 +6,15 @@
 //   p_j = exp(s_j), over the keys that the row sees; lse = ln sum_j p_j.
 //  * Codes are exact in f16 (cvt.rn.f16x2.e4m3x2), so both products run on
 //    mma.sync m16n8k16 with f16 operands and f32 accumulators, and no element
-//    is multiplied by a scale: a_j joins the row's factor of the score, and
-//    b_j joins the exponent.  With x_j the score in log2 units the value
-//    weight is p'_j = 2^(x_j + log2 b_j - m), and the row sum takes
-//    p'_j * 2^(-log2 b_j), so m may follow x + log2 b: p' <= 2^8 then fits
-//    f16 for any scales, and the partial states are ordinary ones.
+//    is multiplied by a scale: a_j multiplies the score, b_j the weight.
+//    m follows x_j + log2 b_j, x_j the score in log2 units: y_j = 2^(x_j - m)
+//    goes into the row sum and p'_j = y_j b_j <= 2^8, rounded to f16, weighs the
+//    codes.  y lies in [0, 2^72] and the largest of a row is at least 2^-64, so
+//    float32 keeps every term of the sum that counts (a term taken as p'_j / b_j
+//    is lost where p' underflows, from scales 2^116 apart on).  The sum's factors
+//    2^(m - m_new) are taken as two halves: m may move by 2^128 without a score
+//    changing.  f16 for p' is the rounding of 2^-11 that the product's operand
+//    type costs; the row sum takes the float32 y.
 //  * A warp owns every WARPS-th tile of 16 tokens (one page, or sixteen
 //    1-token pages) and streams its K rows, V rows and scales through a ring
 //    of STAGES stages with cp.async, rows and pages at any byte strides.
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
   __syncthreads();
 
   // this lane's query rows 8 n + 2t and 8 n + 2t + 1 (k = 2 n and 2 n + 1):
-  // score factor, -m (m the running maximum of x + log2 b, once the row has
+  // score factor, -m (m the running maximum of score + log2 b, once the row has
   // one: bit k of has_max) and sum
   constexpr int NR = 2 * NT;
   float f2[NR], nm2[NR], lrow[NR];
@@ -354,9 +358,10 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
     // ---- the tile's scales: tokens kr0 (A) and kr0 + 8 (B) -----------------
     const uint32_t sc = st + T::OFF_SC + 4 * kr0;
     const float ksA = checked_scale(lds_f32(sc), p.flags);
-    const float lvA = log2_scale(checked_scale(lds_f32(sc + 64), p.flags));
+    const float vsA = checked_scale(lds_f32(sc + 64), p.flags), lvA = log2_scale(vsA);
     const float ksB = P1 ? checked_scale(lds_f32(sc + 32), p.flags) : ksA;
-    const float lvB = P1 ? log2_scale(checked_scale(lds_f32(sc + 96), p.flags)) : lvA;
+    const float vsB = P1 ? checked_scale(lds_f32(sc + 96), p.flags) : vsA;
+    const float lvB = P1 ? log2_scale(vsB) : lvA;
     // (the scale times the sum: times the factor it could pass float32's range
     // where the score does not)
     // x[n][0..3] = tokens kr0, kr0, kr0 + 8, kr0 + 8 x rows 2n, 2n+1, 2n, 2n+1
@@ -366,7 +371,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         x[n][k] = fmaf((sa[n][k] + sb[n][k]) * (k < 2 ? ksA : ksB), f2[2 * n + (k & 1)],
-                       nm2[2 * n + (k & 1)] + (k < 2 ? lvA : lvB));
+                       nm2[2 * n + (k & 1)]);
     const bool masked = tok0 + 15 > min_lim;  // some row does not see some token
     if (masked) {
       const int ta = tok0 + kr0, tb = ta + 8;
@@ -376,10 +381,13 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
         if (tb > lim[k]) x[k / 2][2 + k % 2] = -INFINITY;
       }
     }
-    float top = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[0][2], x[0][3]));
+    float topA = fmaxf(x[0][0], x[0][1]), topB = fmaxf(x[0][2], x[0][3]);
 #pragma unroll
-    for (int n = 1; n < NT; ++n)
-      top = fmaxf(top, fmaxf(fmaxf(x[n][0], x[n][1]), fmaxf(x[n][2], x[n][3])));
+    for (int n = 1; n < NT; ++n) {
+      topA = fmaxf(topA, fmaxf(x[n][0], x[n][1]));
+      topB = fmaxf(topB, fmaxf(x[n][2], x[n][3]));
+    }
+    const float top = P1 ? fmaxf(topA + lvA, topB + lvB) : fmaxf(topA, topB) + lvA;
     if (__builtin_expect(__any_sync(0xffffffffu, top > thr_lane), 0)) {
       // raise each row's maximum to this tile's (a row's values sit in the 8
       // lanes of the same t)
@@ -387,20 +395,21 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
       bool moved = false;
 #pragma unroll
       for (int k = 0; k < NR; ++k) {
-        float mx = fmaxf(x[k / 2][k % 2], x[k / 2][2 + k % 2]);
+        float mx = fmaxf(x[k / 2][k % 2] + lvA, x[k / 2][2 + k % 2] + lvB);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        corr[k] = 1.f;
+        float half = 1.f;  // the square root of the row's factor
         const bool has = (has_max >> k) & 1u;
         if (mx != -INFINITY && (!has || mx > 0.f)) {
-          if (has) corr[k] = ex2(-mx);
+          if (has) half = ex2(-0.5f * mx);
           nm2[k] -= mx;
           has_max |= 1u << k;
           x[k / 2][k % 2] -= mx;
           x[k / 2][2 + k % 2] -= mx;
         }
-        lrow[k] *= corr[k];
-        moved |= corr[k] != 1.f;
+        lrow[k] = lrow[k] * half * half;
+        corr[k] = half * half;
+        moved |= half != 1.f;
       }
       thr_lane = lane_threshold();
       if (moved) {
@@ -412,15 +421,14 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
             for (int k = 0; k < 4; ++k) oacc[n][mt][k] *= corr[2 * n + (k & 1)];
       }
     }
-    const float ivA = ex2(-lvA), ivB = P1 ? ex2(-lvB) : ivA;
     uint32_t pf[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const float p0 = ex2(x[n][0]), p1 = ex2(x[n][1]), p2 = ex2(x[n][2]), p3 = ex2(x[n][3]);
-      lrow[2 * n] += p0 * ivA + p2 * ivB;
-      lrow[2 * n + 1] += p1 * ivA + p3 * ivB;
-      pf[n][0] = movmatrix_trans(f32x2_to_f16x2(p0, p1));
-      pf[n][1] = movmatrix_trans(f32x2_to_f16x2(p2, p3));
+      const float y0 = ex2(x[n][0]), y1 = ex2(x[n][1]), y2 = ex2(x[n][2]), y3 = ex2(x[n][3]);
+      lrow[2 * n] += y0 + y2;
+      lrow[2 * n + 1] += y1 + y3;
+      pf[n][0] = movmatrix_trans(f32x2_to_f16x2(y0 * vsA, y1 * vsA));
+      pf[n][1] = movmatrix_trans(f32x2_to_f16x2(y2 * vsB, y3 * vsB));
     }
 
     // ---- O^T += D^T P'^T ----------------------------------------------------

@@ -10,14 +10,14 @@
 //    four significant bits, so two give a bf16 value's eight and three an f16
 //    value's eleven, down to 2^-17 of the row's largest |q|.
 //    S^T = K (q0 + q1 + ..)^T accumulates in one tile of tensor memory.
-//  * Weights p' = 2^x (at most 2^8): p' = w0 + w1 / 32 + w2 / 1024.  Each piece
+//  * Weights p' = y b (at most 2^8, rounded to f16): p' = w0 + w1 / 32 + w2 / 1024.  Each piece
 //    has its own columns of O^T = V^T (w0 | w1 | w2)^T, added in the epilogue:
 //    twelve bits of a weight, and a weight 2^-20 of the largest is still kept.
 //    (Two pieces hold eight bits; to keep weights that small they allow only
 //    three bits between a tile's maximum and the raise, and a raise of some of
 //    the rows in most tiles then costs more than the third piece: 223 against
 //    218 us on 32 requests of 2000-16000 tokens x 64 rows, when measured.)
-//  * Row sums come from the unsplit float32 weights, a register per query row
+//  * Row sums come from the float32 y = 2^(score - m), a register per query row
 //    and thread, added up over the threads at the end.
 //
 // One CTA = one work unit (request, kv head, chunk of pages) x N = 32 or 64
@@ -30,7 +30,7 @@
 //  * issue (two warps, one thread each): S^T = K Q^T into a ring of tiles in
 //    tensor memory, and O^T += V^T P^T, each once its inputs are ready;
 //  * softmax (four warps for each 16 query rows; thread = token of S^T): the
-//    token's K scale joins the row's factor, log2 of its V scale the exponent.
+//    token's K scale multiplies the sum, its V scale the weight.
 //    The work of a tile is dependent chains, so many warps with few rows each
 //    beat few warps with many (8 warps of 32 rows 258, 16 of 16 rows 236 us).
 // The running maximum is raised only when a value exceeds 2^8.  Every wait is
@@ -166,7 +166,7 @@ struct Ext {
   static constexpr int PBLK = kTileTok * PROW;
   static constexpr int PB = PROW == 128 ? PBLK : kPieces * PBLK;
   static_assert(PROW == 128 || N == 64, "a piece fills a 64-byte row");
-  static constexpr int SCB = kTileTok * 12;        // K scale, log2 and inverse of the V scale
+  static constexpr int SCB = kTileTok * 8;         // K and V scale
   static constexpr int MISC = 4608;
   static constexpr int NPB = 2;                    // P^T buffers
   // Tests of a barrier before a loader or issuer suspends: with 8 softmax warps
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
   uint8_t* sV = smem + T::OFF_V;
   uint8_t* sP = smem + T::OFF_P;
   uint8_t* sQ = smem + T::OFF_Q;
-  float* sSc = reinterpret_cast<float*>(smem + T::OFF_SC);  // [SR][3][128]
+  float* sSc = reinterpret_cast<float*>(smem + T::OFF_SC);  // [SR][2][128]
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::OFF_MISC);
   uint64_t* k_landed = bars;       // [KR] a K tile and its scales are in
   uint64_t* k_empty = bars + 8;    // [KR] S^T done, scales read
@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
   int* s_lim = reinterpret_cast<int*>(s_thr + N);
   float* s_m = reinterpret_cast<float*>(s_lim + N);  // m (log2), -inf before the first tile
   int* s_max = reinterpret_cast<int*>(s_m + N);      // reduction keys, then shifts
-  float* s_corr = reinterpret_cast<float*>(s_max + N);
-  float* s_fin = s_corr + N;                         // [2N + 4]
+  float* s_half = reinterpret_cast<float*>(s_max + N);  // root of a raise's factor
+  float* s_fin = s_half + N;                         // [2N + 4]
   float* s_l = s_fin + 2 * N + 4;                    // [4][N] row sums of the lane quarters
   int* s_nan = reinterpret_cast<int*>(s_l + 4 * N);  // [DV] first NaN token taken out of V
   int* s_tok = s_nan + DV;                           // tok_begin, tok_end of the unit
@@ -655,18 +655,15 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     uint64_t lsum[NH / 2];  // this token's share of the row sums, two rows each
 #pragma unroll
     for (int e = 0; e < NH / 2; ++e) lsum[e] = 0;
-    // x: log2-domain scores of tile i relative to the running maxima, with log2
-    // of the token's V scale, -inf where masked or past the unit's end; iv2: the
-    // inverse of that scale, twice
-    auto scores = [&](int i, float (&x)[NH], uint64_t& iv2) {
+    // x: log2-domain scores of tile i less the running maxima, -inf where masked
+    // or past the unit's end; vs: the token's V scale
+    auto scores = [&](int i, float (&x)[NH], float& vs) {
       const float* sc = sSc + (i % SR) * (T::SCB / 4) + j;
       const float ks0 = sc[0], vs0 = sc[kTileTok];
       const float ks = fminf(fmaxf(ks0, kMinScale), kMaxScale);
-      const float vs = fminf(fmaxf(vs0, kMinScale), kMaxScale);
+      vs = fminf(fmaxf(vs0, kMinScale), kMaxScale);
       if (ks != ks0 || vs != vs0) atomicOr(p.flags, 0x20u);
-      const float lv = log2_scale(vs), iv = ex2(-lv);
-      const uint64_t ks2 = pack_f32x2(ks, ks), lv2 = pack_f32x2(lv, lv);
-      iv2 = pack_f32x2(iv, iv);
+      const uint64_t ks2 = pack_f32x2(ks, ks);
       uint32_t sv[NH];
       tmem_ld<NH>(tmem + lane_base + T::SCOL + N * (i % SB) + c0, sv);
       tmem_wait_ld<NH>(sv);
@@ -678,8 +675,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
         for (int e = 0; e < 2; ++e) {
           const uint64_t s2 = pack_f32x2(__uint_as_float(sv[e4 + 2 * e]),
                                          __uint_as_float(sv[e4 + 2 * e + 1]));
-          unpack_f32x2(fma_f32x2(mul_f32x2(s2, ks2), e ? f.y : f.x,
-                                 add_f32x2(e ? nm.y : nm.x, lv2)),
+          unpack_f32x2(fma_f32x2(mul_f32x2(s2, ks2), e ? f.y : f.x, e ? nm.y : nm.x),
                        x[e4 + 2 * e], x[e4 + 2 * e + 1]);
         }
       }
@@ -701,22 +697,23 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
       warp_wait(&s_full[i % SB], (i / SB) & 1);
       tc_fence_after();
       float x[NH];
-      uint64_t iv2 = 0;
+      float vs = 1.f, lv = 0.f;  // the token's V scale and its log2
       bool trig = false;
       if (active) {
-        scores(i, x, iv2);
+        scores(i, x, vs);
+        lv = log2_scale(vs);
         if (unset) {
 #pragma unroll
           for (int e4 = 0; e4 < NH; e4 += 4) {
             const float4 t4 = *reinterpret_cast<const float4*>(s_thr + c0 + e4);
-            trig |= (x[e4] > t4.x) | (x[e4 + 1] > t4.y) | (x[e4 + 2] > t4.z) |
-                    (x[e4 + 3] > t4.w);
+            trig |= (x[e4] + lv > t4.x) | (x[e4 + 1] + lv > t4.y) | (x[e4 + 2] + lv > t4.z) |
+                    (x[e4 + 3] + lv > t4.w);
           }
         } else {  // every real column has a maximum: one test of the largest
           float mx = fmaxf(x[0], x[1]);
 #pragma unroll
           for (int e = 2; e < NH; e += 2) mx = fmax3(mx, x[e], x[e + 1]);
-          trig = mx > kRaise;
+          trig = mx + lv > kRaise;
         }
       }
       if (named_or(gbar, 128, trig)) {
@@ -727,7 +724,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
           int kk = INT32_MIN;
 #pragma unroll
           for (int e = 0; e < NH; ++e) {
-            const int k = __reduce_max_sync(0xffffffffu, fkey(x[e]));
+            const int k = __reduce_max_sync(0xffffffffu, fkey(x[e] + lv));
             kk = lane == e ? k : kk;
           }
           if (lane < NH) atomicMax(&s_max[c0 + lane], kk);
@@ -738,16 +735,16 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
           const int r = c0 + gtid;
           const float tm = funkey(s_max[r]);  // tile maximum, relative to the old m
           const float m_old = s_m[r];
-          float corr = 1.f;
+          float half = 1.f;  // the square root of the row's factor
           if (tm != -INFINITY && (m_old == -INFINITY || tm > 0.f)) {
             const float m_new = (m_old == -INFINITY ? 0.f : m_old) + tm;
-            if (m_old != -INFINITY) corr = ex2(m_old - m_new);
+            if (m_old != -INFINITY) half = ex2(0.5f * (m_old - m_new));
             s_m[r] = m_new;
             s_nm[r] = -m_new;
             s_thr[r] = kRaise;
-            moved = corr != 1.f;
+            moved = half != 1.f;
           }
-          s_corr[r] = corr;
+          s_half[r] = half;
         }
         const bool rescale = named_or(gbar, 128, moved) && i > 0;
         unset = named_or(gbar, 128, gtid < NH && c0 + gtid < nvalid && s_m[c0 + gtid] == -INFINITY);
@@ -755,8 +752,10 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
           warp_wait(&pv_done[(i - 1) % NPB], ((i - 1) / NPB) & 1);
           tc_fence_after();
 #pragma unroll
-          for (int e = 0; e < NH / 2; ++e)
-            lsum[e] = mul_f32x2(lsum[e], *reinterpret_cast<const uint64_t*>(s_corr + c0 + 2 * e));
+          for (int e = 0; e < NH / 2; ++e) {
+            const uint64_t half = *reinterpret_cast<const uint64_t*>(s_half + c0 + 2 * e);
+            lsum[e] = mul_f32x2(mul_f32x2(lsum[e], half), half);
+          }
           for (int blk = 0; blk < (DV / 128) * kPieces; ++blk) {
             uint32_t ov[NH];
             const uint32_t oa = tmem + lane_base + T::OCOL + blk * N + c0;
@@ -764,12 +763,12 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
             tmem_wait_ld<NH>(ov);
 #pragma unroll
             for (int e = 0; e < NH; ++e)
-              ov[e] = __float_as_uint(__uint_as_float(ov[e]) * s_corr[c0 + e]);
+              ov[e] = __float_as_uint(__uint_as_float(ov[e]) * (s_half[c0 + e] * s_half[c0 + e]));
             tmem_st<NH>(oa, ov);
           }
           tmem_wait_st();
         }
-        if (active) scores(i, x, iv2);  // (again: nothing of the tile is kept over a raise)
+        if (active) scores(i, x, vs);  // (again: nothing of the tile is kept over a raise)
       }
       tc_fence_before();
       __syncwarp();
@@ -778,14 +777,17 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
       if (i >= NPB) warp_wait(&pv_done[sb], (i / NPB - 1) & 1);  // P buffer sb is free
       if (active) {
         uint32_t h[kPieces][NH / 4];
+        const uint64_t vs2 = pack_f32x2(vs, vs);
 #pragma unroll
         for (int e = 0; e < NH / 4; ++e) {
           uint32_t rest[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const int col = 4 * e + 2 * k;
-            const float a = ex2(x[col]), b = ex2(x[col + 1]);
-            lsum[col / 2] = fma_f32x2(pack_f32x2(a, b), iv2, lsum[col / 2]);
+            const uint64_t y = pack_f32x2(ex2(x[col]), ex2(x[col + 1]));
+            lsum[col / 2] = add_f32x2(lsum[col / 2], y);
+            float a, b;
+            unpack_f32x2(mul_f32x2(y, vs2), a, b);
             rest[k] = f32x2_to_f16x2(a, b);
           }
 #pragma unroll

@@ -160,8 +160,9 @@ __device__ __forceinline__ void finish_unit(const AttendParams& p, const WorkUni
 // word in shared memory.  The arrival is one acquire-release atomic after the
 // barrier, which orders the CTA's partial stores before it and the last CTA's
 // loads after it.  A thread folds IT items (row, four dims) at a time, MB
-// partial states loaded together.  A NaN state (a NaN score in its chunk) makes
-// the row NaN, lse too.
+// partial states loaded together.  A state's factor is applied as two halves: one
+// below 2^-126 counts where its state's values are that much larger (value scales
+// 2^128 apart).  A NaN state (a NaN score in its chunk) makes the row NaN, lse too.
 template <int RB, int DV, int NT, int IT, int MB, class Sync>
 __device__ __forceinline__ void fold_if_last(const AttendParams& p, const WorkUnit& u, int row0,
                                              int rows, int* last, int tid, Sync sync) {
@@ -221,17 +222,20 @@ __device__ __forceinline__ void fold_if_last(const AttendParams& p, const WorkUn
             if (isnan(lw[k][j])) mn = 0.f;
           if (mn == -INFINITY) continue;
         }
-        const float cf = ex2(M[k] - mn);  // 0 for -inf
-        L[k] *= cf;
-        acc[k].x *= cf; acc[k].y *= cf; acc[k].z *= cf; acc[k].w *= cf;
+        const float cf = ex2(0.5f * (M[k] - mn));  // 0 for -inf
+        L[k] = L[k] * cf * cf;
+        acc[k].x = acc[k].x * cf * cf;
+        acc[k].y = acc[k].y * cf * cf;
+        acc[k].z = acc[k].z * cf * cf;
+        acc[k].w = acc[k].w * cf * cf;
 #pragma unroll
         for (int j = 0; j < MB; ++j) {
-          const float w = ex2(lw[k][j] - mn);
-          L[k] += w;
-          acc[k].x = fmaf(w, v[k][j].x, acc[k].x);
-          acc[k].y = fmaf(w, v[k][j].y, acc[k].y);
-          acc[k].z = fmaf(w, v[k][j].z, acc[k].z);
-          acc[k].w = fmaf(w, v[k][j].w, acc[k].w);
+          const float w = ex2(0.5f * (lw[k][j] - mn));
+          L[k] = fmaf(w, w, L[k]);
+          acc[k].x = fmaf(w, w * v[k][j].x, acc[k].x);
+          acc[k].y = fmaf(w, w * v[k][j].y, acc[k].y);
+          acc[k].z = fmaf(w, w * v[k][j].z, acc[k].z);
+          acc[k].w = fmaf(w, w * v[k][j].w, acc[k].w);
         }
         M[k] = mn;
       }
@@ -282,8 +286,9 @@ __device__ __forceinline__ void finish_rows(const AttendParams& p, const WorkUni
     if (M != -INFINITY) {
 #pragma unroll
       for (int w = 0; w < WARPS; ++w) {
-        const float sc = ex2(mw[w] - M);  // 0 for -inf
-        L = fmaf(sL[w * RB + rr], sc, L);
+        // 0 for -inf; as two halves, for maxima that differ by more than the sums do
+        const float half = ex2(0.5f * (mw[w] - M)), sc = half * half;
+        L = fmaf(sL[w * RB + rr] * half, half, L);
         if (mw[w] != -INFINITY) {
           o.x = fmaf(ow[w].x, sc, o.x);
           o.y = fmaf(ow[w].y, sc, o.y);
