@@ -107,10 +107,11 @@ __device__ __forceinline__ void append_block(const E4m3AppendParams& p, int kv, 
   m = __float_as_uint(unpack2<F16>(m).x);
   float s = scale_for(m);
   if (a > 0) {
-    if (!(s_old >= kMinScale && s_old <= kMaxScale)) {  // no scale of this format
-      if (lane == 0 && p.flags) atomicOr(p.flags, 0x20u);
-      s_old = kMinScale;
-    }
+    // no scale of this format: the nearer end, as the attention takes it (the
+    // lower for a NaN)
+    const float c_old = fminf(fmaxf(s_old, kMinScale), kMaxScale);
+    if (c_old != s_old && lane == 0 && p.flags) atomicOr(p.flags, 0x20u);
+    s_old = c_old;
     s = fmaxf(s, s_old);
     if (s > s_old && r0 < rpp) {
       const float f = __fdiv_rn(s_old, s);
