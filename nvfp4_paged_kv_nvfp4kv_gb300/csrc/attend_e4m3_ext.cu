@@ -3,13 +3,18 @@
 //
 // The same function as attend_e4m3.cu (which gives the formulas).  The cache's
 // codes are operands of tcgen05.mma kind::f8f6f4 as they stand: no element of K
-// or V is converted.  What is not E4M3 is split into E4M3 pieces whose sum is
+// or V is converted.  What is not E4M3 is split into 8-bit pieces whose sum is
 // exact enough, and the pieces' products are summed by the tensor cores:
 //  * Query rows, times a power of two that puts the row's largest |q| into
-//    [128, 256): q = q0 + q1 (+ q2), each piece the rounded rest.  A piece has
-//    four significant bits, so two give a bf16 value's eight and three an f16
-//    value's eleven, down to 2^-17 of the row's largest |q|.
-//    S^T = K (q0 + q1 + ..)^T accumulates in one tile of tensor memory.
+//    [2^14, 2^15): q = q0 + q1 + q2, E5M2 pieces (the operands of a product have
+//    formats of their own), each the rounded rest.  A piece has three significant
+//    bits and leaves a rest of at most 1/8: of an f16 value's eleven bits, 1024 to
+//    2047 units, |rest| <= 128, then 8 units, which the third piece holds exactly;
+//    bf16 has fewer.  The smallest code is 2^-16, so nothing above 2^-31 of the
+//    row's largest |q| is lost.  (E4M3 pieces, four bits each, would spare bf16 the
+//    third piece and end at 2^-17 of the largest: under one outlier dim the others
+//    lose their bits.)  S^T = K (q0 + q1 + q2)^T accumulates in one tile of tensor
+//    memory.
 //  * Weights p' = y b (at most 2^8, rounded to f16): p' = w0 + w1 / 32 + w2 / 1024.  Each piece
 //    has its own columns of O^T = V^T (w0 | w1 | w2)^T, added in the epilogue:
 //    twelve bits of a weight, and a weight 2^-20 of the largest is still kept.
@@ -74,8 +79,8 @@ constexpr int kPieces = 3;      // of a weight
 constexpr float kRaise = 8.f;  // log2 of the largest weight before m is raised
 constexpr float kMinScale = 0x1p-64f, kMaxScale = 0x1p64f;
 
-// D[tmem] (+)= A[smem] . B[smem], E4M3 operands (the instruction descriptor of
-// kind::f16 with A and B formats 0 = E4M3)
+// D[tmem] (+)= A[smem] . B[smem], 8-bit operands (the instruction descriptor of
+// kind::f16; formats of A at bit 7 and B at bit 10: 0 E4M3, 1 E5M2)
 __device__ __forceinline__ void umma8_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t acc) {
   asm volatile(
@@ -94,13 +99,20 @@ __device__ __forceinline__ uint32_t e4m3x4_of_f16(uint32_t a, uint32_t b) {
       : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t e4m3x4_of_f32(float a, float b, float c, float d) {
+// four float32 values -> four E5M2 codes, the first in the low byte, and back
+__device__ __forceinline__ uint32_t e5m2x4_of_f32(float a, float b, float c, float d) {
   uint32_t r;
-  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n"
-      " cvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}\n"
+  asm("{\n .reg .b16 l, h;\n cvt.rn.satfinite.e5m2x2.f32 l, %2, %1;\n"
+      " cvt.rn.satfinite.e5m2x2.f32 h, %4, %3;\n mov.b32 %0, {l, h};\n}\n"
       : "=r"(r)
       : "f"(a), "f"(b), "f"(c), "f"(d));
   return r;
+}
+__device__ __forceinline__ void e5m2x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e5m2x2 %0, l;\n"
+      " cvt.rn.f16x2.e5m2x2 %1, h;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -156,7 +168,7 @@ struct Ext {
   static constexpr int CG = N / NH;                // column groups of four warps
   static constexpr int SW = 4 * CG;                // softmax warps
   static constexpr int THREADS = 32 * (SW + kLoaders + 2);
-  static constexpr int NQ = 3;                     // query pieces (2 used for bf16)
+  static constexpr int NQ = 3;                     // query pieces
   static constexpr int KB = kTileTok * DK, VB = kTileTok * DV;
   static constexpr int QB = N * DK;                // one query piece
   // P^T: a token's kPieces * N weight pieces, one product's N: at N = 32 a row of
@@ -194,7 +206,7 @@ struct Ext {
   static constexpr int SCOL = 0, OCOL = SB * N;    // S^T ring, O^T blocks of 128 value dims
   static constexpr int COLS = OCOL + (DV / 128) * PN;
   static constexpr int TCOLS = COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
-  static constexpr uint32_t IDESC_QK = idesc_f16(128, N, 0, 0);
+  static constexpr uint32_t IDESC_QK = idesc_f16(128, N, 0, 0) | 1u << 10;  // E4M3 . E5M2
   static constexpr uint32_t IDESC_PV = idesc_f16(128, PN, 1, 1);
   static_assert(DK % 128 == 0 && DV % 128 == 0, "operand rows of 128 bytes");
   static_assert(OFF_P % 1024 == 0 && OFF_Q % 1024 == 0 && OFF_MISC % 16 == 0, "align");
@@ -294,7 +306,6 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
   const int q4 = warp & 3;       // tensor-memory lane quarter
   const int j = 32 * q4 + lane;  // token of the tile / value dim
   const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
-  const int nq = p.q_f16 ? 3 : 2;
   const WorkUnit u = load_unit(p);
   const int R = G * u.qo_len;
   if (row0 >= R) return;  // uniform: before any barrier or tensor memory use
@@ -457,7 +468,8 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
         tc_fence_after();
         const uint32_t d = tmem + T::SCOL + N * (k % SB);
         const uint64_t kd = kd0 + ((st * T::KB) >> 4);
-        for (int q = 0; q < nq; ++q)
+#pragma unroll 1
+        for (int q = 0; q < T::NQ; ++q)
 #pragma unroll
           for (int kk = 0; kk < DK / 32; ++kk)
             umma8_ss(d, kd + (((kk >> 2) * (kTileTok * 128) + (kk & 3) * 32) >> 4),
@@ -584,8 +596,8 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
       }
 #pragma unroll
       for (int o = QW / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      int ex = 0;  // amax * 2^ex in [128, 256)
-      if (amax > 0.f) ex = 7 - (int)((__float_as_uint(amax) >> 23) & 0xFF) + 127;
+      int ex = 0;  // amax * 2^ex in [2^14, 2^15)
+      if (amax > 0.f) ex = 14 - (int)((__float_as_uint(amax) >> 23) & 0xFF) + 127;
       ex = max(-120, min(120, ex));
       // (an infinite element has no pieces: its row is NaN, as 0 * inf makes it)
       const float up = isinf(amax) ? NAN : __uint_as_float((uint32_t)(127 + ex) << 23);
@@ -596,13 +608,14 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
       }
       const uint32_t off = (uint32_t)(c8 >> 4) * (N * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
                            (c8 & 15) * 8;
-      for (int q = 0; q < nq; ++q) {
+#pragma unroll 1
+      for (int q = 0; q < T::NQ; ++q) {
         uint32_t h[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          h[e] = e4m3x4_of_f32(rest[2 * e].x, rest[2 * e].y, rest[2 * e + 1].x, rest[2 * e + 1].y);
+          h[e] = e5m2x4_of_f32(rest[2 * e].x, rest[2 * e].y, rest[2 * e + 1].x, rest[2 * e + 1].y);
           uint32_t back[2];
-          e4m3x4_to_f16(h[e], back[0], back[1]);
+          e5m2x4_to_f16(h[e], back[0], back[1]);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back[k]));
