@@ -116,7 +116,8 @@ int nvfp4kv_build_page_table(const int32_t* kv_len, const int32_t* qo_len, int32
                              uint32_t* device_flags, cudaStream_t stream) {
   if (batch < 0 || max_pages_per_request < 0 || num_free < 0)
     return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "batch, max_pages_per_request or num_free < 0");
-  if (batch > 8192) return fail(NVFP4KV_ERR_UNSUPPORTED, "batch %d (at most 8192)", batch);
+  if (batch > kMaxPageTableBatch)
+    return fail(NVFP4KV_ERR_UNSUPPORTED, "batch %d (at most %d)", batch, kMaxPageTableBatch);
   if (page_size < 1 || page_size > 65536)
     return fail(NVFP4KV_ERR_UNSUPPORTED, "page_size %d (1 to 65536)", page_size);
   if (!out || !out->qo_indptr || !out->kv_indptr || !out->free_head)

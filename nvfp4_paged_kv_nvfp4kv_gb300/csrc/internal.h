@@ -189,6 +189,7 @@ cudaError_t launch_attend(const AttendConfig& cfg, const AttendParams& p,
                           int grid_x, int grid_y, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_dequantize(const DequantParams& p, cudaStream_t stream);
+constexpr int kMaxPageTableBatch = 8192;
 cudaError_t launch_page_table(const PageTableParams& p, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_e4m3_append(const E4m3AppendParams& p, cudaStream_t stream);

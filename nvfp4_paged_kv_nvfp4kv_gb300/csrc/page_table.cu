@@ -216,10 +216,12 @@ __global__ void __launch_bounds__(kThreads) page_table_kernel(const PageTablePar
 }  // namespace
 
 cudaError_t launch_page_table(const PageTableParams& p, cudaStream_t stream) {
+  constexpr int kMaxSmem = (4 * kMaxPageTableBatch + 3) * 4;
   const int smem = (4 * p.batch + 3) * 4;
   if (smem > 40 * 1024) {
+    // the most that any call takes: another thread's call must not find less
     cudaError_t e = cudaFuncSetAttribute(page_table_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
   }
   // one CTA per kWarps chunks of pages or kThreads rows, at most two an SM:
