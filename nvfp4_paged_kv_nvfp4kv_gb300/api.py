@@ -127,11 +127,13 @@ def nvfp4kv_dequantize_paged(cache: PagedCache, page_ids, k_out=None, v_out=None
 class Plan:
     """A decode plan: the C plan_info, its pinned host work list and the
     device workspace it was uploaded into (and the live length array it
-    reads, kept alive with it)."""
+    reads, kept alive with it).  ``kv_end``: the entries that its runs read
+    from kv_indices end there (the last request with rows)."""
 
     def __init__(self, info: PlanInfo, host: torch.Tensor, workspace: torch.Tensor,
-                 live=None):
+                 live=None, kv_end: int = 0):
         self.info, self.host, self.workspace, self.live = info, host, workspace, live
+        self.kv_end = kv_end
 
     def __getattr__(self, name):
         return getattr(self.info, name)
@@ -179,6 +181,9 @@ def nvfp4kv_decode_plan(qo_indptr, kv_indptr, last_page_len, num_qo_heads: int,
                        1 if out_dtype == torch.float16 else 0,
                        None if device_last_page_len is None
                        else device_last_page_len.data_ptr())
+    rows = qo.tolist()
+    kv_end = next((int(kv[b]) for b in range(batch, 0, -1) if rows[b] > rows[b - 1]), 0) \
+        if len(rows) > batch >= 0 else 0
     info = PlanInfo()
     dev = -1 if device is None else int(device)
     args = (qo.data_ptr(), kv.data_ptr(), lp.data_ptr(), batch, num_qo_heads, num_kv_heads,
@@ -188,7 +193,7 @@ def nvfp4kv_decode_plan(qo_indptr, kv_indptr, last_page_len, num_qo_heads: int,
                                    _ptr(reuse.workspace), reuse.workspace.numel(),
                                    _stream(stream), C.byref(info))
         if st == _lib.OK:
-            return Plan(info, reuse.host, reuse.workspace, device_last_page_len)
+            return Plan(info, reuse.host, reuse.workspace, device_last_page_len, kv_end)
         if st != _lib.ERR_WORKSPACE_TOO_SMALL:
             check(st, "nvfp4kv_decode_plan")
     st = L.nvfp4kv_decode_plan(*args, None, 0, None, 0, None, C.byref(info))
@@ -200,13 +205,13 @@ def nvfp4kv_decode_plan(qo_indptr, kv_indptr, last_page_len, num_qo_heads: int,
     if not allocate:
         st = L.nvfp4kv_decode_plan(*args, _ptr(host), nhost, None, 0, None, C.byref(info))
         check(st, "nvfp4kv_decode_plan")
-        return Plan(info, host, None, device_last_page_len)
+        return Plan(info, host, None, device_last_page_len, kv_end)
     ws = torch.empty(max(int(info.workspace_bytes), 256), dtype=torch.uint8,
                      device="cuda" if device is None else "cuda:%d" % device)
     st = L.nvfp4kv_decode_plan(*args, _ptr(host), nhost, _ptr(ws), ws.numel(),
                                _stream(stream), C.byref(info))
     check(st, "nvfp4kv_decode_plan")
-    return Plan(info, host, ws, device_last_page_len)
+    return Plan(info, host, ws, device_last_page_len, kv_end)
 
 
 def _outputs(plan: Plan, out, lse, device):

@@ -314,7 +314,9 @@ class _Run:
         if plan.workspace is None:
             raise ValueError("the plan has no workspace (allocate=False)")
         self.rows, self.heads = i.total_qo_rows, i.num_qo_heads
-        self.dk, self.dv, self.pages = i.head_dim_qk, i.head_dim_vo, i.total_kv_pages
+        self.dk, self.dv = i.head_dim_qk, i.head_dim_vo
+        # total_kv_pages leaves out requests without rows, which may stand in between
+        self.pages = max(plan.kv_end, i.total_kv_pages)
         self.dtype = torch.float16 if i.out_dtype == 1 else torch.bfloat16
         self.of = plan.workspace
         self.workspace, self.nbytes = plan.workspace.data_ptr(), plan.workspace.numel()
@@ -339,7 +341,8 @@ def nvfp4kv_e4m3_decode_run(plan: Plan, q: torch.Tensor, cache: E4m3Cache, kv_in
     if kv_indices.dtype != torch.int32 or not kv_indices.is_contiguous():
         raise ValueError("kv_indices must be contiguous torch.int32")
     if kv_indices.numel() < r.pages:
-        raise ValueError("kv_indices has fewer entries than the plan's pages")
+        raise ValueError("kv_indices has %d entries, the plan reads %d"
+                         % (kv_indices.numel(), r.pages))
     dev = torch.cuda.current_device()
     if not (q.get_device() == kv_indices.get_device() == cache.device == r.device == dev):
         _check_device(dev, q, kv_indices, cache.k_data, plan.workspace)

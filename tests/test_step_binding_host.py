@@ -1,0 +1,42 @@
+"""Host-only checks of the serving-step binding against calls that the library
+itself cannot refuse (a pointer carries no length)."""
+import pytest
+import torch
+
+import nvfp4_paged_kv_nvfp4kv_gb300 as N
+
+
+def plan_on_host(qo, kvp, last):
+    """A plan with kernel 5 whose workspace is host memory: a run gets as far as the
+    checks of its arguments."""
+    plan = N.nvfp4kv_decode_plan(qo, kvp, last, 2, 1, 128, 128, kernel=5, num_sms=152,
+                                 ctas_per_sm=3, allocate=False)
+    plan.workspace = torch.zeros(max(int(plan.info.workspace_bytes), 256), dtype=torch.uint8)
+    return plan
+
+
+def run(plan, entries):
+    rows = plan.info.total_qo_rows
+    q = torch.zeros((rows, 2, 128), dtype=torch.bfloat16)
+    cache = N.E4m3Cache.allocate(200, 1, 128, 128, device="cpu")
+    N.nvfp4kv_e4m3_decode_run(plan, q, cache, torch.zeros(entries, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("qo,kvp,last,need", [
+    ([0, 0, 1], [0, 100, 102], [3, 5], 102),        # an idle request in front
+    ([0, 1, 1, 2], [0, 2, 60, 63], [3, 5, 1], 63),  # and in the middle
+    ([0, 1, 1], [0, 2, 60], [3, 5], 2),             # one behind is not read
+    ([0, 1], [0, 7], [16], 7)])
+def test_kv_indices_reach_the_last_request_with_rows(qo, kvp, last, need):
+    plan = plan_on_host(qo, kvp, last)
+    assert plan.kv_end == need
+    units = plan.host[:48 * plan.info.num_units].view(torch.int32).reshape(-1, 12)
+    assert int((units[:, 2] + units[:, 3]).max()) == need  # first page and pages of a unit
+    with pytest.raises(ValueError, match="kv_indices has %d entries, the plan reads %d"
+                       % (need - 1, need)):
+        run(plan, need - 1)
+
+
+def test_a_plan_without_rows_reads_nothing():
+    assert plan_on_host([0, 0], [0, 9], [1]).kv_end == 0
+    assert plan_on_host([0], [0], []).kv_end == 0
