@@ -141,10 +141,17 @@ def nvfp4kv_build_page_table(kv_len, qo_len, block_table, free_pages, free_head,
 
 # ---- rotary positions -------------------------------------------------------------
 class RopePlan:
-    """Frequencies on the device and the layout they belong to."""
+    """Frequencies on the device and the layout they belong to: ``freq`` holds, for
+    each of the rotary_dim / 2 pairs, the turns of a position in units of 2^-64 (a
+    64-bit integer tensor; ``nvfp4kv_rope_plan`` fills one, other tables may come
+    from the caller)."""
 
     def __init__(self, head_dim, rotary_dim, interleaved, attention_factor, freq):
         self.head_dim, self.rotary_dim = int(head_dim), int(rotary_dim)
+        if freq.dtype not in (torch.int64, torch.uint64) or not freq.is_contiguous():
+            raise ValueError("freq must be a contiguous 64-bit integer tensor")
+        if freq.numel() < self.rotary_dim // 2:
+            raise ValueError("freq has fewer entries than rotary_dim / 2")
         self.interleaved = int(bool(interleaved))
         self.attention_factor = float(attention_factor)
         self.freq = freq  # int64 tensor, the bits of the uint64 table

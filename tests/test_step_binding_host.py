@@ -40,3 +40,12 @@ def test_kv_indices_reach_the_last_request_with_rows(qo, kvp, last, need):
 def test_a_plan_without_rows_reads_nothing():
     assert plan_on_host([0, 0], [0, 9], [1]).kv_end == 0
     assert plan_on_host([0], [0], []).kv_end == 0
+
+
+def test_rope_plan_checks_its_table():
+    """A table of the caller's own must hold every pair that the kernel reads."""
+    table = N.nvfp4kv_rope_plan(128, 64, device="cpu").freq
+    assert N.RopePlan(128, 64, False, 1.0, table).rotary_dim == 64
+    for bad in (table[:31], table.int(), table.double(), table.repeat(2)[::2]):
+        with pytest.raises(ValueError):
+            N.RopePlan(128, 64, False, 1.0, bad)
