@@ -460,8 +460,9 @@ typedef struct nvfp4kv_rope_options {
 } nvfp4kv_rope_options;
 
 /* Fill freq_host [host, rotary_dim / 2]: turns a position in units of 2^-64
- * (modulo one turn), the table of nvfp4kv_rope once it is on the device.
- * rotary_dim is even, 2 to 512. */
+ * (modulo one turn, rounded from 106 bits), the table of nvfp4kv_rope once it is
+ * on the device.  rotary_dim is even, 2 to 512; no pair may turn more than 2^40
+ * times a position (a factor far below 1). */
 int nvfp4kv_rope_frequencies(int32_t rotary_dim, const nvfp4kv_rope_options* options,
                              uint64_t* freq_host);
 
@@ -470,7 +471,8 @@ int nvfp4kv_rope_frequencies(int32_t rotary_dim, const nvfp4kv_rope_options* opt
  * (x1, x2) = dims (i, i + rotary_dim / 2), or (2 i, 2 i + 1) when interleaved,
  *   y1 = attention_factor * (x1 cos - x2 sin),
  *   y2 = attention_factor * (x2 cos + x1 sin),
- * in float32 from angles exact to 2^-26 turns at any position, rounded once.
+ * in float32 from angles that are off by at most 1.02 * 2^-26 turns at any
+ * position (with a table of nvfp4kv_rope_frequencies), rounded once.
  *   q [dev]  element (row, head, d) at q[row*q_stride_tok + head*q_stride_head
  *            + d], q_out the same with its strides, k and k_out likewise;
  *            strides in elements, multiples of 8; 16-byte aligned.  q_out may

@@ -64,6 +64,46 @@ bool lie_apart(int64_t run, std::initializer_list<Span> spans) {
   return true;
 }
 
+// ---- sums of two doubles, 106 bits ------------------------------------------
+// The frequency table is multiplied by positions up to 2^31 and holds units of
+// 2^-64 turns: doubles alone are off by 2^11 units.  Error-free sums and products
+// (Dekker 1971, Knuth); products are fused explicitly, so that every machine's
+// compiler computes the same.
+struct Wide {
+  double hi, lo;  // the number hi + lo, |lo| at most half a unit of hi
+};
+constexpr double kMostTurns = 0x1p40;  // a position: past it 106 bits end above 2^-64
+
+Wide two_sum(double a, double b) {
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+Wide add(Wide a, Wide b) {
+  const Wide s = two_sum(a.hi, b.hi), t = two_sum(a.lo, b.lo);
+  const Wide u = two_sum(s.hi, s.lo + t.hi);
+  return two_sum(u.hi, u.lo + t.lo);
+}
+Wide sub(Wide a, Wide b) { return add(a, {-b.hi, -b.lo}); }
+Wide mul(Wide a, Wide b) {
+  const double p = a.hi * b.hi;
+  return two_sum(p, std::fma(a.hi, b.lo, std::fma(a.lo, b.hi, std::fma(a.hi, b.hi, -p))));
+}
+Wide div(Wide a, Wide b) {
+  const double q = a.hi / b.hi;
+  const Wide r = sub(a, mul(b, {q, 0.0}));
+  const double q2 = r.hi / b.hi;
+  const Wide r2 = sub(r, mul(b, {q2, 0.0}));
+  return add(two_sum(q, q2), {r2.hi / b.hi, 0.0});
+}
+Wide power(Wide x, int n) {
+  Wide y{1.0, 0.0};
+  for (; n > 0; n >>= 1) {
+    if (n & 1) y = mul(y, x);
+    x = mul(x, x);
+  }
+  return y;
+}
+
 int check_e4m3_cache(const nvfp4kv_e4m3_cache* c) {
   if (!c) return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "cache is null");
   if (!c->k_data || !c->v_data || !c->k_scale || !c->v_scale)
@@ -175,21 +215,40 @@ int nvfp4kv_rope_frequencies(int32_t rotary_dim, const nvfp4kv_rope_options* o,
       !(o->high_rotations > o->low_rotations && o->low_rotations >= 0.0 &&
         std::isfinite(o->high_rotations)))
     return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "high_rotations must exceed low_rotations >= 0");
-  constexpr double kTwoPi = 6.283185307179586476925;
-  for (int i = 0; i < rotary_dim / 2; ++i) {
-    double f = std::pow(o->base, -2.0 * i / rotary_dim);
+  const int pairs = rotary_dim / 2;
+  const Wide two_pi{6.283185307179586, 2.4492935982947064e-16};  // 2 pi to 2^-106
+  // x = base^(-1 / pairs) by Newton's steps for base x^pairs = 1
+  Wide x{std::pow(o->base, -1.0 / pairs), 0.0};
+  for (int step = 0; step < 2 && pairs > 1; ++step) {
+    const Wide rest = sub({1.0, 0.0}, mul(power(x, pairs), {o->base, 0.0}));
+    x = add(x, mul(x, div(rest, {static_cast<double>(pairs), 0.0})));
+  }
+  const Wide factor{o->factor, 0.0};
+  for (int i = 0; i < pairs; ++i) {
+    Wide f = power(x, i);
     if (o->original_max_position > 0) {
-      const double r = o->original_max_position * f / kTwoPi;
-      double g = (r - o->low_rotations) / (o->high_rotations - o->low_rotations);
-      g = g < 0.0 ? 0.0 : g > 1.0 ? 1.0 : g;
-      f = f * (1.0 - g) / o->factor + f * g;
+      const int64_t n = o->original_max_position;
+      const Wide length = two_sum(static_cast<double>(n >> 32) * 0x1p32,
+                                  static_cast<double>(n & 0xFFFFFFFF));
+      const Wide low{o->low_rotations, 0.0}, high{o->high_rotations, 0.0};
+      Wide g = div(sub(div(mul(length, f), two_pi), low), sub(high, low));
+      if (g.hi < 0.0) g = {0.0, 0.0};
+      if (g.hi >= 1.0) g = {1.0, 0.0};
+      f = add(div(mul(f, sub({1.0, 0.0}, g)), factor), mul(f, g));
     } else {
-      f /= o->factor;
+      f = div(f, factor);
     }
     // turns a position, its whole part dropped, in units of 2^-64
-    double turns = f / kTwoPi;
-    turns -= std::floor(turns);
-    freq_host[i] = static_cast<uint64_t>(std::ldexp(turns, 64));
+    const Wide turns = div(f, two_pi);
+    if (!(turns.hi < kMostTurns))
+      return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "factor %g: a frequency above 2^40 turns a position",
+                  o->factor);
+    Wide part = two_sum(turns.hi - std::floor(turns.hi), turns.lo);
+    if (part.hi < 0.0) part = add(part, {1.0, 0.0});
+    const double units = part.hi * 0x1p64, whole = std::floor(units);  // at most 2^64
+    freq_host[i] = static_cast<uint64_t>(static_cast<unsigned __int128>(whole)) +
+                   static_cast<uint64_t>(static_cast<int64_t>(
+                       std::floor(units - whole + part.lo * 0x1p64 + 0.5)));
   }
   return ok();
 }

@@ -6,8 +6,9 @@
 // others pass through.  Angles: t F_i turns is taken as an exact product of
 // the 32-bit position and F_i in units of 2^-64, modulo 2^64, so whole turns
 // drop out without a rounding whatever the position; the signed top 32 bits,
-// rounded to float32, are the turn in [-1/2, 1/2) to 2^-26, and sincospif of
-// twice that gives sine and cosine to float32's accuracy.  Products and sums
+// rounded to float32, are the turn in [-1/2, 1/2): off by 2^-26 for the rounding,
+// 2^-32 for the bits below and 2^-34 for the table's half unit at position 2^31.
+// sincospif of twice that gives sine and cosine to float32's accuracy.  Products and sums
 // are float32, rounded once to the tensor's type.
 //
 // Bound by HBM for prompts (each element is read and written once) and by
