@@ -565,11 +565,15 @@ bool make_e4m3(bool page1, AttendConfig* cfg) {
 
 bool attend_config_e4m3(int dk, int dv, int page_size, int rows, AttendConfig* cfg) {
   // More than 16 rows: the tensor-memory kernel where it is built, else row
-  // blocks that each read the keys again.  Both sides at head dims 128: 16 rows
-  // 27 here, 35 us there (16 requests of 512-4096 tokens), 56 and 66 us (4 of
-  // 32771); 32 rows 51 and 39 us, 104 and 71 us; 64 rows 74 and 51 us.  At
-  // 256 / 256: 16 rows 84 and 78 us, 32 rows 217 and 84 us (8 requests of
-  // 2048-16384 tokens, 8 kv heads), with 2 kv heads 23 and 27, 31 and 35 us.
+  // blocks that each read the keys again.  Both sides, here and there, 8 requests
+  // of 2048-16384 tokens, us:
+  //   rows a kv head            9          16          24          32
+  //   128/128, 8 kv heads   38   49     40   49     70   52     71   53
+  //            2            20   19     22   20     24   23     25   24
+  //   256/256, 8            85   82     87   83    150   88    208   90
+  //            2            28   30     29   32     37   36     47   40
+  //   256/128, 8            69   72     70   73    120   76    168   77
+  //            2            21   25     22   25     29   28     38   29
   if (rows > 16 && attend_config_e4m3_ext(dk, dv, page_size, rows, cfg)) return true;
   const bool p1 = page_size == 1, wide = rows > 8;
   if (dk == 64 && dv == 64)

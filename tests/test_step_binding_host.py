@@ -49,3 +49,15 @@ def test_rope_plan_checks_its_table():
     for bad in (table[:31], table.int(), table.double(), table.repeat(2)[::2]):
         with pytest.raises(ValueError):
             N.RopePlan(128, 64, False, 1.0, bad)
+
+
+@pytest.mark.parametrize("heads,dims", [(40, 128), (40, 64), (64, 128)])
+def test_chunks_of_one_page_tiles_fill_the_wave(heads, dims):
+    """9 to 16 rows a kv head stream tiles of one page: a chunk is not rounded up to
+    the 8 pages of the tensor-memory kernel's tiles (9 requests of 70 pages, 4 kv
+    heads, 304 CTAs: 8 chunks a request, where 5 of whole tiles would leave 124 idle)."""
+    kvp = [70 * b for b in range(10)]
+    plan = N.nvfp4kv_decode_plan(list(range(10)), kvp, [7] * 9, heads, 4, dims, dims, kernel=5,
+                                 num_sms=152, ctas_per_sm=2, allocate=False)
+    assert plan.info.rows_per_block == 16
+    assert 288 <= plan.info.num_units <= 304
