@@ -15,8 +15,8 @@
 // and 4 B out per page).  One launch serves both: every CTA takes the three
 // sums over all requests for itself (a few loads a thread; a second launch or
 // a grid-wide wait would cost more than the loads), keeps them in shared
-// memory and fills its share of the flat page and row lists, finding the
-// request of four neighbouring entries by one binary search.
+// memory and fills its share of the flat page and row lists, 256 neighbouring
+// pages a warp at a time: two binary searches give the requests that they span.
 // Whether the batch fits is known to every CTA after the sums, so a batch that
 // does not fit writes nothing but the flag.
 // Measured: 64 requests, one token each, 8.2 us replayed (lengths, sums, searches,

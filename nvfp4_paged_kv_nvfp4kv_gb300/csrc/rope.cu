@@ -108,15 +108,14 @@ __global__ void __launch_bounds__(32) rope_kernel(const RopeParams p, int splits
   const int half = p.rotary_dim / 2;
   const int rcols = INTER ? 0 : half / 8;  // half layout: columns of pairs, then passing ones
   const int cols = rope_columns(p);
-  const int wide = min(32, cols), side = 32 / wide;  // heads side by side
-  const int step = splits * side, h0 = part * side + lane / wide;
-  const bool idle = lane / wide >= side;
+  const int side = 32 / cols;  // heads side by side (512 dims have 32 columns)
+  const int step = splits * side, h0 = part * side + lane / cols, c = lane % cols;
+  const bool idle = lane / cols >= side;
   uint4 va[kBatch], vb[kBatch];
   // the column's two chunks: elements d0 .., d1 .. (d1 may lie past the head)
-  auto chunk0 = [&](int c) { return INTER ? 16 * c : c < rcols ? 8 * c : 2 * half + 16 * (c - rcols); };
-  auto chunk1 = [&](int c) { return !INTER && c < rcols ? half + 8 * c : chunk0(c) + 8; };
-  auto load = [&](int c, int h1) {
-    const int d0 = chunk0(c), d1 = chunk1(c);
+  const int d0 = INTER ? 16 * c : c < rcols ? 8 * c : 2 * half + 16 * (c - rcols);
+  const int d1 = !INTER && c < rcols ? half + 8 * c : d0 + 8;
+  auto load = [&](int h1) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int h = h1 + k * step;
@@ -128,55 +127,51 @@ __global__ void __launch_bounds__(32) rope_kernel(const RopeParams p, int splits
       }
     }
   };
-  if (!idle && lane % wide < cols) load(lane % wide, h0);
+  if (!idle) load(h0);
   angles(p, t, sc, lane);
   if (idle) return;
-  for (int c = lane % wide; c < cols; c += wide) {
-    const int d0 = chunk0(c), d1 = chunk1(c);
-    // pairs of this column that turn (8 unless the rotary dims end in it)
-    const int live = INTER ? min(8, max(0, half - 8 * c)) : c < rcols ? 8 : 0;
-    float cs[8], sn[8];
+  // pairs of this column that turn (8 unless the rotary dims end in it)
+  const int live = INTER ? min(8, max(0, half - 8 * c)) : c < rcols ? 8 : 0;
+  float cs[8], sn[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 x = j < live ? sc[8 * c + j] : make_float2(1.f, 0.f);
-      cs[j] = x.x;
-      sn[j] = x.y;
-    }
-    if (c >= wide) load(c, h0);
-    for (int h1 = h0; h1 < heads; h1 += kBatch * step) {
-      if (h1 > h0) load(c, h1);
+  for (int j = 0; j < 8; ++j) {
+    const float2 x = j < live ? sc[8 * c + j] : make_float2(1.f, 0.f);
+    cs[j] = x.x;
+    sn[j] = x.y;
+  }
+  for (int h1 = h0; h1 < heads; h1 += kBatch * step) {
+    if (h1 > h0) load(h1);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int h = h1 + k * step;
-        if (h >= heads) break;
-        uint32_t a[4] = {va[k].x, va[k].y, va[k].z, va[k].w};
-        uint32_t b[4] = {vb[k].x, vb[k].y, vb[k].z, vb[k].w};
-        if constexpr (INTER) {
+    for (int k = 0; k < kBatch; ++k) {
+      const int h = h1 + k * step;
+      if (h >= heads) break;
+      uint32_t a[4] = {va[k].x, va[k].y, va[k].z, va[k].w};
+      uint32_t b[4] = {vb[k].x, vb[k].y, vb[k].z, vb[k].w};
+      if constexpr (INTER) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 x = unpack2<F16>(a[j]), y = unpack2<F16>(b[j]);
-            const uint32_t oa = pack2<F16>(x.x * cs[j] - x.y * sn[j], x.y * cs[j] + x.x * sn[j]);
-            const uint32_t ob = pack2<F16>(y.x * cs[j + 4] - y.y * sn[j + 4],
-                                           y.y * cs[j + 4] + y.x * sn[j + 4]);
-            a[j] = j < live ? oa : a[j];
-            b[j] = j + 4 < live ? ob : b[j];
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 x = unpack2<F16>(a[j]), y = unpack2<F16>(b[j]);
-            const float c0 = cs[2 * j], c1 = cs[2 * j + 1], s0 = sn[2 * j], s1 = sn[2 * j + 1];
-            const uint32_t oa = pack2<F16>(x.x * c0 - y.x * s0, x.y * c1 - y.y * s1);
-            const uint32_t ob = pack2<F16>(y.x * c0 + x.x * s0, y.y * c1 + x.y * s1);
-            a[j] = live ? oa : a[j];
-            b[j] = live ? ob : b[j];
-          }
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = unpack2<F16>(a[j]), y = unpack2<F16>(b[j]);
+          const uint32_t oa = pack2<F16>(x.x * cs[j] - x.y * sn[j], x.y * cs[j] + x.x * sn[j]);
+          const uint32_t ob = pack2<F16>(y.x * cs[j + 4] - y.y * sn[j + 4],
+                                         y.y * cs[j + 4] + y.x * sn[j + 4]);
+          a[j] = j < live ? oa : a[j];
+          b[j] = j + 4 < live ? ob : b[j];
         }
-        uint16_t* out = row_of(p, t, h).out;
-        *reinterpret_cast<uint4*>(out + d0) = make_uint4(a[0], a[1], a[2], a[3]);
-        if (d1 < p.head_dim)
-          *reinterpret_cast<uint4*>(out + d1) = make_uint4(b[0], b[1], b[2], b[3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = unpack2<F16>(a[j]), y = unpack2<F16>(b[j]);
+          const float c0 = cs[2 * j], c1 = cs[2 * j + 1], s0 = sn[2 * j], s1 = sn[2 * j + 1];
+          const uint32_t oa = pack2<F16>(x.x * c0 - y.x * s0, x.y * c1 - y.y * s1);
+          const uint32_t ob = pack2<F16>(y.x * c0 + x.x * s0, y.y * c1 + x.y * s1);
+          a[j] = live ? oa : a[j];
+          b[j] = live ? ob : b[j];
+        }
       }
+      uint16_t* out = row_of(p, t, h).out;
+      *reinterpret_cast<uint4*>(out + d0) = make_uint4(a[0], a[1], a[2], a[3]);
+      if (d1 < p.head_dim)
+        *reinterpret_cast<uint4*>(out + d1) = make_uint4(b[0], b[1], b[2], b[3]);
     }
   }
 }
