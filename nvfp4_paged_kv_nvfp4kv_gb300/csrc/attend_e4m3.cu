@@ -40,10 +40,10 @@
 #include <cmath>
 #include <cstdint>
 
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "device_common.cuh"
+#include "e4m3.cuh"
 #include "epilogue.cuh"
 #include "internal.h"
 
@@ -53,7 +53,6 @@ namespace {
 using namespace dev;
 
 constexpr float kRaiseLog2 = 8.f;
-constexpr float kMinScale = 0x1p-64f, kMaxScale = 0x1p64f;
 
 template <int DK, int DV, int WARPS, int STAGES, int NT>
 struct E4Traits {
@@ -90,26 +89,13 @@ __device__ __forceinline__ int v_pos(int r, int ch) {
   return DV >= 128 ? ch ^ (r & 6) : ch ^ ((r >> 1) & 2);
 }
 
-__device__ __forceinline__ void cp_async_4(uint32_t s, const void* g) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(s), "l"(g));
-}
-__device__ __forceinline__ void cp_async_16a(uint32_t s, const void* g) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(g));
-}
 __device__ __forceinline__ float lds_f32(uint32_t a) { return __uint_as_float(lds_u32<0>(a)); }
 
-// 2^lo <= s <= 2^hi, or the nearer end with the flag set
+// the scale, or the nearer end of the range with the flag set
 __device__ __forceinline__ float checked_scale(float s, uint32_t* flags) {
-  const float c = fminf(fmaxf(s, kMinScale), kMaxScale);
+  const float c = clamped_scale(s);
   if (c != s) atomicOr(flags, 0x20u);
   return c;
-}
-// log2 of a positive normal float, exact for a power of two
-__device__ __forceinline__ float log2_scale(float s) {
-  const uint32_t u = __float_as_uint(s);
-  float r;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(__uint_as_float((u & 0x7FFFFFu) | 0x3F800000u)));
-  return static_cast<float>(static_cast<int>(u >> 23) - 127) + r;
 }
 
 // P1: 1-token pages
@@ -200,16 +186,16 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
       const int r = kr + i * KRI;
       const uint8_t* src = P1 ? kpage + (int64_t)__shfl_sync(0xffffffffu, ids, r) * c.k_sp
                               : kpage + r * c.k_ss;
-      cp_async_16a(st + r * DK + 16 * k_pos<DK>(r, kc), src);
+      cp_async_16s(st + r * DK + 16 * k_pos<DK>(r, kc), src);
     }
 #pragma unroll
     for (int i = 0; i < VN; ++i) {
       const int r = vr + i * VRI;
       const uint8_t* src = P1 ? vpage + (int64_t)__shfl_sync(0xffffffffu, ids, r) * c.v_sp
                               : vpage + r * c.v_ss;
-      cp_async_16a(st + T::OFF_V + r * DV + 16 * v_pos<DV>(r, vc), src);
+      cp_async_16s(st + T::OFF_V + r * DV + 16 * v_pos<DV>(r, vc), src);
     }
-    cp_async_4(st + T::OFF_SC + 4 * lane, scb + (int64_t)(P1 ? ids : pg) * scp);
+    cp_async_4s(st + T::OFF_SC + 4 * lane, scb + (int64_t)(P1 ? ids : pg) * scp);
     cp_async_commit();
   };
   // tile j of this warp into stage js; ids for it are in ids_cur
@@ -229,8 +215,7 @@ __global__ void __launch_bounds__(WARPS * 32, MINB) attend_e4m3_kernel(const Att
 
   // ---- Q: per-row power-of-two prescale into f16, row limits ---------------
   auto q2 = [&](uint32_t w) -> float2 {
-    if (p.q_f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
-    return make_float2(bf16_bits_to_f32(w & 0xFFFFu), bf16_bits_to_f32(w >> 16));
+    return p.q_f16 ? unpack2<true>(w) : unpack2<false>(w);
   };
 #pragma unroll
   for (int k = 0; k < QPT; ++k) {

@@ -52,10 +52,10 @@
 #include <cmath>
 #include <cstdint>
 
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "device_common.cuh"
+#include "e4m3.cuh"
 #include "epilogue.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
@@ -77,7 +77,6 @@ constexpr int kAllSoftmax = 5;  // named barriers 1 .. 4: the column groups
 constexpr int kNanReady = 6;
 constexpr int kPieces = 3;      // of a weight
 constexpr float kRaise = 8.f;  // log2 of the largest weight before m is raised
-constexpr float kMinScale = 0x1p-64f, kMaxScale = 0x1p64f;
 
 // D[tmem] (+)= A[smem] . B[smem], 8-bit operands (the instruction descriptor of
 // kind::f16; formats of A at bit 7 and B at bit 10: 0 E4M3, 1 E5M2)
@@ -119,24 +118,11 @@ __device__ __forceinline__ uint32_t hsub2(uint32_t a, uint32_t b) {
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ void cp_async_16a(uint32_t s, const void* g) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(g));
-}
 // one arrival on `bar` once this thread's earlier cp.async copies have landed
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_addr(bar))
                : "memory");
 }
-__device__ __forceinline__ void cp_async_4(uint32_t s, const void* g) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(s), "l"(g));
-}
-__device__ __forceinline__ float log2_scale(float s) {
-  const uint32_t u = __float_as_uint(s);
-  float r;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(__uint_as_float((u & 0x7FFFFFu) | 0x3F800000u)));
-  return static_cast<float>(static_cast<int>(u >> 23) - 127) + r;
-}
-
 // pairs of f32 (Blackwell's two-wide float32 arithmetic)
 __device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
   uint64_t r;
@@ -386,14 +372,14 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int32_t pg = __shfl_sync(0xffffffffu, pid[g >> 1], 16 * (g & 1) + 4 * k + r4);
-            cp_async_16a(dst + (k >> 1) * 1024 + (k & 1 ? at1 : at0), from + pg * sp + 16 * ch);
+            cp_async_16s(dst + (k >> 1) * 1024 + (k & 1 ? at1 : at0), from + pg * sp + 16 * ch);
           }
         } else {
           const uint8_t* src =
               from + __shfl_sync(0xffffffffu, pid[g >> 1], 16 * (g & 1)) * sp + r4 * ss + 16 * ch;
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            cp_async_16a(dst + (k >> 1) * 1024 + (k & 1 ? at1 : at0), src + 4 * k * ss);
+            cp_async_16s(dst + (k >> 1) * 1024 + (k & 1 ? at1 : at0), src + 4 * k * ss);
         }
       }
     };
@@ -434,8 +420,8 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
         const uint32_t sc = smem_addr(sSc) + (t % SR) * T::SCB + 4 * lane;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          cp_async_4(sc + 128 * g, ksb + pid[g] * c.ksf_sp);
-          cp_async_4(sc + 128 * g + 4 * kTileTok, vsb + pid[g] * c.vsf_sp);
+          cp_async_4s(sc + 128 * g, ksb + pid[g] * c.ksf_sp);
+          cp_async_4s(sc + 128 * g + 4 * kTileTok, vsb + pid[g] * c.vsf_sp);
         }
       }
       const bool withhold = NVFP4KV_E4M3_TEST_SKIP_ARRIVE && blockIdx.x == 0 &&
@@ -565,8 +551,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     // ================= softmax + epilogue ==================================
     const int c0 = (warp >> 2) * NH;  // this thread's first query row
     auto q2 = [&](uint32_t w) -> float2 {
-      if (p.q_f16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
-      return make_float2(bf16_bits_to_f32(w & 0xFFFFu), bf16_bits_to_f32(w >> 16));
+      return p.q_f16 ? unpack2<true>(w) : unpack2<false>(w);
     };
     // ---- Q pieces, swizzled: a thread takes 8 dims (16 bytes) of a row, the
     // row's neighbouring DK / 8 threads share its largest |q| by shuffles --------
@@ -618,7 +603,7 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
           e5m2x4_to_f16(h[e], back[0], back[1]);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&back[k]));
+            const float2 f = unpack2<true>(back[k]);
             rest[2 * e + k].x -= f.x;
             rest[2 * e + k].y -= f.y;
           }
@@ -673,8 +658,8 @@ __global__ void __launch_bounds__(Ext<DK, DV, N>::THREADS, 1)
     auto scores = [&](int i, float (&x)[NH], float& vs) {
       const float* sc = sSc + (i % SR) * (T::SCB / 4) + j;
       const float ks0 = sc[0], vs0 = sc[kTileTok];
-      const float ks = fminf(fmaxf(ks0, kMinScale), kMaxScale);
-      vs = fminf(fmaxf(vs0, kMinScale), kMaxScale);
+      const float ks = clamped_scale(ks0);
+      vs = clamped_scale(vs0);
       if (ks != ks0 || vs != vs0) atomicOr(p.flags, 0x20u);
       const uint64_t ks2 = pack_f32x2(ks, ks);
       uint32_t sv[NH];

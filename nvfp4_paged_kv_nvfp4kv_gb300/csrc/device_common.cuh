@@ -4,6 +4,7 @@
 
 #include <cstdint>
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "internal.h"
@@ -79,6 +80,20 @@ template <int SOFF = 0, int GOFF = SOFF>
 __device__ __forceinline__ void cp_async_16s(uint32_t s, const void* g) {
   asm volatile("cp.async.cg.shared.global [%0+%2], [%1+%3], 16;\n" ::"r"(s), "l"(g), "n"(SOFF),
                "n"(GOFF));
+}
+
+__device__ __forceinline__ void cp_async_4s(uint32_t s, const void* g) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(s), "l"(g));
+}
+
+// Two packed f16 (F16) or bf16 values, the low half first.
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (F16) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  } else {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
 }
 
 // ---- mbarrier ----

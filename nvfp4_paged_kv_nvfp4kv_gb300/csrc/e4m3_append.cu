@@ -26,26 +26,17 @@
 // 6.2 us, a launch and four dependent loads.
 #include <cstdint>
 
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "device_common.cuh"
+#include "e4m3.cuh"
 #include "internal.h"
 
 namespace nvfp4kv {
 namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
-constexpr float kMinScale = 0x1p-64f, kMaxScale = 0x1p64f;
-
-template <bool F16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  if constexpr (F16) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-  } else {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  }
-}
+using dev::unpack2;
 
 // two E4M3 codes, a in the low byte
 __device__ __forceinline__ uint32_t code2(float a, float b) {
@@ -109,7 +100,7 @@ __device__ __forceinline__ void append_block(const E4m3AppendParams& p, int kv, 
   if (a > 0) {
     // no scale of this format: the nearer end, as the attention takes it (the
     // lower for a NaN)
-    const float c_old = fminf(fmaxf(s_old, kMinScale), kMaxScale);
+    const float c_old = dev::clamped_scale(s_old);
     if (c_old != s_old && lane == 0 && p.flags) atomicOr(p.flags, 0x20u);
     s_old = c_old;
     s = fmaxf(s, s_old);

@@ -25,14 +25,15 @@
 // and 34), four waves of CTAs at least (one: 58.5 and 31.5, sixteen: 61 and 45).
 #include <cstdint>
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "device_common.cuh"
 #include "internal.h"
 
 namespace nvfp4kv {
 namespace {
+
+using dev::unpack2;
 
 constexpr int kMaxPairs = 256;  // rotary_dim / 2
 constexpr int kBatch = 2;       // heads whose loads a lane has in flight
@@ -44,14 +45,6 @@ __host__ __device__ __forceinline__ int rope_columns(const RopeParams& p) {
                        : p.rotary_dim / 16 + (p.head_dim - p.rotary_dim + 15) / 16;
 }
 
-template <bool F16>
-__device__ __forceinline__ float2 unpack2(uint32_t w) {
-  if constexpr (F16) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-  } else {
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-  }
-}
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   uint32_t r;
