@@ -431,13 +431,16 @@ typedef struct nvfp4kv_step_table {
  *                 the old one): copy it back, or swap the two, for the next
  *                 step;
  *   batch at most 8192; page_size 1 to 65536 (the caches here have 16 or 1);
- *   a request has at most 2^30 tokens.
+ *   a request has at most 2^30 tokens.  The lists of *out overlap neither the
+ *   inputs nor one another.
  * Entries of the lists past the step's rows and pages, and table entries past
  * a request's pages, are left as they were.  A batch that cannot be (a length
  * below 0 or above 2^30, qo_len > kv_len, more pages than a table row) sets
  * NVFP4KV_FLAG_BAD_LENGTH, one that does not fit the lists or the free list
  * sets NVFP4KV_FLAG_TABLE_FULL in device_flags [dev, may be NULL]; then
- * nothing else is written.  One launch; can be captured in a CUDA graph. */
+ * nothing else is written.  One launch; can be captured in a CUDA graph.
+ * (nvfp4kv_decode_plan takes host copies of the indptrs: a captured step's plan
+ * holds while no request opens a page, with live last page lengths.) */
 int nvfp4kv_build_page_table(const int32_t* kv_len, const int32_t* qo_len, int32_t batch,
                              int32_t page_size, int32_t* block_table,
                              int64_t block_table_stride, int32_t max_pages_per_request,
@@ -451,7 +454,9 @@ int nvfp4kv_build_page_table(const int32_t* kv_len, const int32_t* qo_len, int32
  * frequencies are divided by it where original_max_position is 0; otherwise by
  * parts: with r_i = original_max_position * f_i / 2 pi rotations over the
  * original length, g = clamp((r_i - low) / (high - low), 0, 1) of the
- * frequency is kept, f_i * ((1 - g) / factor + g). */
+ * frequency is kept, f_i * ((1 - g) / factor + g).  The ramp is linear in the
+ * rotations r_i, not in the pair's index i: a model made with another rule needs
+ * a table of its own, in the units of nvfp4kv_rope_frequencies. */
 typedef struct nvfp4kv_rope_options {
   double base;                    /* > 1, for example 10000                  */
   double factor;                  /* > 0; 1: no scaling                      */
@@ -477,7 +482,7 @@ int nvfp4kv_rope_frequencies(int32_t rotary_dim, const nvfp4kv_rope_options* opt
  *            + d], q_out the same with its strides, k and k_out likewise;
  *            strides in elements, multiples of 8; 16-byte aligned.  q_out may
  *            be q (and k_out k) with the same strides; otherwise an output
- *            must not overlap an input.  num_qo_heads or num_kv_heads may be
+ *            must not overlap an input or the other output.  num_qo_heads or num_kv_heads may be
  *            0 (its pointers are not read).
  *   positions [dev, num_tokens]  any int32; rows past num_tokens stay.
  *   head_dim  a multiple of 8, at most 512; rotary_dim even, at most head_dim.
@@ -528,12 +533,16 @@ typedef struct nvfp4kv_e4m3_cache {
  *            strides in elements, multiples of 8; 16-byte aligned; v likewise.
  *   dtype    0 bf16, 1 f16.
  *   num_rows rows that k and v hold; those past qo_indptr[batch] are not read.
+ *   kv_indices [dev]  kv_indptr[batch] entries: its length is not an argument, so
+ *            kv_indptr is taken as it stands (nvfp4kv_build_page_table writes both,
+ *            or neither, within their capacities).
  *   device_flags [dev, may be NULL]  a request whose rows, lengths or page
  *            count cannot be is skipped, and so is a page id out of the pool:
  *            NVFP4KV_FLAG_BAD_APPEND_TARGET; an old scale outside the range:
  *            NVFP4KV_FLAG_BAD_SCALE.
- * Two requests must not write the same page in one call (its scale and codes
- * would be of either).  One launch; can be captured in a CUDA graph. */
+ * A call must not write one page twice, for two requests or in two places of one
+ * (its scale and codes would be of either).  One launch; can be captured in a CUDA
+ * graph. */
 int nvfp4kv_e4m3_append(const nvfp4kv_e4m3_cache* cache, const void* k, int64_t k_stride_tok,
                         int64_t k_stride_head, const void* v, int64_t v_stride_tok,
                         int64_t v_stride_head, int32_t dtype, int32_t num_rows,
@@ -545,6 +554,12 @@ int nvfp4kv_e4m3_append(const nvfp4kv_e4m3_cache* cache, const void* k, int64_t 
  * split, merge, live lengths, outputs and flags.
  *   q [dev]  as in nvfp4kv_decode_run; q_dtype 0 bf16, 1 f16.
  *   out [dev]  8-byte aligned.
+ * kv_indices [dev] holds every entry up to the end of the last request with rows.
+ * Scores are float32 sums of products without a rounding, and so are row sums and
+ * lse.  A weight is rounded before it meets the value codes: to f16 (2^-11
+ * relative) up to 16 query rows per kv head, above them (where the head dims are
+ * 128 or 256) to three E4M3 pieces of that, 2^-12 more and at least 2^-20 of the
+ * row's largest weight times scale.
  * A scale outside [2^-64, 2^64] sets NVFP4KV_FLAG_BAD_SCALE.  Slots past a
  * request's length may hold anything.  A row with a NaN or an infinity in its
  * query, or a NaN in a key that it sees, is NaN and so is its lse; a NaN value
