@@ -65,3 +65,13 @@ def test_nan_in_the_last_of_many_tiles(dk, dv, chunk):
                                force_chunk_tokens=chunk, seed=dv)
     assert rows_of(plan) > 16
     assert math.isnan(float(o[new - 1, 0, 3])) and not math.isnan(float(o[0, 0, 3]))
+
+
+@pytest.mark.parametrize("dk,dv", [(256, 256), (128, 128)])
+@pytest.mark.parametrize("chunk", [0, 640])
+def test_live_lengths_of_many_tiles(dk, dv, chunk):
+    """A plan made with other last page lengths reads the current ones: the tile in
+    which the request ends, and the rows' limits, move with them."""
+    for kv, planned in (((1110, 700), [1, 16]), ((1121, 690), [16, 1])):
+        T.attend_case(kv, (20, 33), 4, 2, dk, dv, causal=True, live=planned, layout="NHD",
+                      force_chunk_tokens=chunk, seed=dk)
