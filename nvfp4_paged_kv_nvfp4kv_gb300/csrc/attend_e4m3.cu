@@ -31,11 +31,14 @@
 //    does not see whole the codes are taken out of the product, and the first
 //    such token of each value dim makes that dim NaN in the rows that see it.
 // HBM bounds it: Dk + Dv bytes a token and kv head.  Measured (replayed): 4
-// requests of 32771 tokens, 8 kv heads of 128, 49 us, 5.5 TB/s (0.82 of a plain
-// copy; the tile loop alone runs at 7); 16 of 512-4096 tokens 20.7 us, 3.6 TB/s:
+// requests of 32771 tokens, 8 kv heads of 128, 49.7 us, 5.4 TB/s (0.81 of a plain
+// copy; the tile loop alone runs at 7); 16 of 512-4096 tokens 20.6 us, 3.6 TB/s:
 // 4 us of launch, 3 to the first tile, 9 of loop, 2.4 of combining and folding the
-// splits; 8 of 2048-8192 tokens at 512 / 256 dims 20.9 us, 3.0 TB/s; two short
-// requests 6.2 us.
+// splits; 8 of 2048-8192 tokens at 512 / 256 dims 22 us, 2.9 TB/s; two short
+// requests 6.2 us.  The same 4 requests, calls back to back in one graph (128/128
+// 45.6 us), at 64/64, 256/128, 256/256, 512/256: 26.8, 63.7, 86.4, 118.7 us, 0.75 to
+// 1.0 of a copy; with 1-token pages, a row's address and page id each: 42.3 (64/64),
+// 64.0 (128/128), 110 (256/256), 146 us (512/256).
 #include <climits>
 #include <cmath>
 #include <cstdint>

@@ -42,11 +42,13 @@
 // bounded; one that runs out sets flag 0x4 and the CTA winds down.
 //
 // Measured: 32 requests of 2000-16000 tokens, 16 new rows of 32 heads each (64
-// rows to a kv head), 170 us, 3.6 TB/s, 0.54 of a plain copy; 4 requests of 32771
-// tokens x 32 rows 71 us; prompts of 512 rows 82 us.  No unit is full (issue slots
-// 60 %, shared memory 45 %, products a third): a tile's way through the warps
+// rows to a kv head), 170 us, 3.6 TB/s, 0.54 of a plain copy (1-token pages 296: the
+// loaders form an address a row); 4 requests of 32771 tokens x 32 rows 73 us.  At
+// 256/256 and 256/128, blocks of 32 rows that each read the keys, 493 and 419 us.  8
+// prompts of 512 tokens from nothing 170 us.  No unit is full (issue slots
+// 58 %, shared memory 45 %, products a third): a tile's way through the warps
 // bounds it, 1.1 us at either N, and a unit's 12 tiles' worth of start and end.
-// Timed with parts left out: half the query pieces, half of O^T's products, no
+// Timed with parts left out: two query pieces, half of O^T's products, no
 // conversions of weights or no votes change nothing; no loads take 10 % off.
 #include <climits>
 #include <cmath>
