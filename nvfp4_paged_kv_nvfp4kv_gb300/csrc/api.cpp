@@ -151,6 +151,7 @@ bool lookup_kernel(int kind, int dk, int dv, int page_size, int rows, AttendConf
 // tiles: 25 plans (batches of 13-100 requests, 1 to 6 pieces the longest) fit
 // time = 1.16 us x the busiest SM's tiles and units to 3 % with 12.
 constexpr int64_t kUnitTiles = 12;
+constexpr int kMostModelled = 4096;  // CTAs of a plan whose loads the planner models
 constexpr int kMinChunkPages = 8;
 
 // The bulk-copy decode kernel reads each (page, head) region of the four
@@ -469,13 +470,16 @@ int nvfp4kv_decode_plan(const int32_t* qo_indptr_h, const int32_t* kv_indptr_h,
     // 100-60000 332 -> 246 us; even batches keep their whole requests.
     if (kind == kKernelE4m3 && rows_per_block > 16 && opts.force_chunk_tokens == 0 &&
         opts.max_splits == 0 && max_np > kMinChunkPages) {
-      std::vector<int64_t> sms(num_sms);  // a heap, the least loaded SM first
+      // a heap, the least loaded SM first (a SM past the most units that are
+      // looked at stays idle: an option may name any number of them)
+      const int bins = std::min<int>(num_sms, kMostModelled);
+      std::vector<int64_t> sms(bins);
       std::vector<std::pair<int64_t, int64_t>> rest;  // units that are not whole chunks
       int64_t least = INT64_MAX, best = chunk, mean = 0;
       for (int j : {1, 2, 3, 4, 5, 6, 8, 0}) {  // pieces; 0: one wave's chunk
         int64_t c = j == 0 ? chunk : (max_np + j - 1) / j;
         c = std::min<int64_t>(std::max<int64_t>((c + 7) / 8 * 8, kMinChunkPages), max_np);
-        if (ctas_for(c) > 4096) continue;  // (so many even out by themselves)
+        if (ctas_for(c) > kMostModelled) continue;  // (so many even out by themselves)
         auto cost = [](int64_t pages) { return (pages + 7) / 8 + kUnitTiles; };
         int64_t full = 0, work = 0, most = 0;
         rest.clear();
@@ -486,14 +490,14 @@ int nvfp4kv_decode_plan(const int32_t* qo_indptr_h, const int32_t* kv_indptr_h,
           if (nt[b] % c) rest.push_back({cost(nt[b] % c), alike});
         }
         std::sort(rest.begin(), rest.end(), std::greater<>());
-        sms.assign(num_sms, 0);
+        sms.assign(bins, 0);
         auto add = [&](int64_t x, int64_t times) {
           work += x * times;
           for (; times > 0; --times) {
             const int64_t v = sms[0] + x;
             int at = 0;
-            for (int k; (k = 2 * at + 1) < num_sms; at = k) {
-              if (k + 1 < num_sms && sms[k + 1] < sms[k]) ++k;
+            for (int k; (k = 2 * at + 1) < bins; at = k) {
+              if (k + 1 < bins && sms[k + 1] < sms[k]) ++k;
               if (sms[k] >= v) break;
               sms[at] = sms[k];
             }

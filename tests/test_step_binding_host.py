@@ -1,9 +1,14 @@
 """Host-only checks of the serving-step binding against calls that the library
 itself cannot refuse (a pointer carries no length)."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 import nvfp4_paged_kv_nvfp4kv_gb300 as N
+from nvfp4_paged_kv_nvfp4kv_gb300 import _lib
 
 
 def plan_on_host(qo, kvp, last):
@@ -61,3 +66,33 @@ def test_chunks_of_one_page_tiles_fill_the_wave(heads, dims):
                                  num_sms=152, ctas_per_sm=2, allocate=False)
     assert plan.info.rows_per_block == 16
     assert 288 <= plan.info.num_units <= 304
+
+
+_MANY_SMS = """
+import ctypes as C, importlib.util, resource, sys, types
+sys.modules["torch"] = types.ModuleType("torch")  # (its address space is not the library's)
+resource.setrlimit(resource.RLIMIT_AS, (4 << 30, 4 << 30))
+pkg = types.ModuleType("pkg"); pkg.__path__ = [sys.argv[1]]; sys.modules["pkg"] = pkg
+import pkg._lib as L
+lib = L.load()
+a = lambda x: (C.c_int32 * len(x))(*x)
+qo, kv, last = a([0, 20, 40]), a([0, 200, 500]), a([3, 4])
+for sms in (152, 4096, 2 ** 31 - 1):
+    opts, info = L.PlanOptions(1, 0, 0, 0, 5, sms, 1, 0, None), L.PlanInfo()
+    st = lib.nvfp4kv_decode_plan(qo, kv, last, 2, 8, 2, 128, 128, 16, C.byref(opts), -1, None, 0,
+                                 None, 0, None, C.byref(info))
+    print(sms, st, info.num_units)
+"""
+
+
+def test_plan_for_any_number_of_sms():
+    """The option num_sms names any number: the plan's model of their loads takes no
+    memory for SMs that stay idle, and the C entry does not end the process (4 GB of
+    address space)."""
+    run = subprocess.run([sys.executable, "-c", _MANY_SMS, os.path.dirname(_lib.__file__)],
+                         capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
+    lines = [line.split() for line in run.stdout.splitlines()]
+    assert [int(x[0]) for x in lines] == [152, 4096, 2 ** 31 - 1]
+    assert all(int(x[1]) in (_lib.OK, _lib.ERR_WORKSPACE_TOO_SMALL) for x in lines)
+    assert all(int(x[2]) > 0 for x in lines)
