@@ -86,6 +86,10 @@ typedef enum nvfp4kv_status {
                                            page count cannot be            */
 #define NVFP4KV_FLAG_TABLE_FULL 0x80u   /* page table: the step's rows, pages
                                            or new pages do not fit         */
+#define NVFP4KV_FLAG_BAD_TREE 0x100u    /* a drafted node whose parent does not
+                                           stand before it                 */
+#define NVFP4KV_FLAG_BAD_SHARES 0x200u  /* a page given up more often than it
+                                           has owners                      */
 
 const char* nvfp4kv_status_string(int status);
 const char* nvfp4kv_last_error_detail(void);
@@ -497,6 +501,25 @@ int nvfp4kv_rope(const void* q, int64_t q_stride_tok, int64_t q_stride_head, voi
                  int32_t rotary_dim, int32_t interleaved, int32_t dtype, const uint64_t* freq,
                  float attention_factor, cudaStream_t stream);
 
+/* The norms of the query and key heads and their rotary positions in one pass: a head x
+ * becomes n = x / sqrt(sum_d x_d^2 / head_dim + eps) * (weight + weight_offset), then n
+ * turns as in nvfp4kv_rope (dims from rotary_dim on are n as it is), in float32, rounded
+ * once.  A head with an infinity is NaN there and in its pair and 0 elsewhere.
+ *   q_weight, k_weight [dev, head_dim]  16-byte aligned, not read for 0 heads;
+ *   weight_dtype  that of the rows (dtype) or 2: float32;
+ *   weight_offset 1 for weights that are kept around 0;
+ *   eps       in [1e-20, 1e20].
+ * The other arguments are those of nvfp4kv_rope (in place too).  One launch; can be
+ * captured in a CUDA graph. */
+int nvfp4kv_norm_rope(const void* q, int64_t q_stride_tok, int64_t q_stride_head, void* q_out,
+                      int64_t q_out_stride_tok, int64_t q_out_stride_head, int32_t num_qo_heads,
+                      const void* k, int64_t k_stride_tok, int64_t k_stride_head, void* k_out,
+                      int64_t k_out_stride_tok, int64_t k_out_stride_head, int32_t num_kv_heads,
+                      int32_t num_tokens, const int32_t* positions, int32_t head_dim,
+                      int32_t rotary_dim, int32_t interleaved, int32_t dtype, const uint64_t* freq,
+                      float attention_factor, const void* q_weight, const void* k_weight,
+                      int32_t weight_dtype, float weight_offset, float eps, cudaStream_t stream);
+
 /* ---- the E4M3 cache ------------------------------------------------------------ */
 /* A paged cache of 8-bit E4M3 codes with one float32 scale per page and kv
  * head, for layers whose keys or values 4 bits hurt: K = code * k_scale[page,
@@ -569,6 +592,133 @@ int nvfp4kv_e4m3_decode_run(const nvfp4kv_plan_info* info, const void* q, int64_
                             const nvfp4kv_e4m3_cache* cache, const int32_t* kv_indices,
                             float sm_scale, void* workspace, uint64_t workspace_bytes, void* out,
                             float* lse, cudaStream_t stream);
+
+/* ---- drafted trees --------------------------------------------------------------- */
+/* A step that verifies drafted tokens: request b's n_b rows of the step (its last
+ * tokens, as everywhere here) are the nodes of a tree, or of several, each behind the
+ * node that it continues.  Such a step is nvfp4kv_tree_masks, nvfp4kv_norm_rope or
+ * nvfp4kv_rope, an append, nvfp4kv_tree_run; then, once the path of accepted nodes is
+ * known, nvfp4kv_compact_tokens and nvfp4kv_release_pages. */
+
+/* What each node sees of its tree, and where it stands.
+ *   parents [dev, num_rows]  of row qo_indptr[b] + i: the index (below i) of the node
+ *                 of request b that node i continues, -1 for a root;
+ *   qo_indptr [dev, batch + 1], kv_len [dev, batch]  tokens with the step's;
+ *   tree_mask [dev, num_rows x mask_words]  bit j & 31 of word j >> 5 of a row: whether
+ *                 node j is the row's node itself or one that it continues, directly
+ *                 or through others; other bits 0;
+ *   positions [dev, num_rows]  kv_len - n_b + the node's depth (0 for a root);
+ *   mask_words    1 to 32: trees of up to 32 * mask_words nodes.
+ * A parent that is not below its node sets NVFP4KV_FLAG_BAD_TREE (the node stands as a
+ * root); a request whose rows or lengths cannot be, or with more nodes than the words
+ * hold, is left out: NVFP4KV_FLAG_BAD_LENGTH in device_flags [dev, may be NULL].  One
+ * launch; can be captured in a CUDA graph. */
+int nvfp4kv_tree_masks(const int32_t* parents, const int32_t* qo_indptr, const int32_t* kv_len,
+                       int32_t batch, int32_t num_rows, int32_t mask_words, uint32_t* tree_mask,
+                       int32_t* positions, uint32_t* device_flags, cudaStream_t stream);
+
+/* Attention of the nodes: nvfp4kv_decode_run, but a row sees every token before its
+ * request's rows and of these rows' tokens those whose bits are set in its mask.
+ *   info          a plan of kernel 1 or 3 (0 chooses one of them); its causal option is
+ *                 not used;
+ *   tree_mask [dev, rows x mask_words]  as nvfp4kv_tree_masks writes it, or any bits (a row
+ *                 need not see its own token); tokens past the words are not seen, bits
+ *                 past the request's rows not read.  A row that sees nothing has out 0
+ *                 and lse -inf.
+ *   new_k, new_v  NULL, or the step's new tokens, quantised into their pages by the same
+ *                 launch as in nvfp4kv_decode_append_run.
+ * The request's tokens are finite in the cache, as nvfp4kv_quantize_append stores them. */
+int nvfp4kv_tree_run(const nvfp4kv_plan_info* info, const uint32_t* tree_mask, int32_t mask_words,
+                     const void* new_k_bf16, int64_t k_stride_tok, int64_t k_stride_head,
+                     const void* new_v_bf16, int64_t v_stride_tok, int64_t v_stride_head,
+                     const void* q_bf16, int64_t q_stride_tok, int64_t q_stride_head,
+                     const nvfp4kv_paged_cache* cache, const int32_t* kv_indices, float sm_scale,
+                     void* workspace, uint64_t workspace_bytes, void* out_bf16, float* lse,
+                     cudaStream_t stream);
+
+/* The accepted tokens moved together: with n_b = qo_indptr[b + 1] - qo_indptr[b] drafted
+ * tokens at the end of request b's L_b (the page table of the step), the token at
+ * position L_b - n_b + path[b][i] goes to L_b - n_b + i for i < num_kept[b], as if all
+ * were read before any is written.  Tokens behind those are void (their slots are left,
+ * the scale of a page of the E4M3 cache may change).
+ *   path [dev]    entry (b, i) at path[b * path_stride + i], i < path_width; node numbers
+ *                 in rising order;
+ *   num_kept [dev, batch]  0 to n_b.
+ * Codes and scales are moved as they are; but in pages of 16 tokens of the E4M3 cache
+ * the target page gets the largest of the scales that its tokens had (in [2^-64, 2^64],
+ * others as NVFP4KV_FLAG_BAD_SCALE says), and the codes of the others become
+ * E4M3_RNE(code * (old / new)).  A request whose lengths, count or path cannot be is
+ * left as it is: NVFP4KV_FLAG_BAD_APPEND_TARGET; so are a token with a page id out of
+ * the pool and, in the E4M3 cache, the others of its target page:
+ * NVFP4KV_FLAG_BAD_PAGE_INDEX.  No page may be listed twice.  One launch; can be captured
+ * in a CUDA graph. */
+int nvfp4kv_compact_tokens(const nvfp4kv_paged_cache* cache, const int32_t* path,
+                           int64_t path_stride, int32_t path_width, const int32_t* num_kept,
+                           const int32_t* qo_indptr, const int32_t* kv_indptr,
+                           const int32_t* kv_indices, const int32_t* last_page_len, int32_t batch,
+                           uint32_t* device_flags, cudaStream_t stream);
+int nvfp4kv_e4m3_compact_tokens(const nvfp4kv_e4m3_cache* cache, const int32_t* path,
+                                int64_t path_stride, int32_t path_width, const int32_t* num_kept,
+                                const int32_t* qo_indptr, const int32_t* kv_indptr,
+                                const int32_t* kv_indices, const int32_t* last_page_len,
+                                int32_t batch, uint32_t* device_flags, cudaStream_t stream);
+
+/* ---- pages with several owners ------------------------------------------------------ */
+/* page_shares [dev, num_pages] counts the owners of a page beyond the first: 0 for pages of
+ * one request, for those of the free list, and for the pages that
+ * nvfp4kv_build_page_table takes off it.  The block table, its rows and kv_len are those
+ * of nvfp4kv_build_page_table (kv_len of the rows' requests, 0 for a row without one).
+ *
+ * Fork requests: row children[f] of the table becomes a request of kv_len[parents[f]]
+ * tokens that shares the whole pages of row parents[f] and, where the last page is not
+ * full, gets a new one off the free list, in the order of the forks.  kv_len[children[f]]
+ * is set; (copy_src[f], copy_dst[f]) is the parent's last page and the new one, for
+ * nvfp4kv_copy_pages on the cache of every layer, or (-1, -1).
+ *   num_forks at most 8192, num_rows (of the table and kv_len) at most 65536; a parent may
+ *             be forked several times, a child's row must not appear twice;
+ *   free_head [dev, 1] and free_head_out [dev, 1]: two words, as in
+ *             nvfp4kv_build_page_table.
+ * A row out of range, twice a child or child and parent, or a length that cannot be, sets
+ * NVFP4KV_FLAG_BAD_LENGTH, a free list that is too short NVFP4KV_FLAG_TABLE_FULL; then
+ * nothing else is written.  A page id out of the pool is passed on and sets
+ * NVFP4KV_FLAG_BAD_PAGE_INDEX.  One launch; can be captured in a CUDA graph. */
+int nvfp4kv_fork_pages(const int32_t* parents, const int32_t* children, int32_t num_forks,
+                       int32_t* kv_len, int32_t num_rows, int32_t page_size,
+                       int32_t* block_table, int64_t block_table_stride,
+                       int32_t max_pages_per_request, int32_t* page_shares, int32_t num_pages,
+                       const int32_t* free_pages, int32_t num_free, const int32_t* free_head,
+                       int32_t* free_head_out, int32_t* copy_src, int32_t* copy_dst,
+                       uint32_t* device_flags, cudaStream_t stream);
+
+/* Copy pages: everything that page src[i] of the pool holds to page dst[i], i < num.  A
+ * pair (-1, -1) is passed over; another id out of the pool sets
+ * NVFP4KV_FLAG_BAD_PAGE_INDEX and its pair is left out.  A page that is written must not
+ * be in another pair.  One launch; can be captured in a CUDA graph. */
+int nvfp4kv_copy_pages(const nvfp4kv_paged_cache* cache, const int32_t* src, const int32_t* dst,
+                       int32_t num, uint32_t* device_flags, cudaStream_t stream);
+int nvfp4kv_e4m3_copy_pages(const nvfp4kv_e4m3_cache* cache, const int32_t* src,
+                            const int32_t* dst, int32_t num, uint32_t* device_flags,
+                            cudaStream_t stream);
+
+/* Give pages up: row b keeps its first keep_len[b] of kv_len[b] tokens (0: the request
+ * ends) and leaves the pages ceil(keep_len / page_size) .. of its row, whose entries stay
+ * as they are; kv_len[b] becomes keep_len[b].  A page that its last owner leaves goes
+ * back in front of the free list's head: the pages freed stand at
+ * free_pages[head - freed .. head) in the order of the first entry (by row, then by
+ * column) that names them, and free_head_out, which may be free_head, becomes head -
+ * freed.
+ *   num_rows at most 8192.
+ * A length that cannot be (keep_len > kv_len among them) sets NVFP4KV_FLAG_BAD_LENGTH, a
+ * head that is smaller than the pages freed NVFP4KV_FLAG_TABLE_FULL; then nothing else is
+ * changed.  A page id out of the pool is passed over: NVFP4KV_FLAG_BAD_PAGE_INDEX; a page
+ * that is left more often than it has owners is freed once: NVFP4KV_FLAG_BAD_SHARES.  One
+ * launch; can be captured in a CUDA graph. */
+int nvfp4kv_release_pages(const int32_t* keep_len, int32_t* kv_len, int32_t num_rows,
+                          int32_t page_size, const int32_t* block_table,
+                          int64_t block_table_stride, int32_t max_pages_per_request,
+                          int32_t* page_shares, int32_t num_pages, int32_t* free_pages,
+                          int32_t num_free, const int32_t* free_head, int32_t* free_head_out,
+                          uint32_t* device_flags, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -10,5 +10,8 @@ from .api import (NvFp4KvError, PagedCache, Plan, default_sm_scale,  # noqa: F40
                   nvfp4kv_static_workspace_flags,
                   nvfp4kv_decode_append_run, nvfp4kv_dequantize_paged)
 from .step import (E4m3Cache, RopePlan, StepTable, nvfp4kv_build_page_table,  # noqa: F401
-                   nvfp4kv_e4m3_append, nvfp4kv_e4m3_decode_run, nvfp4kv_rope,
-                   nvfp4kv_rope_plan)
+                   nvfp4kv_e4m3_append, nvfp4kv_e4m3_decode_run, nvfp4kv_norm_rope,
+                   nvfp4kv_rope, nvfp4kv_rope_plan)
+from .tree import (nvfp4kv_compact_tokens, nvfp4kv_copy_pages,  # noqa: F401
+                   nvfp4kv_e4m3_compact_tokens, nvfp4kv_e4m3_copy_pages, nvfp4kv_fork_pages,
+                   nvfp4kv_release_pages, nvfp4kv_tree_masks, nvfp4kv_tree_run)

@@ -30,6 +30,8 @@ FLAG_PACE_TIMEOUT = 0x10
 FLAG_BAD_SCALE = 0x20
 FLAG_BAD_LENGTH = 0x40
 FLAG_TABLE_FULL = 0x80
+FLAG_BAD_TREE = 0x100
+FLAG_BAD_SHARES = 0x200
 
 
 class PagedCacheStruct(C.Structure):
@@ -131,6 +133,24 @@ SIGNATURES = {
     "nvfp4kv_e4m3_decode_run": (C.c_int, [
         C.POINTER(PlanInfo), _vp, _i64, _i64, _i32, C.POINTER(E4m3CacheStruct), _vp, _f32, _vp,
         _u64, _vp, _vp, _vp]),
+    "nvfp4kv_norm_rope": (C.c_int, [
+        _vp, _i64, _i64, _vp, _i64, _i64, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _i32, _i32,
+        _vp, _i32, _i32, _i32, _i32, _vp, _f32, _vp, _vp, _i32, _f32, _f32, _vp]),
+    "nvfp4kv_tree_masks": (C.c_int, [_vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp]),
+    "nvfp4kv_tree_run": (C.c_int, [
+        C.POINTER(PlanInfo), _vp, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64,
+        C.POINTER(PagedCacheStruct), _vp, _f32, _vp, _u64, _vp, _vp, _vp]),
+    "nvfp4kv_compact_tokens": (C.c_int, [
+        C.POINTER(PagedCacheStruct), _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "nvfp4kv_e4m3_compact_tokens": (C.c_int, [
+        C.POINTER(E4m3CacheStruct), _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "nvfp4kv_fork_pages": (C.c_int, [
+        _vp, _vp, _i32, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp,
+        _vp, _vp]),
+    "nvfp4kv_copy_pages": (C.c_int, [C.POINTER(PagedCacheStruct), _vp, _vp, _i32, _vp, _vp]),
+    "nvfp4kv_e4m3_copy_pages": (C.c_int, [C.POINTER(E4m3CacheStruct), _vp, _vp, _i32, _vp, _vp]),
+    "nvfp4kv_release_pages": (C.c_int, [
+        _vp, _vp, _i32, _i32, _vp, _i64, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp]),
 }
 
 

@@ -19,9 +19,9 @@
 #include "internal.h"
 
 namespace nvfp4kv {
-bool attend_config_tc(int dk, int dv, int rows, AttendConfig* cfg);
+bool attend_config_tc(int dk, int dv, int rows, bool tree, AttendConfig* cfg);
 bool attend_config_simt(int dk, int dv, int rows, AttendConfig* cfg);
-bool attend_config_tcgen05(int dk, int dv, int rows, AttendConfig* cfg);
+bool attend_config_tcgen05(int dk, int dv, int rows, bool tree, AttendConfig* cfg);
 bool attend_config_dec(int dk, int dv, int rows, int quads, AttendConfig* cfg);
 bool attend_config_tc_fp4qp(int dk, int dv, int rows, int pass, AttendConfig* cfg);
 cudaError_t prepare_kernel(const AttendConfig& cfg);
@@ -138,10 +138,13 @@ CacheView view_of(const nvfp4kv_paged_cache* c) {
   return v;
 }
 
-bool lookup_kernel(int kind, int dk, int dv, int page_size, int rows, AttendConfig* cfg) {
-  if (kind == kKernelTensorCore) return attend_config_tc(dk, dv, rows, cfg);
+// `tree`: the kernel's form that looks the step's tokens up in the rows' masks
+bool lookup_kernel(int kind, int dk, int dv, int page_size, int rows, AttendConfig* cfg,
+                   bool tree = false) {
+  if (kind == kKernelTensorCore) return attend_config_tc(dk, dv, rows, tree, cfg);
+  if (kind == kKernelTcgen05) return attend_config_tcgen05(dk, dv, rows, tree, cfg);
+  if (tree) return false;
   if (kind == kKernelCudaCore) return attend_config_simt(dk, dv, rows, cfg);
-  if (kind == kKernelTcgen05) return attend_config_tcgen05(dk, dv, rows, cfg);
   if (kind == kKernelFp4QP) return attend_config_tc_fp4qp(dk, dv, rows, 2, cfg);
   if (kind == kKernelE4m3) return attend_config_e4m3(dk, dv, page_size, rows, cfg);
   return false;
@@ -740,6 +743,10 @@ AttendParams run_params(const nvfp4kv_plan_info* info, const void* q, int64_t qs
 }  // namespace
 
 namespace nvfp4kv {
+int check_paged_cache(const nvfp4kv_paged_cache* cache, bool for_attention) {
+  return check_cache(cache, for_attention);
+}
+
 // The argument checks of nvfp4kv_decode_run, for entry points that must
 // validate before they enqueue anything of their own.
 int validate_run(const nvfp4kv_plan_info* info, const void* q, int64_t qst, int64_t qsh,
@@ -751,6 +758,11 @@ int validate_run(const nvfp4kv_plan_info* info, const void* q, int64_t qst, int6
 
 namespace {
 
+struct TreeMask {
+  const uint32_t* mask;
+  int32_t words;
+};
+
 struct NewTokens {
   const void* k = nullptr;
   const void* v = nullptr;
@@ -760,10 +772,20 @@ struct NewTokens {
 int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_tok,
            int64_t q_stride_head, const nvfp4kv_paged_cache* cache, const int32_t* kv_indices,
            float sm_scale, void* workspace, uint64_t workspace_bytes, void* out_bf16,
-           float* lse, cudaStream_t stream, const NewTokens* nt) {
+           float* lse, cudaStream_t stream, const NewTokens* nt, const TreeMask* tree = nullptr) {
   if (int st = check_run(info, q_bf16, q_stride_tok, q_stride_head, cache, kv_indices,
                          workspace, workspace_bytes, out_bf16))
     return st;
+  if (tree) {
+    if (info->kernel != kKernelTensorCore && info->kernel != kKernelTcgen05)
+      return fail(NVFP4KV_ERR_UNSUPPORTED, "trees run in the tensor-core kernels (plan option "
+                  "kernel 0, 1 or 3)");
+    if (tree->words < 1 || tree->words > kMaxTreeNodes / 32)
+      return fail(NVFP4KV_ERR_UNSUPPORTED, "mask_words %d (1 to %d)", tree->words,
+                  kMaxTreeNodes / 32);
+    if (info->num_units > 0 && (!tree->mask || !aligned(tree->mask, 4)))
+      return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "tree_mask null or misaligned");
+  }
   if (nt) {
     if (info->kernel != kKernelTensorCore && info->kernel != kKernelTcgen05 &&
         info->kernel != kKernelFp4QP)
@@ -781,12 +803,12 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
   // a tensor-core plan of one block of <= 8 rows runs the bulk-copy decode
   // kernel when the cache layout allows it (same arithmetic, same occupancy
   // or better: the plan's one-wave grid stays one wave)
-  const bool dec = info->kernel == kKernelTensorCore && info->rows_per_block == 8 &&
+  const bool dec = !tree && info->kernel == kKernelTensorCore && info->rows_per_block == 8 &&
                    info->page_size == kPageSize && bulk_decode_layout(cache) &&
                    attend_config_dec(info->head_dim_qk, info->head_dim_vo, 8,
                                      info->num_units <= info->num_sms ? 1 : 4, &cfg);
   if (!dec && !lookup_kernel(info->kernel, info->head_dim_qk, info->head_dim_vo,
-                             info->page_size, info->rows_per_block, &cfg))
+                             info->page_size, info->rows_per_block, &cfg, tree != nullptr))
     return fail(NVFP4KV_ERR_UNSUPPORTED, "planned kernel not available");
   cudaError_t e = prepare_kernel(cfg);
   if (e != cudaSuccess) return cuda_fail(e, "kernel attributes");
@@ -797,6 +819,10 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
   p.qk_scale_log2 = static_cast<float>(static_cast<double>(sm_scale) *
                                        cache->k_global_scale * 1.4426950408889634);
   p.v_scale = cache->v_global_scale;
+  if (tree) {
+    p.tree_mask = tree->mask;
+    p.tree_words = tree->words;
+  }
   if (nt) {
     p.new_k = static_cast<const uint16_t*>(nt->k);
     p.new_v = static_cast<const uint16_t*>(nt->v);
@@ -897,6 +923,28 @@ int nvfp4kv_decode_append_run(const nvfp4kv_plan_info* info, const void* new_k_b
   nt.v_stride_head = v_stride_head;
   return attend(info, q_bf16, q_stride_tok, q_stride_head, cache, kv_indices, sm_scale,
                 workspace, workspace_bytes, out_bf16, lse, stream, &nt);
+}
+
+int nvfp4kv_tree_run(const nvfp4kv_plan_info* info, const uint32_t* tree_mask, int32_t mask_words,
+                     const void* new_k_bf16, int64_t k_stride_tok, int64_t k_stride_head,
+                     const void* new_v_bf16, int64_t v_stride_tok, int64_t v_stride_head,
+                     const void* q_bf16, int64_t q_stride_tok, int64_t q_stride_head,
+                     const nvfp4kv_paged_cache* cache, const int32_t* kv_indices, float sm_scale,
+                     void* workspace, uint64_t workspace_bytes, void* out_bf16, float* lse,
+                     cudaStream_t stream) {
+  if (!new_k_bf16 != !new_v_bf16)
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "new_k and new_v: both or neither");
+  NewTokens nt;
+  nt.k = new_k_bf16;
+  nt.v = new_v_bf16;
+  nt.k_stride_tok = k_stride_tok;
+  nt.k_stride_head = k_stride_head;
+  nt.v_stride_tok = v_stride_tok;
+  nt.v_stride_head = v_stride_head;
+  const TreeMask tree{tree_mask, mask_words};
+  return attend(info, q_bf16, q_stride_tok, q_stride_head, cache, kv_indices, sm_scale,
+                workspace, workspace_bytes, out_bf16, lse, stream, new_k_bf16 ? &nt : nullptr,
+                &tree);
 }
 
 int nvfp4kv_decode_merge(const nvfp4kv_plan_info* info, void* workspace,

@@ -3,14 +3,11 @@
 // rotary positions and the E4M3 cache (argument validation and dispatch).
 #include "nvfp4kv.h"
 
-#include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
-#include <initializer_list>
 
 #include <cuda_runtime_api.h>
 
+#include "checks.h"
 #include "internal.h"
 
 namespace nvfp4kv {
@@ -26,43 +23,6 @@ int attend_e4m3(const nvfp4kv_plan_info* info, const void* q, int64_t q_stride_t
 using namespace nvfp4kv;
 
 namespace {
-
-int fail(int status, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  return set_error_detail(status, buf);
-}
-int ok() { return set_error_detail(NVFP4KV_OK, ""); }
-int launched(cudaError_t e, const char* what) {
-  if (e == cudaSuccess) return ok();
-  return fail(NVFP4KV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-bool aligned(const void* p, uint64_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-bool bad_row_strides(const void* p, int64_t st, int64_t sh) {
-  return !aligned(p, 16) || st % 8 || sh % 8 || st < 0 || sh < 0;
-}
-
-// Whether runs of `run` units at all multiples 0 .. count - 1 of the strides lie
-// apart: in order of their strides, each step passes all that lies below it.
-struct Span {
-  int64_t count, stride;
-};
-bool lie_apart(int64_t run, std::initializer_list<Span> spans) {
-  Span by[3];
-  int n = 0;
-  for (const Span& s : spans)
-    if (s.count > 1) by[n++] = s;
-  std::sort(by, by + n, [](const Span& a, const Span& b) { return a.stride < b.stride; });
-  __int128 extent = run;
-  for (int i = 0; i < n; ++i) {
-    if (by[i].stride < extent) return false;
-    extent += static_cast<__int128>(by[i].count - 1) * by[i].stride;
-  }
-  return true;
-}
 
 // ---- sums of two doubles, 106 bits ------------------------------------------
 // The frequency table is multiplied by positions up to 2^31 and holds units of
@@ -104,6 +64,9 @@ Wide power(Wide x, int n) {
   return y;
 }
 
+}  // namespace
+
+namespace nvfp4kv {
 int check_e4m3_cache(const nvfp4kv_e4m3_cache* c) {
   if (!c) return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "cache is null");
   if (!c->k_data || !c->v_data || !c->k_scale || !c->v_scale)
@@ -144,7 +107,71 @@ int check_e4m3_cache(const nvfp4kv_e4m3_cache* c) {
   return NVFP4KV_OK;
 }
 
-}  // namespace
+}  // namespace nvfp4kv
+
+// The checks of nvfp4kv_rope's arguments, and its launch parameters (num_tokens and both
+// head counts 0 where there is nothing to do).
+static int rope_params(const void* q, int64_t q_stride_tok, int64_t q_stride_head, void* q_out,
+                       int64_t q_out_stride_tok, int64_t q_out_stride_head, int32_t num_qo_heads,
+                       const void* k, int64_t k_stride_tok, int64_t k_stride_head, void* k_out,
+                       int64_t k_out_stride_tok, int64_t k_out_stride_head, int32_t num_kv_heads,
+                       int32_t num_tokens, const int32_t* positions, int32_t head_dim,
+                       int32_t rotary_dim, int32_t interleaved, int32_t dtype,
+                       const uint64_t* freq, float attention_factor, RopeParams* p) {
+  if (num_tokens < 0 || num_qo_heads < 0 || num_kv_heads < 0 || num_qo_heads > (1 << 20) ||
+      num_kv_heads > (1 << 20))
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "bad num_tokens or head counts");
+  if (dtype != 0 && dtype != 1)
+    return fail(NVFP4KV_ERR_UNSUPPORTED, "dtype %d (0 bf16, 1 f16)", dtype);
+  if (head_dim < 8 || head_dim % 8 || head_dim > 512)
+    return fail(NVFP4KV_ERR_UNSUPPORTED, "head_dim %d (a multiple of 8, at most 512)", head_dim);
+  if (rotary_dim < 2 || rotary_dim > head_dim || rotary_dim % 2)
+    return fail(NVFP4KV_ERR_UNSUPPORTED, "rotary_dim %d (even, 2 to head_dim %d)", rotary_dim,
+                head_dim);
+  if (!std::isfinite(attention_factor))
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "attention_factor is not finite");
+  if (num_tokens == 0 || num_qo_heads + num_kv_heads == 0) return NVFP4KV_OK;
+  if (!positions || !freq || (num_qo_heads > 0 && (!q || !q_out)) ||
+      (num_kv_heads > 0 && (!k || !k_out)))
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "null pointer");
+  if (!aligned(freq, 8)) return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "freq misaligned");
+  if ((num_qo_heads > 0 && (bad_row_strides(q, q_stride_tok, q_stride_head) ||
+                            bad_row_strides(q_out, q_out_stride_tok, q_out_stride_head))) ||
+      (num_kv_heads > 0 && (bad_row_strides(k, k_stride_tok, k_stride_head) ||
+                            bad_row_strides(k_out, k_out_stride_tok, k_out_stride_head))))
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT,
+                "rows must be 16-byte aligned with strides multiple of 8 elements");
+  // outputs hold every row apart; in place means the same rows
+  if ((num_qo_heads > 0 && !lie_apart(head_dim, {{num_tokens, q_out_stride_tok},
+                                                 {num_qo_heads, q_out_stride_head}})) ||
+      (num_kv_heads > 0 && !lie_apart(head_dim, {{num_tokens, k_out_stride_tok},
+                                                 {num_kv_heads, k_out_stride_head}})))
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "output strides make rows overlap");
+  if ((num_qo_heads > 0 && q == q_out &&
+       (q_stride_tok != q_out_stride_tok || q_stride_head != q_out_stride_head)) ||
+      (num_kv_heads > 0 && k == k_out &&
+       (k_stride_tok != k_out_stride_tok || k_stride_head != k_out_stride_head)))
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "in place needs the same strides");
+  p->q = static_cast<const uint16_t*>(q);
+  p->k = static_cast<const uint16_t*>(k);
+  p->q_out = static_cast<uint16_t*>(q_out);
+  p->k_out = static_cast<uint16_t*>(k_out);
+  p->q_st = q_stride_tok; p->q_sh = q_stride_head;
+  p->k_st = k_stride_tok; p->k_sh = k_stride_head;
+  p->qo_st = q_out_stride_tok; p->qo_sh = q_out_stride_head;
+  p->ko_st = k_out_stride_tok; p->ko_sh = k_out_stride_head;
+  p->positions = positions;
+  p->freq = freq;
+  p->num_tokens = num_tokens;
+  p->num_qo_heads = num_qo_heads;
+  p->num_kv_heads = num_kv_heads;
+  p->head_dim = head_dim;
+  p->rotary_dim = rotary_dim;
+  p->interleaved = interleaved ? 1 : 0;
+  p->f16 = dtype;
+  p->attention_factor = attention_factor;
+  return NVFP4KV_OK;
+}
 
 extern "C" {
 
@@ -260,60 +287,49 @@ int nvfp4kv_rope(const void* q, int64_t q_stride_tok, int64_t q_stride_head, voi
                  int32_t num_tokens, const int32_t* positions, int32_t head_dim,
                  int32_t rotary_dim, int32_t interleaved, int32_t dtype, const uint64_t* freq,
                  float attention_factor, cudaStream_t stream) {
-  if (num_tokens < 0 || num_qo_heads < 0 || num_kv_heads < 0 || num_qo_heads > (1 << 20) ||
-      num_kv_heads > (1 << 20))
-    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "bad num_tokens or head counts");
-  if (dtype != 0 && dtype != 1)
-    return fail(NVFP4KV_ERR_UNSUPPORTED, "dtype %d (0 bf16, 1 f16)", dtype);
-  if (head_dim < 8 || head_dim % 8 || head_dim > 512)
-    return fail(NVFP4KV_ERR_UNSUPPORTED, "head_dim %d (a multiple of 8, at most 512)", head_dim);
-  if (rotary_dim < 2 || rotary_dim > head_dim || rotary_dim % 2)
-    return fail(NVFP4KV_ERR_UNSUPPORTED, "rotary_dim %d (even, 2 to head_dim %d)", rotary_dim,
-                head_dim);
-  if (!std::isfinite(attention_factor))
-    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "attention_factor is not finite");
-  if (num_tokens == 0 || num_qo_heads + num_kv_heads == 0) return ok();
-  if (!positions || !freq || (num_qo_heads > 0 && (!q || !q_out)) ||
-      (num_kv_heads > 0 && (!k || !k_out)))
-    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "null pointer");
-  if (!aligned(freq, 8)) return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "freq misaligned");
-  if ((num_qo_heads > 0 && (bad_row_strides(q, q_stride_tok, q_stride_head) ||
-                            bad_row_strides(q_out, q_out_stride_tok, q_out_stride_head))) ||
-      (num_kv_heads > 0 && (bad_row_strides(k, k_stride_tok, k_stride_head) ||
-                            bad_row_strides(k_out, k_out_stride_tok, k_out_stride_head))))
-    return fail(NVFP4KV_ERR_INVALID_ARGUMENT,
-                "rows must be 16-byte aligned with strides multiple of 8 elements");
-  // outputs hold every row apart; in place means the same rows
-  if ((num_qo_heads > 0 && !lie_apart(head_dim, {{num_tokens, q_out_stride_tok},
-                                                 {num_qo_heads, q_out_stride_head}})) ||
-      (num_kv_heads > 0 && !lie_apart(head_dim, {{num_tokens, k_out_stride_tok},
-                                                 {num_kv_heads, k_out_stride_head}})))
-    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "output strides make rows overlap");
-  if ((num_qo_heads > 0 && q == q_out &&
-       (q_stride_tok != q_out_stride_tok || q_stride_head != q_out_stride_head)) ||
-      (num_kv_heads > 0 && k == k_out &&
-       (k_stride_tok != k_out_stride_tok || k_stride_head != k_out_stride_head)))
-    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "in place needs the same strides");
   RopeParams p{};
-  p.q = static_cast<const uint16_t*>(q);
-  p.k = static_cast<const uint16_t*>(k);
-  p.q_out = static_cast<uint16_t*>(q_out);
-  p.k_out = static_cast<uint16_t*>(k_out);
-  p.q_st = q_stride_tok; p.q_sh = q_stride_head;
-  p.k_st = k_stride_tok; p.k_sh = k_stride_head;
-  p.qo_st = q_out_stride_tok; p.qo_sh = q_out_stride_head;
-  p.ko_st = k_out_stride_tok; p.ko_sh = k_out_stride_head;
-  p.positions = positions;
-  p.freq = freq;
-  p.num_tokens = num_tokens;
-  p.num_qo_heads = num_qo_heads;
-  p.num_kv_heads = num_kv_heads;
-  p.head_dim = head_dim;
-  p.rotary_dim = rotary_dim;
-  p.interleaved = interleaved ? 1 : 0;
-  p.f16 = dtype;
-  p.attention_factor = attention_factor;
+  if (int st = rope_params(q, q_stride_tok, q_stride_head, q_out, q_out_stride_tok,
+                           q_out_stride_head, num_qo_heads, k, k_stride_tok, k_stride_head, k_out,
+                           k_out_stride_tok, k_out_stride_head, num_kv_heads, num_tokens,
+                           positions, head_dim, rotary_dim, interleaved, dtype, freq,
+                           attention_factor, &p))
+    return st;
   return launched(launch_rope(p, stream), "rope launch");
+}
+
+int nvfp4kv_norm_rope(const void* q, int64_t q_stride_tok, int64_t q_stride_head, void* q_out,
+                      int64_t q_out_stride_tok, int64_t q_out_stride_head, int32_t num_qo_heads,
+                      const void* k, int64_t k_stride_tok, int64_t k_stride_head, void* k_out,
+                      int64_t k_out_stride_tok, int64_t k_out_stride_head, int32_t num_kv_heads,
+                      int32_t num_tokens, const int32_t* positions, int32_t head_dim,
+                      int32_t rotary_dim, int32_t interleaved, int32_t dtype, const uint64_t* freq,
+                      float attention_factor, const void* q_weight, const void* k_weight,
+                      int32_t weight_dtype, float weight_offset, float eps,
+                      cudaStream_t stream) {
+  NormRopeParams n{};
+  if (int st = rope_params(q, q_stride_tok, q_stride_head, q_out, q_out_stride_tok,
+                           q_out_stride_head, num_qo_heads, k, k_stride_tok, k_stride_head, k_out,
+                           k_out_stride_tok, k_out_stride_head, num_kv_heads, num_tokens,
+                           positions, head_dim, rotary_dim, interleaved, dtype, freq,
+                           attention_factor, &n.rope))
+    return st;
+  if (weight_dtype != dtype && weight_dtype != 2)
+    return fail(NVFP4KV_ERR_UNSUPPORTED, "weight_dtype %d (that of the rows, or 2: float32)",
+                weight_dtype);
+  if (!(eps >= 1e-20f && eps <= 1e20f))
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "eps must lie in [1e-20, 1e20]");
+  if (!std::isfinite(weight_offset))
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "weight_offset is not finite");
+  if (n.rope.num_tokens == 0) return ok();
+  if ((num_qo_heads > 0 && (!q_weight || !aligned(q_weight, 16))) ||
+      (num_kv_heads > 0 && (!k_weight || !aligned(k_weight, 16))))
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "weights must be 16-byte aligned");
+  n.q_weight = q_weight;
+  n.k_weight = k_weight;
+  n.weight_f32 = weight_dtype == 2;
+  n.weight_offset = weight_offset;
+  n.eps = eps;
+  return launched(launch_norm_rope(n, stream), "norm_rope launch");
 }
 
 int nvfp4kv_e4m3_append(const nvfp4kv_e4m3_cache* cache, const void* k, int64_t k_stride_tok,

@@ -133,11 +133,12 @@ __device__ __forceinline__ uint32_t e2m1_code_of(float x, const float (&th)[7]) 
          (uint32_t)(x > th[6]);
 }
 
-template <int DK, int DV, int NT, int WARPS, int STAGES, int MODE>
+template <int DK, int DV, int NT, int WARPS, int STAGES, int MODE, bool TREE>
 __global__ void __launch_bounds__(WARPS * 32, (tc_min_blocks<DK, DV, NT>()))
     attend_tc_kernel(const AttendParams p) {
   using T = TcTraits<DK, DV, NT, WARPS, STAGES>;
   static_assert(MODE == 0 || NT == 1, "FP4 query and probabilities: one row block");
+  static_assert(MODE == 0 || !TREE, "drafted trees: f16 query and probabilities");
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* pipe = smem;
   uint16_t* sQ = reinterpret_cast<uint16_t*>(smem + T::MAIN_BYTES);
@@ -268,7 +269,9 @@ __global__ void __launch_bounds__(WARPS * 32, (tc_min_blocks<DK, DV, NT>()))
           make_uint4(h[0], h[1], h[2], h[3]);
       if (ci % (DK / 8) == 0) {
         const int r = row0 + rr;
-        sRowLim[rr] = r >= R ? -1 : (p.causal ? (u.kv_len - u.qo_len + r / G) : (u.kv_len - 1));
+        sRowLim[rr] = r >= R               ? -1
+                      : p.causal && !TREE ? (u.kv_len - u.qo_len + r / G)
+                                          : (u.kv_len - 1);
         // the row factor replaces the amax slot once every thread has read it
         qv[k].x = __float_as_uint(r >= R ? 0.f
                                          : p.qk_scale_log2 *
@@ -329,6 +332,8 @@ __global__ void __launch_bounds__(WARPS * 32, (tc_min_blocks<DK, DV, NT>()))
   }
   for (int rr = 0; rr < T::RB; ++rr)
     if (sRowLim[rr] >= 0) min_lim = min(min_lim, sRowLim[rr]);
+  // (the tree's tokens are looked up in the rows' masks)
+  if constexpr (TREE) min_lim = min(min_lim, u.kv_len - u.qo_len - 1);
   // one row block (NT == 1): this lane's query rows 2t and 2t+1, score
   // factor f, -m_use, raise threshold (-inf until the row has a maximum,
   // +inf for padding rows), causal limit, running max and partial sum
@@ -527,6 +532,11 @@ __global__ void __launch_bounds__(WARPS * 32, (tc_min_blocks<DK, DV, NT>()))
         if (ta > lim2[1]) x[1] = -INFINITY;
         if (tb > lim2[0]) x[2] = -INFINITY;
         if (tb > lim2[1]) x[3] = -INFINITY;
+        if constexpr (TREE) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (tree_hides(p, u, row0 + 2 * t + (k & 1), k < 2 ? ta : tb)) x[k] = -INFINITY;
+        }
       }
       if constexpr (MODE == 1) {
         // the row-maximum pass: this lane's maxima of rows 2t, 2t+1
@@ -688,6 +698,12 @@ __global__ void __launch_bounds__(WARPS * 32, (tc_min_blocks<DK, DV, NT>()))
           if (j0 + 1 > rowlim[hf]) x[1] = -INFINITY;
           if (j0 + 8 > rowlim[hf]) x[2] = -INFINITY;
           if (j0 + 9 > rowlim[hf]) x[3] = -INFINITY;
+          if constexpr (TREE) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (tree_hides(p, u, row0 + 8 * hf + g, j0 + (k & 1) + 8 * (k >> 1)))
+                x[k] = -INFINITY;
+          }
         }
         float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -854,7 +870,7 @@ __global__ void __launch_bounds__(WARPS * 32, (tc_min_blocks<DK, DV, NT>()))
 #define NVFP4KV_TC_STAGES 4
 #endif
 
-template <int DK, int DV, int NT, int MODE = 0>
+template <int DK, int DV, int NT, int MODE = 0, bool TREE = false>
 bool make_tc(AttendConfig* cfg) {
   // 512-wide K rows: 8 warps per CTA (one CTA per SM by shared memory, and
   // twice the warps streaming pages): 30.9 against 42.3 us on the 512/256
@@ -869,16 +885,20 @@ bool make_tc(AttendConfig* cfg) {
   cfg->warps = WARPS;
   cfg->smem_bytes = T::SMEM;
   cfg->func =
-      reinterpret_cast<const void*>(attend_tc_kernel<DK, DV, NT, WARPS, STAGES, MODE>);
+      reinterpret_cast<const void*>(attend_tc_kernel<DK, DV, NT, WARPS, STAGES, MODE, TREE>);
   return true;
 }
 
 }  // namespace
 
-bool attend_config_tc(int dk, int dv, int rows, AttendConfig* cfg) {
+bool attend_config_tc(int dk, int dv, int rows, bool tree, AttendConfig* cfg) {
   const int nt = rows <= 8 ? 1 : 2;
-#define NVFP4KV_TC_CASE(DK_, DV_)                                                   \
-  if (dk == DK_ && dv == DV_) return nt == 1 ? make_tc<DK_, DV_, 1>(cfg) : make_tc<DK_, DV_, 2>(cfg);
+#define NVFP4KV_TC_CASE(DK_, DV_)                                                       \
+  if (dk == DK_ && dv == DV_) {                                                         \
+    if (tree)                                                                           \
+      return nt == 1 ? make_tc<DK_, DV_, 1, 0, true>(cfg) : make_tc<DK_, DV_, 2, 0, true>(cfg); \
+    return nt == 1 ? make_tc<DK_, DV_, 1>(cfg) : make_tc<DK_, DV_, 2>(cfg);             \
+  }
   NVFP4KV_TC_CASE(64, 64)
   NVFP4KV_TC_CASE(128, 128)
   NVFP4KV_TC_CASE(256, 256)

@@ -237,6 +237,18 @@ __device__ __forceinline__ float bf16_bits_to_f32(uint32_t bits16) {
   return __uint_as_float(bits16 << 16);
 }
 
+// Drafted trees: whether row r (of the G x qo_len rows of unit u's kv head) does not see
+// the request's token `tok`.  Tokens before the tree are seen by all.
+__device__ __forceinline__ bool tree_hides(const AttendParams& p, const WorkUnit& u, int r,
+                                           int tok) {
+  const int j = tok - (u.kv_len - u.qo_len), row = r / p.group;
+  if (j < 0) return false;
+  if (row >= u.qo_len || j >= u.qo_len || (j >> 5) >= p.tree_words) return true;
+  const uint32_t word =
+      __ldg(p.tree_mask + (int64_t)(u.qo_begin + row) * p.tree_words + (j >> 5));
+  return !((word >> (j & 31)) & 1u);
+}
+
 }  // namespace dev
 
 // The CTA's work unit.  With a live last_page_len the unit's kv_len is the

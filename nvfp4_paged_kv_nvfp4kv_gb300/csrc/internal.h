@@ -82,6 +82,10 @@ struct AttendParams {
   float* row_max;
   int32_t row_max_splits;
   int32_t q_f16;  // kernel 5: the query's element, 0 bf16, 1 f16
+  // drafted trees: the rows' mask words [rows][tree_words]; bit j of a row says whether
+  // it sees the j-th of its request's qo_len last tokens
+  const uint32_t* tree_mask;
+  int32_t tree_words;
 };
 
 struct AppendParams {
@@ -153,6 +157,14 @@ struct RopeParams {
   float attention_factor;
 };
 
+struct NormRopeParams {
+  RopeParams rope;
+  const void* q_weight;  // [head_dim], the rows' element or float32
+  const void* k_weight;
+  int32_t weight_f32;
+  float weight_offset, eps;
+};
+
 struct E4m3AppendParams {
   uint8_t* data[2];   // K, V codes
   uint8_t* scale[2];  // f32 scales, addressed in bytes
@@ -166,6 +178,78 @@ struct E4m3AppendParams {
   const int32_t* kv_indptr;
   const int32_t* kv_indices;
   const int32_t* last_page_len;
+  uint32_t* flags;
+};
+
+constexpr int kMaxTreeNodes = 1024;
+struct TreeMaskParams {
+  const int32_t* parents;    // [num_rows] within the request, -1 for a root
+  const int32_t* qo_indptr;  // [batch + 1]
+  const int32_t* kv_len;     // [batch] tokens with the nodes
+  int32_t batch, num_rows, mask_words;
+  uint32_t* tree_mask;  // [num_rows, mask_words]
+  int32_t* positions;   // [num_rows]
+  uint32_t* flags;
+};
+
+// The buffers of either cache, seen as rows of bytes: `data` the codes of a (page,
+// slot, head), `scale` its block scales (4-bit cache, scs between slots) or the scale of
+// a (page, head) (E4M3 cache: page_scales).
+struct CacheRows {
+  uint8_t* data[2];   // K, V
+  uint8_t* scale[2];
+  int64_t sp[2], ss[2], sh[2];     // bytes
+  int64_t scp[2], scs[2], sch[2];  // bytes
+  int32_t row_bytes[2], scale_bytes[2];
+  int32_t num_pages, page_size, num_kv_heads, page_scales;
+};
+
+struct CompactParams : CacheRows {
+  const int32_t* path;  // [batch, path_width], rows path_stride apart
+  int64_t path_stride;
+  int32_t path_width, batch;
+  const int32_t* num_kept;
+  const int32_t* qo_indptr;
+  const int32_t* kv_indptr;
+  const int32_t* kv_indices;
+  const int32_t* last_page_len;
+  uint32_t* flags;
+};
+
+struct PageCopyParams : CacheRows {
+  const int32_t* src;
+  const int32_t* dst;
+  int32_t num;
+  uint32_t* flags;
+};
+
+constexpr int kMaxForks = 8192, kMaxForkRows = 65536;
+struct ForkParams {
+  const int32_t* parents;
+  const int32_t* children;
+  int32_t* kv_len;
+  int32_t* block_table;
+  int64_t table_stride;
+  int32_t* page_shares;
+  const int32_t* free_pages;
+  const int32_t* free_head;
+  int32_t* free_head_out;
+  int32_t* copy_src;
+  int32_t* copy_dst;
+  int32_t num_forks, num_rows, page_size, table_width, num_pages, num_free;
+  uint32_t* flags;
+};
+
+struct ReleaseParams {
+  const int32_t* keep_len;
+  int32_t* kv_len;
+  const int32_t* block_table;
+  int64_t table_stride;
+  int32_t* page_shares;
+  int32_t* free_pages;
+  const int32_t* free_head;
+  int32_t* free_head_out;
+  int32_t num_rows, page_size, table_width, num_pages, num_free;
   uint32_t* flags;
 };
 
@@ -192,7 +276,13 @@ cudaError_t launch_dequantize(const DequantParams& p, cudaStream_t stream);
 constexpr int kMaxPageTableBatch = 8192;
 cudaError_t launch_page_table(const PageTableParams& p, cudaStream_t stream);
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
+cudaError_t launch_norm_rope(const NormRopeParams& p, cudaStream_t stream);
 cudaError_t launch_e4m3_append(const E4m3AppendParams& p, cudaStream_t stream);
+cudaError_t launch_tree_masks(const TreeMaskParams& p, cudaStream_t stream);
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream);
+cudaError_t launch_release(const ReleaseParams& p, cudaStream_t stream);
+cudaError_t launch_page_copies(const PageCopyParams& p, cudaStream_t stream);
 // The E4M3-cache attention kernel for (dk, dv), a page size of 16 or 1 and up to
 // `rows` query rows per kv head; false when not built.
 bool attend_config_e4m3(int dk, int dv, int page_size, int rows, AttendConfig* cfg);

@@ -1,0 +1,426 @@
+// page_ops.cu -- requests that share pages: forked, their last pages copied, and
+// given up again, sm_103a.
+//
+// page_shares[p] counts the owners of page p beyond the first, so a page that the page
+// table's kernel takes off the free list has its 0 already.
+//
+// fork: with L tokens of the parent in pages of P, the child gets the parent's L / P
+// whole pages (one more owner each) and, for a last page that is not full, a new page
+// off the free list, in the order of the forks; (the parent's last page, the new page)
+// goes on the list of copies.
+// release: request b keeps K_b of its L_b tokens and gives up the pages ceil(K_b / P) ..
+// ceil(L_b / P) of its row.  A page whose last owner gives it up goes back in front of
+// the free list's head; the pages freed stand there in the order in which the call lists
+// them first (rows, then columns).
+//
+// Both are a list of (row, column) entries over rows of unequal lengths: every CTA takes
+// the sums over the rows for itself (as in page_table.cu) and fills its share of the
+// entries.  The order of a call's atomics changes no result: owners are counted up and
+// down by whole numbers, and of several entries that give up one page the first in the
+// list is found by a minimum.
+#include <climits>
+#include <cstdint>
+
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "internal.h"
+
+namespace nvfp4kv {
+namespace {
+
+constexpr int64_t kMaxLen = (int64_t)1 << 30;  // tokens of a request, as in the planner
+constexpr int kForkThreads = 512;
+constexpr int kChunk = 8;  // entries a lane has in flight
+
+// the last entry of first[lo .. hi) that is <= x, where first[lo] <= x < first[hi]
+__device__ __forceinline__ int owner(const int32_t* first, int lo, int hi, int x) {
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// exclusive sums over the CTA of two counts a thread; the totals too
+template <int THREADS>
+__device__ __forceinline__ longlong2 cta_sums(longlong2 mine, longlong2* total) {
+  __shared__ longlong2 s_warp[THREADS / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  longlong2 run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, run.x, o);
+    const long long y = __shfl_up_sync(0xffffffffu, run.y, o);
+    if (lane >= o) {
+      run.x += x;
+      run.y += y;
+    }
+  }
+  if (lane == 31) s_warp[warp] = run;
+  __syncthreads();
+  longlong2 before = make_longlong2(0, 0), all = before;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w == warp) before = all;
+    all.x += s_warp[w].x;
+    all.y += s_warp[w].y;
+  }
+  *total = all;
+  return make_longlong2(before.x + run.x - mine.x, before.y + run.y - mine.y);
+}
+
+// ---- fork ---------------------------------------------------------------------
+__global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) {
+  extern __shared__ int32_t smem[];
+  const int F = p.num_forks, P = p.page_size;
+  int32_t* s_first = smem;              // [F + 1] first entry (whole page) of each fork
+  int32_t* s_free = s_first + F + 1;    // [F + 1] new pages that the forks before it take
+  int32_t* s_parent = s_free + F + 1;   // [F]
+  uint32_t* s_child = reinterpret_cast<uint32_t*>(s_parent + F);  // a bit a row: a child
+  __shared__ int s_bad;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int head = *p.free_head;
+  if (tid == 0) s_bad = 0;
+  const int words = (p.num_rows + 31) / 32;
+  for (int w = tid; w < words; w += kForkThreads) s_child[w] = 0u;
+  __syncthreads();
+
+  // ---- this thread's neighbouring forks ---------------------------------------
+  const int per = (F + kForkThreads - 1) / kForkThreads;
+  const int f0 = min(F, tid * per), f1 = min(F, f0 + per);
+  longlong2 mine = make_longlong2(0, 0);
+  bool bad = false;
+  for (int f = f0; f < f1; ++f) {
+    const int from = p.parents[f], to = p.children[f];
+    if (from < 0 || from >= p.num_rows || to < 0 || to >= p.num_rows) {
+      bad = true;
+      continue;
+    }
+    // (a row that two forks fill)
+    if (atomicOr(&s_child[to >> 5], 1u << (to & 31)) >> (to & 31) & 1u) bad = true;
+    const int len = p.kv_len[from];
+    if (len < 0 || len > kMaxLen || (len + P - 1) / P > p.table_width) {
+      bad = true;
+      continue;
+    }
+    s_parent[f] = from;
+    s_first[f] = len;  // kept here until its sum takes the place
+    mine.x += len / P;
+    mine.y += len % P > 0;
+  }
+  longlong2 total;
+  longlong2 at = cta_sums<kForkThreads>(mine, &total);  // (its barrier completes s_child)
+  for (int f = f0; f < f1 && !bad; ++f)  // a row that is filled and read
+    bad = s_child[s_parent[f] >> 5] >> (s_parent[f] & 31) & 1u;
+  if (bad) atomicOr(&s_bad, 1);
+  __syncthreads();
+  if (s_bad || total.x > INT_MAX || head < 0 || head + total.y > p.num_free) {
+    if (blockIdx.x == 0 && tid == 0 && p.flags) atomicOr(p.flags, s_bad ? 0x40u : 0x80u);
+    return;
+  }
+  const int nt = gridDim.x * kForkThreads, me = blockIdx.x * kForkThreads + tid;
+  for (int f = f0; f < f1; ++f) {
+    const int len = s_first[f], whole = len / P;
+    const bool rest = len % P > 0;
+    s_first[f] = static_cast<int32_t>(at.x);
+    s_free[f] = static_cast<int32_t>(at.y);
+    at.x += whole;
+    at.y += rest;
+    // the fork's own words, by the one CTA whose turn it is
+    if (f % gridDim.x != blockIdx.x) continue;
+    const int child = p.children[f];
+    int src = -1, dst = -1;
+    if (rest) {
+      src = p.block_table[s_parent[f] * p.table_stride + whole];
+      dst = p.free_pages[head + s_free[f]];
+      p.block_table[child * p.table_stride + whole] = dst;
+    }
+    p.copy_src[f] = src;
+    p.copy_dst[f] = dst;
+    p.kv_len[child] = len;
+  }
+  if (tid == 0) s_first[F] = static_cast<int32_t>(total.x);
+  if (me == 0) *p.free_head_out = head + static_cast<int>(total.y);
+  __syncthreads();
+
+  // ---- the whole pages: a warp takes 32 * kChunk neighbouring entries ------------
+  const int entries = static_cast<int>(total.x);
+  const int64_t stride = (int64_t)(nt / 32) * (32 * kChunk);
+  for (int64_t e0 = (int64_t)(me / 32) * (32 * kChunk); e0 < entries; e0 += stride) {
+    const int first = static_cast<int>(e0);
+    const int stop = static_cast<int>(min(e0 + 32 * kChunk, (int64_t)entries));
+    const int lo = owner(s_first, 0, F, first);
+    const int hi = stop <= s_first[lo + 1] ? lo + 1 : owner(s_first, lo, F, stop - 1) + 1;
+    int32_t id[kChunk];
+    int32_t* to[kChunk];
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) {
+      const int e = first + 32 * j + lane;
+      to[j] = nullptr;
+      if (e < stop) {
+        const int f = owner(s_first, lo, hi, e), c = e - s_first[f];
+        id[j] = p.block_table[s_parent[f] * p.table_stride + c];
+        to[j] = p.block_table + __ldg(p.children + f) * p.table_stride + c;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) {
+      if (!to[j]) continue;
+      *to[j] = id[j];
+      if (id[j] >= 0 && id[j] < p.num_pages)
+        atomicAdd(p.page_shares + id[j], 1);
+      else if (p.flags)
+        atomicOr(p.flags, 0x1u);
+    }
+  }
+}
+
+// ---- release --------------------------------------------------------------------
+// One cluster: its CTAs keep the three passes over the entries apart by the cluster's
+// barrier.  A pass is loads and atomics on the pages' words in L2.
+//   1  every entry counts its page's owners down;
+//   2  where that went below 0, the page is free: its word becomes the least of
+//      INT_MIN + entry;
+//   3  the entry that finds its own number there puts the page on the free list, at the
+//      place that the count of such entries before it gives, and the word back to 0.
+constexpr int kCluster = 8, kThreads = 1024, kWarps = kThreads / 32;
+
+__global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseParams p) {
+  namespace cg = cooperative_groups;
+  extern __shared__ int32_t smem[];
+  const int B = p.num_rows, P = p.page_size;
+  int32_t* s_first = smem;           // [B + 1] first entry of each row
+  int32_t* s_col = s_first + B + 1;  // [B] first column that it gives up
+  __shared__ int s_bad, s_freed[kWarps], s_mine;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int head = *p.free_head;
+  if (tid == 0) s_bad = 0;
+  __syncthreads();
+  const int per = (B + kThreads - 1) / kThreads;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  longlong2 mine = make_longlong2(0, 0);
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    const int len = p.kv_len[b], keep = p.keep_len[b];
+    if (len < 0 || len > kMaxLen || keep < 0 || keep > len || (len + P - 1) / P > p.table_width) {
+      bad = true;
+      continue;
+    }
+    const int lo = (keep + P - 1) / P, hi = (len + P - 1) / P;
+    s_col[b] = lo;
+    s_first[b] = hi - lo;  // kept here until its sum takes the place
+    mine.x += hi - lo;
+  }
+  if (bad) atomicOr(&s_bad, 1);
+  longlong2 total;
+  longlong2 at = cta_sums<kThreads>(mine, &total);
+  // (an entry's number and INT_MIN add up in 32 bits)
+  const bool stop = s_bad || total.x >= INT_MAX / 2 || head < 0 || head > p.num_free;
+  if (!stop) {
+    for (int b = b0; b < b1; ++b) {
+      const int n = s_first[b];
+      s_first[b] = static_cast<int32_t>(at.x);
+      at.x += n;
+    }
+    if (tid == 0) s_first[B] = static_cast<int32_t>(total.x);
+  }
+  __syncthreads();
+  if (stop) {  // (every CTA alike, before the cluster's first barrier)
+    if (rank == 0 && tid == 0 && p.flags) atomicOr(p.flags, s_bad ? 0x40u : 0x80u);
+    return;
+  }
+
+  // this warp's entries: neighbours, so that the free list keeps their order
+  const int entries = static_cast<int>(total.x);
+  const int warps = ranks * kWarps, mw = rank * kWarps + warp;
+  const int share = ((entries + warps - 1) / warps + 31) / 32 * 32;
+  const int e0 = static_cast<int>(min((int64_t)mw * share, (int64_t)entries));
+  const int e1 = min(entries, e0 + share);
+  const int lo = e0 < e1 ? owner(s_first, 0, B, e0) : 0;
+  const int hi = e0 < e1 ? owner(s_first, lo, B, e1 - 1) + 1 : 0;
+  auto page_of = [&](int e) -> int {  // -1: not in the pool (flagged in the first pass)
+    const int b = owner(s_first, lo, hi, e);
+    const int id = p.block_table[b * p.table_stride + s_col[b] + (e - s_first[b])];
+    return id >= 0 && id < p.num_pages ? id : -1;
+  };
+  // A lane's pages stay in registers over the passes while they are few.
+  int32_t kept[kChunk];
+#pragma unroll
+  for (int j = 0; j < kChunk; ++j) {
+    const int e = e0 + 32 * j + lane;
+    kept[j] = e < e1 ? page_of(e) : -1;
+    if (e < e1 && kept[j] < 0 && p.flags) atomicOr(p.flags, 0x1u);
+  }
+  auto each = [&](auto&& act) {
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j) act(e0 + 32 * j + lane, kept[j]);
+    for (int e = e0 + 32 * kChunk + lane; e - lane < e1; e += 32) {
+      const int pg = e < e1 ? page_of(e) : -1;
+      act(e, pg);
+    }
+  };
+  each([&](int e, int pg) {
+    if (pg >= 0)
+      atomicSub(p.page_shares + pg, 1);
+    else if (e < e1 && e >= e0 + 32 * kChunk && p.flags)
+      atomicOr(p.flags, 0x1u);
+  });
+  cluster.sync();
+  each([&](int e, int pg) {
+    if (pg < 0 || __ldcg(p.page_shares + pg) >= 0) return;
+    const int before = atomicMin(p.page_shares + pg, INT_MIN + e);
+    // (given up more often than it has owners: free once)
+    if (before < -1 && before >= INT_MIN + entries && p.flags) atomicOr(p.flags, 0x200u);
+  });
+  cluster.sync();
+  int freed = 0;
+  each([&](int e, int pg) {
+    const bool first = pg >= 0 && __ldcg(p.page_shares + pg) == INT_MIN + e;
+    freed += __popc(__ballot_sync(0xffffffffu, first));
+  });
+  if (lane == 0) s_freed[warp] = freed;
+  __syncthreads();
+  if (tid == 0) {
+    int sum = 0;
+    for (int w = 0; w < kWarps; ++w) sum += s_freed[w];
+    s_mine = sum;
+  }
+  cluster.sync();
+  int before = 0, all = 0;
+  for (int k = 0; k < ranks; ++k) {
+    const int n = *cluster.map_shared_rank(&s_mine, k);
+    if (k < rank) before += n;
+    all += n;
+  }
+  for (int w = 0; w < warp; ++w) before += s_freed[w];
+  cluster.sync();  // (no CTA ends, and no word of a page is put back, while another reads)
+  if (all > head) {
+    // More than ever were taken: the words are put back as they were, nothing is listed.
+    each([&](int e, int pg) {
+      if (pg >= 0 && __ldcg(p.page_shares + pg) == INT_MIN + e) atomicExch(p.page_shares + pg, -1);
+    });
+    cluster.sync();
+    each([&](int, int pg) {
+      if (pg >= 0) atomicAdd(p.page_shares + pg, 1);
+    });
+    if (rank == 0 && tid == 0 && p.flags) atomicOr(p.flags, 0x80u);
+    return;
+  }
+  int place = head - all + before;
+  each([&](int e, int pg) {
+    const bool first = pg >= 0 && __ldcg(p.page_shares + pg) == INT_MIN + e;
+    const unsigned votes = __ballot_sync(0xffffffffu, first);
+    if (first) {
+      p.free_pages[place + __popc(votes & ((1u << lane) - 1u))] = pg;
+      __stcg(p.page_shares + pg, 0);
+    }
+    place += __popc(votes);
+  });
+  for (int b = rank * kThreads + tid; b < B; b += ranks * kThreads) p.kv_len[b] = p.keep_len[b];
+  if (rank == 0 && tid == 0) *p.free_head_out = head - all;
+}
+
+// ---- copies -----------------------------------------------------------------------
+// A warp takes a head of one copy: its rows' pieces, 16 bytes of codes or `small` bytes
+// of scales, four a lane in flight.
+__global__ void __launch_bounds__(128) copy_kernel(const PageCopyParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (id >= (int64_t)p.num * p.num_kv_heads) return;
+  const int i = static_cast<int>(id / p.num_kv_heads), h = static_cast<int>(id % p.num_kv_heads);
+  const int src = p.src[i], dst = p.dst[i];
+  if (src == -1 && dst == -1) return;  // nothing to copy
+  if (src < 0 || src >= p.num_pages || dst < 0 || dst >= p.num_pages) {
+    if (lane == 0 && p.flags) atomicOr(p.flags, 0x1u);
+    return;
+  }
+  if (src == dst) return;
+#pragma unroll 1
+  for (int kv = 0; kv < 2; ++kv) {
+    const uint8_t* from = p.data[kv] + src * p.sp[kv] + h * p.sh[kv];
+    uint8_t* to = p.data[kv] + dst * p.sp[kv] + h * p.sh[kv];
+    const int wide = p.row_bytes[kv] / 16, items = p.page_size * wide;
+    for (int it0 = lane; it0 - lane < items; it0 += 128) {
+      uint4 v[4];
+      int64_t at[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int it = it0 + 32 * k, row = it / wide;
+        at[k] = row * p.ss[kv] + (it - row * wide) * 16;
+        if (it < items) v[k] = *reinterpret_cast<const uint4*>(from + at[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (it0 + 32 * k < items) *reinterpret_cast<uint4*>(to + at[k]) = v[k];
+    }
+    from = p.scale[kv] + src * p.scp[kv] + h * p.sch[kv];
+    to = p.scale[kv] + dst * p.scp[kv] + h * p.sch[kv];
+    if (p.page_scales) {  // one a page and head
+      if (lane == 0) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from);
+      continue;
+    }
+    const int small = p.scale_bytes[kv] % 4 ? 2 : 4, each = p.scale_bytes[kv] / small;
+    for (int it = lane; it < p.page_size * each; it += 32) {
+      const int row = it / each;
+      const int64_t off = row * p.scs[kv] + (it - row * each) * small;
+      if (small == 4)
+        *reinterpret_cast<uint32_t*>(to + off) = *reinterpret_cast<const uint32_t*>(from + off);
+      else
+        *reinterpret_cast<uint16_t*>(to + off) = *reinterpret_cast<const uint16_t*>(from + off);
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream) {
+  const int words = (p.num_rows + 31) / 32;
+  constexpr int kMaxSmem = (3 * kMaxForks + 2 + kMaxForkRows / 32) * 4;
+  const int smem = (3 * p.num_forks + 2 + words) * 4;
+  if (smem > 40 * 1024) {
+    // the most that any call takes: another thread's call must not find less
+    cudaError_t e = cudaFuncSetAttribute(fork_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kMaxSmem);
+    if (e != cudaSuccess) return e;
+  }
+  // at most two CTAs an SM (more would only repeat the sums), as many as the forks' rows
+  // could fill
+  int64_t blocks = ((int64_t)p.num_forks * p.table_width / kChunk + kForkThreads) / kForkThreads;
+  if (blocks > 152 * 2) blocks = 152 * 2;
+  fork_kernel<<<static_cast<int>(blocks), kForkThreads, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_release(const ReleaseParams& p, cudaStream_t stream) {
+  constexpr int kMaxSmem = (2 * kMaxPageTableBatch + 1) * 4;
+  const int smem = (2 * p.num_rows + 1) * 4;
+  if (smem > 40 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(release_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(kCluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kCluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, release_kernel, p);
+}
+
+cudaError_t launch_page_copies(const PageCopyParams& p, cudaStream_t stream) {
+  const int64_t warps = (int64_t)p.num * p.num_kv_heads;
+  if (warps == 0) return cudaSuccess;
+  copy_kernel<<<static_cast<unsigned>((warps + 3) / 4), 128, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace nvfp4kv

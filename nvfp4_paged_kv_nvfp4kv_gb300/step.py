@@ -20,7 +20,7 @@ from ._lib import E4m3CacheStruct, RopeOptions, StepTableStruct, check
 from .api import Plan
 
 __all__ = ["StepTable", "nvfp4kv_build_page_table", "RopePlan", "nvfp4kv_rope_plan",
-           "nvfp4kv_rope", "E4m3Cache", "nvfp4kv_e4m3_append", "nvfp4kv_e4m3_decode_run"]
+           "nvfp4kv_rope", "nvfp4kv_norm_rope", "E4m3Cache", "nvfp4kv_e4m3_append", "nvfp4kv_e4m3_decode_run"]
 
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1}
 
@@ -195,10 +195,49 @@ def nvfp4kv_rope(plan: RopePlan, q: Optional[torch.Tensor], k: Optional[torch.Te
     """Rotate q [tokens, Hq, D] and k [tokens, Hkv, D] (either may be None) by
     ``positions`` [tokens] int32: returns (q_out, k_out), new tensors unless
     given; ``q_out=q`` rotates in place."""
-    first = q if q is not None else k
-    if first is None:
+    if q is None and k is None:
         return None, None
-    dtype = first.dtype
+    args, outs, dev = _rope_args(plan, q, k, positions, q_out, k_out, stream)
+    st = _entry("nvfp4kv_rope")(*args, _stream_of(stream, dev))
+    if st:
+        check(st, "nvfp4kv_rope")
+    return outs
+
+
+def nvfp4kv_norm_rope(plan: RopePlan, q: Optional[torch.Tensor], k: Optional[torch.Tensor],
+                      positions, q_weight=None, k_weight=None, eps: float = 1e-6,
+                      weight_offset: float = 0.0, q_out=None, k_out=None, stream=None):
+    """Norm every head of q [tokens, Hq, D] and k [tokens, Hkv, D] (either may be
+    None), x / sqrt(mean x^2 + eps) * (weight + weight_offset), and rotate it as
+    ``nvfp4kv_rope`` does, in one pass: returns (q_out, k_out).  ``q_weight`` and
+    ``k_weight`` [D] are of the rows' type or both float32."""
+    if q is None and k is None:
+        return None, None
+    args, outs, dev = _rope_args(plan, q, k, positions, q_out, k_out, stream)
+    kind = None
+    for name, x, w in (("q_weight", q, q_weight), ("k_weight", k, k_weight)):
+        if x is None:
+            continue
+        if w is None or w.dim() != 1 or w.numel() != plan.head_dim or w.stride(0) != 1:
+            raise ValueError("%s must be contiguous [%d]" % (name, plan.head_dim))
+        if w.dtype not in (x.dtype, torch.float32) or kind not in (None, w.dtype):
+            raise ValueError("the weights must be of the rows' type or both torch.float32")
+        if w.get_device() != dev:
+            _check_device(dev, w)
+        kind = w.dtype
+    st = _entry("nvfp4kv_norm_rope")(
+        *args, None if q is None else q_weight.data_ptr(),
+        None if k is None else k_weight.data_ptr(), 2 if kind == torch.float32 else _DTYPE[kind],
+        weight_offset, eps, _stream_of(stream, dev))
+    if st:
+        check(st, "nvfp4kv_norm_rope")
+    return outs
+
+
+def _rope_args(plan, q, k, positions, q_out, k_out, stream):
+    """The arguments that both rotations take up to the frequencies and their factor,
+    the outputs, and the device."""
+    dtype = (q if q is not None else k).dtype
     code = _DTYPE.get(dtype)
     if code is None:
         raise ValueError("q and k must be torch.bfloat16 or torch.float16")
@@ -209,11 +248,8 @@ def nvfp4kv_rope(plan: RopePlan, q: Optional[torch.Tensor], k: Optional[torch.Te
         _check_device(dev, positions, plan.freq)
     qa, q_out = _rope_rows(plan.head_dim, "q", q, q_out, n, dtype, dev, stream)
     ka, k_out = _rope_rows(plan.head_dim, "k", k, k_out, n, dtype, dev, stream)
-    st = _entry("nvfp4kv_rope")(*qa, *ka, n, positions.data_ptr(), *plan.layout, code, plan.table,
-                                plan.attention_factor, _stream_of(stream, dev))
-    if st:
-        check(st, "nvfp4kv_rope")
-    return q_out, k_out
+    return ((*qa, *ka, n, positions.data_ptr(), *plan.layout, code, plan.table,
+             plan.attention_factor), (q_out, k_out), dev)
 
 
 def _rope_rows(dim, name, x, out, n, dtype, dev, stream):

@@ -1,0 +1,235 @@
+"""Attention of drafted trees over the 4-bit cache, against 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_paged_kv_nvfp4kv_gb300 as N
+from nvfp4_paged_kv_nvfp4kv_gb300 import _lib
+import step_reference as R
+import tree_reference as T
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+def bits(mask, n, total):
+    """[n, total]: what each row of one request does not see."""
+    hide = np.zeros((n, total), dtype=bool)
+    for i in range(n):
+        for j in range(n):
+            word = int(np.uint32(mask[i, j >> 5])) if j >> 5 < mask.shape[1] else 0
+            hide[i, total - n + j] = not word >> (j & 31) & 1
+    return hide
+
+
+def tree_case(kv, new, hq, hkv, dk, dv, page=16, layout="HND", out="bf16", seed=0, masks=None,
+              words=None, only=None, live=None, q_pad=0, g=(0.75, 1.25), **plan_kw):
+    """Run and check.  Beside the output's own rounding: a weight is rounded to f16
+    (2^-11, at least 2^-25 of the row's largest) in the product and in the row sum; the
+    scores' sums err by Dk 2^-23 of sum |q k| (`reach`) at most, and what follows by
+    2^-21; an error d of a score is one of d of a weight and of the sum."""
+    c = T.Nvfp4Case(kv, page, hkv, dk, dv, layout, seed=seed, g=g)
+    gen = torch.Generator().manual_seed(seed)
+    q = torch.randn((sum(new) + 1, hq + q_pad, dk), generator=gen).to(torch.bfloat16)
+    q = q.cuda()[:, q_pad:]
+    rng = np.random.default_rng(seed + 1)
+    qo = np.concatenate([[0], np.cumsum(new)])
+    words = words or (max(max(new), 1) + 31) // 32
+    if masks is None:
+        masks = [T.mask_words(T.ancestors(T.random_parents(rng, n)), words) for n in new]
+    mask = np.concatenate([m.reshape(-1, words) for m in masks])
+    last = c.last
+    if live is not None:
+        last, plan_kw["device_last_page_len"] = live, c.last_page_len
+    plan = N.nvfp4kv_decode_plan(qo, c.indptr, last, hq, hkv, dk, dv, page_size=page,
+                                 out_dtype=DT[out], **plan_kw)
+    tree_mask = torch.from_numpy(mask.astype(np.int32)).cuda()
+    o, lse = N.nvfp4kv_tree_run(plan, q, c.cache, c.kv_indices, tree_mask)
+    assert N.nvfp4kv_workspace_flags(plan) == 0
+    got, gl = R.to_np(o), R.to_np(lse)
+    eps = torch.finfo(DT[out]).eps / 2
+    scale = 1 / math.sqrt(dk)
+    for b, n in enumerate(new):
+        if not n or (only is not None and b not in only):
+            continue
+        k, v = c.dense(0, b), c.dense(1, b)
+        rows = slice(int(qo[b]), int(qo[b + 1]))
+        ref, rl, mean, reach, floor = T.tree_attention(
+            R.to_np(q[rows]), k, v, bits(masks[b], n, kv[b]), scale)
+        delta = dk * 2.0 ** -23 * reach + 2.0 ** -21
+        tol = (eps * np.abs(ref) + (mean * (2.0 ** -10 + 2.0 ** -19 + 2 * delta[..., None])
+                                    + 2.0 ** -25 * floor) * (1 + eps)
+               + float(torch.finfo(DT[out]).smallest_normal) * eps)
+        none = np.isinf(rl)
+        assert np.array_equal(gl[rows] == -np.inf, none)
+        assert (got[rows][none] == 0).all()
+        err = np.abs(got[rows] - ref)
+        assert (err <= tol).all(), (b, float(err.max()), float((err / tol).max()))
+        lerr = np.abs(gl[rows][~none] - rl[~none])
+        ltol = delta + 2.0 ** -11 + 2.0 ** -19 + np.abs(rl) * 2.0 ** -22
+        assert (lerr <= ltol[~none]).all(), (b, lerr.max())
+    return c, plan, o, lse, q, tree_mask
+
+
+DIMS = [(64, 64), (128, 128), (256, 128), (256, 256), (512, 256)]
+
+
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("page,layout,out", [(16, "HND", "bf16"), (16, "NHD", "f16"),
+                                             (1, "HND", "bf16")])
+@pytest.mark.parametrize("new", [(1, 2, 0), (3, 4, 2), (5, 16, 1), (13, 37, 40)])
+def test_dims_and_rows(dk, dv, page, layout, out, new):
+    """Up to 4, 8, 32 and 80 rows per kv head; the last request is nothing but its tree."""
+    tree_case((37, 300, 40), new, 4, 2, dk, dv, page=page, layout=layout, out=out,
+              seed=dk + sum(new))
+
+
+@pytest.mark.parametrize("page", [16, 1])
+@pytest.mark.parametrize("hq,hkv,new", [(4, 4, (8, 1, 7)), (5, 1, (3, 1, 6)), (16, 1, (1, 4, 1)),
+                                        (32, 4, (9, 65, 90)), (8, 8, (20, 33, 64))])
+def test_groups(hq, hkv, new, page):
+    tree_case((37, 65, 90), new, hq, hkv, 128, 128, page=page, seed=hq + sum(new))
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+@pytest.mark.parametrize("chunk", [16, 64, 176])
+@pytest.mark.parametrize("new", [(5, 1, 0, 30), (16, 1, 17, 64)])
+def test_splits(kernel, chunk, new):
+    """Chunks that begin and end inside the tree, some that hold none of a row's tokens."""
+    _, plan, *_ = tree_case((300, 1, 17, 1111), new, 8, 2, 128, 128, kernel=kernel,
+                            force_chunk_tokens=chunk, seed=chunk)
+    assert plan.info.split == 1
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+@pytest.mark.parametrize("before", [0, 1, 15, 16, 111, 112, 113, 127, 128, 129, 255])
+def test_tree_across_tiles(kernel, before):
+    """The tree's first token anywhere in a tile of 16 and of 128."""
+    tree_case((before + 37,), (37,), 4, 1, 128, 128, kernel=kernel, seed=before)
+
+
+@pytest.mark.parametrize("kernel,hq,hkv", [(1, 2, 2), (1, 4, 2), (1, 8, 1), (3, 4, 2), (3, 32, 1)])
+def test_masks_of_any_kind(kernel, hq, hkv):
+    """Rows that see nothing of the tree, nothing at all, later nodes, all; bits behind the
+    request's rows set."""
+    rng = np.random.default_rng(hq)
+    new, kv = (7, 4, 20, 3), (60, 4, 20, 200)
+    masks = [rng.integers(-2**31, 2**31, (n, 1)).astype(np.int32) for n in new]
+    for m in masks:
+        m[0], m[-1] = 0, -1  # (requests 1 and 2 have no token before the tree: row 0 sees none)
+    _, _, out, lse, *_ = tree_case(kv, new, hq, hkv, 128, 128, masks=masks, words=1, kernel=kernel,
+                                   seed=hq)
+    assert (lse[7] == -math.inf).all() and (lse[11] == -math.inf).all()
+    assert (out[7] == 0).all() and (out[11] == 0).all()
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+def test_tokens_past_the_words_are_not_seen(kernel):
+    masks = [np.full((50, 1), -1, dtype=np.int32), np.full((3, 1), -1, dtype=np.int32)]
+    tree_case((90, 30), (50, 3), 4, 2, 128, 128, masks=masks, words=1, kernel=kernel, seed=5)
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+def test_large_tree(kernel):
+    """300 nodes: ten words a row, several tiles of tree, chains far apart."""
+    rng = np.random.default_rng(7)
+    masks = [T.mask_words(T.ancestors(T.random_parents(rng, 300, deep=True)), 10)]
+    tree_case((301,), (300,), 4, 2, 128, 128, masks=masks, words=10, kernel=kernel, seed=6)
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+def test_values_of_all_sizes(kernel):
+    """Global scales far from 1 (scores stay in range by the query)."""
+    tree_case((70, 200), (9, 30), 4, 2, 128, 128, kernel=kernel, g=(0.75, 2.0 ** -60), seed=8)
+    tree_case((70, 200), (9, 30), 4, 2, 128, 128, kernel=kernel, g=(2.0 ** -30, 2.0 ** 60), seed=9)
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+def test_a_chain_is_the_causal_mask(kernel):
+    """A tree without branches gives what the causal plan gives, bit for bit."""
+    kv, new = (37, 300, 64), (5, 33, 64)
+    chains = [T.mask_words(T.ancestors(range(-1, n - 1)), 2) for n in new]
+    c, plan, out, lse, q, _ = tree_case(kv, new, 8, 2, 128, 128, masks=chains, words=2,
+                                        kernel=kernel, seed=11)
+    qo = np.concatenate([[0], np.cumsum(new)])
+    causal = N.nvfp4kv_decode_plan(qo, c.indptr, c.last, 8, 2, 128, 128, kernel=kernel, causal=True)
+    o2, l2 = N.nvfp4kv_decode_run(causal, q, c.cache, c.kv_indices)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+def test_live_lengths(kernel):
+    """The plan keeps page counts; the tree moves with the lengths that the device holds."""
+    tree_case((21, 35), (5, 9), 8, 2, 128, 128, live=[16, 16], kernel=kernel, seed=12)
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+@pytest.mark.parametrize("page", [16, 1])
+def test_new_tokens_in_the_same_launch(kernel, page):
+    """new_k and new_v: the cache holds what nvfp4kv_quantize_append writes, the output is
+    that of the call without them."""
+    kv, new, hkv = (37, 300, 30), (7, 33, 30), 2
+    c = T.Nvfp4Case(kv, page, hkv, 128, 128, seed=13)
+    other = T.Nvfp4Case(kv, page, hkv, 128, 128, seed=13)
+    g = torch.Generator().manual_seed(13)
+    rows = sum(new)
+    k, v = (torch.randn((rows, hkv + 1, 128), generator=g).to(torch.bfloat16).cuda()[:, 1:]
+            for _ in range(2))
+    q = torch.randn((rows, 8, 128), generator=g).to(torch.bfloat16).cuda()
+    rng = np.random.default_rng(13)
+    mask = i32(np.concatenate([T.mask_words(T.ancestors(T.random_parents(rng, n)), 2)
+                               for n in new]))
+    qo = np.concatenate([[0], np.cumsum(new)])
+    idx = i32([b for b, n in enumerate(new) for _ in range(n)])
+    pos = i32([t for n, m in zip(new, kv) for t in range(m - n, m)])
+    N.nvfp4kv_quantize_append(other.cache, k, v, idx, pos, other.kv_indices, other.kv_indptr,
+                              other.last_page_len)
+    plan = N.nvfp4kv_decode_plan(qo, c.indptr, c.last, 8, hkv, 128, 128, page_size=page,
+                                 kernel=kernel)
+    want = N.nvfp4kv_tree_run(plan, q, other.cache, other.kv_indices, mask)
+    got = N.nvfp4kv_tree_run(plan, q, c.cache, c.kv_indices, mask, new_k=k, new_v=v)
+    assert N.nvfp4kv_workspace_flags(plan) == 0
+    mine, theirs = c.download(), other.download()
+    for n in mine:
+        assert np.array_equal(mine[n], theirs[n]), n
+    for a, b in zip(got, want):
+        assert torch.allclose(a.float(), b.float(), atol=0 if not plan.info.split else 2.0 ** -7)
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+def test_bad_page_ids_are_flagged(kernel):
+    c = T.Nvfp4Case((100,), 16, 2, 128, 128, seed=14)
+    idx = c.kv_indices.clone()
+    idx[2], idx[4] = c.total, -5
+    plan = N.nvfp4kv_decode_plan([0, 6], c.indptr, c.last, 8, 2, 128, 128, kernel=kernel)
+    q = torch.zeros((6, 8, 128), dtype=torch.bfloat16).cuda()
+    N.nvfp4kv_tree_run(plan, q, c.cache, idx, i32(np.full((6, 1), -1)))
+    assert N.nvfp4kv_workspace_flags(plan, clear=True) == _lib.FLAG_BAD_PAGE_INDEX
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+def test_stream_graph_and_given_outputs(kernel):
+    c, plan, out, lse, q, mask = tree_case((37, 300), (9, 16), 8, 2, 128, 128, kernel=kernel,
+                                           seed=15, q_pad=3)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o2, l2 = N.nvfp4kv_tree_run(plan, q, c.cache, c.kv_indices, mask, stream=side)
+    side.synchronize()
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+    o3, l3 = torch.zeros_like(out), torch.zeros_like(lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        N.nvfp4kv_tree_run(plan, q, c.cache, c.kv_indices, mask, out=o3, lse=l3)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, o3) and torch.equal(lse, l3)
+    mask.zero_()  # read at replay: the rows see what stands before the tree only
+    graph.replay()
+    torch.cuda.synchronize()
+    assert not torch.equal(out, o3) and (l3[:9] != lse[:9]).all()
