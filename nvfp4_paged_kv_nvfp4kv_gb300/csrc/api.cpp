@@ -21,7 +21,7 @@
 namespace nvfp4kv {
 bool attend_config_tc(int dk, int dv, int rows, bool tree, AttendConfig* cfg);
 bool attend_config_simt(int dk, int dv, int rows, AttendConfig* cfg);
-bool attend_config_tcgen05(int dk, int dv, int rows, bool tree, AttendConfig* cfg);
+bool attend_config_tcgen05(int dk, int dv, int rows, AttendConfig* cfg);
 bool attend_config_dec(int dk, int dv, int rows, int quads, AttendConfig* cfg);
 bool attend_config_tc_fp4qp(int dk, int dv, int rows, int pass, AttendConfig* cfg);
 cudaError_t prepare_kernel(const AttendConfig& cfg);
@@ -142,8 +142,8 @@ CacheView view_of(const nvfp4kv_paged_cache* c) {
 bool lookup_kernel(int kind, int dk, int dv, int page_size, int rows, AttendConfig* cfg,
                    bool tree = false) {
   if (kind == kKernelTensorCore) return attend_config_tc(dk, dv, rows, tree, cfg);
-  if (kind == kKernelTcgen05) return attend_config_tcgen05(dk, dv, rows, tree, cfg);
   if (tree) return false;
+  if (kind == kKernelTcgen05) return attend_config_tcgen05(dk, dv, rows, cfg);
   if (kind == kKernelCudaCore) return attend_config_simt(dk, dv, rows, cfg);
   if (kind == kKernelFp4QP) return attend_config_tc_fp4qp(dk, dv, rows, 2, cfg);
   if (kind == kKernelE4m3) return attend_config_e4m3(dk, dv, page_size, rows, cfg);
@@ -769,6 +769,18 @@ struct NewTokens {
   int64_t k_stride_tok = 0, k_stride_head = 0, v_stride_tok = 0, v_stride_head = 0;
 };
 
+// CTAs of a cluster of the wide tree kernel: those that share the value dims, doubled
+// while the launch's CTAs stay one wave and each keeps kTreeTiles tiles of a whole unit.
+constexpr int64_t kTreeTiles = 3;
+int tree_cluster(const nvfp4kv_plan_info* info, const TreeConfig& cfg, int blocks) {
+  const int64_t tokens = (int64_t)info->chunk_pages * kPageSize;
+  int ctas = cfg.value_parts;
+  while (ctas < 8 && (int64_t)info->num_units * blocks * ctas * 2 <= info->num_sms &&
+         tokens >= kTreeTiles * cfg.tile_tokens * (2 * ctas / cfg.value_parts))
+    ctas *= 2;
+  return ctas;
+}
+
 int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_tok,
            int64_t q_stride_head, const nvfp4kv_paged_cache* cache, const int32_t* kv_indices,
            float sm_scale, void* workspace, uint64_t workspace_bytes, void* out_bf16,
@@ -807,7 +819,16 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
                    info->page_size == kPageSize && bulk_decode_layout(cache) &&
                    attend_config_dec(info->head_dim_qk, info->head_dim_vo, 8,
                                      info->num_units <= info->num_sms ? 1 : 4, &cfg);
-  if (!dec && !lookup_kernel(info->kernel, info->head_dim_qk, info->head_dim_vo,
+  // trees: more than 16 rows a kv head go to the kernel of 128-row blocks (it takes a plan
+  // of either kernel), up to 16 to the mma.sync kernel's own form
+  TreeConfig tcfg{};
+  const bool wide_tree = tree && (info->kernel == kKernelTcgen05 || info->row_blocks > 1) &&
+                         attend_config_tree(info->head_dim_qk, info->head_dim_vo, &tcfg);
+  if (wide_tree) {
+    cfg.func = tcfg.func;
+    cfg.smem_bytes = tcfg.smem_bytes;
+  }
+  if (!dec && !wide_tree && !lookup_kernel(info->kernel, info->head_dim_qk, info->head_dim_vo,
                              info->page_size, info->rows_per_block, &cfg, tree != nullptr))
     return fail(NVFP4KV_ERR_UNSUPPORTED, "planned kernel not available");
   cudaError_t e = prepare_kernel(cfg);
@@ -822,6 +843,7 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
   if (tree) {
     p.tree_mask = tree->mask;
     p.tree_words = tree->words;
+    p.row_blocks = info->row_blocks;
   }
   if (nt) {
     p.new_k = static_cast<const uint16_t*>(nt->k);
@@ -849,7 +871,13 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
     p.new_k = nullptr;
     p.new_v = nullptr;
   }
-  e = launch_attend(cfg, p, info->num_units, info->row_blocks, stream);
+  if (wide_tree) {
+    const int blocks = (info->row_blocks * info->rows_per_block + kTreeRows - 1) / kTreeRows;
+    e = launch_attend_tree(tcfg, p, info->num_units, blocks, tree_cluster(info, tcfg, blocks),
+                           stream);
+  } else {
+    e = launch_attend(cfg, p, info->num_units, info->row_blocks, stream);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   return ok();
 }

@@ -101,7 +101,7 @@ struct Tg5 {
   static_assert(SMEM <= 232448, "shared memory");
 };
 
-template <int N, bool TREE>
+template <int N>
 __global__ void __launch_bounds__(kThreads, 1) attend_tcgen05_kernel(const AttendParams p) {
   using T = Tg5<N>;
   constexpr int DK = T::DK, DV = T::DV, RS = T::RS, NH = T::NH;
@@ -408,14 +408,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tcgen05_kernel(const Atten
     if (tid < N) {
       const int r = tid, gr = row0 + r;
       if (gr < R) {
-        const int lim =
-            p.causal && !TREE ? (u.kv_len - u.qo_len + gr / G) : (u.kv_len - 1);
+        const int lim = p.causal ? (u.kv_len - u.qo_len + gr / G) : (u.kv_len - 1);
         s_f[r] = p.qk_scale_log2 * __uint_as_float((uint32_t)(127 - exp_of(r)) << 23);
         s_nm[r] = 0.f;
         s_thr[r] = -INFINITY;  // no maximum yet: any visible score raises
         s_lim[r] = lim;
-        // (the tree's tokens are looked up in the rows' masks)
-        atomicMin(s_minlim, TREE ? min(lim, u.kv_len - u.qo_len - 1) : lim);
+        atomicMin(s_minlim, lim);
       } else {  // padding row: every score -inf, never raises
         s_f[r] = 0.f;
         s_nm[r] = -INFINITY;
@@ -461,8 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tcgen05_kernel(const Atten
           const int ll[4] = {lm.x, lm.y, lm.z, lm.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (tok > ll[e] || (TREE && tree_hides(p, u, row0 + cb + e4 + e, tok)))
-              x[e4 + e] = -INFINITY;
+            if (tok > ll[e]) x[e4 + e] = -INFINITY;
         }
       }
     };
@@ -678,26 +675,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tcgen05_kernel(const Atten
 }
 
 template <int N>
-bool make_tg5(bool tree, AttendConfig* cfg) {
+bool make_tg5(AttendConfig* cfg) {
   cfg->kind = kKernelTcgen05;
   cfg->dk = 128;
   cfg->dv = 128;
   cfg->rows = N;
   cfg->warps = kThreads / 32;
   cfg->smem_bytes = Tg5<N>::SMEM;
-  cfg->func = tree ? reinterpret_cast<const void*>(&attend_tcgen05_kernel<N, true>)
-                   : reinterpret_cast<const void*>(&attend_tcgen05_kernel<N, false>);
+  cfg->func = reinterpret_cast<const void*>(&attend_tcgen05_kernel<N>);
   return true;
 }
 
 }  // namespace
 
 // tcgen05 kernel for (dk, dv) with up to `rows` query rows per CTA.
-bool attend_config_tcgen05(int dk, int dv, int rows, bool tree, AttendConfig* cfg) {
+bool attend_config_tcgen05(int dk, int dv, int rows, AttendConfig* cfg) {
   if (dk != 128 || dv != 128) return false;
-  if (rows <= 16) return make_tg5<16>(tree, cfg);
-  if (rows <= 32) return make_tg5<32>(tree, cfg);
-  return make_tg5<64>(tree, cfg);
+  if (rows <= 16) return make_tg5<16>(cfg);
+  if (rows <= 32) return make_tg5<32>(cfg);
+  return make_tg5<64>(cfg);
 }
 
 }  // namespace nvfp4kv

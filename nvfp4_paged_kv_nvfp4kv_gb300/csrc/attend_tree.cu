@@ -1,0 +1,762 @@
+// attend_tree.cu -- attention of drafted trees over the paged NVFP4 cache on the
+// fifth-generation tensor cores, for more than 16 query rows a kv head, sm_103a.
+//
+// Row r (a node of request b's tree and a head of the kv head's group) sees token t where
+//   t < L_b - n_b                       (before the tree), or
+//   bit t - (L_b - n_b) of its words    (itself and what it continues);
+//   s_t = sm_scale * q . k_t,  o = sum_t p_t v_t / sum_t p_t,  p_t = exp(s_t),
+//   lse = ln sum_t p_t; a row that sees nothing has o = 0 and lse = -inf.
+//
+// One CTA takes up to 128 query rows on the M side of both products, so a tile of keys is
+// dequantised once for all of them and a softmax row belongs to two threads:
+//  * K loaders (4 warps) and V loaders (4 warps): cp.async of the packed rows and scales
+//    (a warp its own tokens, RS - 1 tiles ahead), then e2m1 -> f16 times the E4M3 block
+//    scale (exact) into the 128-byte-swizzled operand layouts in shared memory;
+//  * issue (one thread): S = Q K^T (A = Q in tensor memory, N = TT tokens) into one of two
+//    tiles of tensor memory, and O += P V (A = P, which takes the place of its S);
+//  * softmax (8 warps): thread = row and half of the tile's tokens, so the maximum and the
+//    sum need no shuffles; the two halves of a row meet in a barrier of their two warps
+//    once a tile.  m is raised only when a score exceeds it by 2^8 (then O is rescaled).
+//    Row sums are float32 of the unrounded p; P is rounded to f16 (2^-11), the operand's
+//    type.  A tile that reaches into the tree takes each row's 64 (32) bits at once.
+// Value dims beyond 128 go to another CTA (VH of them), which forms the same S.
+//
+// The plan splits long requests for its own row blocks; here a cluster of CTAs divides a
+// unit's tokens (and value dims) further, as many as the SMs allow, and joins its states
+// through distributed shared memory: no workspace beyond the plan's is needed, and each
+// CTA stores a share of the rows.  Units of a split request fold as elsewhere
+// (log-sum-exp over partial states, by the last CTA to arrive).
+// Every wait is bounded; one that runs out sets flag 0x4 and the CTA winds down.
+#include <cstdint>
+
+#include <cuda_runtime.h>
+
+#include "append_fused.cuh"
+#include "device_common.cuh"
+#include "internal.h"
+#include "tcgen05.cuh"
+
+namespace nvfp4kv {
+namespace {
+
+using namespace dev;
+using namespace tc5;
+
+constexpr int kRows = 128;
+constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;  // of K, and of V
+constexpr int kThreads = 32 * (kSoftmaxWarps + 2 * kLoadWarps + 1);
+constexpr float kRaise = 8.f;  // log2 of the largest p before m is raised
+// Test build only: the first K loader of CTA (0, 0) withholds its arrival for the first
+// tile, so the issuer's wait runs out and the CTA winds down.
+#ifndef NVFP4KV_TREE_TEST_SKIP_ARRIVE
+#define NVFP4KV_TREE_TEST_SKIP_ARRIVE 0
+#endif
+
+// DVC: value dims of a CTA, DV = VH * DVC; TT: tokens of a tile
+template <int DK, int DVC, int VH, int TT>
+struct Tree {
+  static constexpr int DV = DVC * VH;
+  static constexpr int KPT = 128 / TT;              // loader threads a token
+  static constexpr int KSEG = DK / 2 / KPT, VSEG = DVC / 2 / KPT;     // packed bytes of each
+  static constexpr int KSF = DK / 16 / KPT, VSF = DVC / 16 / KPT;     // scale bytes of each
+  static constexpr int KW = 32 * (KSEG + KSF), VW = 32 * (VSEG + VSF);  // a warp's stage
+  static constexpr int STAGE = kLoadWarps * (KW + VW);
+  static constexpr int KBYTES = TT * DK * 2, VBYTES = TT * DVC * 2;   // operand tiles
+  static constexpr int KB = 2, VB = DK == 512 ? 2 : 3;
+  static constexpr int RS = DK == 512 ? 2 : DK == 128 ? 3 : 4;
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_V = OFF_K + KB * KBYTES;
+  static constexpr int OFF_RAW = OFF_V + VB * VBYTES;
+  static constexpr int OFF_MISC = OFF_RAW + RS * STAGE;
+  static constexpr int MISC = 256 + 4 * kRows * 4 + 64;
+  static constexpr int SMEM = OFF_MISC + MISC + 1024;  // + alignment slack
+  static constexpr int OROW = DVC + 4;                 // floats of a row in the joined states
+  // tensor memory columns: S (P) x 2, O, Q
+  static constexpr int SCOL = 0, OCOL = 2 * TT, QCOL = OCOL + DVC;
+  static constexpr int COLS = QCOL + DK / 2, TCOLS = 512;
+  static constexpr uint32_t IDESC_S = idesc_f16(kRows, TT, 0, 0);
+  static constexpr uint32_t IDESC_O = idesc_f16(kRows, DVC, 0, 1);
+  static_assert(COLS <= TCOLS && SMEM <= 232448, "resources");
+  static_assert(OFF_RAW % 1024 == 0 && OFF_MISC % 16 == 0, "alignment");
+  static_assert(kRows * OROW * 4 <= OFF_RAW, "the joined states take the operands' place");
+};
+
+__device__ __forceinline__ void cluster_arrive_wait() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n"
+               ::: "memory");
+}
+// the address of shared memory `a` in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t peer(uint32_t a, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float peer_f32(uint32_t a) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_v4(uint32_t a) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+// 16-byte chunk c of row r in a warp's stage (rows of SEG bytes): the lanes of a quarter
+// warp, a row each, then read distinct banks
+template <int SEG>
+__device__ __forceinline__ int raw_chunk(int r, int c) {
+  if constexpr (SEG == 32) return c ^ ((r >> 2) & 1);
+  if constexpr (SEG == 64) return c ^ ((r >> 1) & 3);
+  return c ^ (r & 7);
+}
+
+// One loader warp: K (V false) or V rows of the tiles [t0, t0 + ntiles) of unit u.
+template <class T, int TT, bool V>
+__device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit& u, int w,
+                                           int lane, int t0, int ntiles, int tok_end, int vh,
+                                           uint8_t* raw, uint8_t* tiles, uint64_t* full,
+                                           uint64_t* empty, volatile int* abort) {
+  constexpr int SEG = V ? T::VSEG : T::KSEG, SF = V ? T::VSF : T::KSF;
+  constexpr int BYTES = V ? T::VBYTES : T::KBYTES, NB = V ? T::VB : T::KB, RS = T::RS;
+  constexpr int LPR = SEG / 16, RPI = 32 / LPR;  // lanes a row, rows a copy instruction
+  const CacheView& c = p.cache;
+  const int seg = T::KPT == 1 ? 0 : w >> 1;       // part of the row's dims
+  const int first = T::KPT == 1 ? 32 * w : 32 * (w & 1);  // this warp's first token of a tile
+  const int shift = p.page_size == 1 ? 0 : 4, slots = (1 << shift) - 1;
+  const int64_t sp = V ? c.v_sp : c.k_sp, ss = V ? c.v_ss : c.k_ss;
+  const int64_t fsp = V ? c.vsf_sp : c.ksf_sp, fss = V ? c.vsf_ss : c.ksf_ss;
+  const int part = V ? vh * T::KPT + seg : seg;   // the warp's part of the whole row
+  const uint8_t* data = (V ? c.v_data + u.h_kv * c.v_sh : c.k_data + u.h_kv * c.k_sh) + part * SEG;
+  const uint8_t* sf = (V ? c.v_sf + u.h_kv * c.vsf_sh : c.k_sf + u.h_kv * c.ksf_sh) + part * SF;
+  uint8_t* mine = raw + w * (V ? T::VW : T::KW);
+  const int r0 = lane / LPR, ch = lane % LPR;
+  // page id of this lane's token in tile i, a tile ahead of its use (where it is checked);
+  // a token past the unit's pages takes the last one
+  auto load_pid = [&](int i) -> int32_t {
+    if (i >= ntiles) return 0;
+    const int rel = (t0 + i) * TT + first + lane;
+    return __ldg(p.kv_indices + u.page_begin + min(rel >> shift, u.num_pages - 1));
+  };
+  auto issue = [&](int i, int32_t pid) {
+    if (pid < 0 || pid >= c.num_pages) {
+      atomicOr(p.flags, 0x1u);
+      pid = 0;
+    }
+    uint8_t* st = mine + (i % RS) * T::STAGE;
+    const int rel = (t0 + i) * TT + first;  // of the warp's row 0 (a multiple of 16)
+#pragma unroll
+    for (int k = 0; k < LPR; ++k) {
+      const int r = r0 + k * RPI;
+      const int64_t pg = __shfl_sync(0xffffffffu, pid, r);
+      cp_async_16(st + r * SEG + 16 * raw_chunk<SEG>(r, ch),
+                  data + pg * sp + ((rel + r) & slots) * ss + 16 * ch);
+    }
+    cp_async_small<SF>(st + 32 * SEG + lane * SF, sf + pid * fsp + ((rel + lane) & slots) * fss);
+  };
+#pragma unroll
+  for (int i = 0; i < RS - 1; ++i) {
+    const int32_t pid = load_pid(i);
+    if (i < ntiles) issue(i, pid);
+    cp_async_commit();
+  }
+  int32_t next = load_pid(RS - 1);
+  const int tl = first + lane;  // this lane's token of a tile
+  uint8_t* row = tiles + (tl >> 3) * 1024 + (tl & 7) * 128;
+  for (int i = 0; i < ntiles; ++i) {
+    const int32_t pid = next;
+    next = load_pid(i + RS);
+    if (i + RS - 1 < ntiles) issue(i + RS - 1, pid);
+    cp_async_commit();
+    cp_async_wait<RS - 1>();  // this thread's copies of tile i have landed
+    const int b = i % NB;
+    bool ok = true;
+    if (i >= NB) {
+      if (lane == 0) ok = wait_bar(&empty[b], (i / NB - 1) & 1, abort, p.flags);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    __syncwarp();  // and those of the warp
+    if (!ok) break;
+    const uint8_t* st = mine + (i % RS) * T::STAGE;
+    // slots past the request's end may hold a NaN scale: their values count as 0 (their
+    // scores are replaced)
+    const bool past = V && u.tok_begin + (t0 + i) * TT + tl >= tok_end;
+    uint32_t scales[(SF + 3) / 4];
+#pragma unroll
+    for (int k = 0; k < SF / 4; ++k)
+      scales[k] = past ? 0u : *reinterpret_cast<const uint32_t*>(st + 32 * SEG + lane * SF + 4 * k);
+    uint8_t* out = row + b * BYTES;
+#pragma unroll
+    for (int k = 0; k < LPR; ++k) {
+      const uint4 q = *reinterpret_cast<const uint4*>(st + lane * SEG + 16 * raw_chunk<SEG>(lane, k));
+      const uint32_t s2 = e4m3x2_to_f16x2(scales[k / 2] >> (16 * (k & 1)));
+      const uint32_t lo = bcast_lo(s2), hi = bcast_hi(s2);
+      const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t h[4];
+        e2m1x8_to_f16x8(words[e], h);
+        const uint32_t s = e < 2 ? lo : hi;
+        const int d = 2 * SEG * seg + 32 * k + 8 * e;  // first of the 8 dims
+        *reinterpret_cast<uint4*>(out + (d >> 6) * (TT * 128) +
+                                  ((((d & 63) >> 3) ^ (tl & 7)) << 4)) =
+            make_uint4(hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
+      }
+    }
+    fence_async_smem();
+    __syncwarp();
+    const bool withhold = NVFP4KV_TREE_TEST_SKIP_ARRIVE && !V && blockIdx.x == 0 &&
+                          blockIdx.y == 0 && w == 0 && i == 0;
+    if (lane == 0 && !withhold) mbar_arrive(&full[b]);
+  }
+  cp_async_wait<0>();
+}
+
+template <int DK, int DVC, int VH, int TT>
+__global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendParams p) {
+  using T = Tree<DK, DVC, VH, TT>;
+  constexpr int KB = T::KB, VB = T::VB, DV = T::DV;
+  constexpr int W = TT / 2;      // tokens of a tile that a softmax thread has
+  constexpr float kLn2 = 0.69314718055994530942f;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::OFF_MISC);
+  uint64_t* k_full = bars;        // [KB] K tile in its operand layout
+  uint64_t* k_empty = bars + 3;   // [KB] S done
+  uint64_t* v_full = bars + 6;    // [VB]
+  uint64_t* v_empty = bars + 9;   // [VB] O done
+  uint64_t* s_full = bars + 12;   // [2] S done -> softmax
+  uint64_t* p_full = bars + 14;   // [2] softmax -> issue
+  uint64_t* pv_done = bars + 16;  // [2] O done -> softmax
+  uint64_t* q_full = bars + 18;
+  uint64_t* fin = bars + 19;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 20);
+  volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
+  int* s_last = reinterpret_cast<int*>(s_tmem + 2);
+  float* s_x = reinterpret_cast<float*>(smem + T::OFF_MISC + 256);  // [2][128] the halves' values
+  float* s_m = s_x + 2 * kRows;   // [128] maxima, then
+  float* s_l = s_m + kRows;       // [128] sums of the CTA's state
+
+  const WorkUnit u = load_unit(p);
+  const int G = p.group, R = G * u.qo_len, C = p.tree_ctas;
+  const int block = blockIdx.y / C, rank = blockIdx.y % C;
+  const int vh = rank % VH, part = rank / VH, parts = C / VH;
+  const int row0 = block * kRows;
+  if (row0 >= R) return;  // the whole cluster, before any barrier or tensor memory use
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int nrows = min(kRows, R - row0);
+  // this CTA's tiles of the unit; tokens from tok_end on do not exist
+  const int tok_end = min(u.kv_len, u.tok_begin + p.page_size * u.num_pages);
+  const int all_tiles = (tok_end - u.tok_begin + TT - 1) / TT;
+  const int t0 = static_cast<int>((int64_t)all_tiles * part / parts);
+  const int ntiles = static_cast<int>((int64_t)all_tiles * (part + 1) / parts) - t0;
+
+  if (tid == 0) {
+    for (int b = 0; b < KB; ++b) {
+      mbar_init(&k_full[b], kLoadWarps);
+      mbar_init(&k_empty[b], 1);
+    }
+    for (int b = 0; b < VB; ++b) {
+      mbar_init(&v_full[b], kLoadWarps);
+      mbar_init(&v_empty[b], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&p_full[b], kSoftmaxWarps);
+      mbar_init(&pv_done[b], 1);
+    }
+    mbar_init(q_full, kSoftmaxWarps);
+    mbar_init(fin, 1);
+    mbar_init_fence();
+    *s_abort = 0;
+  }
+  if (warp == 0) {
+    tmem_alloc(s_tmem, T::TCOLS);
+    tmem_relinquish();
+  }
+  // fused append: the step's new tokens among this CTA's tiles, stored before any copy
+  // reads them (CTAs that share tokens store the same bytes)
+  if (p.new_k != nullptr) {
+    const int lo = max(u.kv_len - u.qo_len, u.tok_begin + t0 * TT);
+    const int hi = min(tok_end, u.tok_begin + (t0 + ntiles) * TT);
+    if (lo < hi) append_unit_tokens<DK, DV>(p, u, lo, hi, tid, kThreads);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+
+  if (warp >= kSoftmaxWarps && warp < kSoftmaxWarps + kLoadWarps) {
+    load_tiles<T, TT, false>(p, u, warp - kSoftmaxWarps, lane, t0, ntiles, tok_end, vh,
+                             smem + T::OFF_RAW, smem + T::OFF_K, k_full, k_empty, s_abort);
+  } else if (warp >= kSoftmaxWarps + kLoadWarps && warp < kSoftmaxWarps + 2 * kLoadWarps) {
+    load_tiles<T, TT, true>(p, u, warp - kSoftmaxWarps - kLoadWarps, lane, t0, ntiles, tok_end, vh,
+                            smem + T::OFF_RAW + kLoadWarps * T::KW, smem + T::OFF_V, v_full,
+                            v_empty, s_abort);
+  } else if (warp == kSoftmaxWarps + 2 * kLoadWarps) {
+    // ================= product issue (one thread) =============================
+    if (lane == 0) {
+      const uint64_t kd0 = smem_desc(smem_addr(smem + T::OFF_K), 16, 1024, kSwz128);
+      const uint64_t vd0 = smem_desc(smem_addr(smem + T::OFF_V), TT * 128, 1024, kSwz128);
+      auto issue_s = [&](int i) {
+        tc_fence_after();
+        const uint64_t kd = kd0 + (((i % KB) * T::KBYTES) >> 4);
+        const uint32_t d = tmem + T::SCOL + TT * (i & 1);
+#pragma unroll 8
+        for (int kk = 0; kk < DK / 16; ++kk)
+          umma_ts(d, tmem + T::QCOL + 8 * kk, kd + (((kk >> 2) * (TT * 128) + (kk & 3) * 32) >> 4),
+                  T::IDESC_S, kk > 0 ? 1u : 0u);
+        umma_commit(&s_full[i & 1]);
+        umma_commit(&k_empty[i % KB]);
+      };
+      auto issue_o = [&](int i) {
+        tc_fence_after();
+        const uint64_t vd = vd0 + (((i % VB) * T::VBYTES) >> 4);
+        const uint32_t a = tmem + T::SCOL + TT * (i & 1);
+#pragma unroll
+        for (int k = 0; k < TT / 16; ++k)  // P: each half's tokens in front of its S columns
+          umma_ts(tmem + T::OCOL, a + W * (k / (W / 16)) + 8 * (k % (W / 16)),
+                  vd + ((k * 2048) >> 4), T::IDESC_O, (i > 0 || k > 0) ? 1u : 0u);
+        umma_commit(&pv_done[i & 1]);
+        umma_commit(&v_empty[i % VB]);
+      };
+      // whichever product has its inputs: S(s) once its K is in and the tile's columns
+      // are free (O(s - 2), which reads them as P, is issued), O(o) once P(o) and V are
+      bool ok = ntiles == 0 || wait_bar(q_full, 0, s_abort, p.flags);
+      int s = 0, o = 0;
+      uint32_t idle = 0;
+      while (ok && o < ntiles) {
+        bool prog = false;
+        if (s < ntiles && s < o + 2 && mbar_test_wait(&k_full[s % KB], (s / KB) & 1)) {
+          issue_s(s);
+          ++s;
+          prog = true;
+        }
+        if (o < s && mbar_test_wait(&p_full[o & 1], (o >> 1) & 1) &&
+            mbar_test_wait(&v_full[o % VB], (o / VB) & 1)) {
+          issue_o(o);
+          ++o;
+          prog = true;
+        }
+        if (prog) {
+          idle = 0;
+          continue;
+        }
+        if (*s_abort) break;
+        if (++idle > kIdlePolls) {
+          *s_abort = 1;
+          atomicOr(p.flags, 0x4u);
+          break;
+        }
+        __nanosleep(32);
+      }
+      umma_commit(fin);  // wind-down: every product issued has completed
+      drain_bar(fin, 0, p.flags);
+    }
+    __syncwarp();
+  } else {
+    // ================= softmax (thread = row, half of a tile's tokens) ===========
+    const int q4 = warp & 3, half = warp >> 2, r = 32 * q4 + lane;
+    const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
+    const bool active = 32 * q4 < nrows, real = r < nrows;  // warp-uniform; this row
+    const int gr = row0 + (real ? r : 0), node = gr / G;
+    // ---- Q: bf16 -> f16 times a power of two per row, into tensor memory ----------
+    float f = 0.f;
+    {
+      const uint16_t* q = p.q + (int64_t)(u.qo_begin + node) * p.q_stride_tok +
+                          (int64_t)(u.h_kv * G + gr % G) * p.q_stride_head + half * (DK / 2);
+      auto load = [&](int c) -> uint4 {
+        return real ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0u, 0u, 0u, 0u);
+      };
+      float am = 0.f;
+      if (active) {
+#pragma unroll 8
+        for (int c = 0; c < DK / 16; ++c) {
+          const uint4 v = load(c);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            am = fmax3(am, fabsf(bf16_bits_to_f32(w[e] & 0xFFFFu)),
+                       fabsf(bf16_bits_to_f32(w[e] >> 16)));
+        }
+        s_x[half * kRows + r] = am;
+        named_sync(1 + q4, 64);
+        am = fmaxf(am, s_x[(half ^ 1) * kRows + r]);
+        int e = 0;  // amax * 2^e in [2^14, 2^15)
+        if (am > 0.f) e = 14 - (int)((__float_as_uint(am) >> 23) & 0xFF) + 127;
+        e = max(-120, min(120, e));
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        f = real ? p.qk_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
+#pragma unroll 2
+        for (int c = 0; c < DK / 64; ++c) {  // 16 columns of two dims
+          uint32_t h[16];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint4 v = load(4 * c + k);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              h[4 * k + x] = f32x2_to_f16x2(bf16_bits_to_f32(w[x] & 0xFFFFu) * up,
+                                            bf16_bits_to_f32(w[x] >> 16) * up);
+          }
+          tmem_st16(tmem + lane_base + T::QCOL + half * (DK / 4) + 16 * c, h);
+        }
+        tmem_wait_st();
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
+    // ---- the tiles ---------------------------------------------------------------------
+    const int before = u.kv_len - u.qo_len;  // tokens that every row sees
+    const uint32_t* words = p.tree_mask + (int64_t)(u.qo_begin + node) * p.tree_words;
+    auto word = [&](int k) -> uint64_t {
+      return k >= 0 && k < p.tree_words ? __ldg(words + k) : 0u;
+    };
+    // bit t: whether the row sees token tok + t
+    auto visible = [&](int tok) -> uint64_t {
+      const int j = tok - before, n = tok_end - tok;
+      uint64_t v;
+      if (j <= -64) {
+        v = ~0ull;
+      } else if (j < 0) {
+        v = (word(0) | word(1) << 32) << -j | ((1ull << -j) - 1);
+      } else {
+        const int k = j >> 5, s = j & 31;
+        v = (word(k) | word(k + 1) << 32) >> s;
+        if (s) v |= word(k + 2) << (64 - s);
+      }
+      if (n < 64) v = n <= 0 ? 0ull : v & ((1ull << n) - 1);
+      return real ? v : 0ull;
+    };
+    float m = -INFINITY, nm = 0.f, l = 0.f;  // the row's maximum (log2), -m once it has one
+    float thr = real ? -INFINITY : INFINITY;
+    const int some_hidden = min(before, tok_end);  // tiles that reach past it are masked
+    for (int i = 0; i < ntiles; ++i) {
+      const int sb = i & 1;
+      if (!active) {
+        // (nothing to do for the rows that are not there but to keep the count)
+        if (lane == 0) {
+          wait_bar(&s_full[sb], (i >> 1) & 1, s_abort, p.flags);
+          mbar_arrive(&p_full[sb]);
+        }
+        continue;
+      }
+      const int tok = u.tok_begin + (t0 + i) * TT + half * W;
+      const bool masked = u.tok_begin + (t0 + i + 1) * TT > some_hidden;
+      uint64_t see = ~0ull;
+      if (masked) see = visible(tok);
+      if (lane == 0) wait_bar(&s_full[sb], (i >> 1) & 1, s_abort, p.flags);
+      __syncwarp();
+      tc_fence_after();
+      float x[W];
+      const uint32_t sa = tmem + lane_base + T::SCOL + TT * sb + W * half;
+      {
+        uint32_t sv[W];
+        tmem_ld<W>(sa, sv);
+        tmem_wait_ld<W>(sv);
+#pragma unroll
+        for (int e = 0; e < W; ++e) x[e] = fmaf(__uint_as_float(sv[e]), f, nm);
+      }
+      if (masked) {
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+          if (!((e < 32 ? (uint32_t)see : (uint32_t)(see >> 32)) >> (e & 31) & 1u))
+            x[e] = -INFINITY;
+      }
+      float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+      for (int e = 4; e + 7 < W; e += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmax3(mx[k], x[e + 2 * k], x[e + 2 * k + 1]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[W - 4 + k]);
+      float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+      if (named_or(1 + q4, 64, top > thr)) {
+        // ---- raise the rows' maxima to this tile's ----------------------------------
+        s_x[half * kRows + r] = top;
+        named_sync(1 + q4, 64);
+        top = fmaxf(top, s_x[(half ^ 1) * kRows + r]);
+        float corr = 1.f;
+        if (real && top != -INFINITY && (m == -INFINITY || top > 0.f)) {
+          if (m != -INFINITY) corr = ex2(-top);
+          m = (m == -INFINITY ? 0.f : m) + top;
+          nm = -m;
+          thr = kRaise;
+          l *= corr;
+#pragma unroll
+          for (int e = 0; e < W; ++e) x[e] -= top;
+        }
+        if (i > 0 && __any_sync(0xffffffffu, corr != 1.f)) {  // this half of O's dims
+          if (lane == 0) wait_bar(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, s_abort, p.flags);
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < DVC / 32; ++c) {
+            uint32_t ov[16];
+            const uint32_t oa = tmem + lane_base + T::OCOL + half * (DVC / 2) + 16 * c;
+            tmem_ld16(oa, ov);
+            tmem_wait_ld<16>(ov);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
+            tmem_st16(oa, ov);
+          }
+        }
+      }
+      // ---- p = 2^x, in front of this half's S columns ---------------------------------
+      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < W / 32; ++c) {
+        uint32_t h[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float a = ex2(x[32 * c + 2 * e]), b = ex2(x[32 * c + 2 * e + 1]);
+          l4[e & 3] += a + b;
+          h[e] = f32x2_to_f16x2(a, b);
+        }
+        tmem_st16(sa + 16 * c, h);
+      }
+      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[sb]);
+    }
+    // ---- the CTA's state: sums of the halves, then O ------------------------------------
+    if (active) {
+      if (lane == 0 && ntiles > 0)
+        wait_bar(&pv_done[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1, s_abort, p.flags);
+      __syncwarp();
+      // (only now: the other half may have been reading this word for the last raise)
+      s_x[half * kRows + r] = l;
+      named_sync(1 + q4, 64);
+      l += s_x[(half ^ 1) * kRows + r];
+      tc_fence_after();
+      const bool any = m != -INFINITY;
+      const uint32_t oa = tmem + lane_base + T::OCOL + half * (DVC / 2);
+      if (parts == 1) {
+        const bool partial = p.split && u.num_splits > 1;
+        const float scale = any ? p.v_scale / l : 0.f;
+        const float lse = any ? (m + log2f(l)) * kLn2 : -INFINITY;
+        const int head = u.h_kv * G + gr % G;
+        const int64_t row = (int64_t)(u.qo_begin + node) * p.num_qo_heads + head;
+        const int64_t pi = (int64_t)u.partial_base +
+                           ((int64_t)node * p.num_qo_heads + head) * u.num_splits + u.split;
+        if (real && half == 0 && vh == 0) {
+          if (partial)
+            p.partial_lse[pi] = lse;
+          else if (p.lse)
+            p.lse[row] = lse;
+        }
+        const int d0 = vh * DVC + half * (DVC / 2);
+#pragma unroll 1
+        for (int c = 0; c < DVC / 32; ++c) {
+          uint32_t ov[16];
+          tmem_ld16(oa + 16 * c, ov);
+          tmem_wait_ld<16>(ov);
+          float o[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = any ? __uint_as_float(ov[e]) * scale : 0.f;
+          if (real && partial) {
+            float4* at = reinterpret_cast<float4*>(p.partial_o + pi * DV + d0 + 16 * c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              at[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          } else if (real) {
+            uint32_t* at = reinterpret_cast<uint32_t*>(p.out + row * DV + d0 + 16 * c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) at[e] = pack_out2(o[2 * e], o[2 * e + 1], p.out_f16);
+          }
+          __syncwarp();
+        }
+      } else {
+        // (the operand tiles are free: every product is done)
+        float* so = reinterpret_cast<float*>(smem) + r * T::OROW + half * (DVC / 2);
+        if (half == 0) {
+          s_m[r] = m;
+          s_l[r] = l;
+        }
+#pragma unroll 1
+        for (int c = 0; c < DVC / 32; ++c) {
+          uint32_t ov[16];
+          tmem_ld16(oa + 16 * c, ov);
+          tmem_wait_ld<16>(ov);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<float4*>(so + 16 * c + 4 * e) =
+                any ? make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
+                                  __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]))
+                    : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+    }
+    tc_fence_before();
+  }
+
+  // ---- every role is done: release tensor memory ---------------------------------------
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, T::TCOLS);
+  }
+  const bool partial = p.split && u.num_splits > 1;
+  if (parts > 1) {
+    // ---- join the states of the cluster's CTAs, a share of the rows each ------------------
+    __syncwarp();
+    cluster_arrive_wait();
+    constexpr int DQ = DVC / 4;
+    const int share = kRows / parts, first = part * share, rows = min(share, nrows - first);
+    const uint32_t so = smem_addr(smem), sm = smem_addr(s_m), sl = smem_addr(s_l);
+    for (int idx = tid; idx < rows * DQ; idx += kThreads) {
+      const int rr = first + idx / DQ, d = 4 * (idx % DQ);
+      float mt[8], lt[8], M = -INFINITY;
+      float4 ot[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        if (t >= parts) break;
+        const uint32_t at = t * VH + vh;
+        mt[t] = peer_f32(peer(sm + 4 * rr, at));
+        lt[t] = peer_f32(peer(sl + 4 * rr, at));
+        ot[t] = peer_v4(peer(so + 4 * (rr * T::OROW + d), at));
+      }
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        if (t < parts) M = fmaxf(M, mt[t]);
+      float L = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (M != -INFINITY) {
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          if (t >= parts || mt[t] == -INFINITY) continue;
+          const float w = ex2(mt[t] - M);
+          L = fmaf(lt[t], w, L);
+          o.x = fmaf(ot[t].x, w, o.x);
+          o.y = fmaf(ot[t].y, w, o.y);
+          o.z = fmaf(ot[t].z, w, o.z);
+          o.w = fmaf(ot[t].w, w, o.w);
+        }
+        const float inv = p.v_scale / L;
+        o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+      }
+      const float lse = M == -INFINITY ? M : (M + log2f(L)) * kLn2;
+      const int gr = row0 + rr, node = gr / G, head = u.h_kv * G + gr % G;
+      const int64_t row = (int64_t)(u.qo_begin + node) * p.num_qo_heads + head;
+      if (partial) {
+        const int64_t pi = (int64_t)u.partial_base +
+                           ((int64_t)node * p.num_qo_heads + head) * u.num_splits + u.split;
+        *reinterpret_cast<float4*>(p.partial_o + pi * DV + vh * DVC + d) = o;
+        if (d == 0 && vh == 0) p.partial_lse[pi] = lse;
+      } else {
+        *reinterpret_cast<uint2*>(p.out + row * DV + vh * DVC + d) =
+            make_uint2(pack_out2(o.x, o.y, p.out_f16), pack_out2(o.z, o.w, p.out_f16));
+        if (d == 0 && vh == 0 && p.lse) p.lse[row] = lse;
+      }
+    }
+    __syncwarp();
+    cluster_arrive_wait();  // no CTA ends while another reads its state
+  }
+  if (!partial) return;
+  // ---- the last CTA of the request's units to arrive folds their states --------------------
+  __syncthreads();
+  if (tid == 0) {
+    int* ctr = p.counters + (int64_t)u.pair * p.row_blocks + block;
+    int old;
+    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(ctr) : "memory");
+    *s_last = old == u.num_splits * C - 1;
+    if (*s_last) *ctr = 0;  // every other CTA has arrived
+  }
+  __syncthreads();
+  if (!*s_last) return;
+  constexpr int DQ = DV / 4, MB = 8;
+  constexpr float kLog2e = 1.44269504088896340736f;
+  for (int idx = tid; idx < nrows * DQ; idx += kThreads) {
+    const int gr = row0 + idx / DQ, d = 4 * (idx % DQ), node = gr / G, head = u.h_kv * G + gr % G;
+    const int64_t base = (int64_t)u.partial_base +
+                         ((int64_t)node * p.num_qo_heads + head) * u.num_splits;
+    float M = -INFINITY, L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < u.num_splits; s0 += MB) {
+      float lw[MB];
+      float4 v[MB];
+      float mb = M;
+#pragma unroll
+      for (int k = 0; k < MB; ++k) {
+        lw[k] = -INFINITY;
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (s0 + k < u.num_splits) {
+          lw[k] = __ldcg(p.partial_lse + base + s0 + k) * kLog2e;
+          v[k] = __ldcg(reinterpret_cast<const float4*>(p.partial_o + (base + s0 + k) * DV + d));
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < MB; ++k) mb = fmaxf(mb, lw[k]);
+      if (mb == -INFINITY) continue;
+      const float cf = ex2(M - mb);  // 0 for -inf
+      L *= cf;
+      o.x *= cf; o.y *= cf; o.z *= cf; o.w *= cf;
+#pragma unroll
+      for (int k = 0; k < MB; ++k) {
+        const float w = ex2(lw[k] - mb);
+        L += w;
+        o.x = fmaf(w, v[k].x, o.x);
+        o.y = fmaf(w, v[k].y, o.y);
+        o.z = fmaf(w, v[k].z, o.z);
+        o.w = fmaf(w, v[k].w, o.w);
+      }
+      M = mb;
+    }
+    const float inv = M != -INFINITY ? 1.f / L : 0.f;
+    const int64_t row = (int64_t)(u.qo_begin + node) * p.num_qo_heads + head;
+    *reinterpret_cast<uint2*>(p.out + row * DV + d) =
+        make_uint2(pack_out2(o.x * inv, o.y * inv, p.out_f16),
+                   pack_out2(o.z * inv, o.w * inv, p.out_f16));
+    if (d == 0 && p.lse) p.lse[row] = M != -INFINITY ? (M + log2f(L)) * kLn2 : -INFINITY;
+  }
+}
+
+template <int DK, int DVC, int VH, int TT>
+bool make_tree(TreeConfig* cfg) {
+  using T = Tree<DK, DVC, VH, TT>;
+  cfg->func = reinterpret_cast<const void*>(attend_tree_kernel<DK, DVC, VH, TT>);
+  cfg->smem_bytes = T::SMEM;
+  cfg->value_parts = VH;
+  cfg->tile_tokens = TT;
+  return true;
+}
+
+}  // namespace
+
+bool attend_config_tree(int dk, int dv, TreeConfig* cfg) {
+  // tiles of 64 tokens from 256 dims on: two of K's operand tiles, and tensor memory for
+  // two S tiles beside Q and O
+  if (dk == 64 && dv == 64) return make_tree<64, 64, 1, 128>(cfg);
+  if (dk == 128 && dv == 128) return make_tree<128, 128, 1, 128>(cfg);
+  if (dk == 256 && dv == 128) return make_tree<256, 128, 1, 64>(cfg);
+  if (dk == 256 && dv == 256) return make_tree<256, 128, 2, 64>(cfg);
+  if (dk == 512 && dv == 256) return make_tree<512, 128, 2, 64>(cfg);
+  return false;
+}
+
+cudaError_t launch_attend_tree(const TreeConfig& cfg, AttendParams p, int units, int row_blocks,
+                               int ctas, cudaStream_t stream) {
+  p.tree_ctas = ctas;
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = dim3(units, row_blocks * ctas);
+  lc.blockDim = dim3(kThreads);
+  lc.dynamicSmemBytes = cfg.smem_bytes;
+  lc.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 1;
+  attr.val.clusterDim.y = ctas;
+  attr.val.clusterDim.z = 1;
+  lc.attrs = &attr;
+  lc.numAttrs = 1;
+  void* args[] = {&p};
+  return cudaLaunchKernelExC(&lc, cfg.func, args);
+}
+
+}  // namespace nvfp4kv

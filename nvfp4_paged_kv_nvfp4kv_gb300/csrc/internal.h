@@ -86,6 +86,8 @@ struct AttendParams {
   // it sees the j-th of its request's qo_len last tokens
   const uint32_t* tree_mask;
   int32_t tree_words;
+  int32_t tree_ctas;   // attend_tree: CTAs of a cluster, which share a unit's tokens
+  int32_t row_blocks;  // and the plan's row blocks (merge counters of a pair)
 };
 
 struct AppendParams {
@@ -271,6 +273,16 @@ struct AttendConfig {
 bool attend_config(int kind, int dk, int dv, int rows, AttendConfig* cfg);
 cudaError_t launch_attend(const AttendConfig& cfg, const AttendParams& p,
                           int grid_x, int grid_y, cudaStream_t stream);
+// The kernel of drafted trees for (dk, dv) and more than 16 query rows per kv head, in
+// blocks of 128: value_parts CTAs share the value dims.
+struct TreeConfig {
+  const void* func;
+  int smem_bytes, value_parts, tile_tokens;
+};
+constexpr int kTreeRows = 128;
+bool attend_config_tree(int dk, int dv, TreeConfig* cfg);
+cudaError_t launch_attend_tree(const TreeConfig& cfg, AttendParams p, int units, int row_blocks,
+                               int ctas, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_dequantize(const DequantParams& p, cudaStream_t stream);
 constexpr int kMaxPageTableBatch = 8192;

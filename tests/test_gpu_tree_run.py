@@ -150,17 +150,25 @@ def test_values_of_all_sizes(kernel):
     tree_case((70, 200), (9, 30), 4, 2, 128, 128, kernel=kernel, g=(2.0 ** -30, 2.0 ** 60), seed=9)
 
 
-@pytest.mark.parametrize("kernel", [1, 3])
-def test_a_chain_is_the_causal_mask(kernel):
-    """A tree without branches gives what the causal plan gives, bit for bit."""
-    kv, new = (37, 300, 64), (5, 33, 64)
+def test_a_chain_is_the_causal_mask():
+    """A tree without branches is the causal mask: up to 16 rows a kv head it runs in the
+    causal plan's kernel and gives the same bits."""
+    kv, new = (37, 300, 64), (4, 1, 3)
     chains = [T.mask_words(T.ancestors(range(-1, n - 1)), 2) for n in new]
-    c, plan, out, lse, q, _ = tree_case(kv, new, 8, 2, 128, 128, masks=chains, words=2,
-                                        kernel=kernel, seed=11)
+    c, plan, out, lse, q, _ = tree_case(kv, new, 8, 2, 128, 128, masks=chains, words=2, kernel=1,
+                                        seed=11)
     qo = np.concatenate([[0], np.cumsum(new)])
-    causal = N.nvfp4kv_decode_plan(qo, c.indptr, c.last, 8, 2, 128, 128, kernel=kernel, causal=True)
+    causal = N.nvfp4kv_decode_plan(qo, c.indptr, c.last, 8, 2, 128, 128, kernel=1, causal=True)
+    assert plan.info.rows_per_block == 16
     o2, l2 = N.nvfp4kv_decode_run(causal, q, c.cache, c.kv_indices)
     assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+def test_chains_of_many_rows(kernel):
+    kv, new = (37, 300, 64), (5, 33, 64)
+    chains = [T.mask_words(T.ancestors(range(-1, n - 1)), 2) for n in new]
+    tree_case(kv, new, 8, 2, 128, 128, masks=chains, words=2, kernel=kernel, seed=11)
 
 
 @pytest.mark.parametrize("kernel", [1, 3])
