@@ -52,8 +52,9 @@ constexpr float kRaise = 8.f;  // log2 of the largest p before m is raised
 #define NVFP4KV_TREE_TEST_SKIP_ARRIVE 0
 #endif
 
-// DVC: value dims of a CTA, DV = VH * DVC; TT: tokens of a tile
-template <int DK, int DVC, int VH, int TT>
+// DVC: value dims of a CTA, DV = VH * DVC; TT: tokens of a tile.  ONE: the two halves of a
+// tile's tokens share one O (and so one maximum), where tensor memory has no room for two.
+template <int DK, int DVC, int VH, int TT, bool ONE>
 struct Tree {
   static constexpr int DV = DVC * VH;
   static constexpr int KPT = 128 / TT;              // loader threads a token
@@ -68,11 +69,12 @@ struct Tree {
   static constexpr int OFF_V = OFF_K + KB * KBYTES;
   static constexpr int OFF_RAW = OFF_V + VB * VBYTES;
   static constexpr int OFF_MISC = OFF_RAW + RS * STAGE;
-  static constexpr int MISC = 256 + 4 * kRows * 4 + 64;
+  static constexpr int MISC = 256 + 6 * kRows * 4 + 64;
   static constexpr int SMEM = OFF_MISC + MISC + 1024;  // + alignment slack
   static constexpr int OROW = DVC + 4;                 // floats of a row in the joined states
-  // tensor memory columns: S (P) x 2, O, Q
-  static constexpr int SCOL = 0, OCOL = 2 * TT, QCOL = OCOL + DVC;
+  // tensor memory columns: S, P, O of each half, Q
+  static constexpr int SCOL = 0, PCOL = TT, OCOL = PCOL + TT / 2;
+  static constexpr int QCOL = OCOL + (ONE ? 1 : 2) * DVC;
   static constexpr int COLS = QCOL + DK / 2, TCOLS = 512;
   static constexpr uint32_t IDESC_S = idesc_f16(kRows, TT, 0, 0);
   static constexpr uint32_t IDESC_O = idesc_f16(kRows, DVC, 0, 1);
@@ -80,6 +82,36 @@ struct Tree {
   static_assert(OFF_RAW % 1024 == 0 && OFF_MISC % 16 == 0, "alignment");
   static_assert(kRows * OROW * 4 <= OFF_RAW, "the joined states take the operands' place");
 };
+
+// wait_bar for a barrier that mostly is ready, or soon will be: tested first, as the
+// suspending wait takes about 300 cycles even when it is
+template <int SPINS>
+__device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          uint32_t* flags) {
+#pragma unroll 1
+  for (int k = 0; k < SPINS; ++k)
+    if (mbar_test_wait(bar, parity)) return true;
+  return wait_bar(bar, parity, abort, flags);
+}
+// pairs of f32 (Blackwell's two-wide float32 arithmetic)
+__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 __device__ __forceinline__ void cluster_arrive_wait() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n"
@@ -174,10 +206,8 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
     cp_async_wait<RS - 1>();  // this thread's copies of tile i have landed
     const int b = i % NB;
     bool ok = true;
-    if (i >= NB) {
-      if (lane == 0) ok = wait_bar(&empty[b], (i / NB - 1) & 1, abort, p.flags);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-    }
+    if (i >= NB) ok = __all_sync(0xffffffffu, wait_soon<4>(&empty[b], (i / NB - 1) & 1, abort,
+                                                           p.flags));
     __syncwarp();  // and those of the warp
     if (!ok) break;
     const uint8_t* st = mine + (i % RS) * T::STAGE;
@@ -215,9 +245,9 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
   cp_async_wait<0>();
 }
 
-template <int DK, int DVC, int VH, int TT>
+template <int DK, int DVC, int VH, int TT, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendParams p) {
-  using T = Tree<DK, DVC, VH, TT>;
+  using T = Tree<DK, DVC, VH, TT, ONE>;
   constexpr int KB = T::KB, VB = T::VB, DV = T::DV;
   constexpr int W = TT / 2;      // tokens of a tile that a softmax thread has
   constexpr float kLn2 = 0.69314718055994530942f;
@@ -228,16 +258,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
   uint64_t* k_empty = bars + 3;   // [KB] S done
   uint64_t* v_full = bars + 6;    // [VB]
   uint64_t* v_empty = bars + 9;   // [VB] O done
-  uint64_t* s_full = bars + 12;   // [2] S done -> softmax
-  uint64_t* p_full = bars + 14;   // [2] softmax -> issue
-  uint64_t* pv_done = bars + 16;  // [2] O done -> softmax
+  uint64_t* s_full = bars + 12;   // S done -> softmax
+  uint64_t* s_empty = bars + 13;  // S read -> issue
+  uint64_t* p_full = bars + 14;   // softmax -> issue
+  uint64_t* pv_done = bars + 15;  // O done -> softmax
   uint64_t* q_full = bars + 18;
   uint64_t* fin = bars + 19;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 20);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_last = reinterpret_cast<int*>(s_tmem + 2);
   float* s_x = reinterpret_cast<float*>(smem + T::OFF_MISC + 256);  // [2][128] the halves' values
-  float* s_m = s_x + 2 * kRows;   // [128] maxima, then
+  float* s_ml = s_x + 2 * kRows;  // [2][128] the halves' maxima
+  float* s_m = s_ml + 2 * kRows;  // [128] maxima, then
   float* s_l = s_m + kRows;       // [128] sums of the CTA's state
 
   const WorkUnit u = load_unit(p);
@@ -263,11 +295,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
       mbar_init(&v_full[b], kLoadWarps);
       mbar_init(&v_empty[b], 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&s_full[b], 1);
-      mbar_init(&p_full[b], kSoftmaxWarps);
-      mbar_init(&pv_done[b], 1);
-    }
+    mbar_init(s_full, 1);
+    mbar_init(s_empty, kSoftmaxWarps);
+    mbar_init(p_full, kSoftmaxWarps);
+    mbar_init(pv_done, 1);
     mbar_init(q_full, kSoftmaxWarps);
     mbar_init(fin, 1);
     mbar_init_fence();
@@ -301,57 +332,42 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
     if (lane == 0) {
       const uint64_t kd0 = smem_desc(smem_addr(smem + T::OFF_K), 16, 1024, kSwz128);
       const uint64_t vd0 = smem_desc(smem_addr(smem + T::OFF_V), TT * 128, 1024, kSwz128);
-      auto issue_s = [&](int i) {
-        tc_fence_after();
-        const uint64_t kd = kd0 + (((i % KB) * T::KBYTES) >> 4);
-        const uint32_t d = tmem + T::SCOL + TT * (i & 1);
-#pragma unroll 8
-        for (int kk = 0; kk < DK / 16; ++kk)
-          umma_ts(d, tmem + T::QCOL + 8 * kk, kd + (((kk >> 2) * (TT * 128) + (kk & 3) * 32) >> 4),
-                  T::IDESC_S, kk > 0 ? 1u : 0u);
-        umma_commit(&s_full[i & 1]);
-        umma_commit(&k_empty[i % KB]);
-      };
-      auto issue_o = [&](int i) {
-        tc_fence_after();
-        const uint64_t vd = vd0 + (((i % VB) * T::VBYTES) >> 4);
-        const uint32_t a = tmem + T::SCOL + TT * (i & 1);
-#pragma unroll
-        for (int k = 0; k < TT / 16; ++k)  // P: each half's tokens in front of its S columns
-          umma_ts(tmem + T::OCOL, a + W * (k / (W / 16)) + 8 * (k % (W / 16)),
-                  vd + ((k * 2048) >> 4), T::IDESC_O, (i > 0 || k > 0) ? 1u : 0u);
-        umma_commit(&pv_done[i & 1]);
-        umma_commit(&v_empty[i % VB]);
-      };
-      // whichever product has its inputs: S(s) once its K is in and the tile's columns
-      // are free (O(s - 2), which reads them as P, is issued), O(o) once P(o) and V are
+      // S(i + 1) once the softmax has read S(i) and its K is in, then O(i) once P(i) and its
+      // V are
       bool ok = ntiles == 0 || wait_bar(q_full, 0, s_abort, p.flags);
-      int s = 0, o = 0;
-      uint32_t idle = 0;
-      while (ok && o < ntiles) {
-        bool prog = false;
-        if (s < ntiles && s < o + 2 && mbar_test_wait(&k_full[s % KB], (s / KB) & 1)) {
-          issue_s(s);
-          ++s;
-          prog = true;
+      for (int i = -1; ok && i < ntiles; ++i) {
+        if (i + 1 < ntiles) {
+          const int n = i + 1, b = n % KB;
+          ok = wait_soon<64>(&k_full[b], (n / KB) & 1, s_abort, p.flags) &&
+               (n == 0 || wait_soon<64>(s_empty, i & 1, s_abort, p.flags));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t kd = kd0 + ((b * T::KBYTES) >> 4);
+#pragma unroll 8
+          for (int kk = 0; kk < DK / 16; ++kk)
+            umma_ts(tmem + T::SCOL, tmem + T::QCOL + 8 * kk,
+                    kd + (((kk >> 2) * (TT * 128) + (kk & 3) * 32) >> 4), T::IDESC_S,
+                    kk > 0 ? 1u : 0u);
+          umma_commit(s_full);
+          umma_commit(&k_empty[b]);
         }
-        if (o < s && mbar_test_wait(&p_full[o & 1], (o >> 1) & 1) &&
-            mbar_test_wait(&v_full[o % VB], (o / VB) & 1)) {
-          issue_o(o);
-          ++o;
-          prog = true;
+        if (i >= 0) {
+          const int b = i % VB;
+          ok = wait_soon<64>(&v_full[b], (i / VB) & 1, s_abort, p.flags) &&
+               wait_soon<64>(p_full, i & 1, s_abort, p.flags);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t vd = vd0 + ((b * T::VBYTES) >> 4);
+#pragma unroll
+          for (int k = 0; k < TT / 16; ++k) {
+            const int h = ONE ? 0 : k / (W / 16);  // the half whose tokens these are
+            const bool first = ONE ? k == 0 : k % (W / 16) == 0;
+            umma_ts(tmem + T::OCOL + h * DVC, tmem + T::PCOL + 8 * k, vd + ((k * 2048) >> 4),
+                    T::IDESC_O, (i > 0 || !first) ? 1u : 0u);
+          }
+          umma_commit(pv_done);
+          umma_commit(&v_empty[b]);
         }
-        if (prog) {
-          idle = 0;
-          continue;
-        }
-        if (*s_abort) break;
-        if (++idle > kIdlePolls) {
-          *s_abort = 1;
-          atomicOr(p.flags, 0x4u);
-          break;
-        }
-        __nanosleep(32);
       }
       umma_commit(fin);  // wind-down: every product issued has completed
       drain_bar(fin, 0, p.flags);
@@ -432,72 +448,84 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
       if (n < 64) v = n <= 0 ? 0ull : v & ((1ull << n) - 1);
       return real ? v : 0ull;
     };
-    float m = -INFINITY, nm = 0.f, l = 0.f;  // the row's maximum (log2), -m once it has one
+    // the maximum (log2; ONE: of the row, else of this half's tokens), -m once there is one
+    float m = -INFINITY, nm = 0.f;
     float thr = real ? -INFINITY : INFINITY;
+    uint64_t lsum[2] = {0, 0};  // sums of p (ONE: over this half's tokens)
     const int some_hidden = min(before, tok_end);  // tiles that reach past it are masked
+    auto wait = [&](uint64_t* bar, uint32_t parity) {  // (every lane: no hand-over)
+      wait_soon<16>(bar, parity, s_abort, p.flags);
+      __syncwarp();
+    };
     for (int i = 0; i < ntiles; ++i) {
-      const int sb = i & 1;
       if (!active) {
-        // (nothing to do for the rows that are not there but to keep the count)
-        if (lane == 0) {
-          wait_bar(&s_full[sb], (i >> 1) & 1, s_abort, p.flags);
-          mbar_arrive(&p_full[sb]);
-        }
+        // (nothing to do for the rows that are not there but to keep the counts)
+        wait(s_full, i & 1);
+        if (lane == 0) mbar_arrive(s_empty);
+        if (i > 0) wait(pv_done, (i - 1) & 1);  // (an arrival counts for the phase that is open)
+        if (lane == 0) mbar_arrive(p_full);
         continue;
       }
       const int tok = u.tok_begin + (t0 + i) * TT + half * W;
       const bool masked = u.tok_begin + (t0 + i + 1) * TT > some_hidden;
       uint64_t see = ~0ull;
       if (masked) see = visible(tok);
-      if (lane == 0) wait_bar(&s_full[sb], (i >> 1) & 1, s_abort, p.flags);
-      __syncwarp();
+      wait(s_full, i & 1);
       tc_fence_after();
-      float x[W];
-      const uint32_t sa = tmem + lane_base + T::SCOL + TT * sb + W * half;
-      {
-        uint32_t sv[W];
-        tmem_ld<W>(sa, sv);
-        tmem_wait_ld<W>(sv);
-#pragma unroll
-        for (int e = 0; e < W; ++e) x[e] = fmaf(__uint_as_float(sv[e]), f, nm);
-      }
+      uint32_t x[W];
+      tmem_ld<W>(tmem + lane_base + T::SCOL + W * half, x);
+      tmem_wait_ld<W>(x);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(s_empty);
       if (masked) {
 #pragma unroll
         for (int e = 0; e < W; ++e)
           if (!((e < 32 ? (uint32_t)see : (uint32_t)(see >> 32)) >> (e & 31) & 1u))
-            x[e] = -INFINITY;
+            x[e] = 0xff800000u;  // -inf
       }
-      float mx[4] = {x[0], x[1], x[2], x[3]};
+      // the largest score (f > 0, so that of the sums); f = 0 for rows that are not there
+      float mx[4] = {__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]),
+                     __uint_as_float(x[3])};
 #pragma unroll
       for (int e = 4; e + 7 < W; e += 8)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) mx[k] = fmax3(mx[k], x[e + 2 * k], x[e + 2 * k + 1]);
+        for (int k = 0; k < 4; ++k)
+          mx[k] = fmax3(mx[k], __uint_as_float(x[e + 2 * k]), __uint_as_float(x[e + 2 * k + 1]));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], x[W - 4 + k]);
-      float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
-      if (named_or(1 + q4, 64, top > thr)) {
-        // ---- raise the rows' maxima to this tile's ----------------------------------
-        s_x[half * kRows + r] = top;
-        named_sync(1 + q4, 64);
-        top = fmaxf(top, s_x[(half ^ 1) * kRows + r]);
+      for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(x[W - 4 + k]));
+      float top = fmaf(fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]), f, nm);
+      bool raise = top > thr;
+      if constexpr (ONE)
+        raise = named_or(1 + q4, 64, raise);
+      else
+        raise = __any_sync(0xffffffffu, raise);
+      if (raise) {
+        // ---- raise the maxima to this tile's -----------------------------------------
+        if constexpr (ONE) {
+          s_x[half * kRows + r] = top;
+          named_sync(1 + q4, 64);
+          top = fmaxf(top, s_x[(half ^ 1) * kRows + r]);
+        }
         float corr = 1.f;
         if (real && top != -INFINITY && (m == -INFINITY || top > 0.f)) {
           if (m != -INFINITY) corr = ex2(-top);
           m = (m == -INFINITY ? 0.f : m) + top;
           nm = -m;
           thr = kRaise;
-          l *= corr;
-#pragma unroll
-          for (int e = 0; e < W; ++e) x[e] -= top;
         }
-        if (i > 0 && __any_sync(0xffffffffu, corr != 1.f)) {  // this half of O's dims
-          if (lane == 0) wait_bar(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, s_abort, p.flags);
-          __syncwarp();
+        if (i > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
+          float a, b;
+          unpack_f32x2(add_f32x2(lsum[0], lsum[1]), a, b);
+          lsum[0] = pack_f32x2((a + b) * corr, 0.f);
+          lsum[1] = 0;
+          wait(pv_done, (i - 1) & 1);
           tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < DVC / 32; ++c) {
+          constexpr int OD = ONE ? DVC / 2 : DVC;  // the dims that are this thread's to scale
+#pragma unroll 1
+          for (int c = 0; c < OD / 16; ++c) {
             uint32_t ov[16];
-            const uint32_t oa = tmem + lane_base + T::OCOL + half * (DVC / 2) + 16 * c;
+            const uint32_t oa = tmem + lane_base + T::OCOL + half * OD + 16 * c;
             tmem_ld16(oa, ov);
             tmem_wait_ld<16>(ov);
 #pragma unroll
@@ -506,37 +534,80 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
           }
         }
       }
-      // ---- p = 2^x, in front of this half's S columns ---------------------------------
-      float l4[4] = {0.f, 0.f, 0.f, 0.f};
+      // ---- p = 2^(score - m) ------------------------------------------------------------
+      uint32_t h[W / 2];
+      {
+        const uint64_t f2 = pack_f32x2(f, f), n2 = pack_f32x2(nm, nm);
 #pragma unroll
-      for (int c = 0; c < W / 32; ++c) {
-        uint32_t h[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float a = ex2(x[32 * c + 2 * e]), b = ex2(x[32 * c + 2 * e + 1]);
-          l4[e & 3] += a + b;
+        for (int e = 0; e < W / 2; ++e) {
+          float a, b;
+          unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[2 * e]),
+                                            __uint_as_float(x[2 * e + 1])), f2, n2), a, b);
+          a = ex2(a);
+          b = ex2(b);
+          lsum[e & 1] = add_f32x2(lsum[e & 1], pack_f32x2(a, b));
           h[e] = f32x2_to_f16x2(a, b);
         }
-        tmem_st16(sa + 16 * c, h);
       }
-      l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+      if (i > 0) wait(pv_done, (i - 1) & 1);  // P's columns are free
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < W / 32; ++c)
+        tmem_st16(tmem + lane_base + T::PCOL + (W / 2) * half + 16 * c, h + 16 * c);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[sb]);
+      if (lane == 0) mbar_arrive(p_full);
     }
     // ---- the CTA's state: sums of the halves, then O ------------------------------------
     if (active) {
-      if (lane == 0 && ntiles > 0)
-        wait_bar(&pv_done[(ntiles - 1) & 1], ((ntiles - 1) >> 1) & 1, s_abort, p.flags);
-      __syncwarp();
-      // (only now: the other half may have been reading this word for the last raise)
+      if (ntiles > 0) wait(pv_done, (ntiles - 1) & 1);
+      float l;
+      {
+        float a, b;
+        unpack_f32x2(add_f32x2(lsum[0], lsum[1]), a, b);
+        l = a + b;
+      }
+      // (only now: the other half may have been reading the words for its last raise)
       s_x[half * kRows + r] = l;
+      if constexpr (!ONE) s_ml[half * kRows + r] = m;
       named_sync(1 + q4, 64);
-      l += s_x[(half ^ 1) * kRows + r];
+      const float l1 = s_x[(half ^ 1) * kRows + r];
+      float w[2] = {1.f, 1.f};  // the factors of the halves' O
+      if constexpr (ONE) {
+        l += l1;
+      } else {
+        const float m1 = s_ml[(half ^ 1) * kRows + r], top = fmaxf(m, m1);
+        const float mine = m == -INFINITY ? 0.f : ex2(m - top);
+        const float other = m1 == -INFINITY ? 0.f : ex2(m1 - top);
+        // (the same sum in both threads: each row's first half first)
+        l = half ? fmaf(l1, other, l * mine) : fmaf(l, mine, l1 * other);
+        w[0] = half ? other : mine;
+        w[1] = half ? mine : other;
+        m = top;
+      }
       tc_fence_after();
       const bool any = m != -INFINITY;
       const uint32_t oa = tmem + lane_base + T::OCOL + half * (DVC / 2);
+      // 16 dims of the row, the halves' states joined
+      auto state16 = [&](int c, float (&o)[16]) {
+        uint32_t ov[16];
+        tmem_ld16(oa + 16 * c, ov);
+        if constexpr (ONE) {
+          tmem_wait_ld<16>(ov);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = any ? __uint_as_float(ov[e]) : 0.f;
+        } else {
+          uint32_t ow[16];
+          tmem_ld16(oa + DVC + 16 * c, ow);
+          tmem_wait_ld<16>(ov);
+          tmem_wait_ld<16>(ow);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            o[e] = (w[0] != 0.f ? __uint_as_float(ov[e]) * w[0] : 0.f) +
+                   (w[1] != 0.f ? __uint_as_float(ow[e]) * w[1] : 0.f);
+        }
+      };
       if (parts == 1) {
         const bool partial = p.split && u.num_splits > 1;
         const float scale = any ? p.v_scale / l : 0.f;
@@ -554,12 +625,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
         const int d0 = vh * DVC + half * (DVC / 2);
 #pragma unroll 1
         for (int c = 0; c < DVC / 32; ++c) {
-          uint32_t ov[16];
-          tmem_ld16(oa + 16 * c, ov);
-          tmem_wait_ld<16>(ov);
           float o[16];
+          state16(c, o);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = any ? __uint_as_float(ov[e]) * scale : 0.f;
+          for (int e = 0; e < 16; ++e) o[e] *= scale;
           if (real && partial) {
             float4* at = reinterpret_cast<float4*>(p.partial_o + pi * DV + d0 + 16 * c);
 #pragma unroll
@@ -581,15 +650,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
         }
 #pragma unroll 1
         for (int c = 0; c < DVC / 32; ++c) {
-          uint32_t ov[16];
-          tmem_ld16(oa + 16 * c, ov);
-          tmem_wait_ld<16>(ov);
+          float o[16];
+          state16(c, o);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             *reinterpret_cast<float4*>(so + 16 * c + 4 * e) =
-                any ? make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]),
-                                  __uint_as_float(ov[4 * e + 2]), __uint_as_float(ov[4 * e + 3]))
-                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       }
     }
@@ -717,10 +783,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
   }
 }
 
-template <int DK, int DVC, int VH, int TT>
+template <int DK, int DVC, int VH, int TT, bool ONE = false>
 bool make_tree(TreeConfig* cfg) {
-  using T = Tree<DK, DVC, VH, TT>;
-  cfg->func = reinterpret_cast<const void*>(attend_tree_kernel<DK, DVC, VH, TT>);
+  using T = Tree<DK, DVC, VH, TT, ONE>;
+  cfg->func = reinterpret_cast<const void*>(attend_tree_kernel<DK, DVC, VH, TT, ONE>);
   cfg->smem_bytes = T::SMEM;
   cfg->value_parts = VH;
   cfg->tile_tokens = TT;
@@ -736,7 +802,7 @@ bool attend_config_tree(int dk, int dv, TreeConfig* cfg) {
   if (dk == 128 && dv == 128) return make_tree<128, 128, 1, 128>(cfg);
   if (dk == 256 && dv == 128) return make_tree<256, 128, 1, 64>(cfg);
   if (dk == 256 && dv == 256) return make_tree<256, 128, 2, 64>(cfg);
-  if (dk == 512 && dv == 256) return make_tree<512, 128, 2, 64>(cfg);
+  if (dk == 512 && dv == 256) return make_tree<512, 128, 2, 64, true>(cfg);
   return false;
 }
 
