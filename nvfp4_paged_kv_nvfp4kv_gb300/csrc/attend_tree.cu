@@ -12,8 +12,8 @@
 //  * K loaders (4 warps) and V loaders (4 warps): cp.async of the packed rows and scales
 //    (a warp its own tokens, RS - 1 tiles ahead), then e2m1 -> f16 times the E4M3 block
 //    scale (exact) into the 128-byte-swizzled operand layouts in shared memory;
-//  * issue (one thread): S = Q K^T (A = Q in tensor memory, N = TT tokens) into one of two
-//    tiles of tensor memory, and O += P V (A = P, which takes the place of its S);
+//  * issue (two warps, one thread each): S = Q K^T (A = Q in tensor memory, N = TT tokens),
+//    and O += P V (A = P in tensor memory), each once its inputs are ready;
 //  * softmax (8 warps): thread = row and half of the tile's tokens, so the maximum and the
 //    sum need no shuffles; the two halves of a row meet in a barrier of their two warps
 //    once a tile.  m is raised only when a score exceeds it by 2^8 (then O is rescaled).
@@ -44,7 +44,7 @@ using namespace tc5;
 
 constexpr int kRows = 128;
 constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;  // of K, and of V
-constexpr int kThreads = 32 * (kSoftmaxWarps + 2 * kLoadWarps + 1);
+constexpr int kThreads = 32 * (kSoftmaxWarps + 2 * kLoadWarps + 2);
 constexpr float kRaise = 8.f;  // log2 of the largest p before m is raised
 // Test build only: the first K loader of CTA (0, 0) withholds its arrival for the first
 // tile, so the issuer's wait runs out and the CTA winds down.
@@ -137,6 +137,21 @@ __device__ __forceinline__ float4 peer_v4(uint32_t a) {
   return v;
 }
 
+__device__ __forceinline__ void sts_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z,
+                                       uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z),
+               "r"(w)
+               : "memory");
+}
+// a token's scales: 4, 8 or 16 bytes
+template <int N>
+__device__ __forceinline__ void cp_async_sf(uint32_t s, const void* g) {
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(s), "l"(g));
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(s), "l"(g), "n"(N));
+}
+
 // 16-byte chunk c of row r in a warp's stage (rows of SEG bytes): the lanes of a quarter
 // warp, a row each, then read distinct banks
 template <int SEG>
@@ -164,7 +179,7 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
   const int part = V ? vh * T::KPT + seg : seg;   // the warp's part of the whole row
   const uint8_t* data = (V ? c.v_data + u.h_kv * c.v_sh : c.k_data + u.h_kv * c.k_sh) + part * SEG;
   const uint8_t* sf = (V ? c.v_sf + u.h_kv * c.vsf_sh : c.k_sf + u.h_kv * c.ksf_sh) + part * SF;
-  uint8_t* mine = raw + w * (V ? T::VW : T::KW);
+  const uint32_t mine = smem_addr(raw) + w * (V ? T::VW : T::KW);
   const int r0 = lane / LPR, ch = lane % LPR;
   // page id of this lane's token in tile i, a tile ahead of its use (where it is checked);
   // a token past the unit's pages takes the last one
@@ -173,21 +188,27 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
     const int rel = (t0 + i) * TT + first + lane;
     return __ldg(p.kv_indices + u.page_begin + min(rel >> shift, u.num_pages - 1));
   };
+  // (rows r0, r0 + RPI, ... of the warp's 32 tokens, which begin at a multiple of 16)
+  const uint8_t* from = data + (r0 & slots) * ss + 16 * ch;
+  const uint8_t* sf_from = sf + (lane & slots) * fss;
   auto issue = [&](int i, int32_t pid) {
     if (pid < 0 || pid >= c.num_pages) {
       atomicOr(p.flags, 0x1u);
       pid = 0;
     }
-    uint8_t* st = mine + (i % RS) * T::STAGE;
-    const int rel = (t0 + i) * TT + first;  // of the warp's row 0 (a multiple of 16)
+    const uint32_t st = mine + (i % RS) * T::STAGE;
+    const uint8_t* page = from;
 #pragma unroll
     for (int k = 0; k < LPR; ++k) {
       const int r = r0 + k * RPI;
-      const int64_t pg = __shfl_sync(0xffffffffu, pid, r);
-      cp_async_16(st + r * SEG + 16 * raw_chunk<SEG>(r, ch),
-                  data + pg * sp + ((rel + r) & slots) * ss + 16 * ch);
+      // 16-token pages: the copies of a page differ by whole steps of RPI slots
+      constexpr int PER = RPI < 16 ? 16 / RPI : 1;
+      if (shift == 0 || RPI > 16 || k % PER == 0)
+        page = from + __shfl_sync(0xffffffffu, pid, r) * sp;
+      cp_async_16s(st + r * SEG + 16 * raw_chunk<SEG>(r, ch),
+                   shift == 0 ? page : page + (k % PER) * (RPI * ss));
     }
-    cp_async_small<SF>(st + 32 * SEG + lane * SF, sf + pid * fsp + ((rel + lane) & slots) * fss);
+    cp_async_sf<SF>(st + 32 * SEG + lane * SF, sf_from + pid * fsp);
   };
 #pragma unroll
   for (int i = 0; i < RS - 1; ++i) {
@@ -197,31 +218,33 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
   }
   int32_t next = load_pid(RS - 1);
   const int tl = first + lane;  // this lane's token of a tile
-  uint8_t* row = tiles + (tl >> 3) * 1024 + (tl & 7) * 128;
-  for (int i = 0; i < ntiles; ++i) {
+  // its row, whose 16-byte chunks are xor-ed with the row's number
+  const uint32_t row = smem_addr(tiles) + (tl >> 3) * 1024 + (tl & 7) * 128 + ((tl & 7) << 4);
+  for (int i = 0, b = 0, round = 0; i < ntiles; ++i) {
     const int32_t pid = next;
     next = load_pid(i + RS);
     if (i + RS - 1 < ntiles) issue(i + RS - 1, pid);
     cp_async_commit();
     cp_async_wait<RS - 1>();  // this thread's copies of tile i have landed
-    const int b = i % NB;
     bool ok = true;
-    if (i >= NB) ok = __all_sync(0xffffffffu, wait_soon<4>(&empty[b], (i / NB - 1) & 1, abort,
-                                                           p.flags));
+    if (round > 0)
+      ok = __all_sync(0xffffffffu, wait_soon<4>(&empty[b], (round - 1) & 1, abort, p.flags));
     __syncwarp();  // and those of the warp
     if (!ok) break;
-    const uint8_t* st = mine + (i % RS) * T::STAGE;
+    const uint32_t st = mine + (i % RS) * T::STAGE;
     // slots past the request's end may hold a NaN scale: their values count as 0 (their
     // scores are replaced)
     const bool past = V && u.tok_begin + (t0 + i) * TT + tl >= tok_end;
-    uint32_t scales[(SF + 3) / 4];
+    uint32_t scales[SF / 4];
 #pragma unroll
-    for (int k = 0; k < SF / 4; ++k)
-      scales[k] = past ? 0u : *reinterpret_cast<const uint32_t*>(st + 32 * SEG + lane * SF + 4 * k);
-    uint8_t* out = row + b * BYTES;
+    for (int k = 0; k < SF / 4; ++k) {
+      scales[k] = lds_u32(st + 32 * SEG + lane * SF + 4 * k);
+      if (past) scales[k] = 0;
+    }
+    const uint32_t out = row + b * BYTES;
 #pragma unroll
     for (int k = 0; k < LPR; ++k) {
-      const uint4 q = *reinterpret_cast<const uint4*>(st + lane * SEG + 16 * raw_chunk<SEG>(lane, k));
+      const uint4 q = lds_v4(st + lane * SEG + 16 * raw_chunk<SEG>(lane, k));
       const uint32_t s2 = e4m3x2_to_f16x2(scales[k / 2] >> (16 * (k & 1)));
       const uint32_t lo = bcast_lo(s2), hi = bcast_hi(s2);
       const uint32_t words[4] = {q.x, q.y, q.z, q.w};
@@ -230,10 +253,10 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
         uint32_t h[4];
         e2m1x8_to_f16x8(words[e], h);
         const uint32_t s = e < 2 ? lo : hi;
-        const int d = 2 * SEG * seg + 32 * k + 8 * e;  // first of the 8 dims
-        *reinterpret_cast<uint4*>(out + (d >> 6) * (TT * 128) +
-                                  ((((d & 63) >> 3) ^ (tl & 7)) << 4)) =
-            make_uint4(hmul2(h[0], s), hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
+        const int d = 32 * k + 8 * e;  // first of the 8 dims, from the thread's first
+        static_assert(2 * SEG % 64 == 0, "a thread's dims fill blocks of 64");
+        sts_v4((out + (2 * SEG / 64 * seg + d / 64) * (TT * 128)) ^ (d % 64 / 8 << 4), hmul2(h[0], s),
+               hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
       }
     }
     fence_async_smem();
@@ -241,6 +264,10 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
     const bool withhold = NVFP4KV_TREE_TEST_SKIP_ARRIVE && !V && blockIdx.x == 0 &&
                           blockIdx.y == 0 && w == 0 && i == 0;
     if (lane == 0 && !withhold) mbar_arrive(&full[b]);
+    if (++b == NB) {
+      b = 0;
+      ++round;
+    }
   }
   cp_async_wait<0>();
 }
@@ -263,8 +290,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
   uint64_t* p_full = bars + 14;   // softmax -> issue
   uint64_t* pv_done = bars + 15;  // O done -> softmax
   uint64_t* q_full = bars + 18;
-  uint64_t* fin = bars + 19;
-  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 20);
+  uint64_t* fin = bars + 19;      // [2] wind-down of the two issuers' products
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 22);
   volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
   int* s_last = reinterpret_cast<int*>(s_tmem + 2);
   float* s_x = reinterpret_cast<float*>(smem + T::OFF_MISC + 256);  // [2][128] the halves' values
@@ -300,7 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
     mbar_init(p_full, kSoftmaxWarps);
     mbar_init(pv_done, 1);
     mbar_init(q_full, kSoftmaxWarps);
-    mbar_init(fin, 1);
+    mbar_init(&fin[0], 1);
+    mbar_init(&fin[1], 1);
     mbar_init_fence();
     *s_abort = 0;
   }
@@ -328,49 +356,58 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
                             smem + T::OFF_RAW + kLoadWarps * T::KW, smem + T::OFF_V, v_full,
                             v_empty, s_abort);
   } else if (warp == kSoftmaxWarps + 2 * kLoadWarps) {
-    // ================= product issue (one thread) =============================
+    // ================= issue of S = Q K^T (one thread) =========================
     if (lane == 0) {
       const uint64_t kd0 = smem_desc(smem_addr(smem + T::OFF_K), 16, 1024, kSwz128);
-      const uint64_t vd0 = smem_desc(smem_addr(smem + T::OFF_V), TT * 128, 1024, kSwz128);
-      // S(i + 1) once the softmax has read S(i) and its K is in, then O(i) once P(i) and its
-      // V are
       bool ok = ntiles == 0 || wait_bar(q_full, 0, s_abort, p.flags);
-      for (int i = -1; ok && i < ntiles; ++i) {
-        if (i + 1 < ntiles) {
-          const int n = i + 1, b = n % KB;
-          ok = wait_soon<64>(&k_full[b], (n / KB) & 1, s_abort, p.flags) &&
-               (n == 0 || wait_soon<64>(s_empty, i & 1, s_abort, p.flags));
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t kd = kd0 + ((b * T::KBYTES) >> 4);
+      for (int i = 0, b = 0, round = 0; ok && i < ntiles; ++i) {
+        ok = wait_soon<64>(&k_full[b], round & 1, s_abort, p.flags) &&
+             (i == 0 || wait_soon<64>(s_empty, (i - 1) & 1, s_abort, p.flags));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t kd = kd0 + ((b * T::KBYTES) >> 4);
 #pragma unroll 8
-          for (int kk = 0; kk < DK / 16; ++kk)
-            umma_ts(tmem + T::SCOL, tmem + T::QCOL + 8 * kk,
-                    kd + (((kk >> 2) * (TT * 128) + (kk & 3) * 32) >> 4), T::IDESC_S,
-                    kk > 0 ? 1u : 0u);
-          umma_commit(s_full);
-          umma_commit(&k_empty[b]);
-        }
-        if (i >= 0) {
-          const int b = i % VB;
-          ok = wait_soon<64>(&v_full[b], (i / VB) & 1, s_abort, p.flags) &&
-               wait_soon<64>(p_full, i & 1, s_abort, p.flags);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t vd = vd0 + ((b * T::VBYTES) >> 4);
-#pragma unroll
-          for (int k = 0; k < TT / 16; ++k) {
-            const int h = ONE ? 0 : k / (W / 16);  // the half whose tokens these are
-            const bool first = ONE ? k == 0 : k % (W / 16) == 0;
-            umma_ts(tmem + T::OCOL + h * DVC, tmem + T::PCOL + 8 * k, vd + ((k * 2048) >> 4),
-                    T::IDESC_O, (i > 0 || !first) ? 1u : 0u);
-          }
-          umma_commit(pv_done);
-          umma_commit(&v_empty[b]);
+        for (int kk = 0; kk < DK / 16; ++kk)
+          umma_ts(tmem + T::SCOL, tmem + T::QCOL + 8 * kk,
+                  kd + (((kk >> 2) * (TT * 128) + (kk & 3) * 32) >> 4), T::IDESC_S,
+                  kk > 0 ? 1u : 0u);
+        umma_commit(s_full);
+        umma_commit(&k_empty[b]);
+        if (++b == KB) {
+          b = 0;
+          ++round;
         }
       }
-      umma_commit(fin);  // wind-down: every product issued has completed
-      drain_bar(fin, 0, p.flags);
+      umma_commit(&fin[0]);  // wind-down: every product issued has completed
+      drain_bar(&fin[0], 0, p.flags);
+    }
+    __syncwarp();
+  } else if (warp == kSoftmaxWarps + 2 * kLoadWarps + 1) {
+    // ================= issue of O += P V (one thread) ===========================
+    if (lane == 0) {
+      const uint64_t vd0 = smem_desc(smem_addr(smem + T::OFF_V), TT * 128, 1024, kSwz128);
+      for (int i = 0, b = 0, round = 0; i < ntiles; ++i) {
+        if (!wait_soon<64>(&v_full[b], round & 1, s_abort, p.flags) ||
+            !wait_soon<64>(p_full, i & 1, s_abort, p.flags))
+          break;
+        tc_fence_after();
+        const uint64_t vd = vd0 + ((b * T::VBYTES) >> 4);
+#pragma unroll
+        for (int k = 0; k < TT / 16; ++k) {
+          const int h = ONE ? 0 : k / (W / 16);  // the half whose tokens these are
+          const bool first = ONE ? k == 0 : k % (W / 16) == 0;
+          umma_ts(tmem + T::OCOL + h * DVC, tmem + T::PCOL + 8 * k, vd + ((k * 2048) >> 4),
+                  T::IDESC_O, (i > 0 || !first) ? 1u : 0u);
+        }
+        umma_commit(pv_done);
+        umma_commit(&v_empty[b]);
+        if (++b == VB) {
+          b = 0;
+          ++round;
+        }
+      }
+      umma_commit(&fin[1]);
+      drain_bar(&fin[1], 0, p.flags);
     }
     __syncwarp();
   } else {
