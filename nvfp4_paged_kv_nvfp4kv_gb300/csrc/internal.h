@@ -252,6 +252,7 @@ struct ReleaseParams {
   const int32_t* free_head;
   int32_t* free_head_out;
   int32_t num_rows, page_size, table_width, num_pages, num_free;
+  int32_t marks;  // words of shared memory for marks (launch_release sets it)
   uint32_t* flags;
 };
 
@@ -293,7 +294,7 @@ cudaError_t launch_e4m3_append(const E4m3AppendParams& p, cudaStream_t stream);
 cudaError_t launch_tree_masks(const TreeMaskParams& p, cudaStream_t stream);
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
 cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream);
-cudaError_t launch_release(const ReleaseParams& p, cudaStream_t stream);
+cudaError_t launch_release(ReleaseParams p, cudaStream_t stream);
 cudaError_t launch_page_copies(const PageCopyParams& p, cudaStream_t stream);
 // The E4M3-cache attention kernel for (dk, dv), a page size of 16 or 1 and up to
 // `rows` query rows per kv head; false when not built.

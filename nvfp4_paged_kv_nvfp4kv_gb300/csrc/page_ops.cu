@@ -20,6 +20,8 @@
 // list is found by a minimum.
 #include <climits>
 #include <cstdint>
+#include <map>
+#include <mutex>
 
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -177,110 +179,216 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
 }
 
 // ---- release --------------------------------------------------------------------
-// One cluster: its CTAs keep the three passes over the entries apart by the cluster's
-// barrier.  A pass is loads and atomics on the pages' words in L2.
+// Four passes over the entries, loads and atomics on the pages' words in L2:
 //   1  every entry counts its page's owners down;
 //   2  where that went below 0, the page is free: its word becomes the least of
 //      INT_MIN + entry;
-//   3  the entry that finds its own number there puts the page on the free list, at the
-//      place that the count of such entries before it gives, and the word back to 0.
-constexpr int kCluster = 8, kThreads = 1024, kWarps = kThreads / 32;
+//   3  the entry that finds its own number there is the page's first;
+//   4  it puts the page on the free list, at the place that the count of such entries
+//      before it gives, and the word back to 0.
+// A small call is one launch of one CTA, which keeps its entries' pages in registers over
+// the passes.  For a large one passes 1 and 2 are launches over all SMs (the random words
+// want many loads in flight), 3 and 4 one cluster whose barrier joins the counts.
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kUnits = 4;  // units of 32 entries that a warp has in flight
+constexpr int kOneCta = 16 * kThreads;  // entries up to which one CTA is used
+constexpr int kMostMarks = 8192;  // units of a CTA whose marks are kept (others: all looked at)
 
-__global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseParams p) {
-  namespace cg = cooperative_groups;
-  extern __shared__ int32_t smem[];
-  const int B = p.num_rows, P = p.page_size;
-  int32_t* s_first = smem;           // [B + 1] first entry of each row
-  int32_t* s_col = s_first + B + 1;  // [B] first column that it gives up
-  __shared__ int s_bad, s_freed[kWarps], s_mine;
-  const cg::cluster_group cluster = cg::this_cluster();
-  const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// The rows that give up pages, in shared memory: the first entry of each (and the count of
+// all), the first column that it gives up and its number.
+struct Leaving {
+  int32_t* first;  // [rows + 1]
+  int32_t* col;    // [rows]
+  int32_t* row;    // [rows]
+  int rows, entries;
+};
+
+// (every thread of the CTA)  false, and flagged if `report`: a call that cannot be
+template <int THREADS>
+__device__ __forceinline__ bool leaving_rows(const ReleaseParams& p, int32_t* smem, bool report,
+                                             Leaving* out) {
+  __shared__ int s_bad;
+  const int B = p.num_rows, P = p.page_size, tid = threadIdx.x;
+  Leaving s{smem, smem + B + 1, smem + 2 * B + 1, 0, 0};
   const int head = *p.free_head;
   if (tid == 0) s_bad = 0;
   __syncthreads();
-  const int per = (B + kThreads - 1) / kThreads;
+  const int per = (B + THREADS - 1) / THREADS;
   const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
   longlong2 mine = make_longlong2(0, 0);
   bool bad = false;
   for (int b = b0; b < b1; ++b) {
     const int len = p.kv_len[b], keep = p.keep_len[b];
-    if (len < 0 || len > kMaxLen || keep < 0 || keep > len || (len + P - 1) / P > p.table_width) {
-      bad = true;
-      continue;
-    }
-    const int lo = (keep + P - 1) / P, hi = (len + P - 1) / P;
-    s_col[b] = lo;
-    s_first[b] = hi - lo;  // kept here until its sum takes the place
-    mine.x += hi - lo;
+    bad = bad || len < 0 || len > kMaxLen || keep < 0 || keep > len ||
+          (len + P - 1) / P > p.table_width;
+    const int n = bad ? 0 : (len + P - 1) / P - (keep + P - 1) / P;
+    mine.x += n;
+    mine.y += n > 0;
   }
   if (bad) atomicOr(&s_bad, 1);
   longlong2 total;
-  longlong2 at = cta_sums<kThreads>(mine, &total);
+  longlong2 at = cta_sums<THREADS>(mine, &total);  // (its barrier completes s_bad)
   // (an entry's number and INT_MIN add up in 32 bits)
   const bool stop = s_bad || total.x >= INT_MAX / 2 || head < 0 || head > p.num_free;
-  if (!stop) {
-    for (int b = b0; b < b1; ++b) {
-      const int n = s_first[b];
-      s_first[b] = static_cast<int32_t>(at.x);
-      at.x += n;
-    }
-    if (tid == 0) s_first[B] = static_cast<int32_t>(total.x);
+  for (int b = b0; b < b1 && !stop; ++b) {
+    const int lo = (p.keep_len[b] + P - 1) / P, n = (p.kv_len[b] + P - 1) / P - lo;
+    if (n == 0) continue;
+    s.first[at.y] = static_cast<int32_t>(at.x);
+    s.col[at.y] = lo;
+    s.row[at.y] = b;
+    at.x += n;
+    ++at.y;
   }
+  s.rows = static_cast<int>(total.y);
+  s.entries = static_cast<int>(total.x);
+  if (tid == 0 && !stop) s.first[s.rows] = s.entries;
+  if (tid == 0 && stop && report && p.flags) atomicOr(p.flags, s_bad ? 0x40u : 0x80u);
   __syncthreads();
-  if (stop) {  // (every CTA alike, before the cluster's first barrier)
-    if (rank == 0 && tid == 0 && p.flags) atomicOr(p.flags, s_bad ? 0x40u : 0x80u);
-    return;
-  }
+  *out = s;
+  return !stop;
+}
 
-  // this warp's entries: neighbours, so that the free list keeps their order
-  const int entries = static_cast<int>(total.x);
-  const int warps = ranks * kWarps, mw = rank * kWarps + warp;
-  const int share = ((entries + warps - 1) / warps + 31) / 32 * 32;
-  const int e0 = static_cast<int>(min((int64_t)mw * share, (int64_t)entries));
-  const int e1 = min(entries, e0 + share);
-  const int lo = e0 < e1 ? owner(s_first, 0, B, e0) : 0;
-  const int hi = e0 < e1 ? owner(s_first, lo, B, e1 - 1) + 1 : 0;
-  auto page_of = [&](int e) -> int {  // -1: not in the pool (flagged in the first pass)
-    const int b = owner(s_first, lo, hi, e);
-    const int id = p.block_table[b * p.table_stride + s_col[b] + (e - s_first[b])];
-    return id >= 0 && id < p.num_pages ? id : -1;
-  };
-  // A lane's pages stay in registers over the passes while they are few.
-  int32_t kept[kChunk];
+// The pages of kUnits units from unit u on, those that `wanted` has a bit for, an entry a
+// lane; -1: no entry below `last`, or a page that is not in the pool (flagged if `report`).
+// `row`: the leaving row of an entry before (the whole warp alike); it follows the units.
+__device__ __forceinline__ void pages_of(const ReleaseParams& p, const Leaving& s, int u, int last,
+                                         uint32_t wanted, bool report, int& row,
+                                         int32_t (&pg)[kUnits]) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int j = 0; j < kChunk; ++j) {
-    const int e = e0 + 32 * j + lane;
-    kept[j] = e < e1 ? page_of(e) : -1;
-    if (e < e1 && kept[j] < 0 && p.flags) atomicOr(p.flags, 0x1u);
+  for (int j = 0; j < kUnits; ++j) {
+    const int e0 = (u + j) * 32, e = e0 + lane;
+    pg[j] = -1;
+    if (e0 >= last || !(wanted >> j & 1u)) continue;
+    while (s.first[row + 1] <= e0) ++row;
+    int b = row;
+    // (a row has an entry at least: 32 entries lie in 32 rows at most)
+    if (s.first[row + 1] < min(e0 + 32, last)) b = owner(s.first, row, min(row + 32, s.rows), e);
+    if (e < last) pg[j] = p.block_table[s.row[b] * p.table_stride + s.col[b] + (e - s.first[b])];
   }
-  auto each = [&](auto&& act) {
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) act(e0 + 32 * j + lane, kept[j]);
-    for (int e = e0 + 32 * kChunk + lane; e - lane < e1; e += 32) {
-      const int pg = e < e1 ? page_of(e) : -1;
-      act(e, pg);
+  for (int j = 0; j < kUnits; ++j)
+    if (pg[j] < 0 || pg[j] >= p.num_pages) {
+      if (report && (wanted >> j & 1u) && (u + j) * 32 + lane < last && p.flags)
+        atomicOr(p.flags, 0x1u);
+      pg[j] = -1;
     }
+}
+
+// Pass 1 and pass 2 of the units in hand.
+__device__ __forceinline__ void count_down(const ReleaseParams& p, const int32_t (&pg)[kUnits]) {
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j)
+    if (pg[j] >= 0) atomicSub(p.page_shares + pg[j], 1);
+}
+// (returns the lane's free pages, a bit a unit)
+__device__ __forceinline__ uint32_t least_entry(const ReleaseParams& p, int u, int entries,
+                                                const int32_t (&pg)[kUnits]) {
+  const int lane = threadIdx.x & 31;
+  int v[kUnits];
+  uint32_t free = 0;
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) v[j] = pg[j] >= 0 ? __ldcg(p.page_shares + pg[j]) : 0;
+#pragma unroll
+  for (int j = 0; j < kUnits; ++j) {
+    if (v[j] >= 0) continue;
+    free |= 1u << j;
+    atomicMin(p.page_shares + pg[j], INT_MIN + (u + j) * 32 + lane);
+    // given up more often than it has owners (whoever changes the word first has read it
+    // before)
+    if (v[j] < -1 && v[j] >= INT_MIN + entries && p.flags) atomicOr(p.flags, 0x200u);
+  }
+  return free;
+}
+
+// Pass 1 or 2 over all SMs.
+constexpr int kPassThreads = 256;
+__global__ void __launch_bounds__(kPassThreads) release_pass_kernel(const ReleaseParams p,
+                                                                    int pass) {
+  extern __shared__ int32_t smem[];
+  Leaving s;
+  if (!leaving_rows<kPassThreads>(p, smem, false, &s)) return;
+  const int units = (s.entries + 31) / 32, warps = gridDim.x * (kPassThreads / 32);
+  const int share = (units + warps - 1) / warps;
+  const int w = blockIdx.x * (kPassThreads / 32) + (threadIdx.x >> 5);
+  const int u0 = static_cast<int>(min((int64_t)w * share, (int64_t)units));
+  const int u1 = min(units, u0 + share), last = min(u1 * 32, s.entries);
+  if (u0 == u1) return;
+  int row = owner(s.first, 0, s.rows, u0 * 32);
+  for (int u = u0; u < u1; u += kUnits) {
+    int32_t pg[kUnits];
+    pages_of(p, s, u, last, ~0u, pass == 1, row, pg);
+    if (pass == 1)
+      count_down(p, pg);
+    else
+      least_entry(p, u, s.entries, pg);
+  }
+}
+
+// All passes (from = 1) or the last two (from = 3), one cluster.
+__global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseParams p, int from) {
+  namespace cg = cooperative_groups;
+  extern __shared__ int32_t smem[];
+  uint32_t* s_mark = reinterpret_cast<uint32_t*>(smem + 3 * p.num_rows + 1);  // [p.marks]
+  __shared__ int s_freed[kWarps], s_mine;
+  const cg::cluster_group cluster = cg::this_cluster();
+  const int rank = cluster.block_rank(), ranks = cluster.num_blocks();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int head = *p.free_head;
+  Leaving s;
+  // (every CTA alike, before the cluster's first barrier)
+  if (!leaving_rows<kThreads>(p, smem, rank == 0, &s)) return;
+
+  // this warp's units of 32 entries: neighbours, so that the free list keeps their order
+  const int units = (s.entries + 31) / 32, warps = ranks * kWarps;
+  const int share = (units + warps - 1) / warps;
+  const int u0 = static_cast<int>(min((int64_t)(rank * kWarps + warp) * share, (int64_t)units));
+  const int u1 = min(units, u0 + share), last = min(u1 * 32, s.entries);
+  const int row0 = u0 < u1 ? owner(s.first, 0, s.rows, u0 * 32) : 0;
+  const bool once = u1 - u0 <= kUnits;  // the pages stay in registers
+  const bool marked = share * kWarps <= p.marks;
+  uint32_t* mark = s_mark + warp * share;  // the entries of unit u0 + k that are first
+  int row = row0;
+  int32_t pg[kUnits];
+  auto hold = [&](int u, uint32_t wanted, bool report) {
+    pages_of(p, s, u, last, wanted, report, row, pg);
   };
-  each([&](int e, int pg) {
-    if (pg >= 0)
-      atomicSub(p.page_shares + pg, 1);
-    else if (e < e1 && e >= e0 + 32 * kChunk && p.flags)
-      atomicOr(p.flags, 0x1u);
-  });
-  cluster.sync();
-  each([&](int e, int pg) {
-    if (pg < 0 || __ldcg(p.page_shares + pg) >= 0) return;
-    const int before = atomicMin(p.page_shares + pg, INT_MIN + e);
-    // (given up more often than it has owners: free once)
-    if (before < -1 && before >= INT_MIN + entries && p.flags) atomicOr(p.flags, 0x200u);
-  });
-  cluster.sync();
+  if (once) hold(u0, ~0u, from == 1);
+  if (from == 1) {
+    for (int u = u0; u < u1; u += kUnits) {
+      if (!once) hold(u, ~0u, true);
+      count_down(p, pg);
+    }
+    cluster.sync();
+    row = row0;
+    for (int u = u0; u < u1; u += kUnits) {
+      if (!once) hold(u, ~0u, false);
+      least_entry(p, u, s.entries, pg);
+    }
+    cluster.sync();
+  }
   int freed = 0;
-  each([&](int e, int pg) {
-    const bool first = pg >= 0 && __ldcg(p.page_shares + pg) == INT_MIN + e;
-    freed += __popc(__ballot_sync(0xffffffffu, first));
-  });
+  row = row0;
+  uint32_t firsts = 0;  // of the units in hand, a bit a unit
+  auto find_firsts = [&](int u) {
+    int v[kUnits];
+    firsts = 0;
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) v[j] = pg[j] >= 0 ? __ldcg(p.page_shares + pg[j]) : 0;
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j)
+      if (v[j] == INT_MIN + (u + j) * 32 + lane) firsts |= 1u << j;
+  };
+  for (int u = u0; u < u1; u += kUnits) {
+    if (!once) hold(u, ~0u, false);
+    find_firsts(u);
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) {
+      const uint32_t votes = __ballot_sync(0xffffffffu, firsts >> j & 1u);
+      freed += __popc(votes);
+      if (marked && lane == 0 && u + j < u1) mark[u + j - u0] = votes;
+    }
+  }
   if (lane == 0) s_freed[warp] = freed;
   __syncthreads();
   if (tid == 0) {
@@ -297,29 +405,46 @@ __global__ void __launch_bounds__(kThreads) release_kernel(const ReleaseParams p
   }
   for (int w = 0; w < warp; ++w) before += s_freed[w];
   cluster.sync();  // (no CTA ends, and no word of a page is put back, while another reads)
-  if (all > head) {
-    // More than ever were taken: the words are put back as they were, nothing is listed.
-    each([&](int e, int pg) {
-      if (pg >= 0 && __ldcg(p.page_shares + pg) == INT_MIN + e) atomicExch(p.page_shares + pg, -1);
-    });
+  // More than were ever taken: the words are put back as they were (to -1 by the first
+  // entry, then up by every one), nothing is listed.
+  const bool undo = all > head;
+  int place = head - all + before;
+  row = row0;
+  for (int u = u0; u < u1; u += kUnits) {
+    uint32_t wanted = ~0u;
+    if (marked) {
+      wanted = __ballot_sync(0xffffffffu, lane < kUnits && u + lane < u1 &&
+                                              mark[min(u + lane, u1 - 1) - u0] != 0);
+      if (wanted == 0) continue;
+    }
+    if (!once) {
+      hold(u, wanted, false);
+      find_firsts(u);
+    }
+#pragma unroll
+    for (int j = 0; j < kUnits; ++j) {
+      const bool mine = firsts >> j & 1u;
+      const uint32_t votes = __ballot_sync(0xffffffffu, mine);
+      if (mine) {
+        if (!undo) p.free_pages[place + __popc(votes & ((1u << lane) - 1u))] = pg[j];
+        __stcg(p.page_shares + pg[j], undo ? -1 : 0);
+      }
+      place += __popc(votes);
+    }
+  }
+  if (undo) {
     cluster.sync();
-    each([&](int, int pg) {
-      if (pg >= 0) atomicAdd(p.page_shares + pg, 1);
-    });
+    row = row0;
+    for (int u = u0; u < u1; u += kUnits) {
+      if (!once) hold(u, ~0u, false);
+      for (int j = 0; j < kUnits; ++j)
+        if (pg[j] >= 0) atomicAdd(p.page_shares + pg[j], 1);
+    }
     if (rank == 0 && tid == 0 && p.flags) atomicOr(p.flags, 0x80u);
     return;
   }
-  int place = head - all + before;
-  each([&](int e, int pg) {
-    const bool first = pg >= 0 && __ldcg(p.page_shares + pg) == INT_MIN + e;
-    const unsigned votes = __ballot_sync(0xffffffffu, first);
-    if (first) {
-      p.free_pages[place + __popc(votes & ((1u << lane) - 1u))] = pg;
-      __stcg(p.page_shares + pg, 0);
-    }
-    place += __popc(votes);
-  });
-  for (int b = rank * kThreads + tid; b < B; b += ranks * kThreads) p.kv_len[b] = p.keep_len[b];
+  for (int b = rank * kThreads + tid; b < p.num_rows; b += ranks * kThreads)
+    p.kv_len[b] = p.keep_len[b];
   if (rank == 0 && tid == 0) *p.free_head_out = head - all;
 }
 
@@ -394,26 +519,82 @@ cudaError_t launch_fork(const ForkParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_release(const ReleaseParams& p, cudaStream_t stream) {
-  constexpr int kMaxSmem = (2 * kMaxPageTableBatch + 1) * 4;
-  const int smem = (2 * p.num_rows + 1) * 4;
-  if (smem > 40 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(release_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-    if (e != cudaSuccess) return e;
+// The largest cluster that the current device takes of release_kernel: 16 CTAs, or the 8
+// that every device does.
+static cudaError_t release_cluster(int smem, int* ctas) {
+  static std::mutex mu;
+  static std::map<int, int> known;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto it = known.find(dev);
+  if (it != known.end()) {
+    *ctas = it->second;
+    return cudaSuccess;
   }
+  e = cudaFuncSetAttribute(release_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(release_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kCluster);
+  cfg.gridDim = dim3(16);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = kCluster;
+  attr.val.clusterDim.x = 16;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, release_kernel, p);
+  int clusters = 0;
+  e = cudaOccupancyMaxActiveClusters(&clusters, release_kernel, &cfg);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    clusters = 0;
+  }
+  *ctas = known[dev] = clusters > 0 ? 16 : 8;
+  return cudaSuccess;
+}
+
+cudaError_t launch_release(ReleaseParams p, cudaStream_t stream) {
+  constexpr int kRowsSmem = (3 * kMaxPageTableBatch + 1) * 4;
+  constexpr int kMaxSmem = kRowsSmem + kMostMarks * 4;
+  int ctas = 8;
+  cudaError_t e = release_cluster(kMaxSmem, &ctas);
+  if (e != cudaSuccess) return e;
+  const int rows_smem = (3 * p.num_rows + 1) * 4;
+  const int64_t most = (int64_t)p.num_rows * p.table_width;
+  int from = 1;
+  if (most <= kOneCta) {
+    ctas = 1;
+  } else {
+    if (rows_smem > 40 * 1024) {
+      e = cudaFuncSetAttribute(release_pass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kRowsSmem);
+      if (e != cudaSuccess) return e;
+    }
+    const int64_t want = most / (32 * kUnits * (kPassThreads / 32)) + 1;
+    const int grid = static_cast<int>(want < 152 * 4 ? want : 152 * 4);
+    for (int pass = 1; pass <= 2; ++pass)
+      release_pass_kernel<<<grid, kPassThreads, rows_smem, stream>>>(p, pass);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    from = 3;
+  }
+  const int64_t units = ((most + 31) / 32 + ctas * kWarps - 1) / (ctas * kWarps) * kWarps;
+  p.marks = static_cast<int>(units < kMostMarks ? units : kMostMarks);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = rows_smem + p.marks * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, release_kernel, p, from);
 }
 
 cudaError_t launch_page_copies(const PageCopyParams& p, cudaStream_t stream) {

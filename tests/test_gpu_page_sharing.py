@@ -307,3 +307,26 @@ def test_graph_and_stream():
         assert list(zip(src.tolist(), dst.tolist())) == copies
         for s, d in copies:
             assert all(torch.equal(x[s], x[d]) for x in bufs)
+
+
+def test_more_entries_than_marks():
+    """Nine million pages given up at once, every third of them shared: past the marks that
+    the CTAs keep."""
+    n = 9_000_000
+    ids = torch.randperm(n, generator=torch.Generator().manual_seed(2)).to(torch.int32).cuda()
+    shares = (torch.arange(n, dtype=torch.int32) % 3 == 0).int().cuda()
+    kv_len, flags = i32([n, 0]), torch.zeros(1, dtype=torch.int32).cuda()
+    free, head = torch.full((n + 4,), -1, dtype=torch.int32).cuda(), i32([n + 1])
+    table = torch.stack([ids, torch.full_like(ids, -1)])
+    want = ids[shares[ids.long()] == 0]
+    N.nvfp4kv_release_pages(i32([5, 0]), kv_len, table, shares, free, head, page_size=1,
+                            device_flags=flags)
+    torch.cuda.synchronize()
+    kept = ids[:5].long()
+    want = want[(want[:, None] != kept[None, :].int()).all(1)]
+    assert int(flags) == 0 and kv_len.tolist() == [5, 0]
+    assert int(head) == n + 1 - want.numel()
+    assert torch.equal(free[int(head):n + 1], want) and int(free[int(head) - 1]) == -1
+    left = torch.zeros_like(shares)
+    left[kept] = (kept % 3 == 0).int()
+    assert torch.equal(shares, left)
