@@ -67,20 +67,13 @@ class PagedCache:
                    layout.head_dim_vo, k_global_scale, v_global_scale, layout.page_size)
 
     def struct(self) -> PagedCacheStruct:
-        s = PagedCacheStruct()
-        s.k_data, s.v_data = self.k_data.data_ptr(), self.v_data.data_ptr()
-        s.k_sf, s.v_sf = self.k_sf.data_ptr(), self.v_sf.data_ptr()
-        for w, pre in (("k_data", "k"), ("v_data", "v"), ("k_sf", "k_sf"),
-                       ("v_sf", "v_sf")):
-            sp, ss, sh = self.strides[w]
-            setattr(s, pre + "_stride_page", sp)
-            setattr(s, pre + "_stride_slot", ss)
-            setattr(s, pre + "_stride_head", sh)
-        s.num_pages, s.page_size = self.num_pages, self.page_size
-        s.num_kv_heads = self.num_kv_heads
-        s.head_dim_qk, s.head_dim_vo = self.head_dim_qk, self.head_dim_vo
-        s.k_global_scale, s.v_global_scale = self.k_global_scale, self.v_global_scale
-        return s
+        # (by position, in the struct's order: this runs at every call)
+        st = self.strides
+        return PagedCacheStruct(
+            self.k_data.data_ptr(), self.v_data.data_ptr(), self.k_sf.data_ptr(),
+            self.v_sf.data_ptr(), *st["k_data"], *st["v_data"], *st["k_sf"], *st["v_sf"],
+            self.num_pages, self.page_size, self.num_kv_heads, self.head_dim_qk,
+            self.head_dim_vo, self.k_global_scale, self.v_global_scale)
 
     def host_copy(self):
         return {w: getattr(self, w).cpu() for w in ("k_data", "v_data", "k_sf", "v_sf")}

@@ -57,15 +57,18 @@ def _stream_of(stream, dev):
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, dtype, device, stream, like=None):
     """An output of a call on `stream`, allocated in that stream's order (the
-    caching allocator may hand its memory on as soon as it is freed)."""
+    caching allocator may hand its memory on as soon as it is freed).  ``like``: a
+    tensor of that type and device (sooner done)."""
     if stream is None:
+        if like is not None:
+            return like.new_empty(shape)
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream))
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=device if like is None else like.device)
 
 
 # ---- the step's page table ------------------------------------------------------
@@ -214,24 +217,33 @@ def nvfp4kv_norm_rope(plan: RopePlan, q: Optional[torch.Tensor], k: Optional[tor
     if q is None and k is None:
         return None, None
     args, outs, dev = _rope_args(plan, q, k, positions, q_out, k_out, stream)
-    kind = None
-    for name, x, w in (("q_weight", q, q_weight), ("k_weight", k, k_weight)):
-        if x is None:
-            continue
-        if w is None or w.dim() != 1 or w.numel() != plan.head_dim or w.stride(0) != 1:
-            raise ValueError("%s must be contiguous [%d]" % (name, plan.head_dim))
-        if w.dtype not in (x.dtype, torch.float32) or kind not in (None, w.dtype):
-            raise ValueError("the weights must be of the rows' type or both torch.float32")
-        if w.get_device() != dev:
-            _check_device(dev, w)
-        kind = w.dtype
+    first, w = (q, q_weight) if q is not None else (k, k_weight)
+    kind = _weight("q_weight" if q is not None else "k_weight", w, plan, first.dtype, dev)
+    if q is not None and k is not None and \
+            _weight("k_weight", k_weight, plan, first.dtype, dev) is not kind:
+        raise ValueError("the weights must be of one type")
     st = _entry("nvfp4kv_norm_rope")(
         *args, None if q is None else q_weight.data_ptr(),
-        None if k is None else k_weight.data_ptr(), 2 if kind == torch.float32 else _DTYPE[kind],
-        weight_offset, eps, _stream_of(stream, dev))
+        None if k is None else k_weight.data_ptr(), _WEIGHT[kind], weight_offset, eps,
+        _stream_of(stream, dev))
     if st:
         check(st, "nvfp4kv_norm_rope")
     return outs
+
+
+_WEIGHT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def _weight(name, w, plan, dtype, dev):
+    """Check the weights of a norm; returns their type."""
+    if w is None or w.shape != (plan.head_dim,) or not w.is_contiguous():
+        raise ValueError("%s must be contiguous [%d]" % (name, plan.head_dim))
+    kind = w.dtype
+    if kind is not dtype and kind is not torch.float32:
+        raise ValueError("%s must be of the rows' type or torch.float32" % name)
+    if w.get_device() != dev:
+        _check_device(dev, w)
+    return kind
 
 
 def _rope_args(plan, q, k, positions, q_out, k_out, stream):
@@ -258,7 +270,7 @@ def _rope_rows(dim, name, x, out, n, dtype, dev, stream):
         return (None, 0, 0, None, 0, 0, 0), None
     rows, heads = _rows(name, x, dim, n, dtype)
     if out is None:
-        out = _empty((n, heads, dim), dtype, x.device, stream)
+        out = _empty((n, heads, dim), dtype, None, stream, x)
         to0, to1 = heads * dim, dim
     else:
         (to0, to1, _), out_heads = _rows(name + "_out", out, dim, n, dtype)
