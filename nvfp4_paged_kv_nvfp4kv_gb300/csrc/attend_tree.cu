@@ -33,6 +33,7 @@
 
 #include "append_fused.cuh"
 #include "device_common.cuh"
+#include "f32x2.cuh"
 #include "internal.h"
 #include "tcgen05.cuh"
 
@@ -93,26 +94,6 @@ __device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t parity, volati
     if (mbar_test_wait(bar, parity)) return true;
   return wait_bar(bar, parity, abort, flags);
 }
-// pairs of f32 (Blackwell's two-wide float32 arithmetic)
-__device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
 __device__ __forceinline__ void cluster_arrive_wait() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n"
                ::: "memory");

@@ -19,7 +19,14 @@
 // Bound by HBM for prompts (each element is read and written once), by latency for
 // a few tokens.  As in rope.cu a warp takes a token (with few tokens, some of its
 // heads) and a lane keeps a column of two 16-byte chunks; the column's sum goes
-// over the lanes of its head by shuffles, a power of two of them.
+// over the lanes of its head by shuffles, a power of two of them.  Loads, sum, root and
+// stores of a head are one dependent chain, so a lane keeps three heads' loads in a ring:
+// a head's place is taken by the load three on as soon as it is unpacked.  Measured
+// (replayed, three sets of tensors in turn): 16384 tokens x 40 heads of 128, bf16, 60 us,
+// 5.6 TB/s (0.84 of a plain copy); 211 tokens x 18 heads of 256, a quarter in pairs, f16,
+// 4.2 us.  Loads in batches of three 66 us, of two 73 (and 85 with a token's heads on two
+// warps: the angles and weights are then formed twice); two or four heads in the ring 63
+// and 64; chunks of 8 bytes, half the registers and more warps, 66.
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -37,8 +44,8 @@ using dev::rope_columns;
 using dev::row_of;
 using dev::unpack2;
 
-constexpr int kBatch = 2;           // heads whose loads a lane has in flight
-constexpr int kFewest = 152 * 128;  // warps a launch should have: four waves of CTAs
+constexpr int kBatch = 3;          // heads whose loads a lane has in flight
+constexpr int kFewest = 152 * 64;  // warps a launch should have
 
 __host__ __device__ __forceinline__ int lanes_for(int columns) {  // a power of two, at most 32
   int w = 32;
@@ -54,34 +61,42 @@ __device__ __forceinline__ float weight(const NormRopeParams& p, bool k, int d) 
   return x + p.weight_offset;
 }
 
-// the eight values of a 16-byte chunk
+// 8 elements of 16 bits
+struct Chunk {
+  uint32_t w[4];
+};
+__device__ __forceinline__ Chunk load_chunk(const uint16_t* at) {
+  const uint4 v = *reinterpret_cast<const uint4*>(at);
+  return {{v.x, v.y, v.z, v.w}};
+}
 template <bool F16>
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+__device__ __forceinline__ void store_chunk(uint16_t* at, const float* y) {
+  *reinterpret_cast<uint4*>(at) = make_uint4(pack2<F16>(y[0], y[1]), pack2<F16>(y[2], y[3]),
+                                             pack2<F16>(y[4], y[5]), pack2<F16>(y[6], y[7]));
+}
+template <bool F16>
+__device__ __forceinline__ void unpack_chunk(const Chunk& c, float* x) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float2 f = unpack2<F16>(w[j]);
+    const float2 f = unpack2<F16>(c.w[j]);
     x[2 * j] = f.x;
     x[2 * j + 1] = f.y;
   }
 }
-template <bool F16>
-__device__ __forceinline__ uint4 pack8(const float (&y)[8]) {
-  return make_uint4(pack2<F16>(y[0], y[1]), pack2<F16>(y[2], y[3]), pack2<F16>(y[4], y[5]),
-                    pack2<F16>(y[6], y[7]));
-}
 
-// the weights of a 16-byte chunk of dims
+// the weights of a chunk of dims
 template <bool F16>
-__device__ __forceinline__ void weight8(const NormRopeParams& p, bool k, int d, float (&w)[8]) {
+__device__ __forceinline__ void weight_chunk(const NormRopeParams& p, bool k, int d,
+                                             float (&w)[8]) {
   const void* at = k ? p.k_weight : p.q_weight;
   if (p.weight_f32) {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(at) + d);
-    const float4 a = f[0], b = f[1];
-    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+#pragma unroll
+    for (int j = 0; j < 8; j += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(static_cast<const float*>(at) + d + j);
+      w[j] = a.x; w[j + 1] = a.y; w[j + 2] = a.z; w[j + 3] = a.w;
+    }
   } else {
-    unpack8<F16>(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(at) + d), w);
+    unpack_chunk<F16>(load_chunk(static_cast<const uint16_t*>(at) + d), w);
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) w[j] += p.weight_offset;
@@ -119,11 +134,11 @@ __device__ __forceinline__ float head_factor(const NormRopeParams& p, float (&x)
   return rsqrtf(fmaf(ss, inv_dim, eps));
 }
 
-// Columns as in rope_kernel: in the half layout (R % 16 == 0) the elements 8c ..
-// 8c+7 and R/2 + 8c .., eight pairs, or two neighbouring chunks of the dims behind;
-// interleaved, the elements 16c .. 16c+15.
+// Columns as in rope_kernel: in the half layout (R % 16 == 0) the elements 8c .. 8c+7 and
+// R/2 + 8c .., eight pairs, or two neighbouring chunks of the dims behind; interleaved, the
+// elements 16c .. 16c+15.
 template <bool F16, bool INTER>
-__global__ void __launch_bounds__(32) norm_rope_kernel(const NormRopeParams np, int splits) {
+__global__ void __launch_bounds__(32, 20) norm_rope_kernel(const NormRopeParams np, int splits) {
   __shared__ __align__(16) float2 sc[kMaxPairs];
   const RopeParams& p = np.rope;
   const int lane = threadIdx.x;
@@ -142,27 +157,24 @@ __global__ void __launch_bounds__(32) norm_rope_kernel(const NormRopeParams np, 
   const int d0 = INTER ? 16 * c : c < rcols ? 8 * c : 2 * half + 16 * (c - rcols);
   const int d1 = !INTER && c < rcols ? half + 8 * c : d0 + 8;
   const bool two = !idle && d1 < p.head_dim;
-  uint4 va[kBatch], vb[kBatch];
-  auto load = [&](int hb) {
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int h = hb + hs + k * step;
-      va[k] = vb[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (h < heads && !idle) {
-        const uint16_t* in = row_of(p, t, h).in;
-        va[k] = *reinterpret_cast<const uint4*>(in + d0);
-        if (two) vb[k] = *reinterpret_cast<const uint4*>(in + d1);
-      }
+  Chunk va[kBatch], vb[kBatch];
+  auto load = [&](int h, Chunk& a, Chunk& b) {
+    a = b = Chunk{};
+    if (h < heads && !idle) {
+      const uint16_t* in = row_of(p, t, h).in;
+      a = load_chunk(in + d0);
+      if (two) b = load_chunk(in + d1);
     }
   };
-  load(part * side);
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) load(part * side + hs + k * step, va[k], vb[k]);
   angles(p, t, sc, lane);
   // y of the first chunk's element j: x_j a_j + (the pair's other) b_j; second chunk: e, f
   float ca[8], cb[8], ce[8], cf[8];
   auto coefficients = [&](bool k) {
     float wa[8] = {}, wb[8] = {};
-    if (!idle) weight8<F16>(np, k, d0, wa);
-    if (two) weight8<F16>(np, k, d1, wb);
+    if (!idle) weight_chunk<F16>(np, k, d0, wa);
+    if (two) weight_chunk<F16>(np, k, d1, wb);
     if constexpr (INTER) {
       const int live = min(8, max(0, half - 8 * c));  // pairs of the column that turn
 #pragma unroll
@@ -188,39 +200,34 @@ __global__ void __launch_bounds__(32) norm_rope_kernel(const NormRopeParams np, 
   };
   bool now_k = part * side + hs >= p.num_qo_heads;
   coefficients(now_k);
-  for (int hb = part * side; hb < heads; hb += kBatch * step) {  // (the whole warp together)
-    if (hb > part * side) load(hb);
+  // heads in turn, each one's place in the ring taken by the load of the one kBatch on
+  for (int hb = part * side; hb < heads;) {  // (the whole warp together)
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int h = hb + hs + k * step;
+    for (int k = 0; k < kBatch; ++k, hb += step) {
+      if (hb >= heads) break;
+      const int h = hb + hs;
       float x[16];
-      {
-        float lo[8], hi[8];
-        unpack8<F16>(va[k], lo);
-        unpack8<F16>(vb[k], hi);
+      unpack_chunk<F16>(va[k], x);
+      unpack_chunk<F16>(vb[k], x + 8);
+      load(h + kBatch * step, va[k], vb[k]);
+      const float r = head_factor<F16>(np, x, wide, inv_dim);
+      if (h < heads && !idle) {
+        if (h >= p.num_qo_heads && !now_k) {
+          now_k = true;
+          coefficients(true);
+        }
+        float ya[8], yb[8];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] *= r;  // (first: products of tiny values lose bits)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          x[j] = lo[j];
-          x[8 + j] = hi[j];
+          ya[j] = fmaf(x[j], ca[j], (INTER ? x[j ^ 1] : x[8 + j]) * cb[j]);
+          yb[j] = fmaf(x[8 + j], ce[j], (INTER ? x[8 + (j ^ 1)] : x[j]) * cf[j]);
         }
+        uint16_t* out = row_of(p, t, h).out;
+        store_chunk<F16>(out + d0, ya);
+        if (two) store_chunk<F16>(out + d1, yb);
       }
-      const float r = head_factor<F16>(np, x, wide, inv_dim);
-      if (h >= heads || idle) continue;
-      if (h >= p.num_qo_heads && !now_k) {
-        now_k = true;
-        coefficients(true);
-      }
-      float ya[8], yb[8];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] *= r;  // (first: products of tiny values lose bits)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        ya[j] = fmaf(x[j], ca[j], (INTER ? x[j ^ 1] : x[8 + j]) * cb[j]);
-        yb[j] = fmaf(x[8 + j], ce[j], (INTER ? x[8 + (j ^ 1)] : x[j]) * cf[j]);
-      }
-      uint16_t* out = row_of(p, t, h).out;
-      *reinterpret_cast<uint4*>(out + d0) = pack8<F16>(ya);
-      if (two) *reinterpret_cast<uint4*>(out + d1) = pack8<F16>(yb);
     }
   }
 }
@@ -265,13 +272,10 @@ __global__ void __launch_bounds__(32) norm_rope_odd_kernel(const NormRopeParams 
     float x[8 * CP];
 #pragma unroll
     for (int c = 0; c < CP; ++c) {
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      Chunk v{};
       if (h < heads && col + 32 * c < cols)
-        v = reinterpret_cast<const uint4*>(row_of(p, t, h).in)[col + 32 * c];
-      float f[8];
-      unpack8<F16>(v, f);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[8 * c + j] = f[j];
+        v = load_chunk(row_of(p, t, h).in + 8 * (col + 32 * c));
+      unpack_chunk<F16>(v, x + 8 * c);
     }
     const float r = head_factor<F16>(np, x, wide, inv_dim);
 #pragma unroll
@@ -299,7 +303,7 @@ __global__ void __launch_bounds__(32) norm_rope_odd_kernel(const NormRopeParams 
         const float z = d < 2 * half ? row[other(d)] : 0.f;
         y[j] = fmaf(x[8 * c + j], ca[c][j], z * cb[c][j]);
       }
-      reinterpret_cast<uint4*>(row_of(p, t, h).out)[col + 32 * c] = pack8<F16>(y);
+      store_chunk<F16>(row_of(p, t, h).out + 8 * (col + 32 * c), y);
     }
   }
 }
@@ -318,18 +322,17 @@ cudaError_t launch_norm_rope(const NormRopeParams& np, cudaStream_t stream) {
   const int64_t want = ((int64_t)kFewest + p.num_tokens - 1) / p.num_tokens;
   const int splits = want < most ? static_cast<int>(want) : most;
   const unsigned grid = static_cast<unsigned>(static_cast<int64_t>(p.num_tokens) * splits);
+  auto launch = [&](auto* bf16, auto* f16) {
+    (p.f16 ? f16 : bf16)<<<grid, 32, 0, stream>>>(np, splits);
+  };
   if (odd && cols > 32)
-    (p.f16 ? norm_rope_odd_kernel<true, 2>
-           : norm_rope_odd_kernel<false, 2>)<<<grid, 32, 0, stream>>>(np, splits);
+    launch(norm_rope_odd_kernel<false, 2>, norm_rope_odd_kernel<true, 2>);
   else if (odd)
-    (p.f16 ? norm_rope_odd_kernel<true, 1>
-           : norm_rope_odd_kernel<false, 1>)<<<grid, 32, 0, stream>>>(np, splits);
+    launch(norm_rope_odd_kernel<false, 1>, norm_rope_odd_kernel<true, 1>);
   else if (p.interleaved)
-    (p.f16 ? norm_rope_kernel<true, true>
-           : norm_rope_kernel<false, true>)<<<grid, 32, 0, stream>>>(np, splits);
+    launch(norm_rope_kernel<false, true>, norm_rope_kernel<true, true>);
   else
-    (p.f16 ? norm_rope_kernel<true, false>
-           : norm_rope_kernel<false, false>)<<<grid, 32, 0, stream>>>(np, splits);
+    launch(norm_rope_kernel<false, false>, norm_rope_kernel<true, false>);
   return cudaGetLastError();
 }
 
