@@ -28,6 +28,7 @@
 // (log-sum-exp over partial states, by the last CTA to arrive).
 // Every wait is bounded; one that runs out sets flag 0x4 and the CTA winds down.
 #include <cstdint>
+#include <type_traits>
 
 #include <cuda_runtime.h>
 
@@ -59,6 +60,7 @@ template <int DK, int DVC, int VH, int TT, bool ONE>
 struct Tree {
   static constexpr int DV = DVC * VH;
   static constexpr int KPT = 128 / TT;              // loader threads a token
+  static constexpr int BT = TT / 4;                 // tokens of a softmax thread's block
   static constexpr int KSEG = DK / 2 / KPT, VSEG = DVC / 2 / KPT;     // packed bytes of each
   static constexpr int KSF = DK / 16 / KPT, VSF = DVC / 16 / KPT;     // scale bytes of each
   static constexpr int KW = 32 * (KSEG + KSF), VW = 32 * (VSEG + VSF);  // a warp's stage
@@ -118,10 +120,10 @@ __device__ __forceinline__ float4 peer_v4(uint32_t a) {
   return v;
 }
 
-__device__ __forceinline__ void sts_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z,
-                                       uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z),
-               "r"(w)
+__device__ __forceinline__ void sts_v4(uint32_t a, int off, uint32_t x, uint32_t y, uint32_t z,
+                                       uint32_t w) {  // (off: a constant once unrolled)
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(a + off), "r"(x), "r"(y),
+               "r"(z), "r"(w)
                : "memory");
 }
 // a token's scales: 4, 8 or 16 bytes
@@ -222,7 +224,10 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
       scales[k] = lds_u32(st + 32 * SEG + lane * SF + 4 * k);
       if (past) scales[k] = 0;
     }
-    const uint32_t out = row + b * BYTES;
+    uint32_t out[8];  // the row's chunk c of each block of 64 dims
+#pragma unroll
+    for (int c8 = 0; c8 < 8; ++c8)
+      out[c8] = (row + b * BYTES + (2 * SEG / 64 * seg) * (TT * 128)) ^ (c8 << 4);
 #pragma unroll
     for (int k = 0; k < LPR; ++k) {
       const uint4 q = lds_v4(st + lane * SEG + 16 * raw_chunk<SEG>(lane, k));
@@ -236,8 +241,8 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
         const uint32_t s = e < 2 ? lo : hi;
         const int d = 32 * k + 8 * e;  // first of the 8 dims, from the thread's first
         static_assert(2 * SEG % 64 == 0, "a thread's dims fill blocks of 64");
-        sts_v4((out + (2 * SEG / 64 * seg + d / 64) * (TT * 128)) ^ (d % 64 / 8 << 4), hmul2(h[0], s),
-               hmul2(h[1], s), hmul2(h[2], s), hmul2(h[3], s));
+        sts_v4(out[d % 64 / 8], d / 64 * (TT * 128), hmul2(h[0], s), hmul2(h[1], s),
+               hmul2(h[2], s), hmul2(h[3], s));
       }
     }
     fence_async_smem();
@@ -257,7 +262,6 @@ template <int DK, int DVC, int VH, int TT, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendParams p) {
   using T = Tree<DK, DVC, VH, TT, ONE>;
   constexpr int KB = T::KB, VB = T::VB, DV = T::DV;
-  constexpr int W = TT / 2;      // tokens of a tile that a softmax thread has
   constexpr float kLn2 = 0.69314718055994530942f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -288,6 +292,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
   if (row0 >= R) return;  // the whole cluster, before any barrier or tensor memory use
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nrows = min(kRows, R - row0);
+  // Up to 64 rows are held twice: the copies share each half's tokens, so that all warps
+  // work (16 requests of 512-4096 tokens x 64 rows 48 -> 41 us).
+  const int rows_held = nrows <= kRows / 2 ? kRows / 2 : kRows;
   // this CTA's tiles of the unit; tokens from tok_end on do not exist
   const int tok_end = min(u.kv_len, u.tok_begin + p.page_size * u.num_pages);
   const int all_tiles = (tok_end - u.tok_begin + TT - 1) / TT;
@@ -375,8 +382,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
         const uint64_t vd = vd0 + ((b * T::VBYTES) >> 4);
 #pragma unroll
         for (int k = 0; k < TT / 16; ++k) {
-          const int h = ONE ? 0 : k / (W / 16);  // the half whose tokens these are
-          const bool first = ONE ? k == 0 : k % (W / 16) == 0;
+          const int h = ONE ? 0 : 16 * k / T::BT & 1;  // the half whose tokens these are
+          const bool first = ONE ? k == 0 : 16 * k == h * T::BT;
           umma_ts(tmem + T::OCOL + h * DVC, tmem + T::PCOL + 8 * k, vd + ((k * 2048) >> 4),
                   T::IDESC_O, (i > 0 || !first) ? 1u : 0u);
         }
@@ -395,8 +402,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
     // ================= softmax (thread = row, half of a tile's tokens) ===========
     const int q4 = warp & 3, half = warp >> 2, r = 32 * q4 + lane;
     const uint32_t lane_base = (uint32_t)(32 * q4) << 16;
-    const bool active = 32 * q4 < nrows, real = r < nrows;  // warp-uniform; this row
-    const int gr = row0 + (real ? r : 0), node = gr / G;
+    const int copy = r / rows_held;  // of the row (0 where rows are not held twice)
+    const int row_r = r - copy * rows_held;
+    const bool active = 32 * q4 - copy * rows_held < nrows;  // warp-uniform
+    const bool real = row_r < nrows;
+    const int gr = row0 + (real ? row_r : 0), node = gr / G;
     // ---- Q: bf16 -> f16 times a power of two per row, into tensor memory ----------
     float f = 0.f;
     {
@@ -423,7 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
         if (am > 0.f) e = 14 - (int)((__float_as_uint(am) >> 23) & 0xFF) + 127;
         e = max(-120, min(120, e));
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        f = real ? p.qk_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23) : 0.f;
+        // (above 0: it multiplies the -inf of tokens that are not seen)
+        f = real ? fmaxf(p.qk_scale_log2 * __uint_as_float((uint32_t)(127 - e) << 23), 0x1p-126f)
+                 : 0.f;
 #pragma unroll 2
         for (int c = 0; c < DK / 64; ++c) {  // 16 columns of two dims
           uint32_t h[16];
@@ -447,24 +459,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
     // ---- the tiles ---------------------------------------------------------------------
     const int before = u.kv_len - u.qo_len;  // tokens that every row sees
     const uint32_t* words = p.tree_mask + (int64_t)(u.qo_begin + node) * p.tree_words;
-    auto word = [&](int k) -> uint64_t {
-      return k >= 0 && k < p.tree_words ? __ldg(words + k) : 0u;
-    };
-    // bit t: whether the row sees token tok + t
-    auto visible = [&](int tok) -> uint64_t {
+    auto word = [&](int k) -> uint32_t { return k < p.tree_words ? __ldg(words + k) : 0u; };
+    // bit t: whether the row sees token tok + t (t < 32)
+    auto visible = [&](int tok) -> uint32_t {
       const int j = tok - before, n = tok_end - tok;
-      uint64_t v;
-      if (j <= -64) {
-        v = ~0ull;
+      uint32_t v;
+      if (j <= -32) {
+        v = ~0u;
       } else if (j < 0) {
-        v = (word(0) | word(1) << 32) << -j | ((1ull << -j) - 1);
+        v = word(0) << -j | ((1u << -j) - 1);
       } else {
-        const int k = j >> 5, s = j & 31;
-        v = (word(k) | word(k + 1) << 32) >> s;
-        if (s) v |= word(k + 2) << (64 - s);
+        v = __funnelshift_r(word(j >> 5), word((j >> 5) + 1), j & 31);
       }
-      if (n < 64) v = n <= 0 ? 0ull : v & ((1ull << n) - 1);
-      return real ? v : 0ull;
+      if (n < 32) v = n <= 0 ? 0u : v & ((1u << n) - 1);
+      return real ? v : 0u;
     };
     // the maximum (log2; ONE: of the row, else of this half's tokens), -m once there is one
     float m = -INFINITY, nm = 0.f;
@@ -475,107 +483,127 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
       wait_soon<16>(bar, parity, s_abort, p.flags);
       __syncwarp();
     };
-    for (int i = 0; i < ntiles; ++i) {
-      if (!active) {
-        // (nothing to do for the rows that are not there but to keep the counts)
+    // A half has two blocks of a tile's tokens, the first and the third quarter or the second
+    // and the fourth.  NB: the blocks that this thread looks at, from block b0.
+    constexpr int BT = T::BT;
+    auto tiles = [&](auto blocks) {
+      constexpr int NB = decltype(blocks)::value;
+      const int b0 = NB == 1 ? copy : 0;
+      for (int i = 0; i < ntiles; ++i) {
+        const int tok = u.tok_begin + (t0 + i) * TT + b0 * (TT / 2) + half * BT;
+        const bool masked = u.tok_begin + (t0 + i + 1) * TT > some_hidden;
+        uint32_t see[NB];
+        if (masked) {
+#pragma unroll
+          for (int k = 0; k < NB; ++k) see[k] = visible(tok + k * (TT / 2));
+        }
+        wait(s_full, i & 1);
+        tc_fence_after();
+        uint32_t x[NB * BT];
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+          tmem_ld<BT>(tmem + lane_base + T::SCOL + (b0 + k) * (TT / 2) + half * BT, x + k * BT);
+        tmem_wait_ld<NB * BT>(x);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(s_empty);
+        if (masked) {
+#pragma unroll
+          for (int e = 0; e < NB * BT; ++e)
+            if (!(see[e / BT] >> (e % BT) & 1u)) x[e] = 0xff800000u;  // -inf
+        }
+        // the largest score (f > 0, so that of the sums); f = 0 for rows that are not there
+        float mx[4] = {__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]),
+                       __uint_as_float(x[3])};
+#pragma unroll
+        for (int e = 4; e + 7 < NB * BT; e += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx[k] = fmax3(mx[k], __uint_as_float(x[e + 2 * k]), __uint_as_float(x[e + 2 * k + 1]));
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(x[NB * BT - 4 + k]));
+        float top = fmaf(fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]), f, nm);
+        bool raise = top > thr;
+        if constexpr (ONE)
+          raise = named_or(1 + q4, 64, raise);
+        else
+          raise = __any_sync(0xffffffffu, raise);
+        if (raise) {
+          // ---- raise the maxima to this tile's ---------------------------------------
+          if constexpr (ONE) {
+            s_x[half * kRows + r] = top;
+            named_sync(1 + q4, 64);
+            top = fmaxf(top, s_x[(half ^ 1) * kRows + r]);
+          }
+          float corr = 1.f;
+          if (real && top != -INFINITY && (m == -INFINITY || top > 0.f)) {
+            if (m != -INFINITY) corr = ex2(-top);
+            m = (m == -INFINITY ? 0.f : m) + top;
+            nm = -m;
+            thr = kRaise;
+          }
+          if (i > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
+            float a, b;
+            unpack_f32x2(add_f32x2(lsum[0], lsum[1]), a, b);
+            lsum[0] = pack_f32x2((a + b) * corr, 0.f);
+            lsum[1] = 0;
+            wait(pv_done, (i - 1) & 1);
+            tc_fence_after();
+            constexpr int OD = ONE ? DVC / 2 : DVC;  // the dims that are this thread's to scale
+#pragma unroll 1
+            for (int c = 0; c < OD / 16; ++c) {
+              uint32_t ov[16];
+              const uint32_t oa = tmem + lane_base + T::OCOL + half * OD + 16 * c;
+              tmem_ld16(oa, ov);
+              tmem_wait_ld<16>(ov);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
+              tmem_st16(oa, ov);
+            }
+          }
+        }
+        // ---- p = 2^(score - m) ----------------------------------------------------------
+        uint32_t h[NB * BT / 2];
+        {
+          const uint64_t f2 = pack_f32x2(f, f), n2 = pack_f32x2(nm, nm);
+#pragma unroll
+          for (int e = 0; e < NB * BT / 2; ++e) {
+            float a, b;
+            unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[2 * e]),
+                                              __uint_as_float(x[2 * e + 1])), f2, n2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            lsum[e & 1] = add_f32x2(lsum[e & 1], pack_f32x2(a, b));
+            h[e] = f32x2_to_f16x2(a, b);
+          }
+        }
+        if (i > 0) wait(pv_done, (i - 1) & 1);  // P's columns are free
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+          tmem_st<BT / 2>(tmem + lane_base + T::PCOL + (b0 + k) * (TT / 4) + half * (BT / 2),
+                          h + k * (BT / 2));
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+      }
+    };
+    if (!active) {
+      // (nothing to do for the rows that are not there but to keep the counts)
+      for (int i = 0; i < ntiles; ++i) {
         wait(s_full, i & 1);
         if (lane == 0) mbar_arrive(s_empty);
         if (i > 0) wait(pv_done, (i - 1) & 1);  // (an arrival counts for the phase that is open)
         if (lane == 0) mbar_arrive(p_full);
-        continue;
       }
-      const int tok = u.tok_begin + (t0 + i) * TT + half * W;
-      const bool masked = u.tok_begin + (t0 + i + 1) * TT > some_hidden;
-      uint64_t see = ~0ull;
-      if (masked) see = visible(tok);
-      wait(s_full, i & 1);
-      tc_fence_after();
-      uint32_t x[W];
-      tmem_ld<W>(tmem + lane_base + T::SCOL + W * half, x);
-      tmem_wait_ld<W>(x);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(s_empty);
-      if (masked) {
-#pragma unroll
-        for (int e = 0; e < W; ++e)
-          if (!((e < 32 ? (uint32_t)see : (uint32_t)(see >> 32)) >> (e & 31) & 1u))
-            x[e] = 0xff800000u;  // -inf
-      }
-      // the largest score (f > 0, so that of the sums); f = 0 for rows that are not there
-      float mx[4] = {__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]),
-                     __uint_as_float(x[3])};
-#pragma unroll
-      for (int e = 4; e + 7 < W; e += 8)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mx[k] = fmax3(mx[k], __uint_as_float(x[e + 2 * k]), __uint_as_float(x[e + 2 * k + 1]));
-#pragma unroll
-      for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(x[W - 4 + k]));
-      float top = fmaf(fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]), f, nm);
-      bool raise = top > thr;
-      if constexpr (ONE)
-        raise = named_or(1 + q4, 64, raise);
-      else
-        raise = __any_sync(0xffffffffu, raise);
-      if (raise) {
-        // ---- raise the maxima to this tile's -----------------------------------------
-        if constexpr (ONE) {
-          s_x[half * kRows + r] = top;
-          named_sync(1 + q4, 64);
-          top = fmaxf(top, s_x[(half ^ 1) * kRows + r]);
-        }
-        float corr = 1.f;
-        if (real && top != -INFINITY && (m == -INFINITY || top > 0.f)) {
-          if (m != -INFINITY) corr = ex2(-top);
-          m = (m == -INFINITY ? 0.f : m) + top;
-          nm = -m;
-          thr = kRaise;
-        }
-        if (i > 0 && __any_sync(0xffffffffu, corr != 1.f)) {
-          float a, b;
-          unpack_f32x2(add_f32x2(lsum[0], lsum[1]), a, b);
-          lsum[0] = pack_f32x2((a + b) * corr, 0.f);
-          lsum[1] = 0;
-          wait(pv_done, (i - 1) & 1);
-          tc_fence_after();
-          constexpr int OD = ONE ? DVC / 2 : DVC;  // the dims that are this thread's to scale
-#pragma unroll 1
-          for (int c = 0; c < OD / 16; ++c) {
-            uint32_t ov[16];
-            const uint32_t oa = tmem + lane_base + T::OCOL + half * OD + 16 * c;
-            tmem_ld16(oa, ov);
-            tmem_wait_ld<16>(ov);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
-            tmem_st16(oa, ov);
-          }
-        }
-      }
-      // ---- p = 2^(score - m) ------------------------------------------------------------
-      uint32_t h[W / 2];
-      {
-        const uint64_t f2 = pack_f32x2(f, f), n2 = pack_f32x2(nm, nm);
-#pragma unroll
-        for (int e = 0; e < W / 2; ++e) {
-          float a, b;
-          unpack_f32x2(fma_f32x2(pack_f32x2(__uint_as_float(x[2 * e]),
-                                            __uint_as_float(x[2 * e + 1])), f2, n2), a, b);
-          a = ex2(a);
-          b = ex2(b);
-          lsum[e & 1] = add_f32x2(lsum[e & 1], pack_f32x2(a, b));
-          h[e] = f32x2_to_f16x2(a, b);
-        }
-      }
-      if (i > 0) wait(pv_done, (i - 1) & 1);  // P's columns are free
-      tc_fence_after();
-#pragma unroll
-      for (int c = 0; c < W / 32; ++c)
-        tmem_st16(tmem + lane_base + T::PCOL + (W / 2) * half + 16 * c, h + 16 * c);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_full);
+    } else if (rows_held < kRows) {
+      // the other copy's block: its weights are 0 for this row
+      uint32_t zero[BT / 2] = {};
+      tmem_st<BT / 2>(tmem + lane_base + T::PCOL + (1 - copy) * (TT / 4) + half * (BT / 2), zero);
+      tiles(std::integral_constant<int, 1>{});
+    } else {
+      tiles(std::integral_constant<int, 2>{});
     }
     // ---- the CTA's state: sums of the halves, then O ------------------------------------
     if (active) {
@@ -626,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
                    (w[1] != 0.f ? __uint_as_float(ow[e]) * w[1] : 0.f);
         }
       };
-      if (parts == 1) {
+      if (parts == 1 && rows_held == kRows) {
         const bool partial = p.split && u.num_splits > 1;
         const float scale = any ? p.v_scale / l : 0.f;
         const float lse = any ? (m + log2f(l)) * kLn2 : -INFINITY;
@@ -687,44 +715,52 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
     tmem_dealloc(tmem, T::TCOLS);
   }
   const bool partial = p.split && u.num_splits > 1;
-  if (parts > 1) {
-    // ---- join the states of the cluster's CTAs, a share of the rows each ------------------
+  const int copies = kRows / rows_held;
+  if (parts * copies > 1) {
+    // ---- join the states of the rows' copies in the cluster's CTAs, a share of the rows each
     __syncwarp();
-    cluster_arrive_wait();
-    constexpr int DQ = DVC / 4;
-    const int share = kRows / parts, first = part * share, rows = min(share, nrows - first);
+    if (parts > 1) cluster_arrive_wait();
+    constexpr int DQ = DVC / 4, MB = 4;
+    const int share = (rows_held + parts - 1) / parts, first = part * share;
+    const int rows = min(share, nrows - first);
     const uint32_t so = smem_addr(smem), sm = smem_addr(s_m), sl = smem_addr(s_l);
     for (int idx = tid; idx < rows * DQ; idx += kThreads) {
       const int rr = first + idx / DQ, d = 4 * (idx % DQ);
-      float mt[8], lt[8], M = -INFINITY;
-      float4 ot[8];
-#pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        if (t >= parts) break;
-        const uint32_t at = t * VH + vh;
-        mt[t] = peer_f32(peer(sm + 4 * rr, at));
-        lt[t] = peer_f32(peer(sl + 4 * rr, at));
-        ot[t] = peer_v4(peer(so + 4 * (rr * T::OROW + d), at));
-      }
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-        if (t < parts) M = fmaxf(M, mt[t]);
-      float L = 0.f;
+      float M = -INFINITY, L = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (M != -INFINITY) {
+      for (int s0 = 0; s0 < parts * copies; s0 += MB) {
+        float ms[MB], ls[MB], top = M;
+        float4 os[MB];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          if (t >= parts || mt[t] == -INFINITY) continue;
-          const float w = ex2(mt[t] - M);
-          L = fmaf(lt[t], w, L);
-          o.x = fmaf(ot[t].x, w, o.x);
-          o.y = fmaf(ot[t].y, w, o.y);
-          o.z = fmaf(ot[t].z, w, o.z);
-          o.w = fmaf(ot[t].w, w, o.w);
+        for (int k = 0; k < MB; ++k) {
+          ms[k] = -INFINITY;
+          if (s0 + k >= parts * copies) continue;
+          const uint32_t at = (s0 + k) / copies * VH + vh;
+          const int row = rr + (s0 + k) % copies * rows_held;
+          ms[k] = peer_f32(peer(sm + 4 * row, at));
+          ls[k] = peer_f32(peer(sl + 4 * row, at));
+          os[k] = peer_v4(peer(so + 4 * (row * T::OROW + d), at));
         }
-        const float inv = p.v_scale / L;
-        o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
+#pragma unroll
+        for (int k = 0; k < MB; ++k) top = fmaxf(top, ms[k]);
+        if (top == -INFINITY) continue;
+        const float cf = ex2(M - top);  // 0 for -inf
+        L *= cf;
+        o.x *= cf; o.y *= cf; o.z *= cf; o.w *= cf;
+#pragma unroll
+        for (int k = 0; k < MB; ++k) {
+          if (ms[k] == -INFINITY) continue;
+          const float w = ex2(ms[k] - top);
+          L = fmaf(ls[k], w, L);
+          o.x = fmaf(os[k].x, w, o.x);
+          o.y = fmaf(os[k].y, w, o.y);
+          o.z = fmaf(os[k].z, w, o.z);
+          o.w = fmaf(os[k].w, w, o.w);
+        }
+        M = top;
       }
+      const float inv = M == -INFINITY ? 0.f : p.v_scale / L;
+      o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
       const float lse = M == -INFINITY ? M : (M + log2f(L)) * kLn2;
       const int gr = row0 + rr, node = gr / G, head = u.h_kv * G + gr % G;
       const int64_t row = (int64_t)(u.qo_begin + node) * p.num_qo_heads + head;
@@ -739,8 +775,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
         if (d == 0 && vh == 0 && p.lse) p.lse[row] = lse;
       }
     }
-    __syncwarp();
-    cluster_arrive_wait();  // no CTA ends while another reads its state
+    if (parts > 1) {
+      __syncwarp();
+      cluster_arrive_wait();  // no CTA ends while another reads its state
+    }
   }
   if (!partial) return;
   // ---- the last CTA of the request's units to arrive folds their states --------------------

@@ -29,14 +29,14 @@ def bits(mask, n, total):
 
 
 def tree_case(kv, new, hq, hkv, dk, dv, page=16, layout="HND", out="bf16", seed=0, masks=None,
-              words=None, only=None, live=None, q_pad=0, g=(0.75, 1.25), **plan_kw):
+              words=None, only=None, live=None, q_pad=0, g=(0.75, 1.25), q_scale=1.0, **plan_kw):
     """Run and check.  Beside the output's own rounding: a weight is rounded to f16
     (2^-11, at least 2^-25 of the row's largest) in the product and in the row sum; the
     scores' sums err by Dk 2^-23 of sum |q k| (`reach`) at most, and what follows by
     2^-21; an error d of a score is one of d of a weight and of the sum."""
     c = T.Nvfp4Case(kv, page, hkv, dk, dv, layout, seed=seed, g=g)
     gen = torch.Generator().manual_seed(seed)
-    q = torch.randn((sum(new) + 1, hq + q_pad, dk), generator=gen).to(torch.bfloat16)
+    q = (torch.randn((sum(new) + 1, hq + q_pad, dk), generator=gen) * q_scale).to(torch.bfloat16)
     q = q.cuda()[:, q_pad:]
     rng = np.random.default_rng(seed + 1)
     qo = np.concatenate([[0], np.cumsum(new)])
@@ -129,6 +129,16 @@ def test_masks_of_any_kind(kernel, hq, hkv):
     assert (out[7] == 0).all() and (out[11] == 0).all()
 
 
+@pytest.mark.parametrize("rows", [17, 32, 33, 63, 64, 65, 96, 127, 128, 129, 200])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (256, 256), (512, 256)])
+def test_rows_of_a_block(rows, dk, dv):
+    """Row counts around the warps, the copies and the blocks of the wide kernel, one head a
+    kv head, with and without a split."""
+    for chunk in (0, 64):
+        tree_case((rows, 300), (rows, min(rows, 70)), 1, 1, dk, dv, seed=rows,
+                  force_chunk_tokens=chunk)
+
+
 @pytest.mark.parametrize("kernel", [1, 3])
 def test_tokens_past_the_words_are_not_seen(kernel):
     masks = [np.full((50, 1), -1, dtype=np.int32), np.full((3, 1), -1, dtype=np.int32)]
@@ -148,6 +158,15 @@ def test_values_of_all_sizes(kernel):
     """Global scales far from 1 (scores stay in range by the query)."""
     tree_case((70, 200), (9, 30), 4, 2, 128, 128, kernel=kernel, g=(0.75, 2.0 ** -60), seed=8)
     tree_case((70, 200), (9, 30), 4, 2, 128, 128, kernel=kernel, g=(2.0 ** -30, 2.0 ** 60), seed=9)
+
+
+@pytest.mark.parametrize("kernel", [1, 3])
+@pytest.mark.parametrize("q_scale", [2.0 ** -120, 2.0 ** -60, 0.0, 2.0 ** 60])
+def test_queries_of_all_sizes(kernel, q_scale):
+    """Scores that vanish (every key that is seen weighs the same, none of the others does)
+    and scores kept in range by the cache's scale."""
+    tree_case((70, 200, 9), (9, 30, 9), 4, 2, 128, 128, kernel=kernel, q_scale=q_scale, seed=16,
+              g=(2.0 ** -64, 1.25))
 
 
 def test_a_chain_is_the_causal_mask():
