@@ -45,8 +45,7 @@ using namespace dev;
 using namespace tc5;
 
 constexpr int kRows = 128;
-constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;  // of K, and of V
-constexpr int kThreads = 32 * (kSoftmaxWarps + 2 * kLoadWarps + 2);
+constexpr int kSoftmaxWarps = 8;
 constexpr float kRaise = 8.f;  // log2 of the largest p before m is raised
 // Test build only: the first K loader of CTA (0, 0) withholds its arrival for the first
 // tile, so the issuer's wait runs out and the CTA winds down.
@@ -59,12 +58,15 @@ constexpr float kRaise = 8.f;  // log2 of the largest p before m is raised
 template <int DK, int DVC, int VH, int TT, bool ONE>
 struct Tree {
   static constexpr int DV = DVC * VH;
-  static constexpr int KPT = 128 / TT;              // loader threads a token
+  // loader threads of a token's K and V: 64 or 128 dims each
+  static constexpr int KP = DK > 128 ? DK / 128 : 1, VP = DVC > 128 ? DVC / 128 : 1;
+  static constexpr int KLW = TT * KP / 32, VLW = TT * VP / 32;  // loader warps
+  static constexpr int THREADS = 32 * (kSoftmaxWarps + KLW + VLW + 2);
   static constexpr int BT = TT / 4;                 // tokens of a softmax thread's block
-  static constexpr int KSEG = DK / 2 / KPT, VSEG = DVC / 2 / KPT;     // packed bytes of each
-  static constexpr int KSF = DK / 16 / KPT, VSF = DVC / 16 / KPT;     // scale bytes of each
+  static constexpr int KSEG = DK / 2 / KP, VSEG = DVC / 2 / VP;       // packed bytes of each
+  static constexpr int KSF = DK / 16 / KP, VSF = DVC / 16 / VP;       // scale bytes of each
   static constexpr int KW = 32 * (KSEG + KSF), VW = 32 * (VSEG + VSF);  // a warp's stage
-  static constexpr int STAGE = kLoadWarps * (KW + VW);
+  static constexpr int STAGE = KLW * KW + VLW * VW;
   static constexpr int KBYTES = TT * DK * 2, VBYTES = TT * DVC * 2;   // operand tiles
   static constexpr int KB = 2, VB = DK == 512 ? 2 : 3;
   static constexpr int RS = DK == 512 ? 2 : DK == 128 ? 3 : 4;
@@ -95,6 +97,15 @@ __device__ __forceinline__ bool wait_soon(uint64_t* bar, uint32_t parity, volati
   for (int k = 0; k < SPINS; ++k)
     if (mbar_test_wait(bar, parity)) return true;
   return wait_bar(bar, parity, abort, flags);
+}
+// One lane of a warp that is there as a whole.  What it then runs counts as uniform: the
+// descriptors of its products stay in uniform registers (issued behind lane == 0 instead, a
+// product takes 80 to 100 cycles, 64 tokens x 16 dims 32).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(one));
+  return one != 0;
 }
 __device__ __forceinline__ void cluster_arrive_wait() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n"
@@ -148,21 +159,24 @@ __device__ __forceinline__ int raw_chunk(int r, int c) {
 template <class T, int TT, bool V>
 __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit& u, int w,
                                            int lane, int t0, int ntiles, int tok_end, int vh,
-                                           uint8_t* raw, uint8_t* tiles, uint64_t* full,
-                                           uint64_t* empty, volatile int* abort) {
+                                           uint8_t* smem, int q_stage, uint64_t* full,
+                                           uint64_t* empty, uint64_t* q_full,
+                                           volatile int* abort) {
   constexpr int SEG = V ? T::VSEG : T::KSEG, SF = V ? T::VSF : T::KSF;
   constexpr int BYTES = V ? T::VBYTES : T::KBYTES, NB = V ? T::VB : T::KB, RS = T::RS;
   constexpr int LPR = SEG / 16, RPI = 32 / LPR;  // lanes a row, rows a copy instruction
   const CacheView& c = p.cache;
-  const int seg = T::KPT == 1 ? 0 : w >> 1;       // part of the row's dims
-  const int first = T::KPT == 1 ? 32 * w : 32 * (w & 1);  // this warp's first token of a tile
+  const int seg = w / (TT / 32);           // part of the row's dims
+  const int first = 32 * (w % (TT / 32));  // this warp's first token of a tile
   const int shift = p.page_size == 1 ? 0 : 4, slots = (1 << shift) - 1;
   const int64_t sp = V ? c.v_sp : c.k_sp, ss = V ? c.v_ss : c.k_ss;
   const int64_t fsp = V ? c.vsf_sp : c.ksf_sp, fss = V ? c.vsf_ss : c.ksf_ss;
-  const int part = V ? vh * T::KPT + seg : seg;   // the warp's part of the whole row
+  const int part = V ? vh * T::VP + seg : seg;   // the warp's part of the whole row
   const uint8_t* data = (V ? c.v_data + u.h_kv * c.v_sh : c.k_data + u.h_kv * c.k_sh) + part * SEG;
   const uint8_t* sf = (V ? c.v_sf + u.h_kv * c.vsf_sh : c.k_sf + u.h_kv * c.ksf_sh) + part * SF;
-  const uint32_t mine = smem_addr(raw) + w * (V ? T::VW : T::KW);
+  constexpr int TILES = V ? T::OFF_V : T::OFF_K;
+  const uint32_t mine = smem_addr(smem) + T::OFF_RAW +
+                        (V ? T::KLW * T::KW + w * T::VW : w * T::KW);
   const int r0 = lane / LPR, ch = lane % LPR;
   // page id of this lane's token in tile i, a tile ahead of its use (where it is checked);
   // a token past the unit's pages takes the last one
@@ -202,7 +216,11 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
   int32_t next = load_pid(RS - 1);
   const int tl = first + lane;  // this lane's token of a tile
   // its row, whose 16-byte chunks are xor-ed with the row's number
-  const uint32_t row = smem_addr(tiles) + (tl >> 3) * 1024 + (tl & 7) * 128 + ((tl & 7) << 4);
+  const uint32_t row = smem_addr(smem) + TILES + (tl >> 3) * 1024 + (tl & 7) * 128 + ((tl & 7) << 4);
+  // (Q's rows lie at the end of the operand tiles until they are read)
+  if (ntiles > 0 && TILES + NB * BYTES > q_stage &&
+      !__all_sync(0xffffffffu, wait_bar(q_full, 0, abort, p.flags)))
+    ntiles = 0;
   for (int i = 0, b = 0, round = 0; i < ntiles; ++i) {
     const int32_t pid = next;
     next = load_pid(i + RS);
@@ -259,9 +277,11 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
 }
 
 template <int DK, int DVC, int VH, int TT, bool ONE>
-__global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(Tree<DK, DVC, VH, TT, ONE>::THREADS, 1)
+    attend_tree_kernel(const AttendParams p) {
   using T = Tree<DK, DVC, VH, TT, ONE>;
-  constexpr int KB = T::KB, VB = T::VB, DV = T::DV;
+  constexpr int KB = T::KB, VB = T::VB, DV = T::DV, kThreads = T::THREADS;
+  constexpr int kKWarp = kSoftmaxWarps, kVWarp = kKWarp + T::KLW, kSWarp = kVWarp + T::VLW;
   constexpr float kLn2 = 0.69314718055994530942f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
@@ -285,29 +305,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
   float* s_l = s_m + kRows;       // [128] sums of the CTA's state
 
   const WorkUnit u = load_unit(p);
-  const int G = p.group, R = G * u.qo_len, C = p.tree_ctas;
-  const int block = blockIdx.y / C, rank = blockIdx.y % C;
-  const int vh = rank % VH, part = rank / VH, parts = C / VH;
-  const int row0 = block * kRows;
-  if (row0 >= R) return;  // the whole cluster, before any barrier or tensor memory use
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nrows = min(kRows, R - row0);
-  // Up to 64 rows are held twice: the copies share each half's tokens, so that all warps
-  // work (16 requests of 512-4096 tokens x 64 rows 48 -> 41 us).
-  const int rows_held = nrows <= kRows / 2 ? kRows / 2 : kRows;
-  // this CTA's tiles of the unit; tokens from tok_end on do not exist
-  const int tok_end = min(u.kv_len, u.tok_begin + p.page_size * u.num_pages);
-  const int all_tiles = (tok_end - u.tok_begin + TT - 1) / TT;
-  const int t0 = static_cast<int>((int64_t)all_tiles * part / parts);
-  const int ntiles = static_cast<int>((int64_t)all_tiles * (part + 1) / parts) - t0;
-
-  if (tid == 0) {
+  if (tid == 0) {  // (while the unit is on its way)
     for (int b = 0; b < KB; ++b) {
-      mbar_init(&k_full[b], kLoadWarps);
+      mbar_init(&k_full[b], T::KLW);
       mbar_init(&k_empty[b], 1);
     }
     for (int b = 0; b < VB; ++b) {
-      mbar_init(&v_full[b], kLoadWarps);
+      mbar_init(&v_full[b], T::VLW);
       mbar_init(&v_empty[b], 1);
     }
     mbar_init(s_full, 1);
@@ -320,9 +325,44 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
     mbar_init_fence();
     *s_abort = 0;
   }
-  if (warp == 0) {
+  if (warp == kSoftmaxWarps) {
     tmem_alloc(s_tmem, T::TCOLS);
     tmem_relinquish();
+  }
+  const int G = p.group, R = G * u.qo_len, C = p.tree_ctas;
+  const int block = blockIdx.y / C, rank = blockIdx.y % C;
+  const int vh = rank % VH, part = rank / VH, parts = C / VH;
+  const int row0 = block * kRows;
+  if (row0 >= R) {  // the whole cluster
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kSoftmaxWarps) tmem_dealloc(*s_tmem, T::TCOLS);
+    return;
+  }
+  const int nrows = min(kRows, R - row0);
+  // Up to 64 rows are held twice: the copies share each half's tokens, so that all warps
+  // work (16 requests of 512-4096 tokens x 64 rows 48 -> 41 us).
+  const int rows_held = nrows <= kRows / 2 ? kRows / 2 : kRows;
+  // this CTA's tiles of the unit; tokens from tok_end on do not exist
+  const int tok_end = min(u.kv_len, u.tok_begin + p.page_size * u.num_pages);
+  const int all_tiles = (tok_end - u.tok_begin + TT - 1) / TT;
+  const int t0 = static_cast<int>((int64_t)all_tiles * part / parts);
+  const int ntiles = static_cast<int>((int64_t)all_tiles * (part + 1) / parts) - t0;
+
+  // Q's rows on their way to tensor memory: whole lines at a time to shared memory, the end of
+  // the operand tiles' place, their 16-byte chunks xor-ed with the row's number (a
+  // thread's row straight from global memory would be a line a lane)
+  const int q_stage = T::OFF_RAW - nrows * (DK * 2);
+  if (warp < kSoftmaxWarps) {
+    constexpr int CH = DK / 8;
+    for (int idx = tid; idx < nrows * CH; idx += 32 * kSoftmaxWarps) {
+      const int rr = idx / CH, c = idx % CH, gr = row0 + rr, node = gr / G;
+      cp_async_16s(smem_addr(smem) + q_stage + rr * (DK * 2) + 16 * (c ^ (rr & 7)),
+                   p.q + (int64_t)(u.qo_begin + node) * p.q_stride_tok +
+                       (int64_t)(u.h_kv * G + gr - node * G) * p.q_stride_head + 8 * c);
+    }
+    cp_async_commit();
   }
   // fused append: the step's new tokens among this CTA's tiles, stored before any copy
   // reads them (CTAs that share tokens store the same bytes)
@@ -336,16 +376,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  if (warp >= kSoftmaxWarps && warp < kSoftmaxWarps + kLoadWarps) {
-    load_tiles<T, TT, false>(p, u, warp - kSoftmaxWarps, lane, t0, ntiles, tok_end, vh,
-                             smem + T::OFF_RAW, smem + T::OFF_K, k_full, k_empty, s_abort);
-  } else if (warp >= kSoftmaxWarps + kLoadWarps && warp < kSoftmaxWarps + 2 * kLoadWarps) {
-    load_tiles<T, TT, true>(p, u, warp - kSoftmaxWarps - kLoadWarps, lane, t0, ntiles, tok_end, vh,
-                            smem + T::OFF_RAW + kLoadWarps * T::KW, smem + T::OFF_V, v_full,
-                            v_empty, s_abort);
-  } else if (warp == kSoftmaxWarps + 2 * kLoadWarps) {
+  if (warp >= kKWarp && warp < kVWarp) {
+    load_tiles<T, TT, false>(p, u, warp - kKWarp, lane, t0, ntiles, tok_end, vh,
+                             smem, q_stage, k_full, k_empty, q_full, s_abort);
+  } else if (warp >= kVWarp && warp < kSWarp) {
+    load_tiles<T, TT, true>(p, u, warp - kVWarp, lane, t0, ntiles, tok_end, vh,
+                            smem, q_stage, v_full, v_empty, q_full, s_abort);
+  } else if (warp == kSWarp) {
     // ================= issue of S = Q K^T (one thread) =========================
-    if (lane == 0) {
+    if (elect_one()) {
       const uint64_t kd0 = smem_desc(smem_addr(smem + T::OFF_K), 16, 1024, kSwz128);
       bool ok = ntiles == 0 || wait_bar(q_full, 0, s_abort, p.flags);
       for (int i = 0, b = 0, round = 0; ok && i < ntiles; ++i) {
@@ -370,9 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
       drain_bar(&fin[0], 0, p.flags);
     }
     __syncwarp();
-  } else if (warp == kSoftmaxWarps + 2 * kLoadWarps + 1) {
+  } else if (warp == kSWarp + 1) {
     // ================= issue of O += P V (one thread) ===========================
-    if (lane == 0) {
+    if (elect_one()) {
       const uint64_t vd0 = smem_desc(smem_addr(smem + T::OFF_V), TT * 128, 1024, kSwz128);
       for (int i = 0, b = 0, round = 0; i < ntiles; ++i) {
         if (!wait_soon<64>(&v_full[b], round & 1, s_abort, p.flags) ||
@@ -410,11 +449,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
     // ---- Q: bf16 -> f16 times a power of two per row, into tensor memory ----------
     float f = 0.f;
     {
-      const uint16_t* q = p.q + (int64_t)(u.qo_begin + node) * p.q_stride_tok +
-                          (int64_t)(u.h_kv * G + gr % G) * p.q_stride_head + half * (DK / 2);
+      const uint32_t q = smem_addr(smem) + q_stage + (real ? row_r : 0) * (DK * 2);
       auto load = [&](int c) -> uint4 {
-        return real ? __ldg(reinterpret_cast<const uint4*>(q) + c) : make_uint4(0u, 0u, 0u, 0u);
+        return real ? lds_v4(q + 16 * ((half * (DK / 16) + c) ^ (row_r & 7)))
+                    : make_uint4(0u, 0u, 0u, 0u);
       };
+      cp_async_wait<0>();
+      named_sync(5, 32 * kSoftmaxWarps);
       float am = 0.f;
       if (active) {
 #pragma unroll 8
@@ -551,14 +592,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
             tc_fence_after();
             constexpr int OD = ONE ? DVC / 2 : DVC;  // the dims that are this thread's to scale
 #pragma unroll 1
-            for (int c = 0; c < OD / 16; ++c) {
-              uint32_t ov[16];
-              const uint32_t oa = tmem + lane_base + T::OCOL + half * OD + 16 * c;
-              tmem_ld16(oa, ov);
-              tmem_wait_ld<16>(ov);
+            for (int c = 0; c < OD / 8; ++c) {
+              uint32_t ov[8];
+              const uint32_t oa = tmem + lane_base + T::OCOL + half * OD + 8 * c;
+              tmem_ld8(oa, ov);
+              tmem_wait_ld<8>(ov);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
-              tmem_st16(oa, ov);
+              for (int e = 0; e < 8; ++e) ov[e] = __float_as_uint(__uint_as_float(ov[e]) * corr);
+              tmem_st8(oa, ov);
             }
           }
         }
@@ -710,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
 
   // ---- every role is done: release tensor memory ---------------------------------------
   __syncthreads();
-  if (warp == 0) {
+  if (warp == kSoftmaxWarps) {
     tc_fence_after();
     tmem_dealloc(tmem, T::TCOLS);
   }
@@ -720,60 +761,66 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tree_kernel(const AttendPa
     // ---- join the states of the rows' copies in the cluster's CTAs, a share of the rows each
     __syncwarp();
     if (parts > 1) cluster_arrive_wait();
-    constexpr int DQ = DVC / 4, MB = 4;
-    const int share = (rows_held + parts - 1) / parts, first = part * share;
+    const int n = parts * copies;  // states of a row (a power of two, at most 16)
+    const int share = rows_held / parts, first = part * share;  // n * share = kRows
     const int rows = min(share, nrows - first);
-    const uint32_t so = smem_addr(smem), sm = smem_addr(s_m), sl = smem_addr(s_l);
+    const uint32_t so = smem_addr(smem);
+    if (tid < kRows) {  // a lane a state: its weight in its row's result, to s_x
+      const int s = tid % n, rr = first + tid / n;
+      const int at = s / copies * VH + vh, row = rr + s % copies * rows_held;
+      const float m = peer_f32(peer(smem_addr(s_m) + 4 * row, at));
+      const float l = peer_f32(peer(smem_addr(s_l) + 4 * row, at));
+      float top = m;
+      for (int k = 1; k < n; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      const bool any = top != -INFINITY;
+      const float w = any ? ex2(m - top) : 0.f;  // 0 for m = -inf
+      float L = l * w;
+      for (int k = 1; k < n; k *= 2) L += __shfl_xor_sync(0xffffffffu, L, k);
+      s_x[tid] = any ? w * (p.v_scale / L) : 0.f;
+      if (s == 0 && vh == 0 && rr - first < rows) {
+        const float lse = any ? (top + log2f(L)) * kLn2 : -INFINITY;
+        const int gr = row0 + rr, node = gr / G, head = u.h_kv * G + gr % G;
+        const int64_t at_head = (int64_t)node * p.num_qo_heads + head;
+        if (partial)
+          p.partial_lse[u.partial_base + at_head * u.num_splits + u.split] = lse;
+        else if (p.lse)
+          p.lse[(int64_t)u.qo_begin * p.num_qo_heads + at_head] = lse;
+      }
+    }
+    __syncthreads();
+    constexpr int DQ = DVC / 4, MB = 4;
     for (int idx = tid; idx < rows * DQ; idx += kThreads) {
-      const int rr = first + idx / DQ, d = 4 * (idx % DQ);
-      float M = -INFINITY, L = 0.f;
+      const int rr = idx / DQ, d = 4 * (idx % DQ), gr = row0 + first + rr, node = gr / G;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s0 = 0; s0 < parts * copies; s0 += MB) {
-        float ms[MB], ls[MB], top = M;
+      for (int s0 = 0; s0 < n; s0 += MB) {
         float4 os[MB];
+        float w[MB];
 #pragma unroll
         for (int k = 0; k < MB; ++k) {
-          ms[k] = -INFINITY;
-          if (s0 + k >= parts * copies) continue;
-          const uint32_t at = (s0 + k) / copies * VH + vh;
-          const int row = rr + (s0 + k) % copies * rows_held;
-          ms[k] = peer_f32(peer(sm + 4 * row, at));
-          ls[k] = peer_f32(peer(sl + 4 * row, at));
+          if (s0 + k >= n) break;
+          const int at = (s0 + k) / copies * VH + vh;
+          const int row = first + rr + (s0 + k) % copies * rows_held;
+          w[k] = s_x[rr * n + s0 + k];
           os[k] = peer_v4(peer(so + 4 * (row * T::OROW + d), at));
         }
 #pragma unroll
-        for (int k = 0; k < MB; ++k) top = fmaxf(top, ms[k]);
-        if (top == -INFINITY) continue;
-        const float cf = ex2(M - top);  // 0 for -inf
-        L *= cf;
-        o.x *= cf; o.y *= cf; o.z *= cf; o.w *= cf;
-#pragma unroll
         for (int k = 0; k < MB; ++k) {
-          if (ms[k] == -INFINITY) continue;
-          const float w = ex2(ms[k] - top);
-          L = fmaf(ls[k], w, L);
-          o.x = fmaf(os[k].x, w, o.x);
-          o.y = fmaf(os[k].y, w, o.y);
-          o.z = fmaf(os[k].z, w, o.z);
-          o.w = fmaf(os[k].w, w, o.w);
+          if (s0 + k >= n) break;
+          o.x = fmaf(os[k].x, w[k], o.x);
+          o.y = fmaf(os[k].y, w[k], o.y);
+          o.z = fmaf(os[k].z, w[k], o.z);
+          o.w = fmaf(os[k].w, w[k], o.w);
         }
-        M = top;
       }
-      const float inv = M == -INFINITY ? 0.f : p.v_scale / L;
-      o.x *= inv; o.y *= inv; o.z *= inv; o.w *= inv;
-      const float lse = M == -INFINITY ? M : (M + log2f(L)) * kLn2;
-      const int gr = row0 + rr, node = gr / G, head = u.h_kv * G + gr % G;
-      const int64_t row = (int64_t)(u.qo_begin + node) * p.num_qo_heads + head;
-      if (partial) {
-        const int64_t pi = (int64_t)u.partial_base +
-                           ((int64_t)node * p.num_qo_heads + head) * u.num_splits + u.split;
-        *reinterpret_cast<float4*>(p.partial_o + pi * DV + vh * DVC + d) = o;
-        if (d == 0 && vh == 0) p.partial_lse[pi] = lse;
-      } else {
-        *reinterpret_cast<uint2*>(p.out + row * DV + vh * DVC + d) =
+      const int64_t at_head = (int64_t)node * p.num_qo_heads + u.h_kv * G + gr - node * G;
+      if (partial)
+        *reinterpret_cast<float4*>(
+            p.partial_o + (u.partial_base + at_head * u.num_splits + u.split) * DV + vh * DVC +
+            d) = o;
+      else
+        *reinterpret_cast<uint2*>(
+            p.out + ((int64_t)u.qo_begin * p.num_qo_heads + at_head) * DV + vh * DVC + d) =
             make_uint2(pack_out2(o.x, o.y, p.out_f16), pack_out2(o.z, o.w, p.out_f16));
-        if (d == 0 && vh == 0 && p.lse) p.lse[row] = lse;
-      }
     }
     if (parts > 1) {
       __syncwarp();
@@ -846,6 +893,7 @@ bool make_tree(TreeConfig* cfg) {
   cfg->smem_bytes = T::SMEM;
   cfg->value_parts = VH;
   cfg->tile_tokens = TT;
+  cfg->threads = T::THREADS;
   return true;
 }
 
@@ -867,7 +915,7 @@ cudaError_t launch_attend_tree(const TreeConfig& cfg, AttendParams p, int units,
   p.tree_ctas = ctas;
   cudaLaunchConfig_t lc{};
   lc.gridDim = dim3(units, row_blocks * ctas);
-  lc.blockDim = dim3(kThreads);
+  lc.blockDim = dim3(cfg.threads);
   lc.dynamicSmemBytes = cfg.smem_bytes;
   lc.stream = stream;
   cudaLaunchAttribute attr{};

@@ -278,7 +278,7 @@ cudaError_t launch_attend(const AttendConfig& cfg, const AttendParams& p,
 // blocks of 128: value_parts CTAs share the value dims.
 struct TreeConfig {
   const void* func;
-  int smem_bytes, value_parts, tile_tokens;
+  int smem_bytes, threads, value_parts, tile_tokens;
 };
 constexpr int kTreeRows = 128;
 bool attend_config_tree(int dk, int dv, TreeConfig* cfg);
