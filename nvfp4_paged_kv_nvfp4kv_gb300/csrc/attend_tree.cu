@@ -9,16 +9,18 @@
 //
 // One CTA takes up to 128 query rows on the M side of both products, so a tile of keys is
 // dequantised once for all of them and a softmax row belongs to two threads:
-//  * K loaders (4 warps) and V loaders (4 warps): cp.async of the packed rows and scales
-//    (a warp its own tokens, RS - 1 tiles ahead), then e2m1 -> f16 times the E4M3 block
-//    scale (exact) into the 128-byte-swizzled operand layouts in shared memory;
+//  * K and V loaders (a warp for each 32 tokens x 128 dims of a tile): cp.async of the packed
+//    rows and scales (a warp its own tokens, RS - 1 tiles ahead), then e2m1 -> f16 times the
+//    E4M3 block scale (exact) into the 128-byte-swizzled operand layouts in shared memory;
 //  * issue (two warps, one thread each): S = Q K^T (A = Q in tensor memory, N = TT tokens),
 //    and O += P V (A = P in tensor memory), each once its inputs are ready;
 //  * softmax (8 warps): thread = row and half of the tile's tokens, so the maximum and the
-//    sum need no shuffles; the two halves of a row meet in a barrier of their two warps
-//    once a tile.  m is raised only when a score exceeds it by 2^8 (then O is rescaled).
-//    Row sums are float32 of the unrounded p; P is rounded to f16 (2^-11), the operand's
-//    type.  A tile that reaches into the tree takes each row's 64 (32) bits at once.
+//    sum need no shuffles.  Each half has an O, a maximum and a sum of its own, joined at the
+//    end; where tensor memory has no room for that (ONE: 512 query dims), the halves share
+//    them and meet in a barrier of their two warps once a tile.  The maximum is raised only
+//    when a score exceeds it by 2^8 (then O is rescaled).  Sums are float32 of the unrounded
+//    p; P is rounded to f16 (2^-11), the operand's type.  A tile that reaches into the tree
+//    takes each row's 64 (32) bits at once.
 // Value dims beyond 128 go to another CTA (VH of them), which forms the same S.
 //
 // The plan splits long requests for its own row blocks; here a cluster of CTAs divides a
@@ -27,6 +29,17 @@
 // CTA stores a share of the rows.  Units of a split request fold as elsewhere
 // (log-sum-exp over partial states, by the last CTA to arrive).
 // Every wait is bounded; one that runs out sets flag 0x4 and the CTA winds down.
+//
+// Measured (replayed): 4 requests x 32771 tokens, 104 rows of 8 kv heads (128/128) 89 us, 630
+// TFLOP/s of the rows that are there; 16 requests of 512-4096 tokens x 64 rows 42 us; 8
+// requests of 2048-8192 tokens x 48-88 rows (512/256) 47 us.  Neither memory (1.7 TB/s) nor
+// the tensor cores (a third busy) are full: the softmax warps' chain of a tile (wait, load,
+// maximum, 2^x, store: 2300 cycles of 128 tokens) and, at 512 dims, the dequantisation bound
+// it, with half of the issue slots taken; of the 42 us, 12 are the wait for the longest unit
+// and 8 a CTA's start and end.  (Measured and not kept: products issued by the loaders' first
+// warps, which leaves 128 registers a thread, 53 / 120 / 64 us; barriers of their own for the
+// halves' S 44 / 92 / 47; the copies of the next tiles issued after a tile's arrival 43 / 92 /
+// 49; twice the CTAs, in two waves, 57 / 105 / 71.)
 #include <cstdint>
 #include <type_traits>
 
@@ -342,7 +355,7 @@ __global__ void __launch_bounds__(Tree<DK, DVC, VH, TT, ONE>::THREADS, 1)
   }
   const int nrows = min(kRows, R - row0);
   // Up to 64 rows are held twice: the copies share each half's tokens, so that all warps
-  // work (16 requests of 512-4096 tokens x 64 rows 48 -> 41 us).
+  // work (16 requests of 512-4096 tokens x 64 rows 48 -> 46 us).
   const int rows_held = nrows <= kRows / 2 ? kRows / 2 : kRows;
   // this CTA's tiles of the unit; tokens from tok_end on do not exist
   const int tok_end = min(u.kv_len, u.tok_begin + p.page_size * u.num_pages);

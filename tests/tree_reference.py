@@ -150,6 +150,28 @@ def tree_attention(q, k, v, hide, sm_scale):
     return out, lse, mean, reach, floor
 
 
+def check_tree(got, got_lse, want, dk, dtype):
+    """Rows of one request against `want` (of tree_attention).  Beside the output's own
+    rounding: a weight is rounded to f16 (2^-11, at least 2^-25 of the row's largest) in the
+    product and in the row sum; the scores' sums err by Dk 2^-23 of sum |q k| (`reach`) at
+    most, and what follows by 2^-21; an error d of a score is one of d of a weight and of
+    the sum."""
+    ref, rl, mean, reach, floor = want
+    eps = torch.finfo(dtype).eps / 2
+    delta = dk * 2.0 ** -23 * reach + 2.0 ** -21
+    tol = (eps * np.abs(ref) + (mean * (2.0 ** -10 + 2.0 ** -19 + 2 * delta[..., None])
+                                + 2.0 ** -25 * floor) * (1 + eps)
+           + float(torch.finfo(dtype).smallest_normal) * eps)
+    none = np.isinf(rl)
+    assert np.array_equal(got_lse == -np.inf, none)
+    assert (got[none] == 0).all()
+    err = np.abs(got - ref)
+    assert (err <= tol).all(), (float(err.max()), float((err / tol).max()))
+    lerr = np.abs(got_lse[~none] - rl[~none])
+    ltol = delta + 2.0 ** -11 + 2.0 ** -19 + np.abs(rl) * 2.0 ** -22
+    assert (lerr <= ltol[~none]).all(), lerr.max()
+
+
 # ---- accepted tokens -------------------------------------------------------------------
 def moved(case_pages, page, begin, path):
     """(target page, slot, source page, slot) of every accepted token of one request."""
