@@ -10,7 +10,7 @@
 // One CTA takes up to 128 query rows on the M side of both products, so a tile of keys is
 // dequantised once for all of them and a softmax row belongs to two threads:
 //  * K and V loaders (a warp for each 32 tokens x 128 dims of a tile): cp.async of the packed
-//    rows and scales (a warp its own tokens, RS - 1 tiles ahead), then e2m1 -> f16 times the
+//    rows and scales (a warp its own tokens, RS tiles ahead), then e2m1 -> f16 times the
 //    E4M3 block scale (exact) into the 128-byte-swizzled operand layouts in shared memory;
 //  * issue (two warps, one thread each): S = Q K^T (A = Q in tensor memory, N = TT tokens),
 //    and O += P V (A = P in tensor memory), each once its inputs are ready;
@@ -30,16 +30,19 @@
 // (log-sum-exp over partial states, by the last CTA to arrive).
 // Every wait is bounded; one that runs out sets flag 0x4 and the CTA winds down.
 //
-// Measured (replayed): 4 requests x 32771 tokens, 104 rows of 8 kv heads (128/128) 89 us, 630
-// TFLOP/s of the rows that are there; 16 requests of 512-4096 tokens x 64 rows 42 us; 8
-// requests of 2048-8192 tokens x 48-88 rows (512/256) 47 us.  Neither memory (1.7 TB/s) nor
+// Measured (replayed): 4 requests x 32771 tokens, 104 rows of 8 kv heads (128/128) 84 us, 660
+// TFLOP/s of the rows that are there; 16 requests of 512-4096 tokens x 64 rows 39 us; 8
+// requests of 2048-8192 tokens x 48-88 rows (512/256) 45 us.  Neither memory (1.8 TB/s) nor
 // the tensor cores (a third busy) are full: the softmax warps' chain of a tile (wait, load,
-// maximum, 2^x, store: 2300 cycles of 128 tokens) and, at 512 dims, the dequantisation bound
-// it, with half of the issue slots taken; of the 42 us, 12 are the wait for the longest unit
-// and 8 a CTA's start and end.  (Measured and not kept: products issued by the loaders' first
-// warps, which leaves 128 registers a thread, 53 / 120 / 64 us; barriers of their own for the
-// halves' S 44 / 92 / 47; the copies of the next tiles issued after a tile's arrival 43 / 92 /
-// 49; twice the CTAs, in two waves, 57 / 105 / 71.)
+// maximum, 2^x, store: 2200 cycles of 128 tokens) and, at 512 dims, the dequantisation bound
+// it, with half of the issue slots taken and an eighth of the warps' time spent fetching
+// instructions; of the 39 us, 12 are the wait for the longest unit and 7 a CTA's start and end.
+// Measured and not kept, against the kernel as it then was (16 requests / 4 x 32771 tokens /
+// 512 dims): products issued by the loaders' first warps, which leaves 128 registers a thread,
+// 53 / 120 / 64 for 42 / 89 / 47 us; barriers of their own for the halves' S 44 / 92 / 47;
+// loaders of K and of V in code of their own 43 / 92 / 49 for 40 / 87 / 47; a half's blocks of
+// 32 tokens one after the other, half the registers, 38 / 97 / 45 for 39 / 84 / 45; twice the
+// CTAs, in two waves, 57 / 105 / 71; other shares of registers (setmaxnreg) slower.
 #include <cstdint>
 #include <type_traits>
 
@@ -76,10 +79,10 @@ struct Tree {
   static constexpr int KLW = TT * KP / 32, VLW = TT * VP / 32;  // loader warps
   static constexpr int THREADS = 32 * (kSoftmaxWarps + KLW + VLW + 2);
   static constexpr int BT = TT / 4;                 // tokens of a softmax thread's block
-  static constexpr int KSEG = DK / 2 / KP, VSEG = DVC / 2 / VP;       // packed bytes of each
-  static constexpr int KSF = DK / 16 / KP, VSF = DVC / 16 / VP;       // scale bytes of each
-  static constexpr int KW = 32 * (KSEG + KSF), VW = 32 * (VSEG + VSF);  // a warp's stage
-  static constexpr int STAGE = KLW * KW + VLW * VW;
+  static constexpr int SEG = DK / 2 / KP, SF = DK / 16 / KP;  // packed and scale bytes of each
+  static_assert(DVC / 2 / VP == SEG, "one loader for both");
+  static constexpr int WARP = 32 * (SEG + SF);                // a warp's stage
+  static constexpr int STAGE = (KLW + VLW) * WARP;
   static constexpr int KBYTES = TT * DK * 2, VBYTES = TT * DVC * 2;   // operand tiles
   static constexpr int KB = 2, VB = DK == 512 ? 2 : 3;
   static constexpr int RS = DK == 512 ? 2 : DK == 128 ? 3 : 4;
@@ -168,28 +171,28 @@ __device__ __forceinline__ int raw_chunk(int r, int c) {
   return c ^ (r & 7);
 }
 
-// One loader warp: K (V false) or V rows of the tiles [t0, t0 + ntiles) of unit u.
-template <class T, int TT, bool V>
-__device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit& u, int w,
-                                           int lane, int t0, int ntiles, int tok_end, int vh,
-                                           uint8_t* smem, int q_stage, uint64_t* full,
+// Loader warp w of K or (of_v) V: its rows of the tiles [t0, t0 + ntiles) of unit u.  One code
+// for both, as the warps wait for instructions otherwise.
+template <class T, int TT>
+__device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit& u, bool of_v,
+                                           int w, int lane, int t0, int ntiles, int tok_end,
+                                           int vh, uint8_t* smem, int q_stage, uint64_t* full,
                                            uint64_t* empty, uint64_t* q_full,
                                            volatile int* abort) {
-  constexpr int SEG = V ? T::VSEG : T::KSEG, SF = V ? T::VSF : T::KSF;
-  constexpr int BYTES = V ? T::VBYTES : T::KBYTES, NB = V ? T::VB : T::KB, RS = T::RS;
+  constexpr int SEG = T::SEG, SF = T::SF, RS = T::RS;
+  const int bytes = of_v ? T::VBYTES : T::KBYTES, num = of_v ? T::VB : T::KB;
   constexpr int LPR = SEG / 16, RPI = 32 / LPR;  // lanes a row, rows a copy instruction
   const CacheView& c = p.cache;
   const int seg = w / (TT / 32);           // part of the row's dims
   const int first = 32 * (w % (TT / 32));  // this warp's first token of a tile
   const int shift = p.page_size == 1 ? 0 : 4, slots = (1 << shift) - 1;
-  const int64_t sp = V ? c.v_sp : c.k_sp, ss = V ? c.v_ss : c.k_ss;
-  const int64_t fsp = V ? c.vsf_sp : c.ksf_sp, fss = V ? c.vsf_ss : c.ksf_ss;
-  const int part = V ? vh * T::VP + seg : seg;   // the warp's part of the whole row
-  const uint8_t* data = (V ? c.v_data + u.h_kv * c.v_sh : c.k_data + u.h_kv * c.k_sh) + part * SEG;
-  const uint8_t* sf = (V ? c.v_sf + u.h_kv * c.vsf_sh : c.k_sf + u.h_kv * c.ksf_sh) + part * SF;
-  constexpr int TILES = V ? T::OFF_V : T::OFF_K;
-  const uint32_t mine = smem_addr(smem) + T::OFF_RAW +
-                        (V ? T::KLW * T::KW + w * T::VW : w * T::KW);
+  const int64_t sp = of_v ? c.v_sp : c.k_sp, ss = of_v ? c.v_ss : c.k_ss;
+  const int64_t fsp = of_v ? c.vsf_sp : c.ksf_sp, fss = of_v ? c.vsf_ss : c.ksf_ss;
+  const int part = of_v ? vh * T::VP + seg : seg;  // the warp's part of the whole row
+  const uint8_t* data = (of_v ? c.v_data + u.h_kv * c.v_sh : c.k_data + u.h_kv * c.k_sh) + part * SEG;
+  const uint8_t* sf = (of_v ? c.v_sf + u.h_kv * c.vsf_sh : c.k_sf + u.h_kv * c.ksf_sh) + part * SF;
+  const int tiles = of_v ? T::OFF_V : T::OFF_K;
+  const uint32_t mine = smem_addr(smem) + T::OFF_RAW + ((of_v ? T::KLW : 0) + w) * T::WARP;
   const int r0 = lane / LPR, ch = lane % LPR;
   // page id of this lane's token in tile i, a tile ahead of its use (where it is checked);
   // a token past the unit's pages takes the last one
@@ -201,12 +204,11 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
   // (rows r0, r0 + RPI, ... of the warp's 32 tokens, which begin at a multiple of 16)
   const uint8_t* from = data + (r0 & slots) * ss + 16 * ch;
   const uint8_t* sf_from = sf + (lane & slots) * fss;
-  auto issue = [&](int i, int32_t pid) {
+  auto issue = [&](uint32_t st, int32_t pid) {
     if (pid < 0 || pid >= c.num_pages) {
       atomicOr(p.flags, 0x1u);
       pid = 0;
     }
-    const uint32_t st = mine + (i % RS) * T::STAGE;
     const uint8_t* page = from;
 #pragma unroll
     for (int k = 0; k < LPR; ++k) {
@@ -220,51 +222,50 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
     }
     cp_async_sf<SF>(st + 32 * SEG + lane * SF, sf_from + pid * fsp);
   };
+  int32_t pids[RS];
 #pragma unroll
-  for (int i = 0; i < RS - 1; ++i) {
-    const int32_t pid = load_pid(i);
-    if (i < ntiles) issue(i, pid);
+  for (int i = 0; i < RS; ++i) pids[i] = load_pid(i);
+#pragma unroll
+  for (int i = 0; i < RS; ++i) {
+    if (i < ntiles) issue(mine + i * T::STAGE, pids[i]);
     cp_async_commit();
   }
-  int32_t next = load_pid(RS - 1);
+  int32_t next = load_pid(RS);
+  uint32_t st = mine;  // the stage of tile i
   const int tl = first + lane;  // this lane's token of a tile
   // its row, whose 16-byte chunks are xor-ed with the row's number
-  const uint32_t row = smem_addr(smem) + TILES + (tl >> 3) * 1024 + (tl & 7) * 128 + ((tl & 7) << 4);
+  const uint32_t row = smem_addr(smem) + tiles + (tl >> 3) * 1024 + (tl & 7) * 128 + ((tl & 7) << 4);
   // (Q's rows lie at the end of the operand tiles until they are read)
-  if (ntiles > 0 && TILES + NB * BYTES > q_stage &&
+  if (ntiles > 0 && tiles + num * bytes > q_stage &&
       !__all_sync(0xffffffffu, wait_bar(q_full, 0, abort, p.flags)))
     ntiles = 0;
   for (int i = 0, b = 0, round = 0; i < ntiles; ++i) {
-    const int32_t pid = next;
-    next = load_pid(i + RS);
-    if (i + RS - 1 < ntiles) issue(i + RS - 1, pid);
-    cp_async_commit();
     cp_async_wait<RS - 1>();  // this thread's copies of tile i have landed
-    bool ok = true;
-    if (round > 0)
-      ok = __all_sync(0xffffffffu, wait_soon<4>(&empty[b], (round - 1) & 1, abort, p.flags));
-    __syncwarp();  // and those of the warp
-    if (!ok) break;
-    const uint32_t st = mine + (i % RS) * T::STAGE;
+    __syncwarp();             // and those of the warp
     // slots past the request's end may hold a NaN scale: their values count as 0 (their
     // scores are replaced)
-    const bool past = V && u.tok_begin + (t0 + i) * TT + tl >= tok_end;
+    const bool past = u.tok_begin + (t0 + i) * TT + tl >= tok_end;
     uint32_t scales[SF / 4];
 #pragma unroll
     for (int k = 0; k < SF / 4; ++k) {
       scales[k] = lds_u32(st + 32 * SEG + lane * SF + 4 * k);
       if (past) scales[k] = 0;
     }
+    uint4 q[LPR];
+#pragma unroll
+    for (int k = 0; k < LPR; ++k) q[k] = lds_v4(st + lane * SEG + 16 * raw_chunk<SEG>(lane, k));
+    if (round > 0 &&
+        !__all_sync(0xffffffffu, wait_soon<4>(&empty[b], (round - 1) & 1, abort, p.flags)))
+      break;
     uint32_t out[8];  // the row's chunk c of each block of 64 dims
 #pragma unroll
     for (int c8 = 0; c8 < 8; ++c8)
-      out[c8] = (row + b * BYTES + (2 * SEG / 64 * seg) * (TT * 128)) ^ (c8 << 4);
+      out[c8] = (row + b * bytes + (2 * SEG / 64 * seg) * (TT * 128)) ^ (c8 << 4);
 #pragma unroll
     for (int k = 0; k < LPR; ++k) {
-      const uint4 q = lds_v4(st + lane * SEG + 16 * raw_chunk<SEG>(lane, k));
       const uint32_t s2 = e4m3x2_to_f16x2(scales[k / 2] >> (16 * (k & 1)));
       const uint32_t lo = bcast_lo(s2), hi = bcast_hi(s2);
-      const uint32_t words[4] = {q.x, q.y, q.z, q.w};
+      const uint32_t words[4] = {q[k].x, q[k].y, q[k].z, q[k].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         uint32_t h[4];
@@ -278,10 +279,14 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
     }
     fence_async_smem();
     __syncwarp();
-    const bool withhold = NVFP4KV_TREE_TEST_SKIP_ARRIVE && !V && blockIdx.x == 0 &&
+    const bool withhold = NVFP4KV_TREE_TEST_SKIP_ARRIVE && !of_v && blockIdx.x == 0 &&
                           blockIdx.y == 0 && w == 0 && i == 0;
     if (lane == 0 && !withhold) mbar_arrive(&full[b]);
-    if (++b == NB) {
+    if (i + RS < ntiles) issue(st, next);  // (the warp has read the stage)
+    cp_async_commit();
+    next = load_pid(i + RS + 1);
+    st = st == mine + (RS - 1) * T::STAGE ? mine : st + T::STAGE;
+    if (++b == num) {
       b = 0;
       ++round;
     }
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(Tree<DK, DVC, VH, TT, ONE>::THREADS, 1)
   }
   const int nrows = min(kRows, R - row0);
   // Up to 64 rows are held twice: the copies share each half's tokens, so that all warps
-  // work (16 requests of 512-4096 tokens x 64 rows 48 -> 46 us).
+  // work (16 requests of 512-4096 tokens x 64 rows 48 -> 41 us).
   const int rows_held = nrows <= kRows / 2 ? kRows / 2 : kRows;
   // this CTA's tiles of the unit; tokens from tok_end on do not exist
   const int tok_end = min(u.kv_len, u.tok_begin + p.page_size * u.num_pages);
@@ -389,12 +394,11 @@ __global__ void __launch_bounds__(Tree<DK, DVC, VH, TT, ONE>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
 
-  if (warp >= kKWarp && warp < kVWarp) {
-    load_tiles<T, TT, false>(p, u, warp - kKWarp, lane, t0, ntiles, tok_end, vh,
-                             smem, q_stage, k_full, k_empty, q_full, s_abort);
-  } else if (warp >= kVWarp && warp < kSWarp) {
-    load_tiles<T, TT, true>(p, u, warp - kVWarp, lane, t0, ntiles, tok_end, vh,
-                            smem, q_stage, v_full, v_empty, q_full, s_abort);
+  if (warp >= kKWarp && warp < kSWarp) {
+    const bool of_v = warp >= kVWarp;
+    load_tiles<T, TT>(p, u, of_v, warp - (of_v ? kVWarp : kKWarp), lane, t0, ntiles, tok_end, vh,
+                      smem, q_stage, of_v ? v_full : k_full, of_v ? v_empty : k_empty, q_full,
+                      s_abort);
   } else if (warp == kSWarp) {
     // ================= issue of S = Q K^T (one thread) =========================
     if (elect_one()) {
@@ -538,33 +542,31 @@ __global__ void __launch_bounds__(Tree<DK, DVC, VH, TT, ONE>::THREADS, 1)
       __syncwarp();
     };
     // A half has two blocks of a tile's tokens, the first and the third quarter or the second
-    // and the fourth.  NB: the blocks that this thread looks at, from block b0.
+    // and the fourth.  NB: the blocks that this thread looks at, from block k0.
     constexpr int BT = T::BT;
-    auto tiles = [&](auto blocks) {
+    auto tiles = [&](auto blocks, int k0) {
       constexpr int NB = decltype(blocks)::value;
-      const int b0 = NB == 1 ? copy : 0;
       for (int i = 0; i < ntiles; ++i) {
-        const int tok = u.tok_begin + (t0 + i) * TT + b0 * (TT / 2) + half * BT;
+        const int tok = u.tok_begin + (t0 + i) * TT + half * BT;
         const bool masked = u.tok_begin + (t0 + i + 1) * TT > some_hidden;
-        uint32_t see[NB];
-        if (masked) {
-#pragma unroll
-          for (int k = 0; k < NB; ++k) see[k] = visible(tok + k * (TT / 2));
-        }
         wait(s_full, i & 1);
         tc_fence_after();
         uint32_t x[NB * BT];
 #pragma unroll
         for (int k = 0; k < NB; ++k)
-          tmem_ld<BT>(tmem + lane_base + T::SCOL + (b0 + k) * (TT / 2) + half * BT, x + k * BT);
+          tmem_ld<BT>(tmem + lane_base + T::SCOL + (k0 + k) * (TT / 2) + half * BT, x + k * BT);
         tmem_wait_ld<NB * BT>(x);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(s_empty);
         if (masked) {
 #pragma unroll
-          for (int e = 0; e < NB * BT; ++e)
-            if (!(see[e / BT] >> (e % BT) & 1u)) x[e] = 0xff800000u;  // -inf
+          for (int k = 0; k < NB; ++k) {
+            const uint32_t see = visible(tok + (k0 + k) * (TT / 2));
+#pragma unroll
+            for (int e = 0; e < BT; ++e)
+              if (!(see >> e & 1u)) x[k * BT + e] = 0xff800000u;  // -inf
+          }
         }
         // the largest score (f > 0, so that of the sums); f = 0 for rows that are not there
         float mx[4] = {__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]),
@@ -635,7 +637,7 @@ __global__ void __launch_bounds__(Tree<DK, DVC, VH, TT, ONE>::THREADS, 1)
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < NB; ++k)
-          tmem_st<BT / 2>(tmem + lane_base + T::PCOL + (b0 + k) * (TT / 4) + half * (BT / 2),
+          tmem_st<BT / 2>(tmem + lane_base + T::PCOL + (k0 + k) * (TT / 4) + half * (BT / 2),
                           h + k * (BT / 2));
         tmem_wait_st();
         tc_fence_before();
@@ -655,9 +657,9 @@ __global__ void __launch_bounds__(Tree<DK, DVC, VH, TT, ONE>::THREADS, 1)
       // the other copy's block: its weights are 0 for this row
       uint32_t zero[BT / 2] = {};
       tmem_st<BT / 2>(tmem + lane_base + T::PCOL + (1 - copy) * (TT / 4) + half * (BT / 2), zero);
-      tiles(std::integral_constant<int, 1>{});
+      tiles(std::integral_constant<int, 1>{}, copy);
     } else {
-      tiles(std::integral_constant<int, 2>{});
+      tiles(std::integral_constant<int, 2>{}, 0);
     }
     // ---- the CTA's state: sums of the halves, then O ------------------------------------
     if (active) {
