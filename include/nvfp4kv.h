@@ -712,7 +712,7 @@ int nvfp4kv_e4m3_copy_pages(const nvfp4kv_e4m3_cache* cache, const int32_t* src,
  * head that is smaller than the pages freed NVFP4KV_FLAG_TABLE_FULL; then nothing else is
  * changed.  A page id out of the pool is passed over: NVFP4KV_FLAG_BAD_PAGE_INDEX; a page
  * that is left more often than it has owners is freed once: NVFP4KV_FLAG_BAD_SHARES.  One
- * launch where num_rows * max_pages_per_request is at most 16384, else three; can be
+ * launch where num_rows * max_pages_per_request is at most 32768, else up to three; can be
  * captured in a CUDA graph. */
 int nvfp4kv_release_pages(const int32_t* keep_len, int32_t* kv_len, int32_t num_rows,
                           int32_t page_size, const int32_t* block_table,

@@ -771,6 +771,8 @@ struct NewTokens {
 
 // CTAs of a cluster of the wide tree kernel: those that share the value dims, doubled
 // while the launch's CTAs stay one wave and each keeps kTreeTiles tiles of a whole unit.
+// (4 requests x 32771 tokens 83 us, without clusters 145; 8 x 2048-8192, 512/256 heads, 56 for
+// 62; 2 x 4000, 512/256 heads, 30 for 31 without or with twice the tiles.)
 constexpr int64_t kTreeTiles = 3;
 int tree_cluster(const nvfp4kv_plan_info* info, const TreeConfig& cfg, int blocks) {
   const int64_t tokens = (int64_t)info->chunk_pages * kPageSize;
@@ -820,7 +822,11 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
                    attend_config_dec(info->head_dim_qk, info->head_dim_vo, 8,
                                      info->num_units <= info->num_sms ? 1 : 4, &cfg);
   // trees: more than 16 rows a kv head go to the kernel of 128-row blocks (it takes a plan
-  // of either kernel), up to 16 to the mma.sync kernel's own form
+  // of either kernel), up to 16 to the mma.sync kernel's own form.  Measured, the former for
+  // the latter, us: 16 requests of 512-4096 tokens x 16 rows 34 / 32, x 20 rows 36 / 61, x 64
+  // 39 / 95; 4 x 32771 tokens x 16 rows 71 / 67, x 20 rows 72 / 127; 512/256 heads x 32 rows
+  // 35 / 61; 64/64 heads x 20 and 32 rows 30 / 26 to 70 / 83 (the plan counts on more than
+  // one CTA an SM), x 36 rows 20 / 34.
   TreeConfig tcfg{};
   const bool wide_tree = tree && (info->kernel == kKernelTcgen05 || info->row_blocks > 1) &&
                          attend_config_tree(info->head_dim_qk, info->head_dim_vo, &tcfg);

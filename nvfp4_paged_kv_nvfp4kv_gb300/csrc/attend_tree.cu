@@ -100,6 +100,8 @@ struct Tree {
   static constexpr uint32_t IDESC_S = idesc_f16(kRows, TT, 0, 0);
   static constexpr uint32_t IDESC_O = idesc_f16(kRows, DVC, 0, 1);
   static_assert(COLS <= TCOLS && SMEM <= 232448, "resources");
+  static_assert(2 * (SMEM + 1024) > 233472, "one CTA an SM: two clusters that share SMs might "
+                                            "each hold the tensor memory that the other wants");
   static_assert(OFF_RAW % 1024 == 0 && OFF_MISC % 16 == 0, "alignment");
   static_assert(kRows * OROW * 4 <= OFF_RAW, "the joined states take the operands' place");
 };

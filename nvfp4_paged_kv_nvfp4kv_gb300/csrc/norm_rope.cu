@@ -24,7 +24,7 @@
 // a head's place is taken by the load three on as soon as it is unpacked.  Measured
 // (replayed, three sets of tensors in turn): 16384 tokens x 40 heads of 128, bf16, 60 us,
 // 5.6 TB/s (0.84 of a plain copy); 211 tokens x 18 heads of 256, a quarter in pairs, f16,
-// 4.2 us.  Loads in batches of three 66 us, of two 73 (and 85 with a token's heads on two
+// 3.8 us.  Loads in batches of three 66 us, of two 73 (and 85 with a token's heads on two
 // warps: the angles and weights are then formed twice); two or four heads in the ring 63
 // and 64; chunks of 8 bytes, half the registers and more warps, 66.
 #include <cstdint>

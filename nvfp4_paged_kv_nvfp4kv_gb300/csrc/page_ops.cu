@@ -18,6 +18,13 @@
 // entries.  The order of a call's atomics changes no result: owners are counted up and
 // down by whole numbers, and of several entries that give up one page the first in the
 // list is found by a minimum.
+//
+// Latency bounds them: launches, the chain of loads that finds an entry, and (release) the
+// pages' words, random sectors of L2 or HBM, four times.  Measured (replayed): 16 requests of
+// 512-4096 tokens forked once 6.1 us and released 11; 64 requests of 500-16384 tokens forked 8
+// times each (270 k table entries copied, then given up) 8.1 and 37, of which the last two
+// passes' cluster takes 25 (16 SMs' loads of random words; all SMs would need a place for the
+// counts between launches); the copies of the last pages 3.0 and 5.2 us (17 MB, 3.3 TB/s).
 #include <climits>
 #include <cstdint>
 #include <map>
@@ -186,12 +193,18 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p) 
 //   3  the entry that finds its own number there is the page's first;
 //   4  it puts the page on the free list, at the place that the count of such entries
 //      before it gives, and the word back to 0.
-// A small call is one launch of one CTA, which keeps its entries' pages in registers over
-// the passes.  For a large one passes 1 and 2 are launches over all SMs (the random words
-// want many loads in flight), 3 and 4 one cluster whose barrier joins the counts.
+// A small call is one launch of one CTA, a larger one of a cluster, which keep their
+// entries' pages in registers over the passes.  Where they have no room, passes 1 and 2 are
+// launches over all SMs (the random words want many loads in flight), 3 and 4 one cluster
+// whose barrier joins the counts.
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kUnits = 4;  // units of 32 entries that a warp has in flight
-constexpr int kOneCta = 16 * kThreads;  // entries up to which one CTA is used
+// Entries up to which one CTA is used.  Measured with every page given up (replayed; one CTA /
+// a cluster / three launches, us): 256 entries 8.4 / 10.6 / 14.1, 1024 10.3 / 11.5 / 15.2, 2048
+// 12.8 / 11.9 / 15.7, 4096 18.7 / 12.5 / 16.4, 32768 - / 16.2 / 18.9, 65536 (as many as a
+// cluster's registers hold) - / 22.3 / 21.8, with a tenth given up 35 / 13.1 / 16.4; 131072
+// - / 46.5 / 37.2.
+constexpr int kOneCta = kThreads;
 constexpr int kMostMarks = 8192;  // units of a CTA whose marks are kept (others: all looked at)
 
 // The rows that give up pages, in shared memory: the first entry of each (and the count of
@@ -568,7 +581,7 @@ cudaError_t launch_release(ReleaseParams p, cudaStream_t stream) {
   int from = 1;
   if (most <= kOneCta) {
     ctas = 1;
-  } else {
+  } else if (most > (int64_t)ctas * kWarps * kUnits * 32) {
     if (rows_smem > 40 * 1024) {
       e = cudaFuncSetAttribute(release_pass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                kRowsSmem);

@@ -156,9 +156,10 @@ def test_forks_that_cannot_be(parents, children):
     assert int(b.head2) == -1 and set(src.tolist() + dst.tolist()) == {-7}
 
 
-def test_lengths_that_cannot_be():
-    for length in (-1, 2**30 + 1, 1000):
-        b = Both((33, 16), 8)
+@pytest.mark.parametrize("width", [8, 1000, 20000])  # one CTA, a cluster, three launches
+def test_lengths_that_cannot_be(width):
+    for length in (-1, 2**30 + 1, 16 * width + 1):
+        b = Both((33, 16), 8, width=width)
         b.kv_len[0] = b.ref.kv_len[0] = length
         b.fork([0], [5], check=False)
         torch.cuda.synchronize()
@@ -172,7 +173,7 @@ def test_lengths_that_cannot_be():
         b.flags.zero_()
         b.same()
     for keep in ([34, 0, 0, 0, 0, 0, 0, 0], [-1, 0, 0, 0, 0, 0, 0, 0]):
-        b = Both((33, 16), 8)
+        b = Both((33, 16), 8, width=width)
         b.release(keep, check=False)
         torch.cuda.synchronize()
         assert int(b.flags) == _lib.FLAG_BAD_LENGTH
@@ -180,8 +181,9 @@ def test_lengths_that_cannot_be():
         b.same()
 
 
-def test_free_lists_that_are_too_short():
-    b = Both((33, 5, 16), 8, spare=1)
+@pytest.mark.parametrize("width", [8, 1000, 20000])  # one CTA, a cluster, three launches
+def test_free_lists_that_are_too_short(width):
+    b = Both((33, 5, 16), 8, spare=1, width=width)
     b.fork([0, 1], [5, 6], check=False)  # two new pages, one left
     torch.cuda.synchronize()
     assert int(b.flags) == _lib.FLAG_TABLE_FULL
@@ -208,9 +210,10 @@ def test_free_lists_that_are_too_short():
         b.same()
 
 
-def test_page_ids_out_of_the_pool():
+@pytest.mark.parametrize("width", [8, 1000, 20000])  # one CTA, a cluster, three launches
+def test_page_ids_out_of_the_pool(width):
     """Passed on by a fork and passed over by a release, flagged both times."""
-    b = Both((40, 20), 6)
+    b = Both((40, 20), 6, width=width)
     b.table[0, 1] = b.ref.table[0][1] = b.total
     src, dst = b.fork([0], [3], check=False)
     torch.cuda.synchronize()
@@ -224,9 +227,10 @@ def test_page_ids_out_of_the_pool():
     assert not b.shares.any()
 
 
-def test_a_page_given_up_too_often():
+@pytest.mark.parametrize("width", [8, 1000, 20000])  # one CTA, a cluster, three launches
+def test_a_page_given_up_too_often(width):
     """A page in two rows whose owners were not counted: freed once, flagged."""
-    b = Both((16, 32), 4)
+    b = Both((16, 32), 4, width=width)
     b.table[2, 0] = b.table[0, 0]
     b.kv_len[2] = 16
     page = b.ref.table[0][0]
