@@ -627,7 +627,9 @@ int nvfp4kv_tree_masks(const int32_t* parents, const int32_t* qo_indptr, const i
  *                 and lse -inf.
  *   new_k, new_v  NULL, or the step's new tokens, quantised into their pages by the same
  *                 launch as in nvfp4kv_decode_append_run.
- * The request's tokens are finite in the cache, as nvfp4kv_quantize_append stores them. */
+ * q and the new tokens are finite, and so are the request's tokens in the cache, as
+ * nvfp4kv_quantize_append stores them; slots behind the request's end and pages of others
+ * may hold anything. */
 int nvfp4kv_tree_run(const nvfp4kv_plan_info* info, const uint32_t* tree_mask, int32_t mask_words,
                      const void* new_k_bf16, int64_t k_stride_tok, int64_t k_stride_head,
                      const void* new_v_bf16, int64_t v_stride_tok, int64_t v_stride_head,
@@ -708,6 +710,9 @@ int nvfp4kv_e4m3_copy_pages(const nvfp4kv_e4m3_cache* cache, const int32_t* src,
  * column) that names them, and free_head_out, which may be free_head, becomes head -
  * freed.
  *   num_rows at most 8192.
+ * A request that is cut inside a page which has other owners must not grow there: it is
+ * forked first (its fork has a copy of that page), or its tokens from the page's start
+ * are given up.  (Drafted tokens that stand behind a fork are in pages of their request.)
  * A length that cannot be (keep_len > kv_len among them) sets NVFP4KV_FLAG_BAD_LENGTH, a
  * head that is smaller than the pages freed NVFP4KV_FLAG_TABLE_FULL; then nothing else is
  * changed.  A page id out of the pool is passed over: NVFP4KV_FLAG_BAD_PAGE_INDEX; a page

@@ -108,7 +108,7 @@ def nvfp4kv_tree_run(plan: Plan, q, cache: PagedCache, kv_indices, tree_mask,
                      stream=None):
     """Attention of the nodes of drafted trees: row i of q [rows, Hq, Dk] sees what stood
     before its request's rows, and of these those whose bits are set in its words of
-    ``tree_mask`` [rows, words] int32.  With ``new_k`` and ``new_v`` [rows, Hkv, D] the
+    ``tree_mask`` [rows, words] int32; q is finite.  With ``new_k`` and ``new_v`` [rows, Hkv, D] the
     step's tokens are quantised into their pages by the same launch.  ``plan`` is one of
     kernel 0, 1 or 3.  Returns (out [rows, Hq, Dv], lse [rows, Hq])."""
     r = plan.__dict__.get("_tree_run")
@@ -266,7 +266,8 @@ def nvfp4kv_release_pages(keep_len, kv_len, block_table, page_shares, free_pages
     """Row b of the block table keeps its first ``keep_len[b]`` of ``kv_len[b]`` tokens and
     gives the pages behind them up: a page without another owner goes back in front of
     the free list's head (``free_head`` [1]; the new one goes to ``free_head_out``, by
-    default the same word).  ``kv_len`` and ``page_shares`` are updated."""
+    default the same word).  ``kv_len`` and ``page_shares`` are updated.  A request cut
+    inside a page with other owners must not grow there (fork it first)."""
     if free_head_out is None:
         free_head_out = free_head
     _i32("the lists", keep_len, kv_len, page_shares, free_pages, free_head, free_head_out)

@@ -244,3 +244,38 @@ def test_stream_graph_and_given_outputs(kernel):
     graph.replay()
     torch.cuda.synchronize()
     assert not torch.equal(out, o3) and (l3[:9] != lse[:9]).all()
+
+
+@pytest.mark.parametrize("dk,dv,kv,new", [
+    (128, 128, (2000, 300), (2, 3)), (128, 128, (9000, 4100), (20, 30)),
+    (64, 64, (5000, 700), (9, 40)), (512, 256, (6000, 700), (9, 40))])
+def test_one_plan_for_trees_and_for_causal_rows(dk, dv, kv, new):
+    """A plan's workspace serves both attentions in turn: each leaves the counters of its
+    split requests as it found them."""
+    c, plan, o, lse, q, mask = tree_case(kv, new, 8, 2, dk, dv, seed=21)
+    ref = N.nvfp4kv_decode_plan(np.concatenate([[0], np.cumsum(new)]), c.indptr, c.last, 8, 2, dk,
+                                dv, causal=True)
+    want, want_lse = N.nvfp4kv_decode_run(ref, q, c.cache, c.kv_indices)
+    for _ in range(3):
+        got, got_lse = N.nvfp4kv_tree_run(ref, q, c.cache, c.kv_indices, mask)
+        assert torch.equal(got, o) and torch.equal(got_lse, lse)
+        got, got_lse = N.nvfp4kv_decode_run(ref, q, c.cache, c.kv_indices)
+        assert torch.equal(got, want) and torch.equal(got_lse, want_lse)
+    assert N.nvfp4kv_workspace_flags(ref) == 0
+
+
+def test_two_streams_at_once():
+    """Calls of several kernels' forms in flight together, each with a plan of its own."""
+    cases = [tree_case(kv, new, 8, 2, dk, dv, seed=30 + i) for i, (kv, new, dk, dv) in enumerate(
+        [((9000, 4100), (20, 30), 128, 128), ((6000, 700), (9, 40), 512, 256),
+         ((5000, 7000), (16, 16), 64, 64), ((3000, 200), (3, 2), 128, 128)])]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [(torch.empty_like(o), torch.empty_like(lse)) for _, _, o, lse, _, _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (c, plan, _, _, q, mask), s, (o, lse) in zip(cases, streams, outs):
+            N.nvfp4kv_tree_run(plan, q, c.cache, c.kv_indices, mask, out=o, lse=lse, stream=s)
+    torch.cuda.synchronize()
+    for (_, plan, o, lse, _, _), got in zip(cases, outs):
+        assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+        assert N.nvfp4kv_workspace_flags(plan) == 0
