@@ -769,18 +769,45 @@ struct NewTokens {
   int64_t k_stride_tok = 0, k_stride_head = 0, v_stride_tok = 0, v_stride_head = 0;
 };
 
-// CTAs of a cluster of the wide tree kernel: those that share the value dims, doubled
-// while the launch's CTAs stay one wave and each keeps kTreeTiles tiles of a whole unit.
-// (4 requests x 32771 tokens 83 us, without clusters 145; 8 x 2048-8192, 512/256 heads, 56 for
-// 62; 2 x 4000, 512/256 heads, 30 for 31 without or with twice the tiles.)
-constexpr int64_t kTreeTiles = 3;
-int tree_cluster(const nvfp4kv_plan_info* info, const TreeConfig& cfg, int blocks) {
-  const int64_t tokens = (int64_t)info->chunk_pages * kPageSize;
-  int ctas = cfg.value_parts;
-  while (ctas < 8 && (int64_t)info->num_units * blocks * ctas * 2 <= info->num_sms &&
-         tokens >= kTreeTiles * cfg.tile_tokens * (2 * ctas / cfg.value_parts))
-    ctas *= 2;
-  return ctas;
+// How the wide tree kernel runs a plan: in clusters of `ctas` CTAs that share a unit's value
+// dims and its tokens, or (whole) those of all units of a pair of request and kv head, which
+// the cluster then joins in place of the fold.  Measured, a plan's units / whole pairs, us, 64
+// rows: one request of one kv head, 300 tokens 14.0 / 11.7, 4096 24.8 / 15.9, 32771 64 / 42; of
+// 8 kv heads, 2000 tokens 20 / 14, 8000 22.5 / 20, 32771 36 / 44; 4 of 2000 18.5 / 16, of 32771
+// 85 / 79 (145 without clusters); 8 of 4000 30.5 / 27; 4 of 500-8000 23 / 26; 512/256 heads, one
+// of 2000 28 / 21.5, 8 of 2048-8192 57 / 67.
+struct TreeClusters {
+  int ctas;
+  bool whole;
+};
+constexpr int64_t kTreeTiles = 2;  // tiles of a whole unit that a CTA keeps
+TreeClusters tree_clusters(const nvfp4kv_plan_info* info, const TreeConfig& cfg, int blocks) {
+  // The CTAs that share the value dims, doubled while the launch's stay one wave: of whole
+  // pairs, one of clusters, whose CTAs are neighbours (16 of 8 CTAs are two waves, 38 us for
+  // 26).  Among a plan's units are shorter ones, behind which a cluster too many finds room.
+  auto grow = [&](int64_t units, int64_t tokens, bool whole) {
+    int ctas = cfg.value_parts;
+    while (ctas < 8 && units * blocks * ctas * 2 <= info->num_sms &&
+           (!whole || units * blocks <= tree_max_clusters(cfg, ctas * 2)) &&
+           tokens >= kTreeTiles * cfg.tile_tokens * (2 * ctas / cfg.value_parts))
+      ctas *= 2;
+    return ctas;
+  };
+  auto tiles = [&](int64_t tokens, int ctas) {  // of a CTA
+    const int64_t share = (int64_t)cfg.tile_tokens * (ctas / cfg.value_parts);
+    return (tokens + share - 1) / share;
+  };
+  const int64_t chunk = (int64_t)info->chunk_pages * kPageSize, splits = info->max_units_per_request;
+  const int64_t pairs = (int64_t)info->batch * info->num_kv_heads;
+  const TreeClusters c{grow(info->num_units, chunk, false), false};
+  if (splits < 2 || pairs * blocks * cfg.value_parts > info->num_sms) return c;
+  // In eighths of a tile (1.1 us): a fold takes 2.5 tiles, and 0.37 for each state of 64 rows of
+  // 128 dims; finding a pair's units takes one.
+  const int64_t rows = std::min<int64_t>(kTreeRows, (int64_t)info->row_blocks * info->rows_per_block);
+  const int64_t fold = 20 + 3 * splits * rows * info->head_dim_vo / 8192;
+  const int ctas = grow(pairs, chunk * splits, true);
+  if (8 * tiles(chunk * splits, ctas) + 8 > 8 * tiles(chunk, c.ctas) + fold) return c;
+  return {ctas, true};
 }
 
 int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_tok,
@@ -879,8 +906,10 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
   }
   if (wide_tree) {
     const int blocks = (info->row_blocks * info->rows_per_block + kTreeRows - 1) / kTreeRows;
-    e = launch_attend_tree(tcfg, p, info->num_units, blocks, tree_cluster(info, tcfg, blocks),
-                           stream);
+    const TreeClusters c = tree_clusters(info, tcfg, blocks);
+    p.tree_whole = c.whole ? info->num_units : 0;
+    e = launch_attend_tree(tcfg, p, c.whole ? info->batch * info->num_kv_heads : info->num_units,
+                           blocks, c.ctas, stream);
   } else {
     e = launch_attend(cfg, p, info->num_units, info->row_blocks, stream);
   }

@@ -44,6 +44,7 @@
 // 32 tokens one after the other, half the registers, 38 / 97 / 45 for 39 / 84 / 45; twice the
 // CTAs, in two waves, 57 / 105 / 71; other shares of registers (setmaxnreg) slower.
 #include <cstdint>
+#include <mutex>
 #include <type_traits>
 
 #include <cuda_runtime.h>
@@ -324,8 +325,22 @@ __global__ void __launch_bounds__(Tree<DK, DVC, VH, TT, ONE>::THREADS, 1)
   float* s_m = s_ml + 2 * kRows;  // [128] maxima, then
   float* s_l = s_m + kRows;       // [128] sums of the CTA's state
 
-  const WorkUnit u = load_unit(p);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int unit = blockIdx.x;
+  if (p.tree_whole > 0) {  // of the pair's units the first, which the cluster takes for all
+    if (tid == 0) *s_last = -1;
+    __syncthreads();
+    for (int i = tid; i < p.tree_whole; i += kThreads)
+      if (p.units[i].pair == unit && p.units[i].split == 0) *s_last = i;
+    __syncthreads();
+    unit = *s_last;
+    if (unit < 0) return;  // a request without rows
+  }
+  WorkUnit u = load_unit(p, unit, tid == 0);
+  if (p.tree_whole > 0) {
+    u.num_splits = 1;
+    u.num_pages = (u.kv_len + p.page_size - 1) / p.page_size;
+  }
   if (tid == 0) {  // (while the unit is on its way)
     for (int b = 0; b < KB; ++b) {
       mbar_init(&k_full[b], T::KLW);
@@ -927,21 +942,54 @@ bool attend_config_tree(int dk, int dv, TreeConfig* cfg) {
   return false;
 }
 
-cudaError_t launch_attend_tree(const TreeConfig& cfg, AttendParams p, int units, int row_blocks,
+static void tree_launch(const TreeConfig& cfg, int grid, int rows, int ctas,
+                        cudaLaunchAttribute* attr, cudaLaunchConfig_t* lc) {
+  *lc = cudaLaunchConfig_t{};
+  lc->gridDim = dim3(grid, rows * ctas);
+  lc->blockDim = dim3(cfg.threads);
+  lc->dynamicSmemBytes = cfg.smem_bytes;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = 1;
+  attr->val.clusterDim.y = ctas;
+  attr->val.clusterDim.z = 1;
+  lc->attrs = attr;
+  lc->numAttrs = 1;
+}
+
+// A property of the current device and the kernel, asked for once.
+int tree_max_clusters(const TreeConfig& cfg, int ctas) {
+  struct Known {
+    const void* func;
+    int dev, ctas, clusters;
+  };
+  static std::mutex mu;
+  static Known known[64];
+  static int count = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  for (int i = 0; i < count; ++i)
+    if (known[i].func == cfg.func && known[i].dev == dev && known[i].ctas == ctas)
+      return known[i].clusters;
+  cudaLaunchAttribute attr{};
+  cudaLaunchConfig_t lc;
+  tree_launch(cfg, 1, 1, ctas, &attr, &lc);
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, cfg.func, &lc) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  if (count < 64) known[count++] = {cfg.func, dev, ctas, n};  // (else asked again)
+  return n;
+}
+
+cudaError_t launch_attend_tree(const TreeConfig& cfg, AttendParams p, int grid, int row_blocks,
                                int ctas, cudaStream_t stream) {
   p.tree_ctas = ctas;
-  cudaLaunchConfig_t lc{};
-  lc.gridDim = dim3(units, row_blocks * ctas);
-  lc.blockDim = dim3(cfg.threads);
-  lc.dynamicSmemBytes = cfg.smem_bytes;
-  lc.stream = stream;
   cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = 1;
-  attr.val.clusterDim.y = ctas;
-  attr.val.clusterDim.z = 1;
-  lc.attrs = &attr;
-  lc.numAttrs = 1;
+  cudaLaunchConfig_t lc;
+  tree_launch(cfg, grid, row_blocks, ctas, &attr, &lc);
+  lc.stream = stream;
   void* args[] = {&p};
   return cudaLaunchKernelExC(&lc, cfg.func, args);
 }

@@ -86,7 +86,8 @@ struct AttendParams {
   // it sees the j-th of its request's qo_len last tokens
   const uint32_t* tree_mask;
   int32_t tree_words;
-  int32_t tree_ctas;   // attend_tree: CTAs of a cluster, which share a unit's tokens
+  int32_t tree_ctas;   // attend_tree: CTAs of a cluster, which share a unit's tokens,
+  int32_t tree_whole;  // the plan's units where a cluster takes a whole pair's, else 0
   int32_t row_blocks;  // and the plan's row blocks (merge counters of a pair)
 };
 
@@ -282,7 +283,8 @@ struct TreeConfig {
 };
 constexpr int kTreeRows = 128;
 bool attend_config_tree(int dk, int dv, TreeConfig* cfg);
-cudaError_t launch_attend_tree(const TreeConfig& cfg, AttendParams p, int units, int row_blocks,
+int tree_max_clusters(const TreeConfig& cfg, int ctas);  // that run at a time
+cudaError_t launch_attend_tree(const TreeConfig& cfg, AttendParams p, int grid, int row_blocks,
                                int ctas, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams& p, cudaStream_t stream);
 cudaError_t launch_dequantize(const DequantParams& p, cudaStream_t stream);

@@ -84,10 +84,12 @@ def test_groups(hq, hkv, new, page):
 @pytest.mark.parametrize("kernel", [1, 3])
 @pytest.mark.parametrize("chunk", [16, 64, 176])
 @pytest.mark.parametrize("new", [(5, 1, 0, 30), (16, 1, 17, 64)])
-def test_splits(kernel, chunk, new):
-    """Chunks that begin and end inside the tree, some that hold none of a row's tokens."""
+@pytest.mark.parametrize("num_sms", [0, 1])
+def test_splits(kernel, chunk, new, num_sms):
+    """Chunks that begin and end inside the tree, some that hold none of a row's tokens:
+    joined by a cluster for each request and kv head, or (no room for such: one SM) folded."""
     _, plan, *_ = tree_case((300, 1, 17, 1111), new, 8, 2, 128, 128, kernel=kernel,
-                            force_chunk_tokens=chunk, seed=chunk)
+                            force_chunk_tokens=chunk, num_sms=num_sms, seed=chunk)
     assert plan.info.split == 1
 
 
