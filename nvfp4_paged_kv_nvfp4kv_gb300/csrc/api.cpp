@@ -771,16 +771,21 @@ struct NewTokens {
 
 // How the wide tree kernel runs a plan: in clusters of `ctas` CTAs that share a unit's value
 // dims and its tokens, or (whole) those of all units of a pair of request and kv head, which
-// the cluster then joins in place of the fold.  Measured, a plan's units / whole pairs, us, 64
-// rows: one request of one kv head, 300 tokens 14.0 / 11.7, 4096 24.8 / 15.9, 32771 64 / 42; of
-// 8 kv heads, 2000 tokens 20 / 14, 8000 22.5 / 20, 32771 36 / 44; 4 of 2000 18.5 / 16, of 32771
-// 85 / 79 (145 without clusters); 8 of 4000 30.5 / 27; 4 of 500-8000 23 / 26; 512/256 heads, one
-// of 2000 28 / 21.5, 8 of 2048-8192 57 / 67.
+// the cluster then joins in place of the fold; sorted: in more than one wave, the longest pairs
+// first, where the longest would hold the others up.
+// Measured, a plan's units / whole pairs, us, 64 rows: one request of one kv head, 300 tokens
+// 14.0 / 11.7, 4096 24.8 / 15.9, 32771 64 / 42; of 8 kv heads, 2000 tokens 20 / 14, 8000 22.5 /
+// 20, 32771 36 / 44; 4 of 2000 18.5 / 16, of 32771 85 / 78 (145 without clusters); 8 of 4000
+// 30.5 / 27; 4 of 500-8000 23 / 26; 512/256 heads, one of 2000 28 / 21.5, 8 of 2048-8192 57 /
+// 67.  One wave / sorted: 18 requests of 1000-30000 tokens 210 / 169, 60 of 300-5000, 2 kv heads,
+// 52 / 44, 512/256 heads, 30 of 500-8192, 140 / 95, 64/64 heads, 16 of 500-8192, 53 / 45; 16 of
+// 512-4096 38 / 42, 12 of 100-8000 44 / 46.
 struct TreeClusters {
   int ctas;
-  bool whole;
+  bool whole, sorted;
 };
 constexpr int64_t kTreeTiles = 2;  // tiles of a whole unit that a CTA keeps
+constexpr int kTreeSorted = 512;   // units among which a CTA finds its own by rank
 TreeClusters tree_clusters(const nvfp4kv_plan_info* info, const TreeConfig& cfg, int blocks) {
   // The CTAs that share the value dims, doubled while the launch's stay one wave: of whole
   // pairs, one of clusters, whose CTAs are neighbours (16 of 8 CTAs are two waves, 38 us for
@@ -798,16 +803,33 @@ TreeClusters tree_clusters(const nvfp4kv_plan_info* info, const TreeConfig& cfg,
     return (tokens + share - 1) / share;
   };
   const int64_t chunk = (int64_t)info->chunk_pages * kPageSize, splits = info->max_units_per_request;
-  const int64_t pairs = (int64_t)info->batch * info->num_kv_heads;
-  const TreeClusters c{grow(info->num_units, chunk, false), false};
-  if (splits < 2 || pairs * blocks * cfg.value_parts > info->num_sms) return c;
-  // In eighths of a tile (1.1 us): a fold takes 2.5 tiles, and 0.37 for each state of 64 rows of
-  // 128 dims; finding a pair's units takes one.
+  const int64_t pairs = (int64_t)info->batch * info->num_kv_heads, longest = chunk * splits;
+  TreeClusters best{grow(info->num_units, chunk, false), false, false};
+  if (pairs * blocks * cfg.value_parts > info->num_sms) return best;
+  // In eighths of a tile (1.1 us): a CTA starts and ends in 7 tiles, one that finds its pair's
+  // units in 8, one of several waves in 14; a fold takes 2.5, and 0.37 for each state of 64
+  // rows of 128 dims; the last CTAs of several waves end an eighth late.
   const int64_t rows = std::min<int64_t>(kTreeRows, (int64_t)info->row_blocks * info->rows_per_block);
-  const int64_t fold = 20 + 3 * splits * rows * info->head_dim_vo / 8192;
-  const int ctas = grow(pairs, chunk * splits, true);
-  if (8 * tiles(chunk * splits, ctas) + 8 > 8 * tiles(chunk, c.ctas) + fold) return c;
-  return {ctas, true};
+  const int64_t fold = splits < 2 ? 0 : 20 + 3 * splits * rows * info->head_dim_vo / 8192;
+  int64_t least = 8 * (tiles(chunk, best.ctas) + 7) + fold;
+  const int ctas = grow(pairs, longest, true);
+  const int64_t whole = 8 * (tiles(longest, ctas) + 8);
+  if (splits > 1 && whole <= least) {
+    least = whole;
+    best = {ctas, true, false};
+  }
+  const int64_t mean = info->total_kv_pages * info->page_size / info->batch;
+  for (int n = 2 * cfg.value_parts; n <= 8 && info->num_units <= kTreeSorted; n *= 2) {
+    const int64_t all = pairs * blocks * n;
+    if (all <= info->num_sms) continue;
+    const int64_t cost =
+        std::max(all * (tiles(mean, n) + 14) * 9 / info->num_sms, 8 * (tiles(longest, n) + 8));
+    if (cost < least) {
+      least = cost;
+      best = {n, true, true};
+    }
+  }
+  return best;
 }
 
 int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_tok,
@@ -908,6 +930,7 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
     const int blocks = (info->row_blocks * info->rows_per_block + kTreeRows - 1) / kTreeRows;
     const TreeClusters c = tree_clusters(info, tcfg, blocks);
     p.tree_whole = c.whole ? info->num_units : 0;
+    p.tree_sorted = c.sorted;
     e = launch_attend_tree(tcfg, p, c.whole ? info->batch * info->num_kv_heads : info->num_units,
                            blocks, c.ctas, stream);
   } else {

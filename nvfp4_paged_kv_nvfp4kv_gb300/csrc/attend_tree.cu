@@ -25,13 +25,13 @@
 //
 // The plan splits long requests for its own row blocks; here a cluster of CTAs divides a
 // unit's tokens (and value dims) further, as many as the SMs allow, or those of all units of
-// a request and kv head, and joins its states through distributed shared memory: no workspace
+// a request and kv head (uneven batches: in several waves, the longest first), and joins its states through distributed shared memory: no workspace
 // beyond the plan's is needed, and each CTA stores a share of the rows.  Units of a split
 // request that a cluster does not take as one fold as elsewhere (log-sum-exp over partial
 // states, by the last CTA to arrive: 2.8 us, and 0.4 for each state of 64 rows).
 // Every wait is bounded; one that runs out sets flag 0x4 and the CTA winds down.
 //
-// Measured (replayed): 4 requests x 32771 tokens, 104 rows of 8 kv heads (128/128) 79 us, 700
+// Measured (replayed): 4 requests x 32771 tokens, 104 rows of 8 kv heads (128/128) 78 us, 720
 // TFLOP/s of the rows that are there; 16 requests of 512-4096 tokens x 64 rows 39 us; 8
 // requests of 2048-8192 tokens x 48-88 rows (512/256) 45 us.  Neither memory (1.9 TB/s) nor
 // the tensor cores (a third busy) are full: the softmax warps' chain of a tile (wait, load,
@@ -298,6 +298,26 @@ __device__ __forceinline__ void load_tiles(const AttendParams& p, const WorkUnit
   cp_async_wait<0>();
 }
 
+// The first unit of a pair of request and kv head (-1: none): the pair of this number, or
+// (sorted) the one that as many are longer than.  `len`: room for a word a unit.  (A function
+// of its own: inlined, it costs the loop over the tiles registers, 78 -> 83 us on 4 x 32771
+// tokens.  The append or the fold of their own cost as much: 79 and 91 us.)
+__device__ __noinline__ int first_unit(const WorkUnit* units, int num, int number, bool sorted,
+                                       int* len, int* found) {
+  if (threadIdx.x == 0) *found = -1;
+  for (int i = threadIdx.x; sorted && i < num; i += blockDim.x)
+    len[i] = units[i].split == 0 ? units[i].kv_len : -1;
+  __syncthreads();
+  for (int i = threadIdx.x; i < num; i += blockDim.x) {
+    if (units[i].split != 0) continue;
+    int at = sorted ? 0 : units[i].pair;
+    for (int k = 0; sorted && k < num; ++k) at += len[k] > len[i] || (len[k] == len[i] && k < i);
+    if (at == number) *found = i;
+  }
+  __syncthreads();
+  return *found;
+}
+
 template <int DK, int DVC, int VH, int TT, bool ONE>
 __global__ void __launch_bounds__(Tree<DK, DVC, VH, TT, ONE>::THREADS, 1)
     attend_tree_kernel(const AttendParams p) {
@@ -328,13 +348,9 @@ __global__ void __launch_bounds__(Tree<DK, DVC, VH, TT, ONE>::THREADS, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int unit = blockIdx.x;
-  if (p.tree_whole > 0) {  // of the pair's units the first, which the cluster takes for all
-    if (tid == 0) *s_last = -1;
-    __syncthreads();
-    for (int i = tid; i < p.tree_whole; i += kThreads)
-      if (p.units[i].pair == unit && p.units[i].split == 0) *s_last = i;
-    __syncthreads();
-    unit = *s_last;
+  if (p.tree_whole > 0) {
+    unit = first_unit(p.units, p.tree_whole, unit, p.tree_sorted, reinterpret_cast<int*>(smem),
+                      s_last);
     if (unit < 0) return;  // a request without rows
   }
   WorkUnit u = load_unit(p, unit, tid == 0);

@@ -88,7 +88,8 @@ struct AttendParams {
   int32_t tree_words;
   int32_t tree_ctas;   // attend_tree: CTAs of a cluster, which share a unit's tokens,
   int32_t tree_whole;  // the plan's units where a cluster takes a whole pair's, else 0
-  int32_t row_blocks;  // and the plan's row blocks (merge counters of a pair)
+  int32_t tree_sorted;  // whether those are started longest first
+  int32_t row_blocks;   // the plan's row blocks (merge counters of a pair)
 };
 
 struct AppendParams {

@@ -281,3 +281,14 @@ def test_two_streams_at_once():
     for (_, plan, o, lse, _, _), got in zip(cases, outs):
         assert torch.equal(got[0], o) and torch.equal(got[1], lse)
         assert N.nvfp4kv_workspace_flags(plan) == 0
+
+
+@pytest.mark.parametrize("dk,dv,hq,hkv,new,batch,most", [
+    (128, 128, 16, 2, 10, 60, 5000), (64, 64, 32, 8, 9, 16, 8192), (512, 256, 16, 2, 8, 30, 8192)])
+def test_uneven_batches_in_several_waves(dk, dv, hq, hkv, new, batch, most):
+    """Requests of very unequal lengths, one without rows and equal ones among them: clusters
+    of whole requests, the longest first, in more than one wave (checked are a few)."""
+    rng = np.random.default_rng(dk)
+    kv = [int(x) for x in rng.integers(300, most, batch - 3)] + [1500, 1500, 77]
+    n = [new] * (batch - 1) + [0]
+    tree_case(kv, n, hq, hkv, dk, dv, seed=dv, only=(0, 5, 11, batch - 3, batch - 2))
