@@ -26,7 +26,8 @@
 // 5.6 TB/s (0.84 of a plain copy); 211 tokens x 18 heads of 256, a quarter in pairs, f16,
 // 3.8 us.  Loads in batches of three 66 us, of two 73 (and 85 with a token's heads on two
 // warps: the angles and weights are then formed twice); two or four heads in the ring 63
-// and 64; chunks of 8 bytes, half the registers and more warps, 66.
+// and 64; chunks of 8 bytes, half the registers and more warps, 66; loads that stay out of L1
+// 62, streaming stores 60.2.
 #include <cstdint>
 
 #include <cuda_runtime.h>
