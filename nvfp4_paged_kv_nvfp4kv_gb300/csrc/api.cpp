@@ -783,6 +783,7 @@ struct NewTokens {
 struct TreeClusters {
   int ctas;
   bool whole, sorted;
+  int64_t tokens;  // of a CTA, at most
 };
 constexpr int64_t kTreeTiles = 2;  // tiles of a whole unit that a CTA keeps
 constexpr int kTreeSorted = 512;   // units among which a CTA finds its own by rank
@@ -804,19 +805,20 @@ TreeClusters tree_clusters(const nvfp4kv_plan_info* info, const TreeConfig& cfg,
   };
   const int64_t chunk = (int64_t)info->chunk_pages * kPageSize, splits = info->max_units_per_request;
   const int64_t pairs = (int64_t)info->batch * info->num_kv_heads, longest = chunk * splits;
-  TreeClusters best{grow(info->num_units, chunk, false), false, false};
+  TreeClusters best{grow(info->num_units, chunk, false), false, false, chunk};
   if (pairs * blocks * cfg.value_parts > info->num_sms) return best;
   // In eighths of a tile (1.1 us): a CTA starts and ends in 7 tiles, one that finds its pair's
   // units in 8, one of several waves in 14; a fold takes 2.5, and 0.37 for each state of 64
   // rows of 128 dims; the last CTAs of several waves end an eighth late.
   const int64_t rows = std::min<int64_t>(kTreeRows, (int64_t)info->row_blocks * info->rows_per_block);
   const int64_t fold = splits < 2 ? 0 : 20 + 3 * splits * rows * info->head_dim_vo / 8192;
-  int64_t least = 8 * (tiles(chunk, best.ctas) + 7) + fold;
+  const int64_t waves = ((int64_t)info->num_units * blocks * best.ctas + info->num_sms - 1) / info->num_sms;
+  int64_t least = 8 * waves * (tiles(chunk, best.ctas) + 7) + fold;
   const int ctas = grow(pairs, longest, true);
   const int64_t whole = 8 * (tiles(longest, ctas) + 8);
   if (splits > 1 && whole <= least) {
     least = whole;
-    best = {ctas, true, false};
+    best = {ctas, true, false, tiles(longest, ctas) * cfg.tile_tokens};
   }
   const int64_t mean = info->total_kv_pages * info->page_size / info->batch;
   for (int n = 2 * cfg.value_parts; n <= 8 && info->num_units <= kTreeSorted; n *= 2) {
@@ -826,7 +828,7 @@ TreeClusters tree_clusters(const nvfp4kv_plan_info* info, const TreeConfig& cfg,
         std::max(all * (tiles(mean, n) + 14) * 9 / info->num_sms, 8 * (tiles(longest, n) + 8));
     if (cost < least) {
       least = cost;
-      best = {n, true, true};
+      best = {n, true, true, tiles(longest, n) * cfg.tile_tokens};
     }
   }
   return best;
@@ -871,17 +873,30 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
                    attend_config_dec(info->head_dim_qk, info->head_dim_vo, 8,
                                      info->num_units <= info->num_sms ? 1 : 4, &cfg);
   // trees: more than 16 rows a kv head go to the kernel of 128-row blocks (it takes a plan
-  // of either kernel), up to 16 to the mma.sync kernel's own form.  Measured, the former for
+  // of either kernel), up to 16 to the mma.sync kernel's own form; but 9 to 16 rows where a
+  // cluster takes a whole request of few tokens a CTA (16 rows, 8 kv heads, the former for the
+  // latter, us: 128/128 heads, one request of 300 tokens 10 / 12, 4096 14 / 21, 4 of 2000 14 /
+  // 17.5, 8 of 4000 33 / 30; 256/256, 1000 13 / 23; 512/256, 1000 15 / 22; 64/64, 300 9 / 8.5,
+  // 1000 10 / 9.6).  Measured, the former for
   // the latter, us: 16 requests of 512-4096 tokens x 16 rows 34 / 32, x 20 rows 36 / 61, x 64
   // 39 / 95; 4 x 32771 tokens x 16 rows 71 / 67, x 20 rows 72 / 127; 512/256 heads x 32 rows
-  // 35 / 61; 64/64 heads x 20 and 32 rows 30 / 26 to 70 / 83 (the plan counts on more than
-  // one CTA an SM), x 36 rows 20 / 34.
+  // 35 / 61; 64/64 heads x 20 rows 20 / 26, 56 / 66 and 69 / 83, two requests of 500 10 / 9.
   TreeConfig tcfg{};
-  const bool wide_tree = tree && (info->kernel == kKernelTcgen05 || info->row_blocks > 1) &&
-                         attend_config_tree(info->head_dim_qk, info->head_dim_vo, &tcfg);
+  TreeClusters clusters{};
+  const int tree_blocks = (info->row_blocks * info->rows_per_block + kTreeRows - 1) / kTreeRows;
+  bool wide_tree = tree && (info->rows_per_block > 8 || info->row_blocks > 1) &&
+                   attend_config_tree(info->head_dim_qk, info->head_dim_vo, &tcfg);
   if (wide_tree) {
-    cfg.func = tcfg.func;
-    cfg.smem_bytes = tcfg.smem_bytes;
+    AttendConfig wide{};
+    wide.func = tcfg.func;
+    wide.smem_bytes = tcfg.smem_bytes;
+    if (cudaError_t e = prepare_kernel(wide)) return cuda_fail(e, "kernel attributes");
+    clusters = tree_clusters(info, tcfg, tree_blocks);
+    const int dk = info->head_dim_qk;
+    wide_tree = info->kernel == kKernelTcgen05 || info->row_blocks > 1 ||
+                (dk >= 128 && clusters.whole && !clusters.sorted &&
+                 clusters.tokens <= std::min(4 * dk, 1024));
+    if (wide_tree) cfg = wide;
   }
   if (!dec && !wide_tree && !lookup_kernel(info->kernel, info->head_dim_qk, info->head_dim_vo,
                              info->page_size, info->rows_per_block, &cfg, tree != nullptr))
@@ -927,12 +942,10 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
     p.new_v = nullptr;
   }
   if (wide_tree) {
-    const int blocks = (info->row_blocks * info->rows_per_block + kTreeRows - 1) / kTreeRows;
-    const TreeClusters c = tree_clusters(info, tcfg, blocks);
-    p.tree_whole = c.whole ? info->num_units : 0;
-    p.tree_sorted = c.sorted;
-    e = launch_attend_tree(tcfg, p, c.whole ? info->batch * info->num_kv_heads : info->num_units,
-                           blocks, c.ctas, stream);
+    p.tree_whole = clusters.whole ? info->num_units : 0;
+    p.tree_sorted = clusters.sorted;
+    const int grid = clusters.whole ? info->batch * info->num_kv_heads : info->num_units;
+    e = launch_attend_tree(tcfg, p, grid, tree_blocks, clusters.ctas, stream);
   } else {
     e = launch_attend(cfg, p, info->num_units, info->row_blocks, stream);
   }

@@ -1,5 +1,6 @@
 // attend_tree.cu -- attention of drafted trees over the paged NVFP4 cache on the
-// fifth-generation tensor cores, for more than 16 query rows a kv head, sm_103a.
+// fifth-generation tensor cores, for more than 16 query rows a kv head and, of few short
+// requests, more than 8, sm_103a.
 //
 // Row r (a node of request b's tree and a head of the kv head's group) sees token t where
 //   t < L_b - n_b                       (before the tree), or

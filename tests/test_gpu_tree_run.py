@@ -157,13 +157,15 @@ def test_queries_of_all_sizes(kernel, q_scale):
 
 def test_a_chain_is_the_causal_mask():
     """A tree without branches is the causal mask: up to 16 rows a kv head it runs in the
-    causal plan's kernel and gives the same bits."""
+    causal plan's kernel (with one SM: no cluster takes a whole request) and gives the same
+    bits."""
     kv, new = (37, 300, 64), (4, 1, 3)
     chains = [T.mask_words(T.ancestors(range(-1, n - 1)), 2) for n in new]
     c, plan, out, lse, q, _ = tree_case(kv, new, 8, 2, 128, 128, masks=chains, words=2, kernel=1,
-                                        seed=11)
+                                        num_sms=1, seed=11)
     qo = np.concatenate([[0], np.cumsum(new)])
-    causal = N.nvfp4kv_decode_plan(qo, c.indptr, c.last, 8, 2, 128, 128, kernel=1, causal=True)
+    causal = N.nvfp4kv_decode_plan(qo, c.indptr, c.last, 8, 2, 128, 128, kernel=1, causal=True,
+                                   num_sms=1)
     assert plan.info.rows_per_block == 16
     o2, l2 = N.nvfp4kv_decode_run(causal, q, c.cache, c.kv_indices)
     assert torch.equal(out, o2) and torch.equal(lse, l2)
