@@ -877,14 +877,15 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
   // cluster takes a whole request of few tokens a CTA (16 rows, 8 kv heads, the former for the
   // latter, us: 128/128 heads, one request of 300 tokens 10 / 12, 4096 14 / 21, 4 of 2000 14 /
   // 17.5, 8 of 4000 33 / 30; 256/256, 1000 13 / 23; 512/256, 1000 15 / 22; 64/64, 300 9 / 8.5,
-  // 1000 10 / 9.6).  Measured, the former for
-  // the latter, us: 16 requests of 512-4096 tokens x 16 rows 34 / 32, x 20 rows 36 / 61, x 64
-  // 39 / 95; 4 x 32771 tokens x 16 rows 71 / 67, x 20 rows 72 / 127; 512/256 heads x 32 rows
-  // 35 / 61; 64/64 heads x 20 rows 20 / 26, 56 / 66 and 69 / 83, two requests of 500 10 / 9.
+  // 1000 10 / 9.6).  Other batches, the former / the latter: 16 requests of 512-4096 tokens x 16
+  // rows 34 / 32, x 20 rows 36 / 61, x 64 39 / 95; 4 x 32771 tokens x 16 rows 71 / 67, x 20 rows
+  // 72 / 127; 512/256 heads x 32 rows 35 / 61; 64/64 heads x 20 rows 20 / 26, 56 / 66 and 69 /
+  // 83, two requests of 500 10 / 9.
   TreeConfig tcfg{};
   TreeClusters clusters{};
   const int tree_blocks = (info->row_blocks * info->rows_per_block + kTreeRows - 1) / kTreeRows;
-  bool wide_tree = tree && (info->rows_per_block > 8 || info->row_blocks > 1) &&
+  const bool large = info->kernel == kKernelTcgen05 || info->row_blocks > 1;
+  bool wide_tree = tree && (large || info->rows_per_block > 8) &&
                    attend_config_tree(info->head_dim_qk, info->head_dim_vo, &tcfg);
   if (wide_tree) {
     AttendConfig wide{};
@@ -893,9 +894,8 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
     if (cudaError_t e = prepare_kernel(wide)) return cuda_fail(e, "kernel attributes");
     clusters = tree_clusters(info, tcfg, tree_blocks);
     const int dk = info->head_dim_qk;
-    wide_tree = info->kernel == kKernelTcgen05 || info->row_blocks > 1 ||
-                (dk >= 128 && clusters.whole && !clusters.sorted &&
-                 clusters.tokens <= std::min(4 * dk, 1024));
+    wide_tree = large || (dk >= 128 && clusters.whole && !clusters.sorted &&
+                          clusters.tokens <= std::min(4 * dk, 1024));
     if (wide_tree) cfg = wide;
   }
   if (!dec && !wide_tree && !lookup_kernel(info->kernel, info->head_dim_qk, info->head_dim_vo,
