@@ -671,19 +671,22 @@ int nvfp4kv_e4m3_compact_tokens(const nvfp4kv_e4m3_cache* cache, const int32_t* 
  * nvfp4kv_build_page_table takes off it.  The block table, its rows and kv_len are those
  * of nvfp4kv_build_page_table (kv_len of the rows' requests, 0 for a row without one).
  *
- * Fork requests: row children[f] of the table becomes a request of kv_len[parents[f]]
- * tokens that shares the whole pages of row parents[f] and, where the last page is not
- * full, gets a new one off the free list, in the order of the forks.  kv_len[children[f]]
- * is set; (copy_src[f], copy_dst[f]) is the parent's last page and the new one, for
- * nvfp4kv_copy_pages on the cache of every layer, or (-1, -1).
+ * Fork requests: row children[f] of the table, which is empty (kv_len 0: a request there
+ * is released first), becomes a request of kv_len[parents[f]] tokens that shares the whole
+ * pages of row parents[f] and, where the last page is not full, gets a new one off the free
+ * list, in the order of the forks.  kv_len[children[f]] is set; (copy_src[f], copy_dst[f])
+ * is the parent's last page and the new one, for nvfp4kv_copy_pages on the cache of every
+ * layer, or (-1, -1).
  *   num_forks at most 8192, num_rows (of the table and kv_len) at most 65536; a parent may
- *             be forked several times, a child's row must not appear twice;
+ *             be forked several times, a child's row must not appear twice; a call shares
+ *             at most 2^31 - 1 pages, counted once a fork;
  *   free_head [dev, 1] and free_head_out [dev, 1]: two words, as in
  *             nvfp4kv_build_page_table.
- * A row out of range, twice a child or child and parent, or a length that cannot be, sets
- * NVFP4KV_FLAG_BAD_LENGTH, a free list that is too short NVFP4KV_FLAG_TABLE_FULL; then
- * nothing else is written.  A page id out of the pool is passed on and sets
- * NVFP4KV_FLAG_BAD_PAGE_INDEX.  One launch; can be captured in a CUDA graph. */
+ * A row out of range, twice a child, child and parent or a child that is not empty, or a
+ * length that cannot be, sets NVFP4KV_FLAG_BAD_LENGTH, a free list that is too short or too
+ * many pages NVFP4KV_FLAG_TABLE_FULL; then nothing else is written.  A page id out of the
+ * pool is passed on and sets NVFP4KV_FLAG_BAD_PAGE_INDEX.  One launch where num_forks *
+ * max_pages_per_request is below 32768, else two; can be captured in a CUDA graph. */
 int nvfp4kv_fork_pages(const int32_t* parents, const int32_t* children, int32_t num_forks,
                        int32_t* kv_len, int32_t num_rows, int32_t page_size,
                        int32_t* block_table, int64_t block_table_stride,

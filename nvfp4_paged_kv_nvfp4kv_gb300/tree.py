@@ -211,12 +211,13 @@ def _word(*heads):
 def nvfp4kv_fork_pages(parents, children, kv_len, block_table, page_shares, free_pages,
                        free_head, free_head_out, copy_src, copy_dst, page_size: int = 16,
                        device_flags=None, stream=None):
-    """Make rows ``children`` [forks] of the block table requests that share the whole
-    pages of rows ``parents`` [forks]; a last page that is not full is replaced by a new
-    one off the free list, and the pair stands in ``copy_src`` / ``copy_dst`` [forks] (-1
-    where there is none) for ``nvfp4kv_copy_pages`` on every layer's cache.  ``kv_len``
-    [rows] and ``page_shares`` [pages of the pool] (owners beyond the first) are updated;
-    ``free_head`` [1] is read, ``free_head_out`` [1], another word, is written."""
+    """Make rows ``children`` [forks] of the block table, which are empty (``kv_len`` 0:
+    release what is there first), requests that share the whole pages of rows ``parents``
+    [forks]; a last page that is not full is replaced by a new one off the free list, and
+    the pair stands in ``copy_src`` / ``copy_dst`` [forks] (-1 where there is none) for
+    ``nvfp4kv_copy_pages`` on every layer's cache.  ``kv_len`` [rows] and ``page_shares``
+    [pages of the pool] (owners beyond the first) are updated; ``free_head`` [1] is read,
+    ``free_head_out`` [1], another word, is written."""
     _i32("the lists", parents, children, kv_len, page_shares, free_pages, free_head,
          free_head_out, copy_src, copy_dst)
     forks, rows = parents.numel(), kv_len.numel()
