@@ -638,6 +638,18 @@ int nvfp4kv_tree_run(const nvfp4kv_plan_info* info, const uint32_t* tree_mask, i
                      void* workspace, uint64_t workspace_bytes, void* out_bf16, float* lse,
                      cudaStream_t stream);
 
+/* How nvfp4kv_tree_run runs a plan on the current device; nothing is launched. */
+typedef struct nvfp4kv_tree_launch {
+  int32_t block_rows;      /* query rows of a block: the plan's, or 128; 0: no rows     */
+  int32_t row_blocks;
+  int32_t cluster_ctas;    /* CTAs that share a unit's tokens and value dims, of which  */
+  int32_t value_ctas;      /* so many share the value dims                              */
+  int32_t whole_requests;  /* a cluster takes all units of a request and kv head        */
+  int32_t longest_first;   /* in several waves, the longest first                       */
+  int32_t folded;          /* units leave partial states, which the last one folds      */
+} nvfp4kv_tree_launch;
+int nvfp4kv_tree_form(const nvfp4kv_plan_info* info, nvfp4kv_tree_launch* form);
+
 /* The accepted tokens moved together: with n_b = qo_indptr[b + 1] - qo_indptr[b] drafted
  * tokens at the end of request b's L_b (the page table of the step), the token at
  * position L_b - n_b + path[b][i] goes to L_b - n_b + i for i < num_kept[b], as if all

@@ -14,4 +14,5 @@ from .step import (E4m3Cache, RopePlan, StepTable, nvfp4kv_build_page_table,  # 
                    nvfp4kv_rope, nvfp4kv_rope_plan)
 from .tree import (nvfp4kv_compact_tokens, nvfp4kv_copy_pages,  # noqa: F401
                    nvfp4kv_e4m3_compact_tokens, nvfp4kv_e4m3_copy_pages, nvfp4kv_fork_pages,
-                   nvfp4kv_release_pages, nvfp4kv_tree_masks, nvfp4kv_tree_run)
+                   nvfp4kv_release_pages, nvfp4kv_tree_form, nvfp4kv_tree_masks,
+                   nvfp4kv_tree_run)

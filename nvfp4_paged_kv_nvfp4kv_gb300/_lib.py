@@ -90,6 +90,12 @@ class E4m3CacheStruct(C.Structure):
                                  "head_dim_qk", "head_dim_vo")]
 
 
+class TreeLaunch(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in (
+        "block_rows", "row_blocks", "cluster_ctas", "value_ctas", "whole_requests",
+        "longest_first", "folded")]
+
+
 _vp, _i32, _i64, _u64, _f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_uint64, C.c_float
 SIGNATURES = {
     "nvfp4kv_status_string": (C.c_char_p, [C.c_int]),
@@ -140,6 +146,7 @@ SIGNATURES = {
     "nvfp4kv_tree_run": (C.c_int, [
         C.POINTER(PlanInfo), _vp, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64,
         C.POINTER(PagedCacheStruct), _vp, _f32, _vp, _u64, _vp, _vp, _vp]),
+    "nvfp4kv_tree_form": (C.c_int, [C.POINTER(PlanInfo), C.POINTER(TreeLaunch)]),
     "nvfp4kv_compact_tokens": (C.c_int, [
         C.POINTER(PagedCacheStruct), _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp]),
     "nvfp4kv_e4m3_compact_tokens": (C.c_int, [

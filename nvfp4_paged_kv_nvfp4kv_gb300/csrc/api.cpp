@@ -834,6 +834,49 @@ TreeClusters tree_clusters(const nvfp4kv_plan_info* info, const TreeConfig& cfg,
   return best;
 }
 
+// Trees: more than 16 rows a kv head go to the kernel of 128-row blocks (it takes a plan
+// of either kernel), up to 16 to the mma.sync kernel's own form; but 9 to 16 rows where a
+// cluster takes a whole request of few tokens a CTA (16 rows, 8 kv heads, the former for the
+// latter, us: 128/128 heads, one request of 300 tokens 10 / 12, 4096 14 / 21, 4 of 2000 14 /
+// 17.5, 8 of 4000 33 / 30; 256/256, 1000 13 / 23; 512/256, 1000 15 / 22; 64/64, 300 9 / 8.5,
+// 1000 10 / 9.6).  Other batches, the former / the latter: 16 requests of 512-4096 tokens x 16
+// rows 34 / 32, x 20 rows 36 / 61, x 64 39 / 95; 4 x 32771 tokens x 16 rows 71 / 67, x 20 rows
+// 72 / 127; 512/256 heads x 32 rows 35 / 61; 64/64 heads x 20 rows 20 / 26, 56 / 66 and 69 /
+// 83, two requests of 500 10 / 9.
+struct TreeLaunch {
+  bool wide;  // the kernel of 128-row blocks, in the form that follows
+  TreeConfig cfg;
+  TreeClusters clusters;
+  int blocks;
+};
+int tree_launch_of(const nvfp4kv_plan_info* info, TreeLaunch* t) {
+  *t = TreeLaunch{};
+  const bool large = info->kernel == kKernelTcgen05 || info->row_blocks > 1;
+  TreeConfig cfg{};
+  if ((!large && info->rows_per_block <= 8) ||
+      !attend_config_tree(info->head_dim_qk, info->head_dim_vo, &cfg))
+    return NVFP4KV_OK;
+  AttendConfig wide{};
+  wide.func = cfg.func;
+  wide.smem_bytes = cfg.smem_bytes;
+  if (cudaError_t e = prepare_kernel(wide)) return cuda_fail(e, "kernel attributes");
+  const int blocks = (info->row_blocks * info->rows_per_block + kTreeRows - 1) / kTreeRows;
+  const TreeClusters clusters = tree_clusters(info, cfg, blocks);
+  const int dk = info->head_dim_qk;
+  if (large || (dk >= 128 && clusters.whole && !clusters.sorted &&
+                clusters.tokens <= std::min(4 * dk, 1024)))
+    *t = TreeLaunch{true, cfg, clusters, blocks};
+  return NVFP4KV_OK;
+}
+
+// What a tree run asks of its plan.
+int check_tree_plan(const nvfp4kv_plan_info* info) {
+  if (info->kernel != kKernelTensorCore && info->kernel != kKernelTcgen05)
+    return fail(NVFP4KV_ERR_UNSUPPORTED, "trees run in the tensor-core kernels (plan option "
+                "kernel 0, 1 or 3)");
+  return NVFP4KV_OK;
+}
+
 int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_tok,
            int64_t q_stride_head, const nvfp4kv_paged_cache* cache, const int32_t* kv_indices,
            float sm_scale, void* workspace, uint64_t workspace_bytes, void* out_bf16,
@@ -842,9 +885,7 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
                          workspace, workspace_bytes, out_bf16))
     return st;
   if (tree) {
-    if (info->kernel != kKernelTensorCore && info->kernel != kKernelTcgen05)
-      return fail(NVFP4KV_ERR_UNSUPPORTED, "trees run in the tensor-core kernels (plan option "
-                  "kernel 0, 1 or 3)");
+    if (int st = check_tree_plan(info)) return st;
     if (tree->words < 1 || tree->words > kMaxTreeNodes / 32)
       return fail(NVFP4KV_ERR_UNSUPPORTED, "mask_words %d (1 to %d)", tree->words,
                   kMaxTreeNodes / 32);
@@ -872,34 +913,16 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
                    info->page_size == kPageSize && bulk_decode_layout(cache) &&
                    attend_config_dec(info->head_dim_qk, info->head_dim_vo, 8,
                                      info->num_units <= info->num_sms ? 1 : 4, &cfg);
-  // trees: more than 16 rows a kv head go to the kernel of 128-row blocks (it takes a plan
-  // of either kernel), up to 16 to the mma.sync kernel's own form; but 9 to 16 rows where a
-  // cluster takes a whole request of few tokens a CTA (16 rows, 8 kv heads, the former for the
-  // latter, us: 128/128 heads, one request of 300 tokens 10 / 12, 4096 14 / 21, 4 of 2000 14 /
-  // 17.5, 8 of 4000 33 / 30; 256/256, 1000 13 / 23; 512/256, 1000 15 / 22; 64/64, 300 9 / 8.5,
-  // 1000 10 / 9.6).  Other batches, the former / the latter: 16 requests of 512-4096 tokens x 16
-  // rows 34 / 32, x 20 rows 36 / 61, x 64 39 / 95; 4 x 32771 tokens x 16 rows 71 / 67, x 20 rows
-  // 72 / 127; 512/256 heads x 32 rows 35 / 61; 64/64 heads x 20 rows 20 / 26, 56 / 66 and 69 /
-  // 83, two requests of 500 10 / 9.
-  TreeConfig tcfg{};
-  TreeClusters clusters{};
-  const int tree_blocks = (info->row_blocks * info->rows_per_block + kTreeRows - 1) / kTreeRows;
-  const bool large = info->kernel == kKernelTcgen05 || info->row_blocks > 1;
-  bool wide_tree = tree && (large || info->rows_per_block > 8) &&
-                   attend_config_tree(info->head_dim_qk, info->head_dim_vo, &tcfg);
-  if (wide_tree) {
-    AttendConfig wide{};
-    wide.func = tcfg.func;
-    wide.smem_bytes = tcfg.smem_bytes;
-    if (cudaError_t e = prepare_kernel(wide)) return cuda_fail(e, "kernel attributes");
-    clusters = tree_clusters(info, tcfg, tree_blocks);
-    const int dk = info->head_dim_qk;
-    wide_tree = large || (dk >= 128 && clusters.whole && !clusters.sorted &&
-                          clusters.tokens <= std::min(4 * dk, 1024));
-    if (wide_tree) cfg = wide;
+  TreeLaunch launch{};
+  if (tree)
+    if (int st = tree_launch_of(info, &launch)) return st;
+  if (launch.wide) {
+    cfg.func = launch.cfg.func;
+    cfg.smem_bytes = launch.cfg.smem_bytes;
   }
-  if (!dec && !wide_tree && !lookup_kernel(info->kernel, info->head_dim_qk, info->head_dim_vo,
-                             info->page_size, info->rows_per_block, &cfg, tree != nullptr))
+  if (!dec && !launch.wide &&
+      !lookup_kernel(info->kernel, info->head_dim_qk, info->head_dim_vo, info->page_size,
+                     info->rows_per_block, &cfg, tree != nullptr))
     return fail(NVFP4KV_ERR_UNSUPPORTED, "planned kernel not available");
   cudaError_t e = prepare_kernel(cfg);
   if (e != cudaSuccess) return cuda_fail(e, "kernel attributes");
@@ -941,11 +964,12 @@ int attend(const nvfp4kv_plan_info* info, const void* q_bf16, int64_t q_stride_t
     p.new_k = nullptr;
     p.new_v = nullptr;
   }
-  if (wide_tree) {
-    p.tree_whole = clusters.whole ? info->num_units : 0;
-    p.tree_sorted = clusters.sorted;
-    const int grid = clusters.whole ? info->batch * info->num_kv_heads : info->num_units;
-    e = launch_attend_tree(tcfg, p, grid, tree_blocks, clusters.ctas, stream);
+  if (launch.wide) {
+    const TreeClusters& c = launch.clusters;
+    p.tree_whole = c.whole ? info->num_units : 0;
+    p.tree_sorted = c.sorted;
+    const int grid = c.whole ? info->batch * info->num_kv_heads : info->num_units;
+    e = launch_attend_tree(launch.cfg, p, grid, launch.blocks, c.ctas, stream);
   } else {
     e = launch_attend(cfg, p, info->num_units, info->row_blocks, stream);
   }
@@ -1044,6 +1068,25 @@ int nvfp4kv_tree_run(const nvfp4kv_plan_info* info, const uint32_t* tree_mask, i
   return attend(info, q_bf16, q_stride_tok, q_stride_head, cache, kv_indices, sm_scale,
                 workspace, workspace_bytes, out_bf16, lse, stream, new_k_bf16 ? &nt : nullptr,
                 &tree);
+}
+
+int nvfp4kv_tree_form(const nvfp4kv_plan_info* info, nvfp4kv_tree_launch* form) {
+  if (!info || info->magic != kPlanMagic)
+    return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "info is not a plan");
+  if (!form) return fail(NVFP4KV_ERR_INVALID_ARGUMENT, "form is null");
+  if (int st = check_tree_plan(info)) return st;
+  *form = nvfp4kv_tree_launch{};
+  if (info->num_units == 0) return ok();
+  TreeLaunch t{};
+  if (int st = tree_launch_of(info, &t)) return st;
+  form->block_rows = t.wide ? kTreeRows : info->rows_per_block;
+  form->row_blocks = t.wide ? t.blocks : info->row_blocks;
+  form->cluster_ctas = t.wide ? t.clusters.ctas : 1;
+  form->value_ctas = t.wide ? t.cfg.value_parts : 1;
+  form->whole_requests = t.wide && t.clusters.whole;
+  form->longest_first = t.wide && t.clusters.sorted;
+  form->folded = info->split && !form->whole_requests;
+  return ok();
 }
 
 int nvfp4kv_decode_merge(const nvfp4kv_plan_info* info, void* workspace,

@@ -12,11 +12,11 @@ from typing import Optional
 
 import torch
 
-from ._lib import check
+from ._lib import TreeLaunch, check
 from .api import PagedCache, Plan
 from .step import E4m3Cache, _check_device, _empty, _entry, _flag_ptr, _stream_of
 
-__all__ = ["nvfp4kv_tree_masks", "nvfp4kv_tree_run", "nvfp4kv_compact_tokens",
+__all__ = ["nvfp4kv_tree_masks", "nvfp4kv_tree_run", "nvfp4kv_tree_form", "nvfp4kv_compact_tokens",
            "nvfp4kv_e4m3_compact_tokens", "nvfp4kv_fork_pages", "nvfp4kv_copy_pages",
            "nvfp4kv_e4m3_copy_pages", "nvfp4kv_release_pages"]
 
@@ -150,6 +150,15 @@ def nvfp4kv_tree_run(plan: Plan, q, cache: PagedCache, kv_indices, tree_mask,
     if st:
         check(st, "nvfp4kv_tree_run")
     return out, lse
+
+
+def nvfp4kv_tree_form(plan: Plan) -> dict:
+    """How ``nvfp4kv_tree_run`` runs a plan on the current device: ``block_rows``,
+    ``row_blocks``, ``cluster_ctas``, ``value_ctas``, ``whole_requests``, ``longest_first``
+    and ``folded`` of include/nvfp4kv.h.  Nothing is launched."""
+    form = TreeLaunch()
+    check(_entry("nvfp4kv_tree_form")(C.byref(plan.info), C.byref(form)), "nvfp4kv_tree_form")
+    return {name: getattr(form, name) for name, _ in TreeLaunch._fields_}
 
 
 def _compact(name, cache, ref, path, num_kept, qo_indptr, kv_indptr, kv_indices, last_page_len,
