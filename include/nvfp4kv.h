@@ -627,6 +627,7 @@ int nvfp4kv_tree_masks(const int32_t* parents, const int32_t* qo_indptr, const i
  *                 and lse -inf.
  *   new_k, new_v  NULL, or the step's new tokens, quantised into their pages by the same
  *                 launch as in nvfp4kv_decode_append_run.
+ *   out [dev]     4-byte aligned, as in nvfp4kv_decode_run.
  * q and the new tokens are finite, and so are the request's tokens in the cache, as
  * nvfp4kv_quantize_append stores them; slots behind the request's end and pages of others
  * may hold anything. */

@@ -158,6 +158,12 @@ __device__ __forceinline__ void sts_v4(uint32_t a, int off, uint32_t x, uint32_t
                "r"(z), "r"(w)
                : "memory");
 }
+// 4 elements of a row's output (the output is 4-byte aligned)
+__device__ __forceinline__ void store_out4(uint16_t* at, const float4& o, bool f16) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(at);
+  w[0] = pack_out2(o.x, o.y, f16);
+  w[1] = pack_out2(o.z, o.w, f16);
+}
 // a token's scales: 4, 8 or 16 bytes
 template <int N>
 __device__ __forceinline__ void cp_async_sf(uint32_t s, const void* g) {
@@ -868,9 +874,8 @@ __global__ void __launch_bounds__(Tree<DK, DVC, VH, TT, ONE>::THREADS, 1)
             p.partial_o + (u.partial_base + at_head * u.num_splits + u.split) * DV + vh * DVC +
             d) = o;
       else
-        *reinterpret_cast<uint2*>(
-            p.out + ((int64_t)u.qo_begin * p.num_qo_heads + at_head) * DV + vh * DVC + d) =
-            make_uint2(pack_out2(o.x, o.y, p.out_f16), pack_out2(o.z, o.w, p.out_f16));
+        store_out4(p.out + ((int64_t)u.qo_begin * p.num_qo_heads + at_head) * DV + vh * DVC + d,
+                   o, p.out_f16);
     }
     if (parts > 1) {
       __syncwarp();
@@ -929,9 +934,8 @@ __global__ void __launch_bounds__(Tree<DK, DVC, VH, TT, ONE>::THREADS, 1)
     }
     const float inv = M != -INFINITY ? 1.f / L : 0.f;
     const int64_t row = (int64_t)(u.qo_begin + node) * p.num_qo_heads + head;
-    *reinterpret_cast<uint2*>(p.out + row * DV + d) =
-        make_uint2(pack_out2(o.x * inv, o.y * inv, p.out_f16),
-                   pack_out2(o.z * inv, o.w * inv, p.out_f16));
+    store_out4(p.out + row * DV + d, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv),
+               p.out_f16);
     if (d == 0 && p.lse) p.lse[row] = M != -INFINITY ? (M + log2f(L)) * kLn2 : -INFINITY;
   }
 }

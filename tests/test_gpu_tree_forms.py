@@ -40,7 +40,7 @@ def check_rows(got, got_lse, want, dk, tokens, dtype):
 
 
 def run(kv, new, hq, hkv, dk, dv, page=16, layout="HND", out="bf16", seed=0, only=None,
-        **plan_kw):
+        live=False, **plan_kw):
     """One call, checked (the requests of `only`); its plan's form."""
     c = T.Nvfp4Case(kv, page, hkv, dk, dv, layout, seed=seed)
     gen = torch.Generator().manual_seed(seed)
@@ -49,7 +49,10 @@ def run(kv, new, hq, hkv, dk, dv, page=16, layout="HND", out="bf16", seed=0, onl
     words = (max(new) + 31) // 32
     masks = [T.mask_words(T.ancestors(T.random_parents(rng, n)), words) for n in new]
     qo = np.concatenate([[0], np.cumsum(new)])
-    plan = N.nvfp4kv_decode_plan(qo, c.indptr, c.last, hq, hkv, dk, dv, page_size=page,
+    last = [page] * len(kv) if live else c.last
+    if live:
+        plan_kw["device_last_page_len"] = c.last_page_len
+    plan = N.nvfp4kv_decode_plan(qo, c.indptr, last, hq, hkv, dk, dv, page_size=page,
                                  out_dtype=TR.DT[out], **plan_kw)
     mask = TR.i32(np.concatenate(masks))
     o, lse = N.nvfp4kv_tree_run(plan, q, c.cache, c.kv_indices, mask)
@@ -163,8 +166,8 @@ def test_form_of_plans_without_one():
         N.nvfp4kv_tree_form(plan)
 
 
-# the forms above with the step's tokens in the same launch
-APPENDS = [
+# the forms: requests' tokens, their nodes, the plan (see the tests above)
+FORMS = [
     ((37, 300, 30), (2, 2, 1), dict(num_sms=1)), ((37, 300, 30), (4, 3, 4), dict(num_sms=1)),
     ((37, 300, 30), (7, 33, 30), dict()), ((300, 1111), (17, 40), dict(num_sms=1)),
     ((300, 1111), (17, 40), dict(num_sms=1, disable_split=True)), ((8229,), (20,), dict()),
@@ -173,12 +176,12 @@ APPENDS = [
 
 @pytest.mark.parametrize("dk,dv", [(128, 128), (512, 256)])
 @pytest.mark.parametrize("page", [16, 1])
-@pytest.mark.parametrize("at", range(len(APPENDS)))
+@pytest.mark.parametrize("at", range(len(FORMS)))
 def test_new_tokens_in_the_same_launch_change_no_bit(dk, dv, page, at):
     """Cache, out and lse are those of nvfp4kv_quantize_append and a call without new tokens:
     a CTA that read another's token before it was there would read the NaN scales that the
     cache holds in the new tokens' slots."""
-    kv, new, kw = APPENDS[at]
+    kv, new, kw = FORMS[at]
     if not kw.get("disable_split"):
         kw = dict(kw, force_chunk_tokens=4096 if max(kv) > 4096 else 64)
     hkv, seed = 1, 40 + at
@@ -211,6 +214,44 @@ def test_new_tokens_in_the_same_launch_change_no_bit(dk, dv, page, at):
         assert np.array_equal(mine[n], theirs[n]), n
     for a, b in zip(got, want):
         assert torch.isfinite(b.float()).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dk,dv,value_ctas", DIMS)
+@pytest.mark.parametrize("at", range(len(FORMS)))
+def test_outputs_that_are_4_byte_aligned(dk, dv, value_ctas, at):
+    """An output may start at any multiple of 4 bytes, as for the causal attention; nothing is
+    written around it.  One that is not is refused."""
+    kv, new, kw = FORMS[at]
+    if not kw.get("disable_split"):
+        kw = dict(kw, force_chunk_tokens=4096 if max(kv) > 4096 else 64)
+    c = T.Nvfp4Case(kv, 16, 1, dk, dv, seed=at)
+    q = torch.randn((sum(new), 4, dk), generator=torch.Generator().manual_seed(at))
+    q = q.to(torch.bfloat16).cuda()
+    mask = TR.i32(np.full((sum(new), 2), -1))
+    plan = N.nvfp4kv_decode_plan(np.concatenate([[0], np.cumsum(new)]), c.indptr, c.last, 4, 1,
+                                 dk, dv, kernel=1, **kw)
+    want, want_lse = N.nvfp4kv_tree_run(plan, q, c.cache, c.kv_indices, mask)
+    for shift in (2, 6):
+        wide = torch.full((want.numel() + 8,), 9.0, dtype=torch.bfloat16).cuda()
+        out = wide[shift:shift + want.numel()].view(want.shape)
+        _, lse = N.nvfp4kv_tree_run(plan, q, c.cache, c.kv_indices, mask, out=out)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+        assert (wide[:shift] == 9).all() and (wide[shift + want.numel():] == 9).all()
+    with pytest.raises(N.NvFp4KvError):
+        N.nvfp4kv_tree_run(plan, q, c.cache, c.kv_indices, mask,
+                           out=wide[1:1 + want.numel()].view(want.shape))
+    assert N.nvfp4kv_workspace_flags(plan) == 0
+
+
+@pytest.mark.parametrize("dk,dv,value_ctas", DIMS)
+@pytest.mark.parametrize("at", range(len(FORMS)))
+@pytest.mark.parametrize("page", [16, 1])
+def test_live_lengths_in_every_form(dk, dv, value_ctas, at, page):
+    """A plan made for full last pages, run with the lengths that the device holds."""
+    kv, new, kw = FORMS[at]
+    if not kw.get("disable_split"):
+        kw = dict(kw, force_chunk_tokens=4096 if max(kv) > 4096 else 64)
+    run(kv, new, 4, 1, dk, dv, page=page, kernel=1, seed=at + dk, live=True, only=(0, 1), **kw)
 
 
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 128), (256, 256), (512, 256)])
