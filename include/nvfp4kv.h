@@ -665,8 +665,13 @@ int nvfp4kv_tree_form(const nvfp4kv_plan_info* info, nvfp4kv_tree_launch* form);
  * E4M3_RNE(code * (old / new)).  A request whose lengths, count or path cannot be is
  * left as it is: NVFP4KV_FLAG_BAD_APPEND_TARGET; so are a token with a page id out of
  * the pool and, in the E4M3 cache, the others of its target page:
- * NVFP4KV_FLAG_BAD_PAGE_INDEX.  No page may be listed twice.  One launch; can be captured
- * in a CUDA graph. */
+ * NVFP4KV_FLAG_BAD_PAGE_INDEX.  A page that holds a drafted token is one request's alone
+ * (pages before those may be shared).  kv_indices holds the entries that kv_indptr counts.
+ * One launch; can be captured in a CUDA graph.
+ *   nvfp4kv_tree_run attends over the 4-bit cache only.  Rows attended causally
+ * (nvfp4kv_e4m3_decode_run) verify a chain, whose accepted tokens stand in their places
+ * already: over an E4M3 cache compaction is for programs that attend to the tree in another
+ * way. */
 int nvfp4kv_compact_tokens(const nvfp4kv_paged_cache* cache, const int32_t* path,
                            int64_t path_stride, int32_t path_width, const int32_t* num_kept,
                            const int32_t* qo_indptr, const int32_t* kv_indptr,
@@ -725,16 +730,19 @@ int nvfp4kv_e4m3_copy_pages(const nvfp4kv_e4m3_cache* cache, const int32_t* src,
  * free_pages[head - freed .. head) in the order of the first entry (by row, then by
  * column) that names them, and free_head_out, which may be free_head, becomes head -
  * freed.
- *   num_rows at most 8192.
- * A request that is cut inside a page which has other owners must not grow there: it is
- * forked first (its fork has a copy of that page), or its tokens from the page's start
- * are given up.  (Drafted tokens that stand behind a fork are in pages of their request.)
+ *   num_rows at most 8192; a call gives up fewer than 2^30 entries.
+ * A request that is cut inside a page which has other owners must not grow there, as its
+ * new tokens would be written over theirs: it is forked first (its fork has a copy of that
+ * page), or its tokens from the page's start are given up.  The cut by itself is allowed
+ * and raises no flag.  (Drafted tokens that stand behind a fork are in pages of their
+ * request.)
  * A length that cannot be (keep_len > kv_len among them) sets NVFP4KV_FLAG_BAD_LENGTH, a
- * head that is smaller than the pages freed NVFP4KV_FLAG_TABLE_FULL; then nothing else is
- * changed.  A page id out of the pool is passed over: NVFP4KV_FLAG_BAD_PAGE_INDEX; a page
- * that is left more often than it has owners is freed once: NVFP4KV_FLAG_BAD_SHARES.  One
- * launch where num_rows * max_pages_per_request is at most 32768, else up to three; can be
- * captured in a CUDA graph. */
+ * head that is smaller than the pages freed, or too many entries, NVFP4KV_FLAG_TABLE_FULL;
+ * then nothing else is changed.  A page id out of the pool is passed over:
+ * NVFP4KV_FLAG_BAD_PAGE_INDEX; a page that is left more often than it has owners is freed
+ * once: NVFP4KV_FLAG_BAD_SHARES (where the head is too small as well, its count ends as if
+ * its entries had been its owners).  One launch where num_rows * max_pages_per_request is at
+ * most 32768, else up to three; can be captured in a CUDA graph. */
 int nvfp4kv_release_pages(const int32_t* keep_len, int32_t* kv_len, int32_t num_rows,
                           int32_t page_size, const int32_t* block_table,
                           int64_t block_table_stride, int32_t max_pages_per_request,

@@ -26,15 +26,17 @@
 //
 // The plan splits long requests for its own row blocks; here a cluster of CTAs divides a
 // unit's tokens (and value dims) further, as many as the SMs allow, or those of all units of
-// a request and kv head (uneven batches: in several waves, the longest first), and joins its states through distributed shared memory: no workspace
-// beyond the plan's is needed, and each CTA stores a share of the rows.  Units of a split
-// request that a cluster does not take as one fold as elsewhere (log-sum-exp over partial
-// states, by the last CTA to arrive: 2.8 us, and 0.4 for each state of 64 rows).
+// a request and kv head (uneven batches: in several waves, the longest first), and joins its
+// states through distributed shared memory: no workspace beyond the plan's is needed, and
+// each CTA stores a share of the rows.  Units of a split request that a cluster does not take
+// as one fold as elsewhere (log-sum-exp over partial states, by the last CTA to arrive: 2.8
+// us, and 0.4 for each state of 64 rows).
 // Every wait is bounded; one that runs out sets flag 0x4 and the CTA winds down.
 //
 // Measured (replayed): 4 requests x 32771 tokens, 104 rows of 8 kv heads (128/128) 78 us, 720
 // TFLOP/s of the rows that are there; 16 requests of 512-4096 tokens x 64 rows 39 us; 8
-// requests of 2048-8192 tokens x 48-88 rows (512/256) 45 us.  Neither memory (1.9 TB/s) nor
+// requests of 2048-8192 tokens x 48-88 rows (512/256) 45 us; with the step's tokens appended in
+// the launch 82, 40 and 48.  Neither memory (1.9 TB/s) nor
 // the tensor cores (a third busy) are full: the softmax warps' chain of a tile (wait, load,
 // maximum, 2^x, store: 2200 cycles of 128 tokens) and, at 512 dims, the dequantisation bound
 // it, with half of the issue slots taken and an eighth of the warps' time spent fetching

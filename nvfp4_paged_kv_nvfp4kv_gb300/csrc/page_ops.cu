@@ -21,10 +21,11 @@
 //
 // Latency bounds them: launches, the chain of loads that finds an entry, and (release) the
 // pages' words, random sectors of L2 or HBM, four times.  Measured (replayed): 16 requests of
-// 512-4096 tokens forked once 6.1 us and released 11; 64 requests of 500-16384 tokens forked 8
-// times each (270 k table entries copied, then given up) 8.1 and 37, of which the last two
+// 512-4096 tokens forked once 6.5 us and released 11; 64 requests of 500-16384 tokens forked 8
+// times each (270 k table entries copied, then given up) 8.8 and 37, of which the last two
 // passes' cluster takes 25 (16 SMs' loads of random words; all SMs would need a place for the
-// counts between launches); the copies of the last pages 3.0 and 5.2 us (17 MB, 3.3 TB/s).
+// counts between launches, which the call does not ask for); the copies of the last pages 3.1
+// and 4.9 us (17 MB, 3.5 TB/s).
 #include <climits>
 #include <cstdint>
 #include <mutex>

@@ -20,7 +20,8 @@ from ._lib import E4m3CacheStruct, RopeOptions, StepTableStruct, check
 from .api import Plan
 
 __all__ = ["StepTable", "nvfp4kv_build_page_table", "RopePlan", "nvfp4kv_rope_plan",
-           "nvfp4kv_rope", "nvfp4kv_norm_rope", "E4m3Cache", "nvfp4kv_e4m3_append", "nvfp4kv_e4m3_decode_run"]
+           "nvfp4kv_rope", "nvfp4kv_norm_rope", "E4m3Cache", "nvfp4kv_e4m3_append",
+           "nvfp4kv_e4m3_decode_run"]
 
 _DTYPE = {torch.bfloat16: 0, torch.float16: 1}
 

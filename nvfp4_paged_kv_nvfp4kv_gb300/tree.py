@@ -188,14 +188,15 @@ def nvfp4kv_compact_tokens(cache: PagedCache, path, num_kept, qo_indptr, kv_indp
     """Move the accepted tokens of every request together: of its rows of the step
     (qo_indptr), its last tokens in the page table of the step, those of the nodes
     ``path`` [batch, most] int32 (rising, the first ``num_kept[b]`` entries count) go to
-    the first places."""
+    the first places.  A page with a drafted token is one request's alone."""
     _compact("nvfp4kv_compact_tokens", cache, cache.struct(), path, num_kept, qo_indptr,
              kv_indptr, kv_indices, last_page_len, device_flags, stream)
 
 
 def nvfp4kv_e4m3_compact_tokens(cache: E4m3Cache, path, num_kept, qo_indptr, kv_indptr,
                                 kv_indices, last_page_len, device_flags=None, stream=None):
-    """``nvfp4kv_compact_tokens`` for an E4M3 cache."""
+    """``nvfp4kv_compact_tokens`` for an E4M3 cache (whose own attention is causal: for
+    programs that attend to the tree in another way)."""
     _compact("nvfp4kv_e4m3_compact_tokens", cache, cache._ref, path, num_kept, qo_indptr,
              kv_indptr, kv_indices, last_page_len, device_flags, stream)
 
@@ -277,7 +278,8 @@ def nvfp4kv_release_pages(keep_len, kv_len, block_table, page_shares, free_pages
     gives the pages behind them up: a page without another owner goes back in front of
     the free list's head (``free_head`` [1]; the new one goes to ``free_head_out``, by
     default the same word).  ``kv_len`` and ``page_shares`` are updated.  A request cut
-    inside a page with other owners must not grow there (fork it first)."""
+    inside a page with other owners must not grow there, over their tokens (fork it
+    first)."""
     if free_head_out is None:
         free_head_out = free_head
     _i32("the lists", keep_len, kv_len, page_shares, free_pages, free_head, free_head_out)
