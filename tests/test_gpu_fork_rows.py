@@ -1,4 +1,5 @@
 """Rows that forks may fill, and as many entries as a call of forks takes."""
+import numpy as np
 import pytest
 import torch
 
@@ -62,3 +63,63 @@ def test_as_many_entries_as_a_call_takes():
     torch.cuda.synchronize()
     assert int(flags) == _lib.FLAG_TABLE_FULL and not kv_len[2:].any()
     assert torch.equal(shares, before)
+
+
+@pytest.mark.parametrize("width", [8, 2100, 20000])
+def test_forks_in_a_graph_before_and_behind_calls_that_use_their_lengths(width):
+    """Lengths written just before a fork, read just behind it: launched, and replayed."""
+    b = P.Both((33, 50), 6, width=width)
+    par, child = P.i32([0, 1, 0]), P.i32([2, 3, 4])
+    src, dst = (torch.full((3,), -7, dtype=torch.int32).cuda() for _ in range(2))
+    mid, seen = P.i32([0]), torch.zeros_like(b.kv_len)
+
+    def step():
+        b.kv_len[:2] += 7
+        b.kv_len[:2] -= 7
+        N.nvfp4kv_fork_pages(par, child, b.kv_len, b.table, b.shares, b.free, b.head, mid, src,
+                             dst, device_flags=b.flags)
+        seen.copy_(b.kv_len)
+        N.nvfp4kv_release_pages(b.kv_len * keep, b.kv_len, b.table, b.shares, b.free, mid, b.head,
+                                device_flags=b.flags)
+
+    keep = P.i32([1, 1, 0, 0, 0, 0])
+    step()
+    graph = torch.cuda.CUDAGraph()
+    for replay in range(4):
+        copies = b.ref.fork([0, 1, 0], [2, 3, 4])
+        b.ref.release([33, 50, 0, 0, 0, 0])
+        b.same()
+        assert seen.tolist() == [33, 50, 33, 50, 33, 0]
+        assert list(zip(src.tolist(), dst.tolist())) == copies
+        seen.zero_()
+        if replay == 0:
+            with torch.cuda.graph(graph):
+                step()
+        graph.replay()
+        torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("width", [300, 2100])
+@pytest.mark.parametrize("seed", [0, 1])
+def test_many_steps_in_wide_tables(seed, width):
+    """As test_many_steps, over tables whose forks take a cluster, or two launches (from 16
+    forks on)."""
+    rng = np.random.default_rng(seed)
+    kv = [int(x) for x in rng.integers(0, 300 * 16, 20)]
+    b = P.Both(kv, 60, 16, seed=seed, spare=400, width=width)
+    for _ in range(6):
+        rows = rng.permutation(60).tolist()
+        empty = [r for r in rows if b.ref.kv_len[r] == 0]
+        some = [r for r in rows if b.ref.kv_len[r] > 0]
+        n = min(len(empty), int(rng.integers(1, 30)))
+        if n and some:
+            b.fork([some[int(rng.integers(0, len(some)))] for _ in range(n)], empty[:n])
+            b.same()
+        keep = list(b.ref.kv_len)
+        for r in rows[:40]:
+            keep[r] = int(rng.integers(0, keep[r] + 1)) if rng.random() < 0.4 else 0
+        b.release(keep, out=bool(rng.integers(0, 2)))
+        b.same()
+    b.release([0] * 60)
+    b.same()
+    assert sorted(b.ref.free[b.ref.head:]) == list(range(b.total)) and not any(b.ref.shares)
