@@ -85,8 +85,8 @@ __device__ __forceinline__ longlong2 cta_sums(longlong2 mine, longlong2* total) 
 // that the launch is, or, where more CTAs fill the table (`fill`), by a launch of one CTA
 // behind it, which finds the same inputs: it may start and check while the table is filled,
 // and waits for the end of that before it writes.  Measured (replayed; us): 2048 entries (one
-// CTA) 5.6, 16384 (a cluster of 4) 6.3, 307200 7.5, with an ordinary second launch 9.7;
-// everything in one CTA: 16384 13, 307200 172.
+// CTA) 5.6, 16384 (a cluster of 4) 6.4, 65536 8.2, with an ordinary second launch 10.1;
+// everything in one CTA: 16384 13, 65536 51.
 __global__ void __launch_bounds__(kForkThreads) fork_kernel(const ForkParams p, bool fill,
                                                             bool lengths) {
   extern __shared__ int32_t smem[];
